@@ -409,6 +409,200 @@ argus_status argus_staging_moves_less(const int64_t* row_read_bytes, int64_t n_r
                                       int64_t cache_bytes, int32_t* stage);
 
 /* ---------------------------------------------------------------------------
+ * argus_paged_extend_attn -- attention of several query tokens per sequence
+ * over the paged cache, read in place (drafted tokens to verify, prompt chunks,
+ * a step that mixes both, a decoder's prompt over an encoder's states).
+ *
+ * Sequence b has the query tokens q_start[b] .. q_start[b+1]-1 (a ragged batch:
+ * their number n_b may differ and may be 0) and a cache of seq_lens[b] tokens.
+ * Query token i of sequence b (i = 0 .. n_b-1) and query head hq (KV head
+ * h = hq / G) attend to the cached positions j with
+ *   causal = 1:  j <= seq_lens[b] - n_b + i   (the cache ends with the n_b new
+ *                tokens themselves: argus_rope_append stores them first),
+ *   causal = 0:  j < seq_lens[b]              (cross attention to the states of
+ *                an encoder, whose length has nothing to do with n_b):
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(softmax_scale * q . k_j),
+ *   lse2 = log2 sum_j p_j.
+ * A row that sees nothing (an empty cache, or seq_lens[b] < n_b under the
+ * causal mask) gives o = 0 and lse2 = -inf.
+ *
+ * Pages: 16-bit pages of the query's type, FP8 and INT8 pages (one fp32 scale,
+ * finite and >= 0, per page, KV head and K | V), mixed freely, in device
+ * memory.  INT4 / INT2 / INT1 pools, 16-bit pools of the other type and host
+ * pools are ARGUS_E_UNSUPPORTED.  A page whose slot lies outside its pool, or
+ * whose codec has no pool, is left out of the sums and counted once per
+ * sequence and page in *status.  Stored values at positions < seq_lens[b] must be
+ * finite; whatever the last page holds behind them is not used.
+ * seq_lens[b] is clamped to [0, max_pages * P], q_start[] to [0, total_q].
+ *
+ * Precision: the codes of a page are exact in the query's type, in which Q.K^T
+ * and P.V run on the tensor cores with fp32 accumulation; p_j (times the
+ * page's V scale) is rounded to the query's type (half a step, 2^-8 of its
+ * value for BF16, 2^-11 for FP16); maxima, sums and the accumulators are fp32.
+ *
+ * Arguments: q device [total_q] tokens of [Hq][D] (16-byte aligned; tokens
+ * q_stride elements apart, a multiple of 8, 0 = Hq * D: rows of a fused
+ * projection are read in place); out device [total_q][Hq][D] of q_dtype
+ * (16-byte aligned); lse2_out device [total_q][Hq] or NULL.  Rows of out
+ * that belong to no sequence are left as they were.  Supported: head_dim 64 or
+ * 128, G from 1 to 8, batch <= 65535, total_q * Hq < 2^31.  ws (16-byte
+ * aligned) of argus_extend_workspace_bytes bytes: no initialisation, not to be
+ * shared by calls that overlap on the GPU.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  argus_geom g;
+  int32_t batch;              /* B */
+  int32_t total_q;            /* query tokens of all sequences */
+  int32_t q_dtype;            /* ARGUS_FP16 or ARGUS_BF16 */
+  int32_t causal;             /* 1 or 0 */
+  const void* q;              /* device [total_q][Hq][D], tokens q_stride apart */
+  int64_t q_stride;           /* elements between query tokens; 0 = Hq * D */
+  const int32_t* q_start;     /* device [B + 1] */
+  const argus_pool* pools;    /* host array, at most one pool per codec */
+  int32_t n_pools;
+  int32_t max_pages;          /* row length of page_codec / block_table */
+  const uint8_t* page_codec;  /* device [B][max_pages] */
+  const int32_t* block_table; /* device [B][max_pages] */
+  const int32_t* seq_lens;    /* device [B] */
+  void* out;                  /* device [total_q][Hq][D] of q_dtype */
+  float* lse2_out;            /* device [total_q][Hq] or NULL */
+  uint32_t* status;           /* device uint32 anomaly counter, or NULL (bit 31 as in decode) */
+  float softmax_scale;        /* finite, >= 0 */
+} argus_extend_args;
+
+argus_status argus_extend_workspace_bytes(const argus_extend_args* args, size_t* bytes);
+
+argus_status argus_paged_extend_attn(const argus_extend_args* args, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_rope_append -- rotary positions with one or several axes on the new
+ * tokens' queries and keys, and the append of keys and values to the cache.
+ *
+ * Token t of the ragged batch (sequence b, q_start as in
+ * argus_paged_extend_attn) is the cached position
+ *   c = seq_lens[b] - n_b + (t - q_start[b])
+ * (seq_lens counts the new tokens), stored in row c % P of logical page c / P,
+ * which must be a page of `pool` (16-bit, of the tokens' type).  Pair i of the
+ * rot_dim / 2 rotated pairs turns by the angle
+ *   a = positions[axis(i)][t] * inv_freq[i],  axis(i) = pair_axis[i] (0 if NULL),
+ * where an image's or a video's tokens have a position per axis (time, height,
+ * width) and text tokens the same on each:
+ *   x' = x cos a - y sin a,   y' = y cos a + x sin a,
+ * with (x, y) = elements (i, i + rot_dim / 2), or (2i, 2i + 1) when adjacent.
+ * The elements from rot_dim on are passed through.  The angle is reduced to a
+ * turn in 64-bit fixed point, so it is as exact at position 2^31 - 1 as at 0;
+ * the rotation is fp32, rounded once.
+ *   q_out = rotated q;  cache K row = rotated k;  cache V row = v.
+ * A token whose page lies outside max_pages or the pool, or is not of the
+ * pool's codec, is not stored (its q_out is written all the same), and counted in
+ * *status; so is a pair whose axis is >= n_axes, once per token, and it is
+ * not turned.  Positions may be negative.  Two tokens must not name the
+ * same row of a page.
+ * Arguments: q, k, v device, tokens q_stride / k_stride / v_stride elements
+ * apart (0 = dense; multiples of 8, 16-byte aligned); q_out as q (it may be
+ * q itself with the same stride; otherwise they must not overlap); positions device int32
+ * [n_axes][total_q]; n_axes 1 to 4; inv_freq device double [rot_dim / 2], in
+ * radians per position (finite, >= 0); pair_axis device uint8 [rot_dim / 2] or
+ * NULL; rot_dim a multiple of 16, 16 .. head_dim.  head_dim 64 or 128.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  argus_geom g;
+  int32_t batch;              /* B */
+  int32_t total_q;            /* tokens of all sequences */
+  int32_t dtype;              /* ARGUS_FP16 or ARGUS_BF16 */
+  int32_t rot_dim;
+  int32_t adjacent;           /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2i, 2i + 1) */
+  int32_t n_axes;
+  const void* q;              /* device [total_q][Hq][D] */
+  const void* k;              /* device [total_q][Hkv][D] */
+  const void* v;              /* device [total_q][Hkv][D] */
+  void* q_out;                /* device [total_q][Hq][D] */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const int32_t* positions;   /* device [n_axes][total_q] */
+  const double* inv_freq;     /* device [rot_dim / 2] */
+  const uint8_t* pair_axis;   /* device [rot_dim / 2] or NULL */
+  const int32_t* q_start;     /* device [B + 1] */
+  const int32_t* seq_lens;    /* device [B], the new tokens counted */
+  const argus_pool* pool;     /* host descriptor of the 16-bit pool */
+  const uint8_t* page_codec;  /* device [B][max_pages] */
+  const int32_t* block_table; /* device [B][max_pages] */
+  int32_t max_pages;
+  uint32_t* status;           /* device uint32 anomaly counter, or NULL */
+} argus_rope_args;
+
+argus_status argus_rope_append(const argus_rope_args* args, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_fork_pages -- one step of the page table: sequences forked from their
+ * parents and freed, shared partial pages copied before they are written, and
+ * pages allocated for the tokens about to be appended.
+ *
+ * Every pool has a reference count per slot (int32): how often the slot stands
+ * in the table, plus the holders outside it (a prefix cache).  A slot with
+ * count 0 is free.  From the old table (page_codec, block_table, seq_lens) and
+ * counts the call makes new ones, in arrays of their own:
+ *   1. Row b of the new table is row parents[b] of the old one, with its length
+ *      (b itself: the row stays; -1: the row is freed, length 0).
+ *   2. Rows with parents[b] != b give up the references of their old pages and
+ *      take references on the parent's.
+ *   3. A row with n_new[b] > 0 and a partial last page (length % P != 0) is
+ *      about to write that page.  It gets a copy of its own unless nobody else
+ *      holds the page; of several such rows that hold it with nobody else, the
+ *      lowest keeps it.  The copy leaves the old page's count by one.
+ *   4. Pages of codec new_codec are added up to length + n_new[b].
+ *   5. The copies and new pages of a pool are numbered in order of row, then of
+ *      page; number k gets the k-th lowest slot that is free after step 2, with
+ *      count 1.  Without a free slot the entry is -1 and *status counts it.
+ *   6. The new length is length + n_new[b].  Unused entries are -1, codec 0.
+ * The result does not depend on the order in which the GPU works.
+ * Copied pages (codes and meta) stay within their pool; a page is copied whole.
+ * Anomalies counted in *status: a parent outside -1 .. B-1 (taken as -1), an
+ * old entry that names no slot of a pool (kept, not counted as a reference;
+ * a copy of it is not made), n_new < 0 (taken as 0), a length beyond max_pages * P
+ * (clamped to it).
+ * The output arrays must not be the input arrays (ARGUS_E_INVALID), so a
+ * captured call can be replayed and two table copies alternate.
+ * Arguments: pools host array in device memory (placement DEVICE, else
+ * ARGUS_E_UNSUPPORTED), at most one per codec, n_slots < 2^31; ref_in, ref_out
+ * host arrays of n_pools device int32 [n_slots]; parents, n_new (NULL = 0)
+ * device int32 [B]; batch <= 65535; new_codec one of the pools'.
+ * ------------------------------------------------------------------------- */
+argus_status argus_fork_workspace_bytes(int32_t batch, const argus_pool* pools, int32_t n_pools,
+                                        size_t* bytes);
+
+argus_status argus_fork_pages(const argus_geom* g, int32_t batch, const int32_t* parents,
+                              const int32_t* n_new, int32_t new_codec, const argus_pool* pools,
+                              int32_t n_pools, const int32_t* const* ref_in, int32_t* const* ref_out,
+                              const uint8_t* page_codec, const int32_t* block_table,
+                              const int32_t* seq_lens, uint8_t* page_codec_out,
+                              int32_t* block_table_out, int32_t* seq_lens_out, int32_t max_pages,
+                              void* ws, size_t ws_bytes, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_compact_pages -- the live pages of one pool moved into its lowest slots.
+ *
+ * With L = the number of slots whose count is > 0, the k-th live slot >= L (in
+ * ascending order) moves to the k-th free slot < L: no slot is both read
+ * and written, and the fewest pages move.  ref_out holds the counts at the new
+ * places (0 from slot L on), block_table_out the table with the entries of
+ * this pool's codec rewritten in the pages below seq_lens[b] (all others are
+ * copied), *n_live = L.  The slots from L on may then be given back.  Holders
+ * outside the table follow the same rule.
+ * A negative count is taken as 0.  Entries that name no slot of the pool are
+ * copied and counted in *status.
+ * ref_out and block_table_out must not be the input arrays.
+ * ws of argus_compact_workspace_bytes bytes.  The pool lies in device memory.
+ * ------------------------------------------------------------------------- */
+argus_status argus_compact_workspace_bytes(const argus_pool* pool, size_t* bytes);
+
+argus_status argus_compact_pages(const argus_geom* g, int32_t batch, const argus_pool* pool,
+                                 const int32_t* ref_in, int32_t* ref_out, const uint8_t* page_codec,
+                                 const int32_t* block_table, const int32_t* seq_lens,
+                                 int32_t* block_table_out, int32_t max_pages, int32_t* n_live,
+                                 void* ws, size_t ws_bytes, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Testing only.  argus_test_decode_stall runs argus_paged_decode_attn with
  * every device wait limited to wait_limit_us microseconds (1 .. 2,000,000),
  * and the producer warp (the one issuing copies) of each CTA that reaches stage

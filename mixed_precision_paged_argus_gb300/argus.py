@@ -55,12 +55,39 @@ class DecodeArgs(ctypes.Structure):
                 ("window_tokens", ctypes.c_int32), ("sink_tokens", ctypes.c_int32)]
 
 
+class ExtendArgs(ctypes.Structure):
+    _fields_ = [("g", Geom), ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("q_dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_start", ctypes.c_void_p),
+                ("pools", ctypes.POINTER(PoolDesc)), ("n_pools", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_codec", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse2_out", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("softmax_scale", ctypes.c_float)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("g", Geom), ("batch", ctypes.c_int32), ("total_q", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("pair_axis", ctypes.c_void_p),
+                ("q_start", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("pool", ctypes.POINTER(PoolDesc)), ("page_codec", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("max_pages", ctypes.c_int32),
+                ("status", ctypes.c_void_p)]
+
+
 EXPORTS = ["argus_quantize_pages", "argus_decode_workspace_bytes", "argus_paged_decode_attn",
            "argus_paged_decode_attn_noalloc",
            "argus_select_workspace_bytes", "argus_select_pages", "argus_fold_lse",
            "argus_window_prefill_workspace_bytes", "argus_window_prefill_attn",
            "argus_paged_window_prefill_workspace_bytes", "argus_paged_window_prefill_attn",
-           "argus_staging_moves_less", "argus_test_decode_stall",
+           "argus_staging_moves_less", "argus_extend_workspace_bytes", "argus_paged_extend_attn",
+           "argus_rope_append", "argus_fork_workspace_bytes", "argus_fork_pages",
+           "argus_compact_workspace_bytes", "argus_compact_pages", "argus_test_decode_stall",
            "argus_status_string", "argus_last_error"]
 
 
@@ -112,6 +139,22 @@ def lib():
                                                   i32, i64, i64, i64, ctypes.c_float, vp, vp, i32, i32, vp, sz, vp, vp]
     L.argus_staging_moves_less.restype = ctypes.c_int
     L.argus_staging_moves_less.argtypes = [ctypes.POINTER(ctypes.c_int64), i64, i64, ctypes.POINTER(i32)]
+    L.argus_extend_workspace_bytes.restype = ctypes.c_int
+    L.argus_extend_workspace_bytes.argtypes = [ctypes.POINTER(ExtendArgs), ctypes.POINTER(sz)]
+    L.argus_paged_extend_attn.restype = ctypes.c_int
+    L.argus_paged_extend_attn.argtypes = [ctypes.POINTER(ExtendArgs), vp, sz, vp]
+    L.argus_rope_append.restype = ctypes.c_int
+    L.argus_rope_append.argtypes = [ctypes.POINTER(RopeArgs), vp]
+    L.argus_fork_workspace_bytes.restype = ctypes.c_int
+    L.argus_fork_workspace_bytes.argtypes = [i32, ctypes.POINTER(PoolDesc), i32, ctypes.POINTER(sz)]
+    L.argus_fork_pages.restype = ctypes.c_int
+    L.argus_fork_pages.argtypes = [ctypes.POINTER(Geom), i32, vp, vp, i32, ctypes.POINTER(PoolDesc), i32,
+                                   ctypes.POINTER(vp), ctypes.POINTER(vp), vp, vp, vp, vp, vp, vp, i32, vp, sz, vp, vp]
+    L.argus_compact_workspace_bytes.restype = ctypes.c_int
+    L.argus_compact_workspace_bytes.argtypes = [ctypes.POINTER(PoolDesc), ctypes.POINTER(sz)]
+    L.argus_compact_pages.restype = ctypes.c_int
+    L.argus_compact_pages.argtypes = [ctypes.POINTER(Geom), i32, ctypes.POINTER(PoolDesc), vp, vp, vp, vp, vp, vp, i32,
+                                      vp, vp, sz, vp, vp]
     _lib = L
     return L
 
@@ -337,3 +380,141 @@ def paged_window_prefill_attn(g, n_q, q, pools, page_codec, block_table, max_pag
                                                  int(win_len), int(q_pos0), float(softmax_scale), _ptr(acc_o),
                                                  _ptr(acc_lse2), int(fold), int(num_splits), _ptr(ws),
                                                  ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+
+
+def _token_stride(name, t, heads, head_dim):
+    """Elements between the tokens of t [tokens][heads][head_dim], whose tokens
+    are dense and may lie apart (a slice of a fused projection's rows)."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
+        raise ValueError("%s must be [tokens][%d][%d], not %s" % (name, heads, head_dim, list(t.shape)))
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise ValueError("%s: the heads of a token must be dense" % name)
+    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+
+
+def _dense(**tensors):
+    for name, (t, dtype, numel) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype not in dtype or not t.is_contiguous() or t.numel() < numel:
+            raise ValueError("%s must be a dense %s tensor of %d elements or more" % (name, dtype[0], numel))
+
+
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+_STATUS = (torch.int32, torch.uint32)
+
+
+def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pages, softmax_scale, out,
+                causal=True, lse2_out=None, status=None):
+    """Build an argus_extend_args struct: q [total_q][Hq][D] (its tokens may lie
+    apart), q_start [B + 1], seq_lens [B], out like q and dense."""
+    batch, total = q_start.numel() - 1, q.shape[0]
+    qs = _token_stride("q", q, g.n_q_heads, g.head_dim)
+    _dense(q_start=(q_start, _I32, 1), seq_lens=(seq_lens, _I32, batch), page_codec=(page_codec, _U8, batch * max_pages),
+           block_table=(block_table, _I32, batch * max_pages), out=(out, (q.dtype,), q.numel()),
+           lse2_out=(lse2_out, (torch.float32,), total * g.n_q_heads), status=(status, _STATUS, 1))
+    arr = (PoolDesc * max(1, len(pools)))(*[p.desc() for p in pools])
+    a = ExtendArgs(g, batch, total, DTYPE_CODEC[q.dtype], int(causal), q.data_ptr(), qs, q_start.data_ptr(),
+                   arr, len(pools), int(max_pages), _ptr(page_codec), _ptr(block_table),
+                   _ptr(seq_lens), _ptr(out), _ptr(lse2_out), _ptr(status), float(softmax_scale))
+    # the struct holds raw pointers: keep every tensor it points to alive with it
+    a._keep = (arr, list(pools), q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
+    return a
+
+
+def extend_workspace_bytes(args):
+    n = ctypes.c_size_t(0)
+    _check(lib().argus_extend_workspace_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def paged_extend_attn(args, ws, stream=None):
+    """Attention of several query tokens per sequence over the paged cache;
+    ws of extend_workspace_bytes bytes."""
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().argus_paged_extend_attn(ctypes.byref(args), _ptr(ws), nbytes, _stream(stream)))
+
+
+def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages,
+                pair_axis=None, adjacent=False, status=None, stream=None):
+    """Turn q and k by their positions ([n_axes][tokens], one row per axis;
+    inv_freq [rot_dim / 2] in float64, radians per position) into q_out and the
+    cache, and store v: the tokens of sequence b become the last ones of its
+    seq_lens[b] cached positions."""
+    total, batch = q.shape[0], q_start.numel() - 1
+    hq, hkv, d = g.n_q_heads, g.n_kv_heads, g.head_dim
+    if k.shape[0] != total or v.shape[0] != total or q_out.shape[0] != total or positions.numel() % max(1, total):
+        raise ValueError("rope_append: q, k, v, q_out and positions must have the same tokens")
+    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+        raise ValueError("rope_append: q, k, v and q_out must have the same type")
+    n_axes = positions.numel() // total if total else 1
+    _dense(q_start=(q_start, _I32, 1), seq_lens=(seq_lens, _I32, batch), positions=(positions, _I32, 0),
+           inv_freq=(inv_freq, (torch.float64,), 0), pair_axis=(pair_axis, _U8, inv_freq.numel()),
+           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
+           status=(status, _STATUS, 1))
+    d_pool = pool.desc()
+    a = RopeArgs(g, batch, total, DTYPE_CODEC[q.dtype], 2 * inv_freq.numel(), int(adjacent), n_axes,
+                 _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _token_stride("q", q, hq, d), _token_stride("k", k, hkv, d),
+                 _token_stride("v", v, hkv, d), _token_stride("q_out", q_out, hq, d), _ptr(positions), _ptr(inv_freq),
+                 _ptr(pair_axis), _ptr(q_start), _ptr(seq_lens), ctypes.pointer(d_pool), _ptr(page_codec),
+                 _ptr(block_table), int(max_pages), _ptr(status))
+    _check(lib().argus_rope_append(ctypes.byref(a), _stream(stream)))
+
+
+def _pool_array(pools):
+    return (PoolDesc * max(1, len(pools)))(*[p.desc() for p in pools])
+
+
+def _pointers(tensors):
+    return (ctypes.c_void_p * max(1, len(tensors)))(*[_ptr(t) for t in tensors])
+
+
+def fork_workspace_bytes(batch, pools):
+    n = ctypes.c_size_t(0)
+    _check(lib().argus_fork_workspace_bytes(int(batch), _pool_array(pools), len(pools), ctypes.byref(n)))
+    return n.value
+
+
+def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec, block_table, seq_lens, page_codec_out,
+               block_table_out, seq_lens_out, max_pages, ws, status=None, stream=None):
+    """One step of the page table: row b becomes row parents[b] (-1: freed),
+    partial pages about to be written are copied where others hold them too, and
+    pages of new_codec are added for n_new[b] tokens.  ref_in / ref_out: one
+    int32 count per slot for each pool.  ws of fork_workspace_bytes bytes."""
+    batch = parents.numel()
+    if len(ref_in) != len(pools) or len(ref_out) != len(pools):
+        raise ValueError("fork_pages: one count tensor per pool")
+    _dense(parents=(parents, _I32, 0), n_new=(n_new, _I32, batch), status=(status, _STATUS, 1),
+           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
+           seq_lens=(seq_lens, _I32, batch), page_codec_out=(page_codec_out, _U8, batch * max_pages),
+           block_table_out=(block_table_out, _I32, batch * max_pages), seq_lens_out=(seq_lens_out, _I32, batch))
+    for p, r, s in zip(pools, ref_in, ref_out):
+        _dense(ref_in=(r, _I32, p.n_slots), ref_out=(s, _I32, p.n_slots))
+    _check(lib().argus_fork_pages(ctypes.byref(g), batch, _ptr(parents), _ptr(n_new), int(new_codec), _pool_array(pools),
+                                  len(pools), _pointers(ref_in), _pointers(ref_out), _ptr(page_codec), _ptr(block_table),
+                                  _ptr(seq_lens), _ptr(page_codec_out), _ptr(block_table_out), _ptr(seq_lens_out),
+                                  int(max_pages), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
+                                  _stream(stream)))
+
+
+def compact_workspace_bytes(pool):
+    n = ctypes.c_size_t(0)
+    d = pool.desc()
+    _check(lib().argus_compact_workspace_bytes(ctypes.byref(d), ctypes.byref(n)))
+    return n.value
+
+
+def compact_pages(g, pool, ref_in, ref_out, page_codec, block_table, seq_lens, block_table_out, max_pages, n_live, ws,
+                  status=None, stream=None):
+    """Move the live pages of a pool into its lowest slots; the new counts and
+    table go to ref_out and block_table_out, the number of live slots to n_live.
+    ws of compact_workspace_bytes bytes."""
+    batch = seq_lens.numel()
+    _dense(ref_in=(ref_in, _I32, pool.n_slots), ref_out=(ref_out, _I32, pool.n_slots), n_live=(n_live, _I32, 1),
+           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
+           block_table_out=(block_table_out, _I32, batch * max_pages), seq_lens=(seq_lens, _I32, 0), status=(status, _STATUS, 1))
+    d = pool.desc()
+    _check(lib().argus_compact_pages(ctypes.byref(g), batch, ctypes.byref(d), _ptr(ref_in), _ptr(ref_out), _ptr(page_codec),
+                                     _ptr(block_table), _ptr(seq_lens), _ptr(block_table_out), int(max_pages), _ptr(n_live),
+                                     _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))

@@ -46,3 +46,6 @@ from .attention import (  # noqa: F401
     gather_window, paged_window_attention, staging_moves_less,
 )
 from .selection import compressed_key_scores, select_pages  # noqa: F401
+from .cache import (  # noqa: F401
+    paged_extend, rotate, append_places, fork_pages, compact_pages,
+)

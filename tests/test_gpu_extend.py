@@ -1,0 +1,254 @@
+"""argus_paged_extend_attn on the GPU against the double-precision oracle.
+
+Bound per output element, from the arithmetic (u = eps / 2 of the 16-bit type, a
+rounding to nearest): every p_j is rounded once to that type for P.V, the
+result once for the output; a score sums D exact products in fp32 (at most D
+roundings of 2^-23 of the sum of their magnitudes, truncating adds included), and 2^x
+is off by 2^-21 plus the fp32 rounding of x, in the numerator and in the sum:
+  |o - ref| <= u sum p|v| + u |ref| + 2 e sum p|v|,  e = ln 2 (D 2^-23 qk + 2^-22 smax) + 2^-21
+(plus the 16-bit type's smallest step).
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_paged_argus_gb300.argus as argus
+from mixed_precision_paged_argus_gb300 import workloads as W
+import oracle
+from oracle import codecs as C
+from paged_cases import DEV, build_case
+
+pytestmark = pytest.mark.gpu
+F8, I8 = W.FP8_E4M3, W.INT8
+
+
+def make(Hq, Hkv, D, P, lens, new, codecs, dtype, seed, extra_slots=2):
+    """A paged case with new[b] query tokens for sequence b; codecs: the choices of
+    each page's tier."""
+    rng = np.random.default_rng(seed)
+    max_pages = max(1, max((n + P - 1) // P for n in lens))
+    pc = rng.choice(codecs, size=(len(lens), max_pages))
+    c = build_case(Hq, Hkv, D, P, lens, pc, dtype, seed=seed, extra_slots=extra_slots)
+    c.new = list(new)
+    c.q_start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    total = int(c.q_start[-1])
+    c.q = W.normal((total, Hq, D), dtype, seed + 50).to(DEV)
+    c.dtype = dtype
+    c.to64 = C.f16_bits_to_f64 if dtype == W.FP16 else C.bf16_bits_to_f64
+    return c
+
+
+def spoil_tails(c):
+    """Rows of each last page behind the sequence's end: NaN (0x7F bytes) in the GPU's pools."""
+    by = {p.codec: p for p in c.pools}
+    for b, n in enumerate(c.lens):
+        page = int(n) // c.P
+        for p in range(page, c.max_pages):
+            pool = by[int(c.page_codec[b, p])]
+            pool.codes.view(torch.uint8)[int(c.table[b, p]), :, :, (int(n) - p * c.P if p == page else 0):] = 0x7F
+
+
+def run(c, causal, q=None, status=None, stream=None, ws=None, max_pages=None):
+    q = c.q if q is None else q
+    out = torch.full((q.shape[0], c.Hq, c.D), float("nan"), dtype=q.dtype, device=DEV)
+    lse = torch.full((q.shape[0], c.Hq), float("nan"), dtype=torch.float32, device=DEV)
+    args = argus.extend_args(c.g, q, torch.from_numpy(c.q_start).to(DEV), c.pools, c.d_codec, c.d_table, c.d_lens,
+                             c.max_pages, c.scale, out, causal=causal, lse2_out=lse, status=status)
+    if ws is None:
+        ws = torch.full((argus.extend_workspace_bytes(args),), 0xFF, dtype=torch.uint8, device=DEV)
+    argus.paged_extend_attn(args, ws, stream=stream)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def check(c, out, lse, causal, expect_bad=0, rows=None):
+    q64 = c.to64(W.to_bits(c.q))
+    ref, ref_lse, bad, av, qk, smax = oracle.paged_extend(q64, c.q_start, c.Hkv, c.P, c.opools, c.page_codec, c.table,
+                                                          c.lens, c.scale, causal)
+    assert bad == expect_bad
+    fi = torch.finfo(out.dtype)
+    u = fi.eps / 2
+    e = (math.log(2) * (c.D * 2.0 ** -23 * qk + 2.0 ** -22 * smax) + 2.0 ** -21)[..., None]
+    got = out.float().cpu().numpy().astype(np.float64)
+    bound = u * av + u * np.abs(ref) + 2 * e * av + fi.smallest_normal * fi.eps
+    over = np.abs(got - ref) - bound
+    assert not np.isnan(got).any() and over.max() <= 0, "worst %.3g over its bound" % over.max()
+    gl = lse.cpu().numpy().astype(np.float64)
+    fin = np.isfinite(ref_lse)
+    assert np.array_equal(np.isfinite(gl), fin) and np.all(gl[~fin] == -np.inf)
+    # lse2 in bits: the score's error, the sum's and log2's (2^-21 relative each), and its own fp32 rounding
+    lb = c.D * 2.0 ** -23 * qk + 2.0 ** -22 * smax + 2.0 ** -19 + 2.0 ** -22 * np.abs(np.where(fin, ref_lse, 0))
+    assert np.all(np.abs(gl[fin] - ref_lse[fin]) <= lb[fin])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype,codecs", [
+    (W.FP16, [W.FP16]), (W.BF16, [W.BF16]), (W.FP16, [F8]), (W.BF16, [F8]), (W.FP16, [I8]), (W.BF16, [I8]),
+    (W.FP16, [W.FP16, F8, I8]), (W.BF16, [W.BF16, F8, I8])])
+def test_tiers_types_and_masks(dtype, codecs, D, causal):
+    c = make(8, 2, D, 16, [300, 17, 128, 129, 1], [5, 17, 1, 33, 1], codecs, dtype, seed=11 + D)
+    spoil_tails(c)
+    out, lse = run(c, causal)
+    check(c, out, lse, causal)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (9, 3), (8, 2), (10, 2), (12, 2), (14, 2), (16, 2)])
+def test_head_groupings(Hq, Hkv):
+    c = make(Hq, Hkv, 64, 48, [200, 95, 500], [40, 3, 70], [W.FP16, F8], W.FP16, seed=40 + Hq)
+    spoil_tails(c)
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+
+
+@pytest.mark.parametrize("n_q", [1, 2, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 130])
+def test_row_counts_around_the_tiles(n_q):
+    """n_q * G rows: 4 to 520, around the 32, 64 and 128 rows where the layout changes."""
+    c = make(4, 1, 128, 32, [257, 700], [n_q, max(1, n_q - 1)], [W.BF16, F8], W.BF16, seed=70 + n_q)
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+
+
+@pytest.mark.parametrize("length", [1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 1025])
+@pytest.mark.parametrize("causal", [True, False])
+def test_lengths_around_the_blocks(length, causal):
+    c = make(4, 2, 64, 16, [length], [min(3, length)], [I8], W.FP16, seed=100 + length)
+    spoil_tails(c)
+    out, lse = run(c, causal)
+    check(c, out, lse, causal)
+
+
+def test_rows_that_see_nothing():
+    """An empty cache, a sequence without queries, and a causal batch with more queries than positions."""
+    c = make(4, 2, 128, 16, [0, 40, 3, 0], [2, 0, 7, 0], [F8], W.BF16, seed=130)
+    for causal in (True, False):
+        out, lse = run(c, causal)
+        check(c, out, lse, causal)
+        assert torch.all(out[:2] == 0) and torch.all(torch.isinf(lse[:2]))
+    out, lse = run(c, True)
+    assert torch.all(out[2:6] == 0) and torch.all(torch.isinf(lse[2:6])) and torch.all(torch.isfinite(lse[6:]))
+
+
+def test_rows_of_no_sequence_are_left():
+    c = make(4, 2, 64, 16, [40, 90], [3, 5], [W.FP16], W.FP16, seed=140)
+    total = 8
+    c.q = torch.cat([c.q, torch.full((4, 4, 64), float("nan"), dtype=torch.float16, device=DEV)])
+    out, lse = run(c, True)
+    assert torch.isnan(out[total:]).all() and torch.isnan(lse[total:]).all()
+    c.q, out, lse = c.q[:total], out[:total], lse[:total]
+    check(c, out, lse, True)
+
+
+def test_large_scores_and_scale_ranges():
+    """Scores of hundreds (the running maximum moves far), pages whose V scales differ by 2^40 or are 0."""
+    c = make(8, 2, 128, 16, [600], [6], [F8, I8], W.BF16, seed=150)
+    rng = np.random.default_rng(5)
+    for pool in c.pools:
+        codes, meta = c.opools[pool.codec]
+        meta[:, 1] *= 2.0 ** rng.integers(-20, 21, size=meta[:, 1].shape)
+        meta[::3, 1] = 0
+        meta[:, 0] *= 2.0 ** rng.integers(0, 7, size=meta[:, 0].shape)
+        meta[1::4, 0] = 0
+        pool.meta.copy_(torch.from_numpy(meta))
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+
+
+def test_a_softmax_scale_of_zero_averages():
+    c = make(4, 1, 64, 16, [77], [4], [W.FP16], W.FP16, seed=160)
+    c.scale = 0.0
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+    assert torch.allclose(lse[3], torch.tensor(math.log2(77.0), device=DEV), atol=1e-5)
+
+
+def test_bad_slots_and_missing_pools_are_left_out_and_counted():
+    c = make(4, 2, 64, 16, [400, 130], [70, 2], [F8, I8], W.FP16, seed=170)
+    c.table[0, 3], c.table[0, 9], c.table[1, 8] = -1, 10000, -5       # the last one is the partial last page
+    c.page_codec[0, 5] = W.INT4_G32
+    c.page_codec[1, 2] = W.BF16                                       # no such pool in the call
+    c.page_codec[1, 3] = 200
+    c.d_table, c.d_codec = torch.from_numpy(c.table).to(DEV), torch.from_numpy(c.page_codec).to(DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out, lse = run(c, True, status=status)
+    check(c, out, lse, True, expect_bad=6)
+    assert int(status) == 6
+
+
+def test_strided_queries():
+    c = make(8, 2, 128, 16, [100, 300], [3, 9], [F8], W.BF16, seed=180)
+    wide = torch.full((12, 12, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, 1:9] = c.q
+    dense, dl = run(c, True)
+    out, lse = run(c, True, q=wide[:, 1:9])
+    assert torch.equal(out, dense) and torch.equal(lse, dl)
+
+
+@pytest.mark.parametrize("batch", [40, 700])
+def test_many_sequences(batch):
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 60, batch).tolist()
+    new = [int(rng.integers(0, min(n, 4) + 1)) for n in lens]
+    c = make(4, 2, 64, 16, lens, new, [W.FP16, I8], W.FP16, seed=190)
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+
+
+def test_one_token_equals_the_decode_call():
+    from paged_cases import run_decode
+    c = make(32, 4, 128, 64, [1000, 64, 777], [1, 1, 1], [W.BF16, F8, I8], W.BF16, seed=200)
+    out, lse = run(c, True)
+    check(c, out, lse, True)
+    _, o32, dl, _ = run_decode(c, out_dtype=torch.bfloat16)
+    # two roundings to bf16 apart (p and the output), each half a step of values up to sum p|v| <= max |v|
+    assert (out.float() - o32).abs().max() <= 2 * 2.0 ** -8 * 6.0
+    assert torch.allclose(lse, dl, atol=1e-4)
+
+
+def test_a_long_chunk_at_sampled_rows():
+    """600 new tokens over 9,000 cached ones, three tiers: rows checked at the ends and between."""
+    c = make(16, 2, 128, 64, [9000], [600], [W.BF16, F8, I8], W.BF16, seed=210)
+    out, lse = run(c, True)
+    rows = [0, 1, 15, 16, 299, 583, 599]
+    q64 = c.to64(W.to_bits(c.q))
+    for t in rows:
+        sub = np.array([0, 1])
+        ref, rl, _, av, qk, smax = oracle.paged_extend(q64[t:t + 1], sub, c.Hkv, c.P, c.opools, c.page_codec, c.table,
+                                                       [9000 - 600 + t + 1], c.scale, True)
+        e = (math.log(2) * (c.D * 2.0 ** -23 * qk + 2.0 ** -22 * smax) + 2.0 ** -21)[..., None]
+        bound = 2.0 ** -8 * (av + np.abs(ref)) + 2 * e * av + 1e-38
+        assert np.all(np.abs(out[t:t + 1].float().cpu().numpy() - ref) <= bound), t
+        assert np.abs(lse[t:t + 1].cpu().numpy() - rl).max() <= 1e-3
+
+
+def test_streams_graphs_and_repeats():
+    """The same bits on another stream, from a captured graph with new inputs, and with a dirty workspace."""
+    c = make(8, 2, 128, 16, [2000, 333, 64], [4, 20, 64], [W.BF16, F8], W.BF16, seed=220)
+    ref, rl = run(c, True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out, lse = run(c, True, stream=s)
+    assert torch.equal(out, ref) and torch.equal(lse, rl)
+    args = argus.extend_args(c.g, c.q, torch.from_numpy(c.q_start).to(DEV), c.pools, c.d_codec, c.d_table, c.d_lens,
+                             c.max_pages, c.scale, out, lse2_out=lse)
+    ws = torch.empty(argus.extend_workspace_bytes(args), dtype=torch.uint8, device=DEV)
+    with torch.cuda.stream(s):
+        argus.paged_extend_attn(args, ws)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        argus.paged_extend_attn(args, ws)
+    for shift in (0, 1):
+        if shift:      # other lengths in the same graph
+            c.lens = np.array([1999, 200, 64])
+            c.d_lens.copy_(torch.tensor([1999, 200, 64], dtype=torch.int32))
+        out.fill_(float("nan"))
+        lse.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        if not shift:
+            assert torch.equal(out, ref) and torch.equal(lse, rl)
+        check(c, out, lse, True)
