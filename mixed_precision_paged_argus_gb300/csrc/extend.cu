@@ -37,19 +37,24 @@ constexpr int kBM = 128;             // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;             // keys per block
 constexpr int kGroupWarps = 4;       // one softmax warpgroup: a thread per TMEM lane
 constexpr int kSoftmaxWarps = 2 * kGroupWarps;
-constexpr int kLoadWarps = 8;        // one per 16-token chunk of a block
+constexpr int kLoadWarps = 8;        // four for K, four for V: two 16-token chunks of a block each
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
+// 17 warps get 96 registers a thread at launch; the loaders' four-warp groups give
+// up what the softmax groups take: 256 * 120 + 256 * 72 = 512 * 96
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kLoadRegs = 72;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs) <= 32 * (kSoftmaxWarps + kLoadWarps) * kLaunchRegs, "registers");
 constexpr int kHalf = kBM * 64 * 2;  // 128 rows x 64 dims: one 128-byte swizzle column
 constexpr int kTmemCols = 512;       // S0 S1 O0 O1, 128 columns each
 constexpr float kRescaleThreshold = 8.f;
-constexpr int kScaleSlots = 4;       // blocks whose page scales are kept
+constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chunk's sum is kept apart
+constexpr int kScaleSlots = 8;       // blocks whose page scales are kept
 constexpr int kMergePad = 20;        // floats per row of the replica merge (16 used; conflict-free vectors)
 
 template <int D, bool W16>
 struct Smem {
   static constexpr int kTile = kBM * D * 2;
-  // a loader warp's raw ring: kAhead blocks of a K and a V chunk (16 rows each)
+  // a loader warp's raw ring: two chunks (16 rows each) of kAhead blocks
   static constexpr int kSlot = 16 * D * (W16 ? 2 : 1);
   static constexpr int kAhead = (128 / D) * (W16 ? 1 : 2);
   static constexpr int kRing = 2 * kAhead * kSlot;
@@ -58,7 +63,7 @@ struct Smem {
   static constexpr int kOffV = kOffK + 2 * kTile;
   static constexpr int kOffRaw = kOffV + 2 * kTile;
   static constexpr int kOffScale = kOffRaw + kLoadWarps * kRing;
-  static constexpr int kOffML = kOffScale + kScaleSlots * 8 * 16;
+  static constexpr int kOffML = kOffScale + kScaleSlots * 8 * 12;
   static constexpr int kOffBar = kOffML + 2 * kBM * 8;
   // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drain
   static constexpr int kNumBars = 16;
@@ -289,61 +294,94 @@ __device__ __forceinline__ bool group_bar_any(int id, int n, bool x) {
 // row 128 bytes, vectors permuted by the row (128-byte swizzle)
 __device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)((c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
-// One chunk (16 rows of K or V) from the lane's raw vectors to the tile; rows
-// from n_rows on become zeros (P is 0 there, and 0 times what the page holds
-// behind the sequence would be NaN if that is).
-template <int D, bool BF>
-__device__ __forceinline__ void convert_chunk(uint32_t raw, uint32_t tile, int chunk, int lane, int codec, int n_rows) {
-  if (codec <= ARGUS_BF16) {
+// How a loader lane's vectors lie: step s of a chunk moves 512 raw bytes, lane L
+// the 16-byte vector piece_of(s, L) of the chunk's rows; raw slots are in lane order,
+// so that a lane reads back what it copied itself (no barrier in between).
+// The lanes are dealt so that eight neighbours store to eight different banks:
+// two rows by four vectors of one 64-dim half.
+template <int D, int VB>   // VB: 16-byte vectors of a raw row
+__device__ __forceinline__ int lane_row(int lane) {
+  if (VB == 4) return lane >> 2;
+  if (VB == 8) return D == 64 ? lane >> 3 : 2 * (lane >> 4) + ((lane >> 2) & 1);
+  return lane >> 4;
+}
+template <int D, int VB>
+__device__ __forceinline__ int lane_vec(int lane) {
+  if (VB == 4) return lane & 3;
+  if (VB == 8) return D == 64 ? lane & 7 : 4 * ((lane >> 3) & 1) + (lane & 3);
+  return lane & 15;
+}
+
+// One chunk (16 rows of K or V) from the lane's raw vectors to the tile at
+// `tile` (its row 0 of the chunk); rows from n_rows on become zeros (P is 0
+// there, and 0 times what the page holds behind the sequence would be NaN if
+// that is).  All raw vectors are read first: a read behind a store would wait
+// for it.
+template <int D, bool BF, int CODEC>
+__device__ __forceinline__ void convert_chunk(uint32_t raw, uint32_t tile, int lane, int n_rows) {
+  constexpr int VB = CODEC <= ARGUS_BF16 ? D / 8 : D / 16;   // vectors per raw row
+  constexpr int STEPS = VB / 2, ROWS = 32 / VB;              // rows per step
+  const int r0 = lane_row<D, VB>(lane), j = lane_vec<D, VB>(lane);
+  uint4 v[STEPS];
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const int f = s * 32 + lane, r = f / (D / 8), c = f % (D / 8);
-      uint4 v = lds16(raw + f * 16);
-      if (r >= n_rows) v = make_uint4(0, 0, 0, 0);
-      sts16(tile + tile_off(chunk * 16 + r, c), v.x, v.y, v.z, v.w);
-    }
-  } else {
+  for (int s = 0; s < STEPS; ++s) v[s] = lds16(raw + s * 512);
+  if (n_rows < 16) {
 #pragma unroll
-    for (int s = 0; s < D / 32; ++s) {
-      const int f = s * 32 + lane, r = f / (D / 16), j = f % (D / 16);
-      uint4 v = lds16(raw + f * 16);
-      if (r >= n_rows) v = make_uint4(0, 0, 0, 0);
+    for (int s = 0; s < STEPS; ++s)
+      if (r0 + s * ROWS >= n_rows) v[s] = make_uint4(0, 0, 0, 0);
+  }
+  // the first 16-byte vector of the tile that this lane writes: vector c of row
+  // r0; rows further down are 128 bytes apart, and their permutation differs
+  // by the row's low bits
+  const int c = CODEC <= ARGUS_BF16 ? j : 2 * j;
+  const uint32_t base = tile + (c >> 3) * kHalf + r0 * 128;
+  const uint32_t off = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
+    if constexpr (CODEC <= ARGUS_BF16) {
+      sts16(at, v[s].x, v[s].y, v[s].z, v[s].w);
+    } else {
       uint32_t o[8];
-      if (codec == ARGUS_FP8_E4M3) {
-        fp8_to_16<BF>(v.x, o[0], o[1]);
-        fp8_to_16<BF>(v.y, o[2], o[3]);
-        fp8_to_16<BF>(v.z, o[4], o[5]);
-        fp8_to_16<BF>(v.w, o[6], o[7]);
-      } else {
-        int8_to_16<BF>(v.x, o[0], o[1]);
-        int8_to_16<BF>(v.y, o[2], o[3]);
-        int8_to_16<BF>(v.z, o[4], o[5]);
-        int8_to_16<BF>(v.w, o[6], o[7]);
+      const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (CODEC == ARGUS_FP8_E4M3) fp8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
+        else int8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
       }
-      // lanes of the second half store their odd vector first: eight lanes then
-      // hit eight different 16-byte banks
-      const int sw = (D == 128 && j >= 4) ? 1 : 0;
-      const uint32_t a0 = tile + tile_off(chunk * 16 + r, 2 * j + sw), a1 = tile + tile_off(chunk * 16 + r, 2 * j + 1 - sw);
-      sts16(a0, sw ? o[4] : o[0], sw ? o[5] : o[1], sw ? o[6] : o[2], sw ? o[7] : o[3]);
-      sts16(a1, sw ? o[0] : o[4], sw ? o[1] : o[5], sw ? o[2] : o[6], sw ? o[3] : o[7]);
+      sts16(at, o[0], o[1], o[2], o[3]);
+      sts16(at ^ 16u, o[4], o[5], o[6], o[7]);
     }
   }
 }
 
-// what a loader warp knows of its chunk of a block
-struct Chunk {
-  int codec, slot, row, n_rows, h, first;   // n_rows 0: nothing to read; first: counts a bad page
+// A loader warp looks its pages up for 16 blocks of an item at once, a lane per
+// chunk (lane = 2 * block + chunk of the warp's pair): the two dependent reads
+// (table, then scales) are paid once per 16 blocks.
+struct Lookup {
+  int count;                         // blocks
+  int codec, slot, row, n_rows, h, first;   // first: this chunk counts a page that cannot be read
 };
-struct Loaded {
-  int codec, n_rows;                        // n_rows 0: an empty chunk, -1: a page that cannot be read
-  float ks, vs;
+struct Found {
+  int count;
+  unsigned long long src;
+  int state;                         // codec | rows << 8 (0: nothing to read) | kBad
+  float ks, vs, lvs;                 // score scale, V scale, its log2; ks < 0: not to be read
 };
+constexpr int kBad = 1 << 16;
 
+// BF: q and out are bf16, else fp16.  W16: the call has a 16-bit pool.  The
+// operands are bf16 only where bf16 pages ask for it: over 8-bit pages alone a bf16
+// query becomes fp16 times a power of two per row (its 8 bits fit, and what is
+// 2^-29 of the row's largest element does not count), because e4m3 codes
+// turn into fp16 with one conversion per pair, into bf16 with five operations,
+// and fp16 P has three more bits.
 template <int D, bool BF, bool W16>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   using SM = Smem<D, W16>;
   constexpr int kTile = SM::kTile;
-  constexpr float kPBias = BF ? 0.f : 7.f;   // fp16 P is stored as P * 2^7 (at most 2^15)
+  constexpr bool BFM = BF && W16;            // operand type of the MMAs
+  constexpr float kPBias = BFM ? 0.f : 7.f;  // fp16 P is stored as P * 2^7 (at most 2^15)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {         // the swizzled tiles need it, and there is no room to round up
     if (threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusTimeoutBit);
@@ -362,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
   volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
-  float4* scales = reinterpret_cast<float4*>(smem + SM::kOffScale);     // [slot][chunk]: ks, vs, log2 vs
+  float2* scales = reinterpret_cast<float2*>(smem + SM::kOffScale);     // [slot][chunk]: ks (< 0: not to be read), vs
+  float* log_vs = reinterpret_cast<float*>(scales + kScaleSlots * 8);   // log2 vs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -379,9 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   if (threadIdx.x == 32) {
     mbar_init(q_full, kSoftmaxWarps);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&k_full[b], kLoadWarps);
+      mbar_init(&k_full[b], kLoadWarps / 2);
       mbar_init(&k_empty[b], 1);
-      mbar_init(&v_full[b], kLoadWarps);
+      mbar_init(&v_full[b], kLoadWarps / 2);
       mbar_init(&v_empty[b], 1);
       mbar_init(&s_full[b], 1);
       mbar_init(&p_full[b], kGroupWarps);
@@ -411,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     // ---------------------------------------------------------- MMA issuer
     // within an item: S0, S1, then per block i: P.V of i, S of i + 2
     if (lane == 0) {
-      constexpr uint32_t idQK = idesc_f16kind(BF, false, kBN);
-      constexpr uint32_t idPV = idesc_f16kind(BF, true, D);
+      constexpr uint32_t idQK = idesc_f16kind(BFM, false, kBN);
+      constexpr uint32_t idPV = idesc_f16kind(BFM, true, D);
       const uint32_t q_s = smem_u32(smem + SM::kOffQ);
       Cursor c;
       c.start(p, misc[2], misc64[2], n_blocks);
@@ -465,118 +504,141 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     }
   } else if (warp >= kSoftmaxWarps) {
     // ---------------------------------------------------------- loaders
-    const int ch = warp - kSoftmaxWarps;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    const int lw = warp - kSoftmaxWarps;
+    const bool is_v = lw >= kLoadWarps / 2;
+    const int ch0 = 2 * (lw & (kLoadWarps / 2 - 1));   // the warp's chunks: ch0, ch0 + 1
     constexpr int A = SM::kAhead;
-    const uint32_t ring = smem_u32(smem + SM::kOffRaw + ch * SM::kRing);
+    const uint32_t ring = smem_u32(smem + SM::kOffRaw + lw * SM::kRing);
+    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK));
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
     Cursor c;
     c.start(p, misc[2], misc64[2], n_blocks);
     auto look = [&]() {
-      Chunk k;
-      k.codec = -1;
-      k.slot = -1;
-      k.row = 0;
+      Lookup k;
+      k.count = (int)max(0ll, min(min(16ll, (long long)(c.nb - c.blk)), c.left));
+      k.codec = k.slot = -1;
+      k.row = k.n_rows = k.first = 0;
       k.h = c.h;
-      k.first = 0;
-      k.n_rows = 0;
-      if (c.left <= 0) return k;
-      const int key = c.blk * kBN + ch * 16;
-      k.n_rows = min(max(c.s.len - key, 0), 16);
-      if (k.n_rows > 0) {
-        const int page = key / p.P;
-        k.row = key - page * p.P;
-        const size_t e = (size_t)c.b * p.max_pages + page;
-        k.codec = p.page_codec[e];
-        k.slot = p.block_table[e];
-        k.first = c.h == 0 && c.t == c.T - 1 && k.row == 0;
-      }
-      c.advance(p, 1);
-      return k;
-    };
-    const uint8_t* src = nullptr;      // K chunk of the block being issued
-    long long v_off = 0;
-    auto copy = [&](const Loaded& l, const uint8_t* from, uint32_t to) {
-      if (l.n_rows > 0) {
-        if (W16 && l.codec <= ARGUS_BF16) {
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s) cp_async16(to + (s * 32 + lane) * 16, from + (s * 32 + lane) * 16);
-        } else {
-#pragma unroll
-          for (int s = 0; s < D / 32; ++s) cp_async16(to + (s * 32 + lane) * 16, from + (s * 32 + lane) * 16);
+      if (lane / 2 < k.count) {
+        const int key = (c.blk + lane / 2) * kBN + (ch0 + (lane & 1)) * 16;
+        k.n_rows = min(max(c.s.len - key, 0), 16);
+        if (k.n_rows > 0) {
+          const int page = key / p.P;
+          k.row = key - page * p.P;
+          const size_t e = (size_t)c.b * p.max_pages + page;
+          k.codec = p.page_codec[e];
+          k.slot = p.block_table[e];
+          k.first = c.h == 0 && c.t == c.T - 1 && k.row == 0;
         }
       }
-      cp_async_commit();
+      if (k.count > 0) c.advance(p, k.count);
+      return k;
     };
-    auto resolve = [&](const Chunk& k) {
-      Loaded l;
-      l.codec = k.codec;
-      l.n_rows = k.n_rows;
-      l.ks = l.vs = 1.f;
+    auto resolve = [&](const Lookup& k) {
+      Found f;
+      f.count = k.count;
+      f.src = 0;
+      f.state = 0;
+      f.ks = f.vs = 1.f;
       if (k.n_rows > 0) {
         const bool known = k.codec <= ARGUS_INT8 && (W16 || k.codec >= ARGUS_FP8_E4M3);
-        if (!known || k.slot < 0 || k.slot >= p.pool[k.codec & 3].n_slots) {
-          l.n_rows = -1;
-          if (k.first && lane == 0 && p.status) atomicAdd(p.status, 1u);
+        const PoolRef r = p.pool[k.codec & 3];
+        if (!known || k.slot < 0 || k.slot >= r.n_slots) {
+          f.state = kBad;
+          if (k.first && !is_v && p.status) atomicAdd(p.status, 1u);
         } else {
-          const PoolRef& r = p.pool[k.codec & 3];
           const int rb = k.codec <= ARGUS_BF16 ? 2 * D : D;
           const long long unit = (long long)k.slot * 2 * p.Hkv + k.h;
-          src = r.codes + (unit * p.P + k.row) * rb;
-          v_off = (long long)p.Hkv * p.P * rb;
-          if (k.codec >= ARGUS_FP8_E4M3) {
-            l.ks = r.meta[unit];
-            l.vs = r.meta[unit + p.Hkv];
+          f.src = reinterpret_cast<unsigned long long>(r.codes + ((unit + (is_v ? p.Hkv : 0)) * p.P + k.row) * rb);
+          f.state = k.codec | k.n_rows << 8;
+          if (!is_v && k.codec >= ARGUS_FP8_E4M3) {
+            f.ks = r.meta[unit];
+            f.vs = r.meta[unit + p.Hkv];
           }
         }
       }
-      return l;
+      f.lvs = log2f(f.vs);             // 0: -inf
+      f.ks = f.state == kBad ? -1.f : f.ks * p.scale_log2;
+      return f;
     };
-    Loaded queue[A];
-    Chunk next = look();
+    Lookup ahead = look();
+    Found now = resolve(ahead);
+    ahead = look();
+    int at = 0;                        // block of `now` that is issued next
+    long long ib = 0;                  // its number
+    // chunk `sub` of the next block: its bytes on their way; returns its state
+    auto issue = [&](int sub, uint32_t to) {
+      int state = 0;
+      if (ib < n_blocks) {
+        if (at == now.count) {
+          now = resolve(ahead);
+          ahead = look();
+          at = 0;
+        }
+        const int from = 2 * at + sub;
+        state = __shfl_sync(0xffffffffu, now.state, from);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, now.src, from));
+        if (!is_v && lane == from) {
+          const int x = (int)(ib % kScaleSlots) * 8 + ch0 + sub;
+          scales[x] = make_float2(now.ks, now.vs);
+          log_vs[x] = now.lvs;
+        }
+        if (state & 0xFF00) {
+          if (W16 && (state & 0xFF) <= ARGUS_BF16) {
+            const uint8_t* at16 = src + (lane_row<D, D / 8>(lane) * (D / 8) + lane_vec<D, D / 8>(lane)) * 16;
 #pragma unroll
-    for (int f = 0; f < A; ++f) {
-      queue[f] = resolve(next);
-      next = look();
-      copy(queue[f], src, ring + 2 * f * SM::kSlot);
-      copy(queue[f], src + v_off, ring + (2 * f + 1) * SM::kSlot);
-    }
+            for (int s = 0; s < D / 16; ++s) cp_async16(to + s * 512, at16 + s * 512);
+          } else {
+            const uint8_t* at8 = src + (lane_row<D, D / 16>(lane) * (D / 16) + lane_vec<D, D / 16>(lane)) * 16;
+#pragma unroll
+            for (int s = 0; s < D / 32; ++s) cp_async16(to + s * 512, at8 + s * 512);
+          }
+        }
+        if (sub == 1) { ++at; ++ib; }
+      }
+      cp_async_commit();
+      return state;
+    };
+    int queue[2 * A];
+#pragma unroll
+    for (int f = 0; f < 2 * A; ++f) queue[f] = issue(f & 1, ring + f * SM::kSlot + lane * 16);
     for (long long i = 0; i < n_blocks; ++i) {
-      const int b = (int)(i & 1), at = (int)(i % A);
-      const uint32_t raw_k = ring + 2 * at * SM::kSlot, raw_v = raw_k + SM::kSlot;
-      const Loaded cur = queue[0];
-      const Loaded ahead = resolve(next);
-      next = look();
-      const uint32_t par = (uint32_t)((i >> 1) - 1) & 1;
-      cp_async_wait<2 * A - 1>();
-      if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&k_empty[b], par, &misc[1]))) { misc[1] = 1; break; }
-      convert_chunk<D, BF>(raw_k, smem_u32(smem + SM::kOffK + b * kTile), ch, lane, W16 ? cur.codec : max(cur.codec, 2), max(cur.n_rows, 0));
-      if (lane == 0) {
-        const float lvs = log2f(fminf(fmaxf(cur.vs, 0x1p-64f), 0x1p64f));
-        scales[(int)(i % kScaleSlots) * 8 + ch] = make_float4(cur.n_rows < 0 ? -1.f : cur.ks * p.scale_log2, cur.vs, lvs, 0.f);
+      const int b = (int)(i & 1);
+      const uint32_t raw = ring + (uint32_t)(i % A) * 2 * SM::kSlot + lane * 16;
+      if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]))) { misc[1] = 1; break; }
+#pragma unroll
+      for (int sub = 0; sub < 2; ++sub) {
+        const int state = queue[0], codec = state & 0xFF, n_rows = (state >> 8) & 0xFF;
+        const uint32_t at_raw = raw + sub * SM::kSlot, tile = tiles + b * kTile + (ch0 + sub) * 2048;
+        cp_async_wait<2 * A - 1>();
+        // a chunk without rows: K is masked, V is set to zero
+        if (n_rows > 0 || is_v) {
+          if (W16 && codec <= ARGUS_BF16) convert_chunk<D, BFM, ARGUS_BF16>(at_raw, tile, lane, n_rows);
+          else if (codec == ARGUS_INT8) convert_chunk<D, BFM, ARGUS_INT8>(at_raw, tile, lane, n_rows);
+          else convert_chunk<D, BFM, ARGUS_FP8_E4M3>(at_raw, tile, lane, n_rows);
+        }
+        const int nxt = issue(sub, at_raw);
+#pragma unroll
+        for (int f = 0; f + 1 < 2 * A; ++f) queue[f] = queue[f + 1];
+        queue[2 * A - 1] = nxt;
       }
       fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[b]);
-      copy(ahead, src, raw_k);
-      cp_async_wait<2 * A - 1>();
-      if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&v_empty[b], par, &misc[1]))) { misc[1] = 1; break; }
-      convert_chunk<D, BF>(raw_v, smem_u32(smem + SM::kOffV + b * kTile), ch, lane, W16 ? cur.codec : max(cur.codec, 2), max(cur.n_rows, 0));
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[b]);
-      copy(ahead, src + v_off, raw_v);
-#pragma unroll
-      for (int f = 0; f + 1 < A; ++f) queue[f] = queue[f + 1];
-      queue[A - 1] = ahead;
+      if (lane == 0) mbar_arrive(&full[b]);
     }
     cp_async_wait<0>();
   } else {
     // ---------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int grp = warp / kGroupWarps, wq = warp % kGroupWarps;
-    const int lane_row = wq * 32 + lane;               // TMEM lane
+    const int tl = wq * 32 + lane;                     // TMEM lane
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t sS = tS(grp) + lane_off, sO = tO(grp) + lane_off;
     const uint32_t q_s = smem_u32(smem + SM::kOffQ);
     float* merge = reinterpret_cast<float*>(smem + SM::kOffQ) + grp * 96 * kMergePad;
+    float* q_scale = reinterpret_cast<float*>(smem + SM::kOffML);
     Cursor c;
     c.start(p, misc[2], misc64[2], n_blocks);
     long long n0 = 0;
@@ -587,26 +649,64 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int rows = (int)min((long long)kBM, R - lin0);
       const int nrep = replicas(rows), per = kBM / nrep;
       // ---- Q tile: row l of the tile in lanes l, l + per, ...; zeros behind the last row
-      for (int f = threadIdx.x; f < kBM * (D / 8); f += kSoftmaxWarps * 32) {
+#pragma unroll
+      for (int x = 0; x < kBM * (D / 8) / (kSoftmaxWarps * 32); ++x) {
+        const int f = x * kSoftmaxWarps * 32 + threadIdx.x;
         const int pr = f / (D / 8), v = f % (D / 8), l = pr & (per - 1);
-        uint4 x = make_uint4(0, 0, 0, 0);
+        uint4 q = make_uint4(0, 0, 0, 0);
         if (l < rows) {
           const int lin = (int)lin0 + l, tok = lin / p.G, g = lin - tok * p.G;
-          x = *reinterpret_cast<const uint4*>(p.q + (long long)(c.s.q0 + tok) * p.qs + (c.h * p.G + g) * D + v * 8);
+          q = *reinterpret_cast<const uint4*>(p.q + (long long)(c.s.q0 + tok) * p.qs + (c.h * p.G + g) * D + v * 8);
         }
-        sts16(q_s + tile_off(pr, v), x.x, x.y, x.z, x.w);
+        if (BF && !BFM) {
+          // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
+          uint32_t w[4] = {q.x, q.y, q.z, q.w}, mx = 0;   // magnitudes of bf16 order like their bits
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+#pragma unroll
+          for (int o = D / 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int ex = max((int)(mx >> 23), 15);        // biased; from 15 on 2^(141 - ex) is a normal number
+          const float f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
+          q = make_uint4(w[0], w[1], w[2], w[3]);
+          if (v == 0) q_scale[pr] = 1.f / f1;
+        }
+        sts16(q_s + tile_off(pr, v), q.x, q.y, q.z, q.w);
       }
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
+      float qf = 1.f;
+      if (BF && !BFM) {
+        group_bar(1, kSoftmaxWarps * 32);
+        qf = q_scale[tl];
+        group_bar(1, kSoftmaxWarps * 32);              // (m, l) of the item lie there too
+      }
 
-      const int l_row = lane_row & (per - 1);          // row within the tile
-      const int rep = lane_row / per;                  // this lane's replica: keys of chunks [c0, c1)
+      const int l_row = tl & (per - 1);          // row within the tile
+      const int rep = tl / per;                  // this lane's replica: keys of chunks [c0, c1)
       const int c0 = rep * (8 / nrep), c1 = c0 + 8 / nrep;
       // rows behind the last one (zero queries) see what the last one sees: they are never written
       const int tok = min((int)((lin0 + l_row) / p.G), c.s.n - 1);
       const int vis_last = min(p.causal ? c.s.len - c.s.n + tok : c.s.len - 1, c.s.len - 1);
-      float m = -INFINITY, la = 0.f, lb = 0.f;
+      // running reference and sum; the sum of chunks with a V scale far from 1 is
+      // kept apart, with a reference of its own: relative to m (which bounds p
+      // times the scale) it could leave the fp32 range, and a page whose V is 0 must
+      // not push every other page's P out of the 16-bit range
+      float m = -INFINITY, la = 0.f, lb = 0.f, mz = -INFINITY, lz = 0.f;
+      auto scale_acc = [&](float r) {
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t v[32];
+          tmem_ld32(sO + x * 32, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * r);
+          tmem_st32(sO + x * 32, v);
+        }
+        tmem_wait_st();
+      };
       int last = -1;                                   // this group's last block (local)
       for (int i = (int)((grp - n0) & 1); i < nb; i += 2) {
         const long long n = n0 + i;
@@ -614,17 +714,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tc_fence_after();
         last = i;
         const int k0 = (c.blk + i) * kBN;
-        const float4* sc = scales + (int)(n % kScaleSlots) * 8;
-        bool flagged = false;
-        for (int cc = c0; cc < c1; ++cc) flagged |= sc[cc].x < 0.f;
-        const bool edge = __any_sync(0xffffffffu, k0 + c1 * 16 - 1 > vis_last) || flagged;   // uniform
+        const float2* sc = scales + (int)(n % kScaleSlots) * 8;
+        const float* lv = log_vs + (int)(n % kScaleSlots) * 8;
+        bool flagged = false;                          // uniform across the warp
+        for (int cc = c0; cc < c1; ++cc) flagged |= sc[cc].x < 0.f || fabsf(lv[cc]) > kFarScale;
+        const bool edge = __any_sync(0xffffffffu, k0 + c1 * 16 - 1 > vis_last) || flagged;
         const int lim = vis_last - k0;                 // keys e <= lim of the block are visible
         // pass 1: maximum of score + log2 of the V scale, so that P times that scale stays in range
         float mj = -INFINITY;
         for (int cc = c0; cc < c1; cc += 2) {
           uint32_t v[32];
           tmem_ld32(sS + cc * 16, v);
-          const float4 s0 = sc[cc], s1 = sc[cc + 1];
+          const float2 s0 = sc[cc], s1 = sc[cc + 1];
+          const float l0 = lv[cc], l1 = lv[cc + 1];
           tmem_wait_ld();
           if (!edge) {
             float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
@@ -635,12 +737,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
               b0 = max3(b0, __uint_as_float(v[16 + e]), __uint_as_float(v[16 + e + 1]));
               b1 = max3(b1, __uint_as_float(v[16 + e + 2]), __uint_as_float(v[16 + e + 3]));
             }
-            mj = max3(mj, fmaf(fmaxf(a0, a1), s0.x, s0.z), fmaf(fmaxf(b0, b1), s1.x, s1.z));
+            mj = max3(mj, fmaf(fmaxf(a0, a1), s0.x * qf, l0), fmaf(fmaxf(b0, b1), s1.x * qf, l1));
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              const float4 s = e < 16 ? s0 : s1;
-              if (cc * 16 + e <= lim && s.x >= 0.f) mj = fmaxf(mj, fmaf(__uint_as_float(v[e]), s.x, s.z));
+              const float ks = e < 16 ? s0.x : s1.x;
+              if (cc * 16 + e <= lim && ks >= 0.f) mj = fmaxf(mj, fmaf(__uint_as_float(v[e]), ks * qf, e < 16 ? l0 : l1));
             }
           }
         }
@@ -649,16 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         if (__any_sync(0xffffffffu, scale_o)) {
           // this block's scores are complete, hence also the group's P.V before them
           const float r = scale_o ? fast_exp2(m - mj) : 1.f;
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t v[32];
-            tmem_ld32(sO + x * 32, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * r);
-            tmem_st32(sO + x * 32, v);
-          }
-          tmem_wait_st();
+          scale_acc(r);
           la *= r;
           lb *= r;
         }
@@ -674,27 +767,45 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         for (int cc = c0; cc < c1; ++cc) {
           uint32_t v[16], o[8];
           tmem_ld16(sS + cc * 16, v);
-          const float4 s = sc[cc];
+          const float2 s = sc[cc];
+          const float kq = s.x * qf;
           tmem_wait_ld();
           if (!edge) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               float x0, x1, p0, p1;
-              f2_fma(x0, x1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), s.x, s.x, -mm, -mm);
+              f2_fma(x0, x1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), kq, kq, -mm, -mm);
               p0 = fast_exp2(x0);
               p1 = fast_exp2(x1);
               f2_add(la, lb, la, lb, p0, p1);
               f2_mul(p0, p1, p0, p1, s.y, s.y);
-              o[e] = BF ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+              o[e] = BFM ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
             }
           } else {
-            const bool see = m != -INFINITY && s.x >= 0.f;
+            const float lvc = lv[cc];
+            const bool far = fabsf(lvc) > kFarScale;
+            float x[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = (s.x >= 0.f && cc * 16 + e <= lim) ? __uint_as_float(v[e]) * kq : -INFINITY;
+            if (far) {
+              float top = mz;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e]);
+              if (top != -INFINITY) {
+                lz *= fast_exp2(mz - top);
+                mz = top;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) lz += fast_exp2(x[e] - top);
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float p0 = (see && cc * 16 + 2 * e <= lim) ? fast_exp2(fmaf(__uint_as_float(v[2 * e]), s.x, -mm)) : 0.f;
-              const float p1 = (see && cc * 16 + 2 * e + 1 <= lim) ? fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), s.x, -mm)) : 0.f;
-              f2_add(la, lb, la, lb, p0, p1);
-              o[e] = BF ? pack_bf16x2(p0 * s.y, p1 * s.y) : pack_f16x2(p0 * s.y, p1 * s.y);
+              const float shift = far ? lvc - mm : -mm, vs = far ? 1.f : s.y;
+              const float p0 = m == -INFINITY ? 0.f : fast_exp2(x[2 * e] + shift);
+              const float p1 = m == -INFINITY ? 0.f : fast_exp2(x[2 * e + 1] + shift);
+              if (!far) f2_add(la, lb, la, lb, p0, p1);
+              o[e] = BFM ? pack_bf16x2(p0 * vs, p1 * vs) : pack_f16x2(p0 * vs, p1 * vs);
             }
           }
           tmem_st8(sS + cc * 16, o);
@@ -709,7 +820,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tc_fence_after();
       }
       // references in the units that l was summed in
-      ml[grp * kBM + lane_row] = make_float2(m == -INFINITY ? -INFINITY : m - kPBias, la + lb);
+      float ref = m == -INFINITY ? -INFINITY : m - kPBias, sum = la + lb;
+      if (__any_sync(0xffffffffu, mz != -INFINITY)) {
+        const float top = fmaxf(ref, mz);
+        const float r = (mz == -INFINITY) ? 1.f : fast_exp2(ref - top);   // ref = -inf: 0
+        if (last >= 0) scale_acc(r);
+        if (mz != -INFINITY) {
+          sum = sum * r + lz * fast_exp2(mz - top);
+          ref = top;
+        }
+      }
+      ml[grp * kBM + tl] = make_float2(ref, sum);
       tc_fence_before();
       group_bar(1, kSoftmaxWarps * 32);
       tc_fence_after();
@@ -722,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         const float2 y = ml[(x & 1) * kBM + (x >> 1) * per + l_row];
         if (y.x != -INFINITY) l_all += y.y * fast_exp2(y.x - M);
       }
-      const float2 y0 = ml[lane_row], y1 = ml[kBM + lane_row];
+      const float2 y0 = ml[tl], y1 = ml[kBM + tl];
       const bool have = l_all > 0.f;
       const float inv = have ? 1.f / l_all : 0.f;
       const float w0 = (have && y0.x != -INFINITY) ? fast_exp2(y0.x - M) * inv : 0.f;

@@ -16,9 +16,9 @@ from .codecs import dequant_page
 
 
 def sequence_kv(Hkv, P, pools, page_codec, block_table, b, length):
-    """K, V float64 [Hkv][n][D], the positions of those n keys (pages that name no
-    slot are left out) and the number of such pages."""
-    K, V, pos, bad = [], [], [], 0
+    """K, V float64 [Hkv][n][D], the positions of those n keys, their pages' V scales
+    [Hkv][n] (1 for 16-bit pages) and the number of pages that name no slot (left out)."""
+    K, V, pos, vs, bad = [], [], [], [], 0
     for p in range((length + P - 1) // P):
         codec, slot = int(page_codec[b, p]), int(block_table[b, p])
         if codec not in pools or not 0 <= slot < pools[codec][0].shape[0]:
@@ -29,19 +29,21 @@ def sequence_kv(Hkv, P, pools, page_codec, block_table, b, length):
         K.append(np.stack([dequant_page(codec, codes, meta, slot, 0, h)[:n] for h in range(Hkv)]))
         V.append(np.stack([dequant_page(codec, codes, meta, slot, 1, h)[:n] for h in range(Hkv)]))
         pos.append(p * P + np.arange(n))
+        vs.append(np.repeat(np.ones(Hkv) if codec < 2 else np.asarray(meta[slot, 1], np.float64), n).reshape(Hkv, n))
     if not K:
-        return None, None, np.zeros(0, int), bad
-    return np.concatenate(K, 1), np.concatenate(V, 1), np.concatenate(pos), bad
+        return None, None, np.zeros(0, int), None, bad
+    return np.concatenate(K, 1), np.concatenate(V, 1), np.concatenate(pos), np.concatenate(vs, 1), bad
 
 
 def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, scale, causal=True):
     """q float64 [total][Hq][D].  Returns o, lse2, bad and, for error bounds,
-    av = sum_j p_j |v_j| (as o), qk = max_j scale log2(e) sum_d |q_d k_jd| and
+    av = sum_j p_j |v_j| and pc = max_j (p_j s_j) sum_j |v_j| / s_j with the V scales s_j
+    (as o, over sum_j p_j), qk = max_j scale log2(e) sum_d |q_d k_jd| and
     smax = max_j |score_j| in the log2 domain (as lse2).  Rows of no sequence and rows
     that see nothing have o = 0, lse2 = -inf."""
     total, Hq, D = q.shape
     G = Hq // Hkv
-    o, av = np.zeros(q.shape), np.zeros(q.shape)
+    o, av, pc = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     lse2 = np.full((total, Hq), -math.inf)
     qk, smax = np.zeros((total, Hq)), np.zeros((total, Hq))
     bad = 0
@@ -51,7 +53,7 @@ def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, s
         if t1 <= t0:
             continue
         L = max(0, min(int(seq_lens[b]), max_pages * P))
-        K, V, pos, nbad = sequence_kv(Hkv, P, pools, page_codec, block_table, b, L)
+        K, V, pos, vs, nbad = sequence_kv(Hkv, P, pools, page_codec, block_table, b, L)
         bad += nbad
         if K is None:
             continue
@@ -66,10 +68,13 @@ def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, s
                 w = np.exp(s - m)
                 w_sum = w.sum()
                 o[t, hq], av[t, hq] = w @ v / w_sum, w @ np.abs(v) / w_sum
+                f = vs[hq // G][keep]
+                codes = np.abs(v) / np.where(f > 0, f, 1.0)[:, None]
+                pc[t, hq] = (w * f).max() / w_sum * codes.sum(0)
                 lse2[t, hq] = (m + math.log(w_sum)) * LOG2E
                 qk[t, hq] = scale * LOG2E * (np.abs(k) @ np.abs(q[t, hq])).max()
                 smax[t, hq] = np.abs(s).max() * LOG2E
-    return o, lse2, bad, av, qk, smax
+    return o, lse2, bad, av, pc, qk, smax
 
 
 def rotate(x, positions, inv_freq, pair_axis, adjacent):
