@@ -162,10 +162,10 @@ __device__ __forceinline__ int find_seq(const EParams& p, long long& w) {
 struct Cursor {
   Seq s;
   int b, h, t, T, blk, nb;
-  long long left;                    // blocks of the range still ahead, this one counted
+  int left;                          // blocks of the range still ahead, this one counted
 
   // block `rest` of sequence b
-  __device__ __forceinline__ void start(const EParams& p, int b_, long long rest, long long left_) {
+  __device__ __forceinline__ void start(const EParams& p, int b_, long long rest, int left_) {
     b = b_;
     left = left_;
     s = load_seq(p, b);
@@ -197,6 +197,14 @@ struct Cursor {
       }
     }
     nb = tile_blocks(p, s, t);
+  }
+  // the cursor in shared memory: the softmax threads read of it what they need
+  // when they need it instead of holding it in registers across the block loop
+  __device__ __forceinline__ void store(volatile uint32_t* m) const {
+    m[0] = s.q0; m[1] = s.n; m[2] = s.len; m[3] = b; m[4] = h; m[5] = t; m[6] = T; m[7] = blk; m[8] = nb; m[9] = left;
+  }
+  __device__ __forceinline__ void load(const volatile uint32_t* m) {
+    s.q0 = m[0]; s.n = m[1]; s.len = m[2]; b = m[3]; h = m[4]; t = m[5]; T = m[6]; blk = m[7]; nb = m[8]; left = m[9];
   }
   // `n` blocks further, which end in this item or at its end
   __device__ __forceinline__ void advance(const EParams& p, int n) {
@@ -396,7 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
   uint64_t* drain = o_done + 2;
-  // [0] TMEM base, [1] error, [2] first sequence, [4..5] its block, [6..7] blocks of the range
+  // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] the first one's
+  // number within its sequence, [6..15] the softmax groups' cursor
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
   volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
@@ -412,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     if (lane == 0) {
       misc[2] = b;
       misc64[2] = w;
-      misc64[3] = w1 - w0;
+      misc[3] = (uint32_t)(w1 - w0);   // fewer than 2^31 (checked on the host)
     }
   }
   if (threadIdx.x == 32) {
@@ -440,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const long long n_blocks = misc64[3];
+  const int n_blocks = (int)misc[3];
   auto tS = [tmem](int b) { return tmem + 128u * (uint32_t)b; };
   auto tO = [tmem](int b) { return tmem + 256u + 128u * (uint32_t)b; };
 
@@ -455,9 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const uint32_t q_s = smem_u32(smem + SM::kOffQ);
       Cursor c;
       c.start(p, misc[2], misc64[2], n_blocks);
-      long long n0 = 0;                // blocks before this item's
+      int n0 = 0;                      // blocks before this item's
       bool ok = true;
-      auto issue_s = [&](long long n) {
+      auto issue_s = [&](int n) {
         const int b = (int)(n & 1);
         if (!mbar_wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         tc_fence_after();
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         mma_commit(&k_empty[b]);
         return true;
       };
-      auto issue_pv = [&](long long n, bool first) {
+      auto issue_pv = [&](int n, bool first) {
         const int b = (int)(n & 1);
         if (!mbar_wait(&v_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         if (!mbar_wait(&p_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         return true;
       };
       for (uint32_t item = 0; ok && c.left > 0; ++item) {
-        const int nb = (int)min((long long)(c.nb - c.blk), c.left);
+        const int nb = min(c.nb - c.blk, c.left);
         ok = mbar_wait(q_full, item & 1, &misc[1]);
         if (ok) ok = issue_s(n0);
         if (ok && nb > 1) ok = issue_s(n0 + 1);
@@ -517,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     c.start(p, misc[2], misc64[2], n_blocks);
     auto look = [&]() {
       Lookup k;
-      k.count = (int)max(0ll, min(min(16ll, (long long)(c.nb - c.blk)), c.left));
+      k.count = max(0, min(min(16, c.nb - c.blk), c.left));
       k.codec = k.slot = -1;
       k.row = k.n_rows = k.first = 0;
       k.h = c.h;
@@ -567,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     Found now = resolve(ahead);
     ahead = look();
     int at = 0;                        // block of `now` that is issued next
-    long long ib = 0;                  // its number
+    int ib = 0;                        // its number
     // chunk `sub` of the next block: its bytes on their way; returns its state
     auto issue = [&](int sub, uint32_t to) {
       int state = 0;
@@ -604,11 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     int queue[2 * A];
 #pragma unroll
     for (int f = 0; f < 2 * A; ++f) queue[f] = issue(f & 1, ring + f * SM::kSlot + lane * 16);
-    for (long long i = 0; i < n_blocks; ++i) {
-      const int b = (int)(i & 1);
+    for (int i = 0; i < n_blocks; ++i) {
+      const int b = i & 1;
       const uint32_t raw = ring + (uint32_t)(i % A) * 2 * SM::kSlot + lane * 16;
       if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]))) { misc[1] = 1; break; }
-#pragma unroll
+#pragma unroll 1
       for (int sub = 0; sub < 2; ++sub) {
         const int state = queue[0], codec = state & 0xFF, n_rows = (state >> 8) & 0xFF;
         const uint32_t at_raw = raw + sub * SM::kSlot, tile = tiles + b * kTile + (ch0 + sub) * 2048;
@@ -639,14 +648,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const uint32_t q_s = smem_u32(smem + SM::kOffQ);
     float* merge = reinterpret_cast<float*>(smem + SM::kOffQ) + grp * 96 * kMergePad;
     float* q_scale = reinterpret_cast<float*>(smem + SM::kOffML);
-    Cursor c;
-    c.start(p, misc[2], misc64[2], n_blocks);
-    long long n0 = 0;
+    if (warp == 0) {
+      Cursor c;
+      c.start(p, misc[2], misc64[2], n_blocks);
+      if (lane == 0) c.store(misc + 6);
+    }
+    int n0 = 0;
     bool alive = true;
-    while (c.left > 0) {
-      const int nb = (int)min((long long)(c.nb - c.blk), c.left);
-      const long long R = (long long)c.s.n * p.G, lin0 = (long long)c.t * kBM;
-      const int rows = (int)min((long long)kBM, R - lin0);
+    while (true) {
+      group_bar(1, kSoftmaxWarps * 32);
+      Cursor c;
+      c.load(misc + 6);
+      if (c.left <= 0) break;
+      const int nb = min(c.nb - c.blk, c.left), k_first = c.blk * kBN;
+      const int lin0 = c.t * kBM;                      // rows of a sequence and head: fewer than 2^31
+      const int rows = min(kBM, c.s.n * p.G - lin0);
       const int nrep = replicas(rows), per = kBM / nrep;
       // ---- Q tile: row l of the tile in lanes l, l + per, ...; zeros behind the last row
 #pragma unroll
@@ -655,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         const int pr = f / (D / 8), v = f % (D / 8), l = pr & (per - 1);
         uint4 q = make_uint4(0, 0, 0, 0);
         if (l < rows) {
-          const int lin = (int)lin0 + l, tok = lin / p.G, g = lin - tok * p.G;
+          const int lin = lin0 + l, tok = lin / p.G, g = lin - tok * p.G;
           q = *reinterpret_cast<const uint4*>(p.q + (long long)(c.s.q0 + tok) * p.qs + (c.h * p.G + g) * D + v * 8);
         }
         if (BF && !BFM) {
@@ -688,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int rep = tl / per;                  // this lane's replica: keys of chunks [c0, c1)
       const int c0 = rep * (8 / nrep), c1 = c0 + 8 / nrep;
       // rows behind the last one (zero queries) see what the last one sees: they are never written
-      const int tok = min((int)((lin0 + l_row) / p.G), c.s.n - 1);
+      const int tok = min((lin0 + l_row) / p.G, c.s.n - 1);
       const int vis_last = min(p.causal ? c.s.len - c.s.n + tok : c.s.len - 1, c.s.len - 1);
       // running reference and sum; the sum of chunks with a V scale far from 1 is
       // kept apart, with a reference of its own: relative to m (which bounds p
@@ -708,20 +724,21 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tmem_wait_st();
       };
       int last = -1;                                   // this group's last block (local)
-      for (int i = (int)((grp - n0) & 1); i < nb; i += 2) {
-        const long long n = n0 + i;
+      for (int i = (grp - n0) & 1; i < nb; i += 2) {
+        const int n = n0 + i;
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[grp], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; misc[1] = 1; break; }
         tc_fence_after();
         last = i;
-        const int k0 = (c.blk + i) * kBN;
+        const int k0 = k_first + i * kBN;
         const float2* sc = scales + (int)(n % kScaleSlots) * 8;
         const float* lv = log_vs + (int)(n % kScaleSlots) * 8;
-        bool flagged = false;                          // uniform across the warp
-        for (int cc = c0; cc < c1; ++cc) flagged |= sc[cc].x < 0.f || fabsf(lv[cc]) > kFarScale;
-        const bool edge = __any_sync(0xffffffffu, k0 + c1 * 16 - 1 > vis_last) || flagged;
+        // lanes c0 .. c1-1 look at their chunk, every lane at its row's last key
+        const bool odd = lane >= c0 && lane < c1 && (sc[lane].x < 0.f || fabsf(lv[lane]) > kFarScale);
+        const bool edge = __any_sync(0xffffffffu, odd || k0 + c1 * 16 - 1 > vis_last);
         const int lim = vis_last - k0;                 // keys e <= lim of the block are visible
         // pass 1: maximum of score + log2 of the V scale, so that P times that scale stays in range
         float mj = -INFINITY;
+#pragma unroll 1
         for (int cc = c0; cc < c1; cc += 2) {
           uint32_t v[32];
           tmem_ld32(sS + cc * 16, v);
@@ -760,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         const float mm = (m == -INFINITY) ? 0.f : m - kPBias;
         if (nrep > 1) {
           const uint32_t z[8] = {};
+#pragma unroll 1
           for (int cc = 0; cc < 8; ++cc)
             if (cc < c0 || cc >= c1) tmem_st8(sS + cc * 16, z);
         }
@@ -834,6 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       tc_fence_before();
       group_bar(1, kSoftmaxWarps * 32);
       tc_fence_after();
+      c.load(misc + 6);
       // ---- epilogue: both groups' and all replicas' sums of a row joined; group g takes half the dims
       const bool has0 = nb > 1 || (n0 & 1) == 0, has1 = nb > 1 || (n0 & 1) == 1;   // which groups had a block
       float M = -INFINITY;
@@ -851,9 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const bool whole = c.blk == 0 && nb == c.nb;
       const int piece = 2 * blockIdx.x + (c.blk == 0 ? 1 : 0);
       const bool writes = alive && rep == 0 && l_row < rows;
-      const long long lin = lin0 + l_row;
-      const int otok = (int)(lin / p.G);
-      const size_t orow = writes ? (size_t)(c.s.q0 + otok) * p.Hq + c.h * p.G + (int)(lin - (long long)otok * p.G) : 0;
+      const int lin = c.t * kBM + l_row, otok = lin / p.G;
+      const size_t orow = writes ? (size_t)(c.s.q0 + otok) * p.Hq + c.h * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         const int col = grp * (D / 2) + x * 16;
@@ -915,7 +933,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       tc_fence_before();
       if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) break;   // all leave, or none
       n0 += nb;
-      c.advance(p, nb);
+      if (warp == 0) {
+        c.load(misc + 6);
+        c.advance(p, nb);
+        __syncwarp();                                  // every lane has loaded
+        if (lane == 0) c.store(misc + 6);
+      }
     }
   }
 
@@ -1037,16 +1060,16 @@ static argus_status check(const argus_extend_args* a) {
   return ARGUS_OK;
 }
 
-// One CTA per SM, and no more than there can be key blocks: every query tile
-// has at most all its sequence's blocks.
-static int grid_size(const argus_extend_args* a) {
+// Upper bound of the key blocks of a call: every query tile has at most all of
+// its sequence's (fewer than 2^31 rows and 2^31 tokens: the product is below 2^63).
+static long long max_blocks(const argus_extend_args* a) {
   const long long G = a->g.n_q_heads / a->g.n_kv_heads;
   const long long tiles = ((long long)a->total_q * G + kBM - 1) / kBM + a->batch;
-  const long long blocks = std::max(1ll, ((long long)a->max_pages * a->g.page_tokens + kBN - 1) / kBN);
-  const long long sms = device_sm_count();
-  const long long most = tiles * a->g.n_kv_heads;      // items; the product below cannot overflow
-  return (int)std::min(sms, most >= sms ? sms : most * blocks);
+  return tiles * a->g.n_kv_heads * std::max(1ll, ((long long)a->max_pages * a->g.page_tokens + kBN - 1) / kBN);
 }
+
+// One CTA per SM, and no more than there can be blocks.
+static int grid_size(const argus_extend_args* a) { return (int)std::min<long long>(device_sm_count(), std::max(1ll, max_blocks(a))); }
 
 static size_t workspace(const argus_extend_args* a) {
   return (size_t)2 * std::max(1, grid_size(a)) * kBM * (a->g.head_dim + 1) * sizeof(float);
@@ -1125,6 +1148,7 @@ extern "C" argus_status argus_paged_extend_attn(const argus_extend_args* a, void
   p.scale_log2 = (float)((double)a->softmax_scale * 1.4426950408889634);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.n_ctas = extend::grid_size(a);
+  if (extend::max_blocks(a) / p.n_ctas >= 0x7fffffffll) return fail(ARGUS_E_UNSUPPORTED, "extend: too many key blocks");
   p.ws = static_cast<float*>(ws);
   const bool bf = a->q_dtype == ARGUS_BF16, w16 = p.pool[a->q_dtype].n_slots > 0;
   return D == 64 ? extend::launch_d<64>(bf, w16, p, s) : extend::launch_d<128>(bf, w16, p, s);
