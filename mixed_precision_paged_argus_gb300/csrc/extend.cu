@@ -2,6 +2,7 @@
 // paged cache, read in place.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tcgen05.cuh"
@@ -63,11 +64,17 @@ struct Smem {
   static constexpr int kOffV = kOffK + 2 * kTile;
   static constexpr int kOffRaw = kOffV + 2 * kTile;
   static constexpr int kOffScale = kOffRaw + kLoadWarps * kRing;
-  static constexpr int kOffML = kOffScale + kScaleSlots * 8 * 12;
-  static constexpr int kOffBar = kOffML + 2 * kBM * 8;
-  // q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], drain
-  static constexpr int kNumBars = 16;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffQScale = kOffScale + kScaleSlots * 8 * 12;
+  static constexpr int kOffBar = kOffQScale + kBM * 4;
+  // q_full, k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain, and per
+  // loader warp the raw slots' (a pair of chunks each)
+  static constexpr int kNumBars = 12 + kLoadWarps * kAhead;
+  // (m, l) of both groups, read when an item's P.V are complete: in the Q tile
+  // behind the replica merge where that has room
+  static constexpr int kMerge = 2 * 96 * kMergePad * 4;
+  static constexpr bool kMLInQ = kMerge + 2 * kBM * 8 <= kTile;
+  static constexpr int kOffML = kMLInQ ? kOffQ + kMerge : kOffBar + kNumBars * 8;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8 + (kMLInQ ? 0 : 2 * kBM * 8);
   static constexpr int kBytes = kOffMisc + 64;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -268,14 +275,6 @@ __device__ __forceinline__ void int8_to_16(uint32_t w, uint32_t& lo, uint32_t& h
   }
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -302,63 +301,55 @@ __device__ __forceinline__ bool group_bar_any(int id, int n, bool x) {
 // row 128 bytes, vectors permuted by the row (128-byte swizzle)
 __device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)((c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
-// How a loader lane's vectors lie: step s of a chunk moves 512 raw bytes, lane L
-// the 16-byte vector piece_of(s, L) of the chunk's rows; raw slots are in lane order,
-// so that a lane reads back what it copied itself (no barrier in between).
-// The lanes are dealt so that eight neighbours store to eight different banks:
-// two rows by four vectors of one 64-dim half.
-template <int D, int VB>   // VB: 16-byte vectors of a raw row
-__device__ __forceinline__ int lane_row(int lane) {
-  if (VB == 4) return lane >> 2;
-  if (VB == 8) return D == 64 ? lane >> 3 : 2 * (lane >> 4) + ((lane >> 2) & 1);
-  return lane >> 4;
-}
-template <int D, int VB>
-__device__ __forceinline__ int lane_vec(int lane) {
-  if (VB == 4) return lane & 3;
-  if (VB == 8) return D == 64 ? lane & 7 : 4 * ((lane >> 3) & 1) + (lane & 3);
-  return lane & 15;
-}
-
-// One chunk (16 rows of K or V) from the lane's raw vectors to the tile at
-// `tile` (its row 0 of the chunk); rows from n_rows on become zeros (P is 0
+// R rows of K or V (a chunk, or the warp's pair) from their raw rows to the tile
+// at `tile` (the first row's place); rows from n_rows on become zeros (P is 0
 // there, and 0 times what the page holds behind the sequence would be NaN if
-// that is).  All raw vectors are read first: a read behind a store would wait
-// for it.
-template <int D, bool BF, int CODEC>
-__device__ __forceinline__ void convert_chunk(uint32_t raw, uint32_t tile, int lane, int n_rows) {
+// that is).  The raw rows of the second chunk lie SLOT bytes behind the first's.
+// A step moves 512 raw bytes, 16 per lane.  Raw vectors are read
+// four steps ahead of the stores: a read behind a store would wait for it.
+template <int D, bool BF, int CODEC, int R, int SLOT>
+__device__ __forceinline__ void convert_rows(uint32_t raw, uint32_t tile, int lane, int n_rows) {
   constexpr int VB = CODEC <= ARGUS_BF16 ? D / 8 : D / 16;   // vectors per raw row
-  constexpr int STEPS = VB / 2, ROWS = 32 / VB;              // rows per step
-  const int r0 = lane_row<D, VB>(lane), j = lane_vec<D, VB>(lane);
-  uint4 v[STEPS];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) v[s] = lds16(raw + s * 512);
-  if (n_rows < 16) {
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-      if (r0 + s * ROWS >= n_rows) v[s] = make_uint4(0, 0, 0, 0);
-  }
+  constexpr int ROWS = 32 / VB, STEPS = R / ROWS;            // rows per step
+  constexpr int BATCH = STEPS < 4 ? STEPS : 4, CHUNK = 16 / ROWS;   // steps of a chunk
+  const int r0 = lane / VB, j = lane % VB;
   // the first 16-byte vector of the tile that this lane writes: vector c of row
   // r0; rows further down are 128 bytes apart, and their permutation differs
-  // by the row's low bits
-  const int c = CODEC <= ARGUS_BF16 ? j : 2 * j;
+  // by the row's low bits.  Eight neighbouring lanes have to store to eight
+  // different vectors of 128 bytes: where they take a whole 128-byte raw row, those of
+  // the second 64-dim half store their odd vector first.
+  const bool odd_first = VB == 8 && CODEC > ARGUS_BF16 && j >= 4;
+  const int c = CODEC <= ARGUS_BF16 ? j : 2 * j + odd_first;
   const uint32_t base = tile + (c >> 3) * kHalf + r0 * 128;
   const uint32_t off = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
-    if constexpr (CODEC <= ARGUS_BF16) {
-      sts16(at, v[s].x, v[s].y, v[s].z, v[s].w);
-    } else {
-      uint32_t o[8];
-      const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+  for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
+    uint4 v[BATCH];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (CODEC == ARGUS_FP8_E4M3) fp8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
-        else int8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
+    for (int x = 0; x < BATCH; ++x) v[x] = lds16(raw + (s0 + x) / CHUNK * SLOT + (s0 + x) % CHUNK * 512 + lane * 16);
+    if (n_rows < R) {
+#pragma unroll
+      for (int x = 0; x < BATCH; ++x)
+        if (r0 + (s0 + x) * ROWS >= n_rows) v[x] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int x = 0; x < BATCH; ++x) {
+      const int s = s0 + x;
+      const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
+      if constexpr (CODEC <= ARGUS_BF16) {
+        sts16(at, v[x].x, v[x].y, v[x].z, v[x].w);
+      } else {
+        uint32_t o[8];
+        const uint32_t w[4] = {odd_first ? v[x].z : v[x].x, odd_first ? v[x].w : v[x].y, odd_first ? v[x].x : v[x].z,
+                               odd_first ? v[x].y : v[x].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (CODEC == ARGUS_FP8_E4M3) fp8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
+          else int8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
+        }
+        sts16(at, o[0], o[1], o[2], o[3]);
+        sts16(at ^ 16u, o[4], o[5], o[6], o[7]);
       }
-      sts16(at, o[0], o[1], o[2], o[3]);
-      sts16(at ^ 16u, o[4], o[5], o[6], o[7]);
     }
   }
 }
@@ -373,10 +364,10 @@ struct Lookup {
 struct Found {
   int count;
   unsigned long long src;
-  int state;                         // codec | rows << 8 (0: nothing to read) | kBad
+  int state;                         // codec | rows << 8 (0: nothing to read)
+  int pair;                          // the states of the block's two chunks: first | second << 16
   float ks, vs, lvs;                 // score scale, V scale, its log2; ks < 0: not to be read
 };
-constexpr int kBad = 1 << 16;
 
 // BF: q and out are bf16, else fp16.  W16: the call has a 16-bit pool.  The
 // operands are bf16 only where bf16 pages ask for it: over 8-bit pages alone a bf16
@@ -397,13 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
   uint64_t* k_full = q_full + 1;
-  uint64_t* k_empty = k_full + 2;
-  uint64_t* v_full = k_empty + 2;
-  uint64_t* v_empty = v_full + 2;
-  uint64_t* s_full = v_empty + 2;
+  uint64_t* v_full = k_full + 2;
+  uint64_t* s_full = v_full + 2;     // scores complete; the K tile is free
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
+  uint64_t* o_done = p_full + 2;     // P.V complete; the V tile is free
   uint64_t* drain = o_done + 2;
+  uint64_t* raw_full = drain + 1;    // [loader warp][slot]
   // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] the first one's
   // number within its sequence, [6..15] the softmax groups' cursor
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
@@ -428,14 +418,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     mbar_init(q_full, kSoftmaxWarps);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&k_full[b], kLoadWarps / 2);
-      mbar_init(&k_empty[b], 1);
       mbar_init(&v_full[b], kLoadWarps / 2);
-      mbar_init(&v_empty[b], 1);
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], kGroupWarps);
+      mbar_init(&p_full[b], kSoftmaxWarps);
       mbar_init(&o_done[b], 1);
     }
     mbar_init(drain, 1);
+    for (int f = 0; f < kLoadWarps * SM::kAhead; ++f) mbar_init(&raw_full[f], 2);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -477,20 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           mma_ss(tS(b), sdesc(q_s + off, kHalf, 1024), sdesc(k_s + off, kHalf, 1024), idQK, kk > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[b]);
-        mma_commit(&k_empty[b]);
         return true;
       };
       auto issue_pv = [&](int n, bool first) {
-        const int b = (int)(n & 1);
+        const int b = n & 1;
         if (!mbar_wait(&v_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         if (!mbar_wait(&p_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         tc_fence_after();
         const uint32_t v_s = smem_u32(smem + SM::kOffV + b * kTile);
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          mma_ts(tO(b), tS(b) + kk * 16, sdesc(v_s + kk * 2048, kHalf, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < kBN / 16; ++kk)            // group g: keys 64 g ..., its P and its O
+          mma_ts(tO(kk >> 2), tS(b) + (kk >> 2) * 64 + (kk & 3) * 8, sdesc(v_s + kk * 2048, kHalf, 1024), idPV,
+                 (!first || (kk & 3) > 0) ? 1u : 0u);
         mma_commit(&o_done[b]);
-        mma_commit(&v_empty[b]);
         return true;
       };
       for (uint32_t item = 0; ok && c.left > 0; ++item) {
@@ -499,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         if (ok) ok = issue_s(n0);
         if (ok && nb > 1) ok = issue_s(n0 + 1);
         for (int i = 0; i < nb && ok; ++i) {
-          ok = issue_pv(n0 + i, i < 2);
+          ok = issue_pv(n0 + i, i == 0);
           if (ok && i + 2 < nb) ok = issue_s(n0 + i + 2);
         }
         n0 += nb;
@@ -518,10 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const bool is_v = lw >= kLoadWarps / 2;
     const int ch0 = 2 * (lw & (kLoadWarps / 2 - 1));   // the warp's chunks: ch0, ch0 + 1
     constexpr int A = SM::kAhead;
-    const uint32_t ring = smem_u32(smem + SM::kOffRaw + lw * SM::kRing);
+    uint8_t* ring = smem + SM::kOffRaw + lw * SM::kRing;
     const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK));
     uint64_t* full = is_v ? v_full : k_full;
-    uint64_t* empty = is_v ? v_empty : k_empty;
+    uint64_t* empty = is_v ? o_done : s_full;
+    uint64_t* arrived = raw_full + lw * A;
     Cursor c;
     c.start(p, misc[2], misc64[2], n_blocks);
     auto look = [&]() {
@@ -551,11 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       f.src = 0;
       f.state = 0;
       f.ks = f.vs = 1.f;
+      bool bad = false;
       if (k.n_rows > 0) {
         const bool known = k.codec <= ARGUS_INT8 && (W16 || k.codec >= ARGUS_FP8_E4M3);
         const PoolRef r = p.pool[k.codec & 3];
         if (!known || k.slot < 0 || k.slot >= r.n_slots) {
-          f.state = kBad;
+          bad = true;
           if (k.first && !is_v && p.status) atomicAdd(p.status, 1u);
         } else {
           const int rb = k.codec <= ARGUS_BF16 ? 2 * D : D;
@@ -569,7 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         }
       }
       f.lvs = log2f(f.vs);             // 0: -inf
-      f.ks = f.state == kBad ? -1.f : f.ks * p.scale_log2;
+      f.ks = bad ? -1.f : f.ks * p.scale_log2;
+      const int other = __shfl_xor_sync(0xffffffffu, f.state, 1);
+      f.pair = (lane & 1) ? other | f.state << 16 : f.state | other << 16;
       return f;
     };
     Lookup ahead = look();
@@ -577,77 +569,85 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     ahead = look();
     int at = 0;                        // block of `now` that is issued next
     int ib = 0;                        // its number
-    // chunk `sub` of the next block: its bytes on their way; returns its state
-    auto issue = [&](int sub, uint32_t to) {
-      int state = 0;
-      if (ib < n_blocks) {
-        if (at == now.count) {
-          now = resolve(ahead);
-          ahead = look();
-          at = 0;
+    // the next block's two chunks on their way to raw slot f (a bulk copy each,
+    // issued by the lanes that looked them up); returns their states
+    auto issue = [&](int f) {
+      if (ib >= n_blocks) return 0;
+      if (at == now.count) {
+        now = resolve(ahead);
+        ahead = look();
+        at = 0;
+      }
+      if ((lane >> 1) == at) {
+        const int sub = lane & 1;
+        if (now.state) {
+          const uint32_t bytes = (W16 && (now.state & 0xFF) <= ARGUS_BF16) ? 32 * D : 16 * D;
+          mbar_arrive_expect_tx(&arrived[f], bytes);
+          bulk_g2s(ring + (2 * f + sub) * SM::kSlot, reinterpret_cast<const void*>(now.src), bytes, &arrived[f]);
+        } else {
+          mbar_arrive(&arrived[f]);
         }
-        const int from = 2 * at + sub;
-        state = __shfl_sync(0xffffffffu, now.state, from);
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, now.src, from));
-        if (!is_v && lane == from) {
-          const int x = (int)(ib % kScaleSlots) * 8 + ch0 + sub;
+        if (!is_v) {
+          const int x = (ib % kScaleSlots) * 8 + ch0 + sub;
           scales[x] = make_float2(now.ks, now.vs);
           log_vs[x] = now.lvs;
         }
-        if (state & 0xFF00) {
-          if (W16 && (state & 0xFF) <= ARGUS_BF16) {
-            const uint8_t* at16 = src + (lane_row<D, D / 8>(lane) * (D / 8) + lane_vec<D, D / 8>(lane)) * 16;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s) cp_async16(to + s * 512, at16 + s * 512);
-          } else {
-            const uint8_t* at8 = src + (lane_row<D, D / 16>(lane) * (D / 16) + lane_vec<D, D / 16>(lane)) * 16;
-#pragma unroll
-            for (int s = 0; s < D / 32; ++s) cp_async16(to + s * 512, at8 + s * 512);
-          }
-        }
-        if (sub == 1) { ++at; ++ib; }
       }
-      cp_async_commit();
-      return state;
+      const int pair = __shfl_sync(0xffffffffu, now.pair, 2 * at);
+      ++at;
+      ++ib;
+      return pair;
     };
-    int queue[2 * A];
+    int queue[A];
 #pragma unroll
-    for (int f = 0; f < 2 * A; ++f) queue[f] = issue(f & 1, ring + f * SM::kSlot + lane * 16);
+    for (int f = 0; f < A; ++f) queue[f] = issue(f);
+    bool ok = true;
     for (int i = 0; i < n_blocks; ++i) {
-      const int b = i & 1;
-      const uint32_t raw = ring + (uint32_t)(i % A) * 2 * SM::kSlot + lane * 16;
-      if (i >= 2 && !__all_sync(0xffffffffu, mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]))) { misc[1] = 1; break; }
+      const int b = i & 1, f = i % A;
+      const int pair = queue[0];
+      const uint32_t raw = smem_u32(ring + 2 * f * SM::kSlot), tile = tiles + b * kTile + ch0 * 2048;
+      ok = mbar_wait(&arrived[f], (uint32_t)(i / A) & 1, &misc[1]);
+      if (i >= 2) ok = ok && mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      constexpr int kFull8 = 16 << 8 | 16 << 24;
+      if (pair == (kFull8 | ARGUS_FP8_E4M3 * 0x10001)) {
+        convert_rows<D, BFM, ARGUS_FP8_E4M3, 32, SM::kSlot>(raw, tile, lane, 32);
+      } else {
 #pragma unroll 1
-      for (int sub = 0; sub < 2; ++sub) {
-        const int state = queue[0], codec = state & 0xFF, n_rows = (state >> 8) & 0xFF;
-        const uint32_t at_raw = raw + sub * SM::kSlot, tile = tiles + b * kTile + (ch0 + sub) * 2048;
-        cp_async_wait<2 * A - 1>();
-        // a chunk without rows: K is masked, V is set to zero
-        if (n_rows > 0 || is_v) {
-          if (W16 && codec <= ARGUS_BF16) convert_chunk<D, BFM, ARGUS_BF16>(at_raw, tile, lane, n_rows);
-          else if (codec == ARGUS_INT8) convert_chunk<D, BFM, ARGUS_INT8>(at_raw, tile, lane, n_rows);
-          else convert_chunk<D, BFM, ARGUS_FP8_E4M3>(at_raw, tile, lane, n_rows);
+        for (int sub = 0; sub < 2; ++sub) {
+          const int state = (pair >> (16 * sub)) & 0xFFFF, codec = state & 0xFF, n_rows = state >> 8;
+          const uint32_t from = raw + sub * SM::kSlot, to = tile + sub * 2048;
+          if (n_rows == 0 && !is_v) continue;            // a chunk without rows: K is masked, V is set to zero
+          if (W16 && codec <= ARGUS_BF16) convert_rows<D, BFM, ARGUS_BF16, 16, SM::kSlot>(from, to, lane, n_rows);
+          else if (codec == ARGUS_INT8) convert_rows<D, BFM, ARGUS_INT8, 16, SM::kSlot>(from, to, lane, n_rows);
+          else convert_rows<D, BFM, ARGUS_FP8_E4M3, 16, SM::kSlot>(from, to, lane, n_rows);
         }
-        const int nxt = issue(sub, at_raw);
-#pragma unroll
-        for (int f = 0; f + 1 < 2 * A; ++f) queue[f] = queue[f + 1];
-        queue[2 * A - 1] = nxt;
       }
       fence_async();
-      __syncwarp();
+      __syncwarp();                                      // the tile is written and the slot has been read
       if (lane == 0) mbar_arrive(&full[b]);
+      const int nxt = issue(f);
+#pragma unroll
+      for (int x = 0; x + 1 < A; ++x) queue[x] = queue[x + 1];
+      queue[A - 1] = nxt;
     }
-    cp_async_wait<0>();
+    if (!ok) {
+      misc[1] = 1;
+      // the copies in flight land before the CTA ends: the last one of every slot
+      for (int f = 0; f < A; ++f)
+        if (ib > f) mbar_wait(&arrived[f], (uint32_t)((ib - f + A - 1) / A - 1) & 1);
+    }
   } else {
     // ---------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int grp = warp / kGroupWarps, wq = warp % kGroupWarps;
     const int tl = wq * 32 + lane;                     // TMEM lane
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t sS = tS(grp) + lane_off, sO = tO(grp) + lane_off;
+    const uint32_t sO = tO(grp) + lane_off;
     const uint32_t q_s = smem_u32(smem + SM::kOffQ);
     float* merge = reinterpret_cast<float*>(smem + SM::kOffQ) + grp * 96 * kMergePad;
-    float* q_scale = reinterpret_cast<float*>(smem + SM::kOffML);
+    float* q_scale = reinterpret_cast<float*>(smem + SM::kOffQScale);
     if (warp == 0) {
       Cursor c;
       c.start(p, misc[2], misc64[2], n_blocks);
@@ -697,12 +697,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if (BF && !BFM) {
         group_bar(1, kSoftmaxWarps * 32);
         qf = q_scale[tl];
-        group_bar(1, kSoftmaxWarps * 32);              // (m, l) of the item lie there too
       }
 
       const int l_row = tl & (per - 1);          // row within the tile
-      const int rep = tl / per;                  // this lane's replica: keys of chunks [c0, c1)
-      const int c0 = rep * (8 / nrep), c1 = c0 + 8 / nrep;
+      const int rep = tl / per;                        // this lane's replica: chunks c0 ... of the group's four
+      const int c0 = 4 * grp + rep * (4 / nrep);
       // rows behind the last one (zero queries) see what the last one sees: they are never written
       const int tok = min((lin0 + l_row) / p.G, c.s.n - 1);
       const int vis_last = min(p.causal ? c.s.len - c.s.n + tok : c.s.len - 1, c.s.len - 1);
@@ -711,138 +710,129 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       // times the scale) it could leave the fp32 range, and a page whose V is 0 must
       // not push every other page's P out of the 16-bit range
       float m = -INFINITY, la = 0.f, lb = 0.f, mz = -INFINITY, lz = 0.f;
-      auto scale_acc = [&](float r) {
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t v[32];
-          tmem_ld32(sO + x * 32, v);
+      auto scale_acc = [&](float r) {                  // rare: few registers, not speed
+#pragma unroll 1
+        for (int x = 0; x < D / 8; ++x) {
+          uint32_t v[8];
+          tmem_ld8(sO + x * 8, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * r);
-          tmem_st32(sO + x * 32, v);
+          for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * r);
+          tmem_st8(sO + x * 8, v);
         }
         tmem_wait_st();
       };
-      int last = -1;                                   // this group's last block (local)
-      for (int i = (grp - n0) & 1; i < nb; i += 2) {
-        const int n = n0 + i;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[grp], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; misc[1] = 1; break; }
-        tc_fence_after();
-        last = i;
-        const int k0 = k_first + i * kBN;
-        const float2* sc = scales + (int)(n % kScaleSlots) * 8;
-        const float* lv = log_vs + (int)(n % kScaleSlots) * 8;
-        // lanes c0 .. c1-1 look at their chunk, every lane at its row's last key
-        const bool odd = lane >= c0 && lane < c1 && (sc[lane].x < 0.f || fabsf(lv[lane]) > kFarScale);
-        const bool edge = __any_sync(0xffffffffu, odd || k0 + c1 * 16 - 1 > vis_last);
-        const int lim = vis_last - k0;                 // keys e <= lim of the block are visible
-        // pass 1: maximum of score + log2 of the V scale, so that P times that scale stays in range
+      // One block, N chunks of 16 keys per lane, all scores in registers.
+      auto block = [&](auto chunks, int n, int k0) {
+        constexpr int N = decltype(chunks)::value;
+        const uint32_t sS = tS(n & 1) + lane_off;
+        const float2* sc = scales + (n % kScaleSlots) * 8 + c0;
+        const float* lv = log_vs + (n % kScaleSlots) * 8 + c0;
+        float v[N][16];
+#pragma unroll
+        for (int x = 0; x < N; ++x) tmem_ld16(sS + (c0 + x) * 16, reinterpret_cast<uint32_t(&)[16]>(v[x]));
+        // lanes 0 .. N-1 look at their chunk, every lane at its row's last key
+        const bool odd = lane < N && (sc[lane].x < 0.f || fabsf(lv[lane]) > kFarScale);
+        const int lim = vis_last - k0 - c0 * 16;       // keys e <= lim of the lane's are visible
+        const bool edge = __any_sync(0xffffffffu, odd || lim < N * 16 - 1);
+        tmem_wait_ld();
+        // the maximum of score + log2 of the V scale, so that P times that scale stays in range
         float mj = -INFINITY;
-#pragma unroll 1
-        for (int cc = c0; cc < c1; cc += 2) {
-          uint32_t v[32];
-          tmem_ld32(sS + cc * 16, v);
-          const float2 s0 = sc[cc], s1 = sc[cc + 1];
-          const float l0 = lv[cc], l1 = lv[cc + 1];
-          tmem_wait_ld();
-          if (!edge) {
-            float a0 = -INFINITY, a1 = -INFINITY, b0 = -INFINITY, b1 = -INFINITY;
+        if (edge) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              a0 = max3(a0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-              a1 = max3(a1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
-              b0 = max3(b0, __uint_as_float(v[16 + e]), __uint_as_float(v[16 + e + 1]));
-              b1 = max3(b1, __uint_as_float(v[16 + e + 2]), __uint_as_float(v[16 + e + 3]));
-            }
-            mj = max3(mj, fmaf(fmaxf(a0, a1), s0.x * qf, l0), fmaf(fmaxf(b0, b1), s1.x * qf, l1));
-          } else {
+          for (int x = 0; x < N; ++x) {
+            const float kq = sc[x].x * qf, lvc = lv[x];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float ks = e < 16 ? s0.x : s1.x;
-              if (cc * 16 + e <= lim && ks >= 0.f) mj = fmaxf(mj, fmaf(__uint_as_float(v[e]), ks * qf, e < 16 ? l0 : l1));
+            for (int e = 0; e < 16; ++e) v[x][e] = (kq >= 0.f && x * 16 + e <= lim) ? v[x][e] * kq : -INFINITY;
+            if (fabsf(lvc) > kFarScale) {
+              float top = mz;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, v[x][e]);
+              if (top != -INFINITY) {
+                lz *= fast_exp2(mz - top);
+                mz = top;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) lz += fast_exp2(v[x][e] - top);
+              }
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[x][e] += lvc;
             }
           }
+        }
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          float a0 = max3(v[x][0], v[x][1], v[x][2]), a1 = max3(v[x][3], v[x][4], v[x][5]);
+          a0 = max3(a0, v[x][6], v[x][7]);
+          a1 = max3(a1, v[x][8], v[x][9]);
+          a0 = max3(a0, v[x][10], v[x][11]);
+          a1 = max3(a1, v[x][12], v[x][13]);
+          a0 = max3(a0, v[x][14], v[x][15]);
+          const bool far = edge && fabsf(lv[x]) > kFarScale;
+          mj = fmaxf(mj, fmaf(fmaxf(a0, a1), edge ? 1.f : sc[x].x * qf, far ? 0.f : lv[x]));
         }
         const bool move = mj > m + kRescaleThreshold || (m == -INFINITY && mj != -INFINITY);
         const bool scale_o = move && m != -INFINITY;
         if (__any_sync(0xffffffffu, scale_o)) {
-          // this block's scores are complete, hence also the group's P.V before them
+          // the block before (of this item, as m is set) is the last that added to O
+          if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1, &misc[1]))) return false;
+          tc_fence_after();
           const float r = scale_o ? fast_exp2(m - mj) : 1.f;
           scale_acc(r);
           la *= r;
           lb *= r;
         }
         if (move) m = mj;
-        // pass 2: P over the consumed scores; the keys of the other replicas are zeros
+        // P over the consumed scores, packed: the group's 64 keys in 32 columns, zeros for the other replicas' keys
         const float mm = (m == -INFINITY) ? 0.f : m - kPBias;
-        if (nrep > 1) {
+        const uint32_t sP = sS + 64 * grp;
+        if (N < 4) {
           const uint32_t z[8] = {};
-#pragma unroll 1
-          for (int cc = 0; cc < 8; ++cc)
-            if (cc < c0 || cc >= c1) tmem_st8(sS + cc * 16, z);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (x < c0 - 4 * grp || x >= c0 - 4 * grp + N) tmem_st8(sP + x * 8, z);
         }
-#pragma unroll 2
-        for (int cc = c0; cc < c1; ++cc) {
-          uint32_t v[16], o[8];
-          tmem_ld16(sS + cc * 16, v);
-          const float2 s = sc[cc];
-          const float kq = s.x * qf;
-          tmem_wait_ld();
-          if (!edge) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float x0, x1, p0, p1;
-              f2_fma(x0, x1, __uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]), kq, kq, -mm, -mm);
-              p0 = fast_exp2(x0);
-              p1 = fast_exp2(x1);
-              f2_add(la, lb, la, lb, p0, p1);
-              f2_mul(p0, p1, p0, p1, s.y, s.y);
-              o[e] = BFM ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-            }
-          } else {
-            const float lvc = lv[cc];
-            const bool far = fabsf(lvc) > kFarScale;
-            float x[16];
+        for (int x = 0; x < N; ++x) {
+          const bool far = edge && fabsf(lv[x]) > kFarScale;
+          const float kq = edge ? 1.f : sc[x].x * qf, vs = far ? 1.f : sc[x].y;
+          const float sa = la, sb = lb;
+          uint32_t o[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              x[e] = (s.x >= 0.f && cc * 16 + e <= lim) ? __uint_as_float(v[e]) * kq : -INFINITY;
-            if (far) {
-              float top = mz;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e]);
-              if (top != -INFINITY) {
-                lz *= fast_exp2(mz - top);
-                mz = top;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) lz += fast_exp2(x[e] - top);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float shift = far ? lvc - mm : -mm, vs = far ? 1.f : s.y;
-              const float p0 = m == -INFINITY ? 0.f : fast_exp2(x[2 * e] + shift);
-              const float p1 = m == -INFINITY ? 0.f : fast_exp2(x[2 * e + 1] + shift);
-              if (!far) f2_add(la, lb, la, lb, p0, p1);
-              o[e] = BFM ? pack_bf16x2(p0 * vs, p1 * vs) : pack_f16x2(p0 * vs, p1 * vs);
-            }
+          for (int e = 0; e < 8; ++e) {
+            float x0, x1;
+            f2_fma(x0, x1, v[x][2 * e], v[x][2 * e + 1], kq, kq, -mm, -mm);
+            float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            f2_add(la, lb, la, lb, p0, p1);
+            f2_mul(p0, p1, p0, p1, vs, vs);
+            o[e] = BFM ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
-          tmem_st8(sS + cc * 16, o);
+          if (far) { la = sa; lb = sb; }
+          tmem_st8(sP + (c0 - 4 * grp + x) * 8, o);
         }
         tmem_wait_st();
+        return true;
+      };
+      for (int i = 0; i < nb; ++i) {
+        const int n = n0 + i, k0 = k_first + i * kBN;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; break; }
+        tc_fence_after();
+        if (nrep == 4) alive = block(std::integral_constant<int, 1>{}, n, k0);
+        else if (nrep == 2) alive = block(std::integral_constant<int, 2>{}, n, k0);
+        else alive = block(std::integral_constant<int, 4>{}, n, k0);
+        if (!alive) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[grp]);
+        if (lane == 0) mbar_arrive(&p_full[n & 1]);
       }
-      if (alive && last >= 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[grp], (uint32_t)((n0 + last) >> 1) & 1, &misc[1]))) { alive = false; misc[1] = 1; }
-        tc_fence_after();
-      }
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_done[(n0 + nb - 1) & 1], (uint32_t)((n0 + nb - 1) >> 1) & 1, &misc[1]));
+      if (!alive) misc[1] = 1;
+      tc_fence_after();
       // references in the units that l was summed in
       float ref = m == -INFINITY ? -INFINITY : m - kPBias, sum = la + lb;
       if (__any_sync(0xffffffffu, mz != -INFINITY)) {
         const float top = fmaxf(ref, mz);
         const float r = (mz == -INFINITY) ? 1.f : fast_exp2(ref - top);   // ref = -inf: 0
-        if (last >= 0) scale_acc(r);
+        scale_acc(r);
         if (mz != -INFINITY) {
           sum = sum * r + lz * fast_exp2(mz - top);
           ref = top;
@@ -854,7 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       tc_fence_after();
       c.load(misc + 6);
       // ---- epilogue: both groups' and all replicas' sums of a row joined; group g takes half the dims
-      const bool has0 = nb > 1 || (n0 & 1) == 0, has1 = nb > 1 || (n0 & 1) == 1;   // which groups had a block
       float M = -INFINITY;
       for (int x = 0; x < 2 * nrep; ++x) M = fmaxf(M, ml[(x & 1) * kBM + (x >> 1) * per + l_row].x);
       float l_all = 0.f;
@@ -877,15 +866,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         const int col = grp * (D / 2) + x * 16;
         uint32_t v0[16], v1[16];
         float o[16];
-        if (has0) tmem_ld16(tO(0) + lane_off + col, v0);
-        if (has1) tmem_ld16(tO(1) + lane_off + col, v1);
+        tmem_ld16(tO(0) + lane_off + col, v0);
+        tmem_ld16(tO(1) + lane_off + col, v1);
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          float a = 0.f;
-          if (has0 && w0 != 0.f) a = w0 * __uint_as_float(v0[e]);
-          if (has1 && w1 != 0.f) a += w1 * __uint_as_float(v1[e]);
-          o[e] = a;
+          o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
         }
         if (nrep > 1) {
           if (rep > 0) {
