@@ -38,43 +38,38 @@ constexpr int kBM = 128;             // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;             // keys per block
 constexpr int kGroupWarps = 4;       // one softmax warpgroup: a thread per TMEM lane
 constexpr int kSoftmaxWarps = 2 * kGroupWarps;
-constexpr int kLoadWarps = 8;        // four for K, four for V: two 16-token chunks of a block each
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kLoadWarps = 16;       // eight for K, eight for V: a 16-token chunk of every block each
+constexpr int kLookWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kMmaWarp = kLookWarp + 1;
 constexpr int kThreads = 32 * (kMmaWarp + 1);
-// 17 warps get 96 registers a thread at launch; the loaders' four-warp groups give
-// up what the softmax groups take: 256 * 120 + 256 * 72 = 512 * 96
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 120, kLoadRegs = 72;
-static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs) <= 32 * (kSoftmaxWarps + kLoadWarps) * kLaunchRegs, "registers");
+// 26 warps get 72 registers a thread at launch; the loaders' four-warp groups give
+// up what the softmax groups take: 8 * 104 + 16 * 56 = 24 * 72
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kLoadRegs = 56;
+static_assert(kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs <= (kSoftmaxWarps + kLoadWarps) * kLaunchRegs, "registers");
 constexpr int kHalf = kBM * 64 * 2;  // 128 rows x 64 dims: one 128-byte swizzle column
 constexpr int kTmemCols = 512;       // S0 S1 O0 O1, 128 columns each
 constexpr float kRescaleThreshold = 8.f;
 constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chunk's sum is kept apart
-constexpr int kScaleSlots = 8;       // blocks whose page scales are kept
+constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
+constexpr int kBatches = 4;          // batches whose descriptions are kept
+constexpr int kSlots = kBatch * kBatches;
 constexpr int kMergePad = 20;        // floats per row of the replica merge (16 used; conflict-free vectors)
 
-template <int D, bool W16>
+template <int D>
 struct Smem {
   static constexpr int kTile = kBM * D * 2;
-  // a loader warp's raw ring: two chunks (16 rows each) of kAhead blocks
-  static constexpr int kSlot = 16 * D * (W16 ? 2 : 1);
-  static constexpr int kAhead = (128 / D) * (W16 ? 1 : 2);
-  static constexpr int kRing = 2 * kAhead * kSlot;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kTile;
   static constexpr int kOffV = kOffK + 2 * kTile;
-  static constexpr int kOffRaw = kOffV + 2 * kTile;
-  static constexpr int kOffScale = kOffRaw + kLoadWarps * kRing;
-  static constexpr int kOffQScale = kOffScale + kScaleSlots * 8 * 12;
-  static constexpr int kOffBar = kOffQScale + kBM * 4;
-  // q_full, k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain, and per
-  // loader warp the raw slots' (a pair of chunks each)
-  static constexpr int kNumBars = 12 + kLoadWarps * kAhead;
-  // (m, l) of both groups, read when an item's P.V are complete: in the Q tile
-  // behind the replica merge where that has room
-  static constexpr int kMerge = 2 * 96 * kMergePad * 4;
-  static constexpr bool kMLInQ = kMerge + 2 * kBM * 8 <= kTile;
-  static constexpr int kOffML = kMLInQ ? kOffQ + kMerge : kOffBar + kNumBars * 8;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8 + (kMLInQ ? 0 : 2 * kBM * 8);
+  static constexpr int kOffChunk = kOffV + 2 * kTile;                    // [slot][chunk] uint4: source, state
+  static constexpr int kOffScale = kOffChunk + kSlots * 8 * 16;          // [slot][chunk] float2: ks, vs
+  static constexpr int kOffLogVs = kOffScale + kSlots * 8 * 8;           // [slot][chunk] float
+  static constexpr int kOffQScale = kOffLogVs + kSlots * 8 * 4;
+  static constexpr int kOffML = kOffQScale + kBM * 4;
+  static constexpr int kOffBar = kOffML + 2 * kBM * 8;
+  // q_full, k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain, looked[kBatches], used[kBatches]
+  static constexpr int kNumBars = 12 + 2 * kBatches;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kBytes = kOffMisc + 64;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -275,9 +270,9 @@ __device__ __forceinline__ void int8_to_16(uint32_t w, uint32_t& lo, uint32_t& h
   }
 }
 
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {   // read once: past the L1
   uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
@@ -301,72 +296,69 @@ __device__ __forceinline__ bool group_bar_any(int id, int n, bool x) {
 // row 128 bytes, vectors permuted by the row (128-byte swizzle)
 __device__ __forceinline__ uint32_t tile_off(int r, int c) { return (uint32_t)((c >> 3) * kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)); }
 
-// R rows of K or V (a chunk, or the warp's pair) from their raw rows to the tile
-// at `tile` (the first row's place); rows from n_rows on become zeros (P is 0
-// there, and 0 times what the page holds behind the sequence would be NaN if
-// that is).  The raw rows of the second chunk lie SLOT bytes behind the first's.
-// A step moves 512 raw bytes, 16 per lane.  Raw vectors are read
-// four steps ahead of the stores: a read behind a store would wait for it.
-template <int D, bool BF, int CODEC, int R, int SLOT>
-__device__ __forceinline__ void convert_rows(uint32_t raw, uint32_t tile, int lane, int n_rows) {
+// A loader warp's chunk is 16 rows of K or V, contiguous in its page; a lane
+// holds 16-byte vectors of it in registers, step s the 512 bytes from 512 s on.
+// Eight neighbouring lanes have to store to eight different 16-byte vectors of
+// 128 bytes.  Sixteen codes become two such vectors, so over 128-byte raw rows
+// (8-bit pages, 128 dims) they take two rows by four vectors of one 64-dim
+// half; everywhere else raw order does it.
+template <int D, int VB>             // VB: 16-byte vectors of a raw row
+__device__ __forceinline__ int lane_row(int lane) {
+  return (VB == 8 && D == 128) ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane / VB;
+}
+template <int D, int VB>
+__device__ __forceinline__ int lane_vec(int lane) {
+  return (VB == 8 && D == 128) ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane % VB;
+}
+
+template <int D, int VB, int N>
+__device__ __forceinline__ void load_chunk(uint4 (&v)[N], const uint8_t* src, int lane) {
+  src += (lane_row<D, VB>(lane) * VB + lane_vec<D, VB>(lane)) * 16;
+#pragma unroll
+  for (int s = 0; s < VB / 2; ++s) v[s] = ldg16(src + s * 512);
+}
+
+// The chunk to its tile; `tile`: the place of its first row.  Rows from n_rows on become zeros (P is 0
+// there, and 0 times what the page holds behind the sequence would be NaN if that is).
+template <int D, bool BF, int CODEC, int N>
+__device__ __forceinline__ void store_chunk(uint4 (&v)[N], uint32_t tile, int lane, int n_rows) {
   constexpr int VB = CODEC <= ARGUS_BF16 ? D / 8 : D / 16;   // vectors per raw row
-  constexpr int ROWS = 32 / VB, STEPS = R / ROWS;            // rows per step
-  constexpr int BATCH = STEPS < 4 ? STEPS : 4, CHUNK = 16 / ROWS;   // steps of a chunk
-  const int r0 = lane / VB, j = lane % VB;
-  // the first 16-byte vector of the tile that this lane writes: vector c of row
-  // r0; rows further down are 128 bytes apart, and their permutation differs
-  // by the row's low bits.  Eight neighbouring lanes have to store to eight
-  // different vectors of 128 bytes: where they take a whole 128-byte raw row, those of
-  // the second 64-dim half store their odd vector first.
-  const bool odd_first = VB == 8 && CODEC > ARGUS_BF16 && j >= 4;
-  const int c = CODEC <= ARGUS_BF16 ? j : 2 * j + odd_first;
+  constexpr int STEPS = VB / 2, ROWS = 32 / VB;              // rows per step
+  const int r0 = lane_row<D, VB>(lane), j = lane_vec<D, VB>(lane);
+  if (n_rows < 16) {
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)
+      if (r0 + s * ROWS >= n_rows) v[s] = make_uint4(0, 0, 0, 0);
+  }
+  // vector c of row r0 is the first that this lane writes; rows further down
+  // are 128 bytes apart, and their permutation differs by the row's low bits
+  const int c = CODEC <= ARGUS_BF16 ? j : 2 * j;
   const uint32_t base = tile + (c >> 3) * kHalf + r0 * 128;
   const uint32_t off = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
 #pragma unroll
-  for (int s0 = 0; s0 < STEPS; s0 += BATCH) {
-    uint4 v[BATCH];
+  for (int s = 0; s < STEPS; ++s) {
+    const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
+    if constexpr (CODEC <= ARGUS_BF16) {
+      sts16(at, v[s].x, v[s].y, v[s].z, v[s].w);
+    } else {
+      uint32_t o[8];
+      const uint32_t w[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
 #pragma unroll
-    for (int x = 0; x < BATCH; ++x) v[x] = lds16(raw + (s0 + x) / CHUNK * SLOT + (s0 + x) % CHUNK * 512 + lane * 16);
-    if (n_rows < R) {
-#pragma unroll
-      for (int x = 0; x < BATCH; ++x)
-        if (r0 + (s0 + x) * ROWS >= n_rows) v[x] = make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int x = 0; x < BATCH; ++x) {
-      const int s = s0 + x;
-      const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
-      if constexpr (CODEC <= ARGUS_BF16) {
-        sts16(at, v[x].x, v[x].y, v[x].z, v[x].w);
-      } else {
-        uint32_t o[8];
-        const uint32_t w[4] = {odd_first ? v[x].z : v[x].x, odd_first ? v[x].w : v[x].y, odd_first ? v[x].x : v[x].z,
-                               odd_first ? v[x].y : v[x].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (CODEC == ARGUS_FP8_E4M3) fp8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
-          else int8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
-        }
-        sts16(at, o[0], o[1], o[2], o[3]);
-        sts16(at ^ 16u, o[4], o[5], o[6], o[7]);
+      for (int e = 0; e < 4; ++e) {
+        if (CODEC == ARGUS_FP8_E4M3) fp8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
+        else int8_to_16<BF>(w[e], o[2 * e], o[2 * e + 1]);
       }
+      sts16(at, o[0], o[1], o[2], o[3]);
+      sts16(at ^ 16u, o[4], o[5], o[6], o[7]);
     }
   }
 }
 
-// A loader warp looks its pages up for 16 blocks of an item at once, a lane per
-// chunk (lane = 2 * block + chunk of the warp's pair): the two dependent reads
-// (table, then scales) are paid once per 16 blocks.
+// The lookup warp finds the pages of kBatch blocks at once, a lane per chunk
+// (lane = 8 * block + chunk): the two dependent reads (table, then scales) are
+// paid once per batch, and the batch behind is read meanwhile.
 struct Lookup {
-  int count;                         // blocks
   int codec, slot, row, n_rows, h, first;   // first: this chunk counts a page that cannot be read
-};
-struct Found {
-  int count;
-  unsigned long long src;
-  int state;                         // codec | rows << 8 (0: nothing to read)
-  int pair;                          // the states of the block's two chunks: first | second << 16
-  float ks, vs, lvs;                 // score scale, V scale, its log2; ks < 0: not to be read
 };
 
 // BF: q and out are bf16, else fp16.  W16: the call has a 16-bit pool.  The
@@ -377,7 +369,7 @@ struct Found {
 // and fp16 P has three more bits.
 template <int D, bool BF, bool W16>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
-  using SM = Smem<D, W16>;
+  using SM = Smem<D>;
   constexpr int kTile = SM::kTile;
   constexpr bool BFM = BF && W16;            // operand type of the MMAs
   constexpr float kPBias = BFM ? 0.f : 7.f;  // fp16 P is stored as P * 2^7 (at most 2^15)
@@ -393,14 +385,16 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;     // P.V complete; the V tile is free
   uint64_t* drain = o_done + 2;
-  uint64_t* raw_full = drain + 1;    // [loader warp][slot]
+  uint64_t* looked = drain + 1;      // a batch of blocks is looked up
+  uint64_t* used = looked + kBatches;   // nobody needs the batch any more
   // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] the first one's
   // number within its sequence, [6..15] the softmax groups' cursor
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
   volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
+  uint4* chunks = reinterpret_cast<uint4*>(smem + SM::kOffChunk);       // [slot][chunk]: K source, state
   float2* scales = reinterpret_cast<float2*>(smem + SM::kOffScale);     // [slot][chunk]: ks (< 0: not to be read), vs
-  float* log_vs = reinterpret_cast<float*>(scales + kScaleSlots * 8);   // log2 vs
+  float* log_vs = reinterpret_cast<float*>(smem + SM::kOffLogVs);       // [slot][chunk]: log2 vs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -424,7 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       mbar_init(&o_done[b], 1);
     }
     mbar_init(drain, 1);
-    for (int f = 0; f < kLoadWarps * SM::kAhead; ++f) mbar_init(&raw_full[f], 2);
+    for (int k = 0; k < kBatches; ++k) {
+      mbar_init(&looked[k], 1);
+      mbar_init(&used[k], kLoadWarps);
+    }
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -499,145 +496,133 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         mbar_wait(drain, 0);
       }
     }
-  } else if (warp >= kSoftmaxWarps) {
-    // ---------------------------------------------------------- loaders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int lw = warp - kSoftmaxWarps;
-    const bool is_v = lw >= kLoadWarps / 2;
-    const int ch0 = 2 * (lw & (kLoadWarps / 2 - 1));   // the warp's chunks: ch0, ch0 + 1
-    constexpr int A = SM::kAhead;
-    uint8_t* ring = smem + SM::kOffRaw + lw * SM::kRing;
-    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK));
-    uint64_t* full = is_v ? v_full : k_full;
-    uint64_t* empty = is_v ? o_done : s_full;
-    uint64_t* arrived = raw_full + lw * A;
+  } else if (warp == kLookWarp) {
+    // ---------------------------------------------------------- lookup
     Cursor c;
     c.start(p, misc[2], misc64[2], n_blocks);
     auto look = [&]() {
       Lookup k;
-      k.count = max(0, min(min(16, c.nb - c.blk), c.left));
       k.codec = k.slot = -1;
-      k.row = k.n_rows = k.first = 0;
-      k.h = c.h;
-      if (lane / 2 < k.count) {
-        const int key = (c.blk + lane / 2) * kBN + (ch0 + (lane & 1)) * 16;
-        k.n_rows = min(max(c.s.len - key, 0), 16);
-        if (k.n_rows > 0) {
-          const int page = key / p.P;
-          k.row = key - page * p.P;
-          const size_t e = (size_t)c.b * p.max_pages + page;
-          k.codec = p.page_codec[e];
-          k.slot = p.block_table[e];
-          k.first = c.h == 0 && c.t == c.T - 1 && k.row == 0;
+      k.row = k.n_rows = k.h = k.first = 0;
+      int b = 0, key = 0;
+#pragma unroll 1
+      for (int x = 0; x < kBatch && c.left > 0; ++x) {
+        if (lane / 8 == x) {
+          b = c.b;
+          key = c.blk * kBN + (lane & 7) * 16;
+          k.n_rows = min(max(c.s.len - key, 0), 16);
+          k.h = c.h;
+          k.first = c.h == 0 && c.t == c.T - 1;
         }
+        c.advance(p, 1);
       }
-      if (k.count > 0) c.advance(p, k.count);
+      if (k.n_rows > 0) {
+        const int page = key / p.P;
+        k.row = key - page * p.P;
+        k.first = k.first && k.row == 0;
+        const size_t e = (size_t)b * p.max_pages + page;
+        k.codec = p.page_codec[e];
+        k.slot = p.block_table[e];
+      }
       return k;
     };
-    auto resolve = [&](const Lookup& k) {
-      Found f;
-      f.count = k.count;
-      f.src = 0;
-      f.state = 0;
-      f.ks = f.vs = 1.f;
-      bool bad = false;
-      if (k.n_rows > 0) {
-        const bool known = k.codec <= ARGUS_INT8 && (W16 || k.codec >= ARGUS_FP8_E4M3);
-        const PoolRef r = p.pool[k.codec & 3];
-        if (!known || k.slot < 0 || k.slot >= r.n_slots) {
-          bad = true;
-          if (k.first && !is_v && p.status) atomicAdd(p.status, 1u);
+    Lookup ahead = look();
+    for (int k = 0; k * kBatch < n_blocks; ++k) {
+      const Lookup now = ahead;
+      const uint8_t* src = nullptr;
+      uint32_t state = 0;              // codec | rows << 8; 0: nothing to read
+      float ks = 1.f, vs = 1.f;
+      if (now.n_rows > 0) {
+        const bool known = now.codec <= ARGUS_INT8 && (W16 || now.codec >= ARGUS_FP8_E4M3);
+        const PoolRef r = p.pool[now.codec & 3];
+        if (!known || now.slot < 0 || now.slot >= r.n_slots) {
+          ks = -1.f;
+          if (now.first && p.status) atomicAdd(p.status, 1u);
         } else {
-          const int rb = k.codec <= ARGUS_BF16 ? 2 * D : D;
-          const long long unit = (long long)k.slot * 2 * p.Hkv + k.h;
-          f.src = reinterpret_cast<unsigned long long>(r.codes + ((unit + (is_v ? p.Hkv : 0)) * p.P + k.row) * rb);
-          f.state = k.codec | k.n_rows << 8;
-          if (!is_v && k.codec >= ARGUS_FP8_E4M3) {
-            f.ks = r.meta[unit];
-            f.vs = r.meta[unit + p.Hkv];
+          const int rb = now.codec <= ARGUS_BF16 ? 2 * D : D;
+          const long long unit = (long long)now.slot * 2 * p.Hkv + now.h;
+          src = r.codes + (unit * p.P + now.row) * rb;
+          state = now.codec | now.n_rows << 8;
+          if (now.codec >= ARGUS_FP8_E4M3) {
+            ks = r.meta[unit];
+            vs = r.meta[unit + p.Hkv];
           }
         }
       }
-      f.lvs = log2f(f.vs);             // 0: -inf
-      f.ks = bad ? -1.f : f.ks * p.scale_log2;
-      const int other = __shfl_xor_sync(0xffffffffu, f.state, 1);
-      f.pair = (lane & 1) ? other | f.state << 16 : f.state | other << 16;
-      return f;
-    };
-    Lookup ahead = look();
-    Found now = resolve(ahead);
-    ahead = look();
-    int at = 0;                        // block of `now` that is issued next
-    int ib = 0;                        // its number
-    // the next block's two chunks on their way to raw slot f (a bulk copy each,
-    // issued by the lanes that looked them up); returns their states
-    auto issue = [&](int f) {
-      if (ib >= n_blocks) return 0;
-      if (at == now.count) {
-        now = resolve(ahead);
-        ahead = look();
-        at = 0;
+      ahead = look();
+      if (k >= kBatches && !__all_sync(0xffffffffu, mbar_wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
+        misc[1] = 1;
+        break;
       }
-      if ((lane >> 1) == at) {
-        const int sub = lane & 1;
-        if (now.state) {
-          const uint32_t bytes = (W16 && (now.state & 0xFF) <= ARGUS_BF16) ? 32 * D : 16 * D;
-          mbar_arrive_expect_tx(&arrived[f], bytes);
-          bulk_g2s(ring + (2 * f + sub) * SM::kSlot, reinterpret_cast<const void*>(now.src), bytes, &arrived[f]);
-        } else {
-          mbar_arrive(&arrived[f]);
-        }
-        if (!is_v) {
-          const int x = (ib % kScaleSlots) * 8 + ch0 + sub;
-          scales[x] = make_float2(now.ks, now.vs);
-          log_vs[x] = now.lvs;
-        }
-      }
-      const int pair = __shfl_sync(0xffffffffu, now.pair, 2 * at);
-      ++at;
-      ++ib;
-      return pair;
-    };
-    int queue[A];
-#pragma unroll
-    for (int f = 0; f < A; ++f) queue[f] = issue(f);
+      const int at = (k % kBatches) * 32 + lane;
+      const unsigned long long addr = reinterpret_cast<unsigned long long>(src);
+      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), state, 0);
+      scales[at] = make_float2(ks < 0.f ? -1.f : ks * p.scale_log2, vs);
+      log_vs[at] = log2f(vs);          // 0: -inf
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&looked[k % kBatches]);
+    }
+  } else if (warp >= kSoftmaxWarps) {
+    // ---------------------------------------------------------- loaders
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
+    const int lw = warp - kSoftmaxWarps, ch = lw & 7;
+    const bool is_v = lw >= 8;
+    constexpr int VEC = W16 ? D / 16 : D / 32;         // vectors of a chunk
+    constexpr int A = 8 / VEC;                         // blocks in flight: 32 registers' worth
+    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch * 2048;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? o_done : s_full;
     bool ok = true;
-    for (int i = 0; i < n_blocks; ++i) {
-      const int b = i & 1, f = i % A;
-      const int pair = queue[0];
-      const uint32_t raw = smem_u32(ring + 2 * f * SM::kSlot), tile = tiles + b * kTile + ch0 * 2048;
-      ok = mbar_wait(&arrived[f], (uint32_t)(i / A) & 1, &misc[1]);
-      if (i >= 2) ok = ok && mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      constexpr int kFull8 = 16 << 8 | 16 << 24;
-      if (pair == (kFull8 | ARGUS_FP8_E4M3 * 0x10001)) {
-        convert_rows<D, BFM, ARGUS_FP8_E4M3, 32, SM::kSlot>(raw, tile, lane, 32);
-      } else {
-#pragma unroll 1
-        for (int sub = 0; sub < 2; ++sub) {
-          const int state = (pair >> (16 * sub)) & 0xFFFF, codec = state & 0xFF, n_rows = state >> 8;
-          const uint32_t from = raw + sub * SM::kSlot, to = tile + sub * 2048;
-          if (n_rows == 0 && !is_v) continue;            // a chunk without rows: K is masked, V is set to zero
-          if (W16 && codec <= ARGUS_BF16) convert_rows<D, BFM, ARGUS_BF16, 16, SM::kSlot>(from, to, lane, n_rows);
-          else if (codec == ARGUS_INT8) convert_rows<D, BFM, ARGUS_INT8, 16, SM::kSlot>(from, to, lane, n_rows);
-          else convert_rows<D, BFM, ARGUS_FP8_E4M3, 16, SM::kSlot>(from, to, lane, n_rows);
+    auto fetch = [&](int i, uint4 (&v)[VEC]) {
+      if (i >= n_blocks || !ok) return 0;
+      if (i % kBatch == 0 || i < A) ok = mbar_wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
+      const uint4 d = chunks[(i % kSlots) * 8 + ch];
+      const int state = ok ? (int)d.z : 0;
+      if (state) {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x);
+        if (W16 && (state & 0xFF) <= ARGUS_BF16) {
+          if (is_v) src += (long long)p.Hkv * p.P * (2 * D);
+          load_chunk<D, D / 8>(v, src, lane);
+        } else {
+          if (is_v) src += (long long)p.Hkv * p.P * D;
+          load_chunk<D, D / 16>(v, src, lane);
         }
       }
-      fence_async();
-      __syncwarp();                                      // the tile is written and the slot has been read
-      if (lane == 0) mbar_arrive(&full[b]);
-      const int nxt = issue(f);
+      return state;
+    };
+    uint4 v[A][VEC];
+    int state[A];
 #pragma unroll
-      for (int x = 0; x + 1 < A; ++x) queue[x] = queue[x + 1];
-      queue[A - 1] = nxt;
+    for (int a = 0; a < A; ++a) state[a] = fetch(a, v[a]);
+    for (int i0 = 0; i0 < n_blocks; i0 += A) {
+#pragma unroll
+      for (int a = 0; a < A; ++a) {
+        const int i = i0 + a, b = i & 1;
+        if (i < n_blocks) {
+          if (i >= 2 && ok) ok = mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const int codec = state[a] & 0xFF, n_rows = state[a] >> 8;
+            const uint32_t tile = tiles + b * kTile;
+            if (n_rows > 0 || is_v) {                  // a chunk without rows: K is masked, V is set to zero
+              if (W16 && codec <= ARGUS_BF16) store_chunk<D, BFM, ARGUS_BF16>(v[a], tile, lane, n_rows);
+              else if (codec == ARGUS_INT8) store_chunk<D, BFM, ARGUS_INT8>(v[a], tile, lane, n_rows);
+              else store_chunk<D, BFM, ARGUS_FP8_E4M3>(v[a], tile, lane, n_rows);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&full[b]);
+              // this block's tile was free, so the softmax of four blocks ago is
+              // done: the batch before the last one is not needed any more
+              if (i % kBatch == kBatch - 1 && i >= 2 * kBatch - 1) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
+            }
+            state[a] = fetch(i + A, v[a]);
+          }
+        }
+      }
     }
-    if (!ok) {
-      misc[1] = 1;
-      // the copies in flight land before the CTA ends: the last one of every slot
-      for (int f = 0; f < A; ++f)
-        if (ib > f) mbar_wait(&arrived[f], (uint32_t)((ib - f + A - 1) / A - 1) & 1);
-    }
+    if (!ok) misc[1] = 1;
   } else {
     // ---------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -726,8 +711,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       auto block = [&](auto chunks, int n, int k0) {
         constexpr int N = decltype(chunks)::value;
         const uint32_t sS = tS(n & 1) + lane_off;
-        const float2* sc = scales + (n % kScaleSlots) * 8 + c0;
-        const float* lv = log_vs + (n % kScaleSlots) * 8 + c0;
+        const float2* sc = scales + (n % kSlots) * 8 + c0;
+        const float* lv = log_vs + (n % kSlots) * 8 + c0;
         float v[N][16];
 #pragma unroll
         for (int x = 0; x < N; ++x) tmem_ld16(sS + (c0 + x) * 16, reinterpret_cast<uint32_t(&)[16]>(v[x]));
@@ -1063,7 +1048,7 @@ static size_t workspace(const argus_extend_args* a) {
 
 template <int D, bool BF, bool W16>
 static argus_status launch(const EParams& p, cudaStream_t s) {
-  constexpr int smem = Smem<D, W16>::kBytes;
+  constexpr int smem = Smem<D>::kBytes;
   static PerContext configured;
   argus_status st = configured.ensure([](int) {
     const cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, BF, W16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
