@@ -31,6 +31,7 @@ struct EParams {
   uint32_t* status;
   float scale_log2;
   int n_ctas;
+  int last_query[8];                 // (128 (r + 1) - 1) / G: the query of tile r's last row
   float* ws;                         // pieces: o [2 n_ctas][128][D], then lse2 [2 n_ctas][128]
 };
 
@@ -38,13 +39,16 @@ constexpr int kBM = 128;             // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;             // keys per block
 constexpr int kGroupWarps = 4;       // one softmax warpgroup: a thread per TMEM lane
 constexpr int kSoftmaxWarps = 2 * kGroupWarps;
-constexpr int kLoadWarps = 16;       // eight for K, eight for V: a 16-token chunk of every block each
+constexpr int kLoadWarps = 8;        // four for K, four for V: two 16-token chunks of a block each
+constexpr int kQWarps = 2;
 constexpr int kLookWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kMmaWarp = kLookWarp + 1;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-// 26 warps get 72 registers a thread at launch; the loaders' four-warp groups give
-// up what the softmax groups take: 8 * 104 + 16 * 56 = 24 * 72
-constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kLoadRegs = 56;
+constexpr int kQWarp0 = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kQWarp0 + kQWarps);
+// 20 warps get 96 registers a thread at launch; the loaders' four-warp groups give
+// up what the softmax groups take.  Nothing may spill: the tiles leave the
+// L1 so little that a spilled value comes back from the L2.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kLoadRegs = 88;
 static_assert(kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs <= (kSoftmaxWarps + kLoadWarps) * kLaunchRegs, "registers");
 constexpr int kHalf = kBM * 64 * 2;  // 128 rows x 64 dims: one 128-byte swizzle column
 constexpr int kTmemCols = 512;       // S0 S1 O0 O1, 128 columns each
@@ -58,18 +62,19 @@ constexpr int kMergePad = 20;        // floats per row of the replica merge (16 
 template <int D>
 struct Smem {
   static constexpr int kTile = kBM * D * 2;
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kTile;
+  static constexpr int kOffQ = 0;                                        // two items' tiles
+  static constexpr int kOffK = 2 * kTile;
   static constexpr int kOffV = kOffK + 2 * kTile;
   static constexpr int kOffChunk = kOffV + 2 * kTile;                    // [slot][chunk] uint4: source, state
-  static constexpr int kOffScale = kOffChunk + kSlots * 8 * 16;          // [slot][chunk] float2: ks, vs
-  static constexpr int kOffLogVs = kOffScale + kSlots * 8 * 8;           // [slot][chunk] float
-  static constexpr int kOffQScale = kOffLogVs + kSlots * 8 * 4;
-  static constexpr int kOffML = kOffQScale + kBM * 4;
-  static constexpr int kOffBar = kOffML + 2 * kBM * 8;
-  // q_full, k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], drain, looked[kBatches], used[kBatches]
-  static constexpr int kNumBars = 12 + 2 * kBatches;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kOffScale = kOffChunk + kSlots * 8 * 16;          // [slot][chunk] float4: ks, log2 vs, 1 / vs
+  static constexpr int kOffQScale = kOffScale + kSlots * 8 * 16;         // [2][128]
+  static constexpr int kOffML = kOffQScale + 2 * kBM * 4;
+  static constexpr int kOffMerge = kOffML + 2 * kBM * 8;
+  static constexpr int kOffBar = kOffMerge + 2 * 96 * kMergePad * 4;
+  // q_full[2], k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
+  static constexpr int kNumBars = 15 + 2 * kBatches;
+  static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
+  static constexpr int kOffMisc = kOffItem + 2 * 32;
   static constexpr int kBytes = kOffMisc + 64;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -100,24 +105,27 @@ __device__ __forceinline__ int n_tiles(const EParams& p, const Seq& s) { return 
 __device__ __forceinline__ int tile_blocks(const EParams& p, const Seq& s, int t) {
   int keys = s.len;
   if (p.causal) {
-    const long long last = min(((long long)kBM * (t + 1) - 1) / p.G, (long long)s.n - 1);
-    keys = max(s.len - s.n, 0) + (int)last + 1;
+    const int last = min((int)(((uint32_t)kBM * (t + 1) - 1) / (uint32_t)p.G), s.n - 1);   // rows: fewer than 2^31
+    keys = max(s.len - s.n, 0) + last + 1;
   }
   return max(1, (keys + kBN - 1) / kBN);
 }
 
 // blocks of tiles 0 .. m-1 (m <= T): under the causal mask G tiles further down
-// are 128 queries, hence exactly one block more; only the last tile may be cut short
+// are 128 queries, hence exactly one block more; only the last tile may be cut
+// short.  With f = G a + r tiles before it, residue r of the tiles modulo G occurs
+// a times, or a + 1 times below the remainder.
 __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& s, int m) {
   if (!p.causal) return (long long)m * tile_blocks(p, s, 0);
   const int T = n_tiles(p, s);
   const int f = min(m, T - 1);
-  const int base = max(s.len - s.n, 0);
+  const uint32_t base = (uint32_t)max(s.len - s.n, 0) + kBN;
+  const int a = f / p.G, rem = f - a * p.G;
   long long sum = 0;
-  for (int r = 0; r < min(p.G, f); ++r) {
-    const long long cnt = (f - r + p.G - 1) / p.G;
-    const long long nb0 = (base + (kBM * (r + 1) - 1) / p.G + kBN) / kBN;
-    sum += cnt * nb0 + cnt * (cnt - 1) / 2;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const int cnt = r < p.G ? a + (r < rem) : 0;
+    sum += (long long)cnt * ((base + (uint32_t)p.last_query[r]) / kBN) + (long long)cnt * (cnt - 1) / 2;
   }
   if (m == T && T > 0) sum += tile_blocks(p, s, T - 1);
   return sum;
@@ -200,14 +208,6 @@ struct Cursor {
     }
     nb = tile_blocks(p, s, t);
   }
-  // the cursor in shared memory: the softmax threads read of it what they need
-  // when they need it instead of holding it in registers across the block loop
-  __device__ __forceinline__ void store(volatile uint32_t* m) const {
-    m[0] = s.q0; m[1] = s.n; m[2] = s.len; m[3] = b; m[4] = h; m[5] = t; m[6] = T; m[7] = blk; m[8] = nb; m[9] = left;
-  }
-  __device__ __forceinline__ void load(const volatile uint32_t* m) {
-    s.q0 = m[0]; s.n = m[1]; s.len = m[2]; b = m[3]; h = m[4]; t = m[5]; T = m[6]; blk = m[7]; nb = m[8]; left = m[9];
-  }
   // `n` blocks further, which end in this item or at its end
   __device__ __forceinline__ void advance(const EParams& p, int n) {
     blk += n;
@@ -275,8 +275,29 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {   // read once: past 
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const uint8_t* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// mbar_wait (common.cuh) whose every attempt lets the hardware suspend the warp
+// for up to kSuspendNs: 28 warps share the issue slots, and most of them wait.
+constexpr uint32_t kSuspendNs = 1000;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
+  const unsigned long long t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    if (ok) return true;
+    if (*abort || global_ns() - t0 > kWaitLimitNs) return false;
+  }
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void group_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
@@ -374,27 +395,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   constexpr bool BFM = BF && W16;            // operand type of the MMAs
   constexpr float kPBias = BFM ? 0.f : 7.f;  // fp16 P is stored as P * 2^7 (at most 2^15)
   extern __shared__ __align__(1024) uint8_t smem[];
-  if (smem_u32(smem) & 1023) {         // the swizzled tiles need it, and there is no room to round up
+  if (smem_u32(smem) & 1023) {         // the swizzled tiles need it
     if (threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusTimeoutBit);
     return;
   }
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);
-  uint64_t* k_full = q_full + 1;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);   // item k: buffer k & 1
+  uint64_t* k_full = q_full + 2;       // block n: buffer n & 1
   uint64_t* v_full = k_full + 2;
-  uint64_t* s_full = v_full + 2;     // scores complete; the K tile is free
+  uint64_t* s_full = v_full + 2;       // scores complete; the K tile is free
   uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;     // P.V complete; the V tile is free
-  uint64_t* drain = o_done + 2;
-  uint64_t* looked = drain + 1;      // a batch of blocks is looked up
-  uint64_t* used = looked + kBatches;   // nobody needs the batch any more
+  uint64_t* o_done = p_full + 2;       // P.V complete; the V tile is free
+  uint64_t* o_free = o_done + 2;       // item k: its epilogue is done with O and with its Q buffer
+  uint64_t* drain = o_free + 2;
+  uint64_t* looked = drain + 1;        // a batch of blocks is looked up
+  uint64_t* used = looked + kBatches;  // nobody needs the batch any more
   // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] the first one's
-  // number within its sequence, [6..15] the softmax groups' cursor
+  // number within its sequence
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
   volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
+  // [2][8]: q0, n, len, h, t, first block, blocks of the piece, blocks of the item
+  volatile int* items = reinterpret_cast<volatile int*>(smem + SM::kOffItem);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
+  float* q_scale = reinterpret_cast<float*>(smem + SM::kOffQScale);
   uint4* chunks = reinterpret_cast<uint4*>(smem + SM::kOffChunk);       // [slot][chunk]: K source, state
-  float2* scales = reinterpret_cast<float2*>(smem + SM::kOffScale);     // [slot][chunk]: ks (< 0: not to be read), vs
-  float* log_vs = reinterpret_cast<float*>(smem + SM::kOffLogVs);       // [slot][chunk]: log2 vs
+  float4* scales = reinterpret_cast<float4*>(smem + SM::kOffScale);     // [slot][chunk]: ks (< 0: not to be read), log2 vs, 1 / vs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -409,13 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     }
   }
   if (threadIdx.x == 32) {
-    mbar_init(q_full, kSoftmaxWarps);
     for (int b = 0; b < 2; ++b) {
+      mbar_init(&q_full[b], kQWarps);
       mbar_init(&k_full[b], kLoadWarps / 2);
       mbar_init(&v_full[b], kLoadWarps / 2);
       mbar_init(&s_full[b], 1);
       mbar_init(&p_full[b], kSoftmaxWarps);
       mbar_init(&o_done[b], 1);
+      mbar_init(&o_free[b], kSoftmaxWarps);
     }
     mbar_init(drain, 1);
     for (int k = 0; k < kBatches; ++k) {
@@ -447,14 +472,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     if (lane == 0) {
       constexpr uint32_t idQK = idesc_f16kind(BFM, false, kBN);
       constexpr uint32_t idPV = idesc_f16kind(BFM, true, D);
-      const uint32_t q_s = smem_u32(smem + SM::kOffQ);
       Cursor c;
       c.start(p, misc[2], misc64[2], n_blocks);
       int n0 = 0;                      // blocks before this item's
       bool ok = true;
-      auto issue_s = [&](int n) {
-        const int b = (int)(n & 1);
-        if (!mbar_wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
+      auto issue_s = [&](int n, uint32_t q_s) {
+        const int b = n & 1;
+        if (!wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         tc_fence_after();
         const uint32_t k_s = smem_u32(smem + SM::kOffK + b * kTile);
 #pragma unroll
@@ -467,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       };
       auto issue_pv = [&](int n, bool first) {
         const int b = n & 1;
-        if (!mbar_wait(&v_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
-        if (!mbar_wait(&p_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
+        if (!wait(&v_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
+        if (!wait(&p_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
         tc_fence_after();
         const uint32_t v_s = smem_u32(smem + SM::kOffV + b * kTile);
 #pragma unroll
@@ -478,23 +502,86 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         mma_commit(&o_done[b]);
         return true;
       };
-      for (uint32_t item = 0; ok && c.left > 0; ++item) {
+      for (int k = 0; ok && c.left > 0; ++k) {
         const int nb = min(c.nb - c.blk, c.left);
-        ok = mbar_wait(q_full, item & 1, &misc[1]);
-        if (ok) ok = issue_s(n0);
-        if (ok && nb > 1) ok = issue_s(n0 + 1);
+        const uint32_t q_s = smem_u32(smem + SM::kOffQ + (k & 1) * kTile);
+        ok = wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]);
+        if (ok) ok = issue_s(n0, q_s);
+        if (ok && nb > 1) ok = issue_s(n0 + 1, q_s);
+        // the scores of this item may overtake the epilogue of the one before; its P.V may not
+        if (ok && k > 0) ok = wait(&o_free[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1, &misc[1]);
         for (int i = 0; i < nb && ok; ++i) {
           ok = issue_pv(n0 + i, i == 0);
-          if (ok && i + 2 < nb) ok = issue_s(n0 + i + 2);
+          if (ok && i + 2 < nb) ok = issue_s(n0 + i + 2, q_s);
         }
         n0 += nb;
         c.advance(p, nb);
       }
       if (!ok) {
         misc[1] = 1;
+        const volatile uint32_t never = 0;
         mma_commit(drain);             // TMEM is freed after the MMAs in flight
-        mbar_wait(drain, 0);
+        wait(drain, 0, &never);
       }
+    }
+  } else if (warp >= kQWarp0) {
+    // ---------------------------------------------------------- Q tiles
+    // Row l of an item's tile goes to TMEM lanes l, l + per, ...; zeros behind the
+    // last row.  An item ahead of the softmax groups, so that nothing waits for it
+    // but the first.
+    constexpr int V = D / 8, RS = 32 / V * kQWarps;    // vectors per row; rows of a step
+    const int v = lane % V, r0 = (warp - kQWarp0) * (32 / V) + lane / V;
+    Cursor c;
+    c.start(p, misc[2], misc64[2], n_blocks);
+    for (int k = 0; c.left > 0; ++k) {
+      const int buf = k & 1, nb = min(c.nb - c.blk, c.left);
+      if (k >= 2 && !__all_sync(0xffffffffu, wait(&o_free[buf], (uint32_t)((k - 2) >> 1) & 1, &misc[1]))) { misc[1] = 1; break; }
+      const int lin0 = c.t * kBM, rows = min(kBM, c.s.n * p.G - lin0);
+      const int nrep = replicas(rows), per = kBM / nrep;
+      if (warp == kQWarp0 && lane == 0) {
+        volatile int* it = items + 8 * buf;
+        it[0] = c.s.q0; it[1] = c.s.n; it[2] = c.s.len; it[3] = c.h; it[4] = c.t; it[5] = c.blk; it[6] = nb; it[7] = c.nb;
+      }
+      const uint32_t q_s = smem_u32(smem + SM::kOffQ + buf * kTile);
+      const uint16_t* src = p.q + (long long)c.s.q0 * p.qs + (long long)c.h * p.G * D + v * 8;
+      int tok = (lin0 + r0) / p.G, g = lin0 + r0 - tok * p.G;
+#pragma unroll 1
+      for (int l0 = r0; l0 < per; l0 += 4 * RS) {
+        uint4 q[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          q[x] = make_uint4(0, 0, 0, 0);
+          if (l0 + x * RS < rows) q[x] = *reinterpret_cast<const uint4*>(src + (long long)tok * p.qs + g * D);
+          for (g += RS; g >= p.G; g -= p.G) ++tok;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int l = l0 + x * RS;
+          if (l >= per) break;         // the same for a whole row's lanes, and for the warp (per: a multiple of RS)
+          float f1 = 1.f;
+          if (BF && !BFM) {
+            // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
+            uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w}, mx = 0;   // magnitudes of bf16 order like their bits
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+#pragma unroll
+            for (int o = V / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int ex = max((int)(mx >> 23), 15);    // biased; from 15 on 2^(141 - ex) is a normal number
+            f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
+            q[x] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          for (int r = 0; r < nrep; ++r) {
+            sts16(q_s + tile_off(l + r * per, v), q[x].x, q[x].y, q[x].z, q[x].w);
+            if (v == 0) q_scale[buf * kBM + l + r * per] = 1.f / f1;
+          }
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[buf]);
+      c.advance(p, nb);
     }
   } else if (warp == kLookWarp) {
     // ---------------------------------------------------------- lookup
@@ -517,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         c.advance(p, 1);
       }
       if (k.n_rows > 0) {
-        const int page = key / p.P;
+        const int page = (int)((uint32_t)key / (uint32_t)p.P);
         k.row = key - page * p.P;
         k.first = k.first && k.row == 0;
         const size_t e = (size_t)b * p.max_pages + page;
@@ -543,6 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           const long long unit = (long long)now.slot * 2 * p.Hkv + now.h;
           src = r.codes + (unit * p.P + now.row) * rb;
           state = now.codec | now.n_rows << 8;
+          // toward the L2, some blocks before a loader asks for them: what the
+          // loaders have in flight in registers would not cover a DRAM read
+          prefetch_l2(src, 16 * rb);
+          prefetch_l2(src + (long long)p.Hkv * p.P * rb, 16 * rb);
           if (now.codec >= ARGUS_FP8_E4M3) {
             ks = r.meta[unit];
             vs = r.meta[unit + p.Hkv];
@@ -550,74 +641,75 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         }
       }
       ahead = look();
-      if (k >= kBatches && !__all_sync(0xffffffffu, mbar_wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
+      if (k >= kBatches && !__all_sync(0xffffffffu, wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
         misc[1] = 1;
         break;
       }
       const int at = (k % kBatches) * 32 + lane;
       const unsigned long long addr = reinterpret_cast<unsigned long long>(src);
       chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), state, 0);
-      scales[at] = make_float2(ks < 0.f ? -1.f : ks * p.scale_log2, vs);
-      log_vs[at] = log2f(vs);          // 0: -inf
+      const float lvs = log2f(vs);     // 0: -inf
+      // a scale far from 1: its chunk's sum is kept apart, and does not enter the others'
+      scales[at] = make_float4(ks < 0.f ? -1.f : ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / vs, 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&looked[k % kBatches]);
     }
   } else if (warp >= kSoftmaxWarps) {
     // ---------------------------------------------------------- loaders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int lw = warp - kSoftmaxWarps, ch = lw & 7;
-    const bool is_v = lw >= 8;
+    const int lw = warp - kSoftmaxWarps, ch0 = 2 * (lw & 3);   // chunks ch0, ch0 + 1 of every block
+    const bool is_v = lw >= kLoadWarps / 2;
     constexpr int VEC = W16 ? D / 16 : D / 32;         // vectors of a chunk
-    constexpr int A = 8 / VEC;                         // blocks in flight: 32 registers' worth
-    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch * 2048;
+    constexpr int A = 8 / VEC;                         // chunks in flight: 32 registers' worth
+    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch0 * 2048;
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? o_done : s_full;
+    const long long v_off = is_v ? (long long)p.Hkv * p.P * D : 0;   // V behind K in an 8-bit page
     bool ok = true;
-    auto fetch = [&](int i, uint4 (&v)[VEC]) {
-      if (i >= n_blocks || !ok) return 0;
-      if (i % kBatch == 0 || i < A) ok = mbar_wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
-      const uint4 d = chunks[(i % kSlots) * 8 + ch];
-      const int state = ok ? (int)d.z : 0;
+    // chunk u of the warp's on its way (two per block); returns its state
+    auto fetch = [&](int u, uint4 (&v)[VEC]) {
+      const int i = u >> 1, sub = u & 1;
+      if (i >= n_blocks || !ok) return 0u;
+      if (i % kBatch == 0 && sub == 0) ok = wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
+      const uint4 d = chunks[(i % kSlots) * 8 + ch0 + sub];
+      const uint32_t state = ok ? d.z : 0;
       if (state) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x);
-        if (W16 && (state & 0xFF) <= ARGUS_BF16) {
-          if (is_v) src += (long long)p.Hkv * p.P * (2 * D);
-          load_chunk<D, D / 8>(v, src, lane);
-        } else {
-          if (is_v) src += (long long)p.Hkv * p.P * D;
-          load_chunk<D, D / 16>(v, src, lane);
-        }
+        const uint8_t* src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x) + v_off;
+        if (W16 && (state & 0xFF) <= ARGUS_BF16) load_chunk<D, D / 8>(v, src + v_off, lane);
+        else load_chunk<D, D / 16>(v, src, lane);
       }
       return state;
     };
     uint4 v[A][VEC];
-    int state[A];
+    uint32_t states[A];
 #pragma unroll
-    for (int a = 0; a < A; ++a) state[a] = fetch(a, v[a]);
-    for (int i0 = 0; i0 < n_blocks; i0 += A) {
+    for (int a = 0; a < A; ++a) states[a] = fetch(a, v[a]);
+    for (int u0 = 0; u0 < 2 * n_blocks; u0 += A) {
 #pragma unroll
       for (int a = 0; a < A; ++a) {
-        const int i = i0 + a, b = i & 1;
-        if (i < n_blocks) {
-          if (i >= 2 && ok) ok = mbar_wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
+        const int u = u0 + a, sub = u & 1, i = u >> 1, b = i & 1;
+        if (u < 2 * n_blocks) {
+          if (sub == 0 && i >= 2 && ok) ok = wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            const int codec = state[a] & 0xFF, n_rows = state[a] >> 8;
-            const uint32_t tile = tiles + b * kTile;
+            const int codec = states[a] & 0xFF, n_rows = states[a] >> 8;
+            const uint32_t to = tiles + b * kTile + sub * 2048;
             if (n_rows > 0 || is_v) {                  // a chunk without rows: K is masked, V is set to zero
-              if (W16 && codec <= ARGUS_BF16) store_chunk<D, BFM, ARGUS_BF16>(v[a], tile, lane, n_rows);
-              else if (codec == ARGUS_INT8) store_chunk<D, BFM, ARGUS_INT8>(v[a], tile, lane, n_rows);
-              else store_chunk<D, BFM, ARGUS_FP8_E4M3>(v[a], tile, lane, n_rows);
+              if (W16 && codec <= ARGUS_BF16) store_chunk<D, BFM, ARGUS_BF16>(v[a], to, lane, n_rows);
+              else if (codec == ARGUS_INT8) store_chunk<D, BFM, ARGUS_INT8>(v[a], to, lane, n_rows);
+              else store_chunk<D, BFM, ARGUS_FP8_E4M3>(v[a], to, lane, n_rows);
             }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&full[b]);
-              // this block's tile was free, so the softmax of four blocks ago is
-              // done: the batch before the last one is not needed any more
-              if (i % kBatch == kBatch - 1 && i >= 2 * kBatch - 1) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
+            states[a] = fetch(u + A, v[a]);
+            if (sub == 1) {
+              fence_async();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&full[b]);
+                // this block's tile was free, so the softmax of four blocks ago is
+                // done: the batch before the last one is not needed any more
+                if (i % kBatch == kBatch - 1 && i >= kBatch) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
+              }
             }
-            state[a] = fetch(i + A, v[a]);
           }
         }
       }
@@ -630,71 +722,27 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const int tl = wq * 32 + lane;                     // TMEM lane
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t sO = tO(grp) + lane_off;
-    const uint32_t q_s = smem_u32(smem + SM::kOffQ);
-    float* merge = reinterpret_cast<float*>(smem + SM::kOffQ) + grp * 96 * kMergePad;
-    float* q_scale = reinterpret_cast<float*>(smem + SM::kOffQScale);
-    if (warp == 0) {
-      Cursor c;
-      c.start(p, misc[2], misc64[2], n_blocks);
-      if (lane == 0) c.store(misc + 6);
-    }
+    float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge) + grp * 96 * kMergePad;
     int n0 = 0;
-    bool alive = true;
-    while (true) {
-      group_bar(1, kSoftmaxWarps * 32);
-      Cursor c;
-      c.load(misc + 6);
-      if (c.left <= 0) break;
-      const int nb = min(c.nb - c.blk, c.left), k_first = c.blk * kBN;
-      const int lin0 = c.t * kBM;                      // rows of a sequence and head: fewer than 2^31
-      const int rows = min(kBM, c.s.n * p.G - lin0);
+    for (int k = 0; n0 < n_blocks; ++k) {
+      bool alive = wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]);
+      if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) { misc[1] = 1; break; }   // all leave, or none
+      const volatile int* it = items + 8 * (k & 1);
+      const int nb = it[6], k_first = it[5] * kBN;
+      const int rows = min(kBM, it[1] * p.G - it[4] * kBM);
       const int nrep = replicas(rows), per = kBM / nrep;
-      // ---- Q tile: row l of the tile in lanes l, l + per, ...; zeros behind the last row
-#pragma unroll
-      for (int x = 0; x < kBM * (D / 8) / (kSoftmaxWarps * 32); ++x) {
-        const int f = x * kSoftmaxWarps * 32 + threadIdx.x;
-        const int pr = f / (D / 8), v = f % (D / 8), l = pr & (per - 1);
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (l < rows) {
-          const int lin = lin0 + l, tok = lin / p.G, g = lin - tok * p.G;
-          q = *reinterpret_cast<const uint4*>(p.q + (long long)(c.s.q0 + tok) * p.qs + (c.h * p.G + g) * D + v * 8);
-        }
-        if (BF && !BFM) {
-          // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
-          uint32_t w[4] = {q.x, q.y, q.z, q.w}, mx = 0;   // magnitudes of bf16 order like their bits
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
-#pragma unroll
-          for (int o = D / 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int ex = max((int)(mx >> 23), 15);        // biased; from 15 on 2^(141 - ex) is a normal number
-          const float f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
-          q = make_uint4(w[0], w[1], w[2], w[3]);
-          if (v == 0) q_scale[pr] = 1.f / f1;
-        }
-        sts16(q_s + tile_off(pr, v), q.x, q.y, q.z, q.w);
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      float qf = 1.f;
-      if (BF && !BFM) {
-        group_bar(1, kSoftmaxWarps * 32);
-        qf = q_scale[tl];
-      }
-
-      const int l_row = tl & (per - 1);          // row within the tile
+      const float qf = (BF && !BFM) ? q_scale[(k & 1) * kBM + tl] : 1.f;
+      const int l_row = tl & (per - 1);                // row within the tile
       const int rep = tl / per;                        // this lane's replica: chunks c0 ... of the group's four
       const int c0 = 4 * grp + rep * (4 / nrep);
       // rows behind the last one (zero queries) see what the last one sees: they are never written
-      const int tok = min((lin0 + l_row) / p.G, c.s.n - 1);
-      const int vis_last = min(p.causal ? c.s.len - c.s.n + tok : c.s.len - 1, c.s.len - 1);
+      const int tok = min((it[4] * kBM + l_row) / p.G, it[1] - 1);
+      const int vis_last = min(p.causal ? it[2] - it[1] + tok : it[2] - 1, it[2] - 1);
       // running reference and sum; the sum of chunks with a V scale far from 1 is
       // kept apart, with a reference of its own: relative to m (which bounds p
       // times the scale) it could leave the fp32 range, and a page whose V is 0 must
       // not push every other page's P out of the 16-bit range
-      float m = -INFINITY, la = 0.f, lb = 0.f, mz = -INFINITY, lz = 0.f;
+      float m = -INFINITY, l = 0.f, mz = -INFINITY, lz = 0.f;
       auto scale_acc = [&](float r) {                  // rare: few registers, not speed
 #pragma unroll 1
         for (int x = 0; x < D / 8; ++x) {
@@ -708,25 +756,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tmem_wait_st();
       };
       // One block, N chunks of 16 keys per lane, all scores in registers.
-      auto block = [&](auto chunks, int n, int k0) {
-        constexpr int N = decltype(chunks)::value;
+      auto block = [&](auto chunks_of, int n, int k0) {
+        constexpr int N = decltype(chunks_of)::value;
         const uint32_t sS = tS(n & 1) + lane_off;
-        const float2* sc = scales + (n % kSlots) * 8 + c0;
-        const float* lv = log_vs + (n % kSlots) * 8 + c0;
+        const float4* sc = scales + (n % kSlots) * 8 + c0;
         float v[N][16];
 #pragma unroll
         for (int x = 0; x < N; ++x) tmem_ld16(sS + (c0 + x) * 16, reinterpret_cast<uint32_t(&)[16]>(v[x]));
         // lanes 0 .. N-1 look at their chunk, every lane at its row's last key
-        const bool odd = lane < N && (sc[lane].x < 0.f || fabsf(lv[lane]) > kFarScale);
+        const bool odd = lane < N && (sc[lane].x < 0.f || fabsf(sc[lane].y) > kFarScale);
         const int lim = vis_last - k0 - c0 * 16;       // keys e <= lim of the lane's are visible
         const bool edge = __any_sync(0xffffffffu, odd || lim < N * 16 - 1);
         tmem_wait_ld();
-        // the maximum of score + log2 of the V scale, so that P times that scale stays in range
-        float mj = -INFINITY;
         if (edge) {
+          // the scores scaled and masked here; a far chunk's log2 V scale added, its sum kept apart
 #pragma unroll
           for (int x = 0; x < N; ++x) {
-            const float kq = sc[x].x * qf, lvc = lv[x];
+            const float kq = sc[x].x * qf, lvc = sc[x].y;
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[x][e] = (kq >= 0.f && x * 16 + e <= lim) ? v[x][e] * kq : -INFINITY;
             if (fabsf(lvc) > kFarScale) {
@@ -739,11 +785,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) lz += fast_exp2(v[x][e] - top);
               }
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[x][e] += lvc;
             }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[x][e] += lvc;
           }
         }
+        // the maximum of score + log2 of the V scale, so that P times that scale stays in range
+        float mj = -INFINITY;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
           float a0 = max3(v[x][0], v[x][1], v[x][2]), a1 = max3(v[x][3], v[x][4], v[x][5]);
@@ -752,22 +800,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           a0 = max3(a0, v[x][10], v[x][11]);
           a1 = max3(a1, v[x][12], v[x][13]);
           a0 = max3(a0, v[x][14], v[x][15]);
-          const bool far = edge && fabsf(lv[x]) > kFarScale;
-          mj = fmaxf(mj, fmaf(fmaxf(a0, a1), edge ? 1.f : sc[x].x * qf, far ? 0.f : lv[x]));
+          const float a = fmaxf(a0, a1);
+          mj = fmaxf(mj, edge ? a : fmaf(a, sc[x].x * qf, sc[x].y));
         }
         const bool move = mj > m + kRescaleThreshold || (m == -INFINITY && mj != -INFINITY);
         const bool scale_o = move && m != -INFINITY;
         if (__any_sync(0xffffffffu, scale_o)) {
           // the block before (of this item, as m is set) is the last that added to O
-          if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1, &misc[1]))) return false;
+          if (!__all_sync(0xffffffffu, wait(&o_done[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1, &misc[1]))) return false;
           tc_fence_after();
           const float r = scale_o ? fast_exp2(m - mj) : 1.f;
           scale_acc(r);
-          la *= r;
-          lb *= r;
+          l *= r;
         }
         if (move) m = mj;
-        // P over the consumed scores, packed: the group's 64 keys in 32 columns, zeros for the other replicas' keys
+        // P times the V scale over the consumed scores, packed: the group's 64
+        // keys in 32 columns, zeros for the other replicas' keys.  The row sum wants P
+        // without the scale: a chunk's sum is divided by it once.
         const float mm = (m == -INFINITY) ? 0.f : m - kPBias;
         const uint32_t sP = sS + 64 * grp;
         if (N < 4) {
@@ -778,20 +827,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         }
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-          const bool far = edge && fabsf(lv[x]) > kFarScale;
-          const float kq = edge ? 1.f : sc[x].x * qf, vs = far ? 1.f : sc[x].y;
-          const float sa = la, sb = lb;
+          const float4 s = sc[x];
+          const float kq = edge ? 1.f : s.x * qf, shift = edge ? -mm : s.y - mm;
+          float la = 0.f, lb = 0.f;
           uint32_t o[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float x0, x1;
-            f2_fma(x0, x1, v[x][2 * e], v[x][2 * e + 1], kq, kq, -mm, -mm);
-            float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+            float x0, x1, p0, p1;
+            f2_fma(x0, x1, v[x][2 * e], v[x][2 * e + 1], kq, kq, shift, shift);
+            p0 = fast_exp2(x0);
+            p1 = fast_exp2(x1);
             f2_add(la, lb, la, lb, p0, p1);
-            f2_mul(p0, p1, p0, p1, vs, vs);
             o[e] = BFM ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
-          if (far) { la = sa; lb = sb; }
+          l = fmaf(la + lb, s.z, l);
           tmem_st8(sP + (c0 - 4 * grp + x) * 8, o);
         }
         tmem_wait_st();
@@ -799,7 +848,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       };
       for (int i = 0; i < nb; ++i) {
         const int n = n0 + i, k0 = k_first + i * kBN;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; break; }
+        if (!__all_sync(0xffffffffu, wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; break; }
         tc_fence_after();
         if (nrep == 4) alive = block(std::integral_constant<int, 1>{}, n, k0);
         else if (nrep == 2) alive = block(std::integral_constant<int, 2>{}, n, k0);
@@ -809,11 +858,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[n & 1]);
       }
-      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(&o_done[(n0 + nb - 1) & 1], (uint32_t)((n0 + nb - 1) >> 1) & 1, &misc[1]));
+      if (alive) alive = __all_sync(0xffffffffu, wait(&o_done[(n0 + nb - 1) & 1], (uint32_t)((n0 + nb - 1) >> 1) & 1, &misc[1]));
       if (!alive) misc[1] = 1;
       tc_fence_after();
       // references in the units that l was summed in
-      float ref = m == -INFINITY ? -INFINITY : m - kPBias, sum = la + lb;
+      float ref = m == -INFINITY ? -INFINITY : m - kPBias, sum = l;
       if (__any_sync(0xffffffffu, mz != -INFINITY)) {
         const float top = fmaxf(ref, mz);
         const float r = (mz == -INFINITY) ? 1.f : fast_exp2(ref - top);   // ref = -inf: 0
@@ -827,7 +876,6 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       tc_fence_before();
       group_bar(1, kSoftmaxWarps * 32);
       tc_fence_after();
-      c.load(misc + 6);
       // ---- epilogue: both groups' and all replicas' sums of a row joined; group g takes half the dims
       float M = -INFINITY;
       for (int x = 0; x < 2 * nrep; ++x) M = fmaxf(M, ml[(x & 1) * kBM + (x >> 1) * per + l_row].x);
@@ -841,11 +889,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const float inv = have ? 1.f / l_all : 0.f;
       const float w0 = (have && y0.x != -INFINITY) ? fast_exp2(y0.x - M) * inv : 0.f;
       const float w1 = (have && y1.x != -INFINITY) ? fast_exp2(y1.x - M) * inv : 0.f;
-      const bool whole = c.blk == 0 && nb == c.nb;
-      const int piece = 2 * blockIdx.x + (c.blk == 0 ? 1 : 0);
+      const bool whole = it[5] == 0 && nb == it[7];
+      const int piece = 2 * blockIdx.x + (it[5] == 0 ? 1 : 0);
       const bool writes = alive && rep == 0 && l_row < rows;
-      const int lin = c.t * kBM + l_row, otok = lin / p.G;
-      const size_t orow = writes ? (size_t)(c.s.q0 + otok) * p.Hq + c.h * p.G + (lin - otok * p.G) : 0;
+      const int lin = it[4] * kBM + l_row, otok = lin / p.G;
+      const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         const int col = grp * (D / 2) + x * 16;
@@ -900,16 +948,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         if (!whole) piece_lse(p, D, piece)[l_row] = lse;
         else if (p.lse2) p.lse2[orow] = lse;
       }
-      // O, (m, l) and the merge area (the Q tile) are read before the next item's
+      // O, (m, l), the merge area and the item's description have been read
       tc_fence_before();
       if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) break;   // all leave, or none
+      if (lane == 0) mbar_arrive(&o_free[k & 1]);
       n0 += nb;
-      if (warp == 0) {
-        c.load(misc + 6);
-        c.advance(p, nb);
-        __syncwarp();                                  // every lane has loaded
-        if (lane == 0) c.store(misc + 6);
-      }
     }
   }
 
@@ -1119,6 +1162,7 @@ extern "C" argus_status argus_paged_extend_attn(const argus_extend_args* a, void
   p.scale_log2 = (float)((double)a->softmax_scale * 1.4426950408889634);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.n_ctas = extend::grid_size(a);
+  for (int r = 0; r < 8; ++r) p.last_query[r] = (extend::kBM * (r + 1) - 1) / p.G;
   if (extend::max_blocks(a) / p.n_ctas >= 0x7fffffffll) return fail(ARGUS_E_UNSUPPORTED, "extend: too many key blocks");
   p.ws = static_cast<float*>(ws);
   const bool bf = a->q_dtype == ARGUS_BF16, w16 = p.pool[a->q_dtype].n_slots > 0;
