@@ -39,16 +39,16 @@ constexpr int kBM = 128;             // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;             // keys per block
 constexpr int kGroupWarps = 4;       // one softmax warpgroup: a thread per TMEM lane
 constexpr int kSoftmaxWarps = 2 * kGroupWarps;
-constexpr int kLoadWarps = 8;        // four for K, four for V: two 16-token chunks of a block each
+constexpr int kLoadWarps = 16;       // eight for K, eight for V: a 16-token chunk of every block each
 constexpr int kQWarps = 2;
 constexpr int kLookWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kMmaWarp = kLookWarp + 1;
 constexpr int kQWarp0 = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kQWarp0 + kQWarps);
-// 20 warps get 96 registers a thread at launch; the loaders' four-warp groups give
+// 28 warps get 72 registers a thread at launch; the loaders' four-warp groups give
 // up what the softmax groups take.  Nothing may spill: the tiles leave the
 // L1 so little that a spilled value comes back from the L2.
-constexpr int kLaunchRegs = 96, kSoftmaxRegs = 104, kLoadRegs = 88;
+constexpr int kLaunchRegs = 72, kSoftmaxRegs = 104, kLoadRegs = 56;
 static_assert(kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs <= (kSoftmaxWarps + kLoadWarps) * kLaunchRegs, "registers");
 constexpr int kHalf = kBM * 64 * 2;  // 128 rows x 64 dims: one 128-byte swizzle column
 constexpr int kTmemCols = 512;       // S0 S1 O0 O1, 128 columns each
@@ -332,20 +332,24 @@ __device__ __forceinline__ int lane_vec(int lane) {
   return (VB == 8 && D == 128) ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane % VB;
 }
 
-template <int D, int VB, int N>
-__device__ __forceinline__ void load_chunk(uint4 (&v)[N], const uint8_t* src, int lane) {
-  src += (lane_row<D, VB>(lane) * VB + lane_vec<D, VB>(lane)) * 16;
+// kSteps steps of a chunk from step s0 on: registers from the chunk at src ...
+constexpr int kSteps = 4;
+template <int D, int VB>
+__device__ __forceinline__ void load_steps(uint4 (&v)[kSteps], const uint8_t* src, int lane, int s0) {
+  src += (lane_row<D, VB>(lane) * VB + lane_vec<D, VB>(lane)) * 16 + s0 * 512;
 #pragma unroll
-  for (int s = 0; s < VB / 2; ++s) v[s] = ldg16(src + s * 512);
+  for (int s = 0; s < kSteps; ++s)
+    if (s < VB / 2) v[s] = ldg16(src + s * 512);
 }
 
-// The chunk to its tile; `tile`: the place of its first row.  Rows from n_rows on become zeros (P is 0
-// there, and 0 times what the page holds behind the sequence would be NaN if that is).
-template <int D, bool BF, int CODEC, int N>
-__device__ __forceinline__ void store_chunk(uint4 (&v)[N], uint32_t tile, int lane, int n_rows) {
+// ... and to the tile; `tile`: the place of the chunk's first row.  Rows from
+// n_rows on become zeros (P is 0 there, and 0 times what the page holds behind
+// the sequence would be NaN if that is).
+template <int D, bool BF, int CODEC>
+__device__ __forceinline__ void store_steps(uint4 (&v)[kSteps], uint32_t tile, int lane, int n_rows, int s0) {
   constexpr int VB = CODEC <= ARGUS_BF16 ? D / 8 : D / 16;   // vectors per raw row
-  constexpr int STEPS = VB / 2, ROWS = 32 / VB;              // rows per step
-  const int r0 = lane_row<D, VB>(lane), j = lane_vec<D, VB>(lane);
+  constexpr int STEPS = VB / 2 < kSteps ? VB / 2 : kSteps, ROWS = 32 / VB;   // rows per step
+  const int r0 = lane_row<D, VB>(lane) + s0 * ROWS, j = lane_vec<D, VB>(lane);
   if (n_rows < 16) {
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
@@ -358,6 +362,7 @@ __device__ __forceinline__ void store_chunk(uint4 (&v)[N], uint32_t tile, int la
   const uint32_t off = (uint32_t)(((c & 7) ^ (r0 & 7)) << 4);
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
+    // r0 + s ROWS adds no carry into or out of r0's low bits: xor and sum agree
     const uint32_t at = base + s * ROWS * 128 + (off ^ (uint32_t)(((s * ROWS) & 7) << 4));
     if constexpr (CODEC <= ARGUS_BF16) {
       sts16(at, v[s].x, v[s].y, v[s].z, v[s].w);
@@ -657,60 +662,62 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   } else if (warp >= kSoftmaxWarps) {
     // ---------------------------------------------------------- loaders
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
-    const int lw = warp - kSoftmaxWarps, ch0 = 2 * (lw & 3);   // chunks ch0, ch0 + 1 of every block
+    const int lw = warp - kSoftmaxWarps, ch = lw & 7;
     const bool is_v = lw >= kLoadWarps / 2;
-    constexpr int VEC = W16 ? D / 16 : D / 32;         // vectors of a chunk
-    constexpr int A = 8 / VEC;                         // chunks in flight: 32 registers' worth
-    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch0 * 2048;
+    const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch * 2048;
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? o_done : s_full;
     const long long v_off = is_v ? (long long)p.Hkv * p.P * D : 0;   // V behind K in an 8-bit page
     bool ok = true;
-    // chunk u of the warp's on its way (two per block); returns its state
-    auto fetch = [&](int u, uint4 (&v)[VEC]) {
-      const int i = u >> 1, sub = u & 1;
-      if (i >= n_blocks || !ok) return 0u;
-      if (i % kBatch == 0 && sub == 0) ok = wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
-      const uint4 d = chunks[(i % kSlots) * 8 + ch0 + sub];
-      const uint32_t state = ok ? d.z : 0;
-      if (state) {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x) + v_off;
-        if (W16 && (state & 0xFF) <= ARGUS_BF16) load_chunk<D, D / 8>(v, src + v_off, lane);
-        else load_chunk<D, D / 16>(v, src, lane);
+    uint4 v[kSteps];
+    uint32_t state = 0;
+    const uint8_t* src = nullptr;
+    // the warp's chunk of block i on its way: all of it, or the first half of
+    // 16-bit rows of 128 dims
+    auto fetch = [&](int i) {
+      state = 0;
+      if (i >= n_blocks || !ok) return;
+      if (i % kBatch == 0) ok = wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
+      const uint4 d = chunks[(i % kSlots) * 8 + ch];
+      if (!ok || !d.z) return;
+      state = d.z;
+      src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x) + v_off;
+      if (W16 && (state & 0xFF) <= ARGUS_BF16) {
+        src += v_off;
+        load_steps<D, D / 8>(v, src, lane, 0);
+      } else {
+        load_steps<D, D / 16>(v, src, lane, 0);
       }
-      return state;
     };
-    uint4 v[A][VEC];
-    uint32_t states[A];
-#pragma unroll
-    for (int a = 0; a < A; ++a) states[a] = fetch(a, v[a]);
-    for (int u0 = 0; u0 < 2 * n_blocks; u0 += A) {
-#pragma unroll
-      for (int a = 0; a < A; ++a) {
-        const int u = u0 + a, sub = u & 1, i = u >> 1, b = i & 1;
-        if (u < 2 * n_blocks) {
-          if (sub == 0 && i >= 2 && ok) ok = wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            const int codec = states[a] & 0xFF, n_rows = states[a] >> 8;
-            const uint32_t to = tiles + b * kTile + sub * 2048;
-            if (n_rows > 0 || is_v) {                  // a chunk without rows: K is masked, V is set to zero
-              if (W16 && codec <= ARGUS_BF16) store_chunk<D, BFM, ARGUS_BF16>(v[a], to, lane, n_rows);
-              else if (codec == ARGUS_INT8) store_chunk<D, BFM, ARGUS_INT8>(v[a], to, lane, n_rows);
-              else store_chunk<D, BFM, ARGUS_FP8_E4M3>(v[a], to, lane, n_rows);
+    fetch(0);
+    for (int i = 0; i < n_blocks; ++i) {
+      const int b = i & 1;
+      if (i >= 2 && ok) ok = wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const int codec = state & 0xFF, n_rows = state >> 8;
+        const uint32_t to = tiles + b * kTile;
+        if (n_rows > 0 || is_v) {                      // a chunk without rows: K is masked, V is set to zero
+          if (W16 && codec <= ARGUS_BF16) {
+            store_steps<D, BFM, ARGUS_BF16>(v, to, lane, n_rows, 0);
+            if (D == 128) {
+              if (n_rows > 0) load_steps<D, D / 8>(v, src, lane, kSteps);
+              store_steps<D, BFM, ARGUS_BF16>(v, to, lane, n_rows, kSteps);
             }
-            states[a] = fetch(u + A, v[a]);
-            if (sub == 1) {
-              fence_async();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&full[b]);
-                // this block's tile was free, so the softmax of four blocks ago is
-                // done: the batch before the last one is not needed any more
-                if (i % kBatch == kBatch - 1 && i >= kBatch) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
-              }
-            }
+          } else if (codec == ARGUS_INT8) {
+            store_steps<D, BFM, ARGUS_INT8>(v, to, lane, n_rows, 0);
+          } else {
+            store_steps<D, BFM, ARGUS_FP8_E4M3>(v, to, lane, n_rows, 0);
           }
+        }
+        fetch(i + 1);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[b]);
+          // this block's tile was free, so the softmax of four blocks ago is
+          // done: the batch before the last one is not needed any more
+          if (i % kBatch == kBatch - 1 && i >= kBatch) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
         }
       }
     }
