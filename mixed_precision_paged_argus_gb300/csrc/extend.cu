@@ -71,8 +71,8 @@ struct Smem {
   static constexpr int kOffML = kOffQScale + 2 * kBM * 4;
   static constexpr int kOffMerge = kOffML + 2 * kBM * 8;
   static constexpr int kOffBar = kOffMerge + 2 * 96 * kMergePad * 4;
-  // q_full[2], k_full[2], v_full[2], s_full[2], p_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
-  static constexpr int kNumBars = 15 + 2 * kBatches;
+  // q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
+  static constexpr int kNumBars = 13 + 2 * kBatches;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
   static constexpr int kOffMisc = kOffItem + 2 * 32;
   static constexpr int kBytes = kOffMisc + 64;
@@ -387,6 +387,41 @@ struct Lookup {
   int codec, slot, row, n_rows, h, first;   // first: this chunk counts a page that cannot be read
 };
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t x;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+  return x;
+}
+// Shared-memory operands of 128-byte swizzled tiles: the descriptor's high word
+// is the same for all (stride 1024 bytes between 8-row groups, layout, version; tc::sdesc).
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t saddr, uint32_t lbo) { return (uint32_t)tc::sdesc(saddr, lbo, 1024); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ void mma_ss_lead(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(lead), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lead(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(acc), "r"(lead), "n"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
+}
+
 // BF: q and out are bf16, else fp16.  W16: the call has a 16-bit pool.  The
 // operands are bf16 only where bf16 pages ask for it: over 8-bit pages alone a bf16
 // query becomes fp16 times a power of two per row (its 8 bits fit, and what is
@@ -406,10 +441,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);   // item k: buffer k & 1
   uint64_t* k_full = q_full + 2;       // block n: buffer n & 1
-  uint64_t* v_full = k_full + 2;
-  uint64_t* s_full = v_full + 2;       // scores complete; the K tile is free
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;       // P.V complete; the V tile is free
+  uint64_t* pv_ready = k_full + 2;     // V tile and P written
+  uint64_t* s_full = pv_ready + 2;     // scores complete; the K tile is free
+  uint64_t* o_done = s_full + 2;       // P.V complete; the V tile is free
   uint64_t* o_free = o_done + 2;       // item k: its epilogue is done with O and with its Q buffer
   uint64_t* drain = o_free + 2;
   uint64_t* looked = drain + 1;        // a batch of blocks is looked up
@@ -441,9 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&q_full[b], kQWarps);
       mbar_init(&k_full[b], kLoadWarps / 2);
-      mbar_init(&v_full[b], kLoadWarps / 2);
+      mbar_init(&pv_ready[b], kLoadWarps / 2 + kSoftmaxWarps);
       mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], kSoftmaxWarps);
       mbar_init(&o_done[b], 1);
       mbar_init(&o_free[b], kSoftmaxWarps);
     }
@@ -473,61 +506,64 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     // nothing in this CTA's range
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer
-    // within an item: S0, S1, then per block i: P.V of i, S of i + 2
-    if (lane == 0) {
-      constexpr uint32_t idQK = idesc_f16kind(BFM, false, kBN);
-      constexpr uint32_t idPV = idesc_f16kind(BFM, true, D);
-      Cursor c;
-      c.start(p, misc[2], misc64[2], n_blocks);
-      int n0 = 0;                      // blocks before this item's
-      bool ok = true;
-      auto issue_s = [&](int n, uint32_t q_s) {
-        const int b = n & 1;
-        if (!wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
-        tc_fence_after();
-        const uint32_t k_s = smem_u32(smem + SM::kOffK + b * kTile);
+    // within an item: S0, S1, then per block i: P.V of i, S of i + 2.  The whole
+    // warp runs this, one elected lane issues: descriptors and loop counters
+    // stay warp-uniform, where the MMA instruction wants them.
+    constexpr uint32_t idQK = idesc_f16kind(BFM, false, kBN);
+    constexpr uint32_t idPV = idesc_f16kind(BFM, true, D);
+    const uint32_t lead = elect_one();
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    // low words of the operand descriptors: address and leading offset in 16-byte units
+    const uint32_t q_lo = sdesc_lo(smem_u32(smem + SM::kOffQ), kHalf), k_lo = sdesc_lo(smem_u32(smem + SM::kOffK), kHalf);
+    const uint32_t v_lo = sdesc_lo(smem_u32(smem + SM::kOffV), kHalf);
+    Cursor c;
+    c.start(p, misc[2], misc64[2], n_blocks);
+    int n0 = 0;                        // blocks before this item's
+    bool ok = true;
+    auto issue_s = [&](int n, int k) {
+      const int b = n & 1;
+      if (!__all_sync(0xffffffffu, wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1]))) return false;
+      tc_fence_after();
+      const uint32_t ql = q_lo + (uint32_t)(k & 1) * (kTile / 16), kl = k_lo + (uint32_t)b * (kTile / 16);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-          mma_ss(tS(b), sdesc(q_s + off, kHalf, 1024), sdesc(k_s + off, kHalf, 1024), idQK, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&s_full[b]);
-        return true;
-      };
-      auto issue_pv = [&](int n, bool first) {
-        const int b = n & 1;
-        if (!wait(&v_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
-        if (!wait(&p_full[b], (uint32_t)(n >> 1) & 1, &misc[1])) return false;
-        tc_fence_after();
-        const uint32_t v_s = smem_u32(smem + SM::kOffV + b * kTile);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
+        mma_ss_lead(tm + 128u * b, ql + off, kl + off, idQK, kk > 0, lead);
+      }
+      commit_lead(&s_full[b], lead);
+      return true;
+    };
+    auto issue_pv = [&](int n, bool first) {
+      const int b = n & 1;
+      if (!__all_sync(0xffffffffu, wait(&pv_ready[b], (uint32_t)(n >> 1) & 1, &misc[1]))) return false;
+      tc_fence_after();
+      const uint32_t vl = v_lo + (uint32_t)b * (kTile / 16);
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)            // group g: keys 64 g ..., its P and its O
-          mma_ts(tO(kk >> 2), tS(b) + (kk >> 2) * 64 + (kk & 3) * 8, sdesc(v_s + kk * 2048, kHalf, 1024), idPV,
-                 (!first || (kk & 3) > 0) ? 1u : 0u);
-        mma_commit(&o_done[b]);
-        return true;
-      };
-      for (int k = 0; ok && c.left > 0; ++k) {
-        const int nb = min(c.nb - c.blk, c.left);
-        const uint32_t q_s = smem_u32(smem + SM::kOffQ + (k & 1) * kTile);
-        ok = wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]);
-        if (ok) ok = issue_s(n0, q_s);
-        if (ok && nb > 1) ok = issue_s(n0 + 1, q_s);
-        // the scores of this item may overtake the epilogue of the one before; its P.V may not
-        if (ok && k > 0) ok = wait(&o_free[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1, &misc[1]);
-        for (int i = 0; i < nb && ok; ++i) {
-          ok = issue_pv(n0 + i, i == 0);
-          if (ok && i + 2 < nb) ok = issue_s(n0 + i + 2, q_s);
-        }
-        n0 += nb;
-        c.advance(p, nb);
+      for (int kk = 0; kk < kBN / 16; ++kk)              // group g: keys 64 g ..., its P and its O
+        mma_ts_lead(tm + 256u + 128u * (kk >> 2), tm + 128u * b + (kk >> 2) * 64 + (kk & 3) * 8, vl + kk * 128, idPV,
+                    !first || (kk & 3) > 0, lead);
+      commit_lead(&o_done[b], lead);
+      return true;
+    };
+    for (int k = 0; ok && n0 < n_blocks; ++k) {
+      const int nb = __shfl_sync(0xffffffffu, min(c.nb - c.blk, c.left), 0);
+      ok = __all_sync(0xffffffffu, wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]));
+      if (ok) ok = issue_s(n0, k);
+      if (ok && nb > 1) ok = issue_s(n0 + 1, k);
+      // the scores of this item may overtake the epilogue of the one before; its P.V may not
+      if (ok && k > 0) ok = __all_sync(0xffffffffu, wait(&o_free[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1, &misc[1]));
+      for (int i = 0; i < nb && ok; ++i) {
+        ok = issue_pv(n0 + i, i == 0);
+        if (ok && i + 2 < nb) ok = issue_s(n0 + i + 2, k);
       }
-      if (!ok) {
-        misc[1] = 1;
-        const volatile uint32_t never = 0;
-        mma_commit(drain);             // TMEM is freed after the MMAs in flight
-        wait(drain, 0, &never);
-      }
+      n0 += nb;
+      c.advance(p, nb);
+    }
+    if (!ok) {
+      const volatile uint32_t never = 0;
+      misc[1] = 1;
+      commit_lead(drain, lead);        // TMEM is freed after the MMAs in flight
+      wait(drain, 0, &never);
     }
   } else if (warp >= kQWarp0) {
     // ---------------------------------------------------------- Q tiles
@@ -665,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const int lw = warp - kSoftmaxWarps, ch = lw & 7;
     const bool is_v = lw >= kLoadWarps / 2;
     const uint32_t tiles = smem_u32(smem + (is_v ? SM::kOffV : SM::kOffK)) + ch * 2048;
-    uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* full = is_v ? pv_ready : k_full;
     uint64_t* empty = is_v ? o_done : s_full;
     const long long v_off = is_v ? (long long)p.Hkv * p.P * D : 0;   // V behind K in an 8-bit page
     bool ok = true;
@@ -863,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         if (!alive) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[n & 1]);
+        if (lane == 0) mbar_arrive(&pv_ready[n & 1]);
       }
       if (alive) alive = __all_sync(0xffffffffu, wait(&o_done[(n0 + nb - 1) & 1], (uint32_t)((n0 + nb - 1) >> 1) & 1, &misc[1]));
       if (!alive) misc[1] = 1;
