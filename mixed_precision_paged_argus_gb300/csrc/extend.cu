@@ -32,7 +32,7 @@ struct EParams {
   float scale_log2;
   int n_ctas;
   int last_query[8];                 // (128 (r + 1) - 1) / G: the query of tile r's last row
-  float* ws;                         // pieces: o [2 n_ctas][128][D], then lse2 [2 n_ctas][128]
+  float* ws;                         // pieces: o [2 n_ctas][128][D], then lse2 [2 n_ctas][128]; cuts [n_ctas]
 };
 
 constexpr int kBM = 128;             // query rows per tile (TMEM lanes)
@@ -136,37 +136,52 @@ __device__ __forceinline__ long long seq_blocks(const EParams& p, int b) {
   return s.n == 0 ? 0 : p.Hkv * blocks_before(p, s, n_tiles(p, s));
 }
 
-// by a whole warp: blocks of all sequences
-__device__ __forceinline__ long long total_blocks(const EParams& p) {
+__device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
   const int lane = threadIdx.x & 31;
-  long long x = 0;
-  for (int b = lane; b < p.B; b += 32) x += seq_blocks(p, b);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
   return x;
 }
 
-// by a whole warp: the sequence that block w (< total) belongs to; w becomes its
-// number within the sequence
-__device__ __forceinline__ int find_seq(const EParams& p, long long& w) {
+__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return total * cta / n_ctas; }
+
+// A CTA's range: its number of blocks, and the sequence and the number within it
+// of the first one.  Only the first min(total, CTAs) CTAs have blocks.  By a
+// whole warp.
+struct Range {
+  long long total, w0, w1;           // blocks of the call; the range
+  int n, b;                          // CTAs with blocks; first sequence
+  long long rest;                    // first block's number within it
+};
+__device__ __forceinline__ Range find_range(const EParams& p, int cta) {
   const int lane = threadIdx.x & 31;
+  Range r;
+  long long mine = lane < p.B ? seq_blocks(p, lane) : 0, sum = mine;
+  for (int b = lane + 32; b < p.B; b += 32) sum += seq_blocks(p, b);
+  r.total = __shfl_sync(0xffffffffu, warp_scan(sum), 31);
+  r.n = (int)min((long long)p.n_ctas, r.total);
+  r.w0 = r.w1 = r.rest = 0;
+  r.b = 0;
+  if (cta >= r.n) return r;
+  r.w0 = range_start(r.total, cta, r.n);
+  r.w1 = range_start(r.total, cta + 1, r.n);
+  r.rest = r.w0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const long long mine = b0 + lane < p.B ? seq_blocks(p, b0 + lane) : 0;
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > w);
+    if (b0 > 0) mine = b0 + lane < p.B ? seq_blocks(p, b0 + lane) : 0;
+    const long long incl = warp_scan(mine);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > r.rest);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      w -= __shfl_sync(0xffffffffu, incl - mine, src);
-      return b0 + src;
+      r.rest -= __shfl_sync(0xffffffffu, incl - mine, src);
+      r.b = b0 + src;
+      break;
     }
-    w -= __shfl_sync(0xffffffffu, incl, 31);
+    r.rest -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  return p.B - 1;
+  return r;
 }
 
 struct Cursor {
@@ -216,14 +231,20 @@ struct Cursor {
   }
 };
 
-__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return total * cta / n_ctas; }
-
-// the pieces of the range [w0, w1): the one that does not begin its item (the
+// The pieces of the range [w0, w1): the one that does not begin its item (the
 // first piece of a range at most) and the one that does not end it (the last)
-// lie in the workspace at 2 cta and 2 cta + 1
+// lie in the workspace at 2 cta and 2 cta + 1.  The CTA behind the first cut of an item
+// describes it for the second kernel.
+struct Cut {
+  int rows, last;                    // rows of the tile (0: nothing to join); last CTA of the item
+  int q0, row0, head0, pad[3];       // first query token of the sequence; first row of the tile; first head
+};
 __device__ __forceinline__ float* piece_o(const EParams& p, int D, int piece) { return p.ws + (size_t)piece * kBM * D; }
 __device__ __forceinline__ float* piece_lse(const EParams& p, int D, int piece) {
   return p.ws + (size_t)2 * p.n_ctas * kBM * D + (size_t)piece * kBM;
+}
+__device__ __forceinline__ Cut* cuts(const EParams& p, int D) {
+  return reinterpret_cast<Cut*>(p.ws + (size_t)2 * p.n_ctas * kBM * (D + 1));
 }
 
 // copies of a tile's rows over the 128 TMEM lanes (see the head of the file)
@@ -436,7 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   constexpr float kPBias = BFM ? 0.f : 7.f;  // fp16 P is stored as P * 2^7 (at most 2^15)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {         // the swizzled tiles need it
-    if (threadIdx.x == 0 && p.status) atomicOr(p.status, kStatusTimeoutBit);
+    if (threadIdx.x == 0) {
+      cuts(p, D)[blockIdx.x] = Cut{};
+      if (p.status) atomicOr(p.status, kStatusTimeoutBit);
+    }
     return;
   }
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);   // item k: buffer k & 1
@@ -460,16 +484,31 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   float4* scales = reinterpret_cast<float4*>(smem + SM::kOffScale);     // [slot][chunk]: ks (< 0: not to be read), log2 vs, 1 / vs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // the second kernel may be put in place; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
-    const long long total = total_blocks(p);
-    const long long w0 = range_start(total, blockIdx.x, p.n_ctas), w1 = range_start(total, blockIdx.x + 1, p.n_ctas);
-    long long w = w0;
-    const int b = w1 > w0 ? find_seq(p, w) : 0;
+    const Range r = find_range(p, blockIdx.x);
     if (lane == 0) {
-      misc[2] = b;
-      misc64[2] = w;
-      misc[3] = (uint32_t)(w1 - w0);   // fewer than 2^31 (checked on the host)
+      misc[2] = r.b;
+      misc64[2] = r.rest;
+      misc[3] = (uint32_t)(r.w1 - r.w0);   // fewer than 2^31 (checked on the host)
     }
+    Cut cut = {};
+    if (r.w1 > r.w0) {
+      Cursor c;
+      c.start(p, r.b, r.rest, 1);
+      const long long begin = r.w0 - c.blk, end = begin + c.nb;
+      // this range begins inside an item, and is the first to
+      if (c.blk > 0 && range_start(r.total, blockIdx.x - 1, r.n) <= begin) {
+        cut.rows = min(kBM, c.s.n * p.G - c.t * kBM);
+        cut.last = blockIdx.x;
+        while (cut.last + 1 < r.n && range_start(r.total, cut.last + 1, r.n) < end) ++cut.last;
+        cut.q0 = c.s.q0;
+        cut.row0 = c.t * kBM;
+        cut.head0 = c.h * p.G;
+      }
+    }
+    if (lane == 0) cuts(p, D)[blockIdx.x] = cut;
   }
   if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
@@ -1009,72 +1048,68 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   }
 }
 
-// Joins the pieces of items that the ranges cut: block x looks at the boundary
-// before CTA x + 1 and joins the item that it is the first to cut; a warp per row.
-constexpr int kJoinWarps = 8;
+// Joins the pieces of the items that the ranges cut: block x the item that
+// range x + 1 is the first to cut, a warp per row, lanes over the pieces for their
+// weights and over the dims for the sum.
+constexpr int kJoinWarps = 8, kJoinBlocks = 4;
 template <int D, bool BF>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const EParams p) {
-  __shared__ long long s_w[2];
-  __shared__ int s_b;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cta = blockIdx.x + 1;
-  if (warp == 0) {
-    const long long total = total_blocks(p);
-    const long long at = range_start(total, cta, p.n_ctas);
-    long long w = at;
-    const int b = at < total ? find_seq(p, w) : 0;
-    if (lane == 0) {
-      s_w[0] = total;
-      s_w[1] = w;
-      s_b = b;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, cta = blockIdx.x + 1;
+  const Cut cut = cuts(p, D)[cta];
+  constexpr int L = D / 4, PER = 32 / L;                 // lanes of a row; pieces of a step
+  const int part = lane / L, col = (lane % L) * 4;
+  const int n = cut.last - cta + 2;                      // pieces: 2 (cta - 1) + 1, 2 cta, 2 (cta + 1), ...
+  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < cut.rows; row += kJoinWarps * kJoinBlocks) {
+    float M = -INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = 0; x0 < n; x0 += 32) {
+      const int x = x0 + lane, piece = x == 0 ? 2 * (cta - 1) + 1 : 2 * (cta - 1 + x);
+      const float lse = x < n ? piece_lse(p, D, piece)[row] : -INFINITY;
+      float top = lse;
+#pragma unroll
+      for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+      top = fmaxf(top, M);
+      if (top == -INFINITY) continue;                    // nothing visible so far
+      const float r = fast_exp2(M - top), w = fast_exp2(lse - top);   // 2^-inf = 0
+      M = top;
+      sum = sum * r + w;                                 // this lane's pieces
+      o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
+      const int m = min(32, n - x0);
+#pragma unroll 4
+      for (int y = 0; y < m; y += PER) {
+        const int at = y + part;                         // below 32: PER divides 32
+        const float wy = __shfl_sync(0xffffffffu, w, at);
+        const int pc = x0 + at == 0 ? 2 * (cta - 1) + 1 : 2 * (cta - 1 + x0 + at);
+        if (at < m && wy > 0.f) {
+          const float4 v = *reinterpret_cast<const float4*>(piece_o(p, D, pc) + (size_t)row * D + col);
+          o.x = fmaf(wy, v.x, o.x);
+          o.y = fmaf(wy, v.y, o.y);
+          o.z = fmaf(wy, v.z, o.z);
+          o.w = fmaf(wy, v.w, o.w);
+        }
+      }
     }
+#pragma unroll
+    for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+#pragma unroll
+    for (int y = L; y < 32; y <<= 1) {
+      o.x += __shfl_xor_sync(0xffffffffu, o.x, y);
+      o.y += __shfl_xor_sync(0xffffffffu, o.y, y);
+      o.z += __shfl_xor_sync(0xffffffffu, o.z, y);
+      o.w += __shfl_xor_sync(0xffffffffu, o.w, y);
+    }
+    const int lin = cut.row0 + row, tok = lin / p.G;
+    const size_t orow = (size_t)(cut.q0 + tok) * p.Hq + cut.head0 + (lin - tok * p.G);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (part == 0) {
+      uint2 u;
+      u.x = BF ? pack_bf16x2(o.x * inv, o.y * inv) : pack_f16x2(o.x * inv, o.y * inv);
+      u.y = BF ? pack_bf16x2(o.z * inv, o.w * inv) : pack_f16x2(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(p.out + orow * D + col) = u;
+    }
+    if (lane == 0 && p.lse2) p.lse2[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
   }
-  __syncthreads();
-  const long long total = s_w[0], at = range_start(total, cta, p.n_ctas);
-  if (at >= total) return;
-  Cursor c;
-  c.start(p, s_b, s_w[1], 1);
-  const long long begin = at - c.blk, end = begin + c.nb;
-  const long long prev = range_start(total, cta - 1, p.n_ctas);
-  if (c.blk == 0 || prev > begin || prev == at) return;   // not cut here, cut before, or an empty range
-  const long long lin0 = (long long)c.t * kBM;
-  const int rows = (int)min((long long)kBM, (long long)c.s.n * p.G - lin0);
-  const int row = blockIdx.y * kJoinWarps + warp;
-  if (row >= rows) return;
-  const long long lin = lin0 + row;
-  const int tok = (int)(lin / p.G);
-  const size_t orow = (size_t)(c.s.q0 + tok) * p.Hq + c.h * p.G + (int)(lin - (long long)tok * p.G);
-  auto each = [&](auto&& f) {
-    f(2 * (cta - 1) + 1);
-    for (int x = cta; x < p.n_ctas && range_start(total, x, p.n_ctas) < end; ++x)
-      if (range_start(total, x + 1, p.n_ctas) > range_start(total, x, p.n_ctas)) f(2 * x);
-  };
-  float M = -INFINITY;
-  each([&](int piece) { M = fmaxf(M, piece_lse(p, D, piece)[row]); });
-  float sum = 0.f;
-  float o[D / 32];
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-  if (M != -INFINITY) {
-    each([&](int piece) {
-      const float l = piece_lse(p, D, piece)[row];
-      if (l == -INFINITY) return;
-      const float w = fast_exp2(l - M);
-      sum += w;
-      const float* src = piece_o(p, D, piece) + (size_t)row * D + lane * (D / 32);
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) o[e] = fmaf(w, src[e], o[e]);
-    });
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  uint32_t u[D / 64];
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e)
-    u[e] = BF ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : pack_f16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  uint32_t* d = reinterpret_cast<uint32_t*>(p.out + orow * D) + lane * (D / 64);
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) d[e] = u[e];
-  if (lane == 0 && p.lse2) p.lse2[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
 }
 
 static argus_status check(const argus_extend_args* a) {
@@ -1129,7 +1164,8 @@ static long long max_blocks(const argus_extend_args* a) {
 static int grid_size(const argus_extend_args* a) { return (int)std::min<long long>(device_sm_count(), std::max(1ll, max_blocks(a))); }
 
 static size_t workspace(const argus_extend_args* a) {
-  return (size_t)2 * std::max(1, grid_size(a)) * kBM * (a->g.head_dim + 1) * sizeof(float);
+  const size_t n = (size_t)grid_size(a);
+  return 2 * n * kBM * (a->g.head_dim + 1) * sizeof(float) + n * sizeof(Cut);
 }
 
 template <int D, bool BF, bool W16>
@@ -1142,7 +1178,19 @@ static argus_status launch(const EParams& p, cudaStream_t s) {
   });
   if (st != ARGUS_OK) return st;
   extend_kernel<D, BF, W16><<<p.n_ctas, kThreads, smem, s>>>(p);
-  if (p.n_ctas > 1) join_kernel<D, BF><<<dim3(p.n_ctas - 1, kBM / kJoinWarps), 32 * kJoinWarps, 0, s>>>(p);
+  if (p.n_ctas > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.n_ctas - 1, kJoinBlocks);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D, BF>, p);
+    if (e != cudaSuccess) return fail(ARGUS_E_LAUNCH, "argus_paged_extend_attn: launch failed: %s", cudaGetErrorString(e));
+  }
   return launch_status("argus_paged_extend_attn");
 }
 
