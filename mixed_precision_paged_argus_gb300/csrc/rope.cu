@@ -8,10 +8,12 @@
 // and pos * F in wrapping 64-bit integers IS the angle modulo one turn, exactly
 // up to F's own rounding.  sincospif of twice the signed fraction follows.
 //
-// What bounds it: bytes (q, k, v read, q', k', v written once).  One CTA takes
-// one token: its sines and cosines (rot_dim / 2 of them) are computed once in
-// shared memory and used by all Hq + Hkv heads; every thread moves two 16-byte
-// vectors per step, the two that hold a pair's halves.
+// What bounds it: bytes (q, k, v read, q', k', v written once).  A token is
+// taken by a group of W warps (W = 1 when there are many tokens, up to 8 when there
+// are few), which loop over tokens.  Each warp turns its one or two frequencies
+// per lane into fixed point once, computes a token's sines and cosines into
+// shared memory of its own (no block barrier), and uses them for all Hq + Hkv heads; a lane moves
+// two 16-byte vectors per item, the two that hold a pair's halves, four items in flight.
 #include <algorithm>
 
 #include "common.cuh"
@@ -48,105 +50,151 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return BF ? pack_bf16x2(a, b) : pack_f16x2(a, b);
 }
 
-template <int D, bool BF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p) {
-  __shared__ float s_cos[D / 2], s_sin[D / 2];
-  __shared__ int s_seq, s_bad;
-  const int t = blockIdx.x, tid = threadIdx.x;
-  if (tid == 0) { s_seq = -1; s_bad = 0; }
-  __syncthreads();
-  // the sequence b with q_start[b] <= t < q_start[b + 1]: blocks of `step`
-  // sequences first, then one block
-  const int step = (p.B + kThreads - 1) / kThreads;
-  {
-    const int b = tid * step;
-    if (b < p.B && p.q_start[b] <= t && t < p.q_start[min(b + step, p.B)]) s_seq = b;
+// The last sequence that starts at or before token t, by a whole warp: 32
+// candidates per step.
+__device__ __forceinline__ int seq_of(const RParams& p, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = p.B;               // it is one of lo .. lo + n - 1, if any is
+  while (n > 1) {
+    const int step = (n + 31) / 32, b = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, lane * step < n && p.q_start[b] <= t);
+    const int k = m ? 31 - __clz(m) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  if (tid < p.rot / 2) {
-    const int ax = p.pair_axis ? p.pair_axis[tid] : 0;
-    float c = 1.f, s = 0.f;
-    if (ax < p.n_axes) {
-      const double turns = p.inv_freq[tid] * 0.15915494309189535;   // 1 / (2 pi)
-      const unsigned long long f = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
-      const unsigned long long u = (unsigned long long)(long long)p.pos[(size_t)ax * p.total + t] * f;
-      sincospif((float)(long long)u * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
-    } else {
-      s_bad = 1;
-    }
-    s_cos[tid] = c;
-    s_sin[tid] = s;
-  }
-  __syncthreads();
-  int b = s_seq;
-  if (b < 0) return;                 // a row of no sequence
-  if (step > 1) {
-    const int b0 = b, b1 = min(b + step, p.B);
-    __syncthreads();
-    for (int i = b0 + tid; i < b1; i += kThreads)
-      if (p.q_start[i] <= t && t < p.q_start[i + 1]) s_seq = i;
-    __syncthreads();
-    b = s_seq;
-  }
-  const int start = p.q_start[b], n = p.q_start[b + 1] - start;
-  const long long c = (long long)p.seq_lens[b] - n + (t - start);
-  long long slot = -1;
-  int row = 0;
-  if (c >= 0 && c < (long long)p.max_pages * p.P) {
-    const int page = (int)(c / p.P);
-    row = (int)(c - (long long)page * p.P);
-    const size_t e = (size_t)b * p.max_pages + page;
-    if (p.page_codec[e] == p.codec) slot = p.block_table[e];
-    if (slot >= p.n_slots) slot = -1;
-  }
-  if (tid == 0 && p.status && (slot < 0 || s_bad)) atomicAdd(p.status, (slot < 0) + (s_bad != 0));
+  return lo;
+}
 
-  constexpr int U = D / 16;          // units of 16 elements (two vectors) per head
-  const int n_items = (p.Hq + 2 * p.Hkv) * U;
-  const int ru = p.rot / 16;
-  for (int it = tid; it < n_items; it += kThreads) {
-    const int head = it / U, u = it % U;
-    const bool turn = u < ru && head < p.Hq + p.Hkv;
-    const int e0 = (turn && !p.adjacent) ? 8 * u : 16 * u;
-    const int e1 = (turn && !p.adjacent) ? p.rot / 2 + 8 * u : 16 * u + 8;
-    const uint16_t* src;
-    uint16_t* dst = nullptr;
-    if (head < p.Hq) {
-      src = p.q + t * p.qs + head * D;
-      dst = p.q_out + t * p.qos + head * D;
+template <bool BF>
+__device__ __forceinline__ void turn_pair(uint4& a4, uint4& b4, const float* cs, const float* sn, int u, bool adjacent) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&a4);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&b4);
+  const float4 c0 = *reinterpret_cast<const float4*>(cs + 8 * u), c1 = *reinterpret_cast<const float4*>(cs + 8 * u + 4);
+  const float4 s0 = *reinterpret_cast<const float4*>(sn + 8 * u), s1 = *reinterpret_cast<const float4*>(sn + 8 * u + 4);
+  const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = unpack2<BF>(a[j]), y = unpack2<BF>(b[j]);
+    if (adjacent) {
+      a[j] = pack2<BF>(x.x * c[j] - x.y * s[j], x.y * c[j] + x.x * s[j]);
+      b[j] = pack2<BF>(y.x * c[4 + j] - y.y * s[4 + j], y.y * c[4 + j] + y.x * s[4 + j]);
     } else {
-      const bool is_v = head >= p.Hq + p.Hkv;
-      const int h = head - p.Hq - (is_v ? p.Hkv : 0);
-      src = is_v ? p.v + t * p.vs + h * D : p.k + t * p.ks + h * D;
-      if (slot >= 0) dst = p.codes + (((size_t)slot * 2 + is_v) * p.Hkv + h) * ((size_t)p.P * D) + (size_t)row * D;
+      a[j] = pack2<BF>(x.x * c[2 * j] - y.x * s[2 * j], x.y * c[2 * j + 1] - y.y * s[2 * j + 1]);
+      b[j] = pack2<BF>(y.x * c[2 * j] + x.x * s[2 * j], y.y * c[2 * j + 1] + x.y * s[2 * j + 1]);
     }
-    if (!dst) continue;
-    uint4 a4 = *reinterpret_cast<const uint4*>(src + e0), b4 = *reinterpret_cast<const uint4*>(src + e1);
-    if (turn) {
-      uint32_t* a = reinterpret_cast<uint32_t*>(&a4);
-      uint32_t* bb = reinterpret_cast<uint32_t*>(&b4);
-      if (p.adjacent) {
+  }
+}
+
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) {
+  __shared__ __align__(16) float s_cs[kThreads / 32][2][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* cs = s_cs[warp][0];
+  float* sn = s_cs[warp][1];
+  const int gw = blockIdx.x * (kThreads / 32) + warp, part = gw % W, groups = gridDim.x * (kThreads / 32) / W;
+  // this lane's frequencies, pairs lane and lane + 32, as fractions of a turn
+  constexpr int N = D / 64;
+  unsigned long long freq[N];
+  int axis[N];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = unpack2<BF>(a[j]), y = unpack2<BF>(bb[j]);
-          const float c0 = s_cos[8 * u + j], s0 = s_sin[8 * u + j];
-          const float c1 = s_cos[8 * u + 4 + j], s1 = s_sin[8 * u + 4 + j];
-          a[j] = pack2<BF>(x.x * c0 - x.y * s0, x.y * c0 + x.x * s0);
-          bb[j] = pack2<BF>(y.x * c1 - y.y * s1, y.y * c1 + y.x * s1);
-        }
-      } else {
+  for (int x = 0; x < N; ++x) {
+    const int i = lane + 32 * x;
+    freq[x] = 0;
+    axis[x] = 0;
+    if (i < p.rot / 2) {
+      const double turns = p.inv_freq[i] * 0.15915494309189535;   // 1 / (2 pi)
+      freq[x] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      if (p.pair_axis) axis[x] = p.pair_axis[i];
+    }
+  }
+  bool bad_axis = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = unpack2<BF>(a[j]), y = unpack2<BF>(bb[j]);
-          const float c0 = s_cos[8 * u + 2 * j], s0 = s_sin[8 * u + 2 * j];
-          const float c1 = s_cos[8 * u + 2 * j + 1], s1 = s_sin[8 * u + 2 * j + 1];
-          a[j] = pack2<BF>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
-          bb[j] = pack2<BF>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
-        }
+  for (int x = 0; x < N; ++x) bad_axis |= axis[x] >= p.n_axes;
+  bad_axis = __any_sync(0xffffffffu, bad_axis);
+  constexpr int U = D / 16;          // items of 16 elements (two vectors) per head
+  const int n_items = (p.Hq + 2 * p.Hkv) * U, ru = p.rot / 16;
+
+  for (int t = gw / W; t < p.total; t += groups) {
+    int pos[N];
+#pragma unroll
+    for (int x = 0; x < N; ++x) pos[x] = axis[x] < p.n_axes ? p.pos[(size_t)axis[x] * p.total + t] : 0;
+    const int b = seq_of(p, t), start = p.q_start[b], end = p.q_start[b + 1];
+    if (t < start || t >= end) continue;                 // a row of no sequence
+    const long long c = (long long)p.seq_lens[b] - (end - start) + (t - start);
+    long long slot = -1;
+    int row = 0;
+    if (c >= 0 && c < (long long)p.max_pages * p.P) {
+      const int page = (int)((unsigned long long)c / (unsigned)p.P);
+      row = (int)(c - (long long)page * p.P);
+      const size_t e = (size_t)b * p.max_pages + page;
+      if (p.page_codec[e] == p.codec) slot = p.block_table[e];
+      if (slot >= p.n_slots) slot = -1;
+    }
+    if (part == 0 && lane == 0 && p.status && (slot < 0 || bad_axis)) atomicAdd(p.status, (slot < 0) + bad_axis);
+    __syncwarp();                                        // the token before has been read
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      const int i = lane + 32 * x;
+      if (i < p.rot / 2) {
+        const unsigned long long turn = (unsigned long long)(long long)pos[x] * freq[x];
+        float s, co;
+        sincospif((float)(long long)turn * 1.0842021724855044e-19f, &s, &co);   // 2^-63: half turns
+        cs[i] = co;
+        sn[i] = s;
       }
     }
-    *reinterpret_cast<uint4*>(dst + e0) = a4;
-    *reinterpret_cast<uint4*>(dst + e1) = b4;
+    __syncwarp();
+    uint16_t* page = p.codes + (size_t)(slot < 0 ? 0 : slot) * 2 * p.Hkv * p.P * D + (size_t)row * D;
+    constexpr int M = 4;                                 // items in flight
+    for (int it0 = part * 32 + lane; it0 < n_items; it0 += 32 * W * M) {
+      uint4 a[M], bb[M];
+      uint16_t* dst[M];
+      int un[M];                                         // >= 0: turned, with these pairs
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        const int it = it0 + m * 32 * W;
+        dst[m] = nullptr;
+        if (it >= n_items) continue;
+        const int head = it / U, u = it % U;
+        const bool turned = u < ru && head < p.Hq + p.Hkv, halves = turned && !p.adjacent;
+        un[m] = turned ? u : -1;
+        const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? p.rot / 2 + 8 * u : 16 * u + 8;
+        const uint16_t* src;
+        if (head < p.Hq) {
+          src = p.q + t * p.qs + head * D;
+          dst[m] = p.q_out + t * p.qos + head * D + e0;
+        } else {
+          const bool is_v = head >= p.Hq + p.Hkv;
+          const int h = head - p.Hq - (is_v ? p.Hkv : 0);
+          src = is_v ? p.v + t * p.vs + h * D : p.k + t * p.ks + h * D;
+          if (slot >= 0) dst[m] = page + (size_t)(head - p.Hq) * p.P * D + e0;   // K heads, then V heads
+        }
+        a[m] = *reinterpret_cast<const uint4*>(src + e0);
+        bb[m] = *reinterpret_cast<const uint4*>(src + e1);
+      }
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        if (!dst[m]) continue;
+        if (un[m] >= 0) turn_pair<BF>(a[m], bb[m], cs, sn, un[m], p.adjacent);
+        *reinterpret_cast<uint4*>(dst[m]) = a[m];
+        *reinterpret_cast<uint4*>(dst[m] + ((un[m] >= 0 && !p.adjacent) ? p.rot / 2 : 8)) = bb[m];
+      }
+    }
   }
+}
+
+template <int D, bool BF>
+static void launch(const RParams& p, cudaStream_t s) {
+  constexpr int kWarps = kThreads / 32;
+  const long long sms = device_sm_count();
+  // warps per token: enough of them for every SM to hold some, no more than have an item each
+  const int items = (p.Hq + 2 * p.Hkv) * (D / 16);
+  int W = 1;
+  while (W < kWarps && (long long)p.total * W < sms * 16 && 32 * W < items) W *= 2;
+  const long long blocks = ((long long)p.total * W + kWarps - 1) / kWarps;
+  // three blocks are resident per SM at this register count
+  rope_kernel<D, BF><<<(int)std::min(blocks, sms * 3), kThreads, 0, s>>>(p, W);
 }
 
 }  // namespace rope
@@ -214,12 +262,7 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   p.status = a->status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = a->dtype == ARGUS_BF16;
-  if (D == 64) {
-    if (bf) rope::rope_kernel<64, true><<<p.total, rope::kThreads, 0, s>>>(p);
-    else rope::rope_kernel<64, false><<<p.total, rope::kThreads, 0, s>>>(p);
-  } else {
-    if (bf) rope::rope_kernel<128, true><<<p.total, rope::kThreads, 0, s>>>(p);
-    else rope::rope_kernel<128, false><<<p.total, rope::kThreads, 0, s>>>(p);
-  }
+  if (D == 64) bf ? rope::launch<64, true>(p, s) : rope::launch<64, false>(p, s);
+  else bf ? rope::launch<128, true>(p, s) : rope::launch<128, false>(p, s);
   return launch_status("argus_rope_append");
 }
