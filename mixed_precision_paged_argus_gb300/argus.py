@@ -385,41 +385,59 @@ def paged_window_prefill_attn(g, n_q, q, pools, page_codec, block_table, max_pag
 def _token_stride(name, t, heads, head_dim):
     """Elements between the tokens of t [tokens][heads][head_dim], whose tokens
     are dense and may lie apart (a slice of a fused projection's rows)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim:
-        raise ValueError("%s must be [tokens][%d][%d], not %s" % (name, heads, head_dim, list(t.shape)))
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+        raise ValueError("%s must be [tokens][%d][%d], not %s" % (name, heads, head_dim, list(shape)))
+    if (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)) and t.numel():
         raise ValueError("%s: the heads of a token must be dense" % name)
-    return t.stride(0) if t.shape[0] > 1 else heads * head_dim
+    return stride[0] if shape[0] > 1 else heads * head_dim
 
 
-def _dense(**tensors):
-    for name, (t, dtype, numel) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype not in dtype or not t.is_contiguous() or t.numel() < numel:
-            raise ValueError("%s must be a dense %s tensor of %d elements or more" % (name, dtype[0], numel))
+def _at(name, t, dtype, numel):
+    """Address of a dense tensor of at least numel elements (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError("%s must be a dense %s tensor of %d elements or more" % (name, dtype, numel))
+    return t.data_ptr()
 
 
-_I32 = (torch.int32,)
-_U8 = (torch.uint8,)
-_STATUS = (torch.int32, torch.uint32)
+def _status_at(t):
+    if t is None:
+        return None
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() < 1:
+        raise ValueError("status must be a 32-bit integer tensor")
+    return t.data_ptr()
+
+
+def _stream_of(t, stream):
+    """The stream to launch on: the given one, or t's device's current one.  The
+    library launches on the current device, so t has to lie there."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors lie on cuda:%d, the current device is cuda:%d" % (t.device.index, torch.cuda.current_device()))
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream if t.is_cuda else None
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 
 
 def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pages, softmax_scale, out,
                 causal=True, lse2_out=None, status=None):
     """Build an argus_extend_args struct: q [total_q][Hq][D] (its tokens may lie
     apart), q_start [B + 1], seq_lens [B], out like q and dense."""
-    batch, total = q_start.numel() - 1, q.shape[0]
-    qs = _token_stride("q", q, g.n_q_heads, g.head_dim)
-    _dense(q_start=(q_start, _I32, 1), seq_lens=(seq_lens, _I32, batch), page_codec=(page_codec, _U8, batch * max_pages),
-           block_table=(block_table, _I32, batch * max_pages), out=(out, (q.dtype,), q.numel()),
-           lse2_out=(lse2_out, (torch.float32,), total * g.n_q_heads), status=(status, _STATUS, 1))
-    arr = (PoolDesc * max(1, len(pools)))(*[p.desc() for p in pools])
-    a = ExtendArgs(g, batch, total, DTYPE_CODEC[q.dtype], int(causal), q.data_ptr(), qs, q_start.data_ptr(),
-                   arr, len(pools), int(max_pages), _ptr(page_codec), _ptr(block_table),
-                   _ptr(seq_lens), _ptr(out), _ptr(lse2_out), _ptr(status), float(softmax_scale))
+    batch, total, hq = q_start.numel() - 1, q.shape[0], g.n_q_heads
+    n = len(pools)
+    arr = (PoolDesc * (n or 1))(*[p.desc() for p in pools])
+    a = ExtendArgs(g, batch, total, DTYPE_CODEC[q.dtype], 1 if causal else 0, q.data_ptr(),
+                   _token_stride("q", q, hq, g.head_dim), _at("q_start", q_start, _I32, 1), arr, n, max_pages,
+                   _at("page_codec", page_codec, _U8, batch * max_pages),
+                   _at("block_table", block_table, _I32, batch * max_pages), _at("seq_lens", seq_lens, _I32, batch),
+                   _at("out", out, q.dtype, q.numel()), _at("lse2_out", lse2_out, _F32, total * hq), _status_at(status),
+                   softmax_scale)
     # the struct holds raw pointers: keep every tensor it points to alive with it
-    a._keep = (arr, list(pools), q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
+    a._keep = (arr, pools, q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
     return a
 
 
@@ -432,8 +450,7 @@ def extend_workspace_bytes(args):
 def paged_extend_attn(args, ws, stream=None):
     """Attention of several query tokens per sequence over the paged cache;
     ws of extend_workspace_bytes bytes."""
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().argus_paged_extend_attn(ctypes.byref(args), _ptr(ws), nbytes, _stream(stream)))
+    _check(lib().argus_paged_extend_attn(ctypes.byref(args), ws.data_ptr(), ws.nbytes, _stream_of(args._keep[2], stream)))
 
 
 def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages,
@@ -442,32 +459,26 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
     inv_freq [rot_dim / 2] in float64, radians per position) into q_out and the
     cache, and store v: the tokens of sequence b become the last ones of its
     seq_lens[b] cached positions."""
-    total, batch = q.shape[0], q_start.numel() - 1
+    total, batch, dtype = q.shape[0], q_start.numel() - 1, q.dtype
     hq, hkv, d = g.n_q_heads, g.n_kv_heads, g.head_dim
-    if k.shape[0] != total or v.shape[0] != total or q_out.shape[0] != total or positions.numel() % max(1, total):
+    if k.shape[0] != total or v.shape[0] != total or q_out.shape[0] != total or positions.numel() % (total or 1):
         raise ValueError("rope_append: q, k, v, q_out and positions must have the same tokens")
-    if not (q.dtype == k.dtype == v.dtype == q_out.dtype):
+    if k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype:
         raise ValueError("rope_append: q, k, v and q_out must have the same type")
-    n_axes = positions.numel() // total if total else 1
-    _dense(q_start=(q_start, _I32, 1), seq_lens=(seq_lens, _I32, batch), positions=(positions, _I32, 0),
-           inv_freq=(inv_freq, (torch.float64,), 0), pair_axis=(pair_axis, _U8, inv_freq.numel()),
-           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
-           status=(status, _STATUS, 1))
-    d_pool = pool.desc()
-    a = RopeArgs(g, batch, total, DTYPE_CODEC[q.dtype], 2 * inv_freq.numel(), int(adjacent), n_axes,
-                 _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _token_stride("q", q, hq, d), _token_stride("k", k, hkv, d),
-                 _token_stride("v", v, hkv, d), _token_stride("q_out", q_out, hq, d), _ptr(positions), _ptr(inv_freq),
-                 _ptr(pair_axis), _ptr(q_start), _ptr(seq_lens), ctypes.pointer(d_pool), _ptr(page_codec),
-                 _ptr(block_table), int(max_pages), _ptr(status))
-    _check(lib().argus_rope_append(ctypes.byref(a), _stream(stream)))
+    half = inv_freq.numel()
+    a = RopeArgs(g, batch, total, DTYPE_CODEC[dtype], 2 * half, 1 if adjacent else 0, positions.numel() // total if total else 1,
+                 q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _token_stride("q", q, hq, d),
+                 _token_stride("k", k, hkv, d), _token_stride("v", v, hkv, d), _token_stride("q_out", q_out, hq, d),
+                 _at("positions", positions, _I32, 0), _at("inv_freq", inv_freq, torch.float64, 0),
+                 _at("pair_axis", pair_axis, _U8, half), _at("q_start", q_start, _I32, 1),
+                 _at("seq_lens", seq_lens, _I32, batch), ctypes.pointer(pool.desc()),
+                 _at("page_codec", page_codec, _U8, batch * max_pages),
+                 _at("block_table", block_table, _I32, batch * max_pages), max_pages, _status_at(status))
+    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(q, stream)))
 
 
 def _pool_array(pools):
-    return (PoolDesc * max(1, len(pools)))(*[p.desc() for p in pools])
-
-
-def _pointers(tensors):
-    return (ctypes.c_void_p * max(1, len(tensors)))(*[_ptr(t) for t in tensors])
+    return (PoolDesc * (len(pools) or 1))(*[p.desc() for p in pools])
 
 
 def fork_workspace_bytes(batch, pools):
@@ -482,26 +493,24 @@ def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec,
     partial pages about to be written are copied where others hold them too, and
     pages of new_codec are added for n_new[b] tokens.  ref_in / ref_out: one
     int32 count per slot for each pool.  ws of fork_workspace_bytes bytes."""
-    batch = parents.numel()
-    if len(ref_in) != len(pools) or len(ref_out) != len(pools):
+    batch, n = parents.numel(), len(pools)
+    if len(ref_in) != n or len(ref_out) != n:
         raise ValueError("fork_pages: one count tensor per pool")
-    _dense(parents=(parents, _I32, 0), n_new=(n_new, _I32, batch), status=(status, _STATUS, 1),
-           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
-           seq_lens=(seq_lens, _I32, batch), page_codec_out=(page_codec_out, _U8, batch * max_pages),
-           block_table_out=(block_table_out, _I32, batch * max_pages), seq_lens_out=(seq_lens_out, _I32, batch))
-    for p, r, s in zip(pools, ref_in, ref_out):
-        _dense(ref_in=(r, _I32, p.n_slots), ref_out=(s, _I32, p.n_slots))
-    _check(lib().argus_fork_pages(ctypes.byref(g), batch, _ptr(parents), _ptr(n_new), int(new_codec), _pool_array(pools),
-                                  len(pools), _pointers(ref_in), _pointers(ref_out), _ptr(page_codec), _ptr(block_table),
-                                  _ptr(seq_lens), _ptr(page_codec_out), _ptr(block_table_out), _ptr(seq_lens_out),
-                                  int(max_pages), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-                                  _stream(stream)))
+    pointers = ctypes.c_void_p * (n or 1)
+    rin = pointers(*[_at("ref_in", r, _I32, p.n_slots) for p, r in zip(pools, ref_in)])
+    rout = pointers(*[_at("ref_out", r, _I32, p.n_slots) for p, r in zip(pools, ref_out)])
+    entries = batch * max_pages
+    _check(lib().argus_fork_pages(
+        ctypes.byref(g), batch, _at("parents", parents, _I32, 0), _at("n_new", n_new, _I32, batch), new_codec, _pool_array(pools),
+        n, rin, rout, _at("page_codec", page_codec, _U8, entries), _at("block_table", block_table, _I32, entries),
+        _at("seq_lens", seq_lens, _I32, batch), _at("page_codec_out", page_codec_out, _U8, entries),
+        _at("block_table_out", block_table_out, _I32, entries), _at("seq_lens_out", seq_lens_out, _I32, batch), max_pages,
+        ws.data_ptr(), ws.nbytes, _status_at(status), _stream_of(parents, stream)))
 
 
 def compact_workspace_bytes(pool):
     n = ctypes.c_size_t(0)
-    d = pool.desc()
-    _check(lib().argus_compact_workspace_bytes(ctypes.byref(d), ctypes.byref(n)))
+    _check(lib().argus_compact_workspace_bytes(ctypes.byref(pool.desc()), ctypes.byref(n)))
     return n.value
 
 
@@ -511,10 +520,10 @@ def compact_pages(g, pool, ref_in, ref_out, page_codec, block_table, seq_lens, b
     table go to ref_out and block_table_out, the number of live slots to n_live.
     ws of compact_workspace_bytes bytes."""
     batch = seq_lens.numel()
-    _dense(ref_in=(ref_in, _I32, pool.n_slots), ref_out=(ref_out, _I32, pool.n_slots), n_live=(n_live, _I32, 1),
-           page_codec=(page_codec, _U8, batch * max_pages), block_table=(block_table, _I32, batch * max_pages),
-           block_table_out=(block_table_out, _I32, batch * max_pages), seq_lens=(seq_lens, _I32, 0), status=(status, _STATUS, 1))
-    d = pool.desc()
-    _check(lib().argus_compact_pages(ctypes.byref(g), batch, ctypes.byref(d), _ptr(ref_in), _ptr(ref_out), _ptr(page_codec),
-                                     _ptr(block_table), _ptr(seq_lens), _ptr(block_table_out), int(max_pages), _ptr(n_live),
-                                     _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
+    entries = batch * max_pages
+    _check(lib().argus_compact_pages(
+        ctypes.byref(g), batch, ctypes.byref(pool.desc()), _at("ref_in", ref_in, _I32, pool.n_slots),
+        _at("ref_out", ref_out, _I32, pool.n_slots), _at("page_codec", page_codec, _U8, entries),
+        _at("block_table", block_table, _I32, entries), _at("seq_lens", seq_lens, _I32, 0),
+        _at("block_table_out", block_table_out, _I32, entries), max_pages, _at("n_live", n_live, _I32, 1), ws.data_ptr(),
+        ws.nbytes, _status_at(status), _stream_of(ws, stream)))

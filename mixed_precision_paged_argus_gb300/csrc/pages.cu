@@ -7,11 +7,14 @@
 // integer atomics (order-free), and every rank (the k-th free slot, the k-th
 // request, the k-th live slot) is a prefix count in slot or row order.
 //
-// What bounds them: the bytes of the table and the counts, and of the pages
-// that are copied; for small calls the chain of dependent launches.  A prefix
-// count over a pool takes two passes over tiles of 1,024 slots: a count per
-// tile, then every tile sums the counts before its own (the sum is short: a
-// pool of a million slots has 1,024 tiles), which saves a launch for a scan.
+// What bounds them: the bytes of the table and the counts, and of the pages that
+// are copied; for small calls the chain of dependent steps.  So each call is ONE
+// cooperative launch with a grid barrier between its steps (as a launch per step, the
+// small cases spent most of their time between launches).  A prefix count over
+// a pool takes two steps over tiles of 1,024 slots: a count per tile, then every
+// tile sums the counts before its own (a pool of a million slots has 1,024 tiles).
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -21,9 +24,9 @@ namespace pages {
 
 constexpr int kMaxPools = 7;         // one per codec
 constexpr int kTile = 1024;          // slots per tile: one per thread
-constexpr int kRowThreads = 256;
-constexpr int kCopyThreads = 256;
-constexpr int kPart = kCopyThreads * 4 * 16;   // bytes a CTA copies per step: four 16-byte vectors per thread
+constexpr int kPart = kTile * 4 * 16;   // bytes a block copies per step: four 16-byte vectors per thread
+
+namespace cg = cooperative_groups;
 
 struct PoolRef {
   uint8_t* codes;
@@ -43,6 +46,8 @@ struct RowInfo {
   int pages;     // pages the row has
   int grow;      // new pages
   int copy;      // 1: the row gets a copy of src
+  int copy_at;   // rank of the copy among the requests to its pool
+  int grow_at;   // rank of the first new page among the requests to its pool
 };
 
 struct FParams {
@@ -55,6 +60,7 @@ struct FParams {
   int32_t *table_out, *seq_out;
   RowInfo* rows;
   int32_t* tile_free;                // free slots per tile
+  int32_t* copies;                   // rows with a copy, in order; their number behind them
   uint32_t* status;
 };
 
@@ -119,12 +125,12 @@ __device__ __forceinline__ void copy_part(uint8_t* dst, const uint8_t* src, long
   uint4 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long o = base + (i * kCopyThreads + threadIdx.x) * 16ll;
+    const long long o = base + (i * kTile + threadIdx.x) * 16ll;
     if (o < bytes) v[i] = *reinterpret_cast<const uint4*>(src + o);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const long long o = base + (i * kCopyThreads + threadIdx.x) * 16ll;
+    const long long o = base + (i * kTile + threadIdx.x) * 16ll;
     if (o < bytes) *reinterpret_cast<uint4*>(dst + o) = v[i];
   }
 }
@@ -135,175 +141,227 @@ __device__ __forceinline__ void copy_meta(const PoolRef& r, long long dst, long 
   for (int i = threadIdx.x; i < r.meta_bytes / 4; i += blockDim.x) d[i] = s[i];
 }
 
-// ---------------------------------------------------------------- fork
-__global__ void __launch_bounds__(kTile) fork_counts_kernel(const FParams p) {
-  for (int i = 0; i < p.n_pools; ++i) {
-    const PoolRef& r = p.pool[i];
-    for (long long s = (long long)blockIdx.x * kTile + threadIdx.x; s < r.n_slots; s += (long long)gridDim.x * kTile)
-      r.ref_out[s] = r.ref_in[s];
-  }
-}
-
-// the new rows, the references given up and taken, and what each row asks for
-__global__ void __launch_bounds__(kRowThreads) fork_rows_kernel(const FParams p) {
-  const int b = blockIdx.x;
-  int bad = 0;
-  int par = p.parents[b];
-  if (par < -1 || par >= p.B) { par = -1; bad = 1; }
-  const int old_len = clamped_len(p, b), old_pages = n_pages_of(p, old_len);
-  const int len = par < 0 ? 0 : clamped_len(p, par), np = n_pages_of(p, len);
-  int add = (par >= 0 && p.n_new) ? p.n_new[b] : 0;
-  if (add < 0) { add = 0; bad = bad + 1; }
-  const long long cap = min((long long)p.max_pages * p.P, 0x7fffffffll);
-  long long end = (long long)len + add;
-  if (end > cap) { end = cap; ++bad; }
-  const int ends = n_pages_of(p, (int)end);
-  const size_t rb = (size_t)b * p.max_pages, rp = (size_t)(par < 0 ? 0 : par) * p.max_pages;
-  const bool moves = par != b;
-  const int page0 = blockIdx.y * kRowThreads + threadIdx.x;
-  int bad_entries = 0;
-  for (int page = page0; page < p.max_pages; page += gridDim.y * kRowThreads) {
-    int slot = -1, codec = 0;
-    if (page < np) {
-      slot = p.table_in[rp + page];
-      codec = p.codec_in[rp + page];
-      const int pi = pool_of(p, codec, slot);
-      if (pi < 0) ++bad_entries;
-      else if (moves) atomicAdd(p.pool[pi].ref_out + slot, 1);
-    } else if (page < ends) {
-      codec = p.new_codec;           // its slot is filled in below
-    }
-    p.table_out[rb + page] = slot;
-    p.codec_out[rb + page] = (uint8_t)codec;
-    if (moves && page < old_pages) {
-      const int s = p.table_in[rb + page];
-      const int pi = pool_of(p, p.codec_in[rb + page], s);
-      if (pi >= 0) atomicAdd(p.pool[pi].ref_out + s, -1);
-    }
-  }
-  count(p.status, bad_entries);
-  if (blockIdx.y == 0 && threadIdx.x == 0) {
-    const int raw = p.seq_in[b];
-    if (raw < 0 || raw > cap) ++bad;
-    count(p.status, bad);
-    p.seq_out[b] = (int)end;
-    RowInfo r;
-    r.src = -1;
-    r.pool = -1;
-    r.tail = np - 1;
-    r.pages = np;
-    r.grow = ends - np;
-    r.copy = 0;
-    if (end > len && len % p.P) {
-      const int slot = p.table_in[rp + np - 1];
-      r.pool = pool_of(p, p.codec_in[rp + np - 1], slot);
-      if (r.pool >= 0) r.src = slot;
-    }
-    p.rows[b] = r;
-  }
-}
-
-// blocks [0, n_tiles): free slots per tile.  The blocks behind them, a warp per
-// row: does the row get a copy of its partial page?
-__global__ void __launch_bounds__(kTile) fork_decide_kernel(const FParams p) {
-  __shared__ int sh[33];
-  if ((int)blockIdx.x < p.n_tiles) {
-    int i = 0;
-    while (i + 1 < p.n_pools && (int)blockIdx.x >= p.pool[i + 1].tile0) ++i;
-    const PoolRef& r = p.pool[i];
-    const long long s = (long long)(blockIdx.x - r.tile0) * kTile + threadIdx.x;
-    const int n = block_sum(s < r.n_slots && r.ref_out[s] == 0, sh);
-    if (threadIdx.x == 0) p.tile_free[blockIdx.x] = n;
-    return;
-  }
-  const int b = (blockIdx.x - p.n_tiles) * (kTile / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (b >= p.B) return;
-  const int src = p.rows[b].src, pool = p.rows[b].pool;
-  if (src < 0) return;
-  int writers = 0, lowest = p.B;
-  for (int i = lane; i < p.B; i += 32)
-    if (p.rows[i].src == src && p.rows[i].pool == pool) {
-      ++writers;
-      lowest = min(lowest, i);
-    }
+// exclusive prefix sum over the block; *total: the sum
+__device__ __forceinline__ int block_prefix(int x, int* sh, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int incl = x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    writers += __shfl_xor_sync(0xffffffffu, writers, o);
-    lowest = min(lowest, __shfl_xor_sync(0xffffffffu, lowest, o));
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
   }
-  if (lane == 0) p.rows[b].copy = !(p.pool[pool].ref_out[src] == writers && lowest == b);
+  __syncthreads();
+  if (lane == 31) sh[w] = incl;
+  __syncthreads();
+  if (w == 0) {
+    int y = sh[lane];                // kTile threads: 32 warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) y += z;
+    }
+    sh[lane] = y;
+  }
+  __syncthreads();
+  *total = sh[31];
+  return incl - x + (w > 0 ? sh[w - 1] : 0);
+}
+
+// ---------------------------------------------------------------- fork
+// the pool that tile `tile` belongs to
+__device__ __forceinline__ int pool_of_tile(const FParams& p, int tile) {
+  int i = 0;
+  while (i + 1 < p.n_pools && tile >= p.pool[i + 1].tile0) ++i;
+  return i;
+}
+
+// what a row becomes: its parent, pages and length
+struct RowPlan {
+  int par, len, np, ends, end, bad;
+};
+__device__ __forceinline__ RowPlan plan_row(const FParams& p, int b) {
+  RowPlan r;
+  r.bad = 0;
+  r.par = p.parents[b];
+  if (r.par < -1 || r.par >= p.B) { r.par = -1; ++r.bad; }
+  r.len = r.par < 0 ? 0 : clamped_len(p, r.par);
+  r.np = n_pages_of(p, r.len);
+  int add = (r.par >= 0 && p.n_new) ? p.n_new[b] : 0;
+  if (add < 0) { add = 0; ++r.bad; }
+  const long long cap = min((long long)p.max_pages * p.P, 0x7fffffffll);
+  long long end = (long long)r.len + add;
+  if (end > cap) { end = cap; ++r.bad; }
+  if (p.seq_in[b] < 0 || p.seq_in[b] > cap) ++r.bad;
+  r.end = (int)end;
+  r.ends = n_pages_of(p, r.end);
+  return r;
 }
 
 // what row i asks of pool k
-__device__ __forceinline__ int asks(const FParams& p, int i, int k) {
-  const RowInfo& r = p.rows[i];
+__device__ __forceinline__ int asks(const FParams& p, const RowInfo& r, int k) {
   return (r.copy && r.pool == k) + (k == p.new_pool ? r.grow : 0);
 }
 
-// the first free slots of each pool, as many as are asked for, in order; they
-// are held from here on
-__global__ void __launch_bounds__(kTile) fork_list_kernel(const FParams p) {
+__global__ void __launch_bounds__(kTile, 1) fork_kernel(const FParams p) {
   __shared__ int sh[33];
-  int i = 0;
-  while (i + 1 < p.n_pools && (int)blockIdx.x >= p.pool[i + 1].tile0) ++i;
-  const PoolRef& r = p.pool[i];
-  int x = 0;
-  for (int b = threadIdx.x; b < p.B; b += kTile) x += asks(p, b, i);
-  const int wanted = block_sum(x, sh);
-  if (wanted == 0) return;
-  const int before = block_total(p.tile_free + r.tile0, blockIdx.x - r.tile0, sh);
-  if (before >= wanted) return;
-  const long long s = (long long)(blockIdx.x - r.tile0) * kTile + threadIdx.x;
-  const bool is_free = s < r.n_slots && r.ref_out[s] == 0;
-  const int rank = before + block_rank(is_free, sh);
-  if (is_free && rank < wanted) {
-    r.free_list[rank] = (int)s;
-    r.ref_out[s] = 1;
-  }
-}
+  cg::grid_group grid = cg::this_grid();
+  const int tid = threadIdx.x;
 
-// every row takes its slots and copies its page; blockIdx.y: a part of the page
-__global__ void __launch_bounds__(kCopyThreads) fork_fill_kernel(const FParams p) {
-  __shared__ int sh[33];
-  const int b = blockIdx.x;
-  const RowInfo r = p.rows[b];
-  if (!r.copy && (blockIdx.y > 0 || r.grow == 0)) return;
-  const size_t rb = (size_t)b * p.max_pages;
-  int missing = 0;
-  // requests of pool k before this row's, and that pool's free slots
-  auto before = [&](int k) {
+  // 1. the counts carried over, the new rows, and what each row is about to write
+  for (int i = 0; i < p.n_pools; ++i) {
+    const PoolRef& r = p.pool[i];
+    for (long long s = (long long)blockIdx.x * kTile + tid; s < r.n_slots; s += (long long)gridDim.x * kTile) r.ref_out[s] = r.ref_in[s];
+  }
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const RowPlan r = plan_row(p, b);
+    const size_t rb = (size_t)b * p.max_pages, rp = (size_t)(r.par < 0 ? 0 : r.par) * p.max_pages;
+    int bad = 0;
+    for (int page = tid; page < p.max_pages; page += kTile) {
+      int slot = -1, codec = 0;
+      if (page < r.np) {
+        slot = p.table_in[rp + page];
+        codec = p.codec_in[rp + page];
+        bad += pool_of(p, codec, slot) < 0;
+      } else if (page < r.ends) {
+        codec = p.new_codec;         // its slot comes last
+      }
+      p.table_out[rb + page] = slot;
+      p.codec_out[rb + page] = (uint8_t)codec;
+    }
+    count(p.status, bad);
+    if (tid == 0) {
+      count(p.status, r.bad);
+      p.seq_out[b] = r.end;
+      RowInfo w = {-1, -1, r.np - 1, r.np, r.ends - r.np, 0, 0, 0};
+      if (r.end > r.len && r.len % p.P) {
+        const int slot = p.table_in[rp + r.np - 1];
+        w.pool = pool_of(p, p.codec_in[rp + r.np - 1], slot);
+        if (w.pool >= 0) w.src = slot;
+      }
+      p.rows[b] = w;
+    }
+  }
+  grid.sync();
+
+  // 2. references given up and taken
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    const int raw = p.parents[b], par = (raw < -1 || raw >= p.B) ? -1 : raw;
+    if (par == b) continue;
+    const int old = n_pages_of(p, clamped_len(p, b)), np = par < 0 ? 0 : n_pages_of(p, clamped_len(p, par));
+    const size_t rb = (size_t)b * p.max_pages, rp = (size_t)(par < 0 ? 0 : par) * p.max_pages;
+    for (int page = tid; page < max(old, np); page += kTile) {
+      if (page < old) {
+        const int s = p.table_in[rb + page], i = pool_of(p, p.codec_in[rb + page], s);
+        if (i >= 0) atomicAdd(p.pool[i].ref_out + s, -1);
+      }
+      if (page < np) {
+        const int s = p.table_in[rp + page], i = pool_of(p, p.codec_in[rp + page], s);
+        if (i >= 0) atomicAdd(p.pool[i].ref_out + s, 1);
+      }
+    }
+  }
+  grid.sync();
+
+  // 3. free slots per tile; a warp per row: does it get a copy of its partial page?
+  for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
+    const PoolRef& r = p.pool[pool_of_tile(p, tile)];
+    const long long s = (long long)(tile - r.tile0) * kTile + tid;
+    const int n = block_sum(s < r.n_slots && r.ref_out[s] == 0, sh);
+    if (tid == 0) p.tile_free[tile] = n;
+  }
+  for (int b = blockIdx.x * (kTile / 32) + (tid >> 5); b < p.B; b += gridDim.x * (kTile / 32)) {
+    const int lane = tid & 31, src = p.rows[b].src, pool = p.rows[b].pool;
+    if (src < 0) continue;
+    int writers = 0, lowest = p.B;
+    for (int i = lane; i < p.B; i += 32)
+      if (p.rows[i].src == src && p.rows[i].pool == pool) {
+        ++writers;
+        lowest = min(lowest, i);
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      writers += __shfl_xor_sync(0xffffffffu, writers, o);
+      lowest = min(lowest, __shfl_xor_sync(0xffffffffu, lowest, o));
+    }
+    if (lane == 0) p.rows[b].copy = !(p.pool[pool].ref_out[src] == writers && lowest == b);
+  }
+  grid.sync();
+
+  // 4. the first free slots of each pool, as many as are asked for, in order, held
+  // from here on; a block per pool ranks the requests, one more lists the copies
+  for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
+    const int k = pool_of_tile(p, tile);
+    const PoolRef& r = p.pool[k];
     int x = 0;
-    for (int i = threadIdx.x; i < b; i += kCopyThreads) x += asks(p, i, k);
-    return block_sum(x, sh);
-  };
-  auto n_free = [&](int k) { return block_total(p.tile_free + p.pool[k].tile0, p.pool[k].n_tiles, sh); };
-  if (r.copy) {
-    const PoolRef& pr = p.pool[r.pool];
-    const int at = before(r.pool), have = n_free(r.pool);
-    const int dst = at < have ? pr.free_list[at] : -1;
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
-      p.table_out[rb + r.tail] = dst;
-      atomicAdd(pr.ref_out + r.src, -1);
-      missing += dst < 0;
-    }
-    if (dst >= 0) {
-      const uint8_t* s = pr.codes + (long long)r.src * pr.page_bytes;
-      uint8_t* d = pr.codes + (long long)dst * pr.page_bytes;
-      const int parts = (int)((pr.page_bytes + kPart - 1) / kPart);
-      for (int part = blockIdx.y; part < parts; part += gridDim.y) copy_part(d, s, pr.page_bytes, part);
-      if (blockIdx.y == 0 && pr.meta_bytes) copy_meta(pr, dst, r.src);
+    for (int b = tid; b < p.B; b += kTile) x += asks(p, p.rows[b], k);
+    const int wanted = block_sum(x, sh);
+    const int before = wanted == 0 ? 0 : block_total(p.tile_free + r.tile0, tile - r.tile0, sh);
+    if (before >= wanted) continue;
+    const long long s = (long long)(tile - r.tile0) * kTile + tid;
+    const bool is_free = s < r.n_slots && r.ref_out[s] == 0;
+    const int rank = before + block_rank(is_free, sh);
+    if (is_free && rank < wanted) {
+      r.free_list[rank] = (int)s;
+      r.ref_out[s] = 1;
     }
   }
-  if (blockIdx.y == 0 && r.grow) {
-    const PoolRef& pr = p.pool[p.new_pool];
-    const int at = before(p.new_pool) + (r.copy && r.pool == p.new_pool), have = n_free(p.new_pool);
-    for (int j = threadIdx.x; j < r.grow; j += kCopyThreads) {
-      const int slot = at + j < have ? pr.free_list[at + j] : -1;
-      p.table_out[rb + r.pages + j] = slot;
-      missing += slot < 0;
+  for (int k = gridDim.x - 1 - blockIdx.x; k <= p.n_pools; k += gridDim.x) {
+    int at = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kTile) {
+      const int b = b0 + tid;
+      const RowInfo r = b < p.B ? p.rows[b] : RowInfo{};
+      int total;
+      if (k < p.n_pools) {
+        const int rank = at + block_prefix(b < p.B ? asks(p, r, k) : 0, sh, &total);
+        const bool mine = b < p.B && r.copy && r.pool == k;
+        if (mine) p.rows[b].copy_at = rank;
+        if (b < p.B && k == p.new_pool) p.rows[b].grow_at = rank + mine;
+      } else {
+        const int rank = at + block_prefix(b < p.B && r.copy, sh, &total);
+        if (b < p.B && r.copy) p.copies[rank] = b;
+      }
+      at += total;
+    }
+    if (k == p.n_pools && tid == 0) p.copies[p.B] = at;
+  }
+  grid.sync();
+
+  // 5. every row takes its slots; the pages are copied
+  auto taken = [&](int k, int rank, int have) { return rank < have ? p.pool[k].free_list[rank] : -1; };
+  const int n_copies = p.copies[p.B];
+  for (int k = 0; k < p.n_pools && n_copies > 0; ++k) {
+    const PoolRef& r = p.pool[k];
+    const int have = block_total(p.tile_free + r.tile0, r.n_tiles, sh);
+    const int parts = (int)((r.page_bytes + kPart - 1) / kPart);
+    for (long long u = blockIdx.x; u < (long long)n_copies * parts; u += gridDim.x) {
+      const int b = p.copies[u / parts], part = (int)(u % parts);
+      const RowInfo w = p.rows[b];
+      if (w.pool != k) continue;
+      const int dst = taken(k, w.copy_at, have);
+      if (part == 0 && tid == 0) {
+        p.table_out[(size_t)b * p.max_pages + w.tail] = dst;
+        atomicAdd(r.ref_out + w.src, -1);
+        count(p.status, dst < 0);
+      }
+      if (dst < 0) continue;
+      copy_part(r.codes + (long long)dst * r.page_bytes, r.codes + (long long)w.src * r.page_bytes, r.page_bytes, part);
+      if (part == 0 && r.meta_bytes) copy_meta(r, dst, w.src);
     }
   }
-  count(p.status, missing);
+  {
+    const PoolRef& r = p.pool[p.new_pool];
+    const int have = block_total(p.tile_free + r.tile0, r.n_tiles, sh);
+    for (int b = blockIdx.x * (kTile / 32) + (tid >> 5); b < p.B; b += gridDim.x * (kTile / 32)) {
+      const RowInfo w = p.rows[b];
+      int missing = 0;
+      for (int j = tid & 31; j < w.grow; j += 32) {
+        const int slot = taken(p.new_pool, w.grow_at + j, have);
+        p.table_out[(size_t)b * p.max_pages + w.pages + j] = slot;
+        missing += slot < 0;
+      }
+      count(p.status, missing);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- compact
@@ -313,50 +371,53 @@ struct CParams {
   const int32_t *seq, *table_in;
   const uint8_t* codec_in;
   int32_t *table_out, *n_live;
-  int32_t *tile_live, *src, *dst, *rank, *n_moves;
+  int32_t *tile_live, *src, *dst, *rank;
   uint32_t* status;
 };
 
-__global__ void __launch_bounds__(kTile) compact_count_kernel(const CParams p) {
+__global__ void __launch_bounds__(kTile, 1) compact_kernel(const CParams p) {
   __shared__ int sh[33];
-  const long long s = (long long)blockIdx.x * kTile + threadIdx.x;
-  const int n = block_sum(s < p.pool.n_slots && p.pool.ref_in[s] > 0, sh);
-  if (threadIdx.x == 0) p.tile_live[blockIdx.x] = n;
-}
+  cg::grid_group grid = cg::this_grid();
+  const int tid = threadIdx.x, n = p.pool.n_slots;
 
-__global__ void __launch_bounds__(kTile) compact_list_kernel(const CParams p) {
-  __shared__ int sh[33];
-  const int n = p.pool.n_slots;
+  // 1. live slots per tile
+  for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
+    const long long s = (long long)tile * kTile + tid;
+    const int x = block_sum(s < n && p.pool.ref_in[s] > 0, sh);
+    if (tid == 0) p.tile_live[tile] = x;
+  }
+  grid.sync();
+
+  // 2. the free slots below the number of live ones, the live slots above, in order
   const int live_total = block_total(p.tile_live, p.n_tiles, sh);
-  const int before = block_total(p.tile_live, blockIdx.x, sh);
   // live slots below slot live_total: whole tiles, and part of the one it lies in
   const int lt = live_total / kTile;
-  const long long ls = (long long)lt * kTile + threadIdx.x;
+  const long long ls = (long long)lt * kTile + tid;
   const int below = block_total(p.tile_live, min(lt, p.n_tiles), sh) + block_sum(ls < live_total && ls < n && p.pool.ref_in[ls] > 0, sh);
-  const long long s = (long long)blockIdx.x * kTile + threadIdx.x;
-  const int ref = s < n ? p.pool.ref_in[s] : 0;
-  const bool live = ref > 0;
-  const int rank = before + block_rank(live, sh);
-  if (s < n) {
-    if (s < live_total) {
-      if (live) p.pool.ref_out[s] = ref;         // a free one gets its count with its page
-      else p.dst[s - rank] = (int)s;
-    } else {
-      p.pool.ref_out[s] = 0;
-      if (live) {
-        p.src[rank - below] = (int)s;
-        p.rank[s] = rank - below;
+  const int moves = live_total - below;
+  for (int tile = blockIdx.x; tile < p.n_tiles; tile += gridDim.x) {
+    const int before = block_total(p.tile_live, tile, sh);
+    const long long s = (long long)tile * kTile + tid;
+    const int ref = s < n ? p.pool.ref_in[s] : 0;
+    const bool live = ref > 0;
+    const int rank = before + block_rank(live, sh);
+    if (s < n) {
+      if (s < live_total) {
+        if (live) p.pool.ref_out[s] = ref;       // a free one gets its count with its page
+        else p.dst[s - rank] = (int)s;
+      } else {
+        p.pool.ref_out[s] = 0;
+        if (live) {
+          p.src[rank - below] = (int)s;
+          p.rank[s] = rank - below;
+        }
       }
     }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *p.n_moves = live_total - below;
-    *p.n_live = live_total;
-  }
-}
+  if (blockIdx.x == 0 && tid == 0) *p.n_live = live_total;
+  grid.sync();
 
-__global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CParams p) {
-  const int live = *p.n_live, moves = *p.n_moves;
+  // 3. the pages move, the table follows
   const int parts = (int)((p.pool.page_bytes + kPart - 1) / kPart);
   for (long long w = blockIdx.x; w < (long long)moves * parts; w += gridDim.x) {
     const int k = (int)(w / parts), part = (int)(w - (long long)k * parts);
@@ -364,17 +425,17 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const CParam
     copy_part(p.pool.codes + dst * p.pool.page_bytes, p.pool.codes + src * p.pool.page_bytes, p.pool.page_bytes, part);
     if (part == 0) {
       if (p.pool.meta_bytes) copy_meta(p.pool, dst, src);
-      if (threadIdx.x == 0) p.pool.ref_out[dst] = p.pool.ref_in[src];
+      if (tid == 0) p.pool.ref_out[dst] = p.pool.ref_in[src];
     }
   }
   const long long entries = (long long)p.B * p.max_pages;
   int bad = 0;
-  for (long long e = (long long)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (long long)gridDim.x * kCopyThreads) {
+  for (long long e = (long long)blockIdx.x * kTile + tid; e < entries; e += (long long)gridDim.x * kTile) {
     const int b = (int)(e / p.max_pages), page = (int)(e - (long long)b * p.max_pages);
     int slot = p.table_in[e];
     if (p.codec_in[e] == p.pool.codec && (long long)page * p.P < p.seq[b]) {
-      if (slot < 0 || slot >= p.pool.n_slots) ++bad;
-      else if (slot >= live && p.pool.ref_in[slot] > 0) slot = p.dst[p.rank[slot]];
+      if (slot < 0 || slot >= n) ++bad;
+      else if (slot >= live_total && p.pool.ref_in[slot] > 0) slot = p.dst[p.rank[slot]];
     }
     p.table_out[e] = slot;
   }
@@ -439,11 +500,25 @@ static argus_status fill_pool(const char* what, const argus_geom& g, const argus
   return ARGUS_OK;
 }
 
+// One block of kTile threads per SM at most (the kernels' launch bounds let each
+// SM hold one): all are resident, as the grid barrier needs.
+template <class K, class P>
+static argus_status launch_cooperative(const char* what, K kernel, P& p, long long work, cudaStream_t s) {
+  const int blocks = (int)std::max<long long>(1, std::min<long long>(work, device_sm_count()));
+  void* args[] = {&p};
+  const cudaError_t e = cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(blocks), dim3(kTile), args, 0, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(ARGUS_E_LAUNCH, "%s: launch failed: %s", what, cudaGetErrorString(e));
+  }
+  return ARGUS_OK;
+}
+
 static size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
-// fork workspace: RowInfo [B], free slots per tile, the free lists
+// fork workspace: RowInfo [B], the rows with copies, free slots per tile, the free lists
 static size_t fork_bytes(int B, const argus_pool* pools, int n_pools) {
-  size_t n = up16((size_t)B * sizeof(RowInfo));
+  size_t n = up16((size_t)B * sizeof(RowInfo)) + up16((size_t)(B + 1) * 4);
   for (int i = 0; i < n_pools; ++i)
     n += up16((size_t)((pools[i].n_slots + kTile - 1) / kTile) * 4) + up16((size_t)pools[i].n_slots * 4);
   return n + 16 * kMaxPools;
@@ -501,14 +576,14 @@ extern "C" argus_status argus_fork_pages(const argus_geom* g, int32_t batch, con
   }
   if (p.new_pool < 0) return fail(ARGUS_E_INVALID, "fork: no pool of the new pages' codec %d", new_codec);
   if (batch == 0 && tiles == 0) return ARGUS_OK;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)) return fail(ARGUS_E_INVALID, "fork: ws must be a 16-byte aligned device pointer");
+  if (ws_bytes < fork_bytes(batch, pools, n_pools))
+    return fail(ARGUS_E_WORKSPACE, "fork: workspace of %zu bytes, %zu needed", ws_bytes, fork_bytes(batch, pools, n_pools));
   if (batch > 0) {
     if (!parents || !page_codec || !block_table || !seq_lens || !page_codec_out || !block_table_out || !seq_lens_out)
       return fail(ARGUS_E_INVALID, "fork: NULL pointer");
     if (page_codec == page_codec_out || block_table == block_table_out || seq_lens == seq_lens_out)
       return fail(ARGUS_E_INVALID, "fork: the new table needs arrays of its own");
-    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)) return fail(ARGUS_E_INVALID, "fork: ws must be a 16-byte aligned device pointer");
-    if (ws_bytes < fork_bytes(batch, pools, n_pools))
-      return fail(ARGUS_E_WORKSPACE, "fork: workspace of %zu bytes, %zu needed", ws_bytes, fork_bytes(batch, pools, n_pools));
   }
   p.n_pools = n_pools;
   p.new_codec = new_codec;
@@ -528,6 +603,8 @@ extern "C" argus_status argus_fork_pages(const argus_geom* g, int32_t batch, con
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.rows = reinterpret_cast<RowInfo*>(w);
   w += up16((size_t)batch * sizeof(RowInfo));
+  p.copies = reinterpret_cast<int32_t*>(w);
+  w += up16((size_t)(batch + 1) * 4);
   p.tile_free = reinterpret_cast<int32_t*>(w);
   w += up16((size_t)tiles * 4);
   long long part_max = 1;
@@ -536,17 +613,9 @@ extern "C" argus_status argus_fork_pages(const argus_geom* g, int32_t batch, con
     w += up16((size_t)p.pool[i].n_slots * 4);
     part_max = std::max(part_max, (p.pool[i].page_bytes + kPart - 1) / kPart);
   }
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = device_sm_count();
-  if (tiles > 0) fork_counts_kernel<<<std::min(tiles, 2 * sms), kTile, 0, s>>>(p);
-  if (batch > 0) {
-    const int ychunks = std::max(1, std::min((max_pages + kRowThreads * 4 - 1) / (kRowThreads * 4), std::max(1, 8 * sms / batch)));
-    fork_rows_kernel<<<dim3(batch, ychunks), kRowThreads, 0, s>>>(p);
-    fork_decide_kernel<<<tiles + (batch + kTile / 32 - 1) / (kTile / 32), kTile, 0, s>>>(p);
-    if (tiles > 0) fork_list_kernel<<<tiles, kTile, 0, s>>>(p);
-    fork_fill_kernel<<<dim3(batch, (unsigned)std::min<long long>(part_max, 64)), kCopyThreads, 0, s>>>(p);
-  }
-  return launch_status("argus_fork_pages");
+  // a block per row, tile or copied part that there can be, one per SM at most
+  const long long work = std::max<long long>(tiles, (long long)batch * std::min<long long>(part_max, 64));
+  return launch_cooperative("argus_fork_pages", fork_kernel, p, work, static_cast<cudaStream_t>(stream));
 }
 
 static size_t compact_bytes(const argus_pool& pool) {
@@ -590,20 +659,13 @@ extern "C" argus_status argus_compact_pages(const argus_geom* g, int32_t batch, 
   p.n_live = n_live;
   p.status = status;
   uint8_t* w = static_cast<uint8_t*>(ws);
-  p.n_moves = reinterpret_cast<int32_t*>(w);
-  w += 16;
   p.tile_live = reinterpret_cast<int32_t*>(w);
   w += up16((size_t)p.n_tiles * 4);
   const size_t per = up16((size_t)pool->n_slots * 4);
   p.src = reinterpret_cast<int32_t*>(w);
   p.dst = reinterpret_cast<int32_t*>(w + per);
   p.rank = reinterpret_cast<int32_t*>(w + 2 * per);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int sms = device_sm_count();
-  if (p.n_tiles > 0) compact_count_kernel<<<p.n_tiles, kTile, 0, s>>>(p);
-  compact_list_kernel<<<std::max(1, p.n_tiles), kTile, 0, s>>>(p);   // with no slot: n_live = 0
   const long long parts = (p.pool.page_bytes + kPart - 1) / kPart;
-  const long long work = std::max((long long)pool->n_slots / 2 * parts, ((long long)batch * max_pages + kCopyThreads - 1) / kCopyThreads);
-  compact_move_kernel<<<(int)std::max<long long>(1, std::min<long long>(work, 8ll * sms)), kCopyThreads, 0, s>>>(p);
-  return launch_status("argus_compact_pages");
+  const long long work = std::max((long long)pool->n_slots / 2 * parts, ((long long)batch * max_pages + kTile - 1) / kTile);
+  return launch_cooperative("argus_compact_pages", compact_kernel, p, work, static_cast<cudaStream_t>(stream));
 }
