@@ -413,10 +413,11 @@ def _status_at(t):
 def _stream_of(t, stream):
     """The stream to launch on: the given one, or t's device's current one.  The
     library launches on the current device, so t has to lie there."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError("the tensors lie on cuda:%d, the current device is cuda:%d" % (t.device.index, torch.cuda.current_device()))
+    device = t.get_device()
+    if device >= 0 and device != torch._C._cuda_getDevice():
+        raise ValueError("the tensors lie on cuda:%d, which is not the current device" % device)
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if t.is_cuda else None
+        return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
