@@ -40,10 +40,10 @@ constexpr int kBN = 128;             // keys per block
 constexpr int kGroupWarps = 4;       // one softmax warpgroup: a thread per TMEM lane
 constexpr int kSoftmaxWarps = 2 * kGroupWarps;
 constexpr int kLoadWarps = 16;       // eight for K, eight for V: a 16-token chunk of every block each
-constexpr int kQWarps = 2;
 constexpr int kLookWarp = kSoftmaxWarps + kLoadWarps;
 constexpr int kMmaWarp = kLookWarp + 1;
 constexpr int kQWarp0 = kMmaWarp + 1;
+constexpr int kQWarps = 2;
 constexpr int kThreads = 32 * (kQWarp0 + kQWarps);
 // 28 warps get 72 registers a thread at launch; the loaders' four-warp groups give
 // up what the softmax groups take.  Nothing may spill: the tiles leave the
@@ -296,6 +296,15 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {   // read once: past 
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+// 16 bytes of which `bytes` (16 or 0) are read, the rest zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const uint8_t* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -303,10 +312,12 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 // mbar_wait (common.cuh) whose every attempt lets the hardware suspend the warp
-// for up to kSuspendNs: 28 warps share the issue slots, and most of them wait.
+// for a while (28 warps share the issue slots, and most of them wait), and that
+// reads the clock only every 64 attempts.
 constexpr uint32_t kSuspendNs = 1000;
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const volatile uint32_t* abort) {
-  const unsigned long long t0 = global_ns();
+  if (mbar_try_wait(bar, parity)) return true;
+  unsigned long long t0 = 0;
   for (uint32_t i = 1;; ++i) {
     uint32_t ok;
     asm volatile(
@@ -317,7 +328,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const volat
         : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
         : "memory");
     if (ok) return true;
-    if (*abort || global_ns() - t0 > kWaitLimitNs) return false;
+    if ((i & 63u) == 0) {
+      const unsigned long long t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (*abort || t - t0 > kWaitLimitNs) return false;
+    }
   }
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -403,9 +418,14 @@ __device__ __forceinline__ void store_steps(uint4 (&v)[kSteps], uint32_t tile, i
 
 // The lookup warp finds the pages of kBatch blocks at once, a lane per chunk
 // (lane = 8 * block + chunk): the two dependent reads (table, then scales) are
-// paid once per batch, and the batch behind is read meanwhile.
+// paid once per batch, and the batches behind are read meanwhile.
 struct Lookup {
   int codec, slot, row, n_rows, h, first;   // first: this chunk counts a page that cannot be read
+};
+struct Found {
+  const uint8_t* src;
+  uint32_t state;                    // codec | rows << 8; 0: nothing to read
+  float ks, vs;                      // ks < 0: a page that cannot be read
 };
 
 // One lane of the warp, the same each time.
@@ -608,9 +628,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     // ---------------------------------------------------------- Q tiles
     // Row l of an item's tile goes to TMEM lanes l, l + per, ...; zeros behind the
     // last row.  An item ahead of the softmax groups, so that nothing waits for it
-    // but the first.
-    constexpr int V = D / 8, RS = 32 / V * kQWarps;    // vectors per row; rows of a step
-    const int v = lane % V, r0 = (warp - kQWarp0) * (32 / V) + lane / V;
+    // but the first.  All rows are on their way at once (asynchronous copies,
+    // which write zeros where they read nothing); rows that become fp16 are
+    // turned in place by the lanes that copied them.
+    constexpr int V = D / 8, RW = 32 / V, RS = RW * kQWarps;   // vectors per row; rows of a warp's step, of all warps'
+    const int v = lane % V, r0 = (warp - kQWarp0) * RW + lane / V;
     Cursor c;
     c.start(p, misc[2], misc64[2], n_blocks);
     for (int k = 0; c.left > 0; ++k) {
@@ -623,37 +645,33 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         it[0] = c.s.q0; it[1] = c.s.n; it[2] = c.s.len; it[3] = c.h; it[4] = c.t; it[5] = c.blk; it[6] = nb; it[7] = c.nb;
       }
       const uint32_t q_s = smem_u32(smem + SM::kOffQ + buf * kTile);
-      const uint16_t* src = p.q + (long long)c.s.q0 * p.qs + (long long)c.h * p.G * D + v * 8;
-      int tok = (lin0 + r0) / p.G, g = lin0 + r0 - tok * p.G;
-#pragma unroll 1
-      for (int l0 = r0; l0 < per; l0 += 4 * RS) {
-        uint4 q[4];
+      int g = (lin0 + r0) % p.G;
+      const uint16_t* src = p.q + (long long)(c.s.q0 + (lin0 + r0) / p.G) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
+      const long long next_token = p.qs - (long long)p.G * D;
+#pragma unroll 4
+      for (int l = r0; l < per; l += RS) {
+        const bool real = l < rows;
+        for (int r = 0; r < nrep; ++r) cp_async16(q_s + tile_off(l + r * per, v), real ? src : p.q, real ? 16 : 0);
+        src += RS * D;
+        for (g += RS; g >= p.G; g -= p.G) src += next_token;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (BF && !BFM) {
+        // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
+#pragma unroll 2
+        for (int l = r0; l < per; l += RS) {
+          const uint4 q = lds16(q_s + tile_off(l, v));
+          uint32_t w[4] = {q.x, q.y, q.z, q.w}, mx = 0;   // magnitudes of bf16 order like their bits
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          q[x] = make_uint4(0, 0, 0, 0);
-          if (l0 + x * RS < rows) q[x] = *reinterpret_cast<const uint4*>(src + (long long)tok * p.qs + g * D);
-          for (g += RS; g >= p.G; g -= p.G) ++tok;
-        }
+          for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int l = l0 + x * RS;
-          if (l >= per) break;         // the same for a whole row's lanes, and for the warp (per: a multiple of RS)
-          float f1 = 1.f;
-          if (BF && !BFM) {
-            // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
-            uint32_t w[4] = {q[x].x, q[x].y, q[x].z, q[x].w}, mx = 0;   // magnitudes of bf16 order like their bits
+          for (int o = V / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const int ex = max((int)(mx >> 23), 15);        // biased; from 15 on 2^(141 - ex) is a normal number
+          const float f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
-#pragma unroll
-            for (int o = V / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int ex = max((int)(mx >> 23), 15);    // biased; from 15 on 2^(141 - ex) is a normal number
-            f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
-            q[x] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
           for (int r = 0; r < nrep; ++r) {
-            sts16(q_s + tile_off(l + r * per, v), q[x].x, q[x].y, q[x].z, q[x].w);
+            sts16(q_s + tile_off(l + r * per, v), w[0], w[1], w[2], w[3]);
             if (v == 0) q_scale[buf * kBM + l + r * per] = 1.f / f1;
           }
         }
@@ -693,46 +711,59 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       }
       return k;
     };
-    Lookup ahead = look();
-    for (int k = 0; k * kBatch < n_blocks; ++k) {
-      const Lookup now = ahead;
-      const uint8_t* src = nullptr;
-      uint32_t state = 0;              // codec | rows << 8; 0: nothing to read
-      float ks = 1.f, vs = 1.f;
-      if (now.n_rows > 0) {
-        const bool known = now.codec <= ARGUS_INT8 && (W16 || now.codec >= ARGUS_FP8_E4M3);
-        const PoolRef r = p.pool[now.codec & 3];
-        if (!known || now.slot < 0 || now.slot >= r.n_slots) {
-          ks = -1.f;
-          if (now.first && p.status) atomicAdd(p.status, 1u);
+    auto resolve = [&](const Lookup& k) {
+      Found f;
+      f.src = nullptr;
+      f.state = 0;
+      f.ks = f.vs = 1.f;
+      if (k.n_rows > 0) {
+        const bool known = k.codec <= ARGUS_INT8 && (W16 || k.codec >= ARGUS_FP8_E4M3);
+        const PoolRef r = p.pool[k.codec & 3];
+        if (!known || k.slot < 0 || k.slot >= r.n_slots) {
+          f.ks = -1.f;
+          if (k.first && p.status) atomicAdd(p.status, 1u);
         } else {
-          const int rb = now.codec <= ARGUS_BF16 ? 2 * D : D;
-          const long long unit = (long long)now.slot * 2 * p.Hkv + now.h;
-          src = r.codes + (unit * p.P + now.row) * rb;
-          state = now.codec | now.n_rows << 8;
-          // toward the L2, some blocks before a loader asks for them: what the
-          // loaders have in flight in registers would not cover a DRAM read
-          prefetch_l2(src, 16 * rb);
-          prefetch_l2(src + (long long)p.Hkv * p.P * rb, 16 * rb);
-          if (now.codec >= ARGUS_FP8_E4M3) {
-            ks = r.meta[unit];
-            vs = r.meta[unit + p.Hkv];
+          const int rb = k.codec <= ARGUS_BF16 ? 2 * D : D;
+          const long long unit = (long long)k.slot * 2 * p.Hkv + k.h;
+          f.src = r.codes + (unit * p.P + k.row) * rb;
+          f.state = k.codec | k.n_rows << 8;
+          if (k.codec >= ARGUS_FP8_E4M3) {
+            f.ks = r.meta[unit];
+            f.vs = r.meta[unit + p.Hkv];
           }
         }
       }
-      ahead = look();
+      return f;
+    };
+    // toward the L2, some blocks before a loader asks for it: what the loaders have
+    // in flight in registers would not cover a DRAM read
+    auto ahead = [&](const Found& f) {
+      if (!f.state) return;
+      const int rb = (W16 && (f.state & 0xFF) <= ARGUS_BF16) ? 2 * D : D;
+      prefetch_l2(f.src, 16 * rb);
+      prefetch_l2(f.src + (long long)p.Hkv * p.P * rb, 16 * rb);
+    };
+    // three batches on their way: table entries, scales, and the one handed out
+    Lookup table = look();
+    Found next = resolve(table);
+    table = look();
+    for (int k = 0; k * kBatch < n_blocks; ++k) {
+      const Found now = next;
+      next = resolve(table);
+      table = look();
       if (k >= kBatches && !__all_sync(0xffffffffu, wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
         misc[1] = 1;
         break;
       }
       const int at = (k % kBatches) * 32 + lane;
-      const unsigned long long addr = reinterpret_cast<unsigned long long>(src);
-      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), state, 0);
-      const float lvs = log2f(vs);     // 0: -inf
+      const unsigned long long addr = reinterpret_cast<unsigned long long>(now.src);
+      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), now.state, 0);
+      const float lvs = log2f(now.vs);   // 0: -inf
       // a scale far from 1: its chunk's sum is kept apart, and does not enter the others'
-      scales[at] = make_float4(ks < 0.f ? -1.f : ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / vs, 0.f);
+      scales[at] = make_float4(now.ks < 0.f ? -1.f : now.ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / now.vs, 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&looked[k % kBatches]);
+      ahead(now);
     }
   } else if (warp >= kSoftmaxWarps) {
     // ---------------------------------------------------------- loaders
@@ -747,15 +778,16 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     uint4 v[kSteps];
     uint32_t state = 0;
     const uint8_t* src = nullptr;
-    // the warp's chunk of block i on its way: all of it, or the first half of
-    // 16-bit rows of 128 dims
-    auto fetch = [&](int i) {
-      state = 0;
-      if (i >= n_blocks || !ok) return;
-      if (i % kBatch == 0) ok = wait(&looked[(i / kBatch) % kBatches], (uint32_t)(i / kSlots) & 1, &misc[1]);
-      const uint4 d = chunks[(i % kSlots) * 8 + ch];
-      if (!ok || !d.z) return;
-      state = d.z;
+    // the description of the warp's chunk of block i
+    auto describe = [&](uint32_t i) {
+      if (i >= (uint32_t)n_blocks) return make_uint4(0, 0, 0, 0);
+      if (i % kBatch == 0 && ok) ok = wait(&looked[(i / kBatch) % kBatches], (i / kSlots) & 1, &misc[1]);
+      return chunks[(i % kSlots) * 8 + ch];
+    };
+    // the chunk on its way: all of it, or the first half of 16-bit rows of 128 dims
+    auto fetch = [&](const uint4& d) {
+      state = ok ? d.z : 0;
+      if (!state) return;
       src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x) + v_off;
       if (W16 && (state & 0xFF) <= ARGUS_BF16) {
         src += v_off;
@@ -764,10 +796,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         load_steps<D, D / 16>(v, src, lane, 0);
       }
     };
-    fetch(0);
-    for (int i = 0; i < n_blocks; ++i) {
-      const int b = i & 1;
-      if (i >= 2 && ok) ok = wait(&empty[b], (uint32_t)((i >> 1) - 1) & 1, &misc[1]);
+    fetch(describe(0));
+    uint4 next = describe(1);
+    for (uint32_t i = 0; i < (uint32_t)n_blocks; ++i) {
+      const uint32_t b = i & 1;
+      if (i >= 2 && ok) ok = wait(&empty[b], ((i >> 1) - 1) & 1, &misc[1]);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         const int codec = state & 0xFF, n_rows = state >> 8;
@@ -785,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
             store_steps<D, BFM, ARGUS_FP8_E4M3>(v, to, lane, n_rows, 0);
           }
         }
-        fetch(i + 1);
+        fetch(next);
         fence_async();
         __syncwarp();
         if (lane == 0) {
@@ -794,6 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           // done: the batch before the last one is not needed any more
           if (i % kBatch == kBatch - 1 && i >= kBatch) mbar_arrive(&used[(i / kBatch - 1) % kBatches]);
         }
+        next = describe(i + 2);
       }
     }
     if (!ok) misc[1] = 1;
