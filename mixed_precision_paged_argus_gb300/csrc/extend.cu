@@ -81,10 +81,14 @@ struct Smem {
 
 // ---------------------------------------------------------------- the work list
 // An item is (sequence b, KV head h, tile t of 128 query rows); its work is its
-// key blocks.  All blocks of all items in that order are dealt to the CTAs in equal
-// contiguous ranges, so an item may be cut anywhere: the pieces are
-// partial softmaxes, joined by the second kernel.  The host knows neither the lengths
-// nor the query counts; every CTA finds its range from them.
+// key blocks, plus what every item costs (its first scores, its epilogue), counted as
+// kItemCost blocks in front of them: without that, a CTA that got many short
+// items ran several times as long as the others.  All units of all items in that
+// order are dealt to the CTAs in equal contiguous ranges, so an item's blocks may
+// be cut anywhere: the pieces are partial softmaxes, joined by the second
+// kernel.  The host knows neither the lengths nor the query counts; every
+// CTA finds its range from them.
+constexpr int kItemCost = 3;
 struct Seq {
   int q0, n, len;
 };
@@ -131,9 +135,16 @@ __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& 
   return sum;
 }
 
-__device__ __forceinline__ long long seq_blocks(const EParams& p, int b) {
+// a sequence's items, and its blocks
+struct Load {
+  long long items, blocks;
+  __device__ __forceinline__ long long units() const { return blocks + kItemCost * items; }
+};
+__device__ __forceinline__ Load seq_load(const EParams& p, int b) {
   const Seq s = load_seq(p, b);
-  return s.n == 0 ? 0 : p.Hkv * blocks_before(p, s, n_tiles(p, s));
+  if (s.n == 0) return {0, 0};
+  const int T = n_tiles(p, s);
+  return {(long long)p.Hkv * T, p.Hkv * blocks_before(p, s, T)};
 }
 
 __device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
@@ -148,64 +159,36 @@ __device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
 
 __device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return total * cta / n_ctas; }
 
-// A CTA's range: its number of blocks, and the sequence and the number within it
-// of the first one.  Only the first min(total, CTAs) CTAs have blocks.  By a
-// whole warp.
-struct Range {
-  long long total, w0, w1;           // blocks of the call; the range
-  int n, b;                          // CTAs with blocks; first sequence
-  long long rest;                    // first block's number within it
+// A place in the work list: unit `rest` of sequence b (b = B: the end), and the
+// items and units of the sequences before.
+struct Place {
+  int b;
+  long long rest, items, units;
 };
-__device__ __forceinline__ Range find_range(const EParams& p, int cta) {
-  const int lane = threadIdx.x & 31;
-  Range r;
-  long long mine = lane < p.B ? seq_blocks(p, lane) : 0, sum = mine;
-  for (int b = lane + 32; b < p.B; b += 32) sum += seq_blocks(p, b);
-  r.total = __shfl_sync(0xffffffffu, warp_scan(sum), 31);
-  r.n = (int)min((long long)p.n_ctas, r.total);
-  r.w0 = r.w1 = r.rest = 0;
-  r.b = 0;
-  if (cta >= r.n) return r;
-  r.w0 = range_start(r.total, cta, r.n);
-  r.w1 = range_start(r.total, cta + 1, r.n);
-  r.rest = r.w0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    if (b0 > 0) mine = b0 + lane < p.B ? seq_blocks(p, b0 + lane) : 0;
-    const long long incl = warp_scan(mine);
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > r.rest);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      r.rest -= __shfl_sync(0xffffffffu, incl - mine, src);
-      r.b = b0 + src;
-      break;
-    }
-    r.rest -= __shfl_sync(0xffffffffu, incl, 31);
-  }
-  return r;
-}
 
 struct Cursor {
   Seq s;
   int b, h, t, T, blk, nb;
   int left;                          // blocks of the range still ahead, this one counted
 
-  // block `rest` of sequence b
+  // the item that unit `rest` of sequence b lies in, and the block there: the
+  // units in front of an item's blocks belong to its first
   __device__ __forceinline__ void start(const EParams& p, int b_, long long rest, int left_) {
     b = b_;
     left = left_;
     s = load_seq(p, b);
     T = n_tiles(p, s);
-    const long long per = blocks_before(p, s, T);
+    const long long per = blocks_before(p, s, T) + (long long)kItemCost * T;
     h = (int)(rest / per);
     rest -= h * per;
-    int lo = 0, hi = T - 1;          // the last tile with blocks_before(t) <= rest
+    int lo = 0, hi = T - 1;          // the last tile with units before it <= rest
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
-      if (blocks_before(p, s, mid) <= rest) lo = mid;
+      if (blocks_before(p, s, mid) + (long long)kItemCost * mid <= rest) lo = mid;
       else hi = mid - 1;
     }
     t = lo;
-    blk = (int)(rest - blocks_before(p, s, t));
+    blk = (int)max(0ll, rest - blocks_before(p, s, t) - (long long)kItemCost * (t + 1));
     nb = tile_blocks(p, s, t);
   }
   __device__ __forceinline__ void next_item(const EParams& p) {
@@ -230,6 +213,68 @@ struct Cursor {
     if (blk == nb && left > 0) next_item(p);
   }
 };
+
+// A CTA's range: where it begins, and its number of blocks.  Only the first
+// min(units, CTAs) CTAs have one.  By a whole warp.
+struct Range {
+  long long total, w0;               // units of the call; the range's first
+  int n, n_blocks;                   // CTAs with a range; blocks of it
+  Place at;
+};
+__device__ __forceinline__ Range find_range(const EParams& p, int cta) {
+  const int lane = threadIdx.x & 31;
+  const Load first = lane < p.B ? seq_load(p, lane) : Load{0, 0};
+  Load sum = first;
+  for (int b = lane + 32; b < p.B; b += 32) {
+    const Load x = seq_load(p, b);
+    sum.items += x.items;
+    sum.blocks += x.blocks;
+  }
+  const long long items = __shfl_sync(0xffffffffu, warp_scan(sum.items), 31);
+  Range r;
+  r.total = __shfl_sync(0xffffffffu, warp_scan(sum.blocks), 31) + kItemCost * items;
+  r.n = (int)min((long long)p.n_ctas, r.total);
+  r.w0 = 0;
+  r.n_blocks = 0;
+  r.at = {0, 0, 0, 0};
+  if (cta >= r.n) return r;
+  const long long w[2] = {range_start(r.total, cta, r.n), range_start(r.total, cta + 1, r.n)};
+  Place at[2] = {{p.B, 0, items, r.total}, {p.B, 0, items, r.total}};
+  Place before = {0, 0, 0, 0};
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const Load mine = b0 == 0 ? first : b0 + lane < p.B ? seq_load(p, b0 + lane) : Load{0, 0};
+    const long long units = warp_scan(mine.units()), its = warp_scan(mine.items);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const unsigned hit = __ballot_sync(0xffffffffu, before.units + units > w[x]);
+      if (hit && at[x].b == p.B) {
+        const int src = __ffs(hit) - 1;
+        at[x].b = b0 + src;
+        at[x].units = before.units + __shfl_sync(0xffffffffu, units - mine.units(), src);
+        at[x].items = before.items + __shfl_sync(0xffffffffu, its - mine.items, src);
+        at[x].rest = w[x] - at[x].units;
+      }
+    }
+    if (at[0].b < p.B && at[1].b < p.B) break;
+    before.units += __shfl_sync(0xffffffffu, units, 31);
+    before.items += __shfl_sync(0xffffffffu, its, 31);
+  }
+  // blocks in front of each place
+  long long blocks[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    blocks[x] = at[x].units - kItemCost * at[x].items;
+    if (at[x].b < p.B) {
+      Cursor c;
+      c.start(p, at[x].b, at[x].rest, 1);
+      blocks[x] += c.h * blocks_before(p, c.s, c.T) + blocks_before(p, c.s, c.t) + c.blk;
+    }
+  }
+  r.w0 = w[0];
+  r.at = at[0];
+  r.n_blocks = (int)(blocks[1] - blocks[0]);   // fewer than 2^31 (checked on the host)
+  return r;
+}
 
 // The pieces of the range [w0, w1): the one that does not begin its item (the
 // first piece of a range at most) and the one that does not end it (the last)
@@ -492,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   uint64_t* drain = o_free + 2;
   uint64_t* looked = drain + 1;        // a batch of blocks is looked up
   uint64_t* used = looked + kBatches;  // nobody needs the batch any more
-  // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] the first one's
-  // number within its sequence
+  // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] its first unit
+  // within that sequence
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
   volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   // [2][8]: q0, n, len, h, t, first block, blocks of the piece, blocks of the item
@@ -509,20 +554,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   if (warp == 0) {
     const Range r = find_range(p, blockIdx.x);
     if (lane == 0) {
-      misc[2] = r.b;
-      misc64[2] = r.rest;
-      misc[3] = (uint32_t)(r.w1 - r.w0);   // fewer than 2^31 (checked on the host)
+      misc[2] = r.at.b;
+      misc64[2] = r.at.rest;
+      misc[3] = (uint32_t)r.n_blocks;
     }
     Cut cut = {};
-    if (r.w1 > r.w0) {
+    if (r.n_blocks > 0) {
       Cursor c;
-      c.start(p, r.b, r.rest, 1);
-      const long long begin = r.w0 - c.blk, end = begin + c.nb;
-      // this range begins inside an item, and is the first to
-      if (c.blk > 0 && range_start(r.total, blockIdx.x - 1, r.n) <= begin) {
+      c.start(p, r.at.b, r.at.rest, 1);
+      const long long first = r.w0 - c.blk;              // the unit of the item's first block
+      // this range begins inside an item's blocks, and is the first to
+      if (c.blk > 0 && range_start(r.total, blockIdx.x - 1, r.n) <= first) {
         cut.rows = min(kBM, c.s.n * p.G - c.t * kBM);
         cut.last = blockIdx.x;
-        while (cut.last + 1 < r.n && range_start(r.total, cut.last + 1, r.n) < end) ++cut.last;
+        while (cut.last + 1 < r.n && range_start(r.total, cut.last + 1, r.n) < first + c.nb) ++cut.last;
         cut.q0 = c.s.q0;
         cut.row0 = c.t * kBM;
         cut.head0 = c.h * p.G;
