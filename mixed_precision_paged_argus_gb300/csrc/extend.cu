@@ -57,7 +57,7 @@ constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chu
 constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
 constexpr int kBatches = 4;          // batches whose descriptions are kept
 constexpr int kSlots = kBatch * kBatches;
-constexpr int kMergePad = 20;        // floats per row of the replica merge (16 used; conflict-free vectors)
+constexpr int kMergePad = 36;        // floats per row of the replica merge (32 used; conflict-free vectors)
 
 template <int D>
 struct Smem {
@@ -88,7 +88,7 @@ struct Smem {
 // be cut anywhere: the pieces are partial softmaxes, joined by the second
 // kernel.  The host knows neither the lengths nor the query counts; every
 // CTA finds its range from them.
-constexpr int kItemCost = 3;
+constexpr int kItemCost = 4;
 struct Seq {
   int q0, n, len;
 };
@@ -1056,29 +1056,27 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int lin = it[4] * kBM + l_row, otok = lin / p.G;
       const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
-      for (int x = 0; x < D / 32; ++x) {
-        const int col = grp * (D / 2) + x * 16;
-        uint32_t v0[16], v1[16];
-        float o[16];
-        tmem_ld16(tO(0) + lane_off + col, v0);
-        tmem_ld16(tO(1) + lane_off + col, v1);
+      for (int x = 0; x < D / 64; ++x) {
+        const int col = grp * (D / 2) + x * 32;
+        uint32_t v0[32], v1[32];
+        float o[32];
+        tmem_ld32(tO(0) + lane_off + col, v0);
+        tmem_ld32(tO(1) + lane_off + col, v1);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
-        }
+        for (int e = 0; e < 32; ++e) o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
         if (nrep > 1) {
           if (rep > 0) {
             float4* d = reinterpret_cast<float4*>(merge + ((rep - 1) * per + l_row) * kMergePad);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           group_bar(2 + grp, kGroupWarps * 32);
           if (rep == 0) {
             for (int r = 0; r < nrep - 1; ++r) {
               const float4* d = reinterpret_cast<const float4*>(merge + (r * per + l_row) * kMergePad);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
+              for (int e = 0; e < 8; ++e) {
                 const float4 a = d[e];
                 o[4 * e] += a.x;
                 o[4 * e + 1] += a.y;
@@ -1087,20 +1085,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
               }
             }
           }
-          group_bar(2 + grp, kGroupWarps * 32);
+          if (x + 1 < D / 64) group_bar(2 + grp, kGroupWarps * 32);
         }
         if (writes) {
           if (whole) {
-            uint32_t u[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
             uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + col);
-            d[0] = make_uint4(u[0], u[1], u[2], u[3]);
-            d[1] = make_uint4(u[4], u[5], u[6], u[7]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t u[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                u[y] = BF ? pack_bf16x2(o[8 * e + 2 * y], o[8 * e + 2 * y + 1]) : pack_f16x2(o[8 * e + 2 * y], o[8 * e + 2 * y + 1]);
+              d[e] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
           } else {
             float4* d = reinterpret_cast<float4*>(piece_o(p, D, piece) + (size_t)l_row * D + col);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
         }
       }
