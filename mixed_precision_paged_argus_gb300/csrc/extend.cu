@@ -71,8 +71,8 @@ struct Smem {
   static constexpr int kOffML = kOffQScale + 2 * kBM * 4;
   static constexpr int kOffMerge = kOffML + 2 * kBM * 8;
   static constexpr int kOffBar = kOffMerge + 2 * 96 * kMergePad * 4;
-  // q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
-  static constexpr int kNumBars = 13 + 2 * kBatches;
+  // q_first, q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
+  static constexpr int kNumBars = 14 + 2 * kBatches;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
   static constexpr int kOffMisc = kOffItem + 2 * 32;
   static constexpr int kBytes = kOffMisc + 64;
@@ -135,6 +135,11 @@ __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& 
   return sum;
 }
 
+// units of one KV head's tiles 0 .. m-1
+__device__ __forceinline__ long long units_before(const EParams& p, const Seq& s, int m) {
+  return blocks_before(p, s, m) + (long long)kItemCost * m;
+}
+
 // a sequence's items, and its blocks
 struct Load {
   long long items, blocks;
@@ -172,24 +177,34 @@ struct Cursor {
   int left;                          // blocks of the range still ahead, this one counted
 
   // the item that unit `rest` of sequence b lies in, and the block there: the
-  // units in front of an item's blocks belong to its first
+  // units in front of an item's blocks belong to its first.  By a whole warp:
+  // 32 tiles are tried per step.
   __device__ __forceinline__ void start(const EParams& p, int b_, long long rest, int left_) {
+    const int lane = threadIdx.x & 31;
     b = b_;
     left = left_;
     s = load_seq(p, b);
     T = n_tiles(p, s);
-    const long long per = blocks_before(p, s, T) + (long long)kItemCost * T;
+    const long long per = units_before(p, s, T);
     h = (int)(rest / per);
     rest -= h * per;
-    int lo = 0, hi = T - 1;          // the last tile with units before it <= rest
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (blocks_before(p, s, mid) + (long long)kItemCost * mid <= rest) lo = mid;
-      else hi = mid - 1;
+    t = 0;                           // the last tile with units before it <= rest
+    for (int n = T; n > 1;) {
+      const int step = (n + 31) / 32, i = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, i < n && units_before(p, s, t + i) <= rest);
+      const int k = 31 - __clz(m);   // lane 0's tile is one
+      t += k * step;
+      n = min(step, n - k * step);
     }
-    t = lo;
-    blk = (int)max(0ll, rest - blocks_before(p, s, t) - (long long)kItemCost * (t + 1));
+    blk = (int)max(0ll, rest - units_before(p, s, t) - kItemCost);
     nb = tile_blocks(p, s, t);
+  }
+  // the first warp finds a CTA's start for all
+  __device__ __forceinline__ void store(volatile uint32_t* m) const {
+    m[0] = s.q0; m[1] = s.n; m[2] = s.len; m[3] = b; m[4] = h; m[5] = t; m[6] = T; m[7] = blk; m[8] = nb; m[9] = left;
+  }
+  __device__ __forceinline__ void load(const volatile uint32_t* m) {
+    s.q0 = m[0]; s.n = m[1]; s.len = m[2]; b = m[3]; h = m[4]; t = m[5]; T = m[6]; blk = m[7]; nb = m[8]; left = m[9];
   }
   __device__ __forceinline__ void next_item(const EParams& p) {
     blk = 0;
@@ -218,8 +233,8 @@ struct Cursor {
 // min(units, CTAs) CTAs have one.  By a whole warp.
 struct Range {
   long long total, w0;               // units of the call; the range's first
-  int n, n_blocks;                   // CTAs with a range; blocks of it
-  Place at;
+  int n;                             // CTAs with a range
+  Cursor at;                         // its first block; left: its blocks
 };
 __device__ __forceinline__ Range find_range(const EParams& p, int cta) {
   const int lane = threadIdx.x & 31;
@@ -235,8 +250,7 @@ __device__ __forceinline__ Range find_range(const EParams& p, int cta) {
   r.total = __shfl_sync(0xffffffffu, warp_scan(sum.blocks), 31) + kItemCost * items;
   r.n = (int)min((long long)p.n_ctas, r.total);
   r.w0 = 0;
-  r.n_blocks = 0;
-  r.at = {0, 0, 0, 0};
+  r.at = {};
   if (cta >= r.n) return r;
   const long long w[2] = {range_start(r.total, cta, r.n), range_start(r.total, cta + 1, r.n)};
   Place at[2] = {{p.B, 0, items, r.total}, {p.B, 0, items, r.total}};
@@ -262,23 +276,22 @@ __device__ __forceinline__ Range find_range(const EParams& p, int cta) {
   // blocks in front of each place
   long long blocks[2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 1; x >= 0; --x) {
     blocks[x] = at[x].units - kItemCost * at[x].items;
     if (at[x].b < p.B) {
-      Cursor c;
-      c.start(p, at[x].b, at[x].rest, 1);
-      blocks[x] += c.h * blocks_before(p, c.s, c.T) + blocks_before(p, c.s, c.t) + c.blk;
+      r.at.start(p, at[x].b, at[x].rest, 0);
+      blocks[x] += r.at.h * blocks_before(p, r.at.s, r.at.T) + blocks_before(p, r.at.s, r.at.t) + r.at.blk;
     }
   }
   r.w0 = w[0];
-  r.at = at[0];
-  r.n_blocks = (int)(blocks[1] - blocks[0]);   // fewer than 2^31 (checked on the host)
+  r.at.left = (int)(blocks[1] - blocks[0]);    // fewer than 2^31 (checked on the host)
   return r;
 }
 
 // The pieces of the range [w0, w1): the one that does not begin its item (the
 // first piece of a range at most) and the one that does not end it (the last)
-// lie in the workspace at 2 cta and 2 cta + 1.  The CTA behind the first cut of an item
+// lie in the workspace at 2 cta and 2 cta + 1, four dims by all rows by the next four
+// dims (a lane has a row).  The CTA behind the first cut of an item
 // describes it for the second kernel.
 struct Cut {
   int rows, last;                    // rows of the tile (0: nothing to join); last CTA of the item
@@ -349,6 +362,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 // 16 bytes of which `bytes` (16 or 0) are read, the rest zeros
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 __device__ __forceinline__ void prefetch_l2(const uint8_t* p, int bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
@@ -461,6 +479,62 @@ __device__ __forceinline__ void store_steps(uint4 (&v)[kSteps], uint32_t tile, i
   }
 }
 
+// Q tile of an item, by warps w = 0 .. nw - 1: row l of the tile goes to TMEM lanes
+// l, l + per, ...; zeros behind the last row.  All rows are on their way at
+// once (asynchronous copies, which write zeros where they read nothing); those
+// that become fp16 (TURN: from the tile at q_s to the one at q16) are turned by
+// the lanes that copied them.
+template <int D, bool TURN>
+__device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32_t q_s, uint32_t q16, float* q_scale, int w, int nw, int lane) {
+  constexpr int V = D / 8, RW = 32 / V;                  // vectors per row; rows of a warp's step
+  const int v = lane % V, r0 = w * RW + lane / V, RS = RW * nw;
+  const int lin0 = c.t * kBM, rows = min(kBM, c.s.n * p.G - lin0);
+  const int nrep = replicas(rows), per = kBM / nrep;
+  const int tok = (int)((uint32_t)(lin0 + r0) / (uint32_t)p.G), dt = RS / p.G, dg = RS - dt * p.G;
+  int g = lin0 + r0 - tok * p.G;
+  const uint16_t* src = p.q + (long long)(c.s.q0 + tok) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
+  const long long step = dt * p.qs + dg * D, wrap = p.qs - (long long)p.G * D;
+#pragma unroll 4
+  for (int l = r0; l < per; l += RS) {
+    const bool real = l < rows;
+    for (int r = 0; r < nrep; ++r) cp_async16(q_s + tile_off(l + r * per, v), real ? src : p.q, real ? 16 : 0);
+    src += step;
+    g += dg;
+    if (g >= p.G) {
+      g -= p.G;
+      src += wrap;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (TURN) {
+    // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
+#pragma unroll 4
+    for (int l = r0; l < per; l += RS) {
+      const uint4 q = lds16(q_s + tile_off(l, v));
+      // magnitudes of bf16 order like their bits
+      uint32_t mx = max_u16x2(max_u16x2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), max_u16x2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+#pragma unroll
+      for (int o = V / 2; o > 0; o >>= 1) mx = max_u16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const uint32_t ex = max(max(mx >> 16, mx & 0xFFFFu) >> 7, 15u);   // biased; from 15 on 2^(141 - ex) is a normal number
+      const float f = __uint_as_float((268 - ex) << 23);
+      const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+      uint32_t out[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float a, b;
+        f2_mul(a, b, __uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u), f, f);
+        out[e] = pack_f16x2(a, b);
+      }
+      for (int r = 0; r < nrep; ++r) {
+        sts16(q16 + tile_off(l + r * per, v), out[0], out[1], out[2], out[3]);
+        if (v == 0) q_scale[l + r * per] = __uint_as_float((ex - 14) << 23);   // 1 / f
+      }
+    }
+  }
+  fence_async();
+  __syncwarp();
+}
+
 // The lookup warp finds the pages of kBatch blocks at once, a lane per chunk
 // (lane = 8 * block + chunk): the two dependent reads (table, then scales) are
 // paid once per batch, and the batches behind are read meanwhile.
@@ -509,17 +583,18 @@ __device__ __forceinline__ void commit_lead(uint64_t* bar, uint32_t lead) {
 }
 
 // BF: q and out are bf16, else fp16.  W16: the call has a 16-bit pool.  The
-// operands are bf16 only where bf16 pages ask for it: over 8-bit pages alone a bf16
-// query becomes fp16 times a power of two per row (its 8 bits fit, and what is
+// operands are bf16 only in blocks that hold bf16 pages: elsewhere a bf16 query
+// is taken as fp16 times a power of two per row (its 8 bits fit, and what is
 // 2^-29 of the row's largest element does not count), because e4m3 codes
 // turn into fp16 with one conversion per pair, into bf16 with five operations,
-// and fp16 P has three more bits.
+// and fp16 P has three more bits.  A call with both kinds of pages keeps both
+// query tiles and chooses per block (mixed tiers: see the figures at the end of the file).
 template <int D, bool BF, bool W16>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   using SM = Smem<D>;
   constexpr int kTile = SM::kTile;
-  constexpr bool BFM = BF && W16;            // operand type of the MMAs
-  constexpr float kPBias = BFM ? 0.f : 7.f;  // fp16 P is stored as P * 2^7 (at most 2^15)
+  constexpr bool MIXED = BF && W16;          // bf16 or fp16 operands, block by block
+  constexpr float kPBias = 7.f;              // P is stored as P * 2^7 (fp16: at most 2^15)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {         // the swizzled tiles need it
     if (threadIdx.x == 0) {
@@ -528,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     }
     return;
   }
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);   // item k: buffer k & 1
+  uint64_t* q_first = reinterpret_cast<uint64_t*>(smem + SM::kOffBar);  // the first item's Q tile
+  uint64_t* q_full = q_first + 1;      // item k >= 1: buffer k & 1
   uint64_t* k_full = q_full + 2;       // block n: buffer n & 1
   uint64_t* pv_ready = k_full + 2;     // V tile and P written
   uint64_t* s_full = pv_ready + 2;     // scores complete; the K tile is free
@@ -537,10 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   uint64_t* drain = o_free + 2;
   uint64_t* looked = drain + 1;        // a batch of blocks is looked up
   uint64_t* used = looked + kBatches;  // nobody needs the batch any more
-  // [0] TMEM base, [1] error, [2] first sequence, [3] blocks of the range, [4..5] its first unit
-  // within that sequence
+  // [0] TMEM base, [1] error, [2..11] the range's first block (Cursor::store)
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
-  volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   // [2][8]: q0, n, len, h, t, first block, blocks of the piece, blocks of the item
   volatile int* items = reinterpret_cast<volatile int*>(smem + SM::kOffItem);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
@@ -553,15 +627,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     const Range r = find_range(p, blockIdx.x);
-    if (lane == 0) {
-      misc[2] = r.at.b;
-      misc64[2] = r.at.rest;
-      misc[3] = (uint32_t)r.n_blocks;
-    }
+    const Cursor& c = r.at;
+    if (lane == 0) c.store(misc + 2);
     Cut cut = {};
-    if (r.n_blocks > 0) {
-      Cursor c;
-      c.start(p, r.at.b, r.at.rest, 1);
+    if (c.left > 0) {
       const long long first = r.w0 - c.blk;              // the unit of the item's first block
       // this range begins inside an item's blocks, and is the first to
       if (c.blk > 0 && range_start(r.total, blockIdx.x - 1, r.n) <= first) {
@@ -584,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       mbar_init(&o_done[b], 1);
       mbar_init(&o_free[b], kSoftmaxWarps);
     }
+    mbar_init(q_first, kSoftmaxWarps);
     mbar_init(drain, 1);
     for (int k = 0; k < kBatches; ++k) {
       mbar_init(&looked[k], 1);
@@ -602,7 +672,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int n_blocks = (int)misc[3];
+  const int n_blocks = (int)misc[11];
+  auto describe_item = [&](int k, const Cursor& c, int nb) {
+    volatile int* it = items + 8 * (k & 1);
+    it[0] = c.s.q0; it[1] = c.s.n; it[2] = c.s.len; it[3] = c.h; it[4] = c.t; it[5] = c.blk; it[6] = nb; it[7] = c.nb;
+  };
+  // item k's Q tile and description are there
+  auto wait_q = [&](int k) {
+    return k == 0 ? wait(q_first, 0, &misc[1]) : wait(&q_full[k & 1], (uint32_t)((k - 1) >> 1) & 1, &misc[1]);
+  };
   auto tS = [tmem](int b) { return tmem + 128u * (uint32_t)b; };
   auto tO = [tmem](int b) { return tmem + 256u + 128u * (uint32_t)b; };
 
@@ -613,26 +691,31 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     // within an item: S0, S1, then per block i: P.V of i, S of i + 2.  The whole
     // warp runs this, one elected lane issues: descriptors and loop counters
     // stay warp-uniform, where the MMA instruction wants them.
-    constexpr uint32_t idQK = idesc_f16kind(BFM, false, kBN);
-    constexpr uint32_t idPV = idesc_f16kind(BFM, true, D);
+    constexpr uint32_t kBf16Operands = (1u << 7) | (1u << 10);
+    constexpr uint32_t idQK = idesc_f16kind(false, false, kBN), idPV = idesc_f16kind(false, true, D);
+    static_assert((idQK | kBf16Operands) == idesc_f16kind(true, false, kBN), "operand type bits");
+    // whether block n's operands are bf16
+    auto is_wide = [&](int n) { return MIXED ? __shfl_sync(0xffffffffu, chunks[(n % kSlots) * 8].w, 0) : 0u; };
     const uint32_t lead = elect_one();
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     // low words of the operand descriptors: address and leading offset in 16-byte units
     const uint32_t q_lo = sdesc_lo(smem_u32(smem + SM::kOffQ), kHalf), k_lo = sdesc_lo(smem_u32(smem + SM::kOffK), kHalf);
     const uint32_t v_lo = sdesc_lo(smem_u32(smem + SM::kOffV), kHalf);
     Cursor c;
-    c.start(p, misc[2], misc64[2], n_blocks);
+    c.load(misc + 2);
     int n0 = 0;                        // blocks before this item's
     bool ok = true;
     auto issue_s = [&](int n, int k) {
       const int b = n & 1;
       if (!__all_sync(0xffffffffu, wait(&k_full[b], (uint32_t)(n >> 1) & 1, &misc[1]))) return false;
       tc_fence_after();
-      const uint32_t ql = q_lo + (uint32_t)(k & 1) * (kTile / 16), kl = k_lo + (uint32_t)b * (kTile / 16);
+      const uint32_t wide = is_wide(n), id = idQK | (wide ? kBf16Operands : 0u);
+      // two items' tiles, or an item's bf16 and fp16 tile
+      const uint32_t ql = q_lo + (MIXED ? 1 - wide : (uint32_t)(k & 1)) * (kTile / 16), kl = k_lo + (uint32_t)b * (kTile / 16);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
-        mma_ss_lead(tm + 128u * b, ql + off, kl + off, idQK, kk > 0, lead);
+        mma_ss_lead(tm + 128u * b, ql + off, kl + off, id, kk > 0, lead);
       }
       commit_lead(&s_full[b], lead);
       return true;
@@ -641,17 +724,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int b = n & 1;
       if (!__all_sync(0xffffffffu, wait(&pv_ready[b], (uint32_t)(n >> 1) & 1, &misc[1]))) return false;
       tc_fence_after();
-      const uint32_t vl = v_lo + (uint32_t)b * (kTile / 16);
+      const uint32_t vl = v_lo + (uint32_t)b * (kTile / 16), id = idPV | (is_wide(n) ? kBf16Operands : 0u);
 #pragma unroll
       for (int kk = 0; kk < kBN / 16; ++kk)              // group g: keys 64 g ..., its P and its O
-        mma_ts_lead(tm + 256u + 128u * (kk >> 2), tm + 128u * b + (kk >> 2) * 64 + (kk & 3) * 8, vl + kk * 128, idPV,
+        mma_ts_lead(tm + 256u + 128u * (kk >> 2), tm + 128u * b + (kk >> 2) * 64 + (kk & 3) * 8, vl + kk * 128, id,
                     !first || (kk & 3) > 0, lead);
       commit_lead(&o_done[b], lead);
       return true;
     };
     for (int k = 0; ok && n0 < n_blocks; ++k) {
       const int nb = __shfl_sync(0xffffffffu, min(c.nb - c.blk, c.left), 0);
-      ok = __all_sync(0xffffffffu, wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]));
+      ok = __all_sync(0xffffffffu, wait_q(k));
       if (ok) ok = issue_s(n0, k);
       if (ok && nb > 1) ok = issue_s(n0 + 1, k);
       // the scores of this item may overtake the epilogue of the one before; its P.V may not
@@ -671,65 +754,26 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     }
   } else if (warp >= kQWarp0) {
     // ---------------------------------------------------------- Q tiles
-    // Row l of an item's tile goes to TMEM lanes l, l + per, ...; zeros behind the
-    // last row.  An item ahead of the softmax groups, so that nothing waits for it
-    // but the first.  All rows are on their way at once (asynchronous copies,
-    // which write zeros where they read nothing); rows that become fp16 are
-    // turned in place by the lanes that copied them.
-    constexpr int V = D / 8, RW = 32 / V, RS = RW * kQWarps;   // vectors per row; rows of a warp's step, of all warps'
-    const int v = lane % V, r0 = (warp - kQWarp0) * RW + lane / V;
+    // From the second item on, an item ahead of the softmax groups (which load the
+    // first one's themselves).
     Cursor c;
-    c.start(p, misc[2], misc64[2], n_blocks);
-    for (int k = 0; c.left > 0; ++k) {
-      const int buf = k & 1, nb = min(c.nb - c.blk, c.left);
-      if (k >= 2 && !__all_sync(0xffffffffu, wait(&o_free[buf], (uint32_t)((k - 2) >> 1) & 1, &misc[1]))) { misc[1] = 1; break; }
-      const int lin0 = c.t * kBM, rows = min(kBM, c.s.n * p.G - lin0);
-      const int nrep = replicas(rows), per = kBM / nrep;
-      if (warp == kQWarp0 && lane == 0) {
-        volatile int* it = items + 8 * buf;
-        it[0] = c.s.q0; it[1] = c.s.n; it[2] = c.s.len; it[3] = c.h; it[4] = c.t; it[5] = c.blk; it[6] = nb; it[7] = c.nb;
-      }
-      const uint32_t q_s = smem_u32(smem + SM::kOffQ + buf * kTile);
-      int g = (lin0 + r0) % p.G;
-      const uint16_t* src = p.q + (long long)(c.s.q0 + (lin0 + r0) / p.G) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
-      const long long next_token = p.qs - (long long)p.G * D;
-#pragma unroll 4
-      for (int l = r0; l < per; l += RS) {
-        const bool real = l < rows;
-        for (int r = 0; r < nrep; ++r) cp_async16(q_s + tile_off(l + r * per, v), real ? src : p.q, real ? 16 : 0);
-        src += RS * D;
-        for (g += RS; g >= p.G; g -= p.G) src += next_token;
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      if (BF && !BFM) {
-        // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
-#pragma unroll 2
-        for (int l = r0; l < per; l += RS) {
-          const uint4 q = lds16(q_s + tile_off(l, v));
-          uint32_t w[4] = {q.x, q.y, q.z, q.w}, mx = 0;   // magnitudes of bf16 order like their bits
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7FFF0000u, w[e] & 0x7FFF0000u));
-#pragma unroll
-          for (int o = V / 2; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const int ex = max((int)(mx >> 23), 15);        // biased; from 15 on 2^(141 - ex) is a normal number
-          const float f1 = __uint_as_float((uint32_t)(268 - ex) << 23);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * f1, __uint_as_float(w[e] & 0xFFFF0000u) * f1);
-          for (int r = 0; r < nrep; ++r) {
-            sts16(q_s + tile_off(l + r * per, v), w[0], w[1], w[2], w[3]);
-            if (v == 0) q_scale[buf * kBM + l + r * per] = 1.f / f1;
-          }
-        }
-      }
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[buf]);
+    c.load(misc + 2);
+    c.advance(p, min(c.nb - c.blk, c.left));
+    for (int k = 1; c.left > 0; ++k) {
+      const int nb = min(c.nb - c.blk, c.left);
+      // the buffer's last item is done: two items ago, or with two tiles per item the one before
+      const int last = MIXED ? k - 1 : k - 2;
+      if (last >= 0 && !__all_sync(0xffffffffu, wait(&o_free[last & 1], (uint32_t)(last >> 1) & 1, &misc[1]))) { misc[1] = 1; break; }
+      if (warp == kQWarp0 && lane == 0) describe_item(k, c, nb);
+      const uint32_t q_s = smem_u32(smem + SM::kOffQ + (MIXED ? 0 : (k & 1) * kTile));
+      load_q<D, BF>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale + (k & 1) * kBM, warp - kQWarp0, kQWarps, lane);
+      if (lane == 0) mbar_arrive(&q_full[k & 1]);
       c.advance(p, nb);
     }
   } else if (warp == kLookWarp) {
     // ---------------------------------------------------------- lookup
     Cursor c;
-    c.start(p, misc[2], misc64[2], n_blocks);
+    c.load(misc + 2);
     auto look = [&]() {
       Lookup k;
       k.codec = k.slot = -1;
@@ -802,10 +846,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       }
       const int at = (k % kBatches) * 32 + lane;
       const unsigned long long addr = reinterpret_cast<unsigned long long>(now.src);
-      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), now.state, 0);
+      // does the block (this lane's group of eight) hold a bf16 page?
+      const unsigned bf16s = __ballot_sync(0xffffffffu, MIXED && now.state && (now.state & 0xFF) <= ARGUS_BF16);
+      const uint32_t wide = (bf16s >> (lane & 24) & 0xFF) != 0;
+      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), now.state, wide);
       const float lvs = log2f(now.vs);   // 0: -inf
       // a scale far from 1: its chunk's sum is kept apart, and does not enter the others'
-      scales[at] = make_float4(now.ks < 0.f ? -1.f : now.ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / now.vs, 0.f);
+      scales[at] = make_float4(now.ks < 0.f ? -1.f : now.ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / now.vs, wide ? 1.f : 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&looked[k % kBatches]);
       ahead(now);
@@ -831,8 +878,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     };
     // the chunk on its way: all of it, or the first half of 16-bit rows of 128 dims
     auto fetch = [&](const uint4& d) {
-      state = ok ? d.z : 0;
-      if (!state) return;
+      state = ok ? d.z | d.w << 16 : 0;                  // codec | rows << 8 | bf16 operands << 16
+      if (!(state & 0xFF00)) return;
       src = reinterpret_cast<const uint8_t*>((unsigned long long)d.y << 32 | d.x) + v_off;
       if (W16 && (state & 0xFF) <= ARGUS_BF16) {
         src += v_off;
@@ -848,19 +895,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if (i >= 2 && ok) ok = wait(&empty[b], ((i >> 1) - 1) & 1, &misc[1]);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
-        const int codec = state & 0xFF, n_rows = state >> 8;
+        const int codec = state & 0xFF, n_rows = (state >> 8) & 0xFF;
+        const bool wide = MIXED && (state >> 16);
         const uint32_t to = tiles + b * kTile;
         if (n_rows > 0 || is_v) {                      // a chunk without rows: K is masked, V is set to zero
           if (W16 && codec <= ARGUS_BF16) {
-            store_steps<D, BFM, ARGUS_BF16>(v, to, lane, n_rows, 0);
+            store_steps<D, MIXED, ARGUS_BF16>(v, to, lane, n_rows, 0);
             if (D == 128) {
               if (n_rows > 0) load_steps<D, D / 8>(v, src, lane, kSteps);
-              store_steps<D, BFM, ARGUS_BF16>(v, to, lane, n_rows, kSteps);
+              store_steps<D, MIXED, ARGUS_BF16>(v, to, lane, n_rows, kSteps);
             }
+          } else if (MIXED && wide) {
+            if (codec == ARGUS_INT8) store_steps<D, true, ARGUS_INT8>(v, to, lane, n_rows, 0);
+            else store_steps<D, true, ARGUS_FP8_E4M3>(v, to, lane, n_rows, 0);
           } else if (codec == ARGUS_INT8) {
-            store_steps<D, BFM, ARGUS_INT8>(v, to, lane, n_rows, 0);
+            store_steps<D, false, ARGUS_INT8>(v, to, lane, n_rows, 0);
           } else {
-            store_steps<D, BFM, ARGUS_FP8_E4M3>(v, to, lane, n_rows, 0);
+            store_steps<D, false, ARGUS_FP8_E4M3>(v, to, lane, n_rows, 0);
           }
         }
         fetch(next);
@@ -885,14 +936,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const uint32_t sO = tO(grp) + lane_off;
     float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge) + grp * 96 * kMergePad;
     int n0 = 0;
+    {
+      Cursor c;
+      c.load(misc + 2);
+      if (threadIdx.x == 0) describe_item(0, c, min(c.nb - c.blk, c.left));
+      const uint32_t q_s = smem_u32(smem + SM::kOffQ);
+      load_q<D, BF>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale, warp, kSoftmaxWarps, lane);
+      if (lane == 0) mbar_arrive(q_first);
+    }
     for (int k = 0; n0 < n_blocks; ++k) {
-      bool alive = wait(&q_full[k & 1], (uint32_t)(k >> 1) & 1, &misc[1]);
+      bool alive = wait_q(k);
       if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) { misc[1] = 1; break; }   // all leave, or none
       const volatile int* it = items + 8 * (k & 1);
       const int nb = it[6], k_first = it[5] * kBN;
       const int rows = min(kBM, it[1] * p.G - it[4] * kBM);
       const int nrep = replicas(rows), per = kBM / nrep;
-      const float qf = (BF && !BFM) ? q_scale[(k & 1) * kBM + tl] : 1.f;
+      const float q_fac = BF ? q_scale[(k & 1) * kBM + tl] : 1.f;   // undoes the fp16 query's power of two
       const int l_row = tl & (per - 1);                // row within the tile
       const int rep = tl / per;                        // this lane's replica: chunks c0 ... of the group's four
       const int c0 = 4 * grp + rep * (4 / nrep);
@@ -921,6 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         constexpr int N = decltype(chunks_of)::value;
         const uint32_t sS = tS(n & 1) + lane_off;
         const float4* sc = scales + (n % kSlots) * 8 + c0;
+        const bool wide = MIXED && sc[0].w != 0.f;     // the same for the block's chunks
+        const float qf = wide ? 1.f : q_fac;
         float v[N][16];
 #pragma unroll
         for (int x = 0; x < N; ++x) tmem_ld16(sS + (c0 + x) * 16, reinterpret_cast<uint32_t(&)[16]>(v[x]));
@@ -999,7 +1060,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
             p0 = fast_exp2(x0);
             p1 = fast_exp2(x1);
             f2_add(la, lb, la, lb, p0, p1);
-            o[e] = BFM ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            o[e] = wide ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
           }
           l = fmaf(la + lb, s.z, l);
           tmem_st8(sP + (c0 - 4 * grp + x) * 8, o);
@@ -1087,21 +1148,43 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           }
           if (x + 1 < D / 64) group_bar(2 + grp, kGroupWarps * 32);
         }
-        if (writes) {
-          if (whole) {
+        if (x + 1 == D / 64 && nrep == 1) {
+          // the last of O, (m, l) and the description is in registers: the next
+          // item's P.V need not wait for the stores
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&o_free[k & 1]);
+        }
+        if (!whole) {
+          // columns by rows: 32 lanes, 512 bytes
+          float4* d = reinterpret_cast<float4*>(piece_o(p, D, piece)) + (col / 4) * kBM + l_row;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (writes) d[e * kBM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else {
+          uint32_t u[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
+          if (nrep > 1) {
             uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + col);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t u[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-                u[y] = BF ? pack_bf16x2(o[8 * e + 2 * y], o[8 * e + 2 * y + 1]) : pack_f16x2(o[8 * e + 2 * y], o[8 * e + 2 * y + 1]);
-              d[e] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            for (int e = 0; e < 4; ++e)
+              if (writes) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
           } else {
-            float4* d = reinterpret_cast<float4*>(piece_o(p, D, piece) + (size_t)l_row * D + col);
+            // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
+            uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = e * 8 + lane / 4;
+              const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
+              const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
+              if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
+            }
+            __syncwarp();
           }
         }
       }
@@ -1113,7 +1196,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       // O, (m, l), the merge area and the item's description have been read
       tc_fence_before();
       if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) break;   // all leave, or none
-      if (lane == 0) mbar_arrive(&o_free[k & 1]);
+      if (lane == 0 && nrep > 1) mbar_arrive(&o_free[k & 1]);
       n0 += nb;
     }
   }
@@ -1128,68 +1211,58 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   }
 }
 
-// Joins the pieces of the items that the ranges cut: block x the item that
-// range x + 1 is the first to cut, a warp per row, lanes over the pieces for their
-// weights and over the dims for the sum.
-constexpr int kJoinWarps = 8, kJoinBlocks = 4;
+// Joins the pieces of the items that the ranges cut: blocks (x, .) the item that
+// range x + 1 is the first to cut; a warp per 32 rows (a row per lane) and four dims.
+constexpr int kJoinWarps = 8, kJoinAhead = 8;
 template <int D, bool BF>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const EParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, cta = blockIdx.x + 1;
   const Cut cut = cuts(p, D)[cta];
-  constexpr int L = D / 4, PER = 32 / L;                 // lanes of a row; pieces of a step
-  const int part = lane / L, col = (lane % L) * 4;
+  const int unit = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), col = unit % (D / 4), row = unit / (D / 4) * 32 + lane;
   const int n = cut.last - cta + 2;                      // pieces: 2 (cta - 1) + 1, 2 cta, 2 (cta + 1), ...
-  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < cut.rows; row += kJoinWarps * kJoinBlocks) {
-    float M = -INFINITY, sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = 0; x0 < n; x0 += 32) {
-      const int x = x0 + lane, piece = x == 0 ? 2 * (cta - 1) + 1 : 2 * (cta - 1 + x);
-      const float lse = x < n ? piece_lse(p, D, piece)[row] : -INFINITY;
-      float top = lse;
+  if (row >= cut.rows) return;
+  float M = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int x0 = 0; x0 < n; x0 += kJoinAhead) {
+    float l[kJoinAhead];
+    float4 v[kJoinAhead];
+    float top = M;
 #pragma unroll
-      for (int y = 16; y > 0; y >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
-      top = fmaxf(top, M);
-      if (top == -INFINITY) continue;                    // nothing visible so far
-      const float r = fast_exp2(M - top), w = fast_exp2(lse - top);   // 2^-inf = 0
-      M = top;
-      sum = sum * r + w;                                 // this lane's pieces
-      o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
-      const int m = min(32, n - x0);
-#pragma unroll 4
-      for (int y = 0; y < m; y += PER) {
-        const int at = y + part;                         // below 32: PER divides 32
-        const float wy = __shfl_sync(0xffffffffu, w, at);
-        const int pc = x0 + at == 0 ? 2 * (cta - 1) + 1 : 2 * (cta - 1 + x0 + at);
-        if (at < m && wy > 0.f) {
-          const float4 v = *reinterpret_cast<const float4*>(piece_o(p, D, pc) + (size_t)row * D + col);
-          o.x = fmaf(wy, v.x, o.x);
-          o.y = fmaf(wy, v.y, o.y);
-          o.z = fmaf(wy, v.z, o.z);
-          o.w = fmaf(wy, v.w, o.w);
-        }
+    for (int y = 0; y < kJoinAhead; ++y) {
+      const int x = x0 + y, piece = x == 0 ? 2 * (cta - 1) + 1 : 2 * (cta - 1 + x);
+      l[y] = -INFINITY;
+      v[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x < n) {
+        l[y] = piece_lse(p, D, piece)[row];
+        v[y] = reinterpret_cast<const float4*>(piece_o(p, D, piece))[col * kBM + row];
       }
     }
 #pragma unroll
-    for (int y = 16; y > 0; y >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, y);
+    for (int y = 0; y < kJoinAhead; ++y) top = fmaxf(top, l[y]);
+    if (top == -INFINITY) continue;                      // nothing visible so far
+    const float r = fast_exp2(M - top);                  // 2^-inf = 0
+    M = top;
+    sum *= r;
+    o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 #pragma unroll
-    for (int y = L; y < 32; y <<= 1) {
-      o.x += __shfl_xor_sync(0xffffffffu, o.x, y);
-      o.y += __shfl_xor_sync(0xffffffffu, o.y, y);
-      o.z += __shfl_xor_sync(0xffffffffu, o.z, y);
-      o.w += __shfl_xor_sync(0xffffffffu, o.w, y);
+    for (int y = 0; y < kJoinAhead; ++y) {
+      const float w = fast_exp2(l[y] - top);
+      sum += w;
+      o.x = fmaf(w, v[y].x, o.x);
+      o.y = fmaf(w, v[y].y, o.y);
+      o.z = fmaf(w, v[y].z, o.z);
+      o.w = fmaf(w, v[y].w, o.w);
     }
-    const int lin = cut.row0 + row, tok = lin / p.G;
-    const size_t orow = (size_t)(cut.q0 + tok) * p.Hq + cut.head0 + (lin - tok * p.G);
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    if (part == 0) {
-      uint2 u;
-      u.x = BF ? pack_bf16x2(o.x * inv, o.y * inv) : pack_f16x2(o.x * inv, o.y * inv);
-      u.y = BF ? pack_bf16x2(o.z * inv, o.w * inv) : pack_f16x2(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(p.out + orow * D + col) = u;
-    }
-    if (lane == 0 && p.lse2) p.lse2[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
   }
+  const int lin = cut.row0 + row, tok = lin / p.G;
+  const size_t orow = (size_t)(cut.q0 + tok) * p.Hq + cut.head0 + (lin - tok * p.G);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  uint2 u;
+  u.x = BF ? pack_bf16x2(o.x * inv, o.y * inv) : pack_f16x2(o.x * inv, o.y * inv);
+  u.y = BF ? pack_bf16x2(o.z * inv, o.w * inv) : pack_f16x2(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(p.out + orow * D + 4 * col) = u;
+  if (col == 0 && p.lse2) p.lse2[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
 }
 
 static argus_status check(const argus_extend_args* a) {
@@ -1260,7 +1333,7 @@ static argus_status launch(const EParams& p, cudaStream_t s) {
   extend_kernel<D, BF, W16><<<p.n_ctas, kThreads, smem, s>>>(p);
   if (p.n_ctas > 1) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_ctas - 1, kJoinBlocks);
+    cfg.gridDim = dim3(p.n_ctas - 1, kBM / 32 * (D / 4) / kJoinWarps);
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute at = {};
