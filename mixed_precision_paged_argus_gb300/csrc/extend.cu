@@ -507,27 +507,45 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (TURN) {
-    // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are neighbours
-#pragma unroll 4
-    for (int l = r0; l < per; l += RS) {
-      const uint4 q = lds16(q_s + tile_off(l, v));
-      // magnitudes of bf16 order like their bits
-      uint32_t mx = max_u16x2(max_u16x2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), max_u16x2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+    // the row's largest magnitude comes to [2^14, 2^15); its D / 8 lanes are
+    // neighbours.  Four rows at once: one after the other, their reads,
+    // exchanges and stores would only wait for each other.
+    constexpr int R = 4;
+    for (int l0 = r0; l0 < per; l0 += R * RS) {
+      uint4 q[R];
+      uint32_t mx[R];
 #pragma unroll
-      for (int o = V / 2; o > 0; o >>= 1) mx = max_u16x2(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const uint32_t ex = max(max(mx >> 16, mx & 0xFFFFu) >> 7, 15u);   // biased; from 15 on 2^(141 - ex) is a normal number
-      const float f = __uint_as_float((268 - ex) << 23);
-      const uint32_t in[4] = {q.x, q.y, q.z, q.w};
-      uint32_t out[4];
+      for (int x = 0; x < R; ++x) q[x] = lds16(q_s + tile_off(min(l0 + x * RS, kBM - 1), v));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a, b;
-        f2_mul(a, b, __uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xFFFF0000u), f, f);
-        out[e] = pack_f16x2(a, b);
+      for (int x = 0; x < R; ++x)                        // magnitudes of bf16 order like their bits
+        mx[x] = max_u16x2(max_u16x2(q[x].x & 0x7FFF7FFFu, q[x].y & 0x7FFF7FFFu), max_u16x2(q[x].z & 0x7FFF7FFFu, q[x].w & 0x7FFF7FFFu));
+#pragma unroll
+      for (int o = V / 2; o > 0; o >>= 1) {
+#pragma unroll
+        for (int x = 0; x < R; ++x) mx[x] = max_u16x2(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
+      }
+      uint32_t ex[R];
+#pragma unroll
+      for (int x = 0; x < R; ++x) {
+        ex[x] = max(max(mx[x] >> 16, mx[x] & 0xFFFFu) >> 7, 15u);   // biased; from 15 on 2^(141 - ex) is a normal number
+        const float f = __uint_as_float((268 - ex[x]) << 23);
+        uint32_t* w = reinterpret_cast<uint32_t*>(&q[x]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float a, b;
+          f2_mul(a, b, __uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u), f, f);
+          w[e] = pack_f16x2(a, b);
+        }
       }
       for (int r = 0; r < nrep; ++r) {
-        sts16(q16 + tile_off(l + r * per, v), out[0], out[1], out[2], out[3]);
-        if (v == 0) q_scale[l + r * per] = __uint_as_float((ex - 14) << 23);   // 1 / f
+#pragma unroll
+        for (int x = 0; x < R; ++x) {
+          const int l = l0 + x * RS;
+          if (l < per) {
+            sts16(q16 + tile_off(l + r * per, v), q[x].x, q[x].y, q[x].z, q[x].w);
+            if (v == 0) q_scale[l + r * per] = __uint_as_float((ex[x] - 14) << 23);   // 1 / f
+          }
+        }
       }
     }
   }
