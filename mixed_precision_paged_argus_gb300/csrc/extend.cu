@@ -162,14 +162,12 @@ __device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
   return x;
 }
 
-__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return total * cta / n_ctas; }
+// a / b, both >= 0: in 32 bits where they fit
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
-// A place in the work list: unit `rest` of sequence b (b = B: the end), and the
-// items and units of the sequences before.
-struct Place {
-  int b;
-  long long rest, items, units;
-};
+__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return divide(total * cta, n_ctas); }
 
 struct Cursor {
   Seq s;
@@ -186,7 +184,7 @@ struct Cursor {
     s = load_seq(p, b);
     T = n_tiles(p, s);
     const long long per = units_before(p, s, T);
-    h = (int)(rest / per);
+    h = (int)divide(rest, per);
     rest -= h * per;
     t = 0;                           // the last tile with units before it <= rest
     for (int n = T; n > 1;) {
@@ -201,10 +199,10 @@ struct Cursor {
   }
   // the first warp finds a CTA's start for all
   __device__ __forceinline__ void store(volatile uint32_t* m) const {
-    m[0] = s.q0; m[1] = s.n; m[2] = s.len; m[3] = b; m[4] = h; m[5] = t; m[6] = T; m[7] = blk; m[8] = nb; m[9] = left;
+    m[0] = s.q0; m[1] = s.n; m[2] = s.len; m[3] = b; m[4] = h; m[5] = t; m[6] = T; m[7] = blk; m[8] = nb;
   }
-  __device__ __forceinline__ void load(const volatile uint32_t* m) {
-    s.q0 = m[0]; s.n = m[1]; s.len = m[2]; b = m[3]; h = m[4]; t = m[5]; T = m[6]; blk = m[7]; nb = m[8]; left = m[9];
+  __device__ __forceinline__ void load(const volatile uint32_t* m, int blocks) {
+    s.q0 = m[0]; s.n = m[1]; s.len = m[2]; b = m[3]; h = m[4]; t = m[5]; T = m[6]; blk = m[7]; nb = m[8]; left = blocks;
   }
   __device__ __forceinline__ void next_item(const EParams& p) {
     blk = 0;
@@ -229,14 +227,15 @@ struct Cursor {
   }
 };
 
-// A CTA's range: where it begins, and its number of blocks.  Only the first
-// min(units, CTAs) CTAs have one.  By a whole warp.
-struct Range {
-  long long total, w0;               // units of the call; the range's first
+// Where the range of a CTA begins: its first unit, the block there (left = 0) and
+// the number of blocks in front of it.  Only the first min(units, CTAs) CTAs have
+// a range; behind the last one's lies the end.  By a whole warp.
+struct Boundary {
+  long long total, unit, blocks;     // units of the call
   int n;                             // CTAs with a range
-  Cursor at;                         // its first block; left: its blocks
+  Cursor at;
 };
-__device__ __forceinline__ Range find_range(const EParams& p, int cta) {
+__device__ __forceinline__ Boundary find_boundary(const EParams& p, int cta) {
   const int lane = threadIdx.x & 31;
   const Load first = lane < p.B ? seq_load(p, lane) : Load{0, 0};
   Load sum = first;
@@ -245,46 +244,35 @@ __device__ __forceinline__ Range find_range(const EParams& p, int cta) {
     sum.items += x.items;
     sum.blocks += x.blocks;
   }
-  const long long items = __shfl_sync(0xffffffffu, warp_scan(sum.items), 31);
-  Range r;
-  r.total = __shfl_sync(0xffffffffu, warp_scan(sum.blocks), 31) + kItemCost * items;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum.items += __shfl_xor_sync(0xffffffffu, sum.items, o);
+    sum.blocks += __shfl_xor_sync(0xffffffffu, sum.blocks, o);
+  }
+  Boundary r;
+  r.total = sum.units();
   r.n = (int)min((long long)p.n_ctas, r.total);
-  r.w0 = 0;
+  r.unit = r.total;
+  r.blocks = sum.blocks;
   r.at = {};
   if (cta >= r.n) return r;
-  const long long w[2] = {range_start(r.total, cta, r.n), range_start(r.total, cta + 1, r.n)};
-  Place at[2] = {{p.B, 0, items, r.total}, {p.B, 0, items, r.total}};
-  Place before = {0, 0, 0, 0};
+  r.unit = range_start(r.total, cta, r.n);
+  Load before = {0, 0};
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const Load mine = b0 == 0 ? first : b0 + lane < p.B ? seq_load(p, b0 + lane) : Load{0, 0};
-    const long long units = warp_scan(mine.units()), its = warp_scan(mine.items);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const unsigned hit = __ballot_sync(0xffffffffu, before.units + units > w[x]);
-      if (hit && at[x].b == p.B) {
-        const int src = __ffs(hit) - 1;
-        at[x].b = b0 + src;
-        at[x].units = before.units + __shfl_sync(0xffffffffu, units - mine.units(), src);
-        at[x].items = before.items + __shfl_sync(0xffffffffu, its - mine.items, src);
-        at[x].rest = w[x] - at[x].units;
-      }
+    const Load incl = {warp_scan(mine.items), warp_scan(mine.blocks)};
+    const unsigned hit = __ballot_sync(0xffffffffu, before.units() + incl.units() > r.unit);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      before.items += __shfl_sync(0xffffffffu, incl.items - mine.items, src);
+      before.blocks += __shfl_sync(0xffffffffu, incl.blocks - mine.blocks, src);
+      r.at.start(p, b0 + src, r.unit - before.units(), 0);
+      r.blocks = before.blocks + r.at.h * blocks_before(p, r.at.s, r.at.T) + blocks_before(p, r.at.s, r.at.t) + r.at.blk;
+      break;
     }
-    if (at[0].b < p.B && at[1].b < p.B) break;
-    before.units += __shfl_sync(0xffffffffu, units, 31);
-    before.items += __shfl_sync(0xffffffffu, its, 31);
+    before.items += __shfl_sync(0xffffffffu, incl.items, 31);
+    before.blocks += __shfl_sync(0xffffffffu, incl.blocks, 31);
   }
-  // blocks in front of each place
-  long long blocks[2];
-#pragma unroll
-  for (int x = 1; x >= 0; --x) {
-    blocks[x] = at[x].units - kItemCost * at[x].items;
-    if (at[x].b < p.B) {
-      r.at.start(p, at[x].b, at[x].rest, 0);
-      blocks[x] += r.at.h * blocks_before(p, r.at.s, r.at.T) + blocks_before(p, r.at.s, r.at.t) + r.at.blk;
-    }
-  }
-  r.w0 = w[0];
-  r.at.left = (int)(blocks[1] - blocks[0]);    // fewer than 2^31 (checked on the host)
   return r;
 }
 
@@ -631,8 +619,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   uint64_t* drain = o_free + 2;
   uint64_t* looked = drain + 1;        // a batch of blocks is looked up
   uint64_t* used = looked + kBatches;  // nobody needs the batch any more
-  // [0] TMEM base, [1] error, [2..11] the range's first block (Cursor::store)
+  // [0] TMEM base, [1] error, [2..11] the range's first block (Cursor::store), [12..15] the
+  // blocks in front of the range's begin and end
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
+  volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
   // [2][8]: q0, n, len, h, t, first block, blocks of the piece, blocks of the item
   volatile int* items = reinterpret_cast<volatile int*>(smem + SM::kOffItem);
   float2* ml = reinterpret_cast<float2*>(smem + SM::kOffML);            // [group][lane]: (m, l)
@@ -643,26 +633,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
 
   // the second kernel may be put in place; it waits for this one's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 0) {
-    const Range r = find_range(p, blockIdx.x);
-    const Cursor& c = r.at;
-    if (lane == 0) c.store(misc + 2);
-    Cut cut = {};
-    if (c.left > 0) {
-      const long long first = r.w0 - c.blk;              // the unit of the item's first block
-      // this range begins inside an item's blocks, and is the first to
-      if (c.blk > 0 && range_start(r.total, blockIdx.x - 1, r.n) <= first) {
-        cut.rows = min(kBM, c.s.n * p.G - c.t * kBM);
-        cut.last = blockIdx.x;
-        while (cut.last + 1 < r.n && range_start(r.total, cut.last + 1, r.n) < first + c.nb) ++cut.last;
-        cut.q0 = c.s.q0;
-        cut.row0 = c.t * kBM;
-        cut.head0 = c.h * p.G;
+  if (warp < 2) {
+    // the range's begin and end, a warp each
+    const Boundary r = find_boundary(p, blockIdx.x + warp);
+    if (lane == 0) misc64[6 + warp] = r.blocks;
+    if (warp == 0) {
+      const Cursor& c = r.at;
+      if (lane == 0) c.store(misc + 2);
+      Cut cut = {};
+      if ((int)blockIdx.x < r.n && c.blk > 0) {
+        const long long first = r.unit - c.blk;          // the unit of the item's first block
+        // this range begins inside an item's blocks; is it the first to?
+        if (range_start(r.total, blockIdx.x - 1, r.n) <= first) {
+          cut.rows = min(kBM, c.s.n * p.G - c.t * kBM);
+          cut.last = blockIdx.x;
+          while (cut.last + 1 < r.n && range_start(r.total, cut.last + 1, r.n) < first + c.nb) ++cut.last;
+          cut.q0 = c.s.q0;
+          cut.row0 = c.t * kBM;
+          cut.head0 = c.h * p.G;
+        }
       }
+      if (lane == 0) cuts(p, D)[blockIdx.x] = cut;
     }
-    if (lane == 0) cuts(p, D)[blockIdx.x] = cut;
   }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 64) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&q_full[b], kQWarps);
       mbar_init(&k_full[b], kLoadWarps / 2);
@@ -690,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  const int n_blocks = (int)misc[11];
+  const int n_blocks = (int)(misc64[7] - misc64[6]);   // fewer than 2^31 (checked on the host)
   auto describe_item = [&](int k, const Cursor& c, int nb) {
     volatile int* it = items + 8 * (k & 1);
     it[0] = c.s.q0; it[1] = c.s.n; it[2] = c.s.len; it[3] = c.h; it[4] = c.t; it[5] = c.blk; it[6] = nb; it[7] = c.nb;
@@ -720,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const uint32_t q_lo = sdesc_lo(smem_u32(smem + SM::kOffQ), kHalf), k_lo = sdesc_lo(smem_u32(smem + SM::kOffK), kHalf);
     const uint32_t v_lo = sdesc_lo(smem_u32(smem + SM::kOffV), kHalf);
     Cursor c;
-    c.load(misc + 2);
+    c.load(misc + 2, n_blocks);
     int n0 = 0;                        // blocks before this item's
     bool ok = true;
     auto issue_s = [&](int n, int k) {
@@ -775,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     // From the second item on, an item ahead of the softmax groups (which load the
     // first one's themselves).
     Cursor c;
-    c.load(misc + 2);
+    c.load(misc + 2, n_blocks);
     c.advance(p, min(c.nb - c.blk, c.left));
     for (int k = 1; c.left > 0; ++k) {
       const int nb = min(c.nb - c.blk, c.left);
@@ -791,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   } else if (warp == kLookWarp) {
     // ---------------------------------------------------------- lookup
     Cursor c;
-    c.load(misc + 2);
+    c.load(misc + 2, n_blocks);
     auto look = [&]() {
       Lookup k;
       k.codec = k.slot = -1;
@@ -956,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     int n0 = 0;
     {
       Cursor c;
-      c.load(misc + 2);
+      c.load(misc + 2, n_blocks);
       if (threadIdx.x == 0) describe_item(0, c, min(c.nb - c.blk, c.left));
       const uint32_t q_s = smem_u32(smem + SM::kOffQ);
       load_q<D, BF>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale, warp, kSoftmaxWarps, lane);
