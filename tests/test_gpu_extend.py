@@ -258,3 +258,103 @@ def test_streams_graphs_and_repeats():
         if not shift:
             assert torch.equal(out, ref) and torch.equal(lse, rl)
         check(c, out, lse, True)
+
+
+@pytest.mark.parametrize("dtype,with16", [(W.FP16, False), (W.BF16, False), (W.BF16, True)])
+@pytest.mark.parametrize("codec", [F8, I8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_code_is_exact(D, codec, dtype, with16):
+    """Sequences of one token: the output is that token's V, code times scale, rounded once.  Four sequences hold
+    every code (without e4m3's NaN); with16: the call has a 16-bit page in the same block (bf16 operands)."""
+    P, B = 16, 512 // D
+    codes = np.arange(256, dtype=np.uint8)
+    if codec == F8:
+        codes[[0x7F, 0xFF]] = 0
+    elif codec == I8:
+        codes[0x80] = 0          # -128 is not a code
+    pool = argus.Pool.empty(codec, B, 1, P, D, device=DEV, zero=True)
+    pool.codes[:, 1, 0, 0] = torch.from_numpy(np.resize(codes, (B, D))).to(DEV)
+    pool.meta.fill_(0.5)
+    pools = [pool]
+    table, pc = np.arange(B, dtype=np.int32)[:, None], np.full((B, 1), codec, np.uint8)
+    if with16:                   # an empty 16-bit page in front: V = 0 and K = 0, so each of two keys weighs 1/2
+        pools.append(argus.Pool.empty(dtype, 1, 1, P, D, device=DEV, zero=True))
+        table, pc = np.concatenate([np.zeros_like(table), table], 1), np.concatenate([np.full_like(pc, dtype), pc], 1)
+    lens = [P + 1 if with16 else 1] * B
+    q = torch.ones((B, 1, D), dtype=torch.float16 if dtype == W.FP16 else torch.bfloat16, device=DEV)
+    out = torch.empty_like(q)
+    args = argus.extend_args(argus.geom(1, 1, D, P), q, torch.arange(B + 1, dtype=torch.int32, device=DEV), pools,
+                             torch.from_numpy(pc).to(DEV), torch.from_numpy(table).to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV),
+                             table.shape[1], 1.0, out)
+    argus.paged_extend_attn(args, torch.empty(argus.extend_workspace_bytes(args), dtype=torch.uint8, device=DEV))
+    v = torch.from_numpy(np.resize(codes, (B, D)))
+    want = (v.view(torch.float8_e4m3fn).float() if codec == F8 else v.view(torch.int8).float()) * 0.5
+    if with16:
+        want = want / (P + 1)
+    got = out[:, 0].float().cpu()
+    # alone: exact but for the output's rounding; among P + 1 keys with p = 1: 1 / 17 in fp32 as well
+    u = torch.finfo(out.dtype).eps / 2
+    assert torch.all((got - want).abs() <= want.abs() * (u + 2.0 ** -21) + torch.finfo(out.dtype).smallest_normal * u)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(1000 + seed)
+    B = int(rng.integers(1, 9))
+    Hkv, G = int(rng.integers(1, 4)), int(rng.integers(1, 9))
+    D, P = int(rng.choice([64, 128])), int(rng.choice([16, 32, 48, 80]))
+    dtype = int(rng.choice([W.FP16, W.BF16]))
+    lens = [int(x) for x in rng.integers(0, 700, B)]
+    new = [int(rng.integers(0, min(90, n + 3) + 1)) for n in lens]
+    codecs = [c for c in (dtype, F8, I8) if rng.random() < 0.6] or [F8]
+    c = make(G * Hkv, Hkv, D, P, lens, new, codecs, dtype, seed=300 + seed)
+    if int(c.q_start[-1]) == 0:
+        return
+    spoil_tails(c)
+    for causal in (True, False):
+        out, lse = run(c, causal)
+        check(c, out, lse, causal)
+
+
+def test_many_short_items_and_one_long():
+    """The work list cuts long items and packs short ones: both in one call, causal and full."""
+    c = make(8, 1, 64, 16, [6000] + [30] * 40, [40] + [30] * 40, [F8, W.FP16], W.FP16, seed=500)
+    for causal in (True, False):
+        out, lse = run(c, causal)
+        check(c, out, lse, causal)
+
+
+def test_two_streams_with_a_workspace_each():
+    a = make(8, 2, 128, 16, [900, 40], [9, 40], [F8], W.BF16, seed=510)
+    b = make(8, 2, 128, 16, [70, 1500], [1, 130], [I8, W.BF16], W.BF16, seed=511)
+    refs = [run(c, True) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = []
+    for c, s in zip((a, b), streams):
+        out, lse = torch.full_like(c.q, float("nan")), torch.full(c.q.shape[:2], float("nan"), device=DEV)
+        args = argus.extend_args(c.g, c.q, torch.from_numpy(c.q_start).to(DEV), c.pools, c.d_codec, c.d_table, c.d_lens,
+                                 c.max_pages, c.scale, out, lse2_out=lse)
+        calls.append((args, torch.empty(argus.extend_workspace_bytes(args), dtype=torch.uint8, device=DEV), s, out, lse))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for args, ws, s, _, _ in calls:
+            argus.paged_extend_attn(args, ws, stream=s)
+    torch.cuda.synchronize()
+    for (ref, rl), (_, _, _, out, lse) in zip(refs, calls):
+        assert torch.equal(out, ref) and torch.equal(lse, rl)
+
+
+def test_offsets_beyond_four_gigabytes():
+    """Slots at the end of an FP8 pool of 5 GB, and query rows of a strided tensor."""
+    Hkv, P, D = 8, 16, 128
+    small = make(16, Hkv, D, P, [77, 160], [5, 2], [F8], W.BF16, seed=520)
+    ref, rl = run(small, True)
+    n_slots = (5 << 30) // (2 * Hkv * P * D)
+    codes = torch.empty((n_slots, 2, Hkv, P, D), dtype=torch.uint8, device=DEV)
+    meta = torch.empty((n_slots, 2, Hkv), dtype=torch.float32, device=DEV)
+    pool = small.pools[0]
+    codes[-pool.n_slots:], meta[-pool.n_slots:] = pool.codes, pool.meta
+    small.pools = [argus.Pool(F8, codes, meta, n_slots)]
+    small.d_table = small.d_table + (n_slots - pool.n_slots)
+    out, lse = run(small, True)
+    assert torch.equal(out, ref) and torch.equal(lse, rl)

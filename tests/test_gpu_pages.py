@@ -229,3 +229,29 @@ def test_both_on_another_stream_and_from_a_graph():
         assert np.array_equal(t.cpu().numpy(), ref[0]) and np.array_equal(rout[0].cpu().numpy(), ref[3][W.BF16])
         ot, orf, _, ol, _ = oracle.compact_pages(W.BF16, ref[3][W.BF16], ref[1], ref[0], ref[2], 16)
         assert np.array_equal(tend.cpu().numpy(), ot) and np.array_equal(rend.cpu().numpy(), orf) and int(live) == ol
+
+
+def test_offsets_beyond_four_gigabytes():
+    """A pool of 5 GB: a page forked and one compacted at its far end."""
+    Hkv, P, D = 8, 16, 128
+    page = 2 * Hkv * P * D * 2
+    n = (5 << 30) // page + 3
+    g = argus.geom(Hkv, Hkv, D, P)
+    pool = argus.Pool(W.FP16, torch.empty((n, 2, Hkv, P, D), dtype=torch.float16, device=DEV), None, n)
+    pool.codes[n - 2] = W.normal((2, Hkv, P, D), W.FP16, 1).to(DEV)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    ref = torch.ones(n, dtype=torch.int32, device=DEV)
+    ref[n - 1] = 0
+    t, c, l = torch.empty((2, 1), dtype=torch.int32, device=DEV), torch.empty((2, 1), dtype=torch.uint8, device=DEV), i32([0, 0])
+    r = torch.empty_like(ref)
+    ws = torch.empty(argus.fork_workspace_bytes(2, [pool]), dtype=torch.uint8, device=DEV)
+    argus.fork_pages(g, i32([0, 0]), i32([1, 1]), W.FP16, [pool], [ref], [r], torch.zeros((2, 1), dtype=torch.uint8, device=DEV),
+                     i32([[n - 2], [-1]]), i32([5, 0]), c, t, l, 1, ws)
+    assert t.tolist() == [[n - 2], [n - 1]] and torch.equal(pool.codes[n - 1], pool.codes[n - 2])
+    assert r[n - 2:].tolist() == [1, 1]
+    r.zero_()
+    r[n - 1] = 2
+    out, t2, live = torch.empty_like(r), torch.empty_like(t), torch.empty(1, dtype=torch.int32, device=DEV)
+    ws = torch.empty(argus.compact_workspace_bytes(pool), dtype=torch.uint8, device=DEV)
+    argus.compact_pages(g, pool, r, out, c, t, l, t2, 1, live, ws)
+    assert int(live) == 1 and out[0] == 2 and t2[1, 0] == 0 and torch.equal(pool.codes[0], pool.codes[n - 1])

@@ -148,3 +148,37 @@ def test_rows_of_no_sequence_are_left():
     out = call(s, False)
     assert torch.isnan(out[:2]).all() and torch.isnan(out[7:]).all() and not torch.isnan(out[2:7]).any()
     assert int((before != s["pool"]).any(-1).any(1).any(1).sum()) == 5
+
+
+def test_replayed_from_a_graph_on_another_stream():
+    s = case(6, 2, 128, 16, W.BF16, [5, 100], [3, 40], 96, 3, seed=20)
+    ref = call(s, False)
+    stored = s["pool"].clone()
+    dev = lambda x: torch.from_numpy(x).to(DEV)  # noqa: E731
+    tensors = [dev(s["q_start"]), torch.tensor(s["lens"], dtype=torch.int32, device=DEV), dev(s["pos"]), dev(s["inv"])]
+    codec, table, axis = dev(s["codec"]), dev(s["table"]), dev(s["axis"])
+    q_out = torch.empty(s["q"].shape, dtype=s["q"].dtype, device=DEV)
+    pool = argus.Pool(s["kind"], s["pool"], None, s["n_slots"])
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        argus.rope_append(s["g"], s["q"], s["k"], s["v"], q_out, tensors[0], tensors[1], tensors[2], tensors[3], pool, codec, table,
+                          s["max_pages"], pair_axis=axis)
+    for _ in range(2):
+        q_out.zero_()
+        s["pool"].copy_(stored * 0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(q_out, ref)
+    places = oracle.append_places(s["q_start"], s["lens"], s["P"], s["codec"], s["table"], s["kind"], s["n_slots"])
+    for slot, row in places.values():
+        assert torch.equal(s["pool"][slot, :, :, row], stored[slot, :, :, row])
+
+
+def test_large_ragged_batches():
+    """Thousands of tokens, so that warps loop over tokens; sequences of very different lengths."""
+    rng = np.random.default_rng(21)
+    new = [4000, 1, 0, 700, 33] + rng.integers(0, 60, 60).tolist()
+    s = case(2, 1, 64, 16, W.FP16, rng.integers(0, 900, len(new)).tolist(), new, 64, 3, seed=22)
+    before = s["pool"].clone()
+    assert check(s, call(s, True), before, True) == 0
