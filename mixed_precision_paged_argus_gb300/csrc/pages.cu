@@ -24,7 +24,7 @@ namespace pages {
 
 constexpr int kMaxPools = 7;         // one per codec
 constexpr int kTile = 1024;          // slots per tile: one per thread
-constexpr int kPart = kTile * 4 * 16;   // bytes a block copies per step: four 16-byte vectors per thread
+constexpr int kPart = 32 * 8 * 16;   // bytes a warp copies per step: eight 16-byte vectors per lane
 
 namespace cg = cooperative_groups;
 
@@ -119,26 +119,26 @@ __device__ __forceinline__ int block_total(const int32_t* counts, int n, int* sh
   return block_sum(x, sh);
 }
 
-// bytes [part * kPart, ...) of a page, four vectors in flight per thread
-__device__ __forceinline__ void copy_part(uint8_t* dst, const uint8_t* src, long long bytes, int part) {
-  const long long base = (long long)part * kPart;
-  uint4 v[4];
+// bytes [part * kPart, ...) of a page, by a warp, eight vectors in flight per
+// lane; part 0 with the meta.  Warps copy on their own: one waits for its
+// loads while another stores.
+__device__ __forceinline__ void copy_part(const PoolRef& r, long long dst, long long src, int part) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* s = r.codes + src * r.page_bytes;
+  uint8_t* d = r.codes + dst * r.page_bytes;
+  const long long base = (long long)part * kPart + lane * 16;
+  uint4 v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long o = base + (i * kTile + threadIdx.x) * 16ll;
-    if (o < bytes) v[i] = *reinterpret_cast<const uint4*>(src + o);
-  }
+  for (int i = 0; i < 8; ++i)
+    if (base + i * 512 < r.page_bytes) v[i] = *reinterpret_cast<const uint4*>(s + base + i * 512);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long o = base + (i * kTile + threadIdx.x) * 16ll;
-    if (o < bytes) *reinterpret_cast<uint4*>(dst + o) = v[i];
+  for (int i = 0; i < 8; ++i)
+    if (base + i * 512 < r.page_bytes) *reinterpret_cast<uint4*>(d + base + i * 512) = v[i];
+  if (part == 0 && r.meta_bytes) {
+    const uint32_t* ms = reinterpret_cast<const uint32_t*>(r.meta + src * r.meta_bytes);
+    uint32_t* md = reinterpret_cast<uint32_t*>(r.meta + dst * r.meta_bytes);
+    for (int i = lane; i < r.meta_bytes / 4; i += 32) md[i] = ms[i];
   }
-}
-
-__device__ __forceinline__ void copy_meta(const PoolRef& r, long long dst, long long src) {
-  const uint32_t* s = reinterpret_cast<const uint32_t*>(r.meta + src * r.meta_bytes);
-  uint32_t* d = reinterpret_cast<uint32_t*>(r.meta + dst * r.meta_bytes);
-  for (int i = threadIdx.x; i < r.meta_bytes / 4; i += blockDim.x) d[i] = s[i];
 }
 
 // exclusive prefix sum over the block; *total: the sum
@@ -333,19 +333,17 @@ __global__ void __launch_bounds__(kTile, 1) fork_kernel(const FParams p) {
     const PoolRef& r = p.pool[k];
     const int have = block_total(p.tile_free + r.tile0, r.n_tiles, sh);
     const int parts = (int)((r.page_bytes + kPart - 1) / kPart);
-    for (long long u = blockIdx.x; u < (long long)n_copies * parts; u += gridDim.x) {
+    for (long long u = (long long)blockIdx.x * 32 + (tid >> 5); u < (long long)n_copies * parts; u += (long long)gridDim.x * 32) {
       const int b = p.copies[u / parts], part = (int)(u % parts);
       const RowInfo w = p.rows[b];
       if (w.pool != k) continue;
       const int dst = taken(k, w.copy_at, have);
-      if (part == 0 && tid == 0) {
+      if (part == 0 && (tid & 31) == 0) {
         p.table_out[(size_t)b * p.max_pages + w.tail] = dst;
         atomicAdd(r.ref_out + w.src, -1);
         count(p.status, dst < 0);
       }
-      if (dst < 0) continue;
-      copy_part(r.codes + (long long)dst * r.page_bytes, r.codes + (long long)w.src * r.page_bytes, r.page_bytes, part);
-      if (part == 0 && r.meta_bytes) copy_meta(r, dst, w.src);
+      if (dst >= 0) copy_part(r, dst, w.src, part);
     }
   }
   {
@@ -419,14 +417,11 @@ __global__ void __launch_bounds__(kTile, 1) compact_kernel(const CParams p) {
 
   // 3. the pages move, the table follows
   const int parts = (int)((p.pool.page_bytes + kPart - 1) / kPart);
-  for (long long w = blockIdx.x; w < (long long)moves * parts; w += gridDim.x) {
+  for (long long w = (long long)blockIdx.x * 32 + (tid >> 5); w < (long long)moves * parts; w += (long long)gridDim.x * 32) {
     const int k = (int)(w / parts), part = (int)(w - (long long)k * parts);
     const int src = p.src[k], dst = p.dst[k];
-    copy_part(p.pool.codes + dst * p.pool.page_bytes, p.pool.codes + src * p.pool.page_bytes, p.pool.page_bytes, part);
-    if (part == 0) {
-      if (p.pool.meta_bytes) copy_meta(p.pool, dst, src);
-      if (tid == 0) p.pool.ref_out[dst] = p.pool.ref_in[src];
-    }
+    copy_part(p.pool, dst, src, part);
+    if (part == 0 && (tid & 31) == 0) p.pool.ref_out[dst] = p.pool.ref_in[src];
   }
   const long long entries = (long long)p.B * p.max_pages;
   int bad = 0;
@@ -613,8 +608,8 @@ extern "C" argus_status argus_fork_pages(const argus_geom* g, int32_t batch, con
     w += up16((size_t)p.pool[i].n_slots * 4);
     part_max = std::max(part_max, (p.pool[i].page_bytes + kPart - 1) / kPart);
   }
-  // a block per row, tile or copied part that there can be, one per SM at most
-  const long long work = std::max<long long>(tiles, (long long)batch * std::min<long long>(part_max, 64));
+  // a block per row, tile or 32 copied parts that there can be, one per SM at most
+  const long long work = std::max<long long>(std::max(tiles, batch), ((long long)batch * part_max + 31) / 32);
   return launch_cooperative("argus_fork_pages", fork_kernel, p, work, static_cast<cudaStream_t>(stream));
 }
 
@@ -666,6 +661,6 @@ extern "C" argus_status argus_compact_pages(const argus_geom* g, int32_t batch, 
   p.dst = reinterpret_cast<int32_t*>(w + per);
   p.rank = reinterpret_cast<int32_t*>(w + 2 * per);
   const long long parts = (p.pool.page_bytes + kPart - 1) / kPart;
-  const long long work = std::max((long long)pool->n_slots / 2 * parts, ((long long)batch * max_pages + kTile - 1) / kTile);
+  const long long work = std::max(((long long)pool->n_slots / 2 * parts + 31) / 32, ((long long)batch * max_pages + kTile - 1) / kTile);
   return launch_cooperative("argus_compact_pages", compact_kernel, p, work, static_cast<cudaStream_t>(stream));
 }
