@@ -410,12 +410,23 @@ def _status_at(t):
     return t.data_ptr()
 
 
-def _stream_of(t, stream):
-    """The stream to launch on: the given one, or t's device's current one.  The
-    library launches on the current device, so t has to lie there."""
-    device = t.get_device()
-    if device >= 0 and device != torch._C._cuda_getDevice():
-        raise ValueError("the tensors lie on cuda:%d, which is not the current device" % device)
+def _tensors_of(pools):
+    """The pools' tensors (host pools: none; the library refuses them where it has to)."""
+    return tuple(t for p in pools if p.placement == PLACE_DEVICE for t in (p.codes, p.meta))
+
+
+def _stream_of(tensors, stream):
+    """The stream to launch on: the given one, or the device's current one.  The
+    library launches on the current device, so all tensors have to lie there."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("the tensors lie on different devices")
+    if device >= 0:
+        if device != torch._C._cuda_getDevice():
+            raise ValueError("the tensors lie on cuda:%d, which is not the current device" % device)
+    elif torch.cuda.is_available():
+        raise ValueError("the tensors must lie on the GPU")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device) if device >= 0 else None
     return stream if isinstance(stream, int) else stream.cuda_stream
@@ -439,6 +450,7 @@ def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pag
                    softmax_scale)
     # the struct holds raw pointers: keep every tensor it points to alive with it
     a._keep = (arr, pools, q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
+    a._tensors = a._keep[2:] + _tensors_of(pools)
     return a
 
 
@@ -451,7 +463,7 @@ def extend_workspace_bytes(args):
 def paged_extend_attn(args, ws, stream=None):
     """Attention of several query tokens per sequence over the paged cache;
     ws of extend_workspace_bytes bytes."""
-    _check(lib().argus_paged_extend_attn(ctypes.byref(args), ws.data_ptr(), ws.nbytes, _stream_of(args._keep[2], stream)))
+    _check(lib().argus_paged_extend_attn(ctypes.byref(args), ws.data_ptr(), ws.nbytes, _stream_of((ws,) + args._tensors, stream)))
 
 
 def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages,
@@ -475,7 +487,8 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
                  _at("seq_lens", seq_lens, _I32, batch), ctypes.pointer(pool.desc()),
                  _at("page_codec", page_codec, _U8, batch * max_pages),
                  _at("block_table", block_table, _I32, batch * max_pages), max_pages, _status_at(status))
-    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(q, stream)))
+    tensors = (q, k, v, q_out, q_start, seq_lens, positions, inv_freq, page_codec, block_table, pair_axis, status)
+    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(tensors + _tensors_of([pool]), stream)))
 
 
 def _pool_array(pools):
@@ -501,12 +514,14 @@ def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec,
     rin = pointers(*[_at("ref_in", r, _I32, p.n_slots) for p, r in zip(pools, ref_in)])
     rout = pointers(*[_at("ref_out", r, _I32, p.n_slots) for p, r in zip(pools, ref_out)])
     entries = batch * max_pages
+    tensors = (ws, parents, n_new, page_codec, block_table, seq_lens, page_codec_out, block_table_out, seq_lens_out, status,
+               *ref_in, *ref_out) + _tensors_of(pools)
     _check(lib().argus_fork_pages(
         ctypes.byref(g), batch, _at("parents", parents, _I32, 0), _at("n_new", n_new, _I32, batch), new_codec, _pool_array(pools),
         n, rin, rout, _at("page_codec", page_codec, _U8, entries), _at("block_table", block_table, _I32, entries),
         _at("seq_lens", seq_lens, _I32, batch), _at("page_codec_out", page_codec_out, _U8, entries),
         _at("block_table_out", block_table_out, _I32, entries), _at("seq_lens_out", seq_lens_out, _I32, batch), max_pages,
-        ws.data_ptr(), ws.nbytes, _status_at(status), _stream_of(parents, stream)))
+        ws.data_ptr(), ws.nbytes, _status_at(status), _stream_of(tensors, stream)))
 
 
 def compact_workspace_bytes(pool):
@@ -522,9 +537,10 @@ def compact_pages(g, pool, ref_in, ref_out, page_codec, block_table, seq_lens, b
     ws of compact_workspace_bytes bytes."""
     batch = seq_lens.numel()
     entries = batch * max_pages
+    tensors = (ws, ref_in, ref_out, page_codec, block_table, seq_lens, block_table_out, n_live, status) + _tensors_of([pool])
     _check(lib().argus_compact_pages(
         ctypes.byref(g), batch, ctypes.byref(pool.desc()), _at("ref_in", ref_in, _I32, pool.n_slots),
         _at("ref_out", ref_out, _I32, pool.n_slots), _at("page_codec", page_codec, _U8, entries),
         _at("block_table", block_table, _I32, entries), _at("seq_lens", seq_lens, _I32, 0),
         _at("block_table_out", block_table_out, _I32, entries), max_pages, _at("n_live", n_live, _I32, 1), ws.data_ptr(),
-        ws.nbytes, _status_at(status), _stream_of(ws, stream)))
+        ws.nbytes, _status_at(status), _stream_of(tensors, stream)))

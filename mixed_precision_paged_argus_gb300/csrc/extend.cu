@@ -1116,10 +1116,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       float l_all = 0.f;
       for (int x = 0; x < 2 * nrep; ++x) {
         const float2 y = ml[(x & 1) * kBM + (x >> 1) * per + l_row];
-        if (y.x != -INFINITY) l_all += y.y * fast_exp2(y.x - M);
+        l_all += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M);   // the first: 0, or NaN
       }
       const float2 y0 = ml[tl], y1 = ml[kBM + tl];
-      const bool have = l_all > 0.f;
+      const bool have = l_all != 0.f;                  // NaN (from a query that holds one) is not nothing
       const float inv = have ? 1.f / l_all : 0.f;
       const float w0 = (have && y0.x != -INFINITY) ? fast_exp2(y0.x - M) * inv : 0.f;
       const float w1 = (have && y1.x != -INFINITY) ? fast_exp2(y1.x - M) * inv : 0.f;
@@ -1252,14 +1252,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const EParams p) 
     }
 #pragma unroll
     for (int y = 0; y < kJoinAhead; ++y) top = fmaxf(top, l[y]);
-    if (top == -INFINITY) continue;                      // nothing visible so far
-    const float r = fast_exp2(M - top);                  // 2^-inf = 0
+    const float ref = top == -INFINITY ? 0.f : top;      // nothing visible so far, or NaN
+    const float r = fast_exp2(M - ref);                  // 2^-inf = 0
     M = top;
     sum *= r;
     o = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 #pragma unroll
     for (int y = 0; y < kJoinAhead; ++y) {
-      const float w = fast_exp2(l[y] - top);
+      const float w = fast_exp2(l[y] - ref);
       sum += w;
       o.x = fmaf(w, v[y].x, o.x);
       o.y = fmaf(w, v[y].y, o.y);
@@ -1269,12 +1269,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const EParams p) 
   }
   const int lin = cut.row0 + row, tok = lin / p.G;
   const size_t orow = (size_t)(cut.q0 + tok) * p.Hq + cut.head0 + (lin - tok * p.G);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint2 u;
   u.x = BF ? pack_bf16x2(o.x * inv, o.y * inv) : pack_f16x2(o.x * inv, o.y * inv);
   u.y = BF ? pack_bf16x2(o.z * inv, o.w * inv) : pack_f16x2(o.z * inv, o.w * inv);
   *reinterpret_cast<uint2*>(p.out + orow * D + 4 * col) = u;
-  if (col == 0 && p.lse2) p.lse2[orow] = sum > 0.f ? M + log2f(sum) : -INFINITY;
+  if (col == 0 && p.lse2) p.lse2[orow] = sum != 0.f ? M + log2f(sum) : -INFINITY;
 }
 
 static argus_status check(const argus_extend_args* a) {
@@ -1394,6 +1394,10 @@ extern "C" argus_status argus_paged_extend_attn(const argus_extend_args* a, void
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)) return fail(ARGUS_E_INVALID, "extend: ws must be a 16-byte aligned device pointer");
   if (ws_bytes < extend::workspace(a))
     return fail(ARGUS_E_WORKSPACE, "extend: workspace of %zu bytes, %zu needed", ws_bytes, extend::workspace(a));
+  // an item that two CTAs share has its queries read while rows of others are written
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(a->q), o0 = reinterpret_cast<uintptr_t>(a->out);
+  const uintptr_t token = (uintptr_t)g.n_q_heads * D * 2, q_bytes = (uintptr_t)(a->total_q - 1) * qs * 2 + token;
+  if (q0 < o0 + a->total_q * token && o0 < q0 + q_bytes) return fail(ARGUS_E_INVALID, "extend: out overlaps q");
   extend::EParams p{};
   p.Hq = g.n_q_heads;
   p.Hkv = g.n_kv_heads;

@@ -41,7 +41,7 @@ def _pools(*descs):
 def _extend(**kw):
     f = dict(g=argus.geom(8, 2, 128, 16), batch=2, total_q=5, q_dtype=argus.FP16, causal=1, q=64, q_stride=0, q_start=64,
              pools=[(argus.FP16, 0, 64, None, 4), (argus.FP8_E4M3, 0, 64, 64, 4)], max_pages=4, page_codec=64, block_table=64,
-             seq_lens=64, out=64, lse2_out=None, status=None, softmax_scale=0.5)
+             seq_lens=64, out=1 << 20, lse2_out=None, status=None, softmax_scale=0.5)
     f.update(kw)
     arr = _pools(*f.pop("pools"))
     n = len(kw["pools"]) if "pools" in kw else 2
@@ -71,6 +71,9 @@ def _extend_status(ws=64, ws_bytes=1 << 40, **kw):
     (dict(pools=[(argus.FP8_E4M3, 0, 72, 64, 4)]), INVALID), (dict(pools=[(argus.INT8, 0, 64, 66, 4)]), INVALID),
     (dict(pools=[(argus.INT8, 0, 64, 64, -1)]), INVALID),
     (dict(pools=[(argus.INT8, 0, 64, 64, 4), (argus.INT8, 0, 64, 64, 4)]), INVALID),
+    # five tokens of 2048 bytes: out on, before and behind q, and between its strided tokens
+    (dict(q=1 << 20), INVALID), (dict(q=(1 << 20) + 5 * 2048 - 16), INVALID), (dict(q=(1 << 20) - 5 * 2048 + 16), INVALID),
+    (dict(q=(1 << 20) - 4096, q_stride=8192), INVALID),
     (dict(ws=None), INVALID), (dict(ws=72), INVALID), (dict(ws_bytes=0), WORKSPACE)])
 def test_extend_refusals(kw, status):
     assert _extend_status(**kw) == status
@@ -109,6 +112,29 @@ def _rope_status(**kw):
     (dict(pool=(argus.FP16, 0, 64, None, -1)), INVALID)])
 def test_rope_refusals(kw, status):
     assert _rope_status(**kw) == status
+
+
+class _On:
+    """Stands for a tensor of a device."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+
+def test_binding_refuses_tensors_of_other_devices(monkeypatch):
+    for devices in ((0, -1), (0, None, 1), (-1, 0)):
+        with pytest.raises(ValueError, match="different devices"):
+            argus._stream_of([None if d is None else _On(d) for d in devices], None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="not the current device"):
+        argus._stream_of([_On(1), _On(1)], None)
+    assert argus._stream_of([_On(0), None], 77) == 77
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    with pytest.raises(ValueError, match="on the GPU"):
+        argus._stream_of([_On(-1)], None)
 
 
 def test_rope_without_work_is_a_no_op():

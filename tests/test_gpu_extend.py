@@ -184,6 +184,20 @@ def test_bad_slots_and_missing_pools_are_left_out_and_counted():
     assert int(status) == 6
 
 
+@pytest.mark.parametrize("dtype,codec", [(W.FP16, W.FP16), (W.BF16, F8)])
+def test_nan_queries_stay_in_their_rows(dtype, codec):
+    """A query row that holds NaN gives NaN, also where its item is cut over many CTAs, and leaves the
+    tile's other rows alone."""
+    c = make(4, 1, 64, 16, [20000, 90, 0], [5, 40, 3], [codec], dtype, seed=175)
+    clean, clean_lse = run(c, True)
+    c.q[2, 1, 7] = c.q[20, 3, 63] = c.q[46, 0, 0] = float("nan")      # the last one's cache is empty
+    out, lse = run(c, True)
+    hit = torch.zeros(c.q.shape[:2], dtype=torch.bool, device=DEV)
+    hit[2, 1] = hit[20, 3] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
+
+
 def test_strided_queries():
     c = make(8, 2, 128, 16, [100, 300], [3, 9], [F8], W.BF16, seed=180)
     wide = torch.full((12, 12, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
