@@ -9,6 +9,7 @@ built, lib() raises.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -382,7 +383,7 @@ def paged_window_prefill_attn(g, n_q, q, pools, page_codec, block_table, max_pag
                                                  ws.numel() * ws.element_size(), _ptr(status), _stream(stream)))
 
 
-def _token_stride(name, t, heads, head_dim):
+def _token_stride(name, t, heads, head_dim, device):
     """Elements between the tokens of t [tokens][heads][head_dim], whose tokens
     are dense and may lie apart (a slice of a fused projection's rows)."""
     shape, stride = t.shape, t.stride()
@@ -390,38 +391,35 @@ def _token_stride(name, t, heads, head_dim):
         raise ValueError("%s must be [tokens][%d][%d], not %s" % (name, heads, head_dim, list(shape)))
     if (stride[2] != 1 or (heads > 1 and stride[1] != head_dim)) and t.numel():
         raise ValueError("%s: the heads of a token must be dense" % name)
+    if t.get_device() != device:
+        raise ValueError("%s lies on another device" % name)
     return stride[0] if shape[0] > 1 else heads * head_dim
 
 
-def _at(name, t, dtype, numel):
-    """Address of a dense tensor of at least numel elements (None: NULL)."""
+def _at(name, t, dtype, numel, device):
+    """Address of a dense tensor of at least numel elements on the device (None: NULL)."""
     if t is None:
         return None
     if t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
         raise ValueError("%s must be a dense %s tensor of %d elements or more" % (name, dtype, numel))
+    if t.get_device() != device:
+        raise ValueError("%s lies on another device" % name)
     return t.data_ptr()
 
 
-def _status_at(t):
+def _status_at(t, device):
     if t is None:
         return None
     if t.element_size() != 4 or t.is_floating_point() or t.numel() < 1:
         raise ValueError("status must be a 32-bit integer tensor")
+    if t.get_device() != device:
+        raise ValueError("status lies on another device")
     return t.data_ptr()
 
 
-def _tensors_of(pools):
-    """The pools' tensors (host pools: none; the library refuses them where it has to)."""
-    return tuple(t for p in pools if p.placement == PLACE_DEVICE for t in (p.codes, p.meta))
-
-
-def _stream_of(tensors, stream):
+def _stream_of(device, stream):
     """The stream to launch on: the given one, or the device's current one.  The
-    library launches on the current device, so all tensors have to lie there."""
-    device = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("the tensors lie on different devices")
+    library launches on the current device, so the tensors have to lie there."""
     if device >= 0:
         if device != torch._C._cuda_getDevice():
             raise ValueError("the tensors lie on cuda:%d, which is not the current device" % device)
@@ -432,6 +430,32 @@ def _stream_of(tensors, stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _ws_at(ws, device):
+    if ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError("ws must be a dense tensor on the tensors' device")
+    return ws.data_ptr()
+
+
+_POOL_DESC = struct.Struct("@iiPPq")
+
+
+def _pool_array(pools, device):
+    """The pools' descriptions; device pools on the device (host pools are the
+    library's to refuse)."""
+    raw = []
+    for p in pools:
+        codes, meta = p.codes, p.meta
+        if p.placement == PLACE_DEVICE:
+            for t in (codes, meta):
+                if t is not None and t.get_device() != device:
+                    raise ValueError("a pool lies on another device")
+        raw.append(_POOL_DESC.pack(p.codec, p.placement, 0 if codes is None else codes.data_ptr(),
+                                   0 if meta is None else meta.data_ptr(), p.n_slots))
+    if not raw:
+        return (PoolDesc * 1)()
+    return (PoolDesc * len(raw)).from_buffer_copy(b"".join(raw))
+
+
 _I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 
 
@@ -439,18 +463,17 @@ def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pag
                 causal=True, lse2_out=None, status=None):
     """Build an argus_extend_args struct: q [total_q][Hq][D] (its tokens may lie
     apart), q_start [B + 1], seq_lens [B], out like q and dense."""
-    batch, total, hq = q_start.numel() - 1, q.shape[0], g.n_q_heads
-    n = len(pools)
-    arr = (PoolDesc * (n or 1))(*[p.desc() for p in pools])
+    batch, total, hq, dev = q_start.numel() - 1, q.shape[0], g.n_q_heads, q.get_device()
+    arr = _pool_array(pools, dev)
     a = ExtendArgs(g, batch, total, DTYPE_CODEC[q.dtype], 1 if causal else 0, q.data_ptr(),
-                   _token_stride("q", q, hq, g.head_dim), _at("q_start", q_start, _I32, 1), arr, n, max_pages,
-                   _at("page_codec", page_codec, _U8, batch * max_pages),
-                   _at("block_table", block_table, _I32, batch * max_pages), _at("seq_lens", seq_lens, _I32, batch),
-                   _at("out", out, q.dtype, q.numel()), _at("lse2_out", lse2_out, _F32, total * hq), _status_at(status),
-                   softmax_scale)
+                   _token_stride("q", q, hq, g.head_dim, dev), _at("q_start", q_start, _I32, 1, dev), arr, len(pools), max_pages,
+                   _at("page_codec", page_codec, _U8, batch * max_pages, dev),
+                   _at("block_table", block_table, _I32, batch * max_pages, dev), _at("seq_lens", seq_lens, _I32, batch, dev),
+                   _at("out", out, q.dtype, q.numel(), dev), _at("lse2_out", lse2_out, _F32, total * hq, dev),
+                   _status_at(status, dev), softmax_scale)
     # the struct holds raw pointers: keep every tensor it points to alive with it
     a._keep = (arr, pools, q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
-    a._tensors = a._keep[2:] + _tensors_of(pools)
+    a._device = dev
     return a
 
 
@@ -463,7 +486,7 @@ def extend_workspace_bytes(args):
 def paged_extend_attn(args, ws, stream=None):
     """Attention of several query tokens per sequence over the paged cache;
     ws of extend_workspace_bytes bytes."""
-    _check(lib().argus_paged_extend_attn(ctypes.byref(args), ws.data_ptr(), ws.nbytes, _stream_of((ws,) + args._tensors, stream)))
+    _check(lib().argus_paged_extend_attn(ctypes.byref(args), _ws_at(ws, args._device), ws.nbytes, _stream_of(args._device, stream)))
 
 
 def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages,
@@ -472,7 +495,7 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
     inv_freq [rot_dim / 2] in float64, radians per position) into q_out and the
     cache, and store v: the tokens of sequence b become the last ones of its
     seq_lens[b] cached positions."""
-    total, batch, dtype = q.shape[0], q_start.numel() - 1, q.dtype
+    total, batch, dtype, dev = q.shape[0], q_start.numel() - 1, q.dtype, q.get_device()
     hq, hkv, d = g.n_q_heads, g.n_kv_heads, g.head_dim
     if k.shape[0] != total or v.shape[0] != total or q_out.shape[0] != total or positions.numel() % (total or 1):
         raise ValueError("rope_append: q, k, v, q_out and positions must have the same tokens")
@@ -480,24 +503,19 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
         raise ValueError("rope_append: q, k, v and q_out must have the same type")
     half = inv_freq.numel()
     a = RopeArgs(g, batch, total, DTYPE_CODEC[dtype], 2 * half, 1 if adjacent else 0, positions.numel() // total if total else 1,
-                 q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _token_stride("q", q, hq, d),
-                 _token_stride("k", k, hkv, d), _token_stride("v", v, hkv, d), _token_stride("q_out", q_out, hq, d),
-                 _at("positions", positions, _I32, 0), _at("inv_freq", inv_freq, torch.float64, 0),
-                 _at("pair_axis", pair_axis, _U8, half), _at("q_start", q_start, _I32, 1),
-                 _at("seq_lens", seq_lens, _I32, batch), ctypes.pointer(pool.desc()),
-                 _at("page_codec", page_codec, _U8, batch * max_pages),
-                 _at("block_table", block_table, _I32, batch * max_pages), max_pages, _status_at(status))
-    tensors = (q, k, v, q_out, q_start, seq_lens, positions, inv_freq, page_codec, block_table, pair_axis, status)
-    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(tensors + _tensors_of([pool]), stream)))
-
-
-def _pool_array(pools):
-    return (PoolDesc * (len(pools) or 1))(*[p.desc() for p in pools])
+                 q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _token_stride("q", q, hq, d, dev),
+                 _token_stride("k", k, hkv, d, dev), _token_stride("v", v, hkv, d, dev),
+                 _token_stride("q_out", q_out, hq, d, dev), _at("positions", positions, _I32, 0, dev),
+                 _at("inv_freq", inv_freq, torch.float64, 0, dev), _at("pair_axis", pair_axis, _U8, half, dev),
+                 _at("q_start", q_start, _I32, 1, dev), _at("seq_lens", seq_lens, _I32, batch, dev), _pool_array((pool,), dev),
+                 _at("page_codec", page_codec, _U8, batch * max_pages, dev),
+                 _at("block_table", block_table, _I32, batch * max_pages, dev), max_pages, _status_at(status, dev))
+    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(dev, stream)))
 
 
 def fork_workspace_bytes(batch, pools):
     n = ctypes.c_size_t(0)
-    _check(lib().argus_fork_workspace_bytes(int(batch), _pool_array(pools), len(pools), ctypes.byref(n)))
+    _check(lib().argus_fork_workspace_bytes(int(batch), (PoolDesc * (len(pools) or 1))(*[p.desc() for p in pools]), len(pools), ctypes.byref(n)))
     return n.value
 
 
@@ -507,21 +525,20 @@ def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec,
     partial pages about to be written are copied where others hold them too, and
     pages of new_codec are added for n_new[b] tokens.  ref_in / ref_out: one
     int32 count per slot for each pool.  ws of fork_workspace_bytes bytes."""
-    batch, n = parents.numel(), len(pools)
+    batch, n, dev = parents.numel(), len(pools), parents.get_device()
     if len(ref_in) != n or len(ref_out) != n:
         raise ValueError("fork_pages: one count tensor per pool")
     pointers = ctypes.c_void_p * (n or 1)
-    rin = pointers(*[_at("ref_in", r, _I32, p.n_slots) for p, r in zip(pools, ref_in)])
-    rout = pointers(*[_at("ref_out", r, _I32, p.n_slots) for p, r in zip(pools, ref_out)])
+    rin = pointers(*[_at("ref_in", r, _I32, p.n_slots, dev) for p, r in zip(pools, ref_in)])
+    rout = pointers(*[_at("ref_out", r, _I32, p.n_slots, dev) for p, r in zip(pools, ref_out)])
     entries = batch * max_pages
-    tensors = (ws, parents, n_new, page_codec, block_table, seq_lens, page_codec_out, block_table_out, seq_lens_out, status,
-               *ref_in, *ref_out) + _tensors_of(pools)
     _check(lib().argus_fork_pages(
-        ctypes.byref(g), batch, _at("parents", parents, _I32, 0), _at("n_new", n_new, _I32, batch), new_codec, _pool_array(pools),
-        n, rin, rout, _at("page_codec", page_codec, _U8, entries), _at("block_table", block_table, _I32, entries),
-        _at("seq_lens", seq_lens, _I32, batch), _at("page_codec_out", page_codec_out, _U8, entries),
-        _at("block_table_out", block_table_out, _I32, entries), _at("seq_lens_out", seq_lens_out, _I32, batch), max_pages,
-        ws.data_ptr(), ws.nbytes, _status_at(status), _stream_of(tensors, stream)))
+        ctypes.byref(g), batch, _at("parents", parents, _I32, 0, dev), _at("n_new", n_new, _I32, batch, dev), new_codec,
+        _pool_array(pools, dev), n, rin, rout, _at("page_codec", page_codec, _U8, entries, dev),
+        _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, batch, dev),
+        _at("page_codec_out", page_codec_out, _U8, entries, dev), _at("block_table_out", block_table_out, _I32, entries, dev),
+        _at("seq_lens_out", seq_lens_out, _I32, batch, dev), max_pages, _ws_at(ws, dev), ws.nbytes, _status_at(status, dev),
+        _stream_of(dev, stream)))
 
 
 def compact_workspace_bytes(pool):
@@ -535,12 +552,11 @@ def compact_pages(g, pool, ref_in, ref_out, page_codec, block_table, seq_lens, b
     """Move the live pages of a pool into its lowest slots; the new counts and
     table go to ref_out and block_table_out, the number of live slots to n_live.
     ws of compact_workspace_bytes bytes."""
-    batch = seq_lens.numel()
+    batch, dev = seq_lens.numel(), seq_lens.get_device()
     entries = batch * max_pages
-    tensors = (ws, ref_in, ref_out, page_codec, block_table, seq_lens, block_table_out, n_live, status) + _tensors_of([pool])
     _check(lib().argus_compact_pages(
-        ctypes.byref(g), batch, ctypes.byref(pool.desc()), _at("ref_in", ref_in, _I32, pool.n_slots),
-        _at("ref_out", ref_out, _I32, pool.n_slots), _at("page_codec", page_codec, _U8, entries),
-        _at("block_table", block_table, _I32, entries), _at("seq_lens", seq_lens, _I32, 0),
-        _at("block_table_out", block_table_out, _I32, entries), max_pages, _at("n_live", n_live, _I32, 1), ws.data_ptr(),
-        ws.nbytes, _status_at(status), _stream_of(tensors, stream)))
+        ctypes.byref(g), batch, _pool_array((pool,), dev), _at("ref_in", ref_in, _I32, pool.n_slots, dev),
+        _at("ref_out", ref_out, _I32, pool.n_slots, dev), _at("page_codec", page_codec, _U8, entries, dev),
+        _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, 0, dev),
+        _at("block_table_out", block_table_out, _I32, entries, dev), max_pages, _at("n_live", n_live, _I32, 1, dev),
+        _ws_at(ws, dev), ws.nbytes, _status_at(status, dev), _stream_of(dev, stream)))

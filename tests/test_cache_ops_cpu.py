@@ -114,27 +114,40 @@ def test_rope_refusals(kw, status):
     assert _rope_status(**kw) == status
 
 
-class _On:
-    """Stands for a tensor of a device."""
-
-    def __init__(self, device):
-        self.device = device
+class _Elsewhere(torch.Tensor):
+    """A tensor that says it lies on the second GPU."""
 
     def get_device(self):
-        return self.device
+        return 1
 
 
-def test_binding_refuses_tensors_of_other_devices(monkeypatch):
-    for devices in ((0, -1), (0, None, 1), (-1, 0)):
-        with pytest.raises(ValueError, match="different devices"):
-            argus._stream_of([None if d is None else _On(d) for d in devices], None)
+def _call_extend(**kw):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    pool = argus.Pool(argus.FP8_E4M3, torch.zeros(4, 2, 2, 16, 64, dtype=torch.uint8), torch.zeros(4, 2, 2), 4, argus.PLACE_DEVICE)
+    f = dict(g=argus.geom(8, 2, 64, 16), q=torch.zeros(3, 8, 64, dtype=torch.float16), q_start=i32(3), pools=[pool],
+             page_codec=torch.zeros(2, 4, dtype=torch.uint8), block_table=i32(2, 4), seq_lens=i32(2), max_pages=4, softmax_scale=1.0,
+             out=torch.zeros(3, 8, 64, dtype=torch.float16), lse2_out=torch.zeros(3, 8), status=i32(1))
+    f.update({k: f[k].as_subclass(_Elsewhere) for k in kw if k in f and k != "pools"})
+    if "pools" in kw:
+        pool.meta = pool.meta.as_subclass(_Elsewhere)
+    return argus.extend_args(**f)
+
+
+@pytest.mark.parametrize("name", ["q_start", "page_codec", "block_table", "seq_lens", "out", "lse2_out", "status", "pools", "q"])
+def test_binding_refuses_tensors_of_other_devices(name):
+    _call_extend()
+    with pytest.raises(ValueError, match="another device"):
+        _call_extend(**{name: True})
+
+
+def test_binding_refuses_a_device_that_is_not_current(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     with pytest.raises(ValueError, match="not the current device"):
-        argus._stream_of([_On(1), _On(1)], None)
-    assert argus._stream_of([_On(0), None], 77) == 77
+        argus._stream_of(1, None)
+    assert argus._stream_of(0, 77) == 77
     monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
     with pytest.raises(ValueError, match="on the GPU"):
-        argus._stream_of([_On(-1)], None)
+        argus._stream_of(-1, None)
 
 
 def test_rope_without_work_is_a_no_op():
