@@ -439,13 +439,13 @@ def _ws_at(ws, device):
 _POOL_DESC = struct.Struct("@iiPPq")
 
 
-def _pool_array(pools, device):
-    """The pools' descriptions; device pools on the device (host pools are the
-    library's to refuse)."""
+def _pool_array(pools, device=None):
+    """The pools' descriptions; device pools on the device, if one is given (host
+    pools are the library's to refuse)."""
     raw = []
     for p in pools:
         codes, meta = p.codes, p.meta
-        if p.placement == PLACE_DEVICE:
+        if device is not None and p.placement == PLACE_DEVICE:
             for t in (codes, meta):
                 if t is not None and t.get_device() != device:
                     raise ValueError("a pool lies on another device")
@@ -515,7 +515,7 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
 
 def fork_workspace_bytes(batch, pools):
     n = ctypes.c_size_t(0)
-    _check(lib().argus_fork_workspace_bytes(int(batch), (PoolDesc * (len(pools) or 1))(*[p.desc() for p in pools]), len(pools), ctypes.byref(n)))
+    _check(lib().argus_fork_workspace_bytes(int(batch), _pool_array(pools), len(pools), ctypes.byref(n)))
     return n.value
 
 
@@ -543,7 +543,7 @@ def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec,
 
 def compact_workspace_bytes(pool):
     n = ctypes.c_size_t(0)
-    _check(lib().argus_compact_workspace_bytes(ctypes.byref(pool.desc()), ctypes.byref(n)))
+    _check(lib().argus_compact_workspace_bytes(_pool_array((pool,)), ctypes.byref(n)))
     return n.value
 
 
