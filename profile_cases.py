@@ -22,6 +22,11 @@ and use inputs larger than L2 where the kernel streams HBM.
   prefill         one 131072-token window of the windowed prefill
   prefill_paged   one 32768-token window of FP8 pages staged through the block table
   fold            fold a 16 x 1024 x 128 fp32 partial into an accumulator
+  extend_verify   1 to 8 drafted tokens of 16 sequences over FP8 pages (32/8 heads, D 128, 8192 to 12288 cached)
+  extend_chunk    a 1024-token prompt chunk over 32768 cached FP8 tokens (16/2 heads, D 128)
+  rope_video      three-axis positions and the append of two prompts of 20000 and 32768 tokens (14/2 heads, D 64)
+  fork            a step of 512 rows, a quarter of them forked or freed (32/8 heads, D 128, 16-token pages)
+  compact         a pool of 16384 pages of 64 KB, half of them live
 """
 
 import argparse
@@ -207,6 +212,83 @@ def _fold(dev):
     return lambda: argus.fold_lse(ao, al, po, pl)
 
 
+def _extend(dev, B, Hq, Hkv, D, P, lens, new):
+    g = argus.geom(Hq, Hkv, D, P)
+    maxp = int((max(lens) + P - 1) // P)
+    table, n_slots = W.paged_block_table(np.asarray(lens), P, maxp, 4)
+    src = W.normal((n_slots, 2, Hkv, P, D), W.BF16, 1, device=dev)
+    ids = torch.arange(n_slots, dtype=torch.int32, device=dev)
+    pool = argus.Pool.empty(W.FP8_E4M3, n_slots, Hkv, P, D, device=dev)
+    argus.quantize_pages(g, W.BF16, src, n_slots, ids, pool, ids, n_slots)
+    q = W.normal((int(sum(new)), Hq, D), W.BF16, 0, device=dev)
+    out = torch.empty_like(q)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    a = argus.extend_args(g, q, i32(np.concatenate([[0], np.cumsum(new)])), [pool],
+                          torch.full((B, maxp), W.FP8_E4M3, dtype=torch.uint8, device=dev), i32(table), i32(lens), maxp,
+                          W.softmax_scale(D), out)
+    ws = torch.empty(argus.extend_workspace_bytes(a), dtype=torch.uint8, device=dev)
+    return lambda: argus.paged_extend_attn(a, ws)
+
+
+def _extend_verify(dev):
+    rng = np.random.default_rng(0)
+    return _extend(dev, 16, 32, 8, 128, 16, rng.integers(8192, 12289, 16), rng.integers(1, 9, 16))
+
+
+def _rope_video(dev):
+    Hq, Hkv, D, P, new = 14, 2, 64, 1024, [20000, 32768]
+    g, total = argus.geom(Hq, Hkv, D, P), sum(new)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    pool = argus.Pool.empty(W.FP16, 64, Hkv, P, D, device=dev)
+    q, k, v = (W.normal((total, h, D), W.FP16, 9 + h, device=dev) for h in (Hq, Hkv, Hkv))
+    out = torch.empty_like(q)
+    pos = i32(np.random.default_rng(1).integers(0, 32768, (3, total)))
+    inv = torch.tensor([1e4 ** (-i / 16) for i in range(16)], dtype=torch.float64, device=dev)
+    axis = (torch.arange(16, device=dev) % 3).to(torch.uint8)
+    codec, table = torch.full((2, 32), W.FP16, dtype=torch.uint8, device=dev), i32(np.arange(64).reshape(2, 32))
+    start, lens = i32([0, new[0], total]), i32(new)
+    return lambda: argus.rope_append(g, q, k, v, out, start, lens, pos, inv, pool, codec, table, 32, pair_axis=axis, adjacent=True)
+
+
+def _fork(dev):
+    B, Hkv, D, P, MAXP, spare = 512, 8, 128, 16, 512, 8192
+    rng = np.random.default_rng(2)
+    lens = rng.integers(1, MAXP * P - 64, B)
+    pages = (lens + P - 1) // P
+    n_slots = int(pages.sum()) + spare
+    table, at = np.full((B, MAXP), -1, np.int32), 0
+    for b in range(B):
+        table[b, :pages[b]] = np.arange(at, at + pages[b])
+        at += pages[b]
+    ref = np.zeros(n_slots, np.int32)
+    ref[:at] = 1
+    parents = np.where(rng.random(B) < 0.25, rng.integers(-1, B, B), np.arange(B))
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    pool = argus.Pool.empty(W.BF16, n_slots, Hkv, P, D, device=dev)
+    codec, tab, ln, rf = torch.full((B, MAXP), W.BF16, dtype=torch.uint8, device=dev), i32(table), i32(lens), i32(ref)
+    outs = [torch.empty_like(x) for x in (codec, tab, ln, rf)]
+    par, new = i32(parents), i32(rng.integers(0, 41, B))
+    ws = torch.empty(argus.fork_workspace_bytes(B, [pool]), dtype=torch.uint8, device=dev)
+    return lambda: argus.fork_pages(argus.geom(Hkv, Hkv, D, P), par, new, W.BF16, [pool], [rf], [outs[3]], codec, tab, ln, outs[0],
+                                    outs[1], outs[2], MAXP, ws)
+
+
+def _compact(dev):
+    B, Hkv, D, P, n_slots = 64, 8, 128, 16, 16384
+    rng = np.random.default_rng(3)
+    live = np.flatnonzero(rng.random(n_slots) < 0.5)
+    live = rng.permutation(live[:len(live) // B * B])
+    ref = np.zeros(n_slots, np.int32)
+    ref[live] = 1
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    pool, maxp = argus.Pool.empty(W.BF16, n_slots, Hkv, P, D, device=dev), len(live) // B
+    rf, tab, lens = i32(ref), i32(live.reshape(B, maxp)), i32(np.full(B, maxp * P))
+    codec = torch.full((B, maxp), W.BF16, dtype=torch.uint8, device=dev)
+    ro, to, n = torch.empty_like(rf), torch.empty_like(tab), torch.empty(1, dtype=torch.int32, device=dev)
+    ws = torch.empty(argus.compact_workspace_bytes(pool), dtype=torch.uint8, device=dev)
+    return lambda: argus.compact_pages(argus.geom(Hkv, Hkv, D, P), pool, rf, ro, codec, tab, lens, to, maxp, n, ws)
+
+
 CASES = {
     "decode_mixed": _decode_mixed,
     "decode_bf16": lambda d: _decode_batched(d, W.BF16),
@@ -224,6 +306,11 @@ CASES = {
     "prefill": _prefill,
     "prefill_paged": _prefill_paged,
     "fold": _fold,
+    "extend_verify": _extend_verify,
+    "extend_chunk": lambda d: _extend(d, 1, 16, 2, 128, 64, [32768], [1024]),
+    "rope_video": _rope_video,
+    "fork": _fork,
+    "compact": _compact,
 }
 
 
