@@ -57,7 +57,7 @@ constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chu
 constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
 constexpr int kBatches = 4;          // batches whose descriptions are kept
 constexpr int kSlots = kBatch * kBatches;
-constexpr int kMergePad = 36;        // floats per row of the replica merge (32 used; conflict-free vectors)
+constexpr int kMergeBytes = 12 * 1024 + 1536;   // a group's exchange: 4 replicas x 24 columns of 32 rows, or the warps' turned outputs
 
 template <int D>
 struct Smem {
@@ -70,7 +70,7 @@ struct Smem {
   static constexpr int kOffQScale = kOffScale + kSlots * 8 * 16;         // [2][128]
   static constexpr int kOffML = kOffQScale + 2 * kBM * 4;
   static constexpr int kOffMerge = kOffML + 2 * kBM * 8;
-  static constexpr int kOffBar = kOffMerge + 2 * 96 * kMergePad * 4;
+  static constexpr int kOffBar = kOffMerge + 2 * kMergeBytes;
   // q_first, q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
   static constexpr int kNumBars = 14 + 2 * kBatches;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
@@ -468,24 +468,29 @@ __device__ __forceinline__ void store_steps(uint4 (&v)[kSteps], uint32_t tile, i
 }
 
 // Q tile of an item, by warps w = 0 .. nw - 1: row l of the tile goes to TMEM lanes
-// l, l + per, ...; zeros behind the last row.  All rows are on their way at
-// once (asynchronous copies, which write zeros where they read nothing); those
-// that become fp16 (TURN: from the tile at q_s to the one at q16) are turned by
-// the lanes that copied them.
-template <int D, bool TURN>
-__device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32_t q_s, uint32_t q16, float* q_scale, int w, int nw, int lane) {
+// l, l + per, ....  All rows are on their way at once (asynchronous copies,
+// which write zeros where they read nothing); those that become fp16 (TURN: from
+// the tile at q_s to the one at q16, which may be the same unless KEEP) are
+// turned by the lanes that copied them.  Behind the last row the tile gets zeros
+// if `fill`, else keeps what it holds: finite rows of an item before, whose
+// scores nobody uses.
+template <int D, bool TURN, bool KEEP>
+__device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32_t q_s, uint32_t q16, float* q_scale, int w, int nw, int lane,
+                                       bool fill) {
   constexpr int V = D / 8, RW = 32 / V;                  // vectors per row; rows of a warp's step
   const int v = lane % V, r0 = w * RW + lane / V, RS = RW * nw;
   const int lin0 = c.t * kBM, rows = min(kBM, c.s.n * p.G - lin0);
-  const int nrep = replicas(rows), per = kBM / nrep;
+  const int nrep = replicas(rows), per = kBM / nrep, lim = fill ? per : rows;
+  const int ncopy = TURN && !KEEP ? 1 : nrep;            // the turned rows are copied below
   const int tok = (int)((uint32_t)(lin0 + r0) / (uint32_t)p.G), dt = RS / p.G, dg = RS - dt * p.G;
   int g = lin0 + r0 - tok * p.G;
   const uint16_t* src = p.q + (long long)(c.s.q0 + tok) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
   const long long step = dt * p.qs + dg * D, wrap = p.qs - (long long)p.G * D;
 #pragma unroll 4
-  for (int l = r0; l < per; l += RS) {
+  for (int l = r0; l < lim; l += RS) {
     const bool real = l < rows;
-    for (int r = 0; r < nrep; ++r) cp_async16(q_s + tile_off(l + r * per, v), real ? src : p.q, real ? 16 : 0);
+    const uint32_t at = q_s + tile_off(l, v);            // a copy is per rows of 128 bytes further, with the same permutation
+    for (int r = 0; r < ncopy; ++r) cp_async16(at + r * per * 128, real ? src : p.q, real ? 16 : 0);
     src += step;
     g += dg;
     if (g >= p.G) {
@@ -499,7 +504,8 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
     // neighbours.  Four rows at once: one after the other, their reads,
     // exchanges and stores would only wait for each other.
     constexpr int R = 4;
-    for (int l0 = r0; l0 < per; l0 += R * RS) {
+    for (int i0 = w * RW; i0 < lim; i0 += R * RS) {      // by whole warps
+      const int l0 = i0 + lane / V;
       uint4 q[R];
       uint32_t mx[R];
 #pragma unroll
@@ -525,14 +531,13 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
           w[e] = pack_f16x2(a, b);
         }
       }
-      for (int r = 0; r < nrep; ++r) {
 #pragma unroll
-        for (int x = 0; x < R; ++x) {
-          const int l = l0 + x * RS;
-          if (l < per) {
-            sts16(q16 + tile_off(l + r * per, v), q[x].x, q[x].y, q[x].z, q[x].w);
-            if (v == 0) q_scale[l + r * per] = __uint_as_float((ex[x] - 14) << 23);   // 1 / f
-          }
+      for (int x = 0; x < R; ++x) {
+        const int l = l0 + x * RS;
+        if (l < lim) {
+          const uint32_t at = q16 + tile_off(l, v);
+          for (int r = 0; r < nrep; ++r) sts16(at + r * per * 128, q[x].x, q[x].y, q[x].z, q[x].w);
+          if (v < nrep) q_scale[l + v * per] = __uint_as_float((ex[x] - 14) << 23);   // 1 / f
         }
       }
     }
@@ -778,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if (last >= 0 && !__all_sync(0xffffffffu, wait(&o_free[last & 1], (uint32_t)(last >> 1) & 1, &misc[1]))) { misc[1] = 1; break; }
       if (warp == kQWarp0 && lane == 0) describe_item(k, c, nb);
       const uint32_t q_s = smem_u32(smem + SM::kOffQ + (MIXED ? 0 : (k & 1) * kTile));
-      load_q<D, BF>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale + (k & 1) * kBM, warp - kQWarp0, kQWarps, lane);
+      load_q<D, BF, MIXED>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale + (k & 1) * kBM, warp - kQWarp0, kQWarps, lane, k == 1);
       if (lane == 0) mbar_arrive(&q_full[k & 1]);
       c.advance(p, nb);
     }
@@ -946,14 +951,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const int tl = wq * 32 + lane;                     // TMEM lane
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t sO = tO(grp) + lane_off;
-    float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge) + grp * 96 * kMergePad;
+    float4* merge = reinterpret_cast<float4*>(smem + SM::kOffMerge + grp * kMergeBytes);
     int n0 = 0;
     {
       Cursor c;
       c.load(misc + 2, n_blocks);
       if (threadIdx.x == 0) describe_item(0, c, min(c.nb - c.blk, c.left));
       const uint32_t q_s = smem_u32(smem + SM::kOffQ);
-      load_q<D, BF>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale, warp, kSoftmaxWarps, lane);
+      load_q<D, BF, MIXED>(p, c, q_s, MIXED ? q_s + kTile : q_s, q_scale, warp, kSoftmaxWarps, lane, true);
       if (lane == 0) mbar_arrive(q_first);
     }
     for (int k = 0; n0 < n_blocks; ++k) {
@@ -967,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int l_row = tl & (per - 1);                // row within the tile
       const int rep = tl / per;                        // this lane's replica: chunks c0 ... of the group's four
       const int c0 = 4 * grp + rep * (4 / nrep);
-      // rows behind the last one (zero queries) see what the last one sees: they are never written
+      // rows behind the last one see what the last one sees: they are never written
       const int tok = min((it[4] * kBM + l_row) / p.G, it[1] - 1);
       const int vis_last = min(p.causal ? it[2] - it[1] + tok : it[2] - 1, it[2] - 1);
       // running reference and sum; the sum of chunks with a V scale far from 1 is
@@ -1111,23 +1116,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       group_bar(1, kSoftmaxWarps * 32);
       tc_fence_after();
       // ---- epilogue: both groups' and all replicas' sums of a row joined; group g takes half the dims
-      float M = -INFINITY;
-      for (int x = 0; x < 2 * nrep; ++x) M = fmaxf(M, ml[(x & 1) * kBM + (x >> 1) * per + l_row].x);
-      float l_all = 0.f;
-      for (int x = 0; x < 2 * nrep; ++x) {
-        const float2 y = ml[(x & 1) * kBM + (x >> 1) * per + l_row];
-        l_all += y.x == -INFINITY ? y.y : y.y * fast_exp2(y.x - M);   // the first: 0, or NaN
-      }
+      float M = -INFINITY, l_all = 0.f;
+      float2 y[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) y[x] = x < 2 * nrep ? ml[(x & 1) * kBM + (x >> 1) * per + l_row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) M = fmaxf(M, y[x].x);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) l_all += y[x].x == -INFINITY ? y[x].y : y[x].y * fast_exp2(y[x].x - M);   // the first: 0, or NaN
       const float2 y0 = ml[tl], y1 = ml[kBM + tl];
       const bool have = l_all != 0.f;                  // NaN (from a query that holds one) is not nothing
-      const float inv = have ? 1.f / l_all : 0.f;
+      const float inv = have ? __fdividef(1.f, l_all) : 0.f;   // within 2 units of the last place, as the exponentials are
       const float w0 = (have && y0.x != -INFINITY) ? fast_exp2(y0.x - M) * inv : 0.f;
       const float w1 = (have && y1.x != -INFINITY) ? fast_exp2(y1.x - M) * inv : 0.f;
       const bool whole = it[5] == 0 && nb == it[7];
       const int piece = 2 * blockIdx.x + (it[5] == 0 ? 1 : 0);
-      const bool writes = alive && rep == 0 && l_row < rows;
-      const int lin = it[4] * kBM + l_row, otok = lin / p.G;
-      const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
+      const bool writes = alive && l_row < rows;
+      const size_t orow = writes ? (size_t)(it[0] + tok) * p.Hq + it[3] * p.G + (it[4] * kBM + l_row - tok * p.G) : 0;
 #pragma unroll 1
       for (int x = 0; x < D / 64; ++x) {
         const int col = grp * (D / 2) + x * 32;
@@ -1138,29 +1143,52 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
-        if (nrep > 1) {
-          if (rep > 0) {
-            float4* d = reinterpret_cast<float4*>(merge + ((rep - 1) * per + l_row) * kMergePad);
+        // replica r of a row ends up with the sum of the columns 32 r / nrep ... of all
+        // of them: each writes the other replicas' columns and reads its own
+        auto exchange = [&](auto reps) {
+          constexpr int NR = decltype(reps)::value, V = 8 / NR, PER = kBM / NR;
+          float sum[4 * V];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-          group_bar(2 + grp, kGroupWarps * 32);
-          if (rep == 0) {
-            for (int r = 0; r < nrep - 1; ++r) {
-              const float4* d = reinterpret_cast<const float4*>(merge + (r * per + l_row) * kMergePad);
+          for (int d = 0; d < NR; ++d) {
+            float4* to = merge + ((d * (NR - 1) + rep - (rep > d)) * V) * PER + l_row;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 a = d[e];
-                o[4 * e] += a.x;
-                o[4 * e + 1] += a.y;
-                o[4 * e + 2] += a.z;
-                o[4 * e + 3] += a.w;
+            for (int e = 0; e < V; ++e) {
+              const float* a = o + 4 * (d * V + e);
+              if (rep == d) {
+                sum[4 * e] = a[0]; sum[4 * e + 1] = a[1]; sum[4 * e + 2] = a[2]; sum[4 * e + 3] = a[3];
+              } else {
+                to[e * PER] = make_float4(a[0], a[1], a[2], a[3]);
               }
             }
           }
+          group_bar(2 + grp, kGroupWarps * 32);
+#pragma unroll
+          for (int r = 0; r < NR - 1; ++r) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              const float4 a = merge[((rep * (NR - 1) + r) * V + e) * PER + l_row];
+              sum[4 * e] += a.x; sum[4 * e + 1] += a.y; sum[4 * e + 2] += a.z; sum[4 * e + 3] += a.w;
+            }
+          }
           if (x + 1 < D / 64) group_bar(2 + grp, kGroupWarps * 32);
-        }
-        if (x + 1 == D / 64 && nrep == 1) {
+          if (!writes) return;
+          const int at = col + rep * 4 * V;
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            const float* a = sum + 4 * e;
+            if (!whole) {
+              reinterpret_cast<float4*>(piece_o(p, D, piece))[(at / 4 + e) * kBM + l_row] = make_float4(a[0], a[1], a[2], a[3]);
+            } else if (e % 2 == 0) {
+              uint32_t u[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) u[h] = BF ? pack_bf16x2(a[2 * h], a[2 * h + 1]) : pack_f16x2(a[2 * h], a[2 * h + 1]);
+              *reinterpret_cast<uint4*>(p.out + orow * D + at + 4 * e) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        };
+        if (nrep == 4) { exchange(std::integral_constant<int, 4>{}); continue; }
+        if (nrep == 2) { exchange(std::integral_constant<int, 2>{}); continue; }
+        if (x + 1 == D / 64) {
           // the last of O, (m, l) and the description is in registers: the next
           // item's P.V need not wait for the stores
           tc_fence_before();
@@ -1177,30 +1205,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           uint32_t u[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
-          if (nrep > 1) {
-            uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + col);
+          // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
+          uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (writes) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-          } else {
-            // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
-            uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = e * 8 + lane / 4;
-              const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
-              const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
-              if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
-            }
-            __syncwarp();
+          for (int e = 0; e < 4; ++e) {
+            const int r = e * 8 + lane / 4;
+            const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
+            const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
+            if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
           }
+          __syncwarp();
         }
       }
-      if (writes && grp == 0) {
+      if (writes && grp == 0 && rep == 0) {
         const float lse = have ? M + log2f(l_all) : -INFINITY;
         if (!whole) piece_lse(p, D, piece)[l_row] = lse;
         else if (p.lse2) p.lse2[orow] = lse;
