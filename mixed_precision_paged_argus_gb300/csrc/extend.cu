@@ -57,7 +57,7 @@ constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chu
 constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
 constexpr int kBatches = 4;          // batches whose descriptions are kept
 constexpr int kSlots = kBatch * kBatches;
-constexpr int kMergeBytes = 12 * 1024 + 1536;   // a group's exchange: 4 replicas x 24 columns of 32 rows, or the warps' turned outputs
+constexpr int kMergePad = 36;        // floats per row of the replica merge (32 used; conflict-free vectors)
 
 template <int D>
 struct Smem {
@@ -70,7 +70,7 @@ struct Smem {
   static constexpr int kOffQScale = kOffScale + kSlots * 8 * 16;         // [2][128]
   static constexpr int kOffML = kOffQScale + 2 * kBM * 4;
   static constexpr int kOffMerge = kOffML + 2 * kBM * 8;
-  static constexpr int kOffBar = kOffMerge + 2 * kMergeBytes;
+  static constexpr int kOffBar = kOffMerge + 2 * 96 * kMergePad * 4;
   // q_first, q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
   static constexpr int kNumBars = 14 + 2 * kBatches;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
@@ -472,8 +472,8 @@ __device__ __forceinline__ void store_steps(uint4 (&v)[kSteps], uint32_t tile, i
 // which write zeros where they read nothing); those that become fp16 (TURN: from
 // the tile at q_s to the one at q16, which may be the same unless KEEP) are
 // turned by the lanes that copied them.  Behind the last row the tile gets zeros
-// if `fill`, else keeps what it holds: finite rows of an item before, whose
-// scores nobody uses.
+// if `fill`, else keeps what it holds: rows of an item before, whose scores
+// nobody uses.
 template <int D, bool TURN, bool KEEP>
 __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32_t q_s, uint32_t q16, float* q_scale, int w, int nw, int lane,
                                        bool fill) {
@@ -486,11 +486,11 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
   int g = lin0 + r0 - tok * p.G;
   const uint16_t* src = p.q + (long long)(c.s.q0 + tok) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
   const long long step = dt * p.qs + dg * D, wrap = p.qs - (long long)p.G * D;
-#pragma unroll 4
+#pragma unroll 1
   for (int l = r0; l < lim; l += RS) {
     const bool real = l < rows;
-    const uint32_t at = q_s + tile_off(l, v);            // a copy is per rows of 128 bytes further, with the same permutation
-    for (int r = 0; r < ncopy; ++r) cp_async16(at + r * per * 128, real ? src : p.q, real ? 16 : 0);
+#pragma unroll 1
+    for (int r = 0; r < ncopy; ++r) cp_async16(q_s + tile_off(l + r * per, v), real ? src : p.q, real ? 16 : 0);
     src += step;
     g += dg;
     if (g >= p.G) {
@@ -531,13 +531,15 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
           w[e] = pack_f16x2(a, b);
         }
       }
+#pragma unroll 1
+      for (int r = 0; r < nrep; ++r) {
 #pragma unroll
-      for (int x = 0; x < R; ++x) {
-        const int l = l0 + x * RS;
-        if (l < lim) {
-          const uint32_t at = q16 + tile_off(l, v);
-          for (int r = 0; r < nrep; ++r) sts16(at + r * per * 128, q[x].x, q[x].y, q[x].z, q[x].w);
-          if (v < nrep) q_scale[l + v * per] = __uint_as_float((ex[x] - 14) << 23);   // 1 / f
+        for (int x = 0; x < R; ++x) {
+          const int l = l0 + x * RS;
+          if (l < lim) {
+            sts16(q16 + tile_off(l + r * per, v), q[x].x, q[x].y, q[x].z, q[x].w);
+            if (v == 0) q_scale[l + r * per] = __uint_as_float((ex[x] - 14) << 23);   // 1 / f
+          }
         }
       }
     }
@@ -951,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const int tl = wq * 32 + lane;                     // TMEM lane
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
     const uint32_t sO = tO(grp) + lane_off;
-    float4* merge = reinterpret_cast<float4*>(smem + SM::kOffMerge + grp * kMergeBytes);
+    float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge) + grp * 96 * kMergePad;
     int n0 = 0;
     {
       Cursor c;
@@ -1126,13 +1128,14 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       for (int x = 0; x < 8; ++x) l_all += y[x].x == -INFINITY ? y[x].y : y[x].y * fast_exp2(y[x].x - M);   // the first: 0, or NaN
       const float2 y0 = ml[tl], y1 = ml[kBM + tl];
       const bool have = l_all != 0.f;                  // NaN (from a query that holds one) is not nothing
-      const float inv = have ? __fdividef(1.f, l_all) : 0.f;   // within 2 units of the last place, as the exponentials are
+      const float inv = have ? 1.f / l_all : 0.f;
       const float w0 = (have && y0.x != -INFINITY) ? fast_exp2(y0.x - M) * inv : 0.f;
       const float w1 = (have && y1.x != -INFINITY) ? fast_exp2(y1.x - M) * inv : 0.f;
       const bool whole = it[5] == 0 && nb == it[7];
       const int piece = 2 * blockIdx.x + (it[5] == 0 ? 1 : 0);
-      const bool writes = alive && l_row < rows;
-      const size_t orow = writes ? (size_t)(it[0] + tok) * p.Hq + it[3] * p.G + (it[4] * kBM + l_row - tok * p.G) : 0;
+      const bool writes = alive && rep == 0 && l_row < rows;
+      const int lin = it[4] * kBM + l_row, otok = lin / p.G;
+      const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
       for (int x = 0; x < D / 64; ++x) {
         const int col = grp * (D / 2) + x * 32;
@@ -1143,52 +1146,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         tmem_wait_ld();
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
-        // replica r of a row ends up with the sum of the columns 32 r / nrep ... of all
-        // of them: each writes the other replicas' columns and reads its own
-        auto exchange = [&](auto reps) {
-          constexpr int NR = decltype(reps)::value, V = 8 / NR, PER = kBM / NR;
-          float sum[4 * V];
+        if (nrep > 1) {
+          if (rep > 0) {
+            float4* d = reinterpret_cast<float4*>(merge + ((rep - 1) * per + l_row) * kMergePad);
 #pragma unroll
-          for (int d = 0; d < NR; ++d) {
-            float4* to = merge + ((d * (NR - 1) + rep - (rep > d)) * V) * PER + l_row;
+            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          group_bar(2 + grp, kGroupWarps * 32);
+          if (rep == 0) {
+#pragma unroll 1
+            for (int r = 0; r < nrep - 1; ++r) {
+              const float4* d = reinterpret_cast<const float4*>(merge + (r * per + l_row) * kMergePad);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float* a = o + 4 * (d * V + e);
-              if (rep == d) {
-                sum[4 * e] = a[0]; sum[4 * e + 1] = a[1]; sum[4 * e + 2] = a[2]; sum[4 * e + 3] = a[3];
-              } else {
-                to[e * PER] = make_float4(a[0], a[1], a[2], a[3]);
+              for (int e = 0; e < 8; ++e) {
+                const float4 a = d[e];
+                o[4 * e] += a.x;
+                o[4 * e + 1] += a.y;
+                o[4 * e + 2] += a.z;
+                o[4 * e + 3] += a.w;
               }
             }
           }
-          group_bar(2 + grp, kGroupWarps * 32);
-#pragma unroll
-          for (int r = 0; r < NR - 1; ++r) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              const float4 a = merge[((rep * (NR - 1) + r) * V + e) * PER + l_row];
-              sum[4 * e] += a.x; sum[4 * e + 1] += a.y; sum[4 * e + 2] += a.z; sum[4 * e + 3] += a.w;
-            }
-          }
           if (x + 1 < D / 64) group_bar(2 + grp, kGroupWarps * 32);
-          if (!writes) return;
-          const int at = col + rep * 4 * V;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float* a = sum + 4 * e;
-            if (!whole) {
-              reinterpret_cast<float4*>(piece_o(p, D, piece))[(at / 4 + e) * kBM + l_row] = make_float4(a[0], a[1], a[2], a[3]);
-            } else if (e % 2 == 0) {
-              uint32_t u[4];
-#pragma unroll
-              for (int h = 0; h < 4; ++h) u[h] = BF ? pack_bf16x2(a[2 * h], a[2 * h + 1]) : pack_f16x2(a[2 * h], a[2 * h + 1]);
-              *reinterpret_cast<uint4*>(p.out + orow * D + at + 4 * e) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-          }
-        };
-        if (nrep == 4) { exchange(std::integral_constant<int, 4>{}); continue; }
-        if (nrep == 2) { exchange(std::integral_constant<int, 2>{}); continue; }
-        if (x + 1 == D / 64) {
+        }
+        if (x + 1 == D / 64 && nrep == 1) {
           // the last of O, (m, l) and the description is in registers: the next
           // item's P.V need not wait for the stores
           tc_fence_before();
@@ -1205,23 +1186,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           uint32_t u[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
-          // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
-          uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
+          if (nrep > 1) {
+            uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + col);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
-          __syncwarp();
+            for (int e = 0; e < 4; ++e)
+              if (writes) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+          } else {
+            // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
+            uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = e * 8 + lane / 4;
-            const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
-            const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
-            if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = e * 8 + lane / 4;
+              const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
+              const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
+              if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
-      if (writes && grp == 0 && rep == 0) {
+      if (writes && grp == 0) {
         const float lse = have ? M + log2f(l_all) : -INFINITY;
         if (!whole) piece_lse(p, D, piece)[l_row] = lse;
         else if (p.lse2) p.lse2[orow] = lse;
