@@ -57,7 +57,7 @@ constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chu
 constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
 constexpr int kBatches = 4;          // batches whose descriptions are kept
 constexpr int kSlots = kBatch * kBatches;
-constexpr int kMergePad = 36;        // floats per row of the replica merge (32 used; conflict-free vectors)
+constexpr int kMergePad = 20;        // floats per row of the replica merge (16 used; conflict-free vectors)
 
 template <int D>
 struct Smem {
@@ -1137,20 +1137,20 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int lin = it[4] * kBM + l_row, otok = lin / p.G;
       const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
-      for (int x = 0; x < D / 64; ++x) {
-        const int col = grp * (D / 2) + x * 32;
-        uint32_t v0[32], v1[32];
-        float o[32];
-        tmem_ld32(tO(0) + lane_off + col, v0);
-        tmem_ld32(tO(1) + lane_off + col, v1);
+      for (int x = 0; x < D / 32; ++x) {                 // short code: every item runs through it once, out of a cold cache
+        const int col = grp * (D / 2) + x * 16;
+        uint32_t v0[16], v1[16];
+        float o[16];
+        tmem_ld16(tO(0) + lane_off + col, v0);
+        tmem_ld16(tO(1) + lane_off + col, v1);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
+        for (int e = 0; e < 16; ++e) o[e] = fmaf(w0, __uint_as_float(v0[e]), w1 * __uint_as_float(v1[e]));
         if (nrep > 1) {
           if (rep > 0) {
             float4* d = reinterpret_cast<float4*>(merge + ((rep - 1) * per + l_row) * kMergePad);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) d[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
           }
           group_bar(2 + grp, kGroupWarps * 32);
           if (rep == 0) {
@@ -1158,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
             for (int r = 0; r < nrep - 1; ++r) {
               const float4* d = reinterpret_cast<const float4*>(merge + (r * per + l_row) * kMergePad);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
+              for (int e = 0; e < 4; ++e) {
                 const float4 a = d[e];
                 o[4 * e] += a.x;
                 o[4 * e + 1] += a.y;
@@ -1167,9 +1167,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
               }
             }
           }
-          if (x + 1 < D / 64) group_bar(2 + grp, kGroupWarps * 32);
+          if (x + 1 < D / 32) group_bar(2 + grp, kGroupWarps * 32);
         }
-        if (x + 1 == D / 64 && nrep == 1) {
+        if (x + 1 == D / 32 && nrep == 1) {
           // the last of O, (m, l) and the description is in registers: the next
           // item's P.V need not wait for the stores
           tc_fence_before();
@@ -1180,30 +1180,30 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
           // columns by rows: 32 lanes, 512 bytes
           float4* d = reinterpret_cast<float4*>(piece_o(p, D, piece)) + (col / 4) * kBM + l_row;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 4; ++e)
             if (writes) d[e * kBM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         } else {
-          uint32_t u[16];
+          uint32_t u[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
+          for (int e = 0; e < 8; ++e) u[e] = BF ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : pack_f16x2(o[2 * e], o[2 * e + 1]);
           if (nrep > 1) {
             uint4* d = reinterpret_cast<uint4*>(p.out + orow * D + col);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 2; ++e)
               if (writes) d[e] = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
           } else {
-            // turned over in the (unused) merge area, so that four lanes store a row's 64 bytes
-            uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 20;
+            // turned over in the (unused) merge area, so that two lanes store a row's 32 bytes
+            uint32_t* mine = reinterpret_cast<uint32_t*>(smem + SM::kOffMerge) + warp * 32 * 12;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(mine + lane * 20 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(mine + lane * 12 + 4 * e) = make_uint4(u[4 * e], u[4 * e + 1], u[4 * e + 2], u[4 * e + 3]);
             __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = e * 8 + lane / 4;
-              const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 20 + 4 * (lane & 3));
+            for (int e = 0; e < 2; ++e) {
+              const int r = e * 16 + lane / 2;
+              const uint4 y = *reinterpret_cast<const uint4*>(mine + r * 12 + 4 * (lane & 1));
               const unsigned long long to = __shfl_sync(0xffffffffu, (unsigned long long)(writes ? orow : ~0ull), r);
-              if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 3)) = y;
+              if (to != ~0ull) *reinterpret_cast<uint4*>(p.out + to * D + col + 8 * (lane & 1)) = y;
             }
             __syncwarp();
           }
