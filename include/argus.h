@@ -435,14 +435,17 @@ argus_status argus_staging_moves_less(const int64_t* row_read_bytes, int64_t n_r
  * finite; whatever the last page holds behind them is not used.
  * seq_lens[b] is clamped to [0, max_pages * P], q_start[] to [0, total_q].
  *
- * Precision: the codes of a page are exact in the query's type, in which Q.K^T
- * and P.V run on the tensor cores with fp32 accumulation; p_j (times the
- * page's V scale) is rounded to the query's type (half a step, 2^-8 of its
- * value for BF16, 2^-11 for FP16); maxima, sums and the accumulators are fp32.
+ * Precision: Q.K^T and P.V run on the tensor cores with fp32 accumulation, in
+ * BF16 where a block of 128 positions holds BF16 pages, else in FP16.  The codes of a
+ * page are exact in both; a BF16 query becomes FP16 times a power of two per row
+ * (elements below 2^-31 of the row's largest lose bits).  p_j (times the page's V
+ * scale) is rounded to that type: half a step, 2^-8 of its value for BF16, 2^-11
+ * for FP16, there at least 2^-32 of the row's largest.  Maxima, sums and the
+ * accumulators are fp32.  A NaN in a query row stays in that row.
  *
- * Arguments: q device [total_q] tokens of [Hq][D] (16-byte aligned; tokens
- * q_stride elements apart, a multiple of 8, 0 = Hq * D: rows of a fused
- * projection are read in place); out device [total_q][Hq][D] of q_dtype
+ * Arguments: q device [total_q] tokens of [Hq][D] (16-byte aligned, not
+ * overlapping out; tokens q_stride elements apart, a multiple of 8, 0 = Hq * D:
+ * rows of a fused projection are read in place); out device [total_q][Hq][D] of q_dtype
  * (16-byte aligned); lse2_out device [total_q][Hq] or NULL.  Rows of out
  * that belong to no sequence are left as they were.  Supported: head_dim 64 or
  * 128, G from 1 to 8, batch <= 65535, total_q * Hq < 2^31.  ws (16-byte
@@ -563,6 +566,8 @@ argus_status argus_rope_append(const argus_rope_args* args, void* stream);
  * (clamped to it).
  * The output arrays must not be the input arrays (ARGUS_E_INVALID), so a
  * captured call can be replayed and two table copies alternate.
+ * ws of argus_fork_workspace_bytes bytes (16-byte aligned): no initialisation, not to be
+ * shared by calls that overlap on the GPU.
  * Arguments: pools host array in device memory (placement DEVICE, else
  * ARGUS_E_UNSUPPORTED), at most one per codec, n_slots < 2^31; ref_in, ref_out
  * host arrays of n_pools device int32 [n_slots]; parents, n_new (NULL = 0)
@@ -592,7 +597,8 @@ argus_status argus_fork_pages(const argus_geom* g, int32_t batch, const int32_t*
  * A negative count is taken as 0.  Entries that name no slot of the pool are
  * copied and counted in *status.
  * ref_out and block_table_out must not be the input arrays.
- * ws of argus_compact_workspace_bytes bytes.  The pool lies in device memory.
+ * ws of argus_compact_workspace_bytes bytes (16-byte aligned): no initialisation, not to be
+ * shared by calls that overlap on the GPU.  The pool lies in device memory.
  * ------------------------------------------------------------------------- */
 argus_status argus_compact_workspace_bytes(const argus_pool* pool, size_t* bytes);
 
