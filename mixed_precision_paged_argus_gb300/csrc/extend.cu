@@ -40,7 +40,7 @@
 // MMAs alone 0.67 ms.  BF16, FP8 and INT8 pages mixed, 8 sequences of up to 16,384
 // with 1 to 256 new tokens: 243 us (the same in FP8 alone 151, INT8 218, BF16 314: a
 // 16-bit page is twice the bytes for every query tile).
-// Per-item cost is what bounds short sequences (1,024 of 64 tokens: 273 us): its code
+// Per-item cost is what bounds short sequences (1,024 of 64 tokens: 260 us): its code
 // runs once per item, out of a cold instruction cache, hence the rolled loops in
 // load_q and the epilogue (unrolled as far as registers allow: mixed tiers 259 us, cross
 // attention over INT8 53 instead of 49, the chunk 1.03 ms).
@@ -76,6 +76,7 @@ struct EParams {
   float scale_log2;
   int n_ctas;
   int last_query[8];                 // (128 (r + 1) - 1) / G: the query of tile r's last row
+  uint32_t g_mul, g_shift;           // division by G (group_of)
   float* ws;                         // pieces: o [2 n_ctas][128][D], then lse2 [2 n_ctas][128]; cuts [n_ctas]
 };
 
@@ -137,6 +138,14 @@ struct Seq {
   int q0, n, len;
 };
 
+// x / G for 0 <= x < 2^31.  With s = ceil(log2 G) and mul = ceil(2^(31 + s) / G), mul G
+// is above 2^(31 + s) by less than 2^s, so x mul is above x 2^(31 + s) / G by less
+// than 2^(31 + s) / G: the quotient's whole part is the same.  (A division takes some
+// twenty instructions, at eight places of the code that every item runs through.)
+__device__ __forceinline__ int group_of(const EParams& p, int x) {
+  return p.g_mul ? (int)(__umulhi((uint32_t)x, p.g_mul) >> p.g_shift) : x;
+}
+
 __device__ __forceinline__ Seq load_seq(const EParams& p, int b) {
   Seq s;
   const int a = min(max(p.q_start[b], 0), p.total_q), e = min(max(p.q_start[b + 1], 0), p.total_q);
@@ -153,7 +162,7 @@ __device__ __forceinline__ int n_tiles(const EParams& p, const Seq& s) { return 
 __device__ __forceinline__ int tile_blocks(const EParams& p, const Seq& s, int t) {
   int keys = s.len;
   if (p.causal) {
-    const int last = min((int)(((uint32_t)kBM * (t + 1) - 1) / (uint32_t)p.G), s.n - 1);   // rows: fewer than 2^31
+    const int last = min(group_of(p, (int)((uint32_t)kBM * (t + 1) - 1)), s.n - 1);   // rows: fewer than 2^31
     keys = max(s.len - s.n, 0) + last + 1;
   }
   return max(1, (keys + kBN - 1) / kBN);
@@ -168,7 +177,7 @@ __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& 
   const int T = n_tiles(p, s);
   const int f = min(m, T - 1);
   const uint32_t base = (uint32_t)max(s.len - s.n, 0) + kBN;
-  const int a = f / p.G, rem = f - a * p.G;
+  const int a = group_of(p, f), rem = f - a * p.G;
   long long sum = 0;
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
@@ -526,7 +535,7 @@ __device__ __forceinline__ void load_q(const EParams& p, const Cursor& c, uint32
   const int lin0 = c.t * kBM, rows = min(kBM, c.s.n * p.G - lin0);
   const int nrep = replicas(rows), per = kBM / nrep, lim = fill ? per : rows;
   const int ncopy = TURN && !KEEP ? 1 : nrep;            // the turned rows are copied below
-  const int tok = (int)((uint32_t)(lin0 + r0) / (uint32_t)p.G), dt = RS / p.G, dg = RS - dt * p.G;
+  const int tok = group_of(p, lin0 + r0), dt = group_of(p, RS), dg = RS - dt * p.G;
   int g = lin0 + r0 - tok * p.G;
   const uint16_t* src = p.q + (long long)(c.s.q0 + tok) * p.qs + (long long)(c.h * p.G + g) * D + v * 8;
   const long long step = dt * p.qs + dg * D, wrap = p.qs - (long long)p.G * D;
@@ -1019,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const int rep = tl / per;                        // this lane's replica: chunks c0 ... of the group's four
       const int c0 = 4 * grp + rep * (4 / nrep);
       // rows behind the last one see what the last one sees: they are never written
-      const int tok = min((it[4] * kBM + l_row) / p.G, it[1] - 1);
+      const int tok = min(group_of(p, it[4] * kBM + l_row), it[1] - 1);
       const int vis_last = min(p.causal ? it[2] - it[1] + tok : it[2] - 1, it[2] - 1);
       // running reference and sum; the sum of chunks with a V scale far from 1 is
       // kept apart, with a reference of its own: relative to m (which bounds p
@@ -1178,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       const bool whole = it[5] == 0 && nb == it[7];
       const int piece = 2 * blockIdx.x + (it[5] == 0 ? 1 : 0);
       const bool writes = alive && rep == 0 && l_row < rows;
-      const int lin = it[4] * kBM + l_row, otok = lin / p.G;
+      const int lin = it[4] * kBM + l_row, otok = group_of(p, lin);
       const size_t orow = writes ? (size_t)(it[0] + otok) * p.Hq + it[3] * p.G + (lin - otok * p.G) : 0;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {                 // short code: every item runs through it once, out of a cold cache
@@ -1320,7 +1329,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const EParams p) 
       o.w = fmaf(w, v[y].w, o.w);
     }
   }
-  const int lin = cut.row0 + row, tok = lin / p.G;
+  const int lin = cut.row0 + row, tok = group_of(p, lin);
   const size_t orow = (size_t)(cut.q0 + tok) * p.Hq + cut.head0 + (lin - tok * p.G);
   const float inv = sum != 0.f ? 1.f / sum : 0.f;
   uint2 u;
@@ -1475,6 +1484,12 @@ extern "C" argus_status argus_paged_extend_attn(const argus_extend_args* a, void
   p.scale_log2 = (float)((double)a->softmax_scale * 1.4426950408889634);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.n_ctas = extend::grid_size(a);
+  int bits = 0;
+  while ((1 << bits) < p.G) ++bits;
+  if (bits) {
+    p.g_mul = (uint32_t)(((1ull << (31 + bits)) + p.G - 1) / p.G);
+    p.g_shift = bits - 1;
+  }
   for (int r = 0; r < 8; ++r) p.last_query[r] = (extend::kBM * (r + 1) - 1) / p.G;
   if (extend::max_blocks(a) / p.n_ctas >= 0x7fffffffll) return fail(ARGUS_E_UNSUPPORTED, "extend: too many key blocks");
   p.ws = static_cast<float*>(ws);
