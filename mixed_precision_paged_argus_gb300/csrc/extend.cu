@@ -38,12 +38,12 @@
 // 131,072 FP8 tokens, 16/2 heads of 128: 1.02 ms, 1.08 PFLOP/s (56% of cuBLAS bf16);
 // with neither softmax nor MMAs the loads and conversions alone took 0.71 ms, the
 // MMAs alone 0.67 ms.  BF16, FP8 and INT8 pages mixed, 8 sequences of up to 16,384
-// with 1 to 256 new tokens: 243 us (the same in FP8 alone 151, INT8 218, BF16 314: a
+// with 1 to 256 new tokens: 240 us (the same in FP8 alone 150, INT8 215, BF16 314: a
 // 16-bit page is twice the bytes for every query tile).
 // Per-item cost is what bounds short sequences (1,024 of 64 tokens: 260 us): its code
 // runs once per item, out of a cold instruction cache, hence the rolled loops in
-// load_q and the epilogue (unrolled as far as registers allow: mixed tiers 259 us, cross
-// attention over INT8 53 instead of 49, the chunk 1.03 ms).
+// load_q and the epilogue (unrolled as far as registers allow, mixed tiers took 259 us and cross
+// attention over 1 to 1,500 INT8 states 53 instead of 47).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

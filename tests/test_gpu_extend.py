@@ -198,6 +198,19 @@ def test_nan_queries_stay_in_their_rows(dtype, codec):
     assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], clean_lse[~hit])
 
 
+@pytest.mark.parametrize("dtype,codecs", [(W.FP16, [F8]), (W.BF16, [F8]), (W.BF16, [W.BF16, F8])])
+def test_nan_queries_do_not_reach_later_items(dtype, codecs):
+    """Every CTA takes many items, long ones with NaN rows before short ones whose tiles hold fewer rows."""
+    lens, new = [70, 40, 60, 33] * 200, [32, 3, 17, 1] * 200
+    c = make(4, 1, 64, 16, lens, new, codecs, dtype, seed=176)
+    clean, clean_lse = run(c, True)
+    long = torch.from_numpy(np.repeat(np.array(new) > 16, new)).to(DEV)
+    c.q[long] = float("nan")
+    out, lse = run(c, True)
+    assert torch.isnan(out[long]).all() and torch.isnan(lse[long]).all()
+    assert torch.equal(out[~long], clean[~long]) and torch.equal(lse[~long], clean_lse[~long])
+
+
 def test_strided_queries():
     c = make(8, 2, 128, 16, [100, 300], [3, 9], [F8], W.BF16, seed=180)
     wide = torch.full((12, 12, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
