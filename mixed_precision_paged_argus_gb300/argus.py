@@ -436,7 +436,11 @@ def _ws_at(ws, device):
     return ws.data_ptr()
 
 
+# the structs' layouts, field by field: packing takes a third of the time of building one by its fields
 _POOL_DESC = struct.Struct("@iiPPq")
+_EXTEND_ARGS = struct.Struct("@4i4iPqPPiiPPPPPPf0P")
+_ROPE_ARGS = struct.Struct("@4i6i4P4q8PiP")
+assert [x.size for x in (_POOL_DESC, _EXTEND_ARGS, _ROPE_ARGS)] == [ctypes.sizeof(x) for x in (PoolDesc, ExtendArgs, RopeArgs)]
 
 
 def _pool_array(pools, device=None):
@@ -465,12 +469,13 @@ def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pag
     apart), q_start [B + 1], seq_lens [B], out like q and dense."""
     batch, total, hq, dev = q_start.numel() - 1, q.shape[0], g.n_q_heads, q.get_device()
     arr = _pool_array(pools, dev)
-    a = ExtendArgs(g, batch, total, DTYPE_CODEC[q.dtype], 1 if causal else 0, q.data_ptr(),
-                   _token_stride("q", q, hq, g.head_dim, dev), _at("q_start", q_start, _I32, 1, dev), arr, len(pools), max_pages,
-                   _at("page_codec", page_codec, _U8, batch * max_pages, dev),
-                   _at("block_table", block_table, _I32, batch * max_pages, dev), _at("seq_lens", seq_lens, _I32, batch, dev),
-                   _at("out", out, q.dtype, q.numel(), dev), _at("lse2_out", lse2_out, _F32, total * hq, dev),
-                   _status_at(status, dev), softmax_scale)
+    a = ExtendArgs.from_buffer_copy(_EXTEND_ARGS.pack(
+        hq, g.n_kv_heads, g.head_dim, g.page_tokens, batch, total, DTYPE_CODEC[q.dtype], 1 if causal else 0, q.data_ptr(),
+        _token_stride("q", q, hq, g.head_dim, dev), _at("q_start", q_start, _I32, 1, dev) or 0, ctypes.addressof(arr), len(pools),
+        max_pages, _at("page_codec", page_codec, _U8, batch * max_pages, dev) or 0,
+        _at("block_table", block_table, _I32, batch * max_pages, dev) or 0, _at("seq_lens", seq_lens, _I32, batch, dev) or 0,
+        _at("out", out, q.dtype, q.numel(), dev) or 0, _at("lse2_out", lse2_out, _F32, total * hq, dev) or 0,
+        _status_at(status, dev) or 0, softmax_scale))
     # the struct holds raw pointers: keep every tensor it points to alive with it
     a._keep = (arr, pools, q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
     a._device = dev
@@ -502,14 +507,16 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
     if k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype:
         raise ValueError("rope_append: q, k, v and q_out must have the same type")
     half = inv_freq.numel()
-    a = RopeArgs(g, batch, total, DTYPE_CODEC[dtype], 2 * half, 1 if adjacent else 0, positions.numel() // total if total else 1,
-                 q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), _token_stride("q", q, hq, d, dev),
-                 _token_stride("k", k, hkv, d, dev), _token_stride("v", v, hkv, d, dev),
-                 _token_stride("q_out", q_out, hq, d, dev), _at("positions", positions, _I32, 0, dev),
-                 _at("inv_freq", inv_freq, torch.float64, 0, dev), _at("pair_axis", pair_axis, _U8, half, dev),
-                 _at("q_start", q_start, _I32, 1, dev), _at("seq_lens", seq_lens, _I32, batch, dev), _pool_array((pool,), dev),
-                 _at("page_codec", page_codec, _U8, batch * max_pages, dev),
-                 _at("block_table", block_table, _I32, batch * max_pages, dev), max_pages, _status_at(status, dev))
+    arr = _pool_array((pool,), dev)
+    a = RopeArgs.from_buffer_copy(_ROPE_ARGS.pack(
+        hq, hkv, d, g.page_tokens, batch, total, DTYPE_CODEC[dtype], 2 * half, 1 if adjacent else 0,
+        positions.numel() // total if total else 1, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+        _token_stride("q", q, hq, d, dev), _token_stride("k", k, hkv, d, dev), _token_stride("v", v, hkv, d, dev),
+        _token_stride("q_out", q_out, hq, d, dev), _at("positions", positions, _I32, 0, dev) or 0,
+        _at("inv_freq", inv_freq, torch.float64, 0, dev) or 0, _at("pair_axis", pair_axis, _U8, half, dev) or 0,
+        _at("q_start", q_start, _I32, 1, dev) or 0, _at("seq_lens", seq_lens, _I32, batch, dev) or 0, ctypes.addressof(arr),
+        _at("page_codec", page_codec, _U8, batch * max_pages, dev) or 0,
+        _at("block_table", block_table, _I32, batch * max_pages, dev) or 0, max_pages, _status_at(status, dev) or 0))
     _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(dev, stream)))
 
 

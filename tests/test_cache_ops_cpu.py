@@ -32,6 +32,24 @@ def test_binding_structs_match_the_header_layout(cls, struct, tmp_path):
     assert [getattr(cls, n).offset for n in names] == offs
 
 
+@pytest.mark.parametrize("cls,packed", [(argus.ExtendArgs, argus._EXTEND_ARGS), (argus.RopeArgs, argus._ROPE_ARGS),
+                                        (argus.PoolDesc, argus._POOL_DESC)])
+def test_packed_fields_land_where_the_struct_has_them(cls, packed):
+    n = len(packed.unpack(bytes(packed.size)))
+    a, at = cls.from_buffer_copy(packed.pack(*range(1, n + 1))), 1
+    for name, kind in cls._fields_:
+        x = getattr(a, name)
+        if kind is argus.Geom:
+            assert [getattr(x, f) for f, _ in kind._fields_] == list(range(at, at + 4))
+            at += 4
+            continue
+        if kind is ctypes.POINTER(argus.PoolDesc):
+            x = ctypes.cast(x, ctypes.c_void_p).value
+        assert x == at, name
+        at += 1
+    assert at == n + 1 and ctypes.sizeof(a) == packed.size
+
+
 # ---- refusals: every pointer below is a made-up, aligned number that no call may touch
 
 def _pools(*descs):
