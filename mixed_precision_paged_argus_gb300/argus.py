@@ -393,7 +393,11 @@ def _token_stride(name, t, heads, head_dim, device):
         raise ValueError("%s: the heads of a token must be dense" % name)
     if t.get_device() != device:
         raise ValueError("%s lies on another device" % name)
-    return stride[0] if shape[0] > 1 else heads * head_dim
+    if shape[0] <= 1:
+        return heads * head_dim
+    if stride[0] < heads * head_dim:     # 0 among them (a broadcast token), which the library reads as "dense"
+        raise ValueError("%s: the tokens overlap in memory" % name)
+    return stride[0]
 
 
 def _at(name, t, dtype, numel, device):
