@@ -447,16 +447,50 @@ _ROPE_ARGS = struct.Struct("@4i6i4P4q8PiP")
 assert [x.size for x in (_POOL_DESC, _EXTEND_ARGS, _ROPE_ARGS)] == [ctypes.sizeof(x) for x in (PoolDesc, ExtendArgs, RopeArgs)]
 
 
-def _pool_array(pools, device=None):
-    """The pools' descriptions; device pools on the device, if one is given (host
-    pools are the library's to refuse)."""
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
+
+# per codec: bits of a code, its float type if it has one, the meta's type
+_LAYOUT = {FP16: (16, torch.float16, None), BF16: (16, torch.bfloat16, None), FP8_E4M3: (8, torch.float8_e4m3fn, _F32),
+           INT8: (8, None, _F32), INT4_G32: (4, None, torch.float16), INT2_G32: (2, None, torch.float16), INT1_G32: (1, None, torch.float16)}
+
+
+def _check_pool(p, units, values, device):
+    """A device pool holds n_slots pages, dense, in its codec's types (or integers: their bits); a page has
+    `units` units (a KV head's K or V) of `values` values together.  On the device a slot is compared with n_slots alone."""
+    codec, codes, meta, n = p.codec, p.codes, p.meta, p.n_slots
+    if codec not in _LAYOUT:
+        return                               # the library refuses the codec
+    bits, code_type, meta_type = _LAYOUT[codec]
+    if codes is not None:
+        if codes.get_device() != device:
+            raise ValueError("a pool lies on another device")
+        if codes.nbytes * 8 < n * values * bits or not codes.is_contiguous():
+            raise ValueError("the pool of codec %d: codes must be a dense tensor of n_slots pages of this geometry" % codec)
+        kind = codes.dtype
+        if kind is not _U8 and kind is not code_type and kind.is_floating_point:
+            raise ValueError("the pool of codec %d: codes of type %s" % (codec, kind))
+    if meta is not None and meta_type is not None:
+        if meta.get_device() != device:
+            raise ValueError("a pool lies on another device")
+        # a float per unit, or two halves per 32 values
+        if meta.nbytes < n * (4 * units if meta_type is _F32 else values // 8) or not meta.is_contiguous():
+            raise ValueError("the pool of codec %d: meta must be a dense tensor for n_slots pages of this geometry" % codec)
+        kind = meta.dtype
+        if kind is not meta_type and kind.is_floating_point:
+            raise ValueError("the pool of codec %d: meta of type %s" % (codec, kind))
+
+
+def _pool_array(pools, device=None, g=None):
+    """The pools' descriptions; with a geometry, device pools are checked against it
+    and the device (host pools are the library's to refuse)."""
     raw = []
+    if g is not None:
+        units = 2 * g.n_kv_heads
+        values = units * g.page_tokens * g.head_dim
     for p in pools:
         codes, meta = p.codes, p.meta
-        if device is not None and p.placement == PLACE_DEVICE:
-            for t in (codes, meta):
-                if t is not None and t.get_device() != device:
-                    raise ValueError("a pool lies on another device")
+        if g is not None and p.placement == PLACE_DEVICE:
+            _check_pool(p, units, values, device)
         raw.append(_POOL_DESC.pack(p.codec, p.placement, 0 if codes is None else codes.data_ptr(),
                                    0 if meta is None else meta.data_ptr(), p.n_slots))
     if not raw:
@@ -464,15 +498,12 @@ def _pool_array(pools, device=None):
     return (PoolDesc * len(raw)).from_buffer_copy(b"".join(raw))
 
 
-_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
-
-
 def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pages, softmax_scale, out,
                 causal=True, lse2_out=None, status=None):
     """Build an argus_extend_args struct: q [total_q][Hq][D] (its tokens may lie
     apart), q_start [B + 1], seq_lens [B], out like q and dense."""
     batch, total, hq, dev = q_start.numel() - 1, q.shape[0], g.n_q_heads, q.get_device()
-    arr = _pool_array(pools, dev)
+    arr = _pool_array(pools, dev, g)
     a = ExtendArgs.from_buffer_copy(_EXTEND_ARGS.pack(
         hq, g.n_kv_heads, g.head_dim, g.page_tokens, batch, total, DTYPE_CODEC[q.dtype], 1 if causal else 0, q.data_ptr(),
         _token_stride("q", q, hq, g.head_dim, dev), _at("q_start", q_start, _I32, 1, dev) or 0, ctypes.addressof(arr), len(pools),
@@ -511,7 +542,7 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
     if k.dtype is not dtype or v.dtype is not dtype or q_out.dtype is not dtype:
         raise ValueError("rope_append: q, k, v and q_out must have the same type")
     half = inv_freq.numel()
-    arr = _pool_array((pool,), dev)
+    arr = _pool_array((pool,), dev, g)
     a = RopeArgs.from_buffer_copy(_ROPE_ARGS.pack(
         hq, hkv, d, g.page_tokens, batch, total, DTYPE_CODEC[dtype], 2 * half, 1 if adjacent else 0,
         positions.numel() // total if total else 1, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
@@ -545,7 +576,7 @@ def fork_pages(g, parents, n_new, new_codec, pools, ref_in, ref_out, page_codec,
     entries = batch * max_pages
     _check(lib().argus_fork_pages(
         ctypes.byref(g), batch, _at("parents", parents, _I32, 0, dev), _at("n_new", n_new, _I32, batch, dev), new_codec,
-        _pool_array(pools, dev), n, rin, rout, _at("page_codec", page_codec, _U8, entries, dev),
+        _pool_array(pools, dev, g), n, rin, rout, _at("page_codec", page_codec, _U8, entries, dev),
         _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, batch, dev),
         _at("page_codec_out", page_codec_out, _U8, entries, dev), _at("block_table_out", block_table_out, _I32, entries, dev),
         _at("seq_lens_out", seq_lens_out, _I32, batch, dev), max_pages, _ws_at(ws, dev), ws.nbytes, _status_at(status, dev),
@@ -566,7 +597,7 @@ def compact_pages(g, pool, ref_in, ref_out, page_codec, block_table, seq_lens, b
     batch, dev = seq_lens.numel(), seq_lens.get_device()
     entries = batch * max_pages
     _check(lib().argus_compact_pages(
-        ctypes.byref(g), batch, _pool_array((pool,), dev), _at("ref_in", ref_in, _I32, pool.n_slots, dev),
+        ctypes.byref(g), batch, _pool_array((pool,), dev, g), _at("ref_in", ref_in, _I32, pool.n_slots, dev),
         _at("ref_out", ref_out, _I32, pool.n_slots, dev), _at("page_codec", page_codec, _U8, entries, dev),
         _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, 0, dev),
         _at("block_table_out", block_table_out, _I32, entries, dev), max_pages, _at("n_live", n_live, _I32, 1, dev),

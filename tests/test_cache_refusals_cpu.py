@@ -76,3 +76,70 @@ def test_single_and_strided_tokens_are_taken(no_library):
     one = torch.zeros(1, 4, 64, dtype=torch.float16)
     for q in (one, one[0].expand(1, 4, 64), tokens_over_each_other(4, 0)[:1]):
         assert extend(q=q, q_start=i32(2), seq_lens=i32(1), out=torch.zeros(1, 4, 64, dtype=torch.float16)).q_stride == 256
+
+
+def fork(pool, **kw):
+    table, codec = i32(2, 4), torch.zeros(2, 4, dtype=torch.uint8)
+    argus.fork_pages(kw.get("g", argus.geom(4, 2, 64, 16)), i32(2), i32(2), argus.FP16, [pool_of(argus.FP16), pool],
+                     [i32(4), i32(max(pool.n_slots, 0))], [i32(4), i32(max(pool.n_slots, 0))], codec, table, i32(2), codec.clone(),
+                     table.clone(), i32(2), 4, torch.zeros(64, dtype=torch.uint8))
+
+
+def compact(pool, **kw):
+    table, codec, ref = i32(2, 4), torch.zeros(2, 4, dtype=torch.uint8), i32(max(pool.n_slots, 0))
+    argus.compact_pages(kw.get("g", argus.geom(4, 2, 64, 16)), pool, ref, ref.clone(), codec, table, i32(2), table.clone(), 4, i32(1),
+                        torch.zeros(64, dtype=torch.uint8))
+
+
+def takes(call, *args, **kw):
+    with pytest.raises(_Called):
+        call(*args, **kw)
+
+
+ALL = [argus.FP16, argus.BF16, argus.FP8_E4M3, argus.INT8, argus.INT4_G32, argus.INT2_G32, argus.INT1_G32]
+
+
+@pytest.mark.parametrize("codec", ALL)
+def test_pools_that_do_not_hold_their_pages_are_refused(no_library, codec):
+    """Slots are checked against n_slots alone on the device: n_slots pages of this geometry have to be there."""
+    whole = pool_of(codec)
+    calls = [fork, compact] if codec != argus.FP16 else [compact]
+    if codec <= argus.INT8:
+        calls.append(lambda pool, **kw: extend(pools=[pool], **kw))
+    if codec == argus.FP16:
+        calls.append(lambda pool, **kw: rope(pool=pool, **kw))
+
+    def like(**kw):
+        f = dict(codes=whole.codes, meta=whole.meta, n_slots=4)
+        f.update(kw)
+        return argus.Pool(codec, f["codes"], f["meta"], f["n_slots"], argus.PLACE_DEVICE)
+
+    wide = torch.zeros(whole.codes.shape[:-1] + (2 * whole.codes.shape[-1],), dtype=whole.codes.dtype)
+    bad = [dict(n_slots=5), dict(codes=whole.codes[:3]), dict(codes=wide[..., :whole.codes.shape[-1]]), dict(codes=whole.codes.transpose(1, 2)),
+           dict(codes=whole.codes[:1].expand(whole.codes.shape)), dict(codes=whole.codes.double()),
+           dict(codes=torch.zeros(whole.codes.shape, dtype=torch.float8_e5m2 if codec >= argus.FP8_E4M3 else torch.float32))]
+    if whole.meta is not None:
+        bad += [dict(meta=whole.meta[:3]), dict(meta=whole.meta.double()), dict(meta=whole.meta.bfloat16()),
+                dict(meta=whole.meta[:1].expand(whole.meta.shape)), dict(meta=whole.meta.transpose(1, 2)),
+                dict(meta=whole.meta.half() if codec < argus.INT4_G32 else whole.meta.float())]
+    for call in calls:
+        for kw in bad:
+            with pytest.raises(ValueError, match="pool"):
+                call(like(**kw))
+        for g in (argus.geom(8, 4, 64, 16), argus.geom(4, 2, 128, 16), argus.geom(4, 2, 64, 32)):
+            with pytest.raises(ValueError, match="pool"):
+                call(whole, g=g)
+
+
+def test_pools_of_other_shapes_and_raw_types_are_taken(no_library):
+    """A pool may be larger, flat, of the codes' own float type, or hold its bits as integers."""
+    p = pool_of(argus.FP8_E4M3, n_slots=6)
+    for codes in (p.codes, p.codes.flatten(), p.codes.view(torch.float8_e4m3fn), p.codes.view(torch.int8), p.codes.view(torch.int32)):
+        for n in (0, 4, 6):
+            extend(pools=[argus.Pool(argus.FP8_E4M3, codes, p.meta.flatten(), n, argus.PLACE_DEVICE)])
+    takes(compact, argus.Pool(argus.BF16, pool_of(argus.BF16).codes.view(torch.int16), None, 4, argus.PLACE_DEVICE))
+    extend(pools=[argus.Pool(argus.FP8_E4M3, None, None, 0, argus.PLACE_DEVICE)])
+    for codec in ALL[1:]:
+        takes(fork, pool_of(codec))
+        takes(compact, pool_of(codec))
+    takes(rope, pool=pool_of(argus.FP16))
