@@ -512,7 +512,7 @@ def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pag
         _at("out", out, q.dtype, q.numel(), dev) or 0, _at("lse2_out", lse2_out, _F32, total * hq, dev) or 0,
         _status_at(status, dev) or 0, softmax_scale))
     # the struct holds raw pointers: keep every tensor it points to alive with it
-    a._keep = (arr, pools, q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
+    a._keep = (arr, [(p.codes, p.meta) for p in pools], q, q_start, page_codec, block_table, seq_lens, out, lse2_out, status)
     a._device = dev
     return a
 

@@ -143,3 +143,19 @@ def test_pools_of_other_shapes_and_raw_types_are_taken(no_library):
         takes(fork, pool_of(codec))
         takes(compact, pool_of(codec))
     takes(rope, pool=pool_of(argus.FP16))
+
+
+def test_extend_args_keep_the_pools_alive():
+    """The caller's list of pools, and the pools' own tensors, may change between building the arguments and the call."""
+    import gc
+    import weakref
+    pools = [pool_of(argus.FP8_E4M3), pool_of(argus.INT8)]
+    held = [weakref.ref(t) for p in pools for t in (p.codes, p.meta)]
+    args = extend(pools=pools)
+    pools[1].codes = pools[1].meta = None
+    pools.clear()
+    gc.collect()
+    assert all(r() is not None for r in held)
+    del args
+    gc.collect()
+    assert all(r() is None for r in held)
