@@ -1404,21 +1404,28 @@ static argus_status launch(const EParams& p, cudaStream_t s) {
     return e == cudaSuccess ? ARGUS_OK : fail(ARGUS_E_LAUNCH, "extend: smem attribute: %s", cudaGetErrorString(e));
   });
   if (st != ARGUS_OK) return st;
-  extend_kernel<D, BF, W16><<<p.n_ctas, kThreads, smem, s>>>(p);
-  if (p.n_ctas > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.n_ctas - 1, kBM / 32 * (D / 4) / kJoinWarps);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = s;
-    cudaLaunchAttribute at = {};
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel<D, BF>, p);
-    if (e != cudaSuccess) return fail(ARGUS_E_LAUNCH, "argus_paged_extend_attn: launch failed: %s", cudaGetErrorString(e));
-  }
-  return launch_status("argus_paged_extend_attn");
+  auto status = [](cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return ARGUS_OK;
+    cudaGetLastError();                // not left for the next call to find
+    return fail(ARGUS_E_LAUNCH, "argus_paged_extend_attn: launch of the %s failed: %s", what, cudaGetErrorString(e));
+  };
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.n_ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  st = status(cudaLaunchKernelEx(&cfg, extend_kernel<D, BF, W16>, p), "attention");
+  // without the cuts that the first kernel writes, the join would follow whatever the workspace holds
+  if (st != ARGUS_OK || p.n_ctas == 1) return st;
+  cfg.gridDim = dim3(p.n_ctas - 1, kBM / 32 * (D / 4) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return status(cudaLaunchKernelEx(&cfg, join_kernel<D, BF>, p), "join");
 }
 
 template <int D>
