@@ -98,7 +98,10 @@ static_assert(kSoftmaxWarps * kSoftmaxRegs + kLoadWarps * kLoadRegs <= (kSoftmax
 constexpr int kHalf = kBM * 64 * 2;  // 128 rows x 64 dims: one 128-byte swizzle column
 constexpr int kTmemCols = 512;       // S0 S1 O0 O1, 128 columns each
 constexpr float kRescaleThreshold = 8.f;
-constexpr float kFarScale = 64.f;    // |log2| of a V scale beyond which its chunk's sum is kept apart
+// |log2| of a V scale beyond which it does not enter the sums' reference: with
+// scales within 2^+-32, a P that falls below fp32's range (2^-126) next to the
+// row's largest has a weight below 2^-(126 + 7 - 2 * 32) = 2^-69 of it
+constexpr float kFarScale = 32.f;
 constexpr int kBatch = 4;            // blocks looked up at once: a lane per chunk
 constexpr int kBatches = 4;          // batches whose descriptions are kept
 constexpr int kSlots = kBatch * kBatches;
@@ -1030,11 +1033,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       // rows behind the last one see what the last one sees: they are never written
       const int tok = min(group_of(p, it[4] * kBM + l_row), it[1] - 1);
       const int vis_last = min(p.causal ? it[2] - it[1] + tok : it[2] - 1, it[2] - 1);
-      // running reference and sum; the sum of chunks with a V scale far from 1 is
-      // kept apart, with a reference of its own: relative to m (which bounds p
-      // times the scale) it could leave the fp32 range, and a page whose V is 0 must
-      // not push every other page's P out of the 16-bit range
+      // running reference and sum.  m bounds score + log2 of the V scale, for P's
+      // range; a weight's share of the sum knows nothing of the scale, so where scales
+      // are far from 1 sums are kept apart, in lz relative to mz, the largest score:
+      // of a chunk with a far scale (it may be 0), and from the first one far above 1
+      // on of all chunks (relative to an m that it raised they could leave fp32's range).
       float m = -INFINITY, l = 0.f, mz = -INFINITY, lz = 0.f;
+      bool apart = false;                              // the same in the whole warp
       auto scale_acc = [&](float r) {                  // rare: few registers, not speed
 #pragma unroll 1
         for (int x = 0; x < D / 8; ++x) {
@@ -1060,16 +1065,27 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         // lanes 0 .. N-1 look at their chunk, every lane at its row's last key
         const bool odd = lane < N && (sc[lane].x < 0.f || fabsf(sc[lane].y) > kFarScale);
         const int lim = vis_last - k0 - c0 * 16;       // keys e <= lim of the lane's are visible
-        const bool edge = __any_sync(0xffffffffu, odd || lim < N * 16 - 1);
+        const bool edge = __any_sync(0xffffffffu, odd || lim < N * 16 - 1) || apart;
         tmem_wait_ld();
         if (edge) {
-          // the scores scaled and masked here; a far chunk's log2 V scale added, its sum kept apart
+          // the scores scaled and masked here, log2 of the V scale added, sums kept apart
+          bool above = false;
+#pragma unroll
+          for (int x = 0; x < N; ++x) above |= sc[x].y > kFarScale;
+          if (above && !apart) {
+            apart = true;
+            const float ref = m - kPBias, top = fmaxf(mz, ref);
+            if (m != -INFINITY) {
+              lz = lz * fast_exp2(mz - top) + l * fast_exp2(ref - top);
+              mz = top;
+            }
+          }
 #pragma unroll
           for (int x = 0; x < N; ++x) {
             const float kq = sc[x].x * qf, lvc = sc[x].y;
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[x][e] = (kq >= 0.f && x * 16 + e <= lim) ? v[x][e] * kq : -INFINITY;
-            if (fabsf(lvc) > kFarScale) {
+            if (apart || fabsf(lvc) > kFarScale) {
               float top = mz;
 #pragma unroll
               for (int e = 0; e < 16; ++e) top = fmaxf(top, v[x][e]);
@@ -1155,16 +1171,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if (alive) alive = __all_sync(0xffffffffu, wait(&o_done[(n0 + nb - 1) & 1], (uint32_t)((n0 + nb - 1) >> 1) & 1, &misc[1]));
       if (!alive) misc[1] = 1;
       tc_fence_after();
-      // references in the units that l was summed in
+      // references in the units that l was summed in.  Sums kept apart stay near
+      // mz, a score: what the other group and the other copies have does not fall out
+      // of range beside them.  O in those units is the result times lz: 2^-32 of
+      // it where it could overflow.
       float ref = m == -INFINITY ? -INFINITY : m - kPBias, sum = l;
       if (__any_sync(0xffffffffu, mz != -INFINITY)) {
-        const float top = fmaxf(ref, mz);
-        const float r = (mz == -INFINITY) ? 1.f : fast_exp2(ref - top);   // ref = -inf: 0
-        scale_acc(r);
+        float r = 1.f;                                 // its square is what O is scaled by: 2^+-140
         if (mz != -INFINITY) {
-          sum = sum * r + lz * fast_exp2(mz - top);
+          const float top = apart ? (ref - mz > 64.f ? mz + 32.f : mz) : fmaxf(ref, mz);
+          r = fast_exp2(0.5f * (ref - top));           // ref = -inf: 0
+          // with all sums in lz, l counts for nothing (unless a query that holds NaN made it NaN)
+          sum = sum * (apart ? 0.f : r * r) + lz * fast_exp2(mz - top);
           ref = top;
         }
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) scale_acc(r);
       }
       ml[grp * kBM + tl] = make_float2(ref, sum);
       tc_fence_before();
