@@ -494,7 +494,8 @@ argus_status argus_paged_extend_attn(const argus_extend_args* args, void* ws, si
  *   x' = x cos a - y sin a,   y' = y cos a + x sin a,
  * with (x, y) = elements (i, i + rot_dim / 2), or (2i, 2i + 1) when adjacent.
  * The elements from rot_dim on are passed through.  The angle is reduced to a
- * turn in 64-bit fixed point, so it is as exact at position 2^31 - 1 as at 0;
+ * turn in 64-bit fixed point: off by at most |position| 2^-64 of a turn (2^-33 at
+ * position 2^31 - 1) for inv_freq below 2^40, less than its fp32 form resolves;
  * the rotation is fp32, rounded once.
  *   q_out = rotated q;  cache K row = rotated k;  cache V row = v.
  * A token whose page lies outside max_pages or the pool, or is not of the

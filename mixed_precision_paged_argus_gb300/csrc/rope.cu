@@ -4,14 +4,15 @@
 // Mathematics: pair i of a token turns by a = pos[axis(i)] * inv_freq[i].  Only
 // a mod 2 pi matters, and at a far position the product has no fraction left in
 // fp32 (position 10^6 times 1 rad is known to 0.06 rad).  So the frequency is
-// taken in turns, as a 64-bit fixed-point fraction F = frac(inv_freq / 2 pi) 2^64,
-// and pos * F in wrapping 64-bit integers IS the angle modulo one turn, exactly
-// up to F's own rounding.  sincospif of twice the signed fraction follows.
+// taken in turns, as a 64-bit fixed-point fraction F = frac(inv_freq / 2 pi) 2^64
+// (off by at most 1 for frequencies below 2^40), and pos * F in wrapping 64-bit integers
+// IS the angle modulo one turn: off by at most 2^-33 of a turn at position 2^31.
+// sincospif of twice the signed fraction follows.
 //
 // What bounds it: bytes (q, k, v read, q', k', v written once).  A token is
 // taken by a group of W warps (W = 1 when there are many tokens, up to 8 when there
-// are few), which loop over tokens.  Each warp turns its one or two frequencies
-// per lane into fixed point once, computes a token's sines and cosines into
+// are few), which loop over tokens.  Each block turns the frequencies into fixed
+// point once; a warp computes a token's sines and cosines into
 // shared memory of its own (no block barrier), and uses them for all Hq + Hkv heads; a lane moves
 // two 16-byte vectors per item, the two that hold a pair's halves, four items in flight.
 //
@@ -72,6 +73,15 @@ __device__ __forceinline__ int seq_of(const RParams& p, int t) {
   return lo;
 }
 
+// frac(f / 2 pi) 2^64.  The product with 1 / (2 pi) has 106 bits, in two doubles: the
+// fraction of one double would be off by 2^-54 of the product itself, and a
+// position multiplies that.
+__device__ __forceinline__ unsigned long long turn_fraction(double f) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / (2 pi), its first 53 bits and the next 53
+  const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
+  return __double2ull_rn((hi - floor(hi)) * 0x1p64) + (unsigned long long)__double2ll_rn((lo - rint(lo)) * 0x1p64);
+}
+
 template <bool BF>
 __device__ __forceinline__ void turn_pair(uint4& a4, uint4& b4, const float* cs, const float* sn, int u, bool adjacent) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&a4);
@@ -96,11 +106,16 @@ __device__ __forceinline__ void turn_pair(uint4& a4, uint4& b4, const float* cs,
 template <int D, bool BF>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) {
   __shared__ __align__(16) float s_cs[kThreads / 32][2][D / 2];
+  __shared__ unsigned long long s_freq[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* cs = s_cs[warp][0];
   float* sn = s_cs[warp][1];
   const int gw = blockIdx.x * (kThreads / 32) + warp, part = gw % W, groups = gridDim.x * (kThreads / 32) / W;
-  // this lane's frequencies, pairs lane and lane + 32, as fractions of a turn
+  // this lane's frequencies, pairs lane and lane + 32, as fractions of a turn: found
+  // once per block, as double precision runs at a few results per cycle and SM (in
+  // every warp it took 2 us)
+  if (threadIdx.x < p.rot / 2) s_freq[threadIdx.x] = turn_fraction(p.inv_freq[threadIdx.x]);
+  __syncthreads();
   constexpr int N = D / 64;
   unsigned long long freq[N];
   int axis[N];
@@ -110,8 +125,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
     freq[x] = 0;
     axis[x] = 0;
     if (i < p.rot / 2) {
-      const double turns = p.inv_freq[i] * 0.15915494309189535;   // 1 / (2 pi)
-      freq[x] = __double2ull_rn((turns - floor(turns)) * 18446744073709551616.0);
+      freq[x] = s_freq[i];
       if (p.pair_axis) axis[x] = p.pair_axis[i];
     }
   }
