@@ -505,7 +505,8 @@ argus_status argus_paged_extend_attn(const argus_extend_args* args, void* ws, si
  * same row of a page.
  * Arguments: q, k, v device, tokens q_stride / k_stride / v_stride elements
  * apart (0 = dense; multiples of 8, 16-byte aligned); q_out as q (it may be
- * q itself with the same stride; otherwise they must not overlap); positions device int32
+ * q itself with the same stride; its tokens may lie between others of the same buffer, but
+ * where they overlap tokens of q, k or v otherwise the call is ARGUS_E_INVALID); positions device int32
  * [n_axes][total_q]; n_axes 1 to 4; inv_freq device double [rot_dim / 2], in
  * radians per position (finite, >= 0); pair_axis device uint8 [rot_dim / 2] or
  * NULL; rot_dim a multiple of 16, 16 .. head_dim.  head_dim 64 or 128.

@@ -218,6 +218,27 @@ static void launch(const RParams& p, cudaStream_t s) {
   rope_kernel<D, BF><<<(int)std::min(blocks, sms * 3), kThreads, 0, s>>>(p, W);
 }
 
+// Whether two tensors of n tokens share memory: tokens of la and lb bytes, sa >= la and
+// sb >= lb bytes apart, from a and from b on.
+static bool tokens_meet(uintptr_t a, long long la, long long sa, uintptr_t b, long long lb, long long sb, long long n) {
+  typedef __int128 wide;
+  const wide d = (wide)b - (wide)a;                    // token i of one meets token j of the other: -lb < d + j sb - i sa < la
+  if (d >= (n - 1) * (wide)sa + la || -d >= (n - 1) * (wide)sb + lb) return false;
+  if (sa == sb) {                                      // (slices of one buffer's rows): for some k = i - j, d - la < k s < d + lb
+    const wide low = d - la;
+    wide k = (low >= 0 ? low / sa : -((-low + sa - 1) / sa)) + 1;
+    if (k < 1 - n) k = 1 - n;
+    return k <= n - 1 && k * sa < d + lb;
+  }
+  for (long long i = 0, j = 0; i < n && j < n;) {      // the one that ends first meets none behind the other's
+    const wide gap = d + j * (wide)sb - i * (wide)sa;
+    if (gap >= la) ++i;
+    else if (gap <= -lb) ++j;
+    else return true;
+  }
+  return false;
+}
+
 }  // namespace rope
 }  // namespace argus
 
@@ -260,6 +281,13 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
        reinterpret_cast<uintptr_t>(a->q_out) | reinterpret_cast<uintptr_t>(a->pool->codes)) & 15)
     return fail(ARGUS_E_INVALID, "rope: q, k, v, q_out and the pool must be 16-byte aligned");
   if (a->q_out == a->q && p.qs != p.qos) return fail(ARGUS_E_INVALID, "rope: q_out in place needs q's stride");
+  // a token is turned while others are still read
+  const auto over = [&](const void* x, int heads, long long stride) {
+    return rope::tokens_meet(reinterpret_cast<uintptr_t>(a->q_out), 2ll * p.Hq * D, 2 * p.qos, reinterpret_cast<uintptr_t>(x), 2ll * heads * D,
+                             2 * stride, a->total_q);
+  };
+  if ((a->q_out != a->q && over(a->q, p.Hq, p.qs)) || over(a->k, p.Hkv, p.ks) || over(a->v, p.Hkv, p.vs))
+    return fail(ARGUS_E_INVALID, "rope: q_out overlaps the tokens of q, k or v");
   p.B = a->batch;
   p.total = a->total_q;
   p.rot = a->rot_dim;
