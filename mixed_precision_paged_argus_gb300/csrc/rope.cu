@@ -259,9 +259,9 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   if (a->rot_dim <= 0 || a->rot_dim > g.head_dim) return fail(ARGUS_E_INVALID, "rope: rot_dim %d not in 1..head_dim", a->rot_dim);
   if (a->rot_dim % 16) return fail(ARGUS_E_UNSUPPORTED, "rope: rot_dim %d not a multiple of 16", a->rot_dim);
   if (a->batch == 0 || a->total_q == 0) return ARGUS_OK;
-  if (!a->q || !a->k || !a->v || !a->q_out || !a->positions || !a->inv_freq || !a->q_start || !a->seq_lens || !a->pool ||
-      !a->page_codec || !a->block_table)
+  if (!a->q || !a->k || !a->v || !a->q_out || !a->positions || !a->inv_freq || !a->q_start || !a->seq_lens || !a->pool)
     return fail(ARGUS_E_INVALID, "rope: NULL pointer");
+  if (a->max_pages > 0 && (!a->page_codec || !a->block_table)) return fail(ARGUS_E_INVALID, "rope: NULL page_codec or block_table");
   if (a->pool->codec != a->dtype) return fail(ARGUS_E_UNSUPPORTED, "rope: the pool's codec %d is not the tokens' type", a->pool->codec);
   if (a->pool->placement != ARGUS_PLACE_DEVICE) return fail(ARGUS_E_UNSUPPORTED, "rope: the pool must lie in device memory");
   if (a->pool->n_slots < 0 || (a->pool->n_slots > 0 && !a->pool->codes)) return fail(ARGUS_E_INVALID, "rope: bad pool");

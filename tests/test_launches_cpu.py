@@ -167,3 +167,20 @@ def test_rotated_queries_do_not_overlap_what_is_read(tmp_path):
     want = [(1, 0) if meets(c) else (0, 1) for c in cases]
     assert 100 < sum(w[0] for w in want) < 380
     assert [c for c, g, w in zip(cases, got, want) if g != w] == []
+
+
+EMPTY_TABLES = r"""
+int main(void) {
+  argus_rope_args a = rope_args();
+  a.page_codec = 0; a.block_table = 0;
+  printf("%d\n", argus_rope_append(&a, 0));
+  a.max_pages = 0;
+  printf("%d\n", argus_rope_append(&a, 0));
+  return 0;
+}
+"""
+
+
+def test_a_table_without_pages_needs_no_memory(tmp_path):
+    """An empty table has no address: its tokens have no place, which *status counts, and q_out is written all the same."""
+    assert run_with_fakes(EMPTY_TABLES, tmp_path) == [(1,), (0,)]
