@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
     int pos[N];
 #pragma unroll
     for (int x = 0; x < N; ++x) pos[x] = axis[x] < p.n_axes ? p.pos[(size_t)axis[x] * p.total + t] : 0;
-    const int b = seq_of(p, t), start = p.q_start[b], end = p.q_start[b + 1];
+    const int b = seq_of(p, t), start = max(p.q_start[b], 0), end = min(p.q_start[b + 1], p.total);   // 0 <= t < total between
     if (t < start || t >= end) continue;                 // a row of no sequence
     const long long c = (long long)p.seq_lens[b] - (end - start) + (t - start);
     long long slot = -1;
