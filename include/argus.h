@@ -566,8 +566,8 @@ argus_status argus_rope_append(const argus_rope_args* args, void* stream);
  * old entry that names no slot of a pool (kept, not counted as a reference;
  * a copy of it is not made), n_new < 0 (taken as 0), a length beyond max_pages * P
  * (clamped to it).
- * The output arrays must not be the input arrays (ARGUS_E_INVALID), so a
- * captured call can be replayed and two table copies alternate.
+ * The output arrays and ws overlap neither the input arrays nor each other
+ * (ARGUS_E_INVALID), so a captured call can be replayed and two table copies alternate.
  * ws of argus_fork_workspace_bytes bytes (16-byte aligned): no initialisation, not to be
  * shared by calls that overlap on the GPU.
  * Arguments: pools host array in device memory (placement DEVICE, else
@@ -598,7 +598,8 @@ argus_status argus_fork_pages(const argus_geom* g, int32_t batch, const int32_t*
  * outside the table follow the same rule.
  * A negative count is taken as 0.  Entries that name no slot of the pool are
  * copied and counted in *status.
- * ref_out and block_table_out must not be the input arrays.
+ * ref_out, block_table_out, n_live and ws overlap neither the input arrays nor each
+ * other (ARGUS_E_INVALID).
  * ws of argus_compact_workspace_bytes bytes (16-byte aligned): no initialisation, not to be
  * shared by calls that overlap on the GPU.  The pool lies in device memory.
  * ------------------------------------------------------------------------- */

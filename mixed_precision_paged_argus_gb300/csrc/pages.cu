@@ -517,6 +517,26 @@ static argus_status launch_cooperative(const char* what, K kernel, P& p, long lo
 
 static size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+// An array of a call.  What a call writes overlaps neither what it reads nor what
+// else it writes: every step reads the old table and counts while others write.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+static bool overlap(const Span* out, int n_out, const Span* in, int n_in) {
+  const auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return x && y && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i], in[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 // fork workspace: RowInfo [B], the rows with copies, free slots per tile, the free lists
 static size_t fork_bytes(int B, const argus_pool* pools, int n_pools) {
   size_t n = up16((size_t)B * sizeof(RowInfo)) + up16((size_t)(B + 1) * 4);
@@ -586,6 +606,14 @@ extern "C" argus_status argus_fork_pages(const argus_geom* g, int32_t batch, con
     if (page_codec == page_codec_out || block_table == block_table_out || seq_lens == seq_lens_out)
       return fail(ARGUS_E_INVALID, "fork: the new table needs arrays of its own");
   }
+  const size_t rows = (size_t)batch * 4, entries = (size_t)batch * max_pages;
+  Span out[4 + kMaxPools] = {{page_codec_out, entries}, {block_table_out, 4 * entries}, {seq_lens_out, rows}, {ws, fork_bytes(batch, pools, n_pools)}};
+  Span in[5 + kMaxPools] = {{parents, rows}, {n_new, rows}, {page_codec, entries}, {block_table, 4 * entries}, {seq_lens, rows}};
+  for (int i = 0; i < n_pools; ++i) {
+    out[4 + i] = {ref_out[i], (size_t)pools[i].n_slots * 4};
+    in[5 + i] = {ref_in[i], (size_t)pools[i].n_slots * 4};
+  }
+  if (overlap(out, 4 + n_pools, in, 5 + n_pools)) return fail(ARGUS_E_INVALID, "fork: the new table, counts and ws need memory of their own");
   p.n_pools = n_pools;
   p.new_codec = new_codec;
   p.B = batch;
@@ -649,6 +677,10 @@ extern "C" argus_status argus_compact_pages(const argus_geom* g, int32_t batch, 
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)) return fail(ARGUS_E_INVALID, "compact: ws must be a 16-byte aligned device pointer");
   if (ws_bytes < compact_bytes(*pool))
     return fail(ARGUS_E_WORKSPACE, "compact: workspace of %zu bytes, %zu needed", ws_bytes, compact_bytes(*pool));
+  const size_t entries = (size_t)batch * max_pages, slots = (size_t)pool->n_slots * 4;
+  const Span out[] = {{ref_out, slots}, {block_table_out, 4 * entries}, {n_live, 4}, {ws, compact_bytes(*pool)}};
+  const Span in[] = {{ref_in, slots}, {page_codec, entries}, {block_table, 4 * entries}, {seq_lens, (size_t)batch * 4}};
+  if (overlap(out, 4, in, 4)) return fail(ARGUS_E_INVALID, "compact: the new table, counts, n_live and ws need memory of their own");
   p.B = batch;
   p.P = g->page_tokens;
   p.max_pages = max_pages;

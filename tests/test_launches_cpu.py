@@ -62,8 +62,8 @@ static int rope(void) {
 static int compact(void) {
   argus_pool pool = {ARGUS_FP16, 0, (void*)64, 0, 40};
   argus_geom g = {2, 2, 64, 16};
-  return argus_compact_pages(&g, 3, &pool, (void*)64, (void*)(1 << 12), (void*)64, (void*)64, (void*)64, (void*)(1 << 13), 4, (void*)64,
-                             (void*)64, (size_t)1 << 40, 0, 0);
+  return argus_compact_pages(&g, 3, &pool, (void*)64, (void*)(1 << 12), (void*)64, (void*)64, (void*)64, (void*)(2 << 12), 4,
+                             (void*)(3 << 12), (void*)(4 << 12), (size_t)1 << 40, 0, 0);
 }
 """
 
@@ -184,3 +184,70 @@ int main(void) {
 def test_a_table_without_pages_needs_no_memory(tmp_path):
     """An empty table has no address: its tokens have no place, which *status counts, and q_out is written all the same."""
     assert run_with_fakes(EMPTY_TABLES, tmp_path) == [(1,), (0,)]
+
+
+TABLES = r"""
+/* addresses of fork: parents, n_new, counts in / out of two pools, codecs, table, lengths in and out, workspace */
+static const long long cases[][14] = {CASES};
+int main(void) {
+  for (unsigned i = 0; i < sizeof cases / sizeof cases[0]; ++i) {
+    void* c[14];
+    for (int k = 0; k < 14; ++k) c[k] = (void*)cases[i][k];
+    argus_geom g = {2, 2, 64, 16};
+    argus_pool pools[2] = {{ARGUS_FP16, 0, (void*)64, 0, 40}, {ARGUS_INT8, 0, (void*)64, (void*)64, 50}};
+    const int32_t* in[2] = {c[2], c[3]};
+    int32_t* out[2] = {c[4], c[5]};
+    launches = 0;
+    int st = argus_fork_pages(&g, 6, c[0], c[1], ARGUS_FP16, pools, 2, in, out, c[6], c[7], c[8], c[9], c[10], c[11], 4, c[12], 4096, 0, 0);
+    printf("%d %d ", st, launches);
+    /* compaction of the first pool: counts, codecs, table, lengths, the new table, n_live at parents, workspace */
+    launches = 0;
+    st = argus_compact_pages(&g, 6, &pools[0], c[2], c[4], c[6], c[7], c[8], c[10], 4, c[0], c[12], 4096, 0, 0);
+    printf("%d %d\n", st, launches);
+  }
+  return 0;
+}
+"""
+
+
+def test_new_tables_do_not_overlap_the_old(tmp_path):
+    """Six rows of four pages, pools of 40 and 50 slots: every pair of arrays, apart, touching and overlapping."""
+    names = ["parents", "n_new", "in0", "in1", "out0", "out1", "codec", "table", "lens", "codec_out", "table_out", "lens_out", "ws"]
+    size = dict(zip(names, [24, 24, 160, 200, 160, 200, 24, 96, 24, 24, 96, 24, 4096]))
+    base = {n: (1 << 20) + (i << 14) for i, n in enumerate(names)}
+    cases, want = [], []
+
+    def add(place):
+        def bad(out, ins, sizes):
+            spans = {n: (place[n], place[n] + sizes[n]) for n in out + ins if place[n]}
+            return any(spans[a][0] < spans[b][1] and spans[b][0] < spans[a][1] for a in out if a in spans for b in spans if b != a)
+        cases.append([place[n] for n in names] + [0])
+        f = bad(["out0", "out1", "codec_out", "table_out", "lens_out", "ws"], ["parents", "n_new", "in0", "in1", "codec", "table", "lens"],
+                dict(size, ws=FORK_WS))
+        c = bad(["out0", "table_out", "parents", "ws"], ["in0", "codec", "table", "lens"], dict(size, ws=COMPACT_WS, parents=4))
+        want.append(((1, 0) if f else (0, 1)) + ((1, 0) if c else (0, 1)))
+
+    # the workspaces' sizes, as the library states them
+    sizes = run_with_fakes(r"""
+int main(void) {
+  argus_pool pools[2] = {{ARGUS_FP16, 0, (void*)64, 0, 40}, {ARGUS_INT8, 0, (void*)64, (void*)64, 50}};
+  size_t a, b;
+  argus_fork_workspace_bytes(6, pools, 2, &a);
+  argus_compact_workspace_bytes(&pools[0], &b);
+  printf("%zu %zu\n", a, b);
+  return 0;
+}
+""", tmp_path)
+    FORK_WS, COMPACT_WS = sizes[0]
+    add(base)
+    add(dict(base, n_new=0))
+    for a in names:
+        for b in names:
+            if a != b and not (a == "parents" and b == "ws"):
+                for shift in (0, 4 * (size[b] // 4) - 4, size[b], -4, -size[a]):
+                    if a != "ws" or shift % 16 == 0:
+                        add(dict(base, **{a: base[b] + shift}))
+    rows = ", ".join("{%s}" % ", ".join("%dLL" % x for x in c) for c in cases)
+    got = run_with_fakes(TABLES.replace("CASES", rows), tmp_path)
+    assert [(c, g, w) for c, g, w in zip(cases, got, want) if g != w] == []
+    assert sum(w[0] for w in want) > 100 and sum(w[0] == 0 for w in want) > 100
