@@ -562,6 +562,14 @@ argus_status argus_rope_append(const argus_rope_args* args, void* stream);
  *   6. The new length is length + n_new[b].  Unused entries are -1, codec 0.
  * The result does not depend on the order in which the GPU works.
  * Copied pages (codes and meta) stay within their pool; a page is copied whole.
+ * A row's pages are the entries below its length; the call knows of no others.  A
+ * caller that shortens a row (drafted tokens that were rejected) gives the pages behind
+ * the new end back before the next call: the slot's count less one, the entry
+ * -1.  An entry left there leaves the table without its count, and the slot is not
+ * free again.  Compressed keys (ckeys of argus_select_pages, per row and page) are the
+ * caller's to move along: row b's from row parents[b], a copied page's with its row.
+ * Rows that are about to write are compared with each other, batch^2 reads of 32
+ * bytes: a call takes 0.09 ms where 4,096 rows write, 4.5 ms where 65,535 do.
  * Anomalies counted in *status: a parent outside -1 .. B-1 (taken as -1), an
  * old entry that names no slot of a pool (kept, not counted as a reference;
  * a copy of it is not made), n_new < 0 (taken as 0), a length beyond max_pages * P
@@ -597,7 +605,8 @@ argus_status argus_fork_pages(const argus_geom* g, int32_t batch, const int32_t*
  * copied), *n_live = L.  The slots from L on may then be given back.  Holders
  * outside the table follow the same rule.
  * A negative count is taken as 0.  Entries that name no slot of the pool are
- * copied and counted in *status.
+ * copied and counted in *status.  Compressed keys go by row and page, not by slot: they
+ * stay where they are.
  * ref_out, block_table_out, n_live and ws overlap neither the input arrays nor each
  * other (ARGUS_E_INVALID).
  * ws of argus_compact_workspace_bytes bytes (16-byte aligned): no initialisation, not to be

@@ -13,6 +13,10 @@
 // small cases spent most of their time between launches).  A prefix count over
 // a pool takes two steps over tiles of 1,024 slots: a count per tile, then every
 // tile sums the counts before its own (a pool of a million slots has 1,024 tiles).
+// Which of the rows that are about to write a page keeps it is found row against
+// row, batch^2 reads of 32 bytes, which bound the call from a few thousand rows on: a step
+// in which every row writes took 27 us with 512 rows, 88 us with 4,096, 0.57 ms with
+// 16,384 and 4.5 ms with 65,535.
 //
 // Measured (GB300, CUDA events, buffers rotated past the L2): compaction of 16,384 pages of 64 KB,
 // half of them live: 96 us, 5.6 TB/s read and written (82% of a plain copy).  In a graph,
