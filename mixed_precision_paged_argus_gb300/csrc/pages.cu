@@ -530,7 +530,7 @@ struct Span {
 static bool overlap(const Span* out, int n_out, const Span* in, int n_in) {
   const auto meet = [](const Span& a, const Span& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-    return x && y && x < y + b.bytes && y < x + a.bytes;
+    return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
   };
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < n_in; ++j)

@@ -251,3 +251,23 @@ int main(void) {
     got = run_with_fakes(TABLES.replace("CASES", rows), tmp_path)
     assert [(c, g, w) for c, g, w in zip(cases, got, want) if g != w] == []
     assert sum(w[0] for w in want) > 100 and sum(w[0] == 0 for w in want) > 100
+
+
+NOTHING = r"""
+int main(void) {
+  argus_geom g = {2, 2, 64, 16};
+  argus_pool pools[2] = {{ARGUS_FP16, 0, (void*)64, 0, 40}, {ARGUS_INT8, 0, (void*)64, (void*)64, 0}};
+  /* the empty pool's counts lie at an address inside the other's, and those of compaction inside the table */
+  const int32_t* in[2] = {(void*)(1 << 12), (void*)((1 << 12) + 8)};
+  int32_t* out[2] = {(void*)(2 << 12), (void*)((2 << 12) + 8)};
+  printf("%d\n", argus_fork_pages(&g, 6, (void*)(3 << 12), 0, ARGUS_FP16, pools, 2, in, out, (void*)(4 << 12), (void*)(5 << 12), (void*)(6 << 12),
+                                  (void*)(7 << 12), (void*)(8 << 12), (void*)(9 << 12), 4, (void*)(10 << 12), 4096, 0, 0));
+  printf("%d\n", argus_compact_pages(&g, 6, &pools[1], (void*)((5 << 12) + 8), (void*)((5 << 12) + 8), (void*)(4 << 12), (void*)(5 << 12),
+                                     (void*)(6 << 12), (void*)(8 << 12), 4, (void*)(3 << 12), (void*)(10 << 12), 4096, 0, 0));
+  return 0;
+}
+"""
+
+
+def test_arrays_without_elements_overlap_nothing(tmp_path):
+    assert run_with_fakes(NOTHING, tmp_path) == [(0,), (0,)]
