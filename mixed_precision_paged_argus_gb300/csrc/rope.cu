@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
 }
 
 template <int D, bool BF>
-static void launch(const RParams& p, cudaStream_t s) {
+static argus_status launch(const RParams& p, cudaStream_t s) {
   constexpr int kWarps = kThreads / 32;
   const long long sms = device_sm_count();
   // warps per token: enough of them for every SM to hold some, no more than have an item each
@@ -215,7 +215,14 @@ static void launch(const RParams& p, cudaStream_t s) {
   while (W < kWarps && (long long)p.total * W < sms * 16 && 32 * W < items) W *= 2;
   const long long blocks = ((long long)p.total * W + kWarps - 1) / kWarps;
   // three blocks are resident per SM at this register count
-  rope_kernel<D, BF><<<(int)std::min(blocks, sms * 3), kThreads, 0, s>>>(p, W);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((int)std::min(blocks, sms * 3));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, BF>, p, W);
+  if (e == cudaSuccess) return ARGUS_OK;
+  cudaGetLastError();                  // not left for the next call to find
+  return fail(ARGUS_E_LAUNCH, "argus_rope_append: launch failed: %s", cudaGetErrorString(e));
 }
 
 // Whether two tensors of n tokens share memory: tokens of la and lb bytes, sa >= la and
@@ -311,7 +318,6 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   p.status = a->status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = a->dtype == ARGUS_BF16;
-  if (D == 64) bf ? rope::launch<64, true>(p, s) : rope::launch<64, false>(p, s);
-  else bf ? rope::launch<128, true>(p, s) : rope::launch<128, false>(p, s);
-  return launch_status("argus_rope_append");
+  if (D == 64) return bf ? rope::launch<64, true>(p, s) : rope::launch<64, false>(p, s);
+  return bf ? rope::launch<128, true>(p, s) : rope::launch<128, false>(p, s);
 }

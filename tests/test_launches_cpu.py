@@ -271,3 +271,19 @@ int main(void) {
 
 def test_arrays_without_elements_overlap_nothing(tmp_path):
     assert run_with_fakes(NOTHING, tmp_path) == [(0,), (0,)]
+
+
+STALE = r"""
+int main(void) {
+  int (*calls[])(void) = {extend, rope, compact};
+  for (int c = 0; c < 3; ++c) {
+    last = 701;                              /* somebody else's launch failed before this call */
+    printf("%d\n", calls[c]());
+  }
+  return 0;
+}
+"""
+
+
+def test_an_error_from_before_is_not_the_calls(tmp_path):
+    assert run_with_fakes(STALE, tmp_path) == [(0,), (0,), (0,)]
