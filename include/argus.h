@@ -441,7 +441,8 @@ argus_status argus_staging_moves_less(const int64_t* row_read_bytes, int64_t n_r
  * (elements below 2^-31 of the row's largest lose bits).  p_j (times the page's V
  * scale) is rounded to that type: half a step, 2^-8 of its value for BF16, 2^-11
  * for FP16, there at least 2^-32 of the row's largest.  Maxima, sums and the
- * accumulators are fp32.  A NaN in a query row stays in that row.
+ * accumulators are fp32; the sums, and lse2, do not depend on the V scales, however far
+ * apart these are.  A NaN in a query row stays in that row.
  *
  * Arguments: q device [total_q] tokens of [Hq][D] (16-byte aligned, not
  * overlapping out; tokens q_stride elements apart, a multiple of 8, 0 = Hq * D:

@@ -7,7 +7,9 @@
 // cost nothing: the K scale, the softmax scale and log2 e are one factor of a score,
 // and the V scale w_j enters the exponent, p_j w_j = 2^(s_j + log2 w_j - m), so
 // that codes alone are the MMAs' operands; the row sum divides each 16-key chunk's
-// part by its w again.  P is stored times 2^7 (fp16: at most 2^15 before m moves).
+// part by its w again (where w is far from 1 it sums the weights on their own: relative
+// to an m that holds w they could leave fp32's range).  P is stored times 2^7 (fp16: at
+// most 2^15 before m moves).
 //
 // What bounds it: with few query rows per key (drafted tokens) the bytes of the
 // pages; with many (prompt chunks) the tensor cores, and beside them the
@@ -29,21 +31,24 @@
 //    tile holds 4 or 2 copies of them, and each copy's lanes take other 16-key chunks
 //    (their P is 0 elsewhere); the epilogue adds the copies.
 //  * One CTA per SM; the key blocks of all items are dealt out evenly, found on
-//    the device (below).  Items that are cut leave pieces; a second kernel,
-//    launched early, joins them.
+//    the device (below).  Items that are cut leave pieces; a second kernel joins them.
+//    It is launched early, which saves its launch; its blocks find room only on SMs that
+//    no CTA of the first kernel holds (64,512 of 65,536 registers) any more.
 //
 // Measured (GB300; CUDA events, buffers rotated past the L2): FP8 pages of 16 tokens, 32
-// sequences of 8,192 to 32,768, 1 to 8 drafted tokens, 32/8 heads of 128: 306 us, 4.7 TB/s
-// of pages (69% of a plain copy; decode reaches 72% on the same pages).  A 1,024-token chunk over
-// 131,072 FP8 tokens, 16/2 heads of 128: 1.02 ms, 1.08 PFLOP/s (56% of cuBLAS bf16);
+// sequences of 8,192 to 32,768, 1 to 8 drafted tokens, 32/8 heads of 128: 311 to 313 us, 4.6 TB/s
+// of pages (67% of a plain copy; decode reaches 72% on the same pages).  A 1,024-token chunk over
+// 131,072 FP8 tokens, 16/2 heads of 128: 1.02 ms, 1.07 PFLOP/s (56% of cuBLAS bf16);
 // with neither softmax nor MMAs the loads and conversions alone took 0.71 ms, the
 // MMAs alone 0.67 ms.  BF16, FP8 and INT8 pages mixed, 8 sequences of up to 16,384
-// with 1 to 256 new tokens: 240 us (the same in FP8 alone 150, INT8 215, BF16 314: a
-// 16-bit page is twice the bytes for every query tile).
-// Per-item cost is what bounds short sequences (1,024 of 64 tokens: 260 us): its code
+// with 1 to 256 new tokens: 244 us (the same in FP8 alone 152, INT8 217, BF16 315: a
+// 16-bit page is twice the bytes for every query tile, and the second half of its rows
+// of 128 dims is read only when it is stored).
+// Per-item cost is what bounds short sequences (1,024 of 64 tokens: 263 us): its code
 // runs once per item, out of a cold instruction cache, hence the rolled loops in
 // load_q and the epilogue (unrolled as far as registers allow, mixed tiers took 259 us and cross
-// attention over 1 to 1,500 INT8 states 53 instead of 47).
+// attention over 1 to 1,500 INT8 states 53; it takes 49).  Sums kept apart for far V
+// scales are 1 to 3% of that (mixed tiers 240, cross 48 without them).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

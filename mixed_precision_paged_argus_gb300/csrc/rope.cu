@@ -19,7 +19,7 @@
 // Measured (GB300, CUDA events, buffers rotated past the L2): two video prompts of 52,768
 // tokens together, 14/2 heads of 64, three axes: 54 us, 4.5 TB/s (66% of a plain copy);
 // five prompts of 777 to 2,048 tokens, 32/8 heads of 128: 35 us, 5.1 TB/s (75%); a
-// decode step of 32 rows: 4.6 us in a graph, its launch and two dependent reads.  Warps on
+// decode step of 32 rows: 4.4 us in a graph, its launch and two dependent reads.  Warps on
 // runs of neighbouring tokens (sequence and page looked up once) were no faster, nor
 // sines and cosines kept in registers: 36 and 52 us at best, with more registers.
 #include <algorithm>
