@@ -622,6 +622,142 @@ argus_status argus_compact_pages(const argus_geom* g, int32_t batch, const argus
                                  void* ws, size_t ws_bytes, uint32_t* status, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * argus_paged_window_extend_attn -- argus_paged_extend_attn in a layer with a sliding
+ * window: prompt chunks, drafted tokens and mixed steps of several tokens
+ * (argus_paged_decode_attn has the same window for one).
+ *
+ * Query token i of sequence b, at position pos = seq_lens[b] - n_b + i, sees the cached
+ * positions j <= pos with
+ *   j > pos - window_tokens   or   j < sink_tokens,
+ * and nothing else.  Blocks of 128 positions that no row of a tile of 128 query rows
+ * sees are not read, nor chunks of 16.  A bad page is counted once per
+ * sequence if a query token sees positions of it.
+ * args, ws and everything else as for argus_paged_extend_attn; args->causal must be
+ * 1 (ARGUS_E_INVALID), window_tokens >= 1, sink_tokens >= 0.
+ * ------------------------------------------------------------------------- */
+argus_status argus_paged_window_extend_attn(const argus_extend_args* args, int32_t window_tokens,
+                                            int32_t sink_tokens, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_paged_tree_attn -- argus_paged_extend_attn for a tree of drafted tokens per
+ * sequence.  The n_b query tokens of sequence b are the tree's tokens, the last n_b of its
+ * seq_lens[b] cached ones; token i sees the positions j < seq_lens[b] - n_b and those
+ * tokens x of the tree (position seq_lens[b] - n_b + x) whose bit is set in row i of the
+ * mask:
+ *   tree_mask device uint32 [total_q][mask_words] (4-byte aligned), bit x % 32 of word
+ *   x / 32: token x of the same sequence.
+ * A token's ancestors and itself, as a rule; any mask is taken, a row without a bit sees
+ * the cache alone.  Bits from n_b on are ignored, tokens from 32 mask_words on unseen.
+ * Positions (argus_rope_append) go by a token's depth, not by its place in the cache.
+ * args, ws and everything else as for argus_paged_extend_attn; args->causal must be
+ * 1 (ARGUS_E_INVALID), mask_words >= 1.
+ * ------------------------------------------------------------------------- */
+argus_status argus_paged_tree_attn(const argus_extend_args* args, const uint32_t* tree_mask,
+                                   int32_t mask_words, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_accept_tokens -- the K and V rows of a tree's accepted path moved to where the
+ * sequence goes on, and the lengths that follow.
+ *
+ * Of sequence b's n_b drafted tokens (q_start as in argus_paged_extend_attn, base =
+ * seq_lens[b] - n_b) the tokens path[b][0] < path[b][1] < ... of n_path[b] stay: token
+ * path[b][k] goes from cached position base + path[b][k] to base + k, and
+ *   seq_lens_out[b] = base + the length of the path.
+ * In place, in pages of one 16-bit pool that the sequence alone holds; rows behind the
+ * path are left as they were.  The pages behind the new end are the caller's to give back
+ * (argus_fork_pages).  One call per layer, with that layer's pool; seq_lens_out is the same
+ * for all.
+ * Counted in *status: a path entry that is not above the one before it or not below
+ * n_b (the path ends in front of it); n_path[b] outside 0 .. path_width (clamped);
+ * seq_lens[b] < n_b (nothing is moved, seq_lens_out[b] = seq_lens[b]); a token to be moved
+ * whose page, or whose new one, is not of the pool (it is not moved; the length counts it).
+ * Arguments: path device int32 [B][path_width], n_path device int32 [B]; seq_lens_out
+ * device int32 [B], overlapping no input (ARGUS_E_INVALID).  head_dim 64 or 128.
+ * ------------------------------------------------------------------------- */
+argus_status argus_accept_tokens(const argus_geom* g, int32_t batch, const argus_pool* pool,
+                                 const uint8_t* page_codec, const int32_t* block_table,
+                                 int32_t max_pages, const int32_t* q_start,
+                                 const int32_t* seq_lens, const int32_t* path,
+                                 int32_t path_width, const int32_t* n_path,
+                                 int32_t* seq_lens_out, uint32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_norm_rope_append -- argus_rope_append whose queries and keys are normed first,
+ * each head by itself:
+ *   x <- x / sqrt(mean(x^2) + eps) * weight   over the head_dim elements of a head,
+ * with q_weight for queries and k_weight for keys (device float [head_dim], 4-byte aligned,
+ * or NULL: ones).  Sums, norm and rotation are fp32, rounded once; squares
+ * beyond fp32's range are taken care of.  eps finite, at least 2^-100
+ * (ARGUS_E_INVALID).  V is stored as it is.  Everything else as for argus_rope_append.
+ * ------------------------------------------------------------------------- */
+argus_status argus_norm_rope_append(const argus_rope_args* args, const float* q_weight,
+                                    const float* k_weight, float eps, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_attn_weights -- the attention weights of the call's query tokens, summed per
+ * cached position and KV head: what eviction goes by.
+ *
+ * After an attention over the same pages gave its rows' log-sums L (lse2 of
+ * argus_paged_extend_attn, or of argus_paged_decode_attn with one token per sequence),
+ *   weights[b][h][j] <- decay * weights[b][h][j] + sum over the query tokens i of sequence b
+ *       that see j and the G heads of KV head h of 2^(softmax_scale log2(e) q . k_j - L),
+ * for all j < seq_lens[b] (those behind keep what they hold).  A query token sees
+ * what argus_paged_extend_attn with the same args shows it (causal 0 or 1).  With decay = 0 the
+ * old weights are not read; a sequence without query tokens decays.  A row whose L is -inf
+ * adds nothing; a NaN in a query row makes the sums that it enters NaN.
+ * args as for argus_paged_extend_attn, with these differences: lse2_out is READ (device float
+ * [total_q][Hq]); out is not used; pools may be of every codec (16-bit ones of the query's type).
+ * weights device float [B][Hkv][row_len], row_len >= max_pages * P, overlapping no input
+ * (ARGUS_E_INVALID); decay finite.  A page whose slot lies outside its pool or whose codec
+ * has no pool adds nothing and is counted once per sequence in *status.
+ * Precision: scores as in argus_paged_extend_attn (codes exact, fp32 sums; a BF16 query becomes
+ * FP16 times a power of two per row over 8-bit and group-coded pages, where elements below 2^-31 of
+ * the row's largest lose bits); weights and sums are fp32.  The order of the sums is fixed.
+ * ------------------------------------------------------------------------- */
+argus_status argus_attn_weights(const argus_extend_args* args, float* weights, int64_t row_len,
+                                float decay, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * argus_evict_tokens -- sequences brought to a budget of cached positions, by weight.
+ *
+ * Of a sequence of L = seq_lens[b] > budget positions each KV head keeps, by itself, the
+ * first sink_tokens, the last recent_tokens, and of those between the budget -
+ * sink_tokens - recent_tokens of largest weights[b][h][.] (ties: the lower position; NaN below
+ * all else, -0 = +0); of a shorter one everything.  In ascending order they become positions 0,
+ * 1, ... of a new cache of seq_lens_out[b] = min(L, budget) tokens in pages of `dst`:
+ *   kept[b][h][i]         the old position of new position i (-1 from the new length on),
+ *   weights_out[b][h][i]  its weight (0 from there on),
+ *   dst pages             its K and V rows, position i in row i % P of page
+ *                         dst_table[b][i / P]; rows of the last page behind the end are zeros.
+ * Keys keep the rotary positions they were stored with.  A row's value is what its page's codec says
+ * (code * scale in fp32, and so on); a 16-bit dst takes it as it is (same type) or rounded;
+ * FP8 and INT8 as argus_quantize_pages does, with a scale per new page, KV head and K | V from the
+ * rows kept in it.
+ * Out of place: what the old pages hold is not changed (they may be shared), and dst_table names
+ * no page that the call reads, and no page twice; dst may be one of `pools`.  Giving the old pages back, and
+ * entering the new ones in table and counts, is the caller's.
+ * Counted in *status: a kept position whose page is not in its pool, once per KV head (it becomes
+ * zeros); a new page that dst does not have, once per sequence (it is not written).
+ * Arguments: pools of every codec, at most one each, 16-bit ones of dst's type if dst is 16-bit;
+ * dst 16-bit, FP8 or INT8 (else ARGUS_E_UNSUPPORTED); all in device memory.  weights device float
+ * [B][Hkv][row_len], row_len >= max_pages * P; weights_out [B][Hkv][row_len_out],
+ * row_len_out >= budget; kept device int32 [B][Hkv][budget]; dst_table device int32
+ * [B][dst_pages], dst_pages * P >= budget >= sink_tokens + recent_tokens.  seq_lens_out, kept
+ * and weights_out overlap neither an input nor each other (ARGUS_E_INVALID).
+ * No workspace.  head_dim 64 or 128; stored values finite.
+ * ------------------------------------------------------------------------- */
+argus_status argus_evict_tokens(const argus_geom* g, int32_t batch, const argus_pool* pools,
+                                int32_t n_pools, const uint8_t* page_codec,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                int32_t max_pages, const float* weights, int64_t row_len,
+                                int32_t budget, int32_t sink_tokens, int32_t recent_tokens,
+                                const argus_pool* dst, const int32_t* dst_table,
+                                int32_t dst_pages, int32_t* seq_lens_out, int32_t* kept,
+                                float* weights_out, int64_t row_len_out, uint32_t* status,
+                                void* stream);
+
+/* ---------------------------------------------------------------------------
  * Testing only.  argus_test_decode_stall runs argus_paged_decode_attn with
  * every device wait limited to wait_limit_us microseconds (1 .. 2,000,000),
  * and the producer warp (the one issuing copies) of each CTA that reaches stage

@@ -88,7 +88,9 @@ EXPORTS = ["argus_quantize_pages", "argus_decode_workspace_bytes", "argus_paged_
            "argus_paged_window_prefill_workspace_bytes", "argus_paged_window_prefill_attn",
            "argus_staging_moves_less", "argus_extend_workspace_bytes", "argus_paged_extend_attn",
            "argus_rope_append", "argus_fork_workspace_bytes", "argus_fork_pages",
-           "argus_compact_workspace_bytes", "argus_compact_pages", "argus_test_decode_stall",
+           "argus_compact_workspace_bytes", "argus_compact_pages", "argus_paged_window_extend_attn",
+           "argus_paged_tree_attn", "argus_accept_tokens", "argus_norm_rope_append", "argus_attn_weights",
+           "argus_evict_tokens", "argus_test_decode_stall",
            "argus_status_string", "argus_last_error"]
 
 
@@ -156,6 +158,19 @@ def lib():
     L.argus_compact_pages.restype = ctypes.c_int
     L.argus_compact_pages.argtypes = [ctypes.POINTER(Geom), i32, ctypes.POINTER(PoolDesc), vp, vp, vp, vp, vp, vp, i32,
                                       vp, vp, sz, vp, vp]
+    L.argus_paged_window_extend_attn.restype = ctypes.c_int
+    L.argus_paged_window_extend_attn.argtypes = [ctypes.POINTER(ExtendArgs), i32, i32, vp, sz, vp]
+    L.argus_paged_tree_attn.restype = ctypes.c_int
+    L.argus_paged_tree_attn.argtypes = [ctypes.POINTER(ExtendArgs), vp, i32, vp, sz, vp]
+    L.argus_accept_tokens.restype = ctypes.c_int
+    L.argus_accept_tokens.argtypes = [ctypes.POINTER(Geom), i32, ctypes.POINTER(PoolDesc), vp, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp]
+    L.argus_norm_rope_append.restype = ctypes.c_int
+    L.argus_norm_rope_append.argtypes = [ctypes.POINTER(RopeArgs), vp, vp, ctypes.c_float, vp]
+    L.argus_attn_weights.restype = ctypes.c_int
+    L.argus_attn_weights.argtypes = [ctypes.POINTER(ExtendArgs), vp, i64, ctypes.c_float, vp]
+    L.argus_evict_tokens.restype = ctypes.c_int
+    L.argus_evict_tokens.argtypes = [ctypes.POINTER(Geom), i32, ctypes.POINTER(PoolDesc), i32, vp, vp, vp, i32, vp, i64, i32, i32, i32,
+                                     ctypes.POINTER(PoolDesc), vp, i32, vp, vp, vp, i64, vp, vp]
     _lib = L
     return L
 
@@ -529,12 +544,93 @@ def paged_extend_attn(args, ws, stream=None):
     _check(lib().argus_paged_extend_attn(ctypes.byref(args), _ws_at(ws, args._device), ws.nbytes, _stream_of(args._device, stream)))
 
 
+def paged_window_extend_attn(args, ws, window_tokens, sink_tokens=0, stream=None):
+    """paged_extend_attn where a token sees the newest window_tokens positions up
+    to its own and the first sink_tokens; ws of extend_workspace_bytes bytes."""
+    _check(lib().argus_paged_window_extend_attn(ctypes.byref(args), window_tokens, sink_tokens, _ws_at(ws, args._device), ws.nbytes,
+                                                _stream_of(args._device, stream)))
+
+
+def paged_tree_attn(args, ws, tree_mask, stream=None):
+    """paged_extend_attn for a tree of drafted tokens per sequence: tree_mask int32
+    [tokens][words], bit x of a row: the sequence's drafted token x is seen (a row of
+    no bits sees the cache in front of the tree); ws of extend_workspace_bytes bytes."""
+    if tree_mask.dim() != 2 or tree_mask.shape[0] != args.total_q:
+        raise ValueError("tree_mask must be [%d][words], not %s" % (args.total_q, list(tree_mask.shape)))
+    _check(lib().argus_paged_tree_attn(ctypes.byref(args), _at("tree_mask", tree_mask, _I32, 0, args._device), tree_mask.shape[1],
+                                       _ws_at(ws, args._device), ws.nbytes, _stream_of(args._device, stream)))
+
+
+def accept_tokens(g, pool, page_codec, block_table, max_pages, q_start, seq_lens, path, n_path, seq_lens_out, status=None, stream=None):
+    """Move the K and V rows of each sequence's accepted path (path int32 [B][width], the
+    first n_path[b] entries: drafted tokens in ascending order) to where the sequence goes
+    on; the new lengths go to seq_lens_out."""
+    batch, dev = seq_lens.numel(), seq_lens.get_device()
+    if path.dim() != 2 or path.shape[0] != batch:
+        raise ValueError("path must be [%d][width], not %s" % (batch, list(path.shape)))
+    entries = batch * max_pages
+    _check(lib().argus_accept_tokens(
+        ctypes.byref(g), batch, _pool_array((pool,), dev, g), _at("page_codec", page_codec, _U8, entries, dev),
+        _at("block_table", block_table, _I32, entries, dev), max_pages, _at("q_start", q_start, _I32, batch + 1, dev),
+        _at("seq_lens", seq_lens, _I32, 0, dev), _at("path", path, _I32, 0, dev), path.shape[1], _at("n_path", n_path, _I32, batch, dev),
+        _at("seq_lens_out", seq_lens_out, _I32, batch, dev), _status_at(status, dev), _stream_of(dev, stream)))
+
+
+def attn_weights(args, weights, decay=1.0, stream=None):
+    """weights [B][Hkv][positions] (float32) become decay * weights plus the attention
+    weights of the query tokens of args (extend_args; out may be None), whose log-sums
+    args.lse2_out holds."""
+    batch, hkv = args.batch, args.g.n_kv_heads
+    if weights.dim() != 3 or weights.shape[0] != batch or weights.shape[1] != hkv:
+        raise ValueError("weights must be [%d][%d][positions], not %s" % (batch, hkv, list(weights.shape)))
+    _check(lib().argus_attn_weights(ctypes.byref(args), _at("weights", weights, _F32, 0, args._device), weights.shape[2], decay,
+                                    _stream_of(args._device, stream)))
+
+
+def evict_tokens(g, pools, page_codec, block_table, seq_lens, max_pages, weights, budget, sink_tokens, recent_tokens, dst, dst_table,
+                 dst_pages, seq_lens_out, kept, weights_out, status=None, stream=None):
+    """Bring every sequence to at most budget positions: each KV head keeps the first
+    sink_tokens, the last recent_tokens and the heaviest between, gathered into the pages of
+    dst that dst_table [B][dst_pages] names.  kept [B][Hkv][budget] takes the old positions,
+    weights_out [B][Hkv][positions] their weights."""
+    batch, dev, hkv = seq_lens.numel(), seq_lens.get_device(), g.n_kv_heads
+    for name, t in (("weights", weights), ("weights_out", weights_out)):
+        if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != hkv:
+            raise ValueError("%s must be [%d][%d][positions], not %s" % (name, batch, hkv, list(t.shape)))
+    entries = batch * max_pages
+    _check(lib().argus_evict_tokens(
+        ctypes.byref(g), batch, _pool_array(pools, dev, g), len(pools), _at("page_codec", page_codec, _U8, entries, dev),
+        _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, 0, dev), max_pages,
+        _at("weights", weights, _F32, 0, dev), weights.shape[2], budget, sink_tokens, recent_tokens, _pool_array((dst,), dev, g),
+        _at("dst_table", dst_table, _I32, batch * dst_pages, dev), dst_pages, _at("seq_lens_out", seq_lens_out, _I32, batch, dev),
+        _at("kept", kept, _I32, batch * hkv * budget, dev), _at("weights_out", weights_out, _F32, 0, dev), weights_out.shape[2],
+        _status_at(status, dev), _stream_of(dev, stream)))
+
+
 def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages,
                 pair_axis=None, adjacent=False, status=None, stream=None):
     """Turn q and k by their positions ([n_axes][tokens], one row per axis;
     inv_freq [rot_dim / 2] in float64, radians per position) into q_out and the
     cache, and store v: the tokens of sequence b become the last ones of its
     seq_lens[b] cached positions."""
+    a, dev = _rope_args(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages, pair_axis,
+                        adjacent, status)
+    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(dev, stream)))
+
+
+def norm_rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages, q_weight,
+                     k_weight, eps, pair_axis=None, adjacent=False, status=None, stream=None):
+    """rope_append whose queries and keys are normed first, each head by itself: divided by
+    sqrt(mean(x^2) + eps), times q_weight or k_weight (float32 [head_dim], None: ones)."""
+    a, dev = _rope_args(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages, pair_axis,
+                        adjacent, status)
+    d = g.head_dim
+    _check(lib().argus_norm_rope_append(ctypes.byref(a), _at("q_weight", q_weight, _F32, d, dev), _at("k_weight", k_weight, _F32, d, dev),
+                                        eps, _stream_of(dev, stream)))
+
+
+def _rope_args(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool, page_codec, block_table, max_pages, pair_axis, adjacent,
+               status):
     total, batch, dtype, dev = q.shape[0], q_start.numel() - 1, q.dtype, q.get_device()
     hq, hkv, d = g.n_q_heads, g.n_kv_heads, g.head_dim
     if k.shape[0] != total or v.shape[0] != total or q_out.shape[0] != total or positions.numel() % (total or 1):
@@ -552,7 +648,8 @@ def rope_append(g, q, k, v, q_out, q_start, seq_lens, positions, inv_freq, pool,
         _at("q_start", q_start, _I32, 1, dev) or 0, _at("seq_lens", seq_lens, _I32, batch, dev) or 0, ctypes.addressof(arr),
         _at("page_codec", page_codec, _U8, batch * max_pages, dev) or 0,
         _at("block_table", block_table, _I32, batch * max_pages, dev) or 0, max_pages, _status_at(status, dev) or 0))
-    _check(lib().argus_rope_append(ctypes.byref(a), _stream_of(dev, stream)))
+    a._keep = arr
+    return a, dev
 
 
 def fork_workspace_bytes(batch, pools):

@@ -1,5 +1,6 @@
 // argus_rope_append: rotary positions (one or several axes) on the new tokens'
-// queries and keys, and the append of keys and values to the paged cache.
+// queries and keys, and the append of keys and values to the paged cache; and
+// argus_norm_rope_append, which norms the queries and keys of each head first.
 //
 // Mathematics: pair i of a token turns by a = pos[axis(i)] * inv_freq[i].  Only
 // a mod 2 pi matters, and at a far position the product has no fraction left in
@@ -22,7 +23,13 @@
 // decode step of 32 rows: 4.4 us in a graph, its launch and two dependent reads.  Warps on
 // runs of neighbouring tokens (sequence and page looked up once) were no faster, nor
 // sines and cosines kept in registers: 36 and 52 us at best, with more registers.
+//
+// The norm, y = x w / sqrt(mean x^2 + eps) over a head's D elements, is one more
+// value per head: an item's sum of squares goes around the D / 16 neighbouring lanes that
+// hold the head, in fp32, between the loads and the rotation; nothing is read twice and
+// nothing rounded in between.
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 
@@ -46,6 +53,8 @@ struct RParams {
   const uint8_t* page_codec;
   const int32_t* block_table;
   uint32_t* status;
+  const float *q_weight, *k_weight;  // [D] or NULL (ones)
+  float eps;
 };
 
 template <bool BF>
@@ -103,7 +112,50 @@ __device__ __forceinline__ void turn_pair(uint4& a4, uint4& b4, const float* cs,
   }
 }
 
-template <int D, bool BF>
+// The same two vectors by their norm: r = 1 / sqrt(mean + eps) of the head (its values times
+// `pre`), wa and wb the weights of their elements; turned by the pairs of item u unless u < 0.
+template <bool BF>
+__device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, float pre, float r, const float* wa, const float* wb, const float* cs, const float* sn,
+                                          int u, bool adjacent) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&a4);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&b4);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float2 x = unpack2<BF>(a[j]), y = unpack2<BF>(b[j]);
+    const float2 v = *reinterpret_cast<const float2*>(wa + 2 * j), w = *reinterpret_cast<const float2*>(wb + 2 * j);
+    x = make_float2(x.x * pre * r * v.x, x.y * pre * r * v.y);
+    y = make_float2(y.x * pre * r * w.x, y.y * pre * r * w.y);
+    if (u >= 0) {
+      if (adjacent) {                                    // two pairs, a's and b's
+        const float c0 = cs[8 * u + j], s0 = sn[8 * u + j], c1 = cs[8 * u + 4 + j], s1 = sn[8 * u + 4 + j];
+        x = make_float2(x.x * c0 - x.y * s0, x.y * c0 + x.x * s0);
+        y = make_float2(y.x * c1 - y.y * s1, y.y * c1 + y.x * s1);
+      } else {
+        const float2 c = *reinterpret_cast<const float2*>(cs + 8 * u + 2 * j), s = *reinterpret_cast<const float2*>(sn + 8 * u + 2 * j);
+        const float2 z = x;
+        x = make_float2(z.x * c.x - y.x * s.x, z.y * c.y - y.y * s.y);
+        y = make_float2(y.x * c.x + z.x * s.x, y.y * c.y + z.y * s.y);
+      }
+    }
+    a[j] = pack2<BF>(x.x, x.y);
+    b[j] = pack2<BF>(y.x, y.y);
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ float squares(const uint4& a4, float pre) {
+  const uint32_t* a = reinterpret_cast<const uint32_t*>(&a4);
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = unpack2<BF>(a[j]);
+    s = fmaf(x.x * pre, x.x * pre, s);
+    s = fmaf(x.y * pre, x.y * pre, s);
+  }
+  return s;
+}
+
+template <int D, bool BF, bool NORM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) {
   __shared__ __align__(16) float s_cs[kThreads / 32][2][D / 2];
   __shared__ unsigned long long s_freq[D / 2];
@@ -114,6 +166,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
   // this lane's frequencies, pairs lane and lane + 32, as fractions of a turn: found
   // once per block, as double precision runs at a few results per cycle and SM (in
   // every warp it took 2 us)
+  __shared__ __align__(16) float s_weight[NORM ? 2 : 1][NORM ? D : 4];
+  if (NORM && threadIdx.x < 2 * D) {
+    const float* w = threadIdx.x < D ? p.q_weight : p.k_weight;
+    s_weight[threadIdx.x / D][threadIdx.x % D] = w ? w[threadIdx.x % D] : 1.f;
+  }
   if (threadIdx.x < p.rot / 2) s_freq[threadIdx.x] = turn_fraction(p.inv_freq[threadIdx.x]);
   __syncthreads();
   constexpr int N = D / 64;
@@ -168,18 +225,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
     __syncwarp();
     uint16_t* page = p.codes + (size_t)(slot < 0 ? 0 : slot) * 2 * p.Hkv * p.P * D + (size_t)row * D;
     constexpr int M = 4;                                 // items in flight
-    for (int it0 = part * 32 + lane; it0 < n_items; it0 += 32 * W * M) {
+    for (int it0 = part * 32 + lane; it0 - (NORM ? lane : 0) < n_items; it0 += 32 * W * M) {   // NORM: by whole warps
       uint4 a[M], bb[M];
       uint16_t* dst[M];
       int un[M];                                         // >= 0: turned, with these pairs
+      int hw[M];                                         // NORM: 0 a query's head, 1 a key's, else V's
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         const int it = it0 + m * 32 * W;
         dst[m] = nullptr;
+        hw[m] = 2;
+        a[m] = bb[m] = make_uint4(0, 0, 0, 0);
         if (it >= n_items) continue;
         const int head = it / U, u = it % U;
         const bool turned = u < ru && head < p.Hq + p.Hkv, halves = turned && !p.adjacent;
         un[m] = turned ? u : -1;
+        hw[m] = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
         const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? p.rot / 2 + 8 * u : 16 * u + 8;
         const uint16_t* src;
         if (head < p.Hq) {
@@ -194,10 +255,34 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
         a[m] = *reinterpret_cast<const uint4*>(src + e0);
         bb[m] = *reinterpret_cast<const uint4*>(src + e1);
       }
+      if constexpr (NORM) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          float pre = 1.f, ss = squares<BF>(a[m], 1.f) + squares<BF>(bb[m], 1.f);
+#pragma unroll
+          for (int o = 1; o < U; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (BF && __any_sync(0xffffffffu, ss > 3e38f)) {   // squares beyond fp32's range (bf16 reaches as far as fp32)
+            float far = squares<BF>(a[m], 0x1p-70f) + squares<BF>(bb[m], 0x1p-70f);
+#pragma unroll
+            for (int o = 1; o < U; o *= 2) far += __shfl_xor_sync(0xffffffffu, far, o);
+            if (ss > 3e38f) {
+              ss = far;
+              pre = 0x1p-70f;
+            }
+          }
+          if (hw[m] < 2) {
+            const int u = (it0 + m * 32 * W) % U;
+            const bool halves = un[m] >= 0 && !p.adjacent;
+            const float* w = s_weight[hw[m]];
+            norm_pair<BF>(a[m], bb[m], pre, rsqrtf(ss * (1.f / D) + (pre == 1.f ? p.eps : p.eps * 0x1p-140f)), w + (halves ? 8 : 16) * u,
+                          w + (halves ? p.rot / 2 + 8 * u : 16 * u + 8), cs, sn, un[m], p.adjacent);
+          }
+        }
+      }
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         if (!dst[m]) continue;
-        if (un[m] >= 0) turn_pair<BF>(a[m], bb[m], cs, sn, un[m], p.adjacent);
+        if (!NORM && un[m] >= 0) turn_pair<BF>(a[m], bb[m], cs, sn, un[m], p.adjacent);
         *reinterpret_cast<uint4*>(dst[m]) = a[m];
         *reinterpret_cast<uint4*>(dst[m] + ((un[m] >= 0 && !p.adjacent) ? p.rot / 2 : 8)) = bb[m];
       }
@@ -205,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
   }
 }
 
-template <int D, bool BF>
+template <int D, bool BF, bool NORM>
 static argus_status launch(const RParams& p, cudaStream_t s) {
   constexpr int kWarps = kThreads / 32;
   const long long sms = device_sm_count();
@@ -219,10 +304,10 @@ static argus_status launch(const RParams& p, cudaStream_t s) {
   cfg.gridDim = dim3((int)std::min(blocks, sms * 3));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, BF>, p, W);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, BF, NORM>, p, W);
   if (e == cudaSuccess) return ARGUS_OK;
   cudaGetLastError();                  // not left for the next call to find
-  return fail(ARGUS_E_LAUNCH, "argus_rope_append: launch failed: %s", cudaGetErrorString(e));
+  return fail(ARGUS_E_LAUNCH, "argus_%srope_append: launch failed: %s", NORM ? "norm_" : "", cudaGetErrorString(e));
 }
 
 // Whether two tensors of n tokens share memory: tokens of la and lb bytes, sa >= la and
@@ -246,12 +331,9 @@ static bool tokens_meet(uintptr_t a, long long la, long long sa, uintptr_t b, lo
   return false;
 }
 
-}  // namespace rope
-}  // namespace argus
-
-using namespace argus;
-
-extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream) {
+// The arguments that both forms share, checked and brought into the kernel's form; p.total stays 0
+// where there is nothing to do.
+static argus_status params(const argus_rope_args* a, RParams& p) {
   if (!a) return fail(ARGUS_E_INVALID, "rope: args is NULL");
   const argus_geom& g = a->g;
   if (g.n_q_heads <= 0 || g.n_kv_heads <= 0 || g.n_q_heads % g.n_kv_heads || g.page_tokens <= 0)
@@ -261,7 +343,7 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   if (g.page_tokens % 16) return fail(ARGUS_E_UNSUPPORTED, "rope: page_tokens %d not a multiple of 16", g.page_tokens);
   if (a->dtype != ARGUS_FP16 && a->dtype != ARGUS_BF16) return fail(ARGUS_E_INVALID, "rope: dtype must be FP16 or BF16");
   if (a->batch < 0 || a->total_q < 0 || a->max_pages < 0) return fail(ARGUS_E_INVALID, "rope: negative size");
-  if (a->n_axes < 1 || a->n_axes > rope::kMaxAxes) return fail(ARGUS_E_INVALID, "rope: n_axes %d not in 1..4", a->n_axes);
+  if (a->n_axes < 1 || a->n_axes > kMaxAxes) return fail(ARGUS_E_INVALID, "rope: n_axes %d not in 1..4", a->n_axes);
   if (a->adjacent != 0 && a->adjacent != 1) return fail(ARGUS_E_INVALID, "rope: adjacent must be 0 or 1");
   if (a->rot_dim <= 0 || a->rot_dim > g.head_dim) return fail(ARGUS_E_INVALID, "rope: rot_dim %d not in 1..head_dim", a->rot_dim);
   if (a->rot_dim % 16) return fail(ARGUS_E_UNSUPPORTED, "rope: rot_dim %d not a multiple of 16", a->rot_dim);
@@ -272,7 +354,6 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   if (a->pool->codec != a->dtype) return fail(ARGUS_E_UNSUPPORTED, "rope: the pool's codec %d is not the tokens' type", a->pool->codec);
   if (a->pool->placement != ARGUS_PLACE_DEVICE) return fail(ARGUS_E_UNSUPPORTED, "rope: the pool must lie in device memory");
   if (a->pool->n_slots < 0 || (a->pool->n_slots > 0 && !a->pool->codes)) return fail(ARGUS_E_INVALID, "rope: bad pool");
-  rope::RParams p{};
   p.Hq = g.n_q_heads;
   p.Hkv = g.n_kv_heads;
   p.P = g.page_tokens;
@@ -290,7 +371,7 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   if (a->q_out == a->q && p.qs != p.qos) return fail(ARGUS_E_INVALID, "rope: q_out in place needs q's stride");
   // a token is turned while others are still read
   const auto over = [&](const void* x, int heads, long long stride) {
-    return rope::tokens_meet(reinterpret_cast<uintptr_t>(a->q_out), 2ll * p.Hq * D, 2 * p.qos, reinterpret_cast<uintptr_t>(x), 2ll * heads * D,
+    return tokens_meet(reinterpret_cast<uintptr_t>(a->q_out), 2ll * p.Hq * D, 2 * p.qos, reinterpret_cast<uintptr_t>(x), 2ll * heads * D,
                              2 * stride, a->total_q);
   };
   if ((a->q_out != a->q && over(a->q, p.Hq, p.qs)) || over(a->k, p.Hkv, p.ks) || over(a->v, p.Hkv, p.vs))
@@ -316,8 +397,39 @@ extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream
   p.page_codec = a->page_codec;
   p.block_table = a->block_table;
   p.status = a->status;
+  return ARGUS_OK;
+}
+
+template <bool NORM>
+static argus_status run(const argus_rope_args* a, const RParams& p, void* stream) {
+  if (p.total == 0) return ARGUS_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = a->dtype == ARGUS_BF16;
-  if (D == 64) return bf ? rope::launch<64, true>(p, s) : rope::launch<64, false>(p, s);
-  return bf ? rope::launch<128, true>(p, s) : rope::launch<128, false>(p, s);
+  if (a->g.head_dim == 64) return bf ? launch<64, true, NORM>(p, s) : launch<64, false, NORM>(p, s);
+  return bf ? launch<128, true, NORM>(p, s) : launch<128, false, NORM>(p, s);
+}
+
+}  // namespace rope
+}  // namespace argus
+
+using namespace argus;
+
+extern "C" argus_status argus_rope_append(const argus_rope_args* a, void* stream) {
+  rope::RParams p{};
+  const argus_status st = rope::params(a, p);
+  return st != ARGUS_OK ? st : rope::run<false>(a, p, stream);
+}
+
+extern "C" argus_status argus_norm_rope_append(const argus_rope_args* a, const float* q_weight, const float* k_weight, float eps, void* stream) {
+  rope::RParams p{};
+  const argus_status st = rope::params(a, p);
+  if (st != ARGUS_OK) return st;
+  // below 2^-100 squares that fp32 cannot hold would count beside it
+  if (!(eps >= 0x1p-100f) || !std::isfinite(eps)) return fail(ARGUS_E_INVALID, "rope: eps must be finite and at least 2^-100");
+  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 3)
+    return fail(ARGUS_E_INVALID, "rope: the norms' weights must be 4-byte aligned");
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  return rope::run<true>(a, p, stream);
 }
