@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AParams p) {
   const int len = p.seq_lens[b], n = max(p.q_start[b + 1] - p.q_start[b], 0), want = p.n_path[b];
   const int m = len < n ? 0 : min(max(want, 0), p.width);
   const long long base = (long long)len - n;
-  int taken = 0, bad = len < n || want != min(max(want, 0), p.width);
+  int taken = 0, bad = (len < n) + (want != min(max(want, 0), p.width));
   for (int k0 = 0; k0 < m; k0 += 32) {
     if (warp == 0) {
       const int k = k0 + lane;

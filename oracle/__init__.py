@@ -49,3 +49,6 @@ from .selection import compressed_key_scores, select_pages  # noqa: F401
 from .cache import (  # noqa: F401
     paged_extend, rotate, append_places, fork_pages, compact_pages,
 )
+from .drafts import (  # noqa: F401
+    window_sees, tree_sees, head_norm, accept_tokens, attn_weights, evict_keep, evict_tokens,
+)

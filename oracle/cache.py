@@ -17,7 +17,7 @@ from .codecs import dequant_page
 
 def sequence_kv(Hkv, P, pools, page_codec, block_table, b, length):
     """K, V float64 [Hkv][n][D], the positions of those n keys, their pages' V scales
-    [Hkv][n] (1 for 16-bit pages) and the number of pages that name no slot (left out)."""
+    [Hkv][n] (1 for 16-bit and group-coded pages) and the number of pages that name no slot (left out)."""
     K, V, pos, vs, bad = [], [], [], [], 0
     for p in range((length + P - 1) // P):
         codec, slot = int(page_codec[b, p]), int(block_table[b, p])
@@ -29,18 +29,24 @@ def sequence_kv(Hkv, P, pools, page_codec, block_table, b, length):
         K.append(np.stack([dequant_page(codec, codes, meta, slot, 0, h)[:n] for h in range(Hkv)]))
         V.append(np.stack([dequant_page(codec, codes, meta, slot, 1, h)[:n] for h in range(Hkv)]))
         pos.append(p * P + np.arange(n))
-        vs.append(np.repeat(np.ones(Hkv) if codec < 2 else np.asarray(meta[slot, 1], np.float64), n).reshape(Hkv, n))
+        vs.append(np.repeat(np.ones(Hkv) if codec < 2 or codec >= 4 else np.asarray(meta[slot, 1], np.float64), n).reshape(Hkv, n))
     if not K:
         return None, None, np.zeros(0, int), None, bad
     return np.concatenate(K, 1), np.concatenate(V, 1), np.concatenate(pos), np.concatenate(vs, 1), bad
 
 
-def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, scale, causal=True):
+def _named(pools, codec, slot):
+    return int(codec) in pools and 0 <= slot < pools[int(codec)][0].shape[0]
+
+
+def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, scale, causal=True, sees=None):
     """q float64 [total][Hq][D].  Returns o, lse2, bad and, for error bounds,
     av = sum_j p_j |v_j| and pc = max_j (p_j s_j) sum_j |v_j| / s_j with the V scales s_j
     (as o, over sum_j p_j), qk = max_j scale log2(e) sum_d |q_d k_jd| and
     smax = max_j |score_j| in the log2 domain (as lse2).  Rows of no sequence and rows
-    that see nothing have o = 0, lse2 = -inf."""
+    that see nothing have o = 0, lse2 = -inf.  sees(b, i, n, L, pos): which of the positions
+    pos of L token i of n sees, in place of the causal rule.  A page without a visible
+    position for any token is not counted as bad."""
     total, Hq, D = q.shape
     G = Hq // Hkv
     o, av, pc = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
@@ -54,11 +60,17 @@ def paged_extend(q, q_start, Hkv, P, pools, page_codec, block_table, seq_lens, s
             continue
         L = max(0, min(int(seq_lens[b]), max_pages * P))
         K, V, pos, vs, nbad = sequence_kv(Hkv, P, pools, page_codec, block_table, b, L)
+        if sees is not None:
+            cached = np.arange(L)
+            seen = np.zeros(L, bool)
+            for t in range(t0, t1):
+                seen |= sees(b, t - t0, t1 - t0, L, cached)
+            nbad = sum(not _named(pools, page_codec[b, p], block_table[b, p]) for p in sorted(set(cached[seen] // P)))
         bad += nbad
         if K is None:
             continue
         for t in range(t0, t1):
-            keep = pos <= L - (t1 - t0) + (t - t0) if causal else np.ones(len(pos), bool)
+            keep = sees(b, t - t0, t1 - t0, L, pos) if sees is not None else pos <= L - (t1 - t0) + (t - t0) if causal else np.ones(len(pos), bool)
             if not keep.any():
                 continue
             for hq in range(Hq):
