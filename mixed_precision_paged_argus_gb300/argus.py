@@ -544,11 +544,18 @@ def paged_extend_attn(args, ws, stream=None):
     _check(lib().argus_paged_extend_attn(ctypes.byref(args), _ws_at(ws, args._device), ws.nbytes, _stream_of(args._device, stream)))
 
 
+def _int32(name, x):
+    """x as the library's 32-bit integer: ctypes would drop the bits above."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError("%s = %d does not fit in 32 bits" % (name, x))
+    return x
+
+
 def paged_window_extend_attn(args, ws, window_tokens, sink_tokens=0, stream=None):
     """paged_extend_attn where a token sees the newest window_tokens positions up
     to its own and the first sink_tokens; ws of extend_workspace_bytes bytes."""
-    _check(lib().argus_paged_window_extend_attn(ctypes.byref(args), window_tokens, sink_tokens, _ws_at(ws, args._device), ws.nbytes,
-                                                _stream_of(args._device, stream)))
+    _check(lib().argus_paged_window_extend_attn(ctypes.byref(args), _int32("window_tokens", window_tokens), _int32("sink_tokens", sink_tokens),
+                                                _ws_at(ws, args._device), ws.nbytes, _stream_of(args._device, stream)))
 
 
 def paged_tree_attn(args, ws, tree_mask, stream=None):
@@ -568,7 +575,7 @@ def accept_tokens(g, pool, page_codec, block_table, max_pages, q_start, seq_lens
     batch, dev = seq_lens.numel(), seq_lens.get_device()
     if path.dim() != 2 or path.shape[0] != batch:
         raise ValueError("path must be [%d][width], not %s" % (batch, list(path.shape)))
-    entries = batch * max_pages
+    entries = batch * _int32("max_pages", max_pages)
     _check(lib().argus_accept_tokens(
         ctypes.byref(g), batch, _pool_array((pool,), dev, g), _at("page_codec", page_codec, _U8, entries, dev),
         _at("block_table", block_table, _I32, entries, dev), max_pages, _at("q_start", q_start, _I32, batch + 1, dev),
@@ -597,12 +604,13 @@ def evict_tokens(g, pools, page_codec, block_table, seq_lens, max_pages, weights
     for name, t in (("weights", weights), ("weights_out", weights_out)):
         if t.dim() != 3 or t.shape[0] != batch or t.shape[1] != hkv:
             raise ValueError("%s must be [%d][%d][positions], not %s" % (name, batch, hkv, list(t.shape)))
-    entries = batch * max_pages
+    entries = batch * _int32("max_pages", max_pages)
     _check(lib().argus_evict_tokens(
         ctypes.byref(g), batch, _pool_array(pools, dev, g), len(pools), _at("page_codec", page_codec, _U8, entries, dev),
         _at("block_table", block_table, _I32, entries, dev), _at("seq_lens", seq_lens, _I32, 0, dev), max_pages,
-        _at("weights", weights, _F32, 0, dev), weights.shape[2], budget, sink_tokens, recent_tokens, _pool_array((dst,), dev, g),
-        _at("dst_table", dst_table, _I32, batch * dst_pages, dev), dst_pages, _at("seq_lens_out", seq_lens_out, _I32, batch, dev),
+        _at("weights", weights, _F32, 0, dev), weights.shape[2], _int32("budget", budget),
+        _int32("sink_tokens", sink_tokens), _int32("recent_tokens", recent_tokens), _pool_array((dst,), dev, g),
+        _at("dst_table", dst_table, _I32, batch * dst_pages, dev), _int32("dst_pages", dst_pages), _at("seq_lens_out", seq_lens_out, _I32, batch, dev),
         _at("kept", kept, _I32, batch * hkv * budget, dev), _at("weights_out", weights_out, _F32, 0, dev), weights_out.shape[2],
         _status_at(status, dev), _stream_of(dev, stream)))
 
