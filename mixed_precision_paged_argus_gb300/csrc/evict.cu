@@ -19,6 +19,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -56,7 +57,7 @@ __device__ __forceinline__ int length(const VParams& p, int b) {
 
 // ---------------------------------------------------------------- selection
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
-constexpr int kRegKeys = 32;           // keys per thread that stay in registers
+constexpr int kRegKeys = 32;           // keys per thread that stay in registers, at most
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t order(float w) {
@@ -76,9 +77,8 @@ __device__ __forceinline__ Counts warp_sum(Counts x) {
   return x;
 }
 
-// REG: a thread's keys (at most kRegKeys) stay in registers; else they are read again in every
-// round.
-template <bool REG>
+// KEYS: a thread's keys, which stay in registers; 0: they are read again in every round.
+template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p) {
   __shared__ Counts s_warp[2][kSelWarps];
   __shared__ Counts s_block[2];
@@ -88,43 +88,42 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
   const long long row = (long long)b * p.Hkv + h;
   const float* w = p.weights + row * p.row_len;
   int32_t* kept = p.kept + row * p.budget;
-  float* w_out = p.weights_out + row * p.row_len_out;
   const int len = length(p, b), m = min(len, p.budget);
   if (threadIdx.x == 0 && rank == 0 && h == 0) p.seq_lens_out[b] = m;
   // behind the kept positions
   const int tid = rank * kSelThreads + threadIdx.x, all = C * kSelThreads;
   for (int i = m + tid; i < p.budget; i += all) kept[i] = -1;
+  float* w_out = p.weights_out + row * p.row_len_out;
   for (long long i = m + tid; i < p.row_len_out; i += all) w_out[i] = 0.f;
   if (len <= p.budget) {                               // the same in the whole cluster
-    for (int i = tid; i < m; i += all) {
-      kept[i] = i;
-      w_out[i] = w[i];
-    }
+    for (int i = tid; i < m; i += all) kept[i] = i;
     return;
   }
   const int lo = p.sinks, hi = len - p.recent, k = p.budget - p.sinks - p.recent;   // candidates lo .. hi-1: more than k
   // this warp's positions: steps of 32 neighbours
-  const long long per = ((long long)len + (long long)C * kSelThreads - 1) / ((long long)C * kSelThreads);
-  const long long start = ((long long)rank * kSelWarps + warp) * per * 32;
-  const int steps = (int)per;
-  uint32_t key[REG ? kRegKeys : 1];
-  auto load = [&](int i) -> uint32_t {                 // 0 (below all) for what is not a candidate
-    const long long pos = start + i * 32ll + lane;
-    return pos >= lo && pos < hi ? order(w[pos]) : 0u;
+  const long long all_steps = (long long)C * kSelThreads;
+  const int steps = KEYS > 0 ? KEYS : (int)((len + all_steps - 1) / all_steps);
+  const long long start = ((long long)rank * kSelWarps + warp) * steps * 32 + lane;
+  auto load = [&](int i) -> float {                    // NaN (below all) for what is not a candidate
+    const long long pos = start + i * 32ll;
+    return pos >= lo && pos < hi ? __ldg(w + pos) : __uint_as_float(0x7FC00000u);
   };
-  auto each = [&](auto f) {
-    if constexpr (REG) {
+  uint32_t key[KEYS > 0 ? KEYS : 1];
+  if constexpr (KEYS > 0) {
+    float x[KEYS];                                     // all on their way at once
 #pragma unroll
-      for (int i = 0; i < kRegKeys; ++i)
-        if (i < steps) f(i, key[i]);
+    for (int i = 0; i < KEYS; ++i) x[i] = load(i);
+#pragma unroll
+    for (int i = 0; i < KEYS; ++i) key[i] = order(x[i]);
+  }
+  auto each = [&](auto f) {
+    if constexpr (KEYS > 0) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) f(i, key[i]);
     } else {
-      for (int i = 0; i < steps; ++i) f(i, load(i));
+      for (int i = 0; i < steps; ++i) f(i, order(load(i)));
     }
   };
-  if constexpr (REG) {
-#pragma unroll
-    for (int i = 0; i < kRegKeys; ++i) key[i] = i < steps ? load(i) : 0u;
-  }
   int turn = 0;
   // sums over the cluster; with `before`, those over the warps in front of this one too
   auto total = [&](Counts x, Counts* before) {
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     ties = exact ? 0xFFFFFFFFu : (uint32_t)k - upper;
   }
   auto stays = [&](int i, uint32_t x, bool& tie) {
-    const long long pos = start + i * 32ll + lane;
+    const long long pos = start + i * 32ll;
     const bool mid = pos >= lo && pos < hi;
     tie = mid && x == T && ties > 0;
     return (pos < lo || (pos >= hi && pos < len)) || (mid && x > T);
@@ -201,10 +200,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     const bool keep = stay || (tie && tied + __popc(eq & lt) < ties);
     const uint32_t mask = __ballot_sync(0xffffffffu, keep);
     if (keep) {
-      const uint32_t to = at + __popc(mask & lt);
-      const long long pos = start + i * 32ll + lane;
-      kept[to] = (int32_t)pos;
-      w_out[to] = w[pos];
+      kept[at + __popc(mask & lt)] = (int32_t)(start + i * 32ll);
     }
     at += __popc(mask);
     tied += __popc(eq);
@@ -215,9 +211,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
 // ---------------------------------------------------------------- gathering
 constexpr int kWarps = 8;
 
-// 16 values of a row, as they lie in the page
+// 16 values of a row, as they lie in the page; in a 16-bit page 32 bytes, else 16 at most and
+// the scale (and zero).
+template <bool WIDE>
 struct Raw {
-  uint4 a, b;
+  uint4 a;
+  uint4 b;
+};
+template <>
+struct Raw<false> {
+  uint4 a;
+  uint32_t s;
 };
 
 template <bool BF>
@@ -232,19 +236,23 @@ struct Place {
   int row, codec;
 };
 
-template <int D>
-__device__ __forceinline__ Raw fetch(const VParams& p, const Place& s, int kv, int v) {
-  Raw r;
-  r.a = r.b = make_uint4(0, 0, 0, 0);
+template <int D, bool WIDE>
+__device__ __forceinline__ Raw<WIDE> fetch(const VParams& p, const Place& s, int kv, int v) {
+  Raw<WIDE> r = {};
+  uint32_t scale = 0;
   if (s.codec < 0) return r;
   const long long at = ((s.unit + (kv ? p.Hkv : 0)) * p.P + s.row) * D + 16 * v;   // in values
   const uint8_t* c = p.pool[s.codec].codes;
-  if (s.codec <= ARGUS_BF16) {
-    r.a = __ldg(reinterpret_cast<const uint4*>(c + 2 * at));
-    r.b = __ldg(reinterpret_cast<const uint4*>(c + 2 * at) + 1);
-  } else if (s.codec <= ARGUS_INT8) {
+  if constexpr (WIDE) {
+    if (s.codec <= ARGUS_BF16) {
+      r.a = __ldg(reinterpret_cast<const uint4*>(c + 2 * at));
+      r.b = __ldg(reinterpret_cast<const uint4*>(c + 2 * at) + 1);
+      return r;
+    }
+  }
+  if (s.codec <= ARGUS_INT8) {
     r.a = __ldg(reinterpret_cast<const uint4*>(c + at));
-    r.b.x = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + s.unit + (kv ? p.Hkv : 0));
+    scale = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + s.unit + (kv ? p.Hkv : 0));
   } else {
     if (s.codec == ARGUS_INT4_G32) {
       const uint2 x = __ldg(reinterpret_cast<const uint2*>(c + at / 2));
@@ -255,34 +263,45 @@ __device__ __forceinline__ Raw fetch(const VParams& p, const Place& s, int kv, i
     } else {
       r.a.x = __ldg(reinterpret_cast<const uint16_t*>(c + at / 8));
     }
-    r.b.x = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + at / 32);   // scale, zero
+    scale = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + at / 32);   // scale, zero
   }
+  if constexpr (WIDE) r.b.x = scale;
+  else r.s = scale;
   return r;
 }
 
-__device__ __forceinline__ void values(const Raw& r, int codec, float (&x)[16]) {
-  const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-  if (codec == ARGUS_FP16 || codec == ARGUS_BF16) {
+template <bool WIDE>
+__device__ __forceinline__ void values(const Raw<WIDE>& r, int codec, float (&x)[16]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  uint32_t scale;
+  if constexpr (WIDE) {
+    scale = r.b.x;
+    if (codec == ARGUS_FP16 || codec == ARGUS_BF16) {
+      const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 y = codec == ARGUS_BF16 ? two<true>(w[i]) : two<false>(w[i]);
-      x[2 * i] = y.x;
-      x[2 * i + 1] = y.y;
+      for (int i = 0; i < 8; ++i) {
+        const float2 y = codec == ARGUS_BF16 ? two<true>(u[i]) : two<false>(u[i]);
+        x[2 * i] = y.x;
+        x[2 * i + 1] = y.y;
+      }
+      return;
     }
-  } else if (codec == ARGUS_FP8_E4M3) {
-    const float s = __uint_as_float(r.b.x);
+  } else {
+    scale = r.s;
+  }
+  if (codec == ARGUS_FP8_E4M3) {
+    const float s = __uint_as_float(scale);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 y = two<false>(e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1))));
-      x[2 * i] = y.x * s;
-      x[2 * i + 1] = y.y * s;
+      f2_mul(x[2 * i], x[2 * i + 1], y.x, y.y, s, s);
     }
   } else if (codec == ARGUS_INT8) {
-    const float s = __uint_as_float(r.b.x);
+    const float s = __uint_as_float(scale);
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = (float)(int8_t)(w[i / 4] >> (8 * (i & 3))) * s;
   } else if (codec > 0) {
-    const float2 sz = two<false>(r.b.x);
+    const float2 sz = two<false>(scale);
     const int bits = codec == ARGUS_INT4_G32 ? 4 : codec == ARGUS_INT2_G32 ? 2 : 1;
     const unsigned long long q = (unsigned long long)w[1] << 32 | w[0];
 #pragma unroll
@@ -293,31 +312,101 @@ __device__ __forceinline__ void values(const Raw& r, int codec, float (&x)[16]) 
   }
 }
 
+// The largest magnitude of 16 values.  Of an e4m3 row it is the largest code's: a product with
+// the same scale keeps the order.
+template <bool WIDE>
+__device__ __forceinline__ float largest(const Raw<WIDE>& r, int codec) {
+  float top = 0.f;
+  if (codec == ARGUS_FP8_E4M3) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+    __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t y = e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)));
+      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&y)));
+    }
+    uint32_t scale;
+    if constexpr (WIDE) scale = r.b.x;
+    else scale = r.s;
+    top = fabsf(fmaxf(__low2float(m), __high2float(m)) * __uint_as_float(scale));
+  } else {
+    float x[16];
+    values(r, codec, x);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+  }
+  return top;
+}
+
+// Four codes of y = RN(x / scale).  x times the reciprocal is off by at most 3 2^-24 of y, so
+// y lies between x rcp (1 - 2^-21) and x rcp (1 + 2^-21); both codes are formed, and as
+// encoding keeps the order, y's is theirs where they agree.
+template <int DST>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  if (DST == ARGUS_FP8_E4M3) return f32x2_to_e4m3x2(a, b) | f32x2_to_e4m3x2(c, d) << 16;
+  const float x[4] = {a, b, c, d};
+  uint32_t o = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o |= ((uint32_t)(int)fminf(fmaxf(rintf(x[j]), -127.f), 127.f) & 0xFFu) << (8 * j);
+  return o;
+}
+template <int DST>
+__device__ __forceinline__ uint4 encode(const float (&x)[16], float scale) {
+  uint32_t o[4] = {0, 0, 0, 0};
+  if (scale > 0.f) {
+    const float rcp = 1.f / scale, lo = rcp * (1.f - 0x1p-21f), hi = rcp * (1.f + 0x1p-21f);
+    bool same = scale >= 0x1p-120f && scale <= 0x1p120f;   // outside the reciprocal could lose bits
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float a[4], b[4];
+      f2_mul(a[0], a[1], x[4 * e], x[4 * e + 1], lo, lo);
+      f2_mul(a[2], a[3], x[4 * e + 2], x[4 * e + 3], lo, lo);
+      f2_mul(b[0], b[1], x[4 * e], x[4 * e + 1], hi, hi);
+      f2_mul(b[2], b[3], x[4 * e + 2], x[4 * e + 3], hi, hi);
+      o[e] = encode4<DST>(a[0], a[1], a[2], a[3]);
+      same &= o[e] == encode4<DST>(b[0], b[1], b[2], b[3]);
+    }
+    if (!same) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = encode4<DST>(x[4 * e] / scale, x[4 * e + 1] / scale, x[4 * e + 2] / scale, x[4 * e + 3] / scale);
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Rows row0 .. row0 + 15 of KV head h of sequence b's new cache, by a warp: the places, a row per lane
-// (lanes 16 to 31 hold those of 0 to 15).
-__device__ __forceinline__ Place find(const VParams& p, int b, int h, int row0, int m, int lane, bool& lost) {
+// (lanes 16 to 31 hold those of 0 to 15).  `first`: their weights are copied, and rows
+// without a place counted.
+__device__ __forceinline__ Place find(const VParams& p, int b, int h, int row0, int m, int lane, bool first) {
   Place s = {0, 0, -1};
   const int r = row0 + (lane & 15);
-  lost = false;
+  const long long unit = (long long)b * p.Hkv + h;
+  bool lost = false;
   if (r < m) {
-    const int pos = p.kept[((long long)b * p.Hkv + h) * p.budget + r];
+    const int pos = p.kept[unit * p.budget + r];
     const int page = (int)((unsigned)pos / (unsigned)p.P);
     const size_t e = (size_t)b * p.max_pages + page;
     const int codec = p.page_codec[e];
     const long long slot = p.block_table[e];
     lost = codec > ARGUS_INT1_G32 || slot < 0 || slot >= p.pool[codec > ARGUS_INT1_G32 ? 0 : codec].n_slots;
     if (!lost) s = {slot * 2 * p.Hkv + h, pos - page * p.P, codec};
+    if (first && lane < 16) p.weights_out[unit * p.row_len_out + r] = __ldg(p.weights + unit * p.row_len + pos);
+  }
+  if (first) {
+    const unsigned x = __ballot_sync(0xffffffffu, lost && lane < 16);
+    if (x && lane == 0 && p.status) atomicAdd(p.status, __popc(x));
   }
   return s;
 }
 
-// DST: the new pages' codec.  T warps share a page (1 where rows need no scale): teams of
-// 1, 2, 4 or 8, so that a page of up to 128 tokens has a warp per 16 rows and is read once.
-template <int D, int DST>
+// DST: the new pages' codec; WIDE: there are 16-bit pages among the old.  T warps share a page (1
+// where rows need no scale): teams of 1, 2, 4 or 8, so that a page of up to 128 tokens
+// has a warp per 16 rows and is read once.
+template <int D, int DST, bool WIDE>
 __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const VParams p, int T, int units) {
   constexpr bool kScaled = DST == ARGUS_FP8_E4M3 || DST == ARGUS_INT8;
   constexpr int V = D / 16, RS = 32 / V, STEPS = 16 / RS;   // lanes per row, rows per step
-  __shared__ uint32_t s_max[2][kWarps];
+  __shared__ float s_max[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / T, tw = warp % T;
   const int unit = blockIdx.x * (kWarps / T) + team;        // KV heads fastest, then pages (or 16-row groups), then sequences
   if (unit >= units) return;                                // whole teams
@@ -327,23 +416,10 @@ __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const VParams p, in
   const int page = row0 / p.P, in_page = row0 - page * p.P;
   if (row0 - in_page >= m) return;                          // a page that holds something is written whole
   const long long slot = p.dst_table[(size_t)b * p.dst_pages + page];
-  if (slot < 0 || slot >= p.dst_slots) {
-    if (p.status && h == 0 && in_page == 0 && tw == 0 && lane == 0) atomicAdd(p.status, 1u);
-    return;
-  }
   const int subs = rows / 16;
   const bool once = subs <= T;                              // every warp has one group of 16 rows at most
   const int v = lane % V;
   Place s = {0, 0, -1};
-  Raw raw[STEPS];
-  auto places = [&](int sub, bool count) {
-    bool lost;
-    s = find(p, b, h, row0 + 16 * sub, m, lane, lost);
-    if (count) {
-      const unsigned x = __ballot_sync(0xffffffffu, lost && lane < 16);
-      if (x && lane == 0 && p.status) atomicAdd(p.status, __popc(x));
-    }
-  };
   auto place_of = [&](int step) {
     const int r = step * RS + lane / V;
     Place y;
@@ -352,9 +428,15 @@ __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const VParams p, in
     y.codec = __shfl_sync(0xffffffffu, s.codec, r);
     return y;
   };
+  for (int sub = tw; sub < subs; sub += T) s = find(p, b, h, row0 + 16 * sub, m, lane, true);
+  if (slot < 0 || slot >= p.dst_slots) {                    // the whole team
+    if (p.status && h == 0 && in_page == 0 && tw == 0 && lane == 0) atomicAdd(p.status, 1u);
+    return;
+  }
+  Raw<WIDE> raw[2][STEPS];                                  // K and V on their way together where they are narrow
   auto read = [&](int kv) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) raw[i] = fetch<D>(p, place_of(i), kv, v);
+    for (int i = 0; i < STEPS; ++i) raw[WIDE ? 0 : kv][i] = fetch<D, WIDE>(p, place_of(i), kv, v);
   };
   auto write = [&](int sub, int kv, float scale) {
     const long long at = (((slot * 2 + kv) * p.Hkv + h) * p.P + in_page + 16 * sub) * D + 16 * v;
@@ -362,71 +444,65 @@ __global__ void __launch_bounds__(32 * kWarps) gather_kernel(const VParams p, in
     for (int i = 0; i < STEPS; ++i) {
       const int r = i * RS + lane / V, codec = __shfl_sync(0xffffffffu, s.codec, r);
       const long long to = at + (long long)r * D;
-      if (DST <= ARGUS_BF16) {
-        Raw y = raw[i];
-        if (codec != DST) {
-          float x[16];
-          values(raw[i], codec, x);
-          uint32_t* o = reinterpret_cast<uint32_t*>(&y);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = DST == ARGUS_BF16 ? pack_bf16x2(x[2 * e], x[2 * e + 1]) : pack_f16x2(x[2 * e], x[2 * e + 1]);
-        }
+      const Raw<WIDE>& y = raw[WIDE ? 0 : kv][i];
+      if constexpr (!kScaled) {
         uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * to);
-        d[0] = y.a;
-        d[1] = y.b;
-      } else {
-        float x[16];
-        uint32_t o[4] = {0, 0, 0, 0};
-        values(raw[i], codec, x);
-        if (scale > 0.f) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = x[e] / scale;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (DST == ARGUS_FP8_E4M3) {
-              o[e] = f32x2_to_e4m3x2(x[4 * e], x[4 * e + 1]) | f32x2_to_e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16;
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[e] |= ((uint32_t)(int)fminf(fmaxf(rintf(x[4 * e + j]), -127.f), 127.f) & 0xFFu) << (8 * j);
-            }
+        if constexpr (WIDE) {
+          if (codec == DST) {                               // as it is
+            d[0] = y.a;
+            d[1] = y.b;
+            continue;
           }
         }
-        *reinterpret_cast<uint4*>(p.dst_codes + to) = make_uint4(o[0], o[1], o[2], o[3]);
+        float x[16];
+        uint32_t o[8];
+        values(y, codec, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = DST == ARGUS_BF16 ? pack_bf16x2(x[2 * e], x[2 * e + 1]) : pack_f16x2(x[2 * e], x[2 * e + 1]);
+        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      } else {
+        float x[16];
+        values(y, codec, x);
+        *reinterpret_cast<uint4*>(p.dst_codes + to) = encode<DST>(x, scale);
       }
     }
   };
   if constexpr (!kScaled) {
-    places(0, true);
+    if (!WIDE) {
+      read(0);
+      read(1);
+    }
+#pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      read(kv);
+      if (WIDE) read(kv);
       write(0, kv, 0.f);
     }
   } else {
-    if (tw < subs) places(tw, true);
+    if (!WIDE && once && tw < subs) {
+      read(0);
+      read(1);
+    }
+#pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      uint32_t top = 0;                                     // of the magnitudes' bits, which order like them
+      float top = 0.f;
       for (int sub = tw; sub < subs; sub += T) {
-        if (!once) places(sub, kv == 0 && sub != tw);
-        read(kv);
+        if (!once) s = find(p, b, h, row0 + 16 * sub, m, lane, false);
+        if (WIDE || !once) read(kv);
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) {
-          float x[16];
-          values(raw[i], __shfl_sync(0xffffffffu, s.codec, i * RS + lane / V), x);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-        }
+        for (int i = 0; i < STEPS; ++i) top = fmaxf(top, largest(raw[WIDE ? 0 : kv][i], __shfl_sync(0xffffffffu, s.codec, i * RS + lane / V)));
       }
-      top = __reduce_max_sync(0xffffffffu, top);
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));   // bits of magnitudes order like them
       if (T > 1) {
         if (lane == 0) s_max[kv][warp] = top;
         asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * T) : "memory");
-        for (int i = 0; i < T; ++i) top = max(top, s_max[kv][team * T + i]);
+        for (int i = 0; i < T; ++i) top = fmaxf(top, s_max[kv][team * T + i]);
       }
-      const float scale = __uint_as_float(top) / (DST == ARGUS_FP8_E4M3 ? 448.f : 127.f);
+      const float scale = top / (DST == ARGUS_FP8_E4M3 ? 448.f : 127.f);
       if (tw == 0 && lane == 0) p.dst_meta[(slot * 2 + kv) * p.Hkv + h] = scale;
       for (int sub = tw; sub < subs; sub += T) {
         if (!once) {
-          places(sub, false);
+          s = find(p, b, h, row0 + 16 * sub, m, lane, false);
           read(kv);
         }
         write(sub, kv, scale);
@@ -446,11 +522,16 @@ static cudaError_t launch_gather(const VParams& p, cudaStream_t s) {
   cfg.gridDim = dim3((unsigned)((units + per - 1) / per));
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
+  const bool wide = p.pool[ARGUS_FP16].n_slots > 0 || p.pool[ARGUS_BF16].n_slots > 0;
+  const auto go = [&](auto dst) {
+    constexpr int DST = decltype(dst)::value;
+    return wide ? cudaLaunchKernelEx(&cfg, gather_kernel<D, DST, true>, p, T, (int)units) : cudaLaunchKernelEx(&cfg, gather_kernel<D, DST, false>, p, T, (int)units);
+  };
   switch (p.dst_codec) {
-    case ARGUS_FP16: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_FP16>, p, T, (int)units);
-    case ARGUS_BF16: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_BF16>, p, T, (int)units);
-    case ARGUS_FP8_E4M3: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_FP8_E4M3>, p, T, (int)units);
-    default: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_INT8>, p, T, (int)units);
+    case ARGUS_FP16: return go(std::integral_constant<int, ARGUS_FP16>{});
+    case ARGUS_BF16: return go(std::integral_constant<int, ARGUS_BF16>{});
+    case ARGUS_FP8_E4M3: return go(std::integral_constant<int, ARGUS_FP8_E4M3>{});
+    default: return go(std::integral_constant<int, ARGUS_INT8>{});
   }
 }
 
@@ -475,7 +556,11 @@ static argus_status launch(const VParams& p, int D, cudaStream_t s) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  const argus_status st = status_of(C * keys >= longest ? cudaLaunchKernelEx(&cfg, select_kernel<true>, p) : cudaLaunchKernelEx(&cfg, select_kernel<false>, p), "selection");
+  const auto go = [&](auto n) { return cudaLaunchKernelEx(&cfg, select_kernel<decltype(n)::value>, p); };
+  const long long per = (longest + C * kSelThreads - 1) / (C * kSelThreads);
+  const argus_status st = status_of(per <= 4 ? go(std::integral_constant<int, 4>{}) : per <= 8 ? go(std::integral_constant<int, 8>{})
+                                    : per <= 16 ? go(std::integral_constant<int, 16>{}) : per <= 32 ? go(std::integral_constant<int, 32>{})
+                                                : go(std::integral_constant<int, 0>{}), "selection");
   // without the selection the gathering would follow whatever `kept` holds
   if (st != ARGUS_OK || p.budget == 0) return st;
   return status_of(D == 64 ? launch_gather<64>(p, s) : launch_gather<128>(p, s), "gathering");

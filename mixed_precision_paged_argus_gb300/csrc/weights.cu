@@ -15,11 +15,13 @@
 //    query's fragments are loaded in the order that makes these the operand.  8-bit codes become 16
 //    bits in registers, exactly; of INT4, INT2 and INT1 the codes are multiplied, and a
 //    token's scale and zero are applied per group of 32 dims.
-//  * The weights of a batch of chunks are summed in shared memory and added to the old ones
-//    in whole lines.
+//  * Two chunks at a time, copied into a ring of the warp's own some steps ahead: their 32 sums
+//    end up in the 32 lanes, one line of weights.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
+#include "codes.cuh"
 #include "common.cuh"
 
 namespace argus {
@@ -46,8 +48,14 @@ struct WParams {
   uint32_t* status;
 };
 
-constexpr int kWarps = 8;
+// Warps per block, blocks per SM, bytes of a warp's ring (pairs of chunks on their way) for calls with
+// pages of every codec, and with 8-bit ones alone.
+template <bool ANY>
+struct Shape {
+  static constexpr int kWarps = ANY ? 12 : 8, kBlocks = ANY ? 1 : 2, kRing = ANY ? 16384 : 12288;
+};
 constexpr int kBatch = 32;             // chunks looked up at once
+constexpr int kMaxSlots = 4;
 
 __device__ __forceinline__ long long warp_sum(long long x) {
 #pragma unroll
@@ -74,10 +82,90 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 
-// How a page's operands are formed: 16-bit as they are, 8-bit codes as fp16, group codes as fp16.
+// How a page's operands are formed, and with it the order of a row's dims in them.
 enum Form { kNone = -1, k16 = 0, k8 = 1, kGroup = 2 };
 __device__ __forceinline__ int form_of(int codec) { return codec <= ARGUS_BF16 ? k16 : codec <= ARGUS_INT8 ? k8 : kGroup; }
+
+// Sixteen keys as the MMA's A operand (BF: bf16, else fp16): rows lane / 4 and eight further down, dims by
+// the lane's place c in its row.  src: the chunk in shared memory.
+template <int D, bool BF, bool ANY>
+__device__ __forceinline__ void load_keys(uint32_t src, int codec, int lane, uint32_t (&a)[D / 16][4]) {
+  const int r = lane >> 2, c = lane & 3;
+  if (ANY && codec <= ARGUS_BF16) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 x = lds16(src + r * 2 * D + i * 64 + c * 16), y = lds16(src + (r + 8) * 2 * D + i * 64 + c * 16);
+      a[2 * i][0] = x.x;
+      a[2 * i][1] = y.x;
+      a[2 * i][2] = x.y;
+      a[2 * i][3] = y.y;
+      a[2 * i + 1][0] = x.z;
+      a[2 * i + 1][1] = y.z;
+      a[2 * i + 1][2] = x.w;
+      a[2 * i + 1][3] = y.w;
+    }
+  } else if (!ANY || codec <= ARGUS_INT8) {
+    uint4 y[2][D / 64];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) y[x][i] = lds16(src + (r + 8 * x) * D + i * 64 + c * 16);
+    }
+    auto turn = [&](auto fp8) {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t w[4] = {y[x][i].x, y[x][i].y, y[x][i].z, y[x][i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (decltype(fp8)::value) fp8_to_16<BF>(w[e], a[4 * i + e][x], a[4 * i + e][2 + x]);
+            else int8_to_16<BF>(w[e], a[4 * i + e][x], a[4 * i + e][2 + x]);
+          }
+        }
+      }
+    };
+    if (codec == ARGUS_FP8_E4M3) turn(std::true_type{});
+    else turn(std::false_type{});
+  } else {
+    const int bits = codec == ARGUS_INT4_G32 ? 4 : codec == ARGUS_INT2_G32 ? 2 : 1, row = D * bits / 8;
+    const uint32_t mask = ((1u << bits) - 1) * 0x10001u;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t at = src + (r + 8 * x) * row;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        // eight codes of group i: elements j and j + 4 in the two halves, j codes up
+        uint32_t w;
+        if (codec == ARGUS_INT4_G32) {
+          w = lds4(at + i * 16 + c * 4);
+        } else if (codec == ARGUS_INT2_G32) {
+          const uint32_t y = lds4(at + i * 8 + (c & 2) * 2) >> (16 * (c & 1));
+          w = (y & 0xFF) | (y >> 8 & 0xFF) << 16;
+        } else {
+          const uint32_t y = lds4(at + i * 4) >> (8 * c);
+          w = (y & 0xF) | (y >> 4 & 0xF) << 16;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {                    // fp16 1024 + code, minus 1024; bf16 128 + code, minus 128
+          const uint32_t y = (w >> (bits * j)) & mask;
+          a[2 * i + (j >> 1)][2 * (j & 1) + x] = BF ? bf2_sub(y | 0x43004300u, 0x43004300u) : hsub2_u32(y | 0x64006400u, 0x64006400u);
+        }
+      }
+    }
+  }
+}
 
 // Eight query rows as the MMA's B operand, in the dims' order of a form.
 template <int D>
@@ -87,7 +175,8 @@ struct Query {
   float sum[D / 32][2];                // kGroup: sums of a group's elements
 };
 
-template <int D, bool BF>
+// BF: the query's type.  TURN: a bf16 query becomes fp16 times a power of two per row.
+template <int D, bool BF, bool TURN>
 __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int form, int lane, Query<D>& out) {
   const int c = lane & 3;
   uint4 v[D / 32];                     // 8 elements each
@@ -95,10 +184,10 @@ __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int f
   for (int i = 0; i < D / 32; ++i) {
     // k8: two vectors next to each other, 16 codes; else every fourth
     const int at = form == k8 ? (i / 2) * 64 + c * 16 + (i & 1) * 8 : i * 32 + c * 8;
-    v[i] = real ? *reinterpret_cast<const uint4*>(row + at) : make_uint4(0, 0, 0, 0);
+    v[i] = real ? __ldg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0, 0, 0, 0);
   }
   float fac = 1.f;
-  if (BF && form != k16) {
+  if (TURN && form != k16) {
     // the row's largest magnitude comes to [2^14, 2^15): its 8 bits fit fp16
     uint32_t mx = 0;
 #pragma unroll
@@ -108,7 +197,7 @@ __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int f
     }
     mx = max_u16x2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = max_u16x2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    const uint32_t ex = max(max(mx >> 16, mx & 0xFFFFu) >> 7, 15u);
+    const uint32_t ex = max(max(mx >> 16, mx & 0xFFFFu) >> 7, 15u);   // biased; from 15 on 2^(141 - ex) is a normal number
     const float up = __uint_as_float((268 - ex) << 23);
     fac = __uint_as_float((ex - 14) << 23);
 #pragma unroll
@@ -125,8 +214,12 @@ __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int f
       float s = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
-        s += y.x + y.y;
+        if (BF && !TURN) {
+          s += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xFFFF0000u);
+        } else {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[e]));
+          s += y.x + y.y;
+        }
       }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
@@ -136,8 +229,11 @@ __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int f
       v[i] = make_uint4(prmt(w[0], w[2], 0x5410), prmt(w[0], w[2], 0x7632), prmt(w[1], w[3], 0x5410), prmt(w[1], w[3], 0x7632));
     }
   }
-  out.fac[0] = __shfl_sync(0xffffffffu, fac, 8 * c);
-  out.fac[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
+  out.fac[0] = out.fac[1] = 1.f;
+  if (TURN) {
+    out.fac[0] = __shfl_sync(0xffffffffu, fac, 8 * c);
+    out.fac[1] = __shfl_sync(0xffffffffu, fac, 8 * c + 4);
+  }
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
     out.f[2 * i][0] = v[i].x;
@@ -147,104 +243,37 @@ __device__ __forceinline__ void load_query(const uint16_t* row, bool real, int f
   }
 }
 
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-__device__ __forceinline__ void int8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;  // 1024 + (code + 128), minus 1152
-  lo = hsub2_u32(prmt(u, 0x64646464u, 0x4140), 0x64806480u);
-  hi = hsub2_u32(prmt(u, 0x64646464u, 0x4342), 0x64806480u);
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  if (BF) mma_bf16(d, a[0], a[1], a[2], a[3], b[0], b[1]);
+  else mma_f16(d, a[0], a[1], a[2], a[3], b[0], b[1]);
 }
 
 // Scores of 16 keys by 8 rows: d[0], d[1] key lane / 4, columns 2c and 2c + 1; d[2], d[3] eight keys
-// further down.
+// further down.  meta: the chunk's scales and zeros in shared memory (kGroup).
 template <int D, bool BF>
-__device__ __forceinline__ void scores(const uint8_t* src, const uint8_t* meta, int codec, int lane, const Query<D>& q, float (&d)[4]) {
-  const int r = lane >> 2, c = lane & 3;
-  d[0] = d[1] = d[2] = d[3] = 0.f;
-  if (codec <= ARGUS_BF16) {
-    uint4 a[D / 32], b[D / 32];
+__device__ __forceinline__ void scores(const uint32_t (&a)[D / 16][4], const Query<D>& q, int form, uint32_t meta, int lane, float (&d)[4]) {
+  if (form != kGroup) {
+    float e[4] = {0.f, 0.f, 0.f, 0.f};                   // two chains: an MMA does not wait for the one before
+    d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      a[i] = ldg16(src + r * 2 * D + i * 64 + c * 16);
-      b[i] = ldg16(src + (r + 8) * 2 * D + i * 64 + c * 16);
+    for (int i = 0; i < D / 16; i += 2) {
+      mma<BF>(d, a[i], q.f[i]);
+      mma<BF>(e, a[i + 1], q.f[i + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      if (BF) {
-        mma_bf16(d, a[i].x, b[i].x, a[i].y, b[i].y, q.f[2 * i][0], q.f[2 * i][1]);
-        mma_bf16(d, a[i].z, b[i].z, a[i].w, b[i].w, q.f[2 * i + 1][0], q.f[2 * i + 1][1]);
-      } else {
-        mma_f16(d, a[i].x, b[i].x, a[i].y, b[i].y, q.f[2 * i][0], q.f[2 * i][1]);
-        mma_f16(d, a[i].z, b[i].z, a[i].w, b[i].w, q.f[2 * i + 1][0], q.f[2 * i + 1][1]);
-      }
-    }
-  } else if (codec <= ARGUS_INT8) {
-    uint4 a[D / 64], b[D / 64];
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      a[i] = ldg16(src + r * D + i * 64 + c * 16);
-      b[i] = ldg16(src + (r + 8) * D + i * 64 + c * 16);
-    }
-#pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t a0, a1, b0, b1;
-        if (codec == ARGUS_FP8_E4M3) {
-          a0 = e4m3x2_to_f16x2(wa[e]);
-          a1 = e4m3x2_to_f16x2(wa[e] >> 16);
-          b0 = e4m3x2_to_f16x2(wb[e]);
-          b1 = e4m3x2_to_f16x2(wb[e] >> 16);
-        } else {
-          int8_to_f16(wa[e], a0, a1);
-          int8_to_f16(wb[e], b0, b1);
-        }
-        mma_f16(d, a0, b0, a1, b1, q.f[4 * i + e][0], q.f[4 * i + e][1]);
-      }
-    }
+    for (int x = 0; x < 4; ++x) d[x] += e[x];
   } else {
-    const int bits = codec == ARGUS_INT4_G32 ? 4 : codec == ARGUS_INT2_G32 ? 2 : 1, row = D * bits / 8;
-    const uint32_t mask = ((1u << bits) - 1) * 0x10001u;
-    uint32_t w[2][D / 32];
-    uint32_t sz[2][D / 32];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const uint8_t* at = src + (r + 8 * x) * row;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        // eight codes of group i: elements j and j + 4 in the two halves, j codes up
-        if (codec == ARGUS_INT4_G32) {
-          w[x][i] = __ldg(reinterpret_cast<const uint32_t*>(at + i * 16 + c * 4));
-        } else if (codec == ARGUS_INT2_G32) {
-          const uint32_t y = __ldg(reinterpret_cast<const uint16_t*>(at + i * 8 + c * 2));
-          w[x][i] = (y & 0xFF) | (y >> 8) << 16;
-        } else {
-          const uint32_t y = __ldg(at + i * 4 + c);
-          w[x][i] = (y & 0xF) | (y >> 4) << 16;
-        }
-        sz[x][i] = __ldg(reinterpret_cast<const uint32_t*>(meta) + (r + 8 * x) * (D / 32) + i);
-      }
-    }
+    d[0] = d[1] = d[2] = d[3] = 0.f;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      uint32_t o[2][4];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)                      // 1024 + code, minus 1024
-          o[x][j] = hsub2_u32(((w[x][i] >> (bits * j)) & mask) | 0x64006400u, 0x64006400u);
-      }
       float g[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(g, o[0][0], o[1][0], o[0][1], o[1][1], q.f[2 * i][0], q.f[2 * i][1]);
-      mma_f16(g, o[0][2], o[1][2], o[0][3], o[1][3], q.f[2 * i + 1][0], q.f[2 * i + 1][1]);
+      mma<BF>(g, a[2 * i], q.f[2 * i]);
+      mma<BF>(g, a[2 * i + 1], q.f[2 * i + 1]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&sz[x][i]));
+        const uint32_t sz = lds4(meta + (((lane >> 2) + 8 * x) * (D / 32) + i) * 4);
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&sz));
 #pragma unroll
         for (int k = 0; k < 2; ++k) d[2 * x + k] = fmaf(y.x, g[2 * x + k], fmaf(y.y, q.sum[i][k], d[2 * x + k]));
       }
@@ -252,12 +281,127 @@ __device__ __forceinline__ void scores(const uint8_t* src, const uint8_t* meta, 
   }
 }
 
-// BF: the queries' (and 16-bit pages') type.
-template <int D, bool BF>
-__global__ void __launch_bounds__(32 * kWarps) weights_kernel(const WParams p) {
-  __shared__ __align__(16) float s_sum[kWarps][kBatch * 16];
+// Some chunks of one (sequence, KV head), and its query rows: they are taken in tiles of eight, and
+// for each tile the chunks pass through the ring once (from the L2, behind the first).
+struct Batch {
+  int b, h, c0, n, len;
+  int t0, rows, tiles;                 // first token; its rows by tokens and heads; at least one tile
+};
+
+// Where a chunk lies.
+struct __align__(16) Found {
+  const uint8_t* src;
+  float ks;
+  int codec;                           // -1: nothing to read
+};
+constexpr int kLooked = 2 * kBatch;    // chunks whose places are kept
+
+// Where a warp's range goes on.
+struct Walk {
+  long long left, at;                  // chunks ahead; the next one within its sequence, KV heads one after the other
+  int b;
+};
+
+// The next batch, its chunks looked up into the places from `to` on, a lane each.
+template <int D, bool ANY>
+__device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* found, const uint8_t** metas, uint32_t to, int lane) {
+  Batch x;
+  x.b = x.h = x.c0 = x.n = x.len = x.t0 = x.rows = x.tiles = 0;
+  if (w.left <= 0) return x;
+  int per;
+  for (;;) {                           // there is a chunk ahead: the loop ends at its sequence
+    x.len = length(p, w.b);
+    per = (x.len + 15) / 16;
+    if (w.at < (long long)per * p.Hkv) break;
+    w.at = 0;
+    ++w.b;
+  }
+  x.b = w.b;
+  x.h = (int)(w.at / per);
+  x.c0 = (int)(w.at - (long long)x.h * per);
+  x.n = (int)min(w.left, (long long)min(kBatch, per - x.c0));
+  w.left -= x.n;
+  w.at += x.n;
+  {
+    const int t0 = min(max(p.q_start[x.b], 0), p.total_q), t1 = min(max(p.q_start[x.b + 1], 0), p.total_q);
+    x.t0 = t0;
+    x.rows = max(t1 - t0, 0) * p.G;    // fewer than 2^31
+    x.tiles = max((x.rows + 7) / 8, 1);
+  }
+  if (lane < x.n) {
+    Found f = {nullptr, 1.f, -1};
+    const uint8_t* meta = nullptr;
+    const int key = (x.c0 + lane) * 16, page = (int)((uint32_t)key / (uint32_t)p.P), row = key - page * p.P;
+    const size_t e = (size_t)x.b * p.max_pages + page;
+    const int k = p.page_codec[e];
+    const long long slot = p.block_table[e];
+    const PoolRef r = p.pool[k <= ARGUS_INT1_G32 ? k : 0];
+    if (k > ARGUS_INT1_G32 || slot < 0 || slot >= r.n_slots) {
+      if (x.h == 0 && row == 0 && p.status) atomicAdd(p.status, 1u);
+    } else {
+      f.codec = k;
+      const long long unit = slot * 2 * p.Hkv + x.h, token = unit * p.P + row;
+      f.src = r.codes + token * (!ANY ? D : k <= ARGUS_BF16 ? 2 * D : k <= ARGUS_INT8 ? D : D >> (k - ARGUS_INT8));
+      if (ANY && k >= ARGUS_INT4_G32) meta = r.meta + token * (D / 32) * 4;
+      else if (k >= ARGUS_FP8_E4M3) f.ks = __ldg(reinterpret_cast<const float*>(r.meta) + unit);
+    }
+    found[(to + lane) % kLooked] = f;
+    if (ANY) metas[(to + lane) % kLooked] = meta;
+  }
+  __syncwarp();
+  return x;
+}
+
+// Query row `mine` of a batch: its address (nullptr: there is none), log-sum and last visible key.
+template <int D>
+__device__ __forceinline__ const uint16_t* row_of(const WParams& p, const Batch& x, int mine, float& L, int& last) {
+  const bool real = mine < x.rows;
+  const int tok = real ? mine / p.G : 0, g = real ? mine - tok * p.G : 0;
+  L = INFINITY;                        // a row that sees nothing gives nothing
+  if (real) {
+    L = __ldg(p.lse2 + (size_t)(x.t0 + tok) * p.Hq + x.h * p.G + g);
+    if (L == -INFINITY) L = INFINITY;
+  }
+  last = !real ? -1 : p.causal ? min(x.len - x.rows / p.G + tok, x.len - 1) : x.len - 1;
+  return real ? p.q + (x.t0 + tok) * p.qs + (long long)(x.h * p.G + g) * D : nullptr;
+}
+// ... and of a lane's two columns
+struct Columns {
+  float lse[2];
+  int see[2];
+};
+__device__ __forceinline__ Columns columns(float L, int last, int lane) {
+  Columns x;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    x.lse[i] = __shfl_sync(0xffffffffu, L, 8 * (lane & 3) + 4 * i);
+    x.see[i] = __shfl_sync(0xffffffffu, last, 8 * (lane & 3) + 4 * i);
+  }
+  return x;
+}
+// Weights of the scores d, summed per key over the lane's columns: x key lane / 4, y eight further down.
+// Selected, not multiplied: rows behind the end may hold anything.
+__device__ __forceinline__ float2 weigh(const float (&d)[4], float f0, float f1, const Columns& x, int key) {
+  float2 s;
+  s.x = (key <= x.see[0] ? fast_exp2(fmaf(d[0], f0, -x.lse[0])) : 0.f) + (key <= x.see[1] ? fast_exp2(fmaf(d[1], f1, -x.lse[1])) : 0.f);
+  s.y = (key + 8 <= x.see[0] ? fast_exp2(fmaf(d[2], f0, -x.lse[0])) : 0.f) + (key + 8 <= x.see[1] ? fast_exp2(fmaf(d[3], f1, -x.lse[1])) : 0.f);
+  return s;
+}
+
+// BF: the queries' (and 16-bit pages') type.  ANY: pages of every codec, else of 8 bits alone, which need
+// fewer registers.  slot: bytes of a ring slot, n_slots of them per warp.
+template <int D, bool BF, bool ANY>
+__global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) weights_kernel(const WParams p, int slot, int n_slots) {
+  constexpr int kWarps = Shape<ANY>::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Found s_found[kWarps][kLooked];
+  __shared__ const uint8_t* s_meta[ANY ? kWarps : 1][kLooked];
+  __shared__ uint64_t s_full[kWarps][kMaxSlots];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3;
-  float* sums = s_sum[warp];
+  uint64_t* full = s_full[warp];
+  Found* found = s_found[warp];
+  const uint8_t** metas = s_meta[ANY ? warp : 0];
+  uint8_t* ring = smem + (size_t)warp * slot * n_slots;
   // this warp's range of chunks
   const int nw = gridDim.x * kWarps, w = blockIdx.x * kWarps + warp;
   const long long first = lane < p.B ? chunks_of(p, lane) : 0;
@@ -265,10 +409,8 @@ __global__ void __launch_bounds__(32 * kWarps) weights_kernel(const WParams p) {
   for (int x = lane + 32; x < p.B; x += 32) total += chunks_of(p, x);
   total = warp_sum(total);
   const long long u0 = total / nw * w + total % nw * w / nw, u1 = total / nw * (w + 1) + total % nw * (w + 1) / nw;
-  long long left = u1 - u0;
-  if (left <= 0) return;
-  int b = 0;
-  long long at = 0;                                      // the chunk of sequence b, its KV heads one after the other
+  Walk walk = {u1 - u0, 0, 0};
+  if (walk.left <= 0) return;
   {
     long long before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -276,121 +418,162 @@ __global__ void __launch_bounds__(32 * kWarps) weights_kernel(const WParams p) {
       const unsigned hit = __ballot_sync(0xffffffffu, before + incl > u0);
       if (hit) {
         const int src = __ffs(hit) - 1;
-        b = b0 + src;
-        at = u0 - before - __shfl_sync(0xffffffffu, incl - mine, src);
+        walk.b = b0 + src;
+        walk.at = u0 - before - __shfl_sync(0xffffffffu, incl - mine, src);
         break;
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
+  if (lane < n_slots) mbar_init(&full[lane], 1);
+  fence_mbar_init();
+  __syncwarp();
+  Batch cur = next_batch<D, ANY>(p, walk, found, metas, 0, lane), ahead = next_batch<D, ANY>(p, walk, found, metas, cur.n, lane);
+  uint32_t base = 0;                                     // place of cur's first chunk
+  // the next copies: chunks feed_i and feed_i + 1 for tile feed_t of cur (feed = 0) or ahead (1); 2: all issued
+  int feed = 0, feed_t = 0, feed_i = 0;
+  int put = 0, take = 0, flying = 0;                     // next slot to fill and to read, pairs on their way
+  uint32_t phase = 0;                                    // of the slots
+  auto issue = [&]() {                                   // copies, as far as there are slots
+    while (flying < n_slots && feed < 2) {
+      const int n = feed ? ahead.n : cur.n, tiles = feed ? ahead.tiles : cur.tiles;
+      if (feed_i >= n) {
+        feed_i = 0;
+        if (++feed_t >= tiles) {                         // (no chunks: no tiles)
+          feed_t = 0;
+          ++feed;
+        }
+        continue;
+      }
+      // a lane per chunk; a chunk that is not read adds no bytes
+      uint32_t bytes = 0, more = 0;
+      const uint32_t from = (base + (feed ? cur.n : 0) + feed_i + (lane & 1)) % kLooked;
+      if (feed_i + (lane & 1) < n) {
+        const int k = found[from].codec;
+        if (k >= 0) bytes = ANY ? 16 * (k <= ARGUS_BF16 ? 2 * D : k <= ARGUS_INT8 ? D : D >> (k - ARGUS_INT8)) : 16 * D;
+        if (ANY && k > ARGUS_INT8) more = 16 * (D / 32) * 4;
+      }
+      const uint32_t both = bytes + more + __shfl_xor_sync(0xffffffffu, bytes + more, 1);
+      if (lane == 0) mbar_arrive_expect_tx(&full[put], both);
+      __syncwarp();
+      if (lane < 2 && bytes) {
+        uint8_t* to = ring + put * slot + lane * (slot / 2);
+        bulk_g2s(to, found[from].src, bytes, &full[put]);
+        if (ANY && more) bulk_g2s(to + 8 * D, metas[from], more, &full[put]);   // behind the codes: at most D / 2 bytes a row
+      }
+      feed_i += 2;
+      ++flying;
+      if (++put == n_slots) put = 0;
+    }
+  };
+  bool ok = true;
   Query<D> q;
-  int have_b = -1, have_h = -1, have_t = -1, have_form = kNone;   // what q holds
-  float lse[2] = {0.f, 0.f};
-  int see[2] = {0, 0};                                   // the columns' last visible key
-  while (left > 0) {
-    const int len = length(p, b), per = (len + 15) / 16;
-    if (at >= (long long)per * p.Hkv) {                  // the next sequence that has any
-      at = 0;
-      ++b;
-      continue;
-    }
-    const int h = (int)(at / per), c0 = (int)(at - (long long)h * per);
-    const int n = (int)min(left, (long long)min(kBatch, per - c0));
-    left -= n;
-    at += n;
-    // a chunk per lane
-    const uint8_t *src = nullptr, *meta = nullptr;
-    int codec = -1;
-    float ks = 1.f;
-    if (lane < n) {
-      const int key = (c0 + lane) * 16, page = (int)((uint32_t)key / (uint32_t)p.P), row = key - page * p.P;
-      const size_t e = (size_t)b * p.max_pages + page;
-      const int k = p.page_codec[e];
-      const long long slot = p.block_table[e];
-      const PoolRef r = p.pool[k <= ARGUS_INT1_G32 ? k : 0];
-      if (k > ARGUS_INT1_G32 || slot < 0 || slot >= r.n_slots) {
-        if (h == 0 && row == 0 && p.status) atomicAdd(p.status, 1u);
-      } else {
-        codec = k;
-        const long long unit = slot * 2 * p.Hkv + h, token = unit * p.P + row;
-        const int bytes = k <= ARGUS_BF16 ? 2 * D : k <= ARGUS_INT8 ? D : D >> (k - ARGUS_INT8);
-        src = r.codes + token * bytes;
-        if (k >= ARGUS_INT4_G32) meta = r.meta + token * (D / 32) * 4;
-        else if (k >= ARGUS_FP8_E4M3) ks = __ldg(reinterpret_cast<const float*>(r.meta) + unit);
+  Columns col = {};
+  int have_b = -1, have_h = -1, have_t = -1, have_form = kNone;   // whose rows q and col hold
+  while (cur.n > 0 && ok) {
+    // the lane's position in a pair of chunks: neighbouring lanes have neighbouring keys' sums
+    const int mine = (c >> 1) * 16 + (c & 1) * 8 + (lane >> 2);
+    float* out = p.weights + ((size_t)cur.b * p.Hkv + cur.h) * p.row_len;
+    for (int t = 0; t < cur.tiles && ok; ++t) {
+      for (int i = 0; i < cur.n; i += 2) {
+        issue();
+        const int pos = (cur.c0 + i) * 16 + mine;
+        const bool writes = pos < cur.len && i + (c >> 1) < cur.n;
+        // by t > 0 the sum so far, which this lane wrote
+        const float old = writes && (t > 0 || p.decay != 0.f) ? out[pos] : 0.f;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[take], phase >> take & 1));
+        if (!ok) break;
+        float2 s[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          s[j] = make_float2(0.f, 0.f);
+          const Found at = found[(base + i + j) % kLooked];
+          const int k = i + j < cur.n ? at.codec : -1;
+          if (k < 0) continue;
+          const int form = ANY ? form_of(k) : (int)k8;
+          const uint32_t src = smem_u32(ring + take * slot + j * (slot / 2));
+          if (have_form != form || have_t != t || have_h != cur.h || have_b != cur.b) {
+            have_form = form;
+            have_t = t;
+            have_h = cur.h;
+            have_b = cur.b;
+            float L;
+            int last;
+            const uint16_t* row = row_of<D>(p, cur, 8 * t + (lane >> 2), L, last);
+            load_query<D, BF, BF>(row, row != nullptr, form, lane, q);
+            col = columns(L, last, lane);
+          }
+          uint32_t a[D / 16][4];
+          float d[4];
+          if (ANY && BF && form == k16) {
+            load_keys<D, BF, ANY>(src, k, lane, a);
+            scores<D, BF>(a, q, form, src + 8 * D, lane, d);
+          } else {
+            load_keys<D, false, ANY>(src, k, lane, a);
+            scores<D, false>(a, q, form, src + 8 * D, lane, d);
+          }
+          const float f = at.ks * p.scale_log2;
+          s[j] = weigh(d, f * q.fac[0], f * q.fac[1], col, (cur.c0 + i + j) * 16 + (lane >> 2));
+        }
+        __syncwarp();                                    // the chunks have been read
+        phase ^= 1u << take;
+        --flying;
+        if (++take == n_slots) take = 0;
+        // sums over the four lanes of a row, one of the four values each
+        const bool odd = c & 1, high = c & 2;
+        const float u = (odd ? s[0].y : s[0].x) + __shfl_xor_sync(0xffffffffu, odd ? s[0].x : s[0].y, 1);
+        const float v = (odd ? s[1].y : s[1].x) + __shfl_xor_sync(0xffffffffu, odd ? s[1].x : s[1].y, 1);
+        const float x = (high ? v : u) + __shfl_xor_sync(0xffffffffu, high ? u : v, 2);
+        if (writes) out[pos] = fmaf(t > 0 ? 1.f : p.decay, old, x);
       }
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kBatch * 16 / 128; ++i) reinterpret_cast<float4*>(sums)[i * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
-    __syncwarp();
-    const int t0 = min(max(p.q_start[b], 0), p.total_q), t1 = min(max(p.q_start[b + 1], 0), p.total_q), nq = max(t1 - t0, 0);
-    const long long rows = (long long)nq * p.G;
-    for (int t = 0; (long long)t * 8 < rows; ++t) {
-      for (int i = 0; i < n; ++i) {
-        const int k = __shfl_sync(0xffffffffu, codec, i);
-        if (k < 0) continue;
-        const int form = form_of(k);
-        if (have_form != form || have_t != t || have_h != h || have_b != b) {
-          have_form = form;
-          have_t = t;
-          have_h = h;
-          have_b = b;
-          const long long mine = (long long)t * 8 + (lane >> 2);
-          const bool real = mine < rows;
-          const int tok = real ? (int)(mine / p.G) : 0, g = real ? (int)(mine - (long long)tok * p.G) : 0;
-          load_query<D, BF>(p.q + (t0 + tok) * p.qs + (long long)(h * p.G + g) * D, real, form, lane, q);
-          float L = INFINITY;                            // a row that sees nothing gives nothing
-          if (real) {
-            L = p.lse2[(size_t)(t0 + tok) * p.Hq + h * p.G + g];
-            if (L == -INFINITY) L = INFINITY;
-          }
-          const int last = !real ? -1 : p.causal ? min(len - nq + tok, len - 1) : len - 1;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            lse[x] = __shfl_sync(0xffffffffu, L, 8 * c + 4 * x);
-            see[x] = __shfl_sync(0xffffffffu, last, 8 * c + 4 * x);
-          }
-        }
-        const unsigned long long a = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i);
-        const unsigned long long m = form == kGroup ? __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(meta), i) : 0ull;
-        const float f = __shfl_sync(0xffffffffu, ks, i) * p.scale_log2;
-        float d[4];
-        scores<D, BF>(reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(m), k, lane, q, d);
-        const int key = (c0 + i) * 16 + (lane >> 2);
-        float s[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {                    // selected, not multiplied: rows behind the end may hold anything
-          const float p0 = key + 8 * x <= see[0] ? fast_exp2(fmaf(d[2 * x], f * q.fac[0], -lse[0])) : 0.f;
-          const float p1 = key + 8 * x <= see[1] ? fast_exp2(fmaf(d[2 * x + 1], f * q.fac[1], -lse[1])) : 0.f;
-          s[x] = p0 + p1;
-          s[x] += __shfl_xor_sync(0xffffffffu, s[x], 1);
-          s[x] += __shfl_xor_sync(0xffffffffu, s[x], 2);
-        }
-        if (c < 2) sums[i * 16 + (lane >> 2) + 8 * c] += c ? s[1] : s[0];
-      }
-    }
-    __syncwarp();
-    float* out = p.weights + ((size_t)b * p.Hkv + h) * p.row_len + (size_t)c0 * 16;
-    const int keys = min(len - c0 * 16, n * 16);
-    for (int i = lane; i < keys; i += 32) {
-      float x = sums[i];
-      if (p.decay != 0.f) x = fmaf(p.decay, out[i], x);
-      out[i] = x;
+    if (!ok) break;
+    issue();                                             // what there is room for: steps behind cur in any case
+    base += cur.n;
+    --feed;                                              // all of cur was issued
+    cur = ahead;
+    ahead = next_batch<D, ANY>(p, walk, found, metas, base + cur.n, lane);
+  }
+  if (!ok) {
+    // a copy did not arrive: the caller is told, and the ones in flight get as long again
+    if (lane == 0 && p.status) atomicOr(p.status, kStatusTimeoutBit);
+    for (; flying > 0; --flying) {
+      mbar_wait(&full[take], phase >> take & 1);
+      if (++take == n_slots) take = 0;
     }
   }
 }
 
-template <int D, bool BF>
+template <int D, bool BF, bool ANY>
 static argus_status launch(const WParams& p, cudaStream_t s) {
+  using S = Shape<ANY>;
+  // a slot holds two chunks, 16 rows each, of the widest pages
+  const bool wide = p.pool[ARGUS_FP16].n_slots > 0 || p.pool[ARGUS_BF16].n_slots > 0;
+  const int slot = wide ? 64 * D : 32 * D, n_slots = std::min(kMaxSlots, S::kRing / slot);
+  static PerContext configured;
+  const argus_status st = configured.ensure([](int) {
+    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<D, BF, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kWarps * S::kRing);
+    return e == cudaSuccess ? ARGUS_OK : fail(ARGUS_E_LAUNCH, "weights: smem attribute: %s", cudaGetErrorString(e));
+  });
+  if (st != ARGUS_OK) return st;
   const long long chunks = (long long)p.B * p.Hkv * (((long long)p.max_pages * p.P + 15) / 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::max(1ll, std::min(chunks, device_sm_count() * 3ll)));
-  cfg.blockDim = dim3(32 * kWarps);
+  cfg.gridDim = dim3((unsigned)std::max(1ll, std::min(chunks, device_sm_count() * (long long)S::kBlocks)));
+  cfg.blockDim = dim3(32 * S::kWarps);
+  cfg.dynamicSmemBytes = S::kWarps * slot * n_slots;
   cfg.stream = s;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, weights_kernel<D, BF>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weights_kernel<D, BF, ANY>, p, slot, n_slots);
   if (e == cudaSuccess) return ARGUS_OK;
   cudaGetLastError();                  // not left for the next call to find
   return fail(ARGUS_E_LAUNCH, "argus_attn_weights: launch failed: %s", cudaGetErrorString(e));
+}
+
+template <int D>
+static argus_status launch_d(const WParams& p, bool bf, cudaStream_t s) {
+  bool any = false;
+  for (int k = 0; k < 7; ++k) any |= k != ARGUS_FP8_E4M3 && k != ARGUS_INT8 && p.pool[k].n_slots > 0;
+  if (bf) return any ? launch<D, true, true>(p, s) : launch<D, true, false>(p, s);
+  return any ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
 }
 
 }  // namespace weights
@@ -434,8 +617,8 @@ extern "C" argus_status argus_attn_weights(const argus_extend_args* a, float* we
     if (pl.n_slots > 0 && (!pl.codes || (pl.codec >= ARGUS_FP8_E4M3 && !pl.meta)))
       return fail(ARGUS_E_INVALID, "weights: NULL codes or meta (codec %d)", pl.codec);
     if (reinterpret_cast<uintptr_t>(pl.codes) & 15) return fail(ARGUS_E_INVALID, "weights: codes must be 16-byte aligned");
-    if (pl.codec >= ARGUS_FP8_E4M3 && (reinterpret_cast<uintptr_t>(pl.meta) & 3))
-      return fail(ARGUS_E_INVALID, "weights: meta must be 4-byte aligned");
+    if (pl.codec >= ARGUS_FP8_E4M3 && (reinterpret_cast<uintptr_t>(pl.meta) & (pl.codec >= ARGUS_INT4_G32 ? 15 : 3)))
+      return fail(ARGUS_E_INVALID, "weights: meta must be 4-byte aligned, of group codes 16-byte aligned");
     p.pool[pl.codec] = {static_cast<const uint8_t*>(pl.codes), static_cast<const uint8_t*>(pl.meta), pl.n_slots};
   }
   if (a->batch == 0 || positions == 0) return ARGUS_OK;
@@ -479,6 +662,5 @@ extern "C" argus_status argus_attn_weights(const argus_extend_args* a, float* we
   p.status = a->status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = a->q_dtype == ARGUS_BF16;
-  if (D == 64) return bf ? weights::launch<64, true>(p, s) : weights::launch<64, false>(p, s);
-  return bf ? weights::launch<128, true>(p, s) : weights::launch<128, false>(p, s);
+  return D == 64 ? weights::launch_d<64>(p, bf, s) : weights::launch_d<128>(p, bf, s);
 }
