@@ -18,8 +18,10 @@ __device__ __forceinline__ uint32_t bf2_sub(uint32_t a, uint32_t b) {
 template <bool BF>
 __device__ __forceinline__ void fp8_to_16(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (!BF) {
-    lo = e4m3x2_to_f16x2(w);
-    hi = e4m3x2_to_f16x2(w >> 16);
+    // the word's halves as they are: masks and shifts would be half of the instructions
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
   } else {
     // sign to the top, exponent and fraction to the low exponent bits and the
     // top fraction bits: the value times 2^-120 (e4m3's bias is 7, bf16's 127;
@@ -43,6 +45,15 @@ __device__ __forceinline__ void int8_to_16(uint32_t w, uint32_t& lo, uint32_t& h
     lo = bf2_sub(a & 0xFF7FFF7Fu, a & 0xFF80FF80u);
     hi = bf2_sub(b & 0xFF7FFF7Fu, b & 0xFF80FF80u);
   }
+}
+
+// Four values to e4m3 codes, to nearest even, saturating; a's in the low byte.
+__device__ __forceinline__ uint32_t f32x4_to_e4m3(float a, float b, float c, float d) {
+  uint32_t o;
+  asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+      : "=r"(o)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return o;
 }
 
 }  // namespace argus

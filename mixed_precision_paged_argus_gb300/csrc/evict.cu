@@ -5,7 +5,8 @@
 // of those between the k = budget - S - R of largest weight, ties to the lower position.
 // Floats are mapped to integers of the same order (NaN below all, -0 = +0); the k-th largest
 // key T is found bit by bit, two at a time: with c_d keys at or above each of the three next
-// digits, the largest d with c_d >= k is T's.  Where a count is k exactly, the search ends.
+// digits, the largest d with c_d >= k is T's.  Where a count is k exactly, the search ends; where few
+// keys share T's bits so far, the rest of it looks at these alone.
 // Positions above T stay, and of those at T the first k - #(above T).
 //
 // Selection: a thread block (or a cluster of them for long rows) per sequence and KV head holds
@@ -21,6 +22,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "codes.cuh"
 #include "common.cuh"
 
 namespace argus {
@@ -36,6 +38,7 @@ struct PoolRef {
 
 struct VParams {
   int Hkv, P, B, max_pages, budget, sinks, recent, dst_codec, dst_pages;
+  uint32_t p_mul, p_shift;             // division by P (page_of)
   PoolRef pool[7];
   const uint8_t* page_codec;
   const int32_t *block_table, *seq_lens;
@@ -51,6 +54,10 @@ struct VParams {
   uint32_t* status;
 };
 
+// x / P for 0 <= x < 2^31.  With s = ceil(log2 P) and mul = ceil(2^(31 + s) / P), x mul is above
+// x 2^(31 + s) / P by less than 2^(31 + s) / P: the quotient's whole part is the same.
+__device__ __forceinline__ int page_of(const VParams& p, int x) { return (int)(__umulhi((uint32_t)x, p.p_mul) >> p.p_shift); }
+
 __device__ __forceinline__ int length(const VParams& p, int b) {
   return (int)min((long long)max(p.seq_lens[b], 0), (long long)p.max_pages * p.P);
 }
@@ -59,6 +66,7 @@ __device__ __forceinline__ int length(const VParams& p, int b) {
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kRegKeys = 32;           // keys per thread that stay in registers, at most
 constexpr int kMaxCluster = 8;
+constexpr int kList = 4 * kSelThreads; // keys that share T's first bits, from which on the others are left alone
 
 __device__ __forceinline__ uint32_t order(float w) {
   const uint32_t u = __float_as_uint(w);
@@ -82,6 +90,7 @@ template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p) {
   __shared__ Counts s_warp[2][kSelWarps];
   __shared__ Counts s_block[2];
+  __shared__ uint32_t s_list[kList], s_listed;
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = gridDim.x, rank = blockIdx.x;          // the cluster spans the grid's first dimension
   const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -155,23 +164,54 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
   };
   uint32_t T = 0xFFFFFFFFu, ties = 0;                  // keys above T stay, and the first `ties` at T
   if (k > 0) {
-    uint32_t prefix = 0, upper = 0;                    // keys at or above the prefix's successor
+    uint32_t prefix = 0, upper = 0, at = 0xFFFFFFFFu;  // T's bits so far; keys at or above the prefix's successor, and the prefix
+    int s = 32;                                        // bits still open
+    // two more bits from the counts of keys at or above the three next prefixes; true: the search is over
+    auto narrow = [&](Counts c) {
+      if (c.c >= (uint32_t)k) { prefix |= 3u << s; at = c.c; }
+      else if (c.b >= (uint32_t)k) { prefix |= 2u << s; upper = c.c; at = c.b; }
+      else if (c.a >= (uint32_t)k) { prefix |= 1u << s; upper = c.b; at = c.a; }
+      else { upper = c.a; }
+      return at == (uint32_t)k;
+    };
+    auto count = [&](Counts& c, uint32_t x) {
+      c.a += x >= (prefix | 1u << s);
+      c.b += x >= (prefix | 2u << s);
+      c.c += x >= (prefix | 3u << s);
+    };
     bool exact = false;
-    for (int s = 30; s >= 0; s -= 2) {
-      const uint32_t t1 = prefix | (1u << s), t2 = prefix | (2u << s), t3 = prefix | (3u << s);
+    while (s > 0 && !exact && at - upper > (uint32_t)kList) {
+      s -= 2;
       Counts c = {0, 0, 0};
+      each([&](int, uint32_t x) { count(c, x); });
+      exact = narrow(total(warp_sum(c), nullptr));
+    }
+    if (s > 0 && !exact) {
+      // the few keys that share the prefix, in any order: the other rounds look at these
+      if (threadIdx.x == 0) s_listed = 0;
+      __syncthreads();
       each([&](int, uint32_t x) {
-        c.a += x >= t1;
-        c.b += x >= t2;
-        c.c += x >= t3;
+        const bool in = x >> s == prefix >> s && x != 0;   // 0: never counted
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        if (!m) return;
+        uint32_t to = 0;
+        if (lane == 0) to = atomicAdd(&s_listed, __popc(m));
+        to = __shfl_sync(0xffffffffu, to, 0) + __popc(m & ((1u << lane) - 1));
+        if (in) s_list[to] = x;
       });
-      c = total(warp_sum(c), nullptr);
-      uint32_t at;                                     // keys at or above the new prefix
-      if (c.c >= (uint32_t)k) { prefix = t3; at = c.c; }
-      else if (c.b >= (uint32_t)k) { prefix = t2; upper = c.c; at = c.b; }
-      else if (c.a >= (uint32_t)k) { prefix = t1; upper = c.b; at = c.a; }
-      else { upper = c.a; at = 0; }                    // the count at the old prefix: not k, or the search had ended
-      if (at == (uint32_t)k) { exact = true; break; }
+      __syncthreads();
+      uint32_t mine[kList / kSelThreads];
+#pragma unroll
+      for (int i = 0; i < kList / kSelThreads; ++i) mine[i] = i * kSelThreads + threadIdx.x < s_listed ? s_list[i * kSelThreads + threadIdx.x] : 0u;
+      const uint32_t above = upper;
+      while (s > 0 && !exact) {
+        s -= 2;
+        Counts c = {0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kList / kSelThreads; ++i) count(c, mine[i]);
+        c = total(warp_sum(c), nullptr);
+        exact = narrow({c.a + above, c.b + above, c.c + above});
+      }
     }
     T = prefix;
     ties = exact ? 0xFFFFFFFFu : (uint32_t)k - upper;
@@ -211,185 +251,175 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
 // ---------------------------------------------------------------- gathering
 constexpr int kWarps = 8;
 
-// 16 values of a row, as they lie in the page; in a 16-bit page 32 bytes, else 16 at most and
-// the scale (and zero).
-template <bool WIDE>
-struct Raw {
-  uint4 a;
-  uint4 b;
-};
-template <>
-struct Raw<false> {
-  uint4 a;
-  uint32_t s;
-};
-
-template <bool BF>
-__device__ __forceinline__ float2 two(uint32_t w) {
-  if (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  return __half22float2(*reinterpret_cast<__half2*>(&w));
-}
-
-// Where a kept row lies: its unit (slot, K | V, KV head), the row in it, its codec (-1: nowhere).
+// Where a kept row lies: its K row's first value, in values from the pool's first one; its codec (-1:
+// nowhere); the scale of its unit (8-bit codecs).
 struct Place {
-  long long unit;
-  int row, codec;
+  long long at;
+  int codec;
+  float scale;
 };
 
-template <int D, bool WIDE>
-__device__ __forceinline__ Raw<WIDE> fetch(const VParams& p, const Place& s, int kv, int v) {
-  Raw<WIDE> r = {};
-  uint32_t scale = 0;
-  if (s.codec < 0) return r;
-  const long long at = ((s.unit + (kv ? p.Hkv : 0)) * p.P + s.row) * D + 16 * v;   // in values
-  const uint8_t* c = p.pool[s.codec].codes;
-  if constexpr (WIDE) {
-    if (s.codec <= ARGUS_BF16) {
-      r.a = __ldg(reinterpret_cast<const uint4*>(c + 2 * at));
-      r.b = __ldg(reinterpret_cast<const uint4*>(c + 2 * at) + 1);
-      return r;
-    }
-  }
-  if (s.codec <= ARGUS_INT8) {
-    r.a = __ldg(reinterpret_cast<const uint4*>(c + at));
-    scale = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + s.unit + (kv ? p.Hkv : 0));
-  } else {
-    if (s.codec == ARGUS_INT4_G32) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(c + at / 2));
-      r.a.x = x.x;
-      r.a.y = x.y;
-    } else if (s.codec == ARGUS_INT2_G32) {
-      r.a.x = __ldg(reinterpret_cast<const uint32_t*>(c + at / 4));
-    } else {
-      r.a.x = __ldg(reinterpret_cast<const uint16_t*>(c + at / 8));
-    }
-    scale = __ldg(reinterpret_cast<const uint32_t*>(p.pool[s.codec].meta) + at / 32);   // scale, zero
-  }
-  if constexpr (WIDE) r.b.x = scale;
-  else r.s = scale;
-  return r;
-}
-
-template <bool WIDE>
-__device__ __forceinline__ void values(const Raw<WIDE>& r, int codec, float (&x)[16]) {
-  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-  uint32_t scale;
-  if constexpr (WIDE) {
-    scale = r.b.x;
-    if (codec == ARGUS_FP16 || codec == ARGUS_BF16) {
-      const uint32_t u[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+// ---- rows of any codec: sixteen values at a time
+__device__ __forceinline__ void values(const VParams& p, const Place& s, long long at, float (&x)[16]) {
+  const PoolRef& pool = p.pool[max(s.codec, 0)];
+  if (s.codec < 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 y = codec == ARGUS_BF16 ? two<true>(u[i]) : two<false>(u[i]);
-        x[2 * i] = y.x;
-        x[2 * i + 1] = y.y;
-      }
-      return;
-    }
-  } else {
-    scale = r.s;
-  }
-  if (codec == ARGUS_FP8_E4M3) {
-    const float s = __uint_as_float(scale);
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+  } else if (s.codec <= ARGUS_BF16) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(pool.codes + 2 * at)), b = __ldg(reinterpret_cast<const uint4*>(pool.codes + 2 * at) + 1);
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 y = two<false>(e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1))));
-      f2_mul(x[2 * i], x[2 * i + 1], y.x, y.y, s, s);
+      const float2 y = s.codec == ARGUS_BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
+                                             : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = y.x;
+      x[2 * i + 1] = y.y;
     }
-  } else if (codec == ARGUS_INT8) {
-    const float s = __uint_as_float(scale);
+  } else if (s.codec <= ARGUS_INT8) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(pool.codes + at));
+    const float f = s.scale;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = (float)(int8_t)(w[i / 4] >> (8 * (i & 3))) * s;
-  } else if (codec > 0) {
-    const float2 sz = two<false>(scale);
-    const int bits = codec == ARGUS_INT4_G32 ? 4 : codec == ARGUS_INT2_G32 ? 2 : 1;
+    for (int i = 0; i < 4; ++i) {
+      uint32_t h[2];
+      if (s.codec == ARGUS_FP8_E4M3) fp8_to_16<false>(w[i], h[0], h[1]);
+      else int8_to_16<false>(w[i], h[0], h[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        x[4 * i + 2 * j] = y.x * f;
+        x[4 * i + 2 * j + 1] = y.y * f;
+      }
+    }
+  } else {
+    uint32_t w[2] = {0, 0};
+    if (s.codec == ARGUS_INT4_G32) {
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(pool.codes + at / 2));
+      w[0] = y.x;
+      w[1] = y.y;
+    } else if (s.codec == ARGUS_INT2_G32) {
+      w[0] = __ldg(reinterpret_cast<const uint32_t*>(pool.codes + at / 4));
+    } else {
+      w[0] = __ldg(reinterpret_cast<const uint16_t*>(pool.codes + at / 8));
+    }
+    const uint32_t m = __ldg(reinterpret_cast<const uint32_t*>(pool.meta) + at / 32);   // scale, zero
+    const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    const int bits = s.codec == ARGUS_INT4_G32 ? 4 : s.codec == ARGUS_INT2_G32 ? 2 : 1;
     const unsigned long long q = (unsigned long long)w[1] << 32 | w[0];
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = fmaf((float)((uint32_t)(q >> (bits * i)) & ((1u << bits) - 1)), sz.x, sz.y);   // the product is exact
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
   }
 }
 
-// The largest magnitude of 16 values.  Of an e4m3 row it is the largest code's: a product with
-// the same scale keeps the order.
-template <bool WIDE>
-__device__ __forceinline__ float largest(const Raw<WIDE>& r, int codec) {
-  float top = 0.f;
-  if (codec == ARGUS_FP8_E4M3) {
-    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
-    __half2 m = __float2half2_rn(0.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t y = e4m3x2_to_f16x2(w[i / 2] >> (16 * (i & 1)));
-      m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&y)));
-    }
-    uint32_t scale;
-    if constexpr (WIDE) scale = r.b.x;
-    else scale = r.s;
-    top = fabsf(fmaxf(__low2float(m), __high2float(m)) * __uint_as_float(scale));
-  } else {
-    float x[16];
-    values(r, codec, x);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
-  }
-  return top;
-}
-
-// Four codes of y = RN(x / scale).  x times the reciprocal is off by at most 3 2^-24 of y, so
-// y lies between x rcp (1 - 2^-21) and x rcp (1 + 2^-21); both codes are formed, and as
-// encoding keeps the order, y's is theirs where they agree.
+// ---- codes of RN(x / scale).  With y = RN(1 / scale) the quotient is q + r y, rounded once, for q = RN(x y)
+// and r = x - q scale, which an FMA gives exactly (P. Markstein, IBM J. Res. Dev. 34, 1990): where it is
+// next to a border between codes, a number of few bits, the quotient is no closer to the middle between
+// two floats than 2^-24 of their distance over scale's mantissa, and r y is off by less.
 template <int DST>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-  if (DST == ARGUS_FP8_E4M3) return f32x2_to_e4m3x2(a, b) | f32x2_to_e4m3x2(c, d) << 16;
-  const float x[4] = {a, b, c, d};
-  uint32_t o = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o |= ((uint32_t)(int)fminf(fmaxf(rintf(x[j]), -127.f), 127.f) & 0xFFu) << (8 * j);
-  return o;
+  if (DST == ARGUS_FP8_E4M3) return f32x4_to_e4m3(a, b, c, d);
+  // |y| <= 127: the adder's low bits are the rounded integer
+  constexpr float kRound = 12582912.f;
+  f2_add(a, b, a, b, kRound, kRound);
+  f2_add(c, d, c, d, kRound, kRound);
+  return prmt(prmt(__float_as_uint(a), __float_as_uint(b), 0x0040), prmt(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
 }
+// Sixteen codes of y s / scale; rcp = RN(1 / scale), 0 where the scale is so small or large that a step could leave
+// fp32's range.
 template <int DST>
-__device__ __forceinline__ uint4 encode(const float (&x)[16], float scale) {
-  uint32_t o[4] = {0, 0, 0, 0};
-  if (scale > 0.f) {
-    const float rcp = 1.f / scale, lo = rcp * (1.f - 0x1p-21f), hi = rcp * (1.f + 0x1p-21f);
-    bool same = scale >= 0x1p-120f && scale <= 0x1p120f;   // outside the reciprocal could lose bits
+__device__ __forceinline__ uint4 encode(float (&y)[16], float s, float rcp, float scale) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float a[4], b[4];
-      f2_mul(a[0], a[1], x[4 * e], x[4 * e + 1], lo, lo);
-      f2_mul(a[2], a[3], x[4 * e + 2], x[4 * e + 3], lo, lo);
-      f2_mul(b[0], b[1], x[4 * e], x[4 * e + 1], hi, hi);
-      f2_mul(b[2], b[3], x[4 * e + 2], x[4 * e + 3], hi, hi);
-      o[e] = encode4<DST>(a[0], a[1], a[2], a[3]);
-      same &= o[e] == encode4<DST>(b[0], b[1], b[2], b[3]);
+  for (int e = 0; e < 16; e += 2) f2_mul(y[e], y[e + 1], y[e], y[e + 1], s, s);
+  if (rcp != 0.f) {
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float q[2], r[2];
+      f2_mul(q[0], q[1], y[e], y[e + 1], rcp, rcp);
+      f2_fma(r[0], r[1], q[0], q[1], -scale, -scale, y[e], y[e + 1]);
+      f2_fma(y[e], y[e + 1], r[0], r[1], rcp, rcp, q[0], q[1]);
     }
-    if (!same) {
+  } else {
+#pragma unroll 1
+    for (int e = 0; e < 16; ++e) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] = encode4<DST>(x[4 * e] / scale, x[4 * e + 1] / scale, x[4 * e + 2] / scale, x[4 * e + 3] / scale);
+      for (int j = 0; j < 16; ++j)
+        if (j == e) y[j] = scale > 0.f ? y[j] / scale : 0.f;
     }
   }
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = encode4<DST>(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ bool moderate(float x) { return x >= 0x1p-60f && x <= 0x1p60f; }
+
+// ---- rows of one codec, 16-bit or 8: sixteen values as pairs of fp16 (or bf16) codes
+template <int SRC>
+struct Raw {
+  uint4 a, b;                          // b: the second half of 16-bit rows
+};
+template <int SRC>
+__device__ __forceinline__ Raw<SRC> fetch(const VParams& p, long long at) {   // at < 0: nowhere
+  Raw<SRC> r;
+  r.a = r.b = make_uint4(0, 0, 0, 0);
+  if (at < 0) return r;
+  const uint4* x = reinterpret_cast<const uint4*>(p.pool[SRC].codes + (SRC <= ARGUS_BF16 ? 2 * at : at));
+  r.a = __ldg(x);
+  if (SRC <= ARGUS_BF16) r.b = __ldg(x + 1);
+  return r;
+}
+template <int SRC>
+__device__ __forceinline__ void pairs(const Raw<SRC>& r, uint32_t (&h)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+  if constexpr (SRC <= ARGUS_BF16) {
+    h[0] = r.a.x; h[1] = r.a.y; h[2] = r.a.z; h[3] = r.a.w;
+    h[4] = r.b.x; h[5] = r.b.y; h[6] = r.b.z; h[7] = r.b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (SRC == ARGUS_FP8_E4M3) fp8_to_16<false>(w[i], h[2 * i], h[2 * i + 1]);
+      else int8_to_16<false>(w[i], h[2 * i], h[2 * i + 1]);
+    }
+  }
+}
+template <int SRC>
+__device__ __forceinline__ float2 pair_values(uint32_t h) {
+  if (SRC == ARGUS_BF16) return make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// The largest magnitude of sixteen values: the largest code's, as a product with the same scale keeps the
+// order, and so do the bits of magnitudes.
+template <int SRC>
+__device__ __forceinline__ float largest(const uint32_t (&h)[8], float s) {
+  uint32_t m = h[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(h[i] & 0x7FFF7FFFu));
+  const float2 y = pair_values<SRC>(m);
+  return fabsf(fmaxf(y.x, y.y) * s);
 }
 
 // Rows row0 .. row0 + 15 of KV head h of sequence b's new cache, by a warp: the places, a row per lane
-// (lanes 16 to 31 hold those of 0 to 15).  `first`: their weights are copied, and rows
-// without a place counted.
+// (lanes 16 to 31 hold those of 0 to 15; the scales are K's in lanes 0 to 15, V's in 16 to 31).  `first`: their
+// weights are copied, and rows without a place counted.
+template <int D>
 __device__ __forceinline__ Place find(const VParams& p, int b, int h, int row0, int m, int lane, bool first) {
-  Place s = {0, 0, -1};
+  Place s = {-1, -1, 1.f};
   const int r = row0 + (lane & 15);
   const long long unit = (long long)b * p.Hkv + h;
   bool lost = false;
   if (r < m) {
     const int pos = p.kept[unit * p.budget + r];
-    const int page = (int)((unsigned)pos / (unsigned)p.P);
+    const int page = page_of(p, pos);
     const size_t e = (size_t)b * p.max_pages + page;
     const int codec = p.page_codec[e];
     const long long slot = p.block_table[e];
     lost = codec > ARGUS_INT1_G32 || slot < 0 || slot >= p.pool[codec > ARGUS_INT1_G32 ? 0 : codec].n_slots;
-    if (!lost) s = {slot * 2 * p.Hkv + h, pos - page * p.P, codec};
+    if (!lost) {
+      const long long u = slot * 2 * p.Hkv + h;
+      s.at = (u * p.P + (pos - page * p.P)) * D;
+      s.codec = codec;
+      if (codec == ARGUS_FP8_E4M3 || codec == ARGUS_INT8) s.scale = __ldg(reinterpret_cast<const float*>(p.pool[codec].meta) + u + (lane < 16 ? 0 : p.Hkv));
+    }
     if (first && lane < 16) p.weights_out[unit * p.row_len_out + r] = __ldg(p.weights + unit * p.row_len + pos);
   }
   if (first) {
@@ -399,113 +429,157 @@ __device__ __forceinline__ Place find(const VParams& p, int b, int h, int row0, 
   return s;
 }
 
-// DST: the new pages' codec; WIDE: there are 16-bit pages among the old.  T warps share a page (1
-// where rows need no scale): teams of 1, 2, 4 or 8, so that a page of up to 128 tokens
-// has a warp per 16 rows and is read once.
-template <int D, int DST, bool WIDE>
-__global__ void __launch_bounds__(32 * kWarps) gather_kernel(const VParams p, int T, int units) {
+// DST: the new pages' codec.  T warps share a page (1 where rows need no scale): teams of
+// 1, 2, 4 or 8, so that a page of up to 128 tokens has a warp per 16 rows.  Where all rows of a warp are of
+// one codec, and a warp has one group of 16 rows, they are read once and stay in registers as codes; the path for
+// everything else reads them twice (from the L2, the second time) and is short, so that both
+// fit the instruction cache.
+template <int D, int DST>
+__global__ void __launch_bounds__(32 * kWarps, 3) gather_kernel(const VParams p, int T, int units) {
   constexpr bool kScaled = DST == ARGUS_FP8_E4M3 || DST == ARGUS_INT8;
   constexpr int V = D / 16, RS = 32 / V, STEPS = 16 / RS;   // lanes per row, rows per step
   __shared__ float s_max[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, team = warp / T, tw = warp % T;
-  const int unit = blockIdx.x * (kWarps / T) + team;        // KV heads fastest, then pages (or 16-row groups), then sequences
+  const int unit = blockIdx.x * (kWarps / T) + team;        // KV heads fastest, then pages (or groups of 16 rows)
   if (unit >= units) return;                                // whole teams
-  const int h = unit % p.Hkv, rows = kScaled ? p.P : 16, groups = (p.budget + p.P - 1) / p.P * (p.P / rows);
-  const int g = unit / p.Hkv % groups, b = unit / p.Hkv / groups;
+  const int g = unit / p.Hkv, h = unit - g * p.Hkv, b = blockIdx.y, rows = kScaled ? p.P : 16;
   const int m = min(length(p, b), p.budget), row0 = g * rows;
-  const int page = row0 / p.P, in_page = row0 - page * p.P;
+  const int page = kScaled ? g : page_of(p, row0), in_page = row0 - page * p.P;
   if (row0 - in_page >= m) return;                          // a page that holds something is written whole
   const long long slot = p.dst_table[(size_t)b * p.dst_pages + page];
-  const int subs = rows / 16;
-  const bool once = subs <= T;                              // every warp has one group of 16 rows at most
-  const int v = lane % V;
-  Place s = {0, 0, -1};
-  auto place_of = [&](int step) {
-    const int r = step * RS + lane / V;
-    Place y;
-    y.unit = __shfl_sync(0xffffffffu, s.unit, r);
-    y.row = __shfl_sync(0xffffffffu, s.row, r);
-    y.codec = __shfl_sync(0xffffffffu, s.codec, r);
-    return y;
-  };
-  for (int sub = tw; sub < subs; sub += T) s = find(p, b, h, row0 + 16 * sub, m, lane, true);
+  const int subs = rows / 16, v = lane % V;
+  Place s = {-1, -1, 1.f};
+  for (int sub = tw; sub < subs; sub += T) s = find<D>(p, b, h, row0 + 16 * sub, m, lane, true);
   if (slot < 0 || slot >= p.dst_slots) {                    // the whole team
     if (p.status && h == 0 && in_page == 0 && tw == 0 && lane == 0) atomicAdd(p.status, 1u);
     return;
   }
-  Raw<WIDE> raw[2][STEPS];                                  // K and V on their way together where they are narrow
-  auto read = [&](int kv) {
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) raw[WIDE ? 0 : kv][i] = fetch<D, WIDE>(p, place_of(i), kv, v);
+  const long long to_v = (long long)p.Hkv * p.P * D;         // from a K row to its V row, in old pages and new
+  // this lane's sixteen values in a step's rows: their place, and where they go
+  auto row_at = [&](int step) {
+    const long long at = __shfl_sync(0xffffffffu, s.at, step * RS + lane / V);
+    return at < 0 ? at : at + 16 * v;
   };
-  auto write = [&](int sub, int kv, float scale) {
-    const long long at = (((slot * 2 + kv) * p.Hkv + h) * p.P + in_page + 16 * sub) * D + 16 * v;
+  const long long page_at = ((slot * 2 * p.Hkv + h) * p.P + in_page + lane / V) * D + 16 * v;
+  auto target = [&](int sub, int kv, int step) { return page_at + (kv ? to_v : 0) + (16 * sub + step * RS) * D; };
+  // the page's scale, from every warp's largest magnitude
+  auto scale_of = [&](int kv, float top) {
+    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+    if (T > 1) {
+      if (lane == 0) s_max[kv][warp] = top;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * T) : "memory");
+      for (int i = 0; i < T; ++i) top = fmaxf(top, s_max[kv][team * T + i]);
+    }
+    const float scale = top / (DST == ARGUS_FP8_E4M3 ? 448.f : 127.f);
+    if (tw == 0 && lane == 0) p.dst_meta[(slot * 2 + kv) * p.Hkv + h] = scale;
+    return scale;
+  };
+  // the codec of all this warp's rows that have a place; -1 where they differ, or a warp has several groups
+  const int first = __reduce_max_sync(0xffffffffu, s.codec);
+  const int src = subs <= T && __all_sync(0xffffffffu, s.codec == first || s.codec < 0) ? (first < 0 ? DST : first) : -1;
+  auto fast = [&](auto codec) {
+    constexpr int SRC = decltype(codec)::value;
+#pragma unroll 1
+    for (int kv = 0; kv < 2; ++kv) {
+      uint32_t q[STEPS][8];
+      float f[STEPS], top = 0.f;
+      Raw<SRC> raw[STEPS];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-      const int r = i * RS + lane / V, codec = __shfl_sync(0xffffffffu, s.codec, r);
-      const long long to = at + (long long)r * D;
-      const Raw<WIDE>& y = raw[WIDE ? 0 : kv][i];
-      if constexpr (!kScaled) {
-        uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * to);
-        if constexpr (WIDE) {
-          if (codec == DST) {                               // as it is
-            d[0] = y.a;
-            d[1] = y.b;
-            continue;
+      for (int i = 0; i < STEPS; ++i) {
+        const long long at = row_at(i);
+        raw[i] = fetch<SRC>(p, at < 0 || kv == 0 ? at : at + to_v);
+      }
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        f[i] = SRC <= ARGUS_BF16 ? 1.f : __shfl_sync(0xffffffffu, s.scale, 16 * kv + i * RS + lane / V);
+        pairs<SRC>(raw[i], q[i]);
+        if (kScaled) top = fmaxf(top, largest<SRC>(q[i], f[i]));
+      }
+      [[maybe_unused]] float scale = 1.f, rcp = 1.f;
+      if constexpr (kScaled) {
+        scale = scale_of(kv, top);
+        rcp = moderate(scale) ? 1.f / scale : 0.f;
+      }
+      if (tw < subs) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const long long to = target(tw, kv, i);
+          if constexpr (DST == SRC && !kScaled) {           // as it is
+            uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * to);
+            d[0] = make_uint4(q[i][0], q[i][1], q[i][2], q[i][3]);
+            d[1] = make_uint4(q[i][4], q[i][5], q[i][6], q[i][7]);
+          } else {
+            float y[16];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 z = pair_values<SRC>(q[i][e]);
+              y[2 * e] = z.x;
+              y[2 * e + 1] = z.y;
+            }
+            if constexpr (kScaled) {
+              *reinterpret_cast<uint4*>(p.dst_codes + to) = encode<DST>(y, f[i], rcp, scale);
+            } else {
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                o[e] = DST == ARGUS_BF16 ? pack_bf16x2(y[2 * e] * f[i], y[2 * e + 1] * f[i]) : pack_f16x2(y[2 * e] * f[i], y[2 * e + 1] * f[i]);
+              uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * to);
+              d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
           }
         }
-        float x[16];
-        uint32_t o[8];
-        values(y, codec, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = DST == ARGUS_BF16 ? pack_bf16x2(x[2 * e], x[2 * e + 1]) : pack_f16x2(x[2 * e], x[2 * e + 1]);
-        d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        d[1] = make_uint4(o[4], o[5], o[6], o[7]);
-      } else {
-        float x[16];
-        values(y, codec, x);
-        *reinterpret_cast<uint4*>(p.dst_codes + to) = encode<DST>(x, scale);
       }
     }
   };
-  if constexpr (!kScaled) {
-    if (!WIDE) {
-      read(0);
-      read(1);
-    }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      if (WIDE) read(kv);
-      write(0, kv, 0.f);
-    }
+  // of a team, every warp has to take the same number of barriers: one per scale, on either path
+  if (src == ARGUS_FP8_E4M3) {
+    fast(std::integral_constant<int, ARGUS_FP8_E4M3>{});
+  } else if (src == ARGUS_INT8) {
+    fast(std::integral_constant<int, ARGUS_INT8>{});
+  } else if (src == ARGUS_BF16 && DST != ARGUS_FP16) {
+    fast(std::integral_constant<int, ARGUS_BF16>{});
+  } else if (src == ARGUS_FP16 && DST != ARGUS_BF16) {
+    fast(std::integral_constant<int, ARGUS_FP16>{});
   } else {
-    if (!WIDE && once && tw < subs) {
-      read(0);
-      read(1);
-    }
-#pragma unroll
+#pragma unroll 1
     for (int kv = 0; kv < 2; ++kv) {
-      float top = 0.f;
-      for (int sub = tw; sub < subs; sub += T) {
-        if (!once) s = find(p, b, h, row0 + 16 * sub, m, lane, false);
-        if (WIDE || !once) read(kv);
+      [[maybe_unused]] float scale = 1.f, rcp = 1.f;
+#pragma unroll 1
+      for (int pass = kScaled ? 0 : 1; pass < 2; ++pass) {
+        float top = 0.f;
+#pragma unroll 1
+        for (int sub = tw; sub < subs; sub += T) {
+          if (subs > T) s = find<D>(p, b, h, row0 + 16 * sub, m, lane, false);
+#pragma unroll 1
+          for (int i = 0; i < STEPS; ++i) {
+            const int r = i * RS + lane / V;
+            Place at;
+            at.at = row_at(i);
+            at.codec = __shfl_sync(0xffffffffu, s.codec, r);
+            at.scale = __shfl_sync(0xffffffffu, s.scale, 16 * kv + r);
+            float x[16];
+            values(p, at, at.at + (kv ? to_v : 0), x);
+            if (pass == 0) {
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i) top = fmaxf(top, largest(raw[WIDE ? 0 : kv][i], __shfl_sync(0xffffffffu, s.codec, i * RS + lane / V)));
-      }
-      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));   // bits of magnitudes order like them
-      if (T > 1) {
-        if (lane == 0) s_max[kv][warp] = top;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(32 * T) : "memory");
-        for (int i = 0; i < T; ++i) top = fmaxf(top, s_max[kv][team * T + i]);
-      }
-      const float scale = top / (DST == ARGUS_FP8_E4M3 ? 448.f : 127.f);
-      if (tw == 0 && lane == 0) p.dst_meta[(slot * 2 + kv) * p.Hkv + h] = scale;
-      for (int sub = tw; sub < subs; sub += T) {
-        if (!once) {
-          s = find(p, b, h, row0 + 16 * sub, m, lane, false);
-          read(kv);
+              for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[e]));
+            } else if constexpr (kScaled) {
+              *reinterpret_cast<uint4*>(p.dst_codes + target(sub, kv, i)) = encode<DST>(x, 1.f, rcp, scale);
+            } else {
+              // a 16-bit value of the same type comes back as it was
+              uint32_t o[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[e] = DST == ARGUS_BF16 ? pack_bf16x2(x[2 * e], x[2 * e + 1]) : pack_f16x2(x[2 * e], x[2 * e + 1]);
+              uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * target(sub, kv, i));
+              d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+              d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+          }
         }
-        write(sub, kv, scale);
+        if (kScaled && pass == 0) {
+          scale = scale_of(kv, top);
+          rcp = moderate(scale) ? 1.f / scale : 0.f;
+        }
       }
     }
   }
@@ -517,21 +591,16 @@ static cudaError_t launch_gather(const VParams& p, cudaStream_t s) {
   const int rows = scaled ? p.P : 16;
   int T = 1;
   while (scaled && T < kWarps && 16 * T < p.P) T *= 2;
-  const long long units = (long long)p.B * p.Hkv * ((p.budget + p.P - 1) / p.P) * (p.P / rows), per = kWarps / T;
+  const long long units = (long long)p.Hkv * ((p.budget + p.P - 1) / p.P) * (p.P / rows), per = kWarps / T;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((units + per - 1) / per));
+  cfg.gridDim = dim3((unsigned)((units + per - 1) / per), p.B);
   cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = s;
-  const bool wide = p.pool[ARGUS_FP16].n_slots > 0 || p.pool[ARGUS_BF16].n_slots > 0;
-  const auto go = [&](auto dst) {
-    constexpr int DST = decltype(dst)::value;
-    return wide ? cudaLaunchKernelEx(&cfg, gather_kernel<D, DST, true>, p, T, (int)units) : cudaLaunchKernelEx(&cfg, gather_kernel<D, DST, false>, p, T, (int)units);
-  };
   switch (p.dst_codec) {
-    case ARGUS_FP16: return go(std::integral_constant<int, ARGUS_FP16>{});
-    case ARGUS_BF16: return go(std::integral_constant<int, ARGUS_BF16>{});
-    case ARGUS_FP8_E4M3: return go(std::integral_constant<int, ARGUS_FP8_E4M3>{});
-    default: return go(std::integral_constant<int, ARGUS_INT8>{});
+    case ARGUS_FP16: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_FP16>, p, T, (int)units);
+    case ARGUS_BF16: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_BF16>, p, T, (int)units);
+    case ARGUS_FP8_E4M3: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_FP8_E4M3>, p, T, (int)units);
+    default: return cudaLaunchKernelEx(&cfg, gather_kernel<D, ARGUS_INT8>, p, T, (int)units);
   }
 }
 
@@ -542,7 +611,9 @@ static argus_status status_of(cudaError_t e, const char* what) {
 }
 
 static argus_status launch(const VParams& p, int D, cudaStream_t s) {
-  // blocks per row: one holds 32,768 keys; more than 8 times that are read again in every round
+  // blocks per row: one holds 32,768 keys; more than 8 times that are read again in every round.  (More
+  // blocks than a row needs cost more in the cluster's barriers than they save: 16,384 keys 28 us
+  // by one block, 37 by eight.)
   const long long keys = (long long)kSelThreads * kRegKeys, longest = (long long)p.max_pages * p.P;
   int C = 1;
   while (C < kMaxCluster && C * keys < longest) C *= 2;
@@ -598,7 +669,7 @@ extern "C" argus_status argus_evict_tokens(const argus_geom* g, int32_t batch, c
     return fail(ARGUS_E_INVALID, "evict: budget must hold sink_tokens and recent_tokens (all >= 0)");
   if ((long long)dst_pages * g->page_tokens < budget) return fail(ARGUS_E_INVALID, "evict: dst_pages do not hold the budget");
   if (row_len < positions || row_len_out < budget) return fail(ARGUS_E_INVALID, "evict: rows of weights shorter than the cache, or weights_out than the budget");
-  if ((long long)batch * g->n_kv_heads > 0x7fffffffll / std::max(1ll, ((long long)budget + g->page_tokens - 1) / g->page_tokens * (g->page_tokens / 16))) return fail(ARGUS_E_UNSUPPORTED, "evict: 2^31 groups of 16 rows or more");
+  if ((long long)g->n_kv_heads > 0x7fffffffll / std::max(1ll, ((long long)budget + g->page_tokens - 1) / g->page_tokens * (g->page_tokens / 16))) return fail(ARGUS_E_UNSUPPORTED, "evict: 2^31 groups of 16 rows or more");
   if (n_pools > 0 && !pools) return fail(ARGUS_E_INVALID, "evict: pools is NULL");
   if (dst->codec < 0 || dst->codec > ARGUS_INT1_G32) return fail(ARGUS_E_INVALID, "evict: bad codec %d", dst->codec);
   if (dst->codec > ARGUS_INT8) return fail(ARGUS_E_UNSUPPORTED, "evict: new pages of codec %d (supported: 16-bit, FP8, INT8)", dst->codec);
@@ -642,6 +713,10 @@ extern "C" argus_status argus_evict_tokens(const argus_geom* g, int32_t batch, c
   p.budget = budget;
   p.sinks = sink_tokens;
   p.recent = recent_tokens;
+  int bits = 0;
+  while ((1ll << bits) < p.P) ++bits;  // P >= 16
+  p.p_mul = (uint32_t)(((1ull << (31 + bits)) + p.P - 1) / p.P);
+  p.p_shift = bits - 1;
   p.dst_codec = dst->codec;
   p.dst_pages = dst_pages;
   p.page_codec = page_codec;
