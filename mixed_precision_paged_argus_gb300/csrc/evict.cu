@@ -68,11 +68,12 @@ constexpr int kRegKeys = 32;           // keys per thread that stay in registers
 constexpr int kMaxCluster = 8;
 constexpr int kList = 4 * kSelThreads; // keys that share T's first bits, from which on the others are left alone
 
+// Keys of the weights' order: NaN 1, -inf 0x7FFFFF, zeros 0x80000000, inf 0xFF800000.  A position that
+// stays in any case has the key kAlways, one that is not there 0.
+constexpr uint32_t kAlways = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t order(float w) {
-  const uint32_t u = __float_as_uint(w);
-  if (w != w) return 0u;
-  if (w == 0.f) return 0x80000000u;
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f);         // -0 becomes 0
+  return w != w ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 struct Counts {
@@ -108,14 +109,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     for (int i = tid; i < m; i += all) kept[i] = i;
     return;
   }
-  const int lo = p.sinks, hi = len - p.recent, k = p.budget - p.sinks - p.recent;   // candidates lo .. hi-1: more than k
-  // this warp's positions: steps of 32 neighbours
-  const long long all_steps = (long long)C * kSelThreads;
-  const int steps = KEYS > 0 ? KEYS : (int)((len + all_steps - 1) / all_steps);
-  const long long start = ((long long)rank * kSelWarps + warp) * steps * 32 + lane;
-  auto load = [&](int i) -> float {                    // NaN (below all) for what is not a candidate
-    const long long pos = start + i * 32ll;
-    return pos >= lo && pos < hi ? __ldg(w + pos) : __uint_as_float(0x7FC00000u);
+  const int lo = p.sinks, hi = len - p.recent, k = p.budget;   // what lies outside lo .. hi-1 is among the k, and less than len are
+  // this warp's positions: steps of 32 neighbours (all within 8,192 of the row's end)
+  const int steps = KEYS > 0 ? KEYS : (int)(((long long)len + C * kSelThreads - 1) / (C * kSelThreads));
+  const int start = (rank * kSelWarps + warp) * steps * 32 + lane;
+  auto load = [&](int i) -> float {
+    const int pos = start + i * 32;
+    return pos >= lo && pos < hi ? __ldg(w + pos) : 0.f;
+  };
+  auto key_of = [&](int i, float x) {
+    const int pos = start + i * 32;
+    return pos >= lo && pos < hi ? order(x) : pos < len ? kAlways : 0u;
   };
   uint32_t key[KEYS > 0 ? KEYS : 1];
   if constexpr (KEYS > 0) {
@@ -123,14 +127,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
 #pragma unroll
     for (int i = 0; i < KEYS; ++i) x[i] = load(i);
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) key[i] = order(x[i]);
+    for (int i = 0; i < KEYS; ++i) key[i] = key_of(i, x[i]);
   }
   auto each = [&](auto f) {
     if constexpr (KEYS > 0) {
 #pragma unroll
       for (int i = 0; i < KEYS; ++i) f(i, key[i]);
     } else {
-      for (int i = 0; i < steps; ++i) f(i, order(load(i)));
+      for (int i = 0; i < steps; ++i) f(i, key_of(i, load(i)));
     }
   };
   int turn = 0;
@@ -162,8 +166,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     if (before) *before = in;
     return y;
   };
-  uint32_t T = 0xFFFFFFFFu, ties = 0;                  // keys above T stay, and the first `ties` at T
-  if (k > 0) {
+  uint32_t T = 0, ties = 0;                            // keys above T stay, and the first `ties` at T
+  {
     uint32_t prefix = 0, upper = 0, at = 0xFFFFFFFFu;  // T's bits so far; keys at or above the prefix's successor, and the prefix
     int s = 32;                                        // bits still open
     // two more bits from the counts of keys at or above the three next prefixes; true: the search is over
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
       if (threadIdx.x == 0) s_listed = 0;
       __syncthreads();
       each([&](int, uint32_t x) {
-        const bool in = x >> s == prefix >> s && x != 0;   // 0: never counted
+        const bool in = x >> s == prefix >> s;
         const uint32_t m = __ballot_sync(0xffffffffu, in);
         if (!m) return;
         uint32_t to = 0;
@@ -213,37 +217,31 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
         exact = narrow({c.a + above, c.b + above, c.c + above});
       }
     }
-    T = prefix;
-    ties = exact ? 0xFFFFFFFFu : (uint32_t)k - upper;
+    // k keys at or above the prefix: all of them; T is not 0, as there are more than k keys above 0
+    T = exact ? prefix - 1 : prefix;
+    ties = exact ? 0u : (uint32_t)k - upper;
   }
-  auto stays = [&](int i, uint32_t x, bool& tie) {
-    const long long pos = start + i * 32ll;
-    const bool mid = pos >= lo && pos < hi;
-    tie = mid && x == T && ties > 0;
-    return (pos < lo || (pos >= hi && pos < len)) || (mid && x > T);
-  };
   Counts mine = {0, 0, 0};
-  each([&](int i, uint32_t x) {
-    bool tie;
-    const bool stay = stays(i, x, tie);
-    mine.a += __popc(__ballot_sync(0xffffffffu, stay));
-    mine.b += __popc(__ballot_sync(0xffffffffu, tie));
+  each([&](int, uint32_t x) {
+    mine.a += x > T;
+    mine.b += x == T;
   });
+  mine = warp_sum(mine);
   Counts before;
   total(mine, &before);
-  uint32_t at = before.a + min(before.b, ties), tied = before.b;
   const uint32_t lt = (1u << lane) - 1;
+  uint32_t at = before.a + min(before.b, ties), tied = before.b;
+  const bool some = ties > 0;
   each([&](int i, uint32_t x) {
-    bool tie;
-    const bool stay = stays(i, x, tie);
-    const uint32_t eq = __ballot_sync(0xffffffffu, tie);
-    const bool keep = stay || (tie && tied + __popc(eq & lt) < ties);
-    const uint32_t mask = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      kept[at + __popc(mask & lt)] = (int32_t)(start + i * 32ll);
+    bool keep = x > T;
+    if (some) {                                        // the first `ties` of those at T
+      const uint32_t eq = __ballot_sync(0xffffffffu, x == T);
+      keep = keep || (x == T && tied + __popc(eq & lt) < ties);
+      tied += __popc(eq);
     }
+    const uint32_t mask = __ballot_sync(0xffffffffu, keep);
+    if (keep) kept[at + __popc(mask & lt)] = start + i * 32;
     at += __popc(mask);
-    tied += __popc(eq);
   });
   if (C > 1) cluster.sync();                           // the others may still read this block's sums
 }
