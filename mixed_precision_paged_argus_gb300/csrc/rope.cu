@@ -112,51 +112,78 @@ __device__ __forceinline__ void turn_pair(uint4& a4, uint4& b4, const float* cs,
   }
 }
 
-// The same two vectors by their norm: r = 1 / sqrt(mean + eps) of the head (its values times
-// `pre`), wa and wb the weights of their elements; turned by the pairs of item u unless u < 0.
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight eight(const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+
+// The same two vectors by their norm: r = 1 / sqrt(mean + eps) of the head (its values times `pre`, if `far`), wa and wb
+// the weights of their elements; turned by the pairs of item u unless u < 0.
 template <bool BF>
-__device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, float pre, float r, const float* wa, const float* wb, const float* cs, const float* sn,
-                                          int u, bool adjacent) {
+__device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, bool far, float pre, float r, const float* wa, const float* wb, const float* cs,
+                                          const float* sn, int u, bool adjacent) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&a4);
   uint32_t* b = reinterpret_cast<uint32_t*>(&b4);
+  float x[8], y[8];
+  const Eight v = eight(wa), w = eight(wb);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float2 x = unpack2<BF>(a[j]), y = unpack2<BF>(b[j]);
-    const float2 v = *reinterpret_cast<const float2*>(wa + 2 * j), w = *reinterpret_cast<const float2*>(wb + 2 * j);
-    x = make_float2(x.x * pre * r * v.x, x.y * pre * r * v.y);
-    y = make_float2(y.x * pre * r * w.x, y.y * pre * r * w.y);
-    if (u >= 0) {
-      if (adjacent) {                                    // two pairs, a's and b's
-        const float c0 = cs[8 * u + j], s0 = sn[8 * u + j], c1 = cs[8 * u + 4 + j], s1 = sn[8 * u + 4 + j];
-        x = make_float2(x.x * c0 - x.y * s0, x.y * c0 + x.x * s0);
-        y = make_float2(y.x * c1 - y.y * s1, y.y * c1 + y.x * s1);
-      } else {
-        const float2 c = *reinterpret_cast<const float2*>(cs + 8 * u + 2 * j), s = *reinterpret_cast<const float2*>(sn + 8 * u + 2 * j);
-        const float2 z = x;
-        x = make_float2(z.x * c.x - y.x * s.x, z.y * c.y - y.y * s.y);
-        y = make_float2(y.x * c.x + z.x * s.x, y.y * c.y + z.y * s.y);
+    float2 p = unpack2<BF>(a[j]), q = unpack2<BF>(b[j]);
+    if (BF && far) {
+      p = make_float2(p.x * pre, p.y * pre);
+      q = make_float2(q.x * pre, q.y * pre);
+    }
+    x[2 * j] = p.x * r * v.v[2 * j];
+    x[2 * j + 1] = p.y * r * v.v[2 * j + 1];
+    y[2 * j] = q.x * r * w.v[2 * j];
+    y[2 * j + 1] = q.y * r * w.v[2 * j + 1];
+  }
+  if (u >= 0) {
+    const Eight c = eight(cs + 8 * u), s = eight(sn + 8 * u);
+    if (adjacent) {                                      // pairs of neighbours, four in each vector
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = x[2 * j], q = y[2 * j];
+        x[2 * j] = p * c.v[j] - x[2 * j + 1] * s.v[j];
+        x[2 * j + 1] = x[2 * j + 1] * c.v[j] + p * s.v[j];
+        y[2 * j] = q * c.v[4 + j] - y[2 * j + 1] * s.v[4 + j];
+        y[2 * j + 1] = y[2 * j + 1] * c.v[4 + j] + q * s.v[4 + j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p = x[j];
+        x[j] = p * c.v[j] - y[j] * s.v[j];
+        y[j] = y[j] * c.v[j] + p * s.v[j];
       }
     }
-    a[j] = pack2<BF>(x.x, x.y);
-    b[j] = pack2<BF>(y.x, y.y);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    a[j] = pack2<BF>(x[2 * j], x[2 * j + 1]);
+    b[j] = pack2<BF>(y[2 * j], y[2 * j + 1]);
   }
 }
 
 template <bool BF>
-__device__ __forceinline__ float squares(const uint4& a4, float pre) {
+__device__ __forceinline__ float squares(const uint4& a4, bool far, float pre) {
   const uint32_t* a = reinterpret_cast<const uint32_t*>(&a4);
   float s = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 x = unpack2<BF>(a[j]);
-    s = fmaf(x.x * pre, x.x * pre, s);
-    s = fmaf(x.y * pre, x.y * pre, s);
+    float2 x = unpack2<BF>(a[j]);
+    if (far) x = make_float2(x.x * pre, x.y * pre);
+    s = fmaf(x.x, x.x, s);
+    s = fmaf(x.y, x.y, s);
   }
   return s;
 }
 
 template <int D, bool BF, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) {
+__device__ __forceinline__ void rope_tokens(const RParams& p, int W) {
   __shared__ __align__(16) float s_cs[kThreads / 32][2][D / 2];
   __shared__ unsigned long long s_freq[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -224,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
     }
     __syncwarp();
     uint16_t* page = p.codes + (size_t)(slot < 0 ? 0 : slot) * 2 * p.Hkv * p.P * D + (size_t)row * D;
-    constexpr int M = 4;                                 // items in flight
+    constexpr int M = NORM ? 2 : 4;                      // items in flight: what three blocks per SM have registers for
     for (int it0 = part * 32 + lane; it0 - (NORM ? lane : 0) < n_items; it0 += 32 * W * M) {   // NORM: by whole warps
       uint4 a[M], bb[M];
       uint16_t* dst[M];
@@ -234,13 +261,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
       for (int m = 0; m < M; ++m) {
         const int it = it0 + m * 32 * W;
         dst[m] = nullptr;
-        hw[m] = 2;
-        a[m] = bb[m] = make_uint4(0, 0, 0, 0);
+        if (NORM) {
+          hw[m] = 2;
+          a[m] = bb[m] = make_uint4(0, 0, 0, 0);
+        }
         if (it >= n_items) continue;
         const int head = it / U, u = it % U;
         const bool turned = u < ru && head < p.Hq + p.Hkv, halves = turned && !p.adjacent;
         un[m] = turned ? u : -1;
-        hw[m] = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
+        if (NORM) hw[m] = head < p.Hq ? 0 : head < p.Hq + p.Hkv ? 1 : 2;
         const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? p.rot / 2 + 8 * u : 16 * u + 8;
         const uint16_t* src;
         if (head < p.Hq) {
@@ -258,15 +287,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
       if constexpr (NORM) {
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          float pre = 1.f, ss = squares<BF>(a[m], 1.f) + squares<BF>(bb[m], 1.f);
+          float pre = 1.f, ss = squares<BF>(a[m], false, 1.f) + squares<BF>(bb[m], false, 1.f);
 #pragma unroll
           for (int o = 1; o < U; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (BF && __any_sync(0xffffffffu, ss > 3e38f)) {   // squares beyond fp32's range (bf16 reaches as far as fp32)
-            float far = squares<BF>(a[m], 0x1p-70f) + squares<BF>(bb[m], 0x1p-70f);
+          const bool far = BF && __any_sync(0xffffffffu, ss > 3e38f);   // squares beyond fp32's range (bf16 reaches as far as fp32)
+          if (far) {
+            float less = squares<BF>(a[m], true, 0x1p-70f) + squares<BF>(bb[m], true, 0x1p-70f);
 #pragma unroll
-            for (int o = 1; o < U; o *= 2) far += __shfl_xor_sync(0xffffffffu, far, o);
+            for (int o = 1; o < U; o *= 2) less += __shfl_xor_sync(0xffffffffu, less, o);
             if (ss > 3e38f) {
-              ss = far;
+              ss = less;
               pre = 0x1p-70f;
             }
           }
@@ -274,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
             const int u = (it0 + m * 32 * W) % U;
             const bool halves = un[m] >= 0 && !p.adjacent;
             const float* w = s_weight[hw[m]];
-            norm_pair<BF>(a[m], bb[m], pre, rsqrtf(ss * (1.f / D) + (pre == 1.f ? p.eps : p.eps * 0x1p-140f)), w + (halves ? 8 : 16) * u,
+            norm_pair<BF>(a[m], bb[m], far, pre, rsqrtf(ss * (1.f / D) + (pre == 1.f ? p.eps : p.eps * 0x1p-140f)), w + (halves ? 8 : 16) * u,
                           w + (halves ? p.rot / 2 + 8 * u : 16 * u + 8), cs, sn, un[m], p.adjacent);
           }
         }
@@ -290,6 +320,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) 
   }
 }
 
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RParams p, int W) { rope_tokens<D, BF, false>(p, W); }
+template <int D, bool BF>
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const RParams p, int W) { rope_tokens<D, BF, true>(p, W); }
+
 template <int D, bool BF, bool NORM>
 static argus_status launch(const RParams& p, cudaStream_t s) {
   constexpr int kWarps = kThreads / 32;
@@ -304,7 +339,7 @@ static argus_status launch(const RParams& p, cudaStream_t s) {
   cfg.gridDim = dim3((int)std::min(blocks, sms * 3));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rope_kernel<D, BF, NORM>, p, W);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, NORM ? norm_rope_kernel<D, BF> : rope_kernel<D, BF>, p, W);
   if (e == cudaSuccess) return ARGUS_OK;
   cudaGetLastError();                  // not left for the next call to find
   return fail(ARGUS_E_LAUNCH, "argus_%srope_append: launch failed: %s", NORM ? "norm_" : "", cudaGetErrorString(e));
