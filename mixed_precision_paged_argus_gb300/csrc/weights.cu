@@ -23,30 +23,10 @@
 
 #include "codes.cuh"
 #include "common.cuh"
+#include "weights.cuh"
 
 namespace argus {
 namespace weights {
-
-struct PoolRef {
-  const uint8_t* codes;
-  const uint8_t* meta;
-  long long n_slots;
-};
-
-struct WParams {
-  int Hq, Hkv, G, P, B, total_q, causal, max_pages;
-  const uint16_t* q;
-  long long qs;
-  const int32_t *q_start, *seq_lens;
-  PoolRef pool[7];
-  const uint8_t* page_codec;
-  const int32_t* block_table;
-  const float* lse2;
-  float* weights;
-  long long row_len;
-  float decay, scale_log2;
-  uint32_t* status;
-};
 
 // Warps per block, blocks per SM, bytes of a warp's ring (pairs of chunks on their way) for calls with
 // pages of every codec, and with 8-bit ones alone.
@@ -56,26 +36,7 @@ struct Shape {
 };
 constexpr int kBatch = 32;             // chunks looked up at once
 constexpr int kMaxSlots = 4;
-
-__device__ __forceinline__ long long warp_sum(long long x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
-
-__device__ __forceinline__ int length(const WParams& p, int b) {
-  return (int)min((long long)max(p.seq_lens[b], 0), (long long)p.max_pages * p.P);
-}
-__device__ __forceinline__ long long chunks_of(const WParams& p, int b) { return (long long)p.Hkv * ((length(p, b) + 15) / 16); }
+constexpr int kMany = 16;              // rows from which on the tensor cores' large tiles pay
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -91,6 +52,11 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
   return v;
+}
+
+// A sequence's chunks, KV heads one after the other; those of many rows have none here.
+__device__ __forceinline__ long long chunks_of(const WParams& p, int b) {
+  return rows_of(p, b).rows > p.many ? 0 : (long long)p.Hkv * ((length(p, b) + 15) / 16);
 }
 
 // How a page's operands are formed, and with it the order of a row's dims in them.
@@ -312,7 +278,7 @@ __device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* fo
   for (;;) {                           // there is a chunk ahead: the loop ends at its sequence
     x.len = length(p, w.b);
     per = (x.len + 15) / 16;
-    if (w.at < (long long)per * p.Hkv) break;
+    if (w.at < chunks_of(p, w.b)) break;
     w.at = 0;
     ++w.b;
   }
@@ -322,12 +288,10 @@ __device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* fo
   x.n = (int)min(w.left, (long long)min(kBatch, per - x.c0));
   w.left -= x.n;
   w.at += x.n;
-  {
-    const int t0 = min(max(p.q_start[x.b], 0), p.total_q), t1 = min(max(p.q_start[x.b + 1], 0), p.total_q);
-    x.t0 = t0;
-    x.rows = max(t1 - t0, 0) * p.G;    // fewer than 2^31
-    x.tiles = max((x.rows + 7) / 8, 1);
-  }
+  const Span r = rows_of(p, x.b);
+  x.t0 = r.t0;
+  x.rows = r.rows;
+  x.tiles = max((x.rows + 7) / 8, 1);
   if (lane < x.n) {
     Found f = {nullptr, 1.f, -1};
     const uint8_t* meta = nullptr;
@@ -335,15 +299,15 @@ __device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* fo
     const size_t e = (size_t)x.b * p.max_pages + page;
     const int k = p.page_codec[e];
     const long long slot = p.block_table[e];
-    const PoolRef r = p.pool[k <= ARGUS_INT1_G32 ? k : 0];
-    if (k > ARGUS_INT1_G32 || slot < 0 || slot >= r.n_slots) {
+    const PoolRef pool = p.pool[k <= ARGUS_INT1_G32 ? k : 0];
+    if (k > ARGUS_INT1_G32 || slot < 0 || slot >= pool.n_slots) {
       if (x.h == 0 && row == 0 && p.status) atomicAdd(p.status, 1u);
     } else {
       f.codec = k;
       const long long unit = slot * 2 * p.Hkv + x.h, token = unit * p.P + row;
-      f.src = r.codes + token * (!ANY ? D : k <= ARGUS_BF16 ? 2 * D : k <= ARGUS_INT8 ? D : D >> (k - ARGUS_INT8));
-      if (ANY && k >= ARGUS_INT4_G32) meta = r.meta + token * (D / 32) * 4;
-      else if (k >= ARGUS_FP8_E4M3) f.ks = __ldg(reinterpret_cast<const float*>(r.meta) + unit);
+      f.src = pool.codes + token * (!ANY ? D : k <= ARGUS_BF16 ? 2 * D : k <= ARGUS_INT8 ? D : D >> (k - ARGUS_INT8));
+      if (ANY && k >= ARGUS_INT4_G32) meta = pool.meta + token * (D / 32) * 4;
+      else if (k >= ARGUS_FP8_E4M3) f.ks = __ldg(reinterpret_cast<const float*>(pool.meta) + unit);
     }
     found[(to + lane) % kLooked] = f;
     if (ANY) metas[(to + lane) % kLooked] = meta;
@@ -569,9 +533,21 @@ static argus_status launch(const WParams& p, cudaStream_t s) {
 }
 
 template <int D>
-static argus_status launch_d(const WParams& p, bool bf, cudaStream_t s) {
-  bool any = false;
-  for (int k = 0; k < 7; ++k) any |= k != ARGUS_FP8_E4M3 && k != ARGUS_INT8 && p.pool[k].n_slots > 0;
+static argus_status launch_d(WParams p, bool bf, cudaStream_t s) {
+  bool any = false, group = false;
+  for (int k = 0; k < 7; ++k) {
+    if (p.pool[k].n_slots <= 0) continue;
+    any |= k != ARGUS_FP8_E4M3 && k != ARGUS_INT8;
+    group |= k >= ARGUS_INT4_G32;
+  }
+  // A decode step has as many tokens as sequences.  With more, some sequence has several, and a second
+  // kernel takes those of more than kMany rows; that one knows no group codes.
+  p.many = 0x7fffffff;
+  if (!group && p.total_q > p.B && (long long)p.total_q * p.G > kMany) {
+    p.many = kMany;
+    const argus_status st = launch_rows(p, D, bf, any, s);
+    if (st != ARGUS_OK) return st;
+  }
   if (bf) return any ? launch<D, true, true>(p, s) : launch<D, true, false>(p, s);
   return any ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
 }
