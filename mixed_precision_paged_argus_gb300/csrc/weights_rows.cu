@@ -9,7 +9,7 @@
 //  * K tiles are converted into the query's type on their way to shared memory (the loader warps are
 //    extend.cuh's), up to four tiles of 128 rows of Q stay there; more rows take another pass
 //    over the keys, by the same block, whose threads add to the weights that they wrote.
-//  * Two groups of four warps sum 64 columns each of every tile; four score tiles in TMEM let the
+//  * Four groups of four warps sum 32 columns each of every tile; four score tiles in TMEM let the
 //    MMAs run ahead.  Exponentials (32 per cycle) and MMAs take 512 cycles per tile each.
 // One block per SM; key blocks, weighted by their tiles, are dealt in equal ranges.
 #include <algorithm>
@@ -28,13 +28,10 @@ namespace rowwise {
 constexpr int kBM = 128;               // keys per block: TMEM lanes
 constexpr int kBN = 128;               // query rows per tile: TMEM columns
 constexpr int kTiles = 4;              // of Q in shared memory, and of scores in TMEM
-constexpr int kSumWarps = 8, kLoadWarps = 8, kMmaWarp = kSumWarps + kLoadWarps;
-constexpr int kWarps = kMmaWarp + 4;   // whole groups of four: registers are dealt out by group
+constexpr int kSumWarps = 16, kLoadWarps = 8, kMmaWarp = kSumWarps + kLoadWarps;
+constexpr int kGroups = kSumWarps / 4, kCols = kBN / kGroups;   // of warps that see all lanes; columns each
+constexpr int kWarps = kMmaWarp + 1;
 constexpr int kThreads = 32 * kWarps;
-// a thread's registers at launch, and what the groups give up or take; nothing may spill, as the tiles
-// leave the L1 no room
-constexpr int kLaunchRegs = 96, kSumRegs = 136, kLoadRegs = 72, kMmaRegs = 64;
-static_assert(kSumWarps * kSumRegs + kLoadWarps * kLoadRegs + 4 * kMmaRegs <= kWarps * kLaunchRegs, "registers");
 constexpr int kScales = 8;             // blocks whose scales are kept: loaders are two ahead of the MMAs, these four tiles of the sums
 
 template <int D>
@@ -44,10 +41,12 @@ struct Smem {
   static constexpr int kOffK = kTiles * kTile;
   static constexpr int kOffL = kOffK + 2 * kTile;                  // [kTiles * kBN] minus the rows' log-sums
   static constexpr int kOffScale = kOffL + kTiles * kBN * 4;       // [kScales][8]
-  static constexpr int kOffHalf = kOffScale + kScales * 8 * 4;     // [2][kBM]: the second group's sums
-  static constexpr int kOffBar = kOffHalf + 2 * kBM * 4;           // k_full[2], k_empty[2], s_full[4], s_free[4], drain
+  static constexpr int kOffHalf = kOffScale + kScales * 8 * 4;     // [2][kGroups - 1][kBM]: the other groups' sums
+  static constexpr int kOffBar = kOffHalf + 2 * (kGroups - 1) * kBM * 4;           // k_full[2], k_empty[2], s_full[4], s_free[4], drain
   static constexpr int kOffMisc = kOffBar + 13 * 8 + 8;
-  static constexpr int kBytes = kOffMisc + 64;
+  static constexpr int kOffPass = kOffMisc + 32;
+  static constexpr int kOffWalk = kOffPass + 48;
+  static constexpr int kBytes = kOffWalk + 32;
   static_assert(kBytes <= 232448, "shared memory");
 };
 
@@ -67,6 +66,48 @@ __device__ __forceinline__ Seq load_seq(const WParams& p, int b) {
   return s;
 }
 
+// What a block does between two barriers of all its warps: blocks blk0 .. of a sequence's KV head, up to kTiles tiles
+// of rows from tile0 on; n0 blocks and i0 score tiles before it.  n_blk = 0: its range is done.
+struct Pass {
+  int t0, rows, len, b, h, blk0, n_blk, tile0, tiles;
+  uint32_t n0, i0;
+};
+// Where its range goes on: units ahead, the next one within its sequence.
+struct Walk {
+  long long left, at;
+  int b;
+};
+// By one thread: the pass behind x, in x.
+__device__ __noinline__ void next_pass(const WParams& p, Walk& w, Pass& x) {
+  x.n0 += x.n_blk;
+  x.i0 += x.n_blk * x.tiles;
+  x.tile0 += kTiles;
+  if (x.n_blk == 0 || (long long)x.tile0 * kBN >= x.rows) {   // the first, or the last of its blocks' passes
+    x.n_blk = 0;
+    x.tile0 = 0;
+    while (w.left > 0 && x.n_blk == 0) {
+      const Seq s = load_seq(p, w.b);
+      const long long per = s.units();
+      if (w.at >= p.Hkv * per) {                         // the next sequence that has any
+        w.at = 0;
+        ++w.b;
+        continue;
+      }
+      x.h = (int)(w.at / per);
+      const long long in = w.at - x.h * per, take = min(w.left, per - in);
+      x.t0 = s.t0;
+      x.rows = s.rows;
+      x.len = s.len;
+      x.b = w.b;
+      x.blk0 = (int)(in / s.tiles);
+      x.n_blk = (int)((in + take) / s.tiles) - x.blk0;
+      w.at += take;
+      w.left -= take;
+    }
+  }
+  x.tiles = min(kTiles, (int)(((long long)x.rows + kBN - 1) / kBN) - x.tile0);
+}
+
 // BF: queries and operands are bf16, else fp16; W16: there are 16-bit pages.
 template <int D, bool BF, bool W16>
 __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams p) {
@@ -82,9 +123,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
   uint64_t* s_full = k_empty + 2;
   uint64_t* s_free = s_full + kTiles;
   uint64_t* drain = s_free + kTiles;
-  // [0] TMEM base, [1] error, [2] first sequence, [4..9] total, where the range begins and ends, units in front of the sequence
+  // [0] TMEM base, [1] error
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffMisc);
-  volatile long long* misc64 = reinterpret_cast<volatile long long*>(smem + SM::kOffMisc);
+  Pass& pass = *reinterpret_cast<Pass*>(smem + SM::kOffPass);
+  Walk& range = *reinterpret_cast<Walk*>(smem + SM::kOffWalk);
   float* neg_lse = reinterpret_cast<float*>(smem + SM::kOffL);
   float* scales = reinterpret_cast<float*>(smem + SM::kOffScale);
   float* half = reinterpret_cast<float*>(smem + SM::kOffHalf);
@@ -110,9 +152,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
-      misc[2] = first;
-      misc64[2] = u0 - before;                           // within the first sequence
-      misc64[3] = u1 - u0;
+      range = {u1 - u0, u0 - before, first};
+      pass = {};
     }
   }
   if (threadIdx.x == 64) {
@@ -136,80 +177,45 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = misc[0];
-  // The passes of this block's range, walked by every role in step: a sequence's KV head, its blocks blk0 ..
-  // blk1 - 1, up to kTiles tiles of rows from tile0 on; n0 blocks and i0 score tiles before it.
-  struct Pass {
-    Seq s;
-    int b, h, blk0, blk1, tile0, tiles;
-    uint32_t n0, i0, n_blk;
-  };
+  // every role goes through the same passes
   auto walk = [&](auto role) {
-    int b = misc[2];
-    long long at = misc64[2], left = misc64[3];
-    uint32_t n0 = 0, i0 = 0;
-    while (left > 0) {
-      Pass x;
-      x.s = load_seq(p, b);
-      const Seq& s = x.s;
-      const long long per = s.units();
-      if (at >= p.Hkv * per) {                           // the next sequence that has any
-        at = 0;
-        ++b;
-        continue;
-      }
-      x.b = b;
-      x.h = (int)(at / per);
-      const long long in = at - x.h * per, take = min(left, per - in);
-      x.blk0 = (int)(in / s.tiles);
-      x.blk1 = (int)((in + take) / s.tiles);
-      x.n_blk = x.blk1 - x.blk0;
-      at += take;
-      left -= take;
-      if (x.n_blk == 0) continue;
-      for (x.tile0 = 0; x.tile0 < s.tiles; x.tile0 += kTiles) {
-        x.tiles = min(kTiles, s.tiles - x.tile0);
-        x.n0 = n0;
-        x.i0 = i0;
-        // Q tiles and log-sums; the pass before is over
-        const int row0 = x.tile0 * kBN;
+    for (;;) {
+      tc_fence_before();
+      __syncthreads();                                   // the tiles, scores and halves have been used
+      tc_fence_after();
+      if (misc[1]) return;
+      if (threadIdx.x == 0) next_pass(p, range, pass);
+      __syncthreads();
+      const Pass x = pass;
+      if (x.n_blk == 0) return;
+      // Q tiles and log-sums
+      const int row0 = x.tile0 * kBN;
 #pragma unroll 1
-        for (int y = threadIdx.x; y < x.tiles * kBN * V; y += kThreads) {
-          const int l = y / V, v = y % V, r = row0 + l;
-          const bool real = r < s.rows;
-          const int tok = real ? r / p.G : 0, g = real ? r - tok * p.G : 0;
-          const uint16_t* src = p.q + (s.t0 + tok) * p.qs + (long long)(x.h * p.G + g) * D + v * 8;
-          extend::cp_async16(smem_u32(smem + SM::kOffQ) + (l / kBN) * kTile + extend::tile_off(l % kBN, v), real ? src : p.q, real ? 16 : 0);
-        }
-#pragma unroll 1
-        for (int l = threadIdx.x; l < x.tiles * kBN; l += kThreads) {
-          const int r = row0 + l, tok = r / p.G;
-          float L = INFINITY;                            // a row that is not there, or sees nothing, gives nothing
-          if (r < s.rows) {
-            L = p.lse2[(size_t)(s.t0 + tok) * p.Hq + x.h * p.G + (r - tok * p.G)];
-            if (L == -INFINITY) L = INFINITY;
-          }
-          neg_lse[l] = -L;
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        extend::fence_async();
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        role(x);
-        // the tiles, scores and halves have been used
-        tc_fence_before();
-        __syncthreads();
-        tc_fence_after();
-        if (misc[1]) return;
-        n0 += x.n_blk;
-        i0 += x.n_blk * x.tiles;
+      for (int y = threadIdx.x; y < x.tiles * kBN * V; y += kThreads) {
+        const int l = y / V, v = y % V, r = row0 + l;
+        const bool real = r < x.rows;
+        const int tok = real ? r / p.G : 0, g = real ? r - tok * p.G : 0;
+        const uint16_t* src = p.q + (x.t0 + tok) * p.qs + (long long)(x.h * p.G + g) * D + v * 8;
+        extend::cp_async16(smem_u32(smem + SM::kOffQ) + (l / kBN) * kTile + extend::tile_off(l % kBN, v), real ? src : p.q, real ? 16 : 0);
       }
+#pragma unroll 1
+      for (int l = threadIdx.x; l < x.tiles * kBN; l += kThreads) {
+        const int r = row0 + l, tok = r / p.G;
+        float L = INFINITY;                              // a row that is not there, or sees nothing, gives nothing
+        if (r < x.rows) {
+          L = p.lse2[(size_t)(x.t0 + tok) * p.Hq + x.h * p.G + (r - tok * p.G)];
+          if (L == -INFINITY) L = INFINITY;
+        }
+        neg_lse[l] = -L;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      extend::fence_async();
+      __syncthreads();
+      role(x);
     }
   };
   if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
     walk([&](const Pass& x) {
-      if (warp > kMmaWarp) return;
         // -------------------------------------------------------- MMAs
         constexpr uint32_t id = idesc_f16kind(BF, false, kBN);
         const uint32_t lead = extend::elect_one(), tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -240,13 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
         }
     });
   } else if (warp >= kSumWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
     walk([&](const Pass& x) {
         // -------------------------------------------------------- K tiles: 16 keys of every block per warp
         const int ch = warp - kSumWarps;
         const uint32_t tile = smem_u32(smem + SM::kOffK) + ch * 2048;
         bool ok = true;
-        uint4 v[extend::kSteps];
+        constexpr bool kTwice = W16 && D == 128;         // 16-bit rows of 128 dims: a chunk is twice as many vectors
+        uint4 v[extend::kSteps], v2[kTwice ? extend::kSteps : 1];
         const uint8_t* src = nullptr;
         int codec = -1, rows = 0;
         float ks = 0.f;
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
           f_state = -1;
           f_ks = -1.f;
           const int blk = x.blk0 + (int)(n - x.n0) + lane, key = blk * kBM + ch * 16;
-          if (blk < x.blk1 && key < x.s.len) {
+          if (blk < x.blk0 + x.n_blk && key < x.len) {
             const int page = (int)((uint32_t)key / (uint32_t)p.P), row = key - page * p.P;
             const size_t e = (size_t)x.b * p.max_pages + page;
             const int k = p.page_codec[e];
@@ -275,19 +281,23 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
             }
           }
         };
-        // block n's chunk on its way: all of it, or the first half of 16-bit rows of 128 dims
+        // block n's chunk on its way
         auto fetch = [&](uint32_t n) {
           codec = -1;
           if (n >= x.n0 + x.n_blk) return;
-          if ((n - x.n0) % 32 == 0) look(n);
-          const int from = (n - x.n0) % 32;
+          const int from = (int)((n - x.n0) % 32);
+          if (from == 0) look(n);
           codec = __shfl_sync(0xffffffffu, f_state, from);
           src = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, f_src, from));
           ks = __shfl_sync(0xffffffffu, f_ks, from);
           rows = 16;                                     // a chunk's page is whole
           if (codec < 0) return;
-          if (W16 && codec <= ARGUS_BF16) extend::load_steps<D, D / 8>(v, src, lane, 0);
-          else extend::load_steps<D, D / 16>(v, src, lane, 0);
+          if (W16 && codec <= ARGUS_BF16) {
+            extend::load_steps<D, D / 8>(v, src, lane, 0);
+            if constexpr (kTwice) extend::load_steps<D, D / 8>(v2, src, lane, extend::kSteps);
+          } else {
+            extend::load_steps<D, D / 16>(v, src, lane, 0);
+          }
         };
         fetch(x.n0);
         for (uint32_t n = x.n0; n < x.n0 + x.n_blk; ++n) {
@@ -299,10 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
           if (codec >= 0) {
             if (W16 && codec <= ARGUS_BF16) {
               extend::store_steps<D, BF, ARGUS_BF16>(v, to, lane, rows, 0);
-              if (D == 128) {
-                extend::load_steps<D, D / 8>(v, src, lane, extend::kSteps);
-                extend::store_steps<D, BF, ARGUS_BF16>(v, to, lane, rows, extend::kSteps);
-              }
+              if constexpr (kTwice) extend::store_steps<D, BF, ARGUS_BF16>(v2, to, lane, rows, extend::kSteps);
             } else if (codec == ARGUS_INT8) {
               extend::store_steps<D, BF, ARGUS_INT8>(v, to, lane, rows, 0);
             } else {
@@ -318,73 +325,81 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
         if (!ok) misc[1] = 1;
     });
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
     walk([&](const Pass& x) {
         // -------------------------------------------------------- sums
-        const int grp = warp / 4, tl = threadIdx.x & 127;   // half of the columns; key within the block
+        const int grp = warp / 4, tl = threadIdx.x & 127;   // its share of the columns; key within the block
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-        const int shift = x.s.len - x.s.rows / p.G;          // causal: token i sees keys <= shift + i
+        const int shift = x.len - x.rows / p.G;          // causal: token i sees keys <= shift + i
         float* out = p.weights + ((size_t)x.b * p.Hkv + x.h) * p.row_len;
         bool ok = true;
         for (uint32_t n = x.n0; n < x.n0 + x.n_blk; ++n) {
           const int key = (x.blk0 + (int)(n - x.n0)) * kBM + tl;
           // by a later pass the sum so far, which this thread wrote
-          const bool writes = grp == 0 && key < x.s.len;
+          const bool writes = grp == 0 && key < x.len;
           const float old = writes && (x.tile0 > 0 || p.decay != 0.f) ? out[key] : 0.f;
-          // the first row that sees the key
-          const long long need = p.causal ? max(0ll, ((long long)key - shift) * p.G) : 0;
-          float sum = 0.f, sum1 = 0.f, f = 0.f;
+          // the first row that sees the key: a token for each key behind the first token's
+          const int need = p.causal ? min(max(key - shift, 0), x.rows / p.G) * p.G : 0;
+          float sum = 0.f, f = 0.f;
           for (int t = 0; t < x.tiles; ++t) {
             const uint32_t i = x.i0 + (n - x.n0) * x.tiles + t, sb = i % kTiles;
             ok = __all_sync(0xffffffffu, extend::wait(&s_full[sb], i / kTiles & 1, &misc[1]));
             if (!ok) break;
             tc_fence_after();
-            uint32_t u[4][16];
+            uint32_t u[kCols / 16][16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld16(tmem + lanes + kBN * sb + 64 * grp + 16 * c, u[c]);
+            for (int c = 0; c < kCols / 16; ++c) tmem_ld16(tmem + lanes + kBN * sb + kCols * grp + 16 * c, u[c]);
             if (t == 0) f = scales[n % kScales * 8 + tl / 16];   // the block's K tile was full
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_free[sb]);
             const float m = f * p.scale_log2;
-            const int col = x.tile0 * kBN + t * kBN + 64 * grp;
-            const float4* L = reinterpret_cast<const float4*>(neg_lse + t * kBN + 64 * grp);
+            const int col = x.tile0 * kBN + t * kBN + kCols * grp;
+            const float4* L = reinterpret_cast<const float4*>(neg_lse + t * kBN + kCols * grp);
             const bool edge = __any_sync(0xffffffffu, need > col);
-            const int hidden = (int)min(max(need - col, 0ll), 64ll);   // columns in front of the first that sees the key
+            const int hidden = need - col;   // columns in front of the first that sees the key
+            // sixteen columns at a time: a chain of sums through all of them would be waited for
+            auto run = [&](auto masked) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+              for (int c = 0; c < kCols / 16; ++c) {
+                float q[16];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 l4 = L[4 * c + e];
-                float a0, a1, a2, a3;
-                const float *y = reinterpret_cast<const float*>(&u[c][4 * e]);
-                f2_fma(a0, a1, y[0], y[1], m, m, l4.x, l4.y);
-                f2_fma(a2, a3, y[2], y[3], m, m, l4.z, l4.w);
-                a0 = fast_exp2(a0);
-                a1 = fast_exp2(a1);
-                a2 = fast_exp2(a2);
-                a3 = fast_exp2(a3);
-                if (edge) {
-                  const int at_col = 16 * c + 4 * e;
-                  a0 = at_col >= hidden ? a0 : 0.f;
-                  a1 = at_col + 1 >= hidden ? a1 : 0.f;
-                  a2 = at_col + 2 >= hidden ? a2 : 0.f;
-                  a3 = at_col + 3 >= hidden ? a3 : 0.f;
+                for (int e = 0; e < 4; ++e) {
+                  const float4 l4 = L[4 * c + e];
+                  const float* y = reinterpret_cast<const float*>(&u[c][4 * e]);
+                  q[4 * e] = fmaf(y[0], m, l4.x);
+                  q[4 * e + 1] = fmaf(y[1], m, l4.y);
+                  q[4 * e + 2] = fmaf(y[2], m, l4.z);
+                  q[4 * e + 3] = fmaf(y[3], m, l4.w);
                 }
-                f2_add(sum, sum1, sum, sum1, a0, a1);
-                f2_add(sum, sum1, sum, sum1, a2, a3);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  q[e] = fast_exp2(q[e]);
+                  if (decltype(masked)::value) q[e] = 16 * c + e >= hidden ? q[e] : 0.f;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) {
+#pragma unroll
+                  for (int e = 0; e < o; ++e) q[e] += q[e + o];
+                }
+                sum += q[0];
               }
-            }
+            };
+            if (edge) run(std::true_type{});
+            else run(std::false_type{});
           }
-          sum += sum1;
-          if (grp == 1) half[(n & 1) * kBM + tl] = sum;
+          float* mine = half + (n & 1) * (kGroups - 1) * kBM + tl;
+          if (grp > 0) mine[(grp - 1) * kBM] = sum;
           if (extend::group_bar_any(1, kSumWarps * 32, !ok)) {   // all leave, or none
             ok = false;
             break;
           }
           // a chunk that cannot be read adds nothing, whatever its tile held
-          if (writes) out[key] = fmaf(x.tile0 > 0 ? 1.f : p.decay, old, f < 0.f ? 0.f : sum + half[(n & 1) * kBM + tl]);
+          if (writes) {
+#pragma unroll
+            for (int g = 0; g < kGroups - 1; ++g) sum += mine[g * kBM];
+            out[key] = fmaf(x.tile0 > 0 ? 1.f : p.decay, old, f < 0.f ? 0.f : sum);
+          }
         }
         if (!ok) misc[1] = 1;
     });
