@@ -734,6 +734,7 @@ argus_status argus_attn_weights(const argus_extend_args* args, float* weights, i
  * (code * scale in fp32, and so on); a 16-bit dst takes it as it is (same type) or rounded;
  * FP8 and INT8 as argus_quantize_pages does, with a scale per new page, KV head and K | V from the
  * rows kept in it.
+ * A sequence that goes on is appended to 16-bit pages: 8-bit ones suit budgets of whole pages.
  * Out of place: what the old pages hold is not changed (they may be shared), and dst_table names
  * no page that the call reads, and no page twice; dst may be one of `pools`.  Giving the old pages back, and
  * entering the new ones in table and counts, is the caller's.

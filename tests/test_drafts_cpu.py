@@ -139,7 +139,7 @@ def _evict(**kw):
     (dict(pools=[(argus.INT2_G32, 0, 64, None, 4)]), INVALID), (dict(lens=None), INVALID), (dict(out=None), INVALID), (dict(weights=None), INVALID),
     (dict(page_codec=None), INVALID), (dict(table=None), INVALID), (dict(kept=None), INVALID), (dict(dst_table=None), INVALID), (dict(w_out=None), INVALID),
     (dict(out=64), INVALID), (dict(kept=64), INVALID), (dict(w_out=64 + 1532), INVALID), (dict(kept=(3 << 20) + 8), INVALID), (dict(out=(2 << 20) + 956), INVALID),
-    (dict(dst_table=(1 << 20) + 8), INVALID), (dict(batch=60000, budget=10 ** 6, dst_pages=10 ** 5, row_out=10 ** 6), UNSUPPORTED)])
+    (dict(dst_table=(1 << 20) + 8), INVALID), (dict(g=argus.geom(65535, 65535, 128, 16), batch=1, budget=10 ** 6, dst_pages=10 ** 5, row_out=10 ** 6), UNSUPPORTED)])
 def test_evict_refusals(kw, status):
     assert _evict(**kw) == status
 
@@ -245,14 +245,15 @@ static int evict(void) {
 }
 static int norm(void) { const argus_rope_args a = rope_args(); return argus_norm_rope_append(&a, 0, 0, 1e-6f, 0); }
 static int weigh(void) { argus_extend_args a = ext(&pool); return argus_attn_weights(&a, (void*)(4 << 20), 1600, 1.f, 0); }
+static int step(void) { argus_extend_args a = ext(&pool); a.total_q = 2; return argus_attn_weights(&a, (void*)(4 << 20), 1600, 1.f, 0); }
 static int accept_(void) {
   argus_geom g = {8, 2, 128, 16};
   argus_pool p = {ARGUS_FP16, 0, (void*)64, 0, 400};
   return argus_accept_tokens(&g, 2, &p, (void*)64, (void*)64, 100, (void*)64, (void*)64, (void*)64, 4, (void*)64, (void*)(1 << 20), 0, 0);
 }
 int main(void) {
-  int (*calls[])(void) = {window, tree, evict, norm, weigh, accept_};
-  for (int c = 0; c < 6; ++c)
+  int (*calls[])(void) = {window, tree, evict, weigh, norm, accept_, step};
+  for (int c = 0; c < 7; ++c)
     for (int at = -1; at < 2; ++at) {
       fail_at = at; launches = 0; last = 0;
       const int st = calls[c]();
@@ -266,11 +267,11 @@ int main(void) {
 
 def test_a_refused_launch_ends_the_call_and_leaves_no_error(tmp_path):
     """The join reads what the attention describes, the gathering what the selection keeps: without the first kernel the
-    second must not be launched."""
+    second must not be launched; of the weights' two kernels each has sequences of its own, but one refused ends the call."""
     got = run_with_fakes(LAUNCHES, tmp_path)
     two = [(0, 2, 0), (4, 1, 0), (4, 2, 0)]
     one = [(0, 1, 0), (4, 1, 0), (0, 1, 0)]
-    assert got == two * 3 + one * 3
+    assert got == two * 4 + one * 3
 
 
 # ---- oracle pins
