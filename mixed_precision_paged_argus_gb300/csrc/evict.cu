@@ -389,6 +389,13 @@ __device__ __forceinline__ float2 pair_values(uint32_t h) {
 // order, and so do the bits of magnitudes.
 template <int SRC>
 __device__ __forceinline__ float largest(const uint32_t (&h)[8], float s) {
+  if constexpr (SRC != ARGUS_BF16) {
+    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&h[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&h[i])));
+    const float2 y = __half22float2(m);
+    return fabsf(fmaxf(y.x, y.y) * s);
+  }
   uint32_t m = h[0] & 0x7FFF7FFFu;
 #pragma unroll
   for (int i = 1; i < 8; ++i) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(h[i] & 0x7FFF7FFFu));

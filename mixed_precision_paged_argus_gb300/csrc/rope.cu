@@ -131,15 +131,25 @@ __device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, bool far, float 
   const Eight v = eight(wa), w = eight(wb);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float2 p = unpack2<BF>(a[j]), q = unpack2<BF>(b[j]);
-    if (BF && far) {
-      p = make_float2(p.x * pre, p.y * pre);
-      q = make_float2(q.x * pre, q.y * pre);
+    const float2 p = unpack2<BF>(a[j]), q = unpack2<BF>(b[j]);
+    x[2 * j] = p.x;
+    x[2 * j + 1] = p.y;
+    y[2 * j] = q.x;
+    y[2 * j + 1] = q.y;
+  }
+  if (BF && far) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      x[j] *= pre;
+      y[j] *= pre;
     }
-    x[2 * j] = p.x * r * v.v[2 * j];
-    x[2 * j + 1] = p.y * r * v.v[2 * j + 1];
-    y[2 * j] = q.x * r * w.v[2 * j];
-    y[2 * j + 1] = q.y * r * w.v[2 * j + 1];
+  }
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {                       // r first: it brings the values to a few units
+    f2_mul(x[j], x[j + 1], x[j], x[j + 1], r, r);
+    f2_mul(y[j], y[j + 1], y[j], y[j + 1], r, r);
+    f2_mul(x[j], x[j + 1], x[j], x[j + 1], v.v[j], v.v[j + 1]);
+    f2_mul(y[j], y[j + 1], y[j], y[j + 1], w.v[j], w.v[j + 1]);
   }
   if (u >= 0) {
     const Eight c = eight(cs + 8 * u), s = eight(sn + 8 * u);
@@ -154,10 +164,13 @@ __device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, bool far, float 
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float p = x[j];
-        x[j] = p * c.v[j] - y[j] * s.v[j];
-        y[j] = y[j] * c.v[j] + p * s.v[j];
+      for (int j = 0; j < 8; j += 2) {
+        float t[2], z[2];
+        f2_mul(t[0], t[1], y[j], y[j + 1], s.v[j], s.v[j + 1]);
+        f2_mul(z[0], z[1], x[j], x[j + 1], s.v[j], s.v[j + 1]);
+        f2_mul(x[j], x[j + 1], x[j], x[j + 1], c.v[j], c.v[j + 1]);
+        f2_sub(x[j], x[j + 1], x[j], x[j + 1], t[0], t[1]);
+        f2_fma(y[j], y[j + 1], y[j], y[j + 1], c.v[j], c.v[j + 1], z[0], z[1]);
       }
     }
   }
@@ -171,15 +184,14 @@ __device__ __forceinline__ void norm_pair(uint4& a4, uint4& b4, bool far, float 
 template <bool BF>
 __device__ __forceinline__ float squares(const uint4& a4, bool far, float pre) {
   const uint32_t* a = reinterpret_cast<const uint32_t*>(&a4);
-  float s = 0.f;
+  float s0 = 0.f, s1 = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     float2 x = unpack2<BF>(a[j]);
     if (far) x = make_float2(x.x * pre, x.y * pre);
-    s = fmaf(x.x, x.x, s);
-    s = fmaf(x.y, x.y, s);
+    f2_fma(s0, s1, x.x, x.y, x.x, x.y, s0, s1);
   }
-  return s;
+  return s0 + s1;
 }
 
 template <int D, bool BF, bool NORM>
