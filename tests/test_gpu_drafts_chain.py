@@ -228,3 +228,44 @@ def test_a_servers_steps():
     s.evict(34, 2, 10, W.BF16)                           # ends within a page, or keeps a shorter row whole
     s.append([1, 5, 9], 7)
     s.attend(lambda args, ws: argus.paged_window_extend_attn(args, ws, 30, 1), oracle.window_sees(30, 1))
+
+
+def test_calls_on_two_streams_at_once():
+    """Every operator on two streams together, with outputs (and workspaces) of their own: the bits of calls one by one."""
+    from test_gpu_evict import call as evict, weights as some_weights
+    from test_gpu_extend import make
+    from test_gpu_masks import args_of, tree, words_of
+
+    def steps(seed):
+        c = make(8, 2, 128, 16, [900, 40, 333], [9, 40, 33], [W.BF16, W.FP8_E4M3], W.BF16, seed=seed)
+        mask = words_of([tree(n, n) for n in c.new], 2)
+        results = []
+
+        def run(stream):
+            args, ws, out, lse = args_of(c)
+            args2, ws2, out2, lse2 = args_of(c)
+            w = torch.zeros((3, 2, c.max_pages * 16), device=DEV)
+            torch.cuda.synchronize()
+            for _ in range(3):
+                argus.paged_window_extend_attn(args, ws, 100, 4, stream=stream)
+                argus.paged_tree_attn(args2, ws2, mask, stream=stream)
+                argus.attn_weights(args, w, 0.0, stream=stream)
+            return out, lse, out2, lse2, w
+        return c, run, results
+
+    cases = [steps(900), steps(901)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    alone = []
+    for c, run, _ in cases:
+        got = run(torch.cuda.current_stream())
+        torch.cuda.synchronize()
+        alone.append([x.clone() for x in got])
+    together = [run(s) for (_, run, _), s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for a, t in zip(alone, together):
+        for x, y in zip(a, t):
+            assert torch.equal(x, y)
+    refs = [evict(c, some_weights(c, 3), 200, 4, 50, W.FP8_E4M3) for c, _, _ in cases]
+    for s, (c, _, _), r in zip(streams, cases, refs):
+        e = evict(c, some_weights(c, 3), 200, 4, 50, W.FP8_E4M3, stream=s)
+        assert torch.equal(e.kept, r.kept) and torch.equal(e.w, r.w) and torch.equal(e.dst.meta, r.dst.meta) and torch.equal(e.dst.codes, r.dst.codes)
