@@ -516,7 +516,8 @@ def _pool_array(pools, device=None, g=None):
 def extend_args(g, q, q_start, pools, page_codec, block_table, seq_lens, max_pages, softmax_scale, out,
                 causal=True, lse2_out=None, status=None):
     """Build an argus_extend_args struct: q [total_q][Hq][D] (its tokens may lie
-    apart), q_start [B + 1], seq_lens [B], out like q and dense."""
+    apart), q_start [B + 1], seq_lens [B], out like q and dense (None for attn_weights, which
+    reads lse2_out)."""
     batch, total, hq, dev = q_start.numel() - 1, q.shape[0], g.n_q_heads, q.get_device()
     arr = _pool_array(pools, dev, g)
     a = ExtendArgs.from_buffer_copy(_EXTEND_ARGS.pack(

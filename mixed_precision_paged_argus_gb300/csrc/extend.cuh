@@ -49,6 +49,15 @@
 // load_q and the epilogue (unrolled as far as registers allow, mixed tiers took 259 us and cross
 // attention over 1 to 1,500 INT8 states 53; it takes 49).  Sums kept apart for far V
 // scales are 1 to 3% of that (mixed tiers 240, cross 48 without them).
+//
+// With a window a tile's blocks are those of the first tokens and those of the window; the blocks between are skipped
+// in the work list in closed form, chunks that no row sees are not read, and only the blocks at the ends are
+// masked, by 16 bits per chunk.  With a tree only the blocks that hold drafted tokens look at the mask, two words
+// per chunk and row.  Measured: a chunk of 2,048 tokens over 65,536 FP8 tokens, window 4,096 and 64 first tokens, 16/2 heads of
+// 128: 111 us (630 TFLOP/s; per-item cost: 34 blocks of 1.2 us each); BF16, FP8 and INT8 mixed, 8
+// sequences of up to 16,384 with 1 to 256 tokens, window 1,024: 78 us; trees of 8 to 64 tokens of 32 sequences of 2,048 to
+// 16,384 FP8 tokens, 32/8 heads of 128: 303 us (744 TFLOP/s; 1.6 tiles per KV head, each reads the pages, mostly from DRAM
+// again: the CTAs' sequences together are larger than the L2); 26 tokens over 4,096: 26 us in a graph.  The plain form is within 1% of what it was before.
 #pragma once
 
 #include <type_traits>

