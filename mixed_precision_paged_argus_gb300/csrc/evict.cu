@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
   for (int i = m + tid; i < p.budget; i += all) kept[i] = -1;
   float* w_out = p.weights_out + row * p.row_len_out;
   for (long long i = m + tid; i < p.row_len_out; i += all) w_out[i] = 0.f;
+  if (p.budget == 0) return;
   if (len <= p.budget) {                               // the same in the whole cluster
     for (int i = tid; i < m; i += all) kept[i] = i;
     return;

@@ -222,3 +222,52 @@ def test_random_batches(seed):
     if int(c.q_start[-1]) == 0:
         return
     check(c, bool(rng.integers(0, 2)), float(rng.choice([0.0, 0.7, 1.0])))
+
+
+def test_one_sequence_asks_for_all():
+    """No more tokens than sequences, all of one: its many rows go through the kernel of decode steps."""
+    for n_q in (5, 30):
+        c = make(8, 2, 128, 16, [200] + [40, 0, 17] * 10, [n_q] + [0] * 30, [F8, W.BF16], W.BF16, seed=192)
+        spoil_tails(c)
+        check(c, decay=0.5)
+
+
+@pytest.mark.parametrize("L,n_q,codec", [(300000, 1, F8), (100000, 32, F8), (70000, 40, W.BF16), (300000, 1, W.BF16)])
+def test_long_sequences(L, n_q, codec):
+    """More chunks and blocks per warp and CTA than are looked up at once; against a dense computation in 64 bits."""
+    Hq, Hkv, D, P = 16, 8, 128, 64
+    pages = -(-L // P)
+    gen = torch.Generator(device=DEV).manual_seed(L + n_q)
+    rand = lambda *s: torch.randn(s, generator=gen, device=DEV)  # noqa: E731
+    if codec == F8:
+        codes = (rand(pages, 2, Hkv, P, D) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        meta = 0.008 + 0.004 * torch.rand((pages, 2, Hkv), generator=gen, device=DEV)
+    else:
+        codes, meta = rand(pages, 2, Hkv, P, D).bfloat16(), None
+    pool = argus.Pool(codec, codes, meta, pages)
+    q = rand(n_q, Hq, D).bfloat16()
+    table = torch.randperm(pages, generator=gen, device=DEV).to(torch.int32)[None].contiguous()
+    args_of_ = lambda lse: argus.extend_args(  # noqa: E731
+        argus.geom(Hq, Hkv, D, P), q, torch.tensor([0, n_q], dtype=torch.int32, device=DEV), [pool],
+        torch.full((1, pages), codec, dtype=torch.uint8, device=DEV), table, torch.tensor([L], dtype=torch.int32, device=DEV), pages, D ** -0.5, None,
+        lse2_out=lse)
+    ref, bound = torch.empty((Hkv, L), dtype=torch.float64, device=DEV), torch.empty((Hkv, L), dtype=torch.float64, device=DEV)
+    lse = torch.empty((n_q, Hq), device=DEV)
+    see = torch.arange(L, device=DEV)[None] <= L - n_q + torch.arange(n_q, device=DEV)[:, None]
+    for h in range(Hkv):
+        k = codes[table[0].long(), 0, h]
+        k = (k.view(torch.float8_e4m3fn).double() * meta[table[0].long(), 0, h].double()[:, None, None] if codec == F8 else k.double()).reshape(-1, D)[:L]
+        x = torch.einsum("ngd,kd->gnk", q[:, 2 * h:2 * h + 2].double(), k) * (D ** -0.5 * 1.4426950408889634)
+        mag = torch.einsum("ngd,kd->gnk", q[:, 2 * h:2 * h + 2].double().abs(), k.abs()) * (D ** -0.5 * 1.4426950408889634)
+        x = x.masked_fill(~see, -float("inf"))
+        L2 = torch.logsumexp(x * 0.6931471805599453, -1) * 1.4426950408889634
+        lse[:, 2 * h:2 * h + 2] = L2.t().float()
+        p = torch.exp2(x - lse[:, 2 * h:2 * h + 2].t().double()[..., None])
+        ref[h] = p.sum((0, 1))
+        e = 0.6931471805599453 * (D * 2.0 ** -23 * mag + 2.0 ** -22 * (x.abs().nan_to_num(posinf=0.0) + L2.abs()[..., None])) + 2.0 ** -21
+        bound[h] = (2 * p * e).sum((0, 1))
+    w = torch.full((1, Hkv, pages * P), 0.25, device=DEV)
+    argus.attn_weights(args_of_(lse), w, 0.5)
+    got = w[0, :, :L].double() - 0.125
+    assert torch.all((got - ref).abs() <= bound + (2 * n_q + 2) * 2.0 ** -24 * (ref + 0.125))
+    assert torch.all(w[0, :, L:] == 0.25)
