@@ -120,7 +120,6 @@ static argus_status params(const argus_extend_args* a, void* ws, size_t ws_bytes
     p.g_mul = (uint32_t)(((1ull << (31 + bits)) + p.G - 1) / p.G);
     p.g_shift = bits - 1;
   }
-  for (int r = 0; r < 8; ++r) p.last_query[r] = (kBM * (r + 1) - 1) / p.G;
   if (max_blocks(a) / p.n_ctas >= 0x7fffffffll) return fail(ARGUS_E_UNSUPPORTED, "extend: too many key blocks");
   p.ws = static_cast<float*>(ws);
   return ARGUS_OK;
@@ -161,7 +160,6 @@ extern "C" argus_status argus_paged_window_extend_attn(const argus_extend_args* 
   p.window = window_tokens;
   p.sinks = sink_tokens;
   p.sink_blocks = (int)(((long long)sink_tokens + extend::kBN - 1) / extend::kBN);
-  for (int r = 0; r < 8; ++r) p.first_query[r] = extend::kBM * r / std::max(p.G, 1);
   return extend::run<extend::kWindow>(a, p, stream);
 }
 

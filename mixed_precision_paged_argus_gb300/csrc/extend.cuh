@@ -90,8 +90,6 @@ struct EParams {
   uint32_t* status;
   float scale_log2;
   int n_ctas;
-  int last_query[8];                 // (128 (r + 1) - 1) / G: the query of tile r's last row
-  int first_query[8];                // 128 r / G: of its first (kWindow)
   int window, sinks, sink_blocks;    // kWindow: positions that a token sees; blocks of the first `sinks` of the cache
   const uint32_t* tree;              // kTree: [total_q][tree_words], bit j: the sequence's query token j is seen
   int tree_words;
@@ -213,11 +211,16 @@ __device__ __forceinline__ int tile_blocks(const EParams& p, const Seq& s, int t
   return max(1, (keys + kBN - 1) / kBN) - tile_skip<MASK>(p, s, t);
 }
 
-// blocks of tiles 0 .. m-1 (m <= T): under the causal mask G tiles further down
-// are 128 queries, hence exactly one block more; only the last tile may be cut
-// short.  With f = G a + r tiles before it, residue r of the tiles modulo G occurs
-// a times, or a + 1 times below the remainder.  Under a window the same sum over the
-// blocks left out is taken off (skipped_before).
+// Sum over the tiles t < m of floor((x + floor((128 t + e) / G)) / 128), e = 127 for their last rows' queries
+// or 0 for their first ones'.  With x = 128 a + d and t = G u + r a term is a + u, and one more from the residue
+// r = ceil((G (128 - d) - e) / 128) on: G tiles further down are 128 queries.
+__device__ __forceinline__ long long sum_of_blocks(const EParams& p, long long x, int m, int e) {
+  const long long a = x / kBN;
+  const int d = (int)(x % kBN), r0 = (p.G * (kBN - d) + kBN - 1 - e) / kBN, A = group_of(p, m), R = m - A * p.G;
+  return a * m + (long long)A * (A - 1) / 2 * p.G + (long long)A * (R + p.G - r0) + max(0, R - r0);
+}
+// blocks of tiles 0 .. m-1 (m <= T): under the causal mask up to each tile's last query, and only the last
+// tile may be cut short.  Under a window the sum over the blocks left out is taken off.
 __device__ __forceinline__ long long skipped_before(const EParams& p, const Seq& s, int m) {
   // tile t leaves out max(0, floor((c + q(t)) / 128)), q(t) = floor(128 t / G) its first query
   long long c = (long long)s.len - s.n - p.window + 1 - (long long)kBN * p.sink_blocks;
@@ -228,31 +231,13 @@ __device__ __forceinline__ long long skipped_before(const EParams& p, const Seq&
     c += below * kBN;
   }
   if (t0 >= m) return 0;
-  auto sum = [&](int f) {
-    const int a = group_of(p, f), rem = f - a * p.G;
-    long long x = 0;
-#pragma unroll 1
-    for (int r = 0; r < p.G; ++r) {
-      const long long cnt = a + (r < rem);
-      x += cnt * ((c + p.first_query[r]) / kBN) + cnt * (cnt - 1) / 2;
-    }
-    return x;
-  };
-  return sum(m) - sum((int)t0) - below * (m - t0);
+  return sum_of_blocks(p, c, m, 0) - sum_of_blocks(p, c, (int)t0, 0) - below * (m - t0);
 }
 template <int MASK>
 __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& s, int m) {
   if (!p.causal) return (long long)m * tile_blocks<MASK>(p, s, 0);
-  const int T = n_tiles(p, s);
-  const int f = min(m, T - 1);
-  const uint32_t base = (uint32_t)max(s.len - s.n, 0) + kBN;
-  const int a = group_of(p, f), rem = f - a * p.G;
-  long long sum = 0;
-#pragma unroll
-  for (int r = 0; r < 8; ++r) {
-    const int cnt = r < p.G ? a + (r < rem) : 0;
-    sum += (long long)cnt * ((base + (uint32_t)p.last_query[r]) / kBN) + (long long)cnt * (cnt - 1) / 2;
-  }
+  const int T = n_tiles(p, s), f = min(m, T - 1);
+  long long sum = sum_of_blocks(p, (long long)max(s.len - s.n, 0) + kBN, f, kBN - 1);
   if (MASK == kWindow) sum -= skipped_before(p, s, f);
   if (m == T && T > 0) sum += tile_blocks<MASK>(p, s, T - 1);
   return sum;
