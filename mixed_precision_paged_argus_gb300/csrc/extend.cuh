@@ -144,7 +144,8 @@ struct Smem {
   // q_first, q_full[2], k_full[2], pv_ready[2], s_full[2], o_done[2], o_free[2], drain, looked[kBatches], used[kBatches]
   static constexpr int kNumBars = 14 + 2 * kBatches;
   static constexpr int kOffItem = (kOffBar + kNumBars * 8 + 15) / 16 * 16;   // two items' descriptions
-  static constexpr int kOffMisc = kOffItem + 2 * 32;
+  static constexpr int kOffCursor = kOffItem + 2 * 32;                 // two items' cursors (OWN_Q)
+  static constexpr int kOffMisc = kOffCursor + 2 * 48;
   static constexpr int kBytes = kOffMisc + 64;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -694,6 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   using SM = Smem<D>;
   constexpr int kTile = SM::kTile;
   constexpr bool MIXED = BF && W16;          // bf16 or fp16 operands, block by block
+  // Both of a mixed item's tiles are free only when the item before is done.  Then the eight softmax warps load
+  // them in half of the two Q warps' time; under a window items are short, and that counts (mixed tiers under a
+  // window of 1,024: 69 us instead of 74), while long items lose more by the registers it takes (without a window
+  // 256 us instead of 243).
+  constexpr bool OWN_Q = MIXED && MASK == kWindow;
   constexpr float kPBias = 7.f;              // P is stored as P * 2^7 (fp16: at most 2^15)
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {         // the swizzled tiles need it
@@ -752,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   }
   if (threadIdx.x == 64) {
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&q_full[b], kQWarps);
+      mbar_init(&q_full[b], OWN_Q ? kSoftmaxWarps : kQWarps);
       mbar_init(&k_full[b], kLoadWarps / 2);
       mbar_init(&pv_ready[b], kLoadWarps / 2 + kSoftmaxWarps);
       mbar_init(&s_full[b], 1);
@@ -858,6 +864,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       commit_lead(drain, lead);        // TMEM is freed after the MMAs in flight
       wait(drain, 0, &never);
     }
+  } else if (OWN_Q && warp >= kQWarp0) {
+    // the softmax groups load every item's tiles
   } else if (warp >= kQWarp0) {
     // ---------------------------------------------------------- Q tiles
     // From the second item on, an item ahead of the softmax groups (which load the
@@ -951,30 +959,34 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       prefetch_l2(f.src, 16 * rb);
       prefetch_l2(f.src + (long long)p.Hkv * p.P * rb, 16 * rb);
     };
-    // three batches on their way: table entries, scales, and the one handed out
+    // three batches on their way: table entries, scales, and the one handed out; but the first is
+    // handed out at once
     Lookup table = look();
-    Found next = resolve(table);
+    Found now = resolve(table), next = now;
     table = look();
-    for (int k = 0; k * kBatch < n_blocks; ++k) {
-      const Found now = next;
+    for (int k = 0, step = 0; k * kBatch < n_blocks; ++step) {
+      if (step != 1) {
+        if (k >= kBatches && !__all_sync(0xffffffffu, wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
+          misc[1] = 1;
+          break;
+        }
+        const int at = (k % kBatches) * 32 + lane;
+        const unsigned long long addr = reinterpret_cast<unsigned long long>(now.src);
+        // does the block (this lane's group of eight) hold a bf16 page?
+        const unsigned bf16s = __ballot_sync(0xffffffffu, MIXED && now.state && (now.state & 0xFF) <= ARGUS_BF16);
+        const uint32_t wide = (bf16s >> (lane & 24) & 0xFF) != 0;
+        chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), now.state, wide);
+        const float lvs = log2f(now.vs);   // 0: -inf
+        // a scale far from 1: its chunk's sum is kept apart, and does not enter the others'
+        scales[at] = make_float4(now.ks < 0.f ? -1.f : now.ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / now.vs, wide ? 1.f : 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&looked[k % kBatches]);
+        ahead(now);
+        ++k;
+      }
+      now = next;
       next = resolve(table);
       table = look();
-      if (k >= kBatches && !__all_sync(0xffffffffu, wait(&used[k % kBatches], (uint32_t)(k / kBatches - 1) & 1, &misc[1]))) {
-        misc[1] = 1;
-        break;
-      }
-      const int at = (k % kBatches) * 32 + lane;
-      const unsigned long long addr = reinterpret_cast<unsigned long long>(now.src);
-      // does the block (this lane's group of eight) hold a bf16 page?
-      const unsigned bf16s = __ballot_sync(0xffffffffu, MIXED && now.state && (now.state & 0xFF) <= ARGUS_BF16);
-      const uint32_t wide = (bf16s >> (lane & 24) & 0xFF) != 0;
-      chunks[at] = make_uint4((uint32_t)addr, (uint32_t)(addr >> 32), now.state, wide);
-      const float lvs = log2f(now.vs);   // 0: -inf
-      // a scale far from 1: its chunk's sum is kept apart, and does not enter the others'
-      scales[at] = make_float4(now.ks < 0.f ? -1.f : now.ks * p.scale_log2, lvs, fabsf(lvs) > kFarScale ? 0.f : 1.f / now.vs, wide ? 1.f : 0.f);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&looked[k % kBatches]);
-      ahead(now);
     }
   } else if (warp >= kSoftmaxWarps) {
     // ---------------------------------------------------------- loaders
@@ -1055,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
     const uint32_t sO = tO(grp) + lane_off;
     float* merge = reinterpret_cast<float*>(smem + SM::kOffMerge) + grp * 96 * kMergePad;
     int n0 = 0;
-    {
+    if constexpr (!OWN_Q) {
       Cursor<MASK> c;
       c.load(misc + 2, n_blocks);
       if (threadIdx.x == 0) describe_item(0, c, min(c.nb - c.blk, c.left));
@@ -1064,6 +1076,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if (lane == 0) mbar_arrive(q_first);
     }
     for (int k = 0; n0 < n_blocks; ++k) {
+      if constexpr (OWN_Q) {
+        // where this item is was left by the item before
+        volatile uint32_t* cur = reinterpret_cast<volatile uint32_t*>(smem + SM::kOffCursor);
+        Cursor<MASK> c;
+        c.load(k == 0 ? misc + 2 : cur + 12 * (k & 1), n_blocks - n0);
+        const int nb = min(c.nb - c.blk, c.left);
+        if (threadIdx.x == 0) describe_item(k, c, nb);
+        const uint32_t q_s = smem_u32(smem + SM::kOffQ);
+        load_q<D, BF, true>(p, c, q_s, q_s + kTile, q_scale + (k & 1) * kBM, warp, kSoftmaxWarps, lane, k == 0);
+        if (lane == 0) mbar_arrive(k == 0 ? q_first : &q_full[k & 1]);
+        if (threadIdx.x == 0 && c.left > nb) {
+          c.advance(p, nb);
+          c.store(cur + 12 * (~k & 1));
+        }
+        __syncwarp();
+      }
       bool alive = wait_q(k);
       if (group_bar_any(1, kSoftmaxWarps * 32, !alive)) { misc[1] = 1; break; }   // all leave, or none
       const volatile int* it = items + 8 * (k & 1);
