@@ -2,6 +2,7 @@
 // side.  The kernels and what they measured stand in extend.cuh.
 #include <algorithm>
 #include <cmath>
+#include <numeric>
 
 #include "extend.cuh"
 
@@ -159,7 +160,13 @@ extern "C" argus_status argus_paged_window_extend_attn(const argus_extend_args* 
   if (!a->causal) return fail(ARGUS_E_INVALID, "extend: a window needs causal = 1");
   p.window = window_tokens;
   p.sinks = sink_tokens;
-  p.sink_blocks = (int)(((long long)sink_tokens + extend::kBN - 1) / extend::kBN);
+  // A tile's rows belong to at most `tokens` tokens: its first row is a multiple of gcd(128, G) into a token.
+  // The positions that they see behind the first ones, one less than the window and a position per token, touch
+  // at most `chunks` chunks of 16.  (2^24 blocks hold every sequence.)
+  const long long first = ((long long)p.G - std::gcd(extend::kBM, p.G) + extend::kBM - 1) / p.G, tokens = first + 1;
+  const long long chunks = (window_tokens - 1 + tokens + 14) / 16 + 1, sunk = ((long long)sink_tokens + 15) / 16;
+  p.sink_chunks = (int)std::min(sunk, (1ll << 27) - 1);
+  p.window_blocks = (int)std::min((sunk + chunks + 7) / 8, 1ll << 24);
   return extend::run<extend::kWindow>(a, p, stream);
 }
 

@@ -36,8 +36,8 @@
 //    no CTA of the first kernel holds (64,512 of 65,536 registers) any more.
 //
 // Measured (GB300; CUDA events, buffers rotated past the L2): FP8 pages of 16 tokens, 32
-// sequences of 8,192 to 32,768, 1 to 8 drafted tokens, 32/8 heads of 128: 311 to 313 us, 4.6 TB/s
-// of pages (67% of a plain copy; decode reaches 72% on the same pages).  A 1,024-token chunk over
+// sequences of 8,192 to 32,768, 1 to 8 drafted tokens, 32/8 heads of 128: 300 us, 4.8 TB/s
+// of pages (70% of a plain copy; decode reaches 72% on the same pages).  A 1,024-token chunk over
 // 131,072 FP8 tokens, 16/2 heads of 128: 1.02 ms, 1.07 PFLOP/s (56% of cuBLAS bf16);
 // with neither softmax nor MMAs the loads and conversions alone took 0.71 ms, the
 // MMAs alone 0.67 ms.  BF16, FP8 and INT8 pages mixed, 8 sequences of up to 16,384
@@ -50,14 +50,18 @@
 // attention over 1 to 1,500 INT8 states 53; it takes 49).  Sums kept apart for far V
 // scales are 1 to 3% of that (mixed tiers 240, cross 48 without them).
 //
-// With a window a tile's blocks are those of the first tokens and those of the window; the blocks between are skipped
-// in the work list in closed form, chunks that no row sees are not read, and only the blocks at the ends are
-// masked, by 16 bits per chunk.  With a tree only the blocks that hold drafted tokens look at the mask, two words
-// per chunk and row.  Measured: a chunk of 2,048 tokens over 65,536 FP8 tokens, window 4,096 and 64 first tokens, 16/2 heads of
-// 128: 111 us (630 TFLOP/s; per-item cost: 34 blocks of 1.2 us each); BF16, FP8 and INT8 mixed, 8
-// sequences of up to 16,384 with 1 to 256 tokens, window 1,024: 78 us; trees of 8 to 64 tokens of 32 sequences of 2,048 to
-// 16,384 FP8 tokens, 32/8 heads of 128: 303 us (744 TFLOP/s; 1.6 tiles per KV head, each reads the pages, mostly from DRAM
-// again: the CTAs' sequences together are larger than the L2); 26 tokens over 4,096: 26 us in a graph.  The plain form is within 1% of what it was before.
+// With a window a tile's blocks are as many as the first positions and the widest tile's window can fill, in chunks of
+// 16, and the window's chunks follow the first positions' in the same block: what lies between is skipped in the
+// work list in closed form (skipped in whole blocks, window and first positions apart: 69 and 104 us instead of
+// the 62 and 100 below), chunks that no row sees are not read, and only the blocks at the ends are masked, by 16 bits per
+// chunk.  With a tree only the blocks that hold drafted tokens look at the mask, two words per chunk and row.
+// Measured (replayed from a graph): a chunk of 2,048 tokens over 65,536 FP8 tokens, window 4,096 and 64 first
+// tokens, 16/2 heads of 128: 100 us (698 TFLOP/s; 33 blocks an item at 1.2 us each, two to three pieces per
+// CTA); BF16, FP8 and INT8 mixed, 8 sequences of up to 16,384 with 1 to 256 tokens, window 1,024: 62 us; trees
+// of 8 to 64 tokens of 32 sequences of 2,048 to 16,384 FP8 tokens, 32/8 heads of 128: 305 us (740 TFLOP/s; 1.6
+// tiles per KV head, each reads the pages, mostly from DRAM again: the CTAs' sequences together are larger than
+// the L2; every other tile through its blocks from the end, to meet the one before in the L2, was no
+// faster, and a long chunk 2% slower); 26 tokens over 4,096: 20 us.
 #pragma once
 
 #include <type_traits>
@@ -90,7 +94,8 @@ struct EParams {
   uint32_t* status;
   float scale_log2;
   int n_ctas;
-  int window, sinks, sink_blocks;    // kWindow: positions that a token sees; blocks of the first `sinks` of the cache
+  int window, sinks;                 // kWindow: newest positions that a token sees, and first ones of the cache
+  int sink_chunks, window_blocks;    // chunks that hold the first positions; blocks that hold them and any tile's window
   const uint32_t* tree;              // kTree: [total_q][tree_words], bit j: the sequence's query token j is seen
   int tree_words;
   uint32_t g_mul, g_shift;           // division by G (group_of)
@@ -189,15 +194,21 @@ __device__ __forceinline__ int window_begin(const EParams& p, const Seq& s, int 
   const int pos = s.len - s.n + group_of(p, kBM * t);
   return pos < p.window ? 0 : pos - p.window + 1;
 }
-// ... and the blocks between the first tokens' and the window's, which no row of the tile
-// sees: block x of a tile is key block x, or x + tile_skip behind the first tokens'
+// the last query token of tile t
+__device__ __forceinline__ int last_token(const EParams& p, const Seq& s, int t) {
+  return min(group_of(p, (int)((uint32_t)kBM * (t + 1) - 1)), s.n - 1);   // rows: fewer than 2^31
+}
+// kWindow: a tile has at most window_blocks blocks.  Where that is fewer than reach its last key, its chunks
+// behind the first positions' are the last ones in front of that key: chunk x of the tile is chunk x of the
+// sequence, or x + tile_skip from sink_chunks on.  What lies between, no row sees.
 template <int MASK>
 __device__ __forceinline__ int tile_skip(const EParams& p, const Seq& s, int t) {
-  return MASK == kWindow ? max(0, window_begin(p, s, t) / kBN - p.sink_blocks) : 0;
+  return MASK == kWindow ? max(0, (s.len - s.n + last_token(p, s, t) + 16) / 16 - 8 * p.window_blocks) : 0;
 }
+// a tile's first key of a chunk that would be key `key` without the skip
 template <int MASK>
-__device__ __forceinline__ int key_block(const EParams& p, int blk, int skip) {
-  return MASK == kWindow && blk >= p.sink_blocks ? blk + skip : blk;
+__device__ __forceinline__ int key_at(const EParams& p, int key, int skip) {
+  return MASK == kWindow && key >= 16 * p.sink_chunks ? key + 16 * skip : key;
 }
 
 // key blocks of tile t: up to its last row's last key (at least one, so that
@@ -206,40 +217,35 @@ template <int MASK>
 __device__ __forceinline__ int tile_blocks(const EParams& p, const Seq& s, int t) {
   int keys = s.len;
   if (p.causal) {
-    const int last = min(group_of(p, (int)((uint32_t)kBM * (t + 1) - 1)), s.n - 1);   // rows: fewer than 2^31
-    keys = max(s.len - s.n, 0) + last + 1;
+    keys = max(s.len - s.n, 0) + last_token(p, s, t) + 1;
   }
-  return max(1, (keys + kBN - 1) / kBN) - tile_skip<MASK>(p, s, t);
+  const int nb = max(1, (keys + kBN - 1) / kBN);
+  return MASK == kWindow ? min(nb, p.window_blocks) : nb;
 }
 
-// Sum over the tiles t < m of floor((x + floor((128 t + e) / G)) / 128), e = 127 for their last rows' queries
-// or 0 for their first ones'.  With x = 128 a + d and t = G u + r a term is a + u, and one more from the residue
-// r = ceil((G (128 - d) - e) / 128) on: G tiles further down are 128 queries.
-__device__ __forceinline__ long long sum_of_blocks(const EParams& p, long long x, int m, int e) {
+// Sum over the tiles t < m of floor((x + floor((128 t + 127) / G)) / 128), x >= 0, the latter their last rows'
+// queries.  With x = 128 a + d and t = G u + r a term is a + u, and one more from the residue
+// r = ceil((G (128 - d) - 127) / 128) on: G tiles further down are 128 queries.
+__device__ __forceinline__ long long sum_of_blocks(const EParams& p, long long x, int m) {
   const long long a = x / kBN;
-  const int d = (int)(x % kBN), r0 = (p.G * (kBN - d) + kBN - 1 - e) / kBN, A = group_of(p, m), R = m - A * p.G;
+  const int d = (int)(x % kBN), r0 = p.G * (kBN - d) / kBN, A = group_of(p, m), R = m - A * p.G;
   return a * m + (long long)A * (A - 1) / 2 * p.G + (long long)A * (R + p.G - r0) + max(0, R - r0);
 }
 // blocks of tiles 0 .. m-1 (m <= T): under the causal mask up to each tile's last query, and only the last
-// tile may be cut short.  Under a window the sum over the blocks left out is taken off.
-__device__ __forceinline__ long long skipped_before(const EParams& p, const Seq& s, int m) {
-  // tile t leaves out max(0, floor((c + q(t)) / 128)), q(t) = floor(128 t / G) its first query
-  long long c = (long long)s.len - s.n - p.window + 1 - (long long)kBN * p.sink_blocks;
-  long long t0 = 0, below = 0;       // the first tile whose c + q(t) is not negative; multiples of 128 that bring c to 0 or above
-  if (c < 0) {
-    t0 = (-c * p.G + kBN - 1) / kBN;
-    below = (-c + kBN - 1) / kBN;
-    c += below * kBN;
-  }
-  if (t0 >= m) return 0;
-  return sum_of_blocks(p, c, m, 0) - sum_of_blocks(p, c, (int)t0, 0) - below * (m - t0);
-}
+// tile may be cut short.  Under a window no more than window_blocks each, from tile c on.
 template <int MASK>
 __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& s, int m) {
   if (!p.causal) return (long long)m * tile_blocks<MASK>(p, s, 0);
   const int T = n_tiles(p, s), f = min(m, T - 1);
-  long long sum = sum_of_blocks(p, (long long)max(s.len - s.n, 0) + kBN, f, kBN - 1);
-  if (MASK == kWindow) sum -= skipped_before(p, s, f);
+  const long long x = max(s.len - s.n, 0);
+  int c = f;
+  if (MASK == kWindow) {
+    // 128 c + 127 >= G (128 window_blocks - x)
+    const long long rows = p.G * ((long long)kBN * p.window_blocks - x) - 127;
+    c = rows <= 0 ? 0 : (int)min((long long)f, (rows + kBM - 1) / kBM);
+  }
+  long long sum = sum_of_blocks(p, x + kBN, c);
+  if (MASK == kWindow) sum += (long long)(f - c) * p.window_blocks;
   if (m == T && T > 0) sum += tile_blocks<MASK>(p, s, T - 1);
   return sum;
 }
@@ -898,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       for (int x = 0; x < kBatch && c.left > 0; ++x) {
         if (lane / 8 == x) {
           b = c.b;
-          key = key_block<MASK>(p, c.blk, tile_skip<MASK>(p, c.s, c.t)) * kBN + (lane & 7) * 16;
+          key = key_at<MASK>(p, c.blk * kBN + (lane & 7) * 16, tile_skip<MASK>(p, c.s, c.t));
           k.n_rows = min(max(c.s.len - key, 0), 16);
           k.h = c.h;
           k.first = c.h == 0 && c.t == c.T - 1;
@@ -1106,7 +1112,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       // rows behind the last one see what the last one sees: they are never written
       const int tok = min(group_of(p, it[4] * kBM + l_row), it[1] - 1);
       const int vis_last = min(p.causal ? it[2] - it[1] + tok : it[2] - 1, it[2] - 1);
-      // kWindow: the first key of the row's window, and the tile's blocks left out; kTree: the first new key
+      // kWindow: the first key of the row's window, and the tile's chunks left out; kTree: the first new key
       const int vis_first = MASK == kTree ? it[2] - it[1] : MASK == kWindow && vis_last >= p.window ? vis_last - p.window + 1 : 0;
       const int skip = tile_skip<MASK>(p, Seq{it[0], it[1], it[2]}, it[4]);
       const uint32_t* tree = MASK == kTree ? p.tree + (size_t)(it[0] + tok) * p.tree_words : nullptr;
@@ -1133,6 +1139,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       // One block, N chunks of 16 keys per lane, all scores in registers.
       auto block = [&](auto chunks_of, int n, int k0) {
         constexpr int N = decltype(chunks_of)::value;
+        // kWindow: the lane's first chunk may lie further on, and, where the first positions end behind it, the later ones
+        const int past = MASK == kWindow ? 16 * p.sink_chunks - k0 - c0 * 16 : 0;
+        const int near = MASK == kWindow && past <= 0 ? 16 * skip : 0;
+        const int gap = MASK == kWindow && past > 0 && past < N * 16 ? 16 * skip : 0;
         const uint32_t sS = tS(n & 1) + lane_off;
         const float4* sc = scales + (n % kSlots) * 8 + c0;
         const bool wide = MIXED && sc[0].w != 0.f;     // the same for the block's chunks
@@ -1142,10 +1152,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         for (int x = 0; x < N; ++x) tmem_ld16(sS + (c0 + x) * 16, reinterpret_cast<uint32_t(&)[16]>(v[x]));
         // lanes 0 .. N-1 look at their chunk, every lane at its row's last key
         const bool odd = lane < N && (sc[lane].x < 0.f || fabsf(sc[lane].y) > kFarScale);
-        const int lim = vis_last - k0 - c0 * 16;       // keys e <= lim of the lane's are visible
-        const int from = vis_first - k0 - c0 * 16;     // kWindow: and e >= from or e < sunk; kTree: from e = from on as the mask says
-        const int sunk = p.sinks - k0 - c0 * 16;
-        const bool hides = MASK == kTree ? from < N * 16 : lim < N * 16 - 1 || (MASK == kWindow && from > max(sunk, 0));
+        const int lim = vis_last - k0 - c0 * 16 - near;     // keys e <= lim of the lane's are visible
+        const int from = vis_first - k0 - c0 * 16 - near;   // kWindow: and e >= from or e < sunk; kTree: from e = from on as the mask says
+        const int sunk = p.sinks - k0 - c0 * 16 - near;
+        const bool hides = MASK == kTree ? from < N * 16 : lim < N * 16 - 1 || (MASK == kWindow && (gap > 0 || from > max(sunk, 0)));
         const bool edge = __any_sync(0xffffffffu, odd || hides) || apart;
         tmem_wait_ld();
         if (edge) {
@@ -1166,7 +1176,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
             const float kq = sc[x].x * qf, lvc = sc[x].y;
             uint32_t seen = 0xFFFFu;                   // kTree, kWindow: bit e: key e of the chunk
             if (MASK == kTree) seen = tree_bits(tree, p.tree_words, n_new, x * 16 - from);
-            if (MASK == kWindow) seen = below(lim - x * 16 + 1) & (~below(from - x * 16) | below(sunk - x * 16));
+            if (MASK == kWindow) {
+              const int e0 = x * 16 + (x * 16 >= past ? gap : 0);
+              seen = below(lim - e0 + 1) & (~below(from - e0) | below(sunk - e0));
+            }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               v[x][e] = (kq >= 0.f && (MASK == kPlain ? x * 16 + e <= lim : (seen >> e & 1) != 0)) ? v[x][e] * kq : -INFINITY;
@@ -1242,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
         return true;
       };
       for (int i = 0; i < nb; ++i) {
-        const int n = n0 + i, k0 = key_block<MASK>(p, blk0 + i, skip) * kBN;
+        const int n = n0 + i, k0 = (blk0 + i) * kBN;
         if (!__all_sync(0xffffffffu, wait(&s_full[n & 1], (uint32_t)(n >> 1) & 1, &misc[1]))) { alive = false; break; }
         tc_fence_after();
         if (nrep == 4) alive = block(std::integral_constant<int, 1>{}, n, k0);

@@ -96,6 +96,16 @@ def test_windows_and_head_groupings(Hq, Hkv, w, sinks):
     check(c, out, lse, oracle.window_sees(w, sinks))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(3, 1), (5, 1), (14, 2), (8, 1)])
+@pytest.mark.parametrize("w,sinks", [(33, 36), (300, 516), (112, 16), (113, 113), (1, 129)])
+def test_first_positions_that_end_inside_a_block(Hq, Hkv, w, sinks):
+    """The window's chunks follow the first positions' in one block; tokens in front of the cache see nothing."""
+    c = make(Hq, Hkv, 64, 16, [1900, 1153, 640, 90], [260, 33, 1, 200], [W.BF16, F8, I8], W.BF16, seed=645 + Hq)
+    spoil_tails(c)
+    out, lse = window(c, w, sinks)
+    check(c, out, lse, oracle.window_sees(w, sinks))
+
+
 def test_a_window_as_wide_as_the_cache_is_plain_attention():
     from test_gpu_extend import run
     c = make(8, 2, 128, 16, [700, 300], [40, 3], [W.BF16, F8], W.BF16, seed=650)
