@@ -11,21 +11,27 @@
 //
 // Selection: a thread block (or a cluster of them for long rows) per sequence and KV head holds
 // the keys in registers, read once; a round is three compares a key, a reduction within
-// the warps and one over them.  A warp's positions are neighbours, so the ranks that put the kept
+// the warps and one over them.  The first seven rounds count on the keys' first 15 bits, two in a register;
+// once 4,096 keys share T's bits they go to a list of four a lane, and once 128 do one warp goes on alone.
+// A warp's positions are neighbours, so the ranks that put the kept
 // ones in order are ballots and one scan over the warps.
 //
 // Gathering: a warp takes 16 rows of a new page and KV head, looks their places up at once
 // and has K's (then V's) 16-byte vectors on their way together.  8-bit pages have one scale
 // per page, KV head and K | V: a team of warps shares the page's largest magnitude.
 //
-// Measured (GB300, L2 flushed).  16 sequences of 8,192 to 32,768 FP8 tokens to 4,096, 8 KV heads of 128: 106 us;
-// selection 30 us, bound by the instructions of its compares (128 rows, one block each; 71 us with
-// keys loaded one by one and all rounds on all keys, 38 before the late rounds went to a list and
-// positions to 32 bits); gathering 76 us for 268 MB, 3.5 TB/s (53% of a copy), issue slots 45%: converting, and
-// dependent reads that three blocks per SM hide in part (two blocks with V fetched behind K 122 us in all; blocks of four
-// warps 120).  Divisions as the compiler makes them cost 100 us instead of 76, two encodings from both sides of the quotient
-// with a division where they differ 98: rows of the page's largest scale often hit ties.  One sequence of 16,384
-// fp16 tokens to 2,048, 2 KV heads of 64: 24 us, the rounds' barriers (a cluster of eight blocks: 37).
+// Measured (GB300, L2 flushed).  16 sequences of 8,192 to 32,768 FP8 tokens to 4,096, 8 KV heads of 128: 89 us.
+// Selection 21 us (128 rows, one block each): a round over 32 keys a thread takes 1.2 us (1.9 on whole keys), one over the
+// list 0.5 and by one warp 0.25; reading, and the latency of the first loads, 5.  (Before: 71 us with keys loaded one
+// by one and all rounds on all keys; 30 with whole keys, one atomic a warp and key for the list, and the zeros behind the kept
+// weights stored four bytes at a time in front of the loads.  Counting the list's digits by atomics in shared
+// memory, eight bits at once: 26.)  Gathering 67 us for 268 MB, 4.0 TB/s (60% of a copy): converting, and
+// dependent reads that four blocks per SM hide in part (three blocks with the pairs kept in registers instead of the
+// codes 76 us, five 71; two blocks with V fetched behind K 122 us in all; blocks of four warps 120; V's rows fetched
+// to the L2 beside K's, or the kernel launched early: no faster).  Divisions as the compiler makes them cost 24 us more, two
+// encodings from both sides of the quotient with a division where they differ 22: rows of the page's largest
+// scale often hit ties.  One sequence of 16,384 fp16 tokens to 2,048, 2 KV heads of 64: 19 us, the rounds' barriers
+// (a cluster of eight blocks took 13 us longer than one).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -88,9 +94,17 @@ __device__ __forceinline__ uint32_t order(float w) {
 struct Counts {
   uint32_t a, b, c;
 };
+// SMALL: the sums are below 2^16, and two go as one.
+template <bool SMALL>
 __device__ __forceinline__ Counts warp_sum(Counts x) {
-  x.a = __reduce_add_sync(0xffffffffu, x.a);
-  x.b = __reduce_add_sync(0xffffffffu, x.b);
+  if (SMALL) {
+    const uint32_t ab = __reduce_add_sync(0xffffffffu, x.a | x.b << 16);
+    x.a = ab & 0xFFFFu;
+    x.b = ab >> 16;
+  } else {
+    x.a = __reduce_add_sync(0xffffffffu, x.a);
+    x.b = __reduce_add_sync(0xffffffffu, x.b);
+  }
   x.c = __reduce_add_sync(0xffffffffu, x.c);
   return x;
 }
@@ -98,9 +112,10 @@ __device__ __forceinline__ Counts warp_sum(Counts x) {
 // KEYS: a thread's keys, which stay in registers; 0: they are read again in every round.
 template <int KEYS>
 __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p) {
+  constexpr bool kSmall = KEYS > 0;                    // a block's counts are at most 32,768
   __shared__ Counts s_warp[2][kSelWarps];
   __shared__ Counts s_block[2];
-  __shared__ uint32_t s_list[kList], s_listed;
+  __shared__ uint32_t s_list[kList], s_listed, s_close, s_few[2][kSelWarps], s_found[3];
   const cg::cluster_group cluster = cg::this_cluster();
   const int C = gridDim.x, rank = blockIdx.x;          // the cluster spans the grid's first dimension
   const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -109,14 +124,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
   int32_t* kept = p.kept + row * p.budget;
   const int len = length(p, b), m = min(len, p.budget);
   if (threadIdx.x == 0 && rank == 0 && h == 0) p.seq_lens_out[b] = m;
-  // behind the kept positions
   const int tid = rank * kSelThreads + threadIdx.x, all = C * kSelThreads;
-  for (int i = m + tid; i < p.budget; i += all) kept[i] = -1;
-  float* w_out = p.weights_out + row * p.row_len_out;
-  for (long long i = m + tid; i < p.row_len_out; i += all) w_out[i] = 0.f;
-  if (p.budget == 0) return;
-  if (len <= p.budget) {                               // the same in the whole cluster
+  // behind the kept positions
+  auto clear = [&]() {
+    for (int i = m + tid; i < p.budget; i += all) kept[i] = -1;
+    // the weights 16 bytes at a time: up to the first whole vector, the vectors, the rest
+    float* w_out = p.weights_out + row * p.row_len_out;
+    const uintptr_t end = reinterpret_cast<uintptr_t>(w_out + p.row_len_out), from = reinterpret_cast<uintptr_t>(w_out + m);
+    const uintptr_t first = min(end, (from + 15) & ~(uintptr_t)15), last = max(first, end & ~(uintptr_t)15);
+    uint4* to = reinterpret_cast<uint4*>(first) + tid;
+    const uint4* stop = reinterpret_cast<const uint4*>(last);
+    for (; to < stop; to += all) *to = make_uint4(0, 0, 0, 0);
+    if (tid < 4 && from + 4 * tid < first) reinterpret_cast<float*>(from)[tid] = 0.f;
+    if (tid < 4 && last + 4 * tid < end) reinterpret_cast<float*>(last)[tid] = 0.f;
+  };
+  if (p.budget == 0 || len <= p.budget) {              // the same in the whole cluster
     for (int i = tid; i < m; i += all) kept[i] = i;
+    clear();
     return;
   }
   const int lo = p.sinks, hi = len - p.recent, k = p.budget;   // what lies outside lo .. hi-1 is among the k, and less than len are
@@ -132,12 +156,30 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     return pos >= lo && pos < hi ? order(x) : pos < len ? kAlways : 0u;
   };
   uint32_t key[KEYS > 0 ? KEYS : 1];
+  // the first 15 bits of two keys each: the early rounds take less than half of the instructions on these
+  [[maybe_unused]] uint32_t high[KEYS > 0 ? KEYS / 2 : 1];
   if constexpr (KEYS > 0) {
     float x[KEYS];                                     // all on their way at once
+    const bool inner = start - lane >= lo && start - lane + KEYS * 32 <= hi;   // the whole warp's
+    if (inner) {
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) x[i] = load(i);
+      for (int i = 0; i < KEYS; ++i) x[i] = __ldg(w + start + i * 32);
+    } else {
 #pragma unroll
-    for (int i = 0; i < KEYS; ++i) key[i] = key_of(i, x[i]);
+      for (int i = 0; i < KEYS; ++i) x[i] = load(i);
+    }
+    clear();
+    if (inner) {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) key[i] = order(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) key[i] = key_of(i, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < KEYS / 2; ++i) high[i] = prmt(key[2 * i], key[2 * i + 1], 0x7632) >> 1 & 0x7FFF7FFFu;
+  } else {
+    clear();
   }
   auto each = [&](auto f) {
     if constexpr (KEYS > 0) {
@@ -158,9 +200,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     Counts in = {0, 0, 0};
     if (before) {
       in = {lane < warp ? y.a : 0, lane < warp ? y.b : 0, lane < warp ? y.c : 0};
-      in = warp_sum(in);
+      in = warp_sum<kSmall>(in);
     }
-    y = warp_sum(y);
+    y = warp_sum<kSmall>(y);
     if (C > 1) {
       if (threadIdx.x == 0) s_block[t] = y;
       cluster.sync();
@@ -168,10 +210,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
       if (lane < C) z = *cluster.map_shared_rank(&s_block[t], lane);
       if (before) {
         const bool f = lane < rank;
-        const Counts g = warp_sum({f ? z.a : 0, f ? z.b : 0, f ? z.c : 0});
+        const Counts g = warp_sum<false>({f ? z.a : 0, f ? z.b : 0, f ? z.c : 0});
         in = {in.a + g.a, in.b + g.b, in.c + g.c};
       }
-      y = warp_sum(z);
+      y = warp_sum<false>(z);
     }
     if (before) *before = in;
     return y;
@@ -182,10 +224,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     int s = 32;                                        // bits still open
     // two more bits from the counts of keys at or above the three next prefixes; true: the search is over
     auto narrow = [&](Counts c) {
-      if (c.c >= (uint32_t)k) { prefix |= 3u << s; at = c.c; }
-      else if (c.b >= (uint32_t)k) { prefix |= 2u << s; upper = c.c; at = c.b; }
-      else if (c.a >= (uint32_t)k) { prefix |= 1u << s; upper = c.b; at = c.a; }
-      else { upper = c.a; }
+      const bool a = c.a >= (uint32_t)k, b = c.b >= (uint32_t)k, d = c.c >= (uint32_t)k;
+      prefix |= ((uint32_t)a + b + d) << s;
+      upper = d ? upper : b ? c.c : a ? c.b : c.a;
+      at = d ? c.c : b ? c.b : a ? c.a : at;
       return at == (uint32_t)k;
     };
     auto count = [&](Counts& c, uint32_t x) {
@@ -197,35 +239,96 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     while (s > 0 && !exact && at - upper > (uint32_t)kList) {
       s -= 2;
       Counts c = {0, 0, 0};
-      each([&](int, uint32_t x) { count(c, x); });
-      exact = narrow(total(warp_sum(c), nullptr));
+      if (KEYS > 0 && s >= 18) {
+        // per half max(min(x + 1 - t, 1), 0): is x >= t?
+        const auto less = [&](uint32_t d) { return (1u - ((prefix | d << s) >> 17) & 0xFFFFu) * 0x10001u; };
+        const uint32_t ta = less(1), tb = less(2), tc = less(3);
+#pragma unroll
+        for (int i = 0; i < KEYS / 2; ++i) {
+          c.a += __viaddmin_s16x2_relu(high[i], ta, 0x10001u);
+          c.b += __viaddmin_s16x2_relu(high[i], tb, 0x10001u);
+          c.c += __viaddmin_s16x2_relu(high[i], tc, 0x10001u);
+        }
+        c = {(c.a & 0xFFFFu) + (c.a >> 16), (c.b & 0xFFFFu) + (c.b >> 16), (c.c & 0xFFFFu) + (c.c >> 16)};
+      } else {
+        each([&](int, uint32_t x) { count(c, x); });
+      }
+      exact = narrow(total(warp_sum<kSmall>(c), nullptr));
     }
     if (s > 0 && !exact) {
       // the few keys that share the prefix, in any order: the other rounds look at these
-      if (threadIdx.x == 0) s_listed = 0;
+      if (threadIdx.x == 0) s_listed = s_close = 0;
       __syncthreads();
-      each([&](int, uint32_t x) {
-        const bool in = x >> s == prefix >> s;
-        const uint32_t m = __ballot_sync(0xffffffffu, in);
-        if (!m) return;
-        uint32_t to = 0;
-        if (lane == 0) to = atomicAdd(&s_listed, __popc(m));
-        to = __shfl_sync(0xffffffffu, to, 0) + __popc(m & ((1u << lane) - 1));
-        if (in) s_list[to] = x;
+      uint32_t n = 0, to = 0;
+      each([&](int, uint32_t x) { n += x >> s == prefix >> s; });
+      uint32_t upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      if (lane == 31 && upto) to = atomicAdd(&s_listed, upto);
+      to = __shfl_sync(0xffffffffu, to, 31) + upto - n;
+      if (n) each([&](int, uint32_t x) {
+        if (x >> s == prefix >> s) s_list[to++] = x;
       });
       __syncthreads();
-      uint32_t mine[kList / kSelThreads];
+      const int listed = (int)s_listed;
+      int few = C > 1 ? kSelWarps : (listed + 127) / 128;        // warps that go on, with up to four keys a lane
+      if (warp < few) {
+        constexpr int kMine = kList / kSelThreads;
+        static_assert(kMine * 32 < 1 << 10 && kList < 1 << 16, "packed counts");
+        uint32_t mine[kMine], above = upper;
 #pragma unroll
-      for (int i = 0; i < kList / kSelThreads; ++i) mine[i] = i * kSelThreads + threadIdx.x < s_listed ? s_list[i * kSelThreads + threadIdx.x] : 0u;
-      const uint32_t above = upper;
-      while (s > 0 && !exact) {
-        s -= 2;
-        Counts c = {0, 0, 0};
+        for (int i = 0; i < kMine; ++i) mine[i] = i * few * 32 + (int)threadIdx.x < listed ? s_list[i * few * 32 + threadIdx.x] : 0u;
+        while (s > 0 && !exact) {
+          if (C == 1 && few > 1 && at - upper <= 128u) {
+            // few enough for one warp, without barriers
+            uint32_t n = 0;
 #pragma unroll
-        for (int i = 0; i < kList / kSelThreads; ++i) count(c, mine[i]);
-        c = total(warp_sum(c), nullptr);
-        exact = narrow({c.a + above, c.b + above, c.c + above});
+            for (int i = 0; i < kMine; ++i) n += mine[i] >> s == prefix >> s;
+            if (n) {
+              uint32_t to = atomicAdd(&s_close, n);
+#pragma unroll
+              for (int i = 0; i < kMine; ++i)
+                if (mine[i] >> s == prefix >> s) s_list[to++] = mine[i];
+            }
+            asm volatile("bar.sync 1, %0;" ::"r"(few * 32) : "memory");
+            if (warp > 0) break;
+            few = 1;
+            above = upper;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) mine[i] = i * 32 + lane < (int)s_close ? s_list[i * 32 + lane] : 0u;
+          }
+          s -= 2;
+          Counts c = {0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) count(c, mine[i]);
+          if (C > 1) {
+            c = total(warp_sum<true>(c), nullptr);
+          } else {
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, c.a | c.b << 10 | c.c << 20);
+            c = {sum & 0x3FFu, sum >> 10 & 0x3FFu, sum >> 20};
+            if (few > 1) {
+              const int t = s >> 1 & 1;                // the other buffer may still be read
+              if (lane == 0) s_few[t][warp] = sum;
+              asm volatile("bar.sync 1, %0;" ::"r"(few * 32) : "memory");
+              const uint32_t y = lane < few ? s_few[t][lane] : 0u;
+              c = warp_sum<true>({y & 0x3FFu, y >> 10 & 0x3FFu, y >> 20});
+            }
+          }
+          exact = narrow({c.a + above, c.b + above, c.c + above});
+        }
+        if (threadIdx.x == 0) {
+          s_found[0] = prefix;
+          s_found[1] = upper;
+          s_found[2] = exact;
+        }
       }
+      __syncthreads();
+      prefix = s_found[0];
+      upper = s_found[1];
+      exact = s_found[2] != 0;
     }
     // k keys at or above the prefix: all of them; T is not 0, as there are more than k keys above 0
     T = exact ? prefix - 1 : prefix;
@@ -236,7 +339,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const VParams p)
     mine.a += x > T;
     mine.b += x == T;
   });
-  mine = warp_sum(mine);
+  mine = warp_sum<kSmall>(mine);
   Counts before;
   total(mine, &before);
   const uint32_t lt = (1u << lane) - 1;
@@ -450,7 +553,7 @@ __device__ __forceinline__ Place find(const VParams& p, int b, int h, int row0, 
 // everything else reads them twice (from the L2, the second time) and is short, so that both
 // fit the instruction cache.
 template <int D, int DST>
-__global__ void __launch_bounds__(32 * kWarps, 3) gather_kernel(const VParams p, int T, int units) {
+__global__ void __launch_bounds__(32 * kWarps, 4) gather_kernel(const VParams p, int T, int units) {
   constexpr bool kScaled = DST == ARGUS_FP8_E4M3 || DST == ARGUS_INT8;
   constexpr int V = D / 16, RS = 32 / V, STEPS = 16 / RS;   // lanes per row, rows per step
   __shared__ float s_max[2][kWarps];
@@ -496,7 +599,6 @@ __global__ void __launch_bounds__(32 * kWarps, 3) gather_kernel(const VParams p,
     constexpr int SRC = decltype(codec)::value;
 #pragma unroll 1
     for (int kv = 0; kv < 2; ++kv) {
-      uint32_t q[STEPS][8];
       float f[STEPS], top = 0.f;
       Raw<SRC> raw[STEPS];
 #pragma unroll
@@ -507,8 +609,13 @@ __global__ void __launch_bounds__(32 * kWarps, 3) gather_kernel(const VParams p,
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         f[i] = SRC <= ARGUS_BF16 ? 1.f : __shfl_sync(0xffffffffu, s.scale, 16 * kv + i * RS + lane / V);
-        pairs<SRC>(raw[i], q[i]);
-        if (kScaled) top = fmaxf(top, largest<SRC>(q[i], f[i]));
+        if (kScaled) {
+          uint32_t q[8];
+          pairs<SRC>(raw[i], q);
+          top = fmaxf(top, largest<SRC>(q, f[i]));
+          // codes stay in registers, not the pairs, which are twice as many
+          if (SRC > ARGUS_BF16) asm volatile("" : "+r"(raw[i].a.x), "+r"(raw[i].a.y), "+r"(raw[i].a.z), "+r"(raw[i].a.w));
+        }
       }
       [[maybe_unused]] float scale = 1.f, rcp = 1.f;
       if constexpr (kScaled) {
@@ -519,15 +626,17 @@ __global__ void __launch_bounds__(32 * kWarps, 3) gather_kernel(const VParams p,
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
           const long long to = target(tw, kv, i);
+          uint32_t q[8];
+          pairs<SRC>(raw[i], q);
           if constexpr (DST == SRC && !kScaled) {           // as it is
             uint4* d = reinterpret_cast<uint4*>(p.dst_codes + 2 * to);
-            d[0] = make_uint4(q[i][0], q[i][1], q[i][2], q[i][3]);
-            d[1] = make_uint4(q[i][4], q[i][5], q[i][6], q[i][7]);
+            d[0] = make_uint4(q[0], q[1], q[2], q[3]);
+            d[1] = make_uint4(q[4], q[5], q[6], q[7]);
           } else {
             float y[16];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float2 z = pair_values<SRC>(q[i][e]);
+              const float2 z = pair_values<SRC>(q[e]);
               y[2 * e] = z.x;
               y[2 * e + 1] = z.y;
             }

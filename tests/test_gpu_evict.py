@@ -154,6 +154,28 @@ def test_long_rows(L):
         w = -torch.log(w + 1e-3)                         # the range wanders, negative values among them
 
 
+@pytest.mark.parametrize("bits", [6, 10, 14])
+def test_many_weights_that_differ_in_their_last_bits(bits):
+    """More keys share their first bits than the late rounds' list holds."""
+    rng = np.random.default_rng(40 + bits)
+    c = make(2, 1, 64, 64, [20000, 5000], [1, 1], [W.FP16], W.FP16, seed=40)
+    w = (np.float32(1.0).view(np.int32) + rng.integers(0, 1 << bits, (2, 1, c.max_pages * c.P), dtype=np.int32)).view(np.float32)
+    w[0, 0, 5000:5030] = -w[0, 0, 5000:5030]
+    for budget in (1, 333, 4999):
+        check(c, w, budget, 1 if budget > 1 else 0, 0, W.FP16)
+
+
+@pytest.mark.parametrize("extra", [0, 1, 2, 130, 5003])
+def test_weights_behind_the_kept_ones_are_cleared(extra):
+    c = make(4, 2, 64, 16, [700, 0, 33, 50], [1, 1, 1, 1], [W.FP16], W.FP16, seed=44)
+    for budget in (0, 1, 50, 64):
+        w = weights(c, 45)
+        if budget:
+            check(c, w, budget, 0, 0, W.FP16, extra_out=extra)
+        elif extra:
+            assert not call(c, w, 0, 0, 0, W.FP16, extra_out=extra).w.any()
+
+
 def test_pages_without_a_place():
     c = make(4, 2, 64, 16, [400, 130], [1, 1], [F8, I8], W.FP16, seed=170)
     c.table[0, 3], c.table[0, 0], c.table[1, 8] = -1, 10000, -5
