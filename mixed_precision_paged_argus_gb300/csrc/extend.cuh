@@ -58,7 +58,7 @@
 // Measured (replayed from a graph): a chunk of 2,048 tokens over 65,536 FP8 tokens, window 4,096 and 64 first
 // tokens, 16/2 heads of 128: 100 us (698 TFLOP/s; 33 blocks an item at 1.2 us each, two to three pieces per
 // CTA); BF16, FP8 and INT8 mixed, 8 sequences of up to 16,384 with 1 to 256 tokens, window 1,024: 62 us; trees
-// of 8 to 64 tokens of 32 sequences of 2,048 to 16,384 FP8 tokens, 32/8 heads of 128: 305 us (740 TFLOP/s; 1.6
+// of 8 to 64 tokens of 32 sequences of 2,048 to 16,384 FP8 tokens, 32/8 heads of 128: 296 us (763 TFLOP/s; 1.6
 // tiles per KV head, each reads the pages, mostly from DRAM again: the CTAs' sequences together are larger than
 // the L2; every other tile through its blocks from the end, to meet the one before in the L2, was no
 // faster, and a long chunk 2% slower); 26 tokens over 4,096: 20 us.
@@ -164,7 +164,9 @@ struct Smem {
 // be cut anywhere: the pieces are partial softmaxes, joined by the second
 // kernel.  The host knows neither the lengths nor the query counts; every
 // CTA finds its range from them.
-constexpr int kItemCost = 4;
+// Trees, whose last blocks look at the mask, count 5: 296 us for the batch of trees above instead of 305 (3: 309, 6: 297).
+template <int MASK>
+constexpr int kItemCost = MASK == kTree ? 5 : 4;
 struct Seq {
   int q0, n, len;
 };
@@ -253,13 +255,14 @@ __device__ __forceinline__ long long blocks_before(const EParams& p, const Seq& 
 // units of one KV head's tiles 0 .. m-1
 template <int MASK>
 __device__ __forceinline__ long long units_before(const EParams& p, const Seq& s, int m) {
-  return blocks_before<MASK>(p, s, m) + (long long)kItemCost * m;
+  return blocks_before<MASK>(p, s, m) + (long long)kItemCost<MASK> * m;
 }
 
 // a sequence's items, and its blocks
 struct Load {
   long long items, blocks;
-  __device__ __forceinline__ long long units() const { return blocks + kItemCost * items; }
+  template <int MASK>
+  __device__ __forceinline__ long long units() const { return blocks + kItemCost<MASK> * items; }
 };
 template <int MASK>
 __device__ __forceinline__ Load seq_load(const EParams& p, int b) {
@@ -312,7 +315,7 @@ struct Cursor {
       t += k * step;
       n = min(step, n - k * step);
     }
-    blk = (int)max(0ll, rest - units_before<MASK>(p, s, t) - kItemCost);
+    blk = (int)max(0ll, rest - units_before<MASK>(p, s, t) - kItemCost<MASK>);
     nb = tile_blocks<MASK>(p, s, t);
   }
   // the first warp finds a CTA's start for all
@@ -370,7 +373,7 @@ __device__ __forceinline__ Boundary<MASK> find_boundary(const EParams& p, int ct
     sum.blocks += __shfl_xor_sync(0xffffffffu, sum.blocks, o);
   }
   Boundary<MASK> r;
-  r.total = sum.units();
+  r.total = sum.units<MASK>();
   r.n = (int)min((long long)p.n_ctas, r.total);
   r.unit = r.total;
   r.blocks = sum.blocks;
@@ -381,12 +384,12 @@ __device__ __forceinline__ Boundary<MASK> find_boundary(const EParams& p, int ct
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const Load mine = b0 == 0 ? first : b0 + lane < p.B ? seq_load<MASK>(p, b0 + lane) : Load{0, 0};
     const Load incl = {warp_scan(mine.items), warp_scan(mine.blocks)};
-    const unsigned hit = __ballot_sync(0xffffffffu, before.units() + incl.units() > r.unit);
+    const unsigned hit = __ballot_sync(0xffffffffu, before.units<MASK>() + incl.units<MASK>() > r.unit);
     if (hit) {
       const int src = __ffs(hit) - 1;
       before.items += __shfl_sync(0xffffffffu, incl.items - mine.items, src);
       before.blocks += __shfl_sync(0xffffffffu, incl.blocks - mine.blocks, src);
-      r.at.start(p, b0 + src, r.unit - before.units(), 0);
+      r.at.start(p, b0 + src, r.unit - before.units<MASK>(), 0);
       r.blocks = before.blocks + r.at.h * blocks_before<MASK>(p, r.at.s, r.at.T) + blocks_before<MASK>(p, r.at.s, r.at.t) + r.at.blk;
       break;
     }
