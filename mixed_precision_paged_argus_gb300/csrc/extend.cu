@@ -158,6 +158,7 @@ extern "C" argus_status argus_paged_window_extend_attn(const argus_extend_args* 
   if (st != ARGUS_OK) return st;
   if (window_tokens < 1 || sink_tokens < 0) return fail(ARGUS_E_INVALID, "extend: window_tokens must be >= 1 and sink_tokens >= 0");
   if (!a->causal) return fail(ARGUS_E_INVALID, "extend: a window needs causal = 1");
+  if (p.n_ctas == 0) return ARGUS_OK;  // nothing to do: p holds no sizes
   p.window = window_tokens;
   p.sinks = sink_tokens;
   // A tile's rows belong to at most `tokens` tokens: its first row is a multiple of gcd(128, G) into a token.
