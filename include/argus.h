@@ -744,7 +744,8 @@ argus_status argus_attn_weights(const argus_extend_args* args, float* weights, i
  * dst 16-bit, FP8 or INT8 (else ARGUS_E_UNSUPPORTED); all in device memory.  weights device float
  * [B][Hkv][row_len], row_len >= max_pages * P; weights_out [B][Hkv][row_len_out],
  * row_len_out >= budget; kept device int32 [B][Hkv][budget]; dst_table device int32
- * [B][dst_pages], dst_pages * P >= budget >= sink_tokens + recent_tokens.  seq_lens_out, kept
+ * [B][dst_pages], dst_pages * P >= budget >= sink_tokens + recent_tokens, the budget's pages below
+ * 2^31 - 65,536 tokens.  seq_lens_out, kept
  * and weights_out overlap neither an input nor each other (ARGUS_E_INVALID).
  * No workspace.  head_dim 64 or 128; stored values finite.
  * ------------------------------------------------------------------------- */

@@ -792,6 +792,8 @@ extern "C" argus_status argus_evict_tokens(const argus_geom* g, int32_t batch, c
   if (budget < 0 || sink_tokens < 0 || recent_tokens < 0 || (long long)sink_tokens + recent_tokens > budget)
     return fail(ARGUS_E_INVALID, "evict: budget must hold sink_tokens and recent_tokens (all >= 0)");
   if ((long long)dst_pages * g->page_tokens < budget) return fail(ARGUS_E_INVALID, "evict: dst_pages do not hold the budget");
+  if (((long long)budget + g->page_tokens - 1) / g->page_tokens * g->page_tokens > 0x7fffffffll - 65536)
+    return fail(ARGUS_E_UNSUPPORTED, "evict: new pages of 2^31 tokens per sequence or more");
   if (row_len < positions || row_len_out < budget) return fail(ARGUS_E_INVALID, "evict: rows of weights shorter than the cache, or weights_out than the budget");
   if ((long long)g->n_kv_heads > 0x7fffffffll / std::max(1ll, ((long long)budget + g->page_tokens - 1) / g->page_tokens * (g->page_tokens / 16))) return fail(ARGUS_E_UNSUPPORTED, "evict: 2^31 groups of 16 rows or more");
   if (n_pools > 0 && !pools) return fail(ARGUS_E_INVALID, "evict: pools is NULL");

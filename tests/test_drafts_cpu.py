@@ -144,6 +144,13 @@ def test_evict_refusals(kw, status):
     assert _evict(**kw) == status
 
 
+def test_evict_refuses_budgets_whose_pages_pass_32_bits():
+    big = dict(batch=1, row_out=2 ** 31, sinks=0, recent=0, out=1 << 10, w_out=3 << 50, kept=1 << 50, dst_table=4 << 50)
+    assert _evict(budget=2 ** 31 - 1, dst_pages=2 ** 27, **big) == UNSUPPORTED
+    assert _evict(budget=2 ** 31 - 65519, dst_pages=2 ** 27 - 4094, **big) == UNSUPPORTED
+    assert _evict(g=argus.geom(8, 2, 128, 2 ** 30 + 2 ** 29), max_pages=1, row_len=2 ** 31, weights=5 << 50, budget=2 ** 31 - 70000, dst_pages=2, **big) == UNSUPPORTED
+
+
 def test_evict_without_work_is_a_no_op():
     assert _evict(batch=0) == OK
 
