@@ -17,12 +17,14 @@
 //    token's scale and zero are applied per group of 32 dims.
 //  * Two chunks at a time, copied into a ring of the warp's own some steps ahead: their 32 sums
 //    end up in the 32 lanes, one line of weights.
-// Many rows per KV head are weights_rows.cu's.
+// Many rows per KV head are weights_rows.cu's, but not over group codes, whose scales its products cannot carry.
 //
 // Measured (GB300): one token of 32 sequences of 8,192 to 32,768 FP8 tokens, 32/8 heads of 128: 133 to 136 us, 5.3 TB/s
 // (78 to 80% of a plain copy).  On the way: chunks loaded into registers when they were wanted 238 us, a ring of single
 // chunks 168 to 204 (spilled values came back from the L2, as the rings leave the L1 little room), pairs with three
-// blocks of 80 registers per SM 171, with two of 127 as it is.
+// blocks of 80 registers per SM 171, with two of 127 as it is.  11 sequences of 3,736 to 13,632 tokens, 32/8 heads of 128:
+// INT4, one token 24 us, 21 tokens 153 (215 with one tile of rows per pass, 148 with four, in bf16 187 and 190: four
+// cost registers, and with them warps); 4 tokens over 16-bit pages 38 (58 with one).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -254,10 +256,10 @@ __device__ __forceinline__ void scores(const uint32_t (&a)[D / 16][4], const Que
 }
 
 // Some chunks of one (sequence, KV head), and its query rows: they are taken in tiles of eight, and
-// for each tile the chunks pass through the ring once (from the L2, behind the first).
+// for one tile, or two, the chunks pass through the ring once (from the L2, behind the first).
 struct Batch {
   int b, h, c0, n, len;
-  int t0, rows, tiles;                 // first token; its rows by tokens and heads; at least one tile
+  int t0, rows, passes;                // first token; its rows by tokens and heads; at least one pass
 };
 
 // Where a chunk lies.
@@ -275,10 +277,10 @@ struct Walk {
 };
 
 // The next batch, its chunks looked up into the places from `to` on, a lane each.
-template <int D, bool ANY>
+template <int D, bool ANY, int TILES>
 __device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* found, const uint8_t** metas, uint32_t to, int lane) {
   Batch x;
-  x.b = x.h = x.c0 = x.n = x.len = x.t0 = x.rows = x.tiles = 0;
+  x.b = x.h = x.c0 = x.n = x.len = x.t0 = x.rows = x.passes = 0;
   if (w.left <= 0) return x;
   int per;
   for (;;) {                           // there is a chunk ahead: the loop ends at its sequence
@@ -297,7 +299,7 @@ __device__ __forceinline__ Batch next_batch(const WParams& p, Walk& w, Found* fo
   const Span r = rows_of(p, x.b);
   x.t0 = r.t0;
   x.rows = r.rows;
-  x.tiles = max((x.rows + 7) / 8, 1);
+  x.passes = max((x.rows + 8 * TILES - 1) / (8 * TILES), 1);
   if (lane < x.n) {
     Found f = {nullptr, 1.f, -1};
     const uint8_t* meta = nullptr;
@@ -359,8 +361,8 @@ __device__ __forceinline__ float2 weigh(const float (&d)[4], float f0, float f1,
 }
 
 // BF: the queries' (and 16-bit pages') type.  ANY: pages of every codec, else of 8 bits alone, which need
-// fewer registers.  slot: bytes of a ring slot, n_slots of them per warp.
-template <int D, bool BF, bool ANY>
+// fewer registers.  TILES: of eight query rows per pass over the chunks.  slot: bytes of a ring slot, n_slots of them per warp.
+template <int D, bool BF, bool ANY, int TILES>
 __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) weights_kernel(const WParams p, int slot, int n_slots) {
   constexpr int kWarps = Shape<ANY>::kWarps;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -398,18 +400,18 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
   if (lane < n_slots) mbar_init(&full[lane], 1);
   fence_mbar_init();
   __syncwarp();
-  Batch cur = next_batch<D, ANY>(p, walk, found, metas, 0, lane), ahead = next_batch<D, ANY>(p, walk, found, metas, cur.n, lane);
+  Batch cur = next_batch<D, ANY, TILES>(p, walk, found, metas, 0, lane), ahead = next_batch<D, ANY, TILES>(p, walk, found, metas, cur.n, lane);
   uint32_t base = 0;                                     // place of cur's first chunk
-  // the next copies: chunks feed_i and feed_i + 1 for tile feed_t of cur (feed = 0) or ahead (1); 2: all issued
+  // the next copies: chunks feed_i and feed_i + 1 for pass feed_t of cur (feed = 0) or ahead (1); 2: all issued
   int feed = 0, feed_t = 0, feed_i = 0;
   int put = 0, take = 0, flying = 0;                     // next slot to fill and to read, pairs on their way
   uint32_t phase = 0;                                    // of the slots
   auto issue = [&]() {                                   // copies, as far as there are slots
     while (flying < n_slots && feed < 2) {
-      const int n = feed ? ahead.n : cur.n, tiles = feed ? ahead.tiles : cur.tiles;
+      const int n = feed ? ahead.n : cur.n, passes = feed ? ahead.passes : cur.passes;
       if (feed_i >= n) {
         feed_i = 0;
-        if (++feed_t >= tiles) {                         // (no chunks: no tiles)
+        if (++feed_t >= passes) {                        // (no chunks: no passes)
           feed_t = 0;
           ++feed;
         }
@@ -437,14 +439,15 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
     }
   };
   bool ok = true;
-  Query<D> q;
-  Columns col = {};
+  Query<D> q[TILES];
+  Columns col[TILES] = {};
   int have_b = -1, have_h = -1, have_t = -1, have_form = kNone;   // whose rows q and col hold
   while (cur.n > 0 && ok) {
     // the lane's position in a pair of chunks: neighbouring lanes have neighbouring keys' sums
     const int mine = (c >> 1) * 16 + (c & 1) * 8 + (lane >> 2);
     float* out = p.weights + ((size_t)cur.b * p.Hkv + cur.h) * p.row_len;
-    for (int t = 0; t < cur.tiles && ok; ++t) {
+    for (int t = 0; t < cur.passes && ok; ++t) {
+      const int tiles = (cur.rows + 7) / 8 - TILES * t;
       for (int i = 0; i < cur.n; i += 2) {
         issue();
         const int pos = (cur.c0 + i) * 16 + mine;
@@ -467,23 +470,31 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
             have_t = t;
             have_h = cur.h;
             have_b = cur.b;
-            float L;
-            int last;
-            const uint16_t* row = row_of<D>(p, cur, 8 * t + (lane >> 2), L, last);
-            load_query<D, BF, BF>(row, row != nullptr, form, lane, q);
-            col = columns(L, last, lane);
+#pragma unroll
+            for (int u = 0; u < TILES; ++u) {
+              if (u > 0 && u >= tiles) break;
+              float L;
+              int last;
+              const uint16_t* row = row_of<D>(p, cur, 8 * (TILES * t + u) + (lane >> 2), L, last);
+              load_query<D, BF, BF>(row, row != nullptr, form, lane, q[u]);
+              col[u] = columns(L, last, lane);
+            }
           }
           uint32_t a[D / 16][4];
-          float d[4];
-          if (ANY && BF && form == k16) {
-            load_keys<D, BF, ANY>(src, k, lane, a);
-            scores<D, BF>(a, q, form, src + 8 * D, lane, d);
-          } else {
-            load_keys<D, false, ANY>(src, k, lane, a);
-            scores<D, false>(a, q, form, src + 8 * D, lane, d);
-          }
+          const bool wide = ANY && BF && form == k16;
+          if (wide) load_keys<D, BF, ANY>(src, k, lane, a);
+          else load_keys<D, false, ANY>(src, k, lane, a);
           const float f = at.ks * p.scale_log2;
-          s[j] = weigh(d, f * q.fac[0], f * q.fac[1], col, (cur.c0 + i + j) * 16 + (lane >> 2));
+#pragma unroll
+          for (int u = 0; u < TILES; ++u) {
+            if (u > 0 && u >= tiles) break;
+            float d[4];
+            if (wide) scores<D, BF>(a, q[u], form, src + 8 * D, lane, d);
+            else scores<D, false>(a, q[u], form, src + 8 * D, lane, d);
+            const float2 x = weigh(d, f * q[u].fac[0], f * q[u].fac[1], col[u], (cur.c0 + i + j) * 16 + (lane >> 2));
+            s[j].x += x.x;
+            s[j].y += x.y;
+          }
         }
         __syncwarp();                                    // the chunks have been read
         phase ^= 1u << take;
@@ -502,7 +513,7 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
     base += cur.n;
     --feed;                                              // all of cur was issued
     cur = ahead;
-    ahead = next_batch<D, ANY>(p, walk, found, metas, base + cur.n, lane);
+    ahead = next_batch<D, ANY, TILES>(p, walk, found, metas, base + cur.n, lane);
   }
   if (!ok) {
     // a copy did not arrive: the caller is told, and the ones in flight get as long again
@@ -514,7 +525,7 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
   }
 }
 
-template <int D, bool BF, bool ANY>
+template <int D, bool BF, bool ANY, int TILES>
 static argus_status launch(const WParams& p, cudaStream_t s) {
   using S = Shape<ANY>;
   // a slot holds two chunks, 16 rows each, of the widest pages
@@ -522,7 +533,7 @@ static argus_status launch(const WParams& p, cudaStream_t s) {
   const int slot = wide ? 64 * D : 32 * D, n_slots = std::min(kMaxSlots, S::kRing / slot);
   static PerContext configured;
   const argus_status st = configured.ensure([](int) {
-    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<D, BF, ANY>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kWarps * S::kRing);
+    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<D, BF, ANY, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kWarps * S::kRing);
     return e == cudaSuccess ? ARGUS_OK : fail(ARGUS_E_LAUNCH, "weights: smem attribute: %s", cudaGetErrorString(e));
   });
   if (st != ARGUS_OK) return st;
@@ -532,7 +543,7 @@ static argus_status launch(const WParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(32 * S::kWarps);
   cfg.dynamicSmemBytes = S::kWarps * slot * n_slots;
   cfg.stream = s;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, weights_kernel<D, BF, ANY>, p, slot, n_slots);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, weights_kernel<D, BF, ANY, TILES>, p, slot, n_slots);
   if (e == cudaSuccess) return ARGUS_OK;
   cudaGetLastError();                  // not left for the next call to find
   return fail(ARGUS_E_LAUNCH, "argus_attn_weights: launch failed: %s", cudaGetErrorString(e));
@@ -554,8 +565,15 @@ static argus_status launch_d(WParams p, bool bf, cudaStream_t s) {
     const argus_status st = launch_rows(p, D, bf, any, s);
     if (st != ARGUS_OK) return st;
   }
-  if (bf) return any ? launch<D, true, true>(p, s) : launch<D, true, false>(p, s);
-  return any ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
+  const auto go = [&](auto all, auto tiles) {
+    constexpr bool ANY = decltype(all)::value;
+    constexpr int TILES = decltype(tiles)::value;
+    return bf ? launch<D, true, ANY, TILES>(p, s) : launch<D, false, ANY, TILES>(p, s);
+  };
+  if (!any) return go(std::false_type{}, std::integral_constant<int, 1>{});
+  // two tiles of rows per pass where sequences have more than one on average (one of eight rows: 24 us by one, 26 by two)
+  if ((long long)p.total_q * p.G > 8ll * p.B) return go(std::true_type{}, std::integral_constant<int, 2>{});
+  return go(std::true_type{}, std::integral_constant<int, 1>{});
 }
 
 }  // namespace weights

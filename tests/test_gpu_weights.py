@@ -83,6 +83,14 @@ def test_many_rows(n_q, dtype, codecs):
     check(c, decay=0.9)
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 2, 0], [6, 5, 4], [21, 1, 1], [9, 1, 0], [1, 30, 2]])
+@pytest.mark.parametrize("dtype,codecs", [(W.FP16, [W.FP16, W.INT4_G32, F8]), (W.BF16, [W.BF16, W.INT2_G32, I8])])
+def test_uneven_rows_over_group_codes(new, dtype, codecs):
+    """Odd and even numbers of tiles of eight rows, a sequence without rows beside one of many."""
+    c = make(8, 2, 128, 32, [257, 700, 40], new, codecs, dtype, seed=75)
+    check(c, decay=0.9)
+
+
 @pytest.mark.parametrize("length", [1, 15, 16, 17, 127, 128, 129, 511, 512, 513, 1025])
 def test_lengths_around_the_chunks(length):
     for new in (1, min(70, length)):
