@@ -429,14 +429,15 @@ __device__ __forceinline__ void values(const VParams& p, const Place& s, long lo
 template <int DST>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   if (DST == ARGUS_FP8_E4M3) return f32x4_to_e4m3(a, b, c, d);
-  // |y| <= 127: the adder's low bits are the rounded integer
+  // |y| <= 127, or next to it by a rounding: the adder's low bits are the rounded integer
   constexpr float kRound = 12582912.f;
   f2_add(a, b, a, b, kRound, kRound);
   f2_add(c, d, c, d, kRound, kRound);
   return prmt(prmt(__float_as_uint(a), __float_as_uint(b), 0x0040), prmt(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
 }
 // Sixteen codes of y s / scale; rcp = RN(1 / scale), 0 where the scale is so small or large that a step could leave
-// fp32's range.
+// fp32's range.  There an INT8 scale may be a few units of 2^-149, whose rounding takes quotients past 127: they end
+// there (e4m3's conversion saturates).
 template <int DST>
 __device__ __forceinline__ uint4 encode(float (&y)[16], float s, float rcp, float scale) {
 #pragma unroll
@@ -454,7 +455,10 @@ __device__ __forceinline__ uint4 encode(float (&y)[16], float s, float rcp, floa
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
       for (int j = 0; j < 16; ++j)
-        if (j == e) y[j] = scale > 0.f ? y[j] / scale : 0.f;
+        if (j == e) {
+          const float q = scale > 0.f ? y[j] / scale : 0.f;
+          y[j] = DST == ARGUS_INT8 ? fminf(fmaxf(q, -127.f), 127.f) : q;
+        }
     }
   }
   uint32_t o[4];
