@@ -425,7 +425,15 @@ __device__ __forceinline__ void values(const VParams& p, const Place& s, long lo
 // ---- codes of RN(x / scale).  With y = RN(1 / scale) the quotient is q + r y, rounded once, for q = RN(x y)
 // and r = x - q scale, which an FMA gives exactly (P. Markstein, IBM J. Res. Dev. 34, 1990): where it is
 // next to a border between codes, a number of few bits, the quotient is no closer to the middle between
-// two floats than 2^-24 of their distance over scale's mantissa, and r y is off by less.
+// two floats than 2^-24 of their distance over scale's mantissa, and r y is off by less.  r is taken towards -inf, which
+// changes nothing in an exact one but makes a difference of equals -0: so a quotient of -0 keeps its sign.
+__device__ __forceinline__ void f2_fma_down(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rm.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 template <int DST>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
   if (DST == ARGUS_FP8_E4M3) return f32x4_to_e4m3(a, b, c, d);
@@ -447,7 +455,7 @@ __device__ __forceinline__ uint4 encode(float (&y)[16], float s, float rcp, floa
     for (int e = 0; e < 16; e += 2) {
       float q[2], r[2];
       f2_mul(q[0], q[1], y[e], y[e + 1], rcp, rcp);
-      f2_fma(r[0], r[1], q[0], q[1], -scale, -scale, y[e], y[e + 1]);
+      f2_fma_down(r[0], r[1], q[0], q[1], -scale, -scale, y[e], y[e + 1]);
       f2_fma(y[e], y[e + 1], r[0], r[1], rcp, rcp, q[0], q[1]);
     }
   } else {
