@@ -62,9 +62,10 @@ __device__ __forceinline__ uint32_t lds4(uint32_t a) {
   return v;
 }
 
-// A sequence's chunks, KV heads one after the other; those of many rows have none here.
+// A sequence's chunks, KV heads one after the other; those that another kernel takes have none here.
 __device__ __forceinline__ long long chunks_of(const WParams& p, int b) {
-  return rows_of(p, b).rows > p.many ? 0 : (long long)p.Hkv * ((length(p, b) + 15) / 16);
+  const int rows = rows_of(p, b).rows;
+  return rows <= p.few || rows > p.many ? 0 : (long long)p.Hkv * ((length(p, b) + 15) / 16);
 }
 
 // How a page's operands are formed, and with it the order of a row's dims in them.
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
   Found* found = s_found[warp];
   const uint8_t** metas = s_meta[ANY ? warp : 0];
   uint8_t* ring = smem + (size_t)warp * slot * n_slots;
+  if (p.leads) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // this warp's range of chunks
   const int nw = gridDim.x * kWarps, w = blockIdx.x * kWarps + warp;
   const long long first = lane < p.B ? chunks_of(p, lane) : 0;
@@ -382,7 +384,10 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
   total = warp_sum(total);
   const long long u0 = total / nw * w + total % nw * w / nw, u1 = total / nw * (w + 1) + total % nw * (w + 1) / nw;
   Walk walk = {u1 - u0, 0, 0};
-  if (walk.left <= 0) return;
+  if (walk.left <= 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   {
     long long before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -523,10 +528,13 @@ __global__ void __launch_bounds__(32 * Shape<ANY>::kWarps, Shape<ANY>::kBlocks) 
       if (++take == n_slots) take = 0;
     }
   }
+  // who waits for this kernel waits for the call's other one too
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// follows: behind another kernel of the call, which has other sequences: it may start while that one runs.
 template <int D, bool BF, bool ANY, int TILES>
-static argus_status launch(const WParams& p, cudaStream_t s) {
+static argus_status launch(const WParams& p, cudaStream_t s, bool follows) {
   using S = Shape<ANY>;
   // a slot holds two chunks, 16 rows each, of the widest pages
   const bool wide = p.pool[ARGUS_FP16].n_slots > 0 || p.pool[ARGUS_BF16].n_slots > 0;
@@ -543,6 +551,11 @@ static argus_status launch(const WParams& p, cudaStream_t s) {
   cfg.blockDim = dim3(32 * S::kWarps);
   cfg.dynamicSmemBytes = S::kWarps * slot * n_slots;
   cfg.stream = s;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = follows ? 1 : 0;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, weights_kernel<D, BF, ANY, TILES>, p, slot, n_slots);
   if (e == cudaSuccess) return ARGUS_OK;
   cudaGetLastError();                  // not left for the next call to find
@@ -557,23 +570,46 @@ static argus_status launch_d(WParams p, bool bf, cudaStream_t s) {
     any |= k != ARGUS_FP8_E4M3 && k != ARGUS_INT8;
     group |= k >= ARGUS_INT4_G32;
   }
-  // A decode step has as many tokens as sequences.  With more, some sequence has several, and a second
-  // kernel takes those of more than kMany rows; that one knows no group codes.
+  const auto go = [&](auto all, auto tiles, bool follows) {
+    constexpr bool ANY = decltype(all)::value;
+    constexpr int TILES = decltype(tiles)::value;
+    return bf ? launch<D, true, ANY, TILES>(p, s, follows) : launch<D, false, ANY, TILES>(p, s, follows);
+  };
+  const std::integral_constant<int, 1> one;
+  const std::integral_constant<int, 2> two;
+  // A call of as many tokens as sequences is taken for a decode step, with one token each.  In any other, one sequence may
+  // have all the tokens, whatever the average is (idle slots), and the sequences of many rows get a kernel of their own,
+  // beside which the other one may run.  Where no sequence has many it is empty: 2 us of a small step of 16 us, 0 to 2 of
+  // one of 69.  One sequence of 16,384 tokens asks with 32, 63 slots are empty: FP8 25 us (68 without), BF16 26 (85);
+  // the 63 hold 2,000 to 8,192 tokens: FP8 108 (691), BF16 169 (1,214), INT4, with 21 tokens, 184 (1,267).
+  const long long all_rows = (long long)p.total_q * p.G;
+  const bool decode = p.total_q == p.B, more = all_rows > 8ll * p.B;   // more than one tile of rows on average
+  p.few = -1;
   p.many = 0x7fffffff;
-  if (!group && p.total_q > p.B && (long long)p.total_q * p.G > kMany) {
+  if (group && !decode && p.B > 1 && all_rows > 8) {
+    // more than a tile of rows: two tiles per pass, as the large tiles know no group codes; apart from the others
+    // also because a chunk of many rows is many times their work.  The kernel that likely has the fewer sequences
+    // leads.  (A single sequence of 21 tokens: 67 us by one kernel, 71 by two.)
+    const auto part = [&](auto tiles, bool follows) {
+      p.few = decltype(tiles)::value == 2 ? 8 : -1;
+      p.many = decltype(tiles)::value == 2 ? 0x7fffffff : 8;
+      p.leads = !follows;
+      return go(std::true_type{}, tiles, follows);
+    };
+    const argus_status st = more ? part(one, false) : part(two, false);
+    if (st != ARGUS_OK) return st;
+    return more ? part(two, true) : part(one, true);
+  }
+  bool follows = false;
+  if (!group && !decode && all_rows > kMany) {
     p.many = kMany;
     const argus_status st = launch_rows(p, D, bf, any, s);
     if (st != ARGUS_OK) return st;
+    follows = true;
   }
-  const auto go = [&](auto all, auto tiles) {
-    constexpr bool ANY = decltype(all)::value;
-    constexpr int TILES = decltype(tiles)::value;
-    return bf ? launch<D, true, ANY, TILES>(p, s) : launch<D, false, ANY, TILES>(p, s);
-  };
-  if (!any) return go(std::false_type{}, std::integral_constant<int, 1>{});
-  // two tiles of rows per pass where sequences have more than one on average (one of eight rows: 24 us by one, 26 by two)
-  if ((long long)p.total_q * p.G > 8ll * p.B) return go(std::true_type{}, std::integral_constant<int, 2>{});
-  return go(std::true_type{}, std::integral_constant<int, 1>{});
+  if (!any) return go(std::false_type{}, one, follows);
+  // up to kMany rows: two tiles where sequences have more than one on average (one of eight rows: 24 us by one, 26 by two)
+  return more ? go(std::true_type{}, two, follows) : go(std::true_type{}, one, follows);
 }
 
 }  // namespace weights

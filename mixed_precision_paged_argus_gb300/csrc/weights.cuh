@@ -24,7 +24,9 @@ struct WParams {
   float* weights;
   long long row_len;
   float decay, scale_log2;
-  int many;                            // sequences of more query rows per KV head are weights_rows.cu's
+  int few, many;                       // a kernel takes the sequences of more than `few` query rows per KV head and up to `many`;
+                                       // weights_rows.cu's takes those of more than `many`
+  bool leads;                          // another kernel of this call follows, which may be put in place at once
   uint32_t* status;
 };
 

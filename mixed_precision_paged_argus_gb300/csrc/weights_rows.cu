@@ -138,6 +138,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_rows_kernel(const WParams
   float* half = reinterpret_cast<float*>(smem + SM::kOffHalf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  // the other sequences' kernel shares nothing with this one but the caller's status
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 0) {
     long long total = 0;
     for (int b = lane; b < p.B; b += 32) total += p.Hkv * load_seq(p, b).units();
