@@ -282,12 +282,18 @@ __device__ __forceinline__ long long warp_scan(long long x) {   // inclusive
   return x;
 }
 
-// a / b, both >= 0: in 32 bits where they fit
-__device__ __forceinline__ long long divide(long long a, long long b) {
+// a / b, both >= 0: in 32 bits where they fit.  APART: as a function of its own.  The kernel of calls that mix bf16 and
+// 8-bit pages has the longest code, and with four quotients in it loses 1% (mixed tiers 247.5 us instead of 244.8); the
+// others are as fast or faster with them (trees 296.7 instead of 299.4, the long chunk 1,020 instead of 1,022).
+__device__ __forceinline__ long long divide_here(long long a, long long b) {
   return ((unsigned long long)(a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
+static __device__ __noinline__ long long divide_apart(long long a, long long b) { return divide_here(a, b); }
+template <bool APART>
+__device__ __forceinline__ long long divide(long long a, long long b) { return APART ? divide_apart(a, b) : divide_here(a, b); }
 
-__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return divide(total * cta, n_ctas); }
+template <bool APART>
+__device__ __forceinline__ long long range_start(long long total, int cta, int n_ctas) { return divide<APART>(total * cta, n_ctas); }
 
 template <int MASK>
 struct Cursor {
@@ -298,6 +304,7 @@ struct Cursor {
   // the item that unit `rest` of sequence b lies in, and the block there: the
   // units in front of an item's blocks belong to its first.  By a whole warp:
   // 32 tiles are tried per step.
+  template <bool APART>
   __device__ __forceinline__ void start(const EParams& p, int b_, long long rest, int left_) {
     const int lane = threadIdx.x & 31;
     b = b_;
@@ -305,7 +312,7 @@ struct Cursor {
     s = load_seq(p, b);
     T = n_tiles(p, s);
     const long long per = units_before<MASK>(p, s, T);
-    h = (int)divide(rest, per);
+    h = (int)divide<APART>(rest, per);
     rest -= h * per;
     t = 0;                           // the last tile with units before it <= rest
     for (int n = T; n > 1;) {
@@ -357,7 +364,7 @@ struct Boundary {
   int n;                             // CTAs with a range
   Cursor<MASK> at;
 };
-template <int MASK>
+template <int MASK, bool APART>
 __device__ __forceinline__ Boundary<MASK> find_boundary(const EParams& p, int cta) {
   const int lane = threadIdx.x & 31;
   const Load first = lane < p.B ? seq_load<MASK>(p, lane) : Load{0, 0};
@@ -379,7 +386,7 @@ __device__ __forceinline__ Boundary<MASK> find_boundary(const EParams& p, int ct
   r.blocks = sum.blocks;
   r.at = {};
   if (cta >= r.n) return r;
-  r.unit = range_start(r.total, cta, r.n);
+  r.unit = range_start<APART>(r.total, cta, r.n);
   Load before = {0, 0};
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const Load mine = b0 == 0 ? first : b0 + lane < p.B ? seq_load<MASK>(p, b0 + lane) : Load{0, 0};
@@ -389,7 +396,7 @@ __device__ __forceinline__ Boundary<MASK> find_boundary(const EParams& p, int ct
       const int src = __ffs(hit) - 1;
       before.items += __shfl_sync(0xffffffffu, incl.items - mine.items, src);
       before.blocks += __shfl_sync(0xffffffffu, incl.blocks - mine.blocks, src);
-      r.at.start(p, b0 + src, r.unit - before.units<MASK>(), 0);
+      r.at.template start<APART>(p, b0 + src, r.unit - before.units<MASK>(), 0);
       r.blocks = before.blocks + r.at.h * blocks_before<MASK>(p, r.at.s, r.at.T) + blocks_before<MASK>(p, r.at.s, r.at.t) + r.at.blk;
       break;
     }
@@ -704,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   using SM = Smem<D>;
   constexpr int kTile = SM::kTile;
   constexpr bool MIXED = BF && W16;          // bf16 or fp16 operands, block by block
+  constexpr bool APART = MIXED && MASK == kPlain;
   // Both of a mixed item's tiles are free only when the item before is done.  Then the eight softmax warps load
   // them in half of the two Q warps' time; under a window items are short, and that counts (mixed tiers under a
   // window of 1,024: 69 us instead of 74), while long items lose more by the registers it takes (without a window
@@ -744,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp < 2) {
     // the range's begin and end, a warp each
-    const Boundary<MASK> r = find_boundary<MASK>(p, blockIdx.x + warp);
+    const Boundary<MASK> r = find_boundary<MASK, APART>(p, blockIdx.x + warp);
     if (lane == 0) misc64[6 + warp] = r.blocks;
     if (warp == 0) {
       const Cursor<MASK>& c = r.at;
@@ -753,11 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const EParams p) {
       if ((int)blockIdx.x < r.n && c.blk > 0) {
         const long long first = r.unit - c.blk;          // the unit of the item's first block
         // this range begins inside an item's blocks; is it the first to?
-        if (range_start(r.total, blockIdx.x - 1, r.n) <= first) {
+        if (range_start<APART>(r.total, blockIdx.x - 1, r.n) <= first) {
           cut.rows = min(kBM, c.s.n * p.G - c.t * kBM);
           // the last range that starts in front of the item's end: total x / n < end (counted up one by one it took
           // 8 us where one item is spread over 30 CTAs)
-          cut.last = min(r.n - 1, (int)divide((first + c.nb) * r.n - 1, r.total));
+          cut.last = min(r.n - 1, (int)divide<APART>((first + c.nb) * r.n - 1, r.total));
           cut.q0 = c.s.q0;
           cut.row0 = c.t * kBM;
           cut.head0 = c.h * p.G;
