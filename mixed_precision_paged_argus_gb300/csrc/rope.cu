@@ -55,7 +55,7 @@ struct RParams {
   const int32_t* block_table;
   uint32_t* status;
   const float *q_weight, *k_weight;  // [D] or NULL (ones)
-  float eps;
+  float eps_4;                       // a quarter of eps: its sum with a quarter of the mean stays in fp32's range
 };
 
 template <bool BF>
@@ -317,7 +317,7 @@ __device__ __forceinline__ void rope_tokens(const RParams& p, int W) {
             const int u = (it0 + m * 32 * W) % U;
             const bool halves = un[m] >= 0 && !p.adjacent;
             const float* w = s_weight[hw[m]];
-            norm_pair<BF>(a[m], bb[m], far, pre, rsqrtf(ss * (1.f / D) + (pre == 1.f ? p.eps : p.eps * 0x1p-140f)), w + (halves ? 8 : 16) * u,
+            norm_pair<BF>(a[m], bb[m], far, pre, 0.5f * rsqrtf(ss * (0.25f / D) + (pre == 1.f ? p.eps_4 : p.eps_4 * 0x1p-140f)), w + (halves ? 8 : 16) * u,
                           w + (halves ? p.rot / 2 + 8 * u : 16 * u + 8), cs, sn, un[m], p.adjacent);
           }
         }
@@ -478,6 +478,6 @@ extern "C" argus_status argus_norm_rope_append(const argus_rope_args* a, const f
     return fail(ARGUS_E_INVALID, "rope: the norms' weights must be 4-byte aligned");
   p.q_weight = q_weight;
   p.k_weight = k_weight;
-  p.eps = eps;
+  p.eps_4 = 0.25f * eps;
   return rope::run<true>(a, p, stream);
 }
