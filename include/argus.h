@@ -673,7 +673,8 @@ argus_status argus_paged_tree_attn(const argus_extend_args* args, const uint32_t
  * seq_lens[b] < n_b (nothing is moved, seq_lens_out[b] = seq_lens[b]); a token to be moved
  * whose page, or whose new one, is not of the pool (it is not moved; the length counts it).
  * Arguments: path device int32 [B][path_width], n_path device int32 [B]; seq_lens_out
- * device int32 [B], overlapping no input (ARGUS_E_INVALID).  head_dim 64 or 128.
+ * device int32 [B], overlapping none of the other arrays (ARGUS_E_INVALID); that it lies outside
+ * the pool is the caller's to see to, and not checked.  head_dim 64 or 128.
  * ------------------------------------------------------------------------- */
 argus_status argus_accept_tokens(const argus_geom* g, int32_t batch, const argus_pool* pool,
                                  const uint8_t* page_codec, const int32_t* block_table,
@@ -708,9 +709,14 @@ argus_status argus_norm_rope_append(const argus_rope_args* args, const float* q_
  * adds nothing; a NaN in a query row makes the sums that it enters NaN.
  * args as for argus_paged_extend_attn, with these differences: lse2_out is READ (device float
  * [total_q][Hq]); out is not used; pools may be of every codec (16-bit ones of the query's type).
- * weights device float [B][Hkv][row_len], row_len >= max_pages * P, overlapping no input
- * (ARGUS_E_INVALID); decay finite.  A page whose slot lies outside its pool or whose codec
+ * weights device float [B][Hkv][row_len], row_len >= max_pages * P, overlapping neither queries,
+ * log-sums, lengths nor tables (ARGUS_E_INVALID); that it lies outside the pools is the caller's to
+ * see to, and not checked.  decay finite.  A page whose slot lies outside its pool or whose codec
  * has no pool adds nothing and is counted once per sequence in *status.
+ * The rule of sight is that call's alone: log-sums of argus_paged_window_extend_attn or
+ * argus_paged_tree_attn are of other rows of sight, and the sums would not be their weights.
+ * total_q == batch is taken for a decode step, one token each; where one sequence has most of them
+ * the sums are the same, but slower.
  * Precision: scores as in argus_paged_extend_attn (codes exact, fp32 sums; a BF16 query becomes
  * FP16 times a power of two per row over 8-bit and group-coded pages, where elements below 2^-31 of
  * the row's largest lose bits); weights and sums are fp32.  The order of the sums is fixed.
@@ -745,8 +751,9 @@ argus_status argus_attn_weights(const argus_extend_args* args, float* weights, i
  * [B][Hkv][row_len], row_len >= max_pages * P; weights_out [B][Hkv][row_len_out],
  * row_len_out >= budget; kept device int32 [B][Hkv][budget]; dst_table device int32
  * [B][dst_pages], dst_pages * P >= budget >= sink_tokens + recent_tokens, the budget's pages below
- * 2^31 - 65,536 tokens.  seq_lens_out, kept
- * and weights_out overlap neither an input nor each other (ARGUS_E_INVALID).
+ * 2^31 - 65,536 tokens.  seq_lens_out, kept and weights_out overlap neither lengths, weights and
+ * tables nor each other (ARGUS_E_INVALID); that they lie outside the pools and dst is the caller's
+ * to see to, and not checked.
  * No workspace.  head_dim 64 or 128; stored values finite.
  * ------------------------------------------------------------------------- */
 argus_status argus_evict_tokens(const argus_geom* g, int32_t batch, const argus_pool* pools,
