@@ -26,12 +26,13 @@
 // by one and all rounds on all keys; 30 with whole keys, one atomic a warp and key for the list, and the zeros behind the kept
 // weights stored four bytes at a time in front of the loads.  Counting the list's digits by atomics in shared
 // memory, eight bits at once: 26.)  Gathering 67 us for 268 MB, 4.0 TB/s (60% of a copy): converting, and
-// dependent reads that four blocks per SM hide in part (three blocks with the pairs kept in registers instead of the
+// dependent reads that four blocks per SM hide in part, at the price of spills (64 registers a thread; 100 to 330 bytes
+// read back) (three blocks with the pairs kept in registers instead of the
 // codes 76 us, five 71; two blocks with V fetched behind K 122 us in all; blocks of four warps 120; V's rows fetched
 // to the L2 beside K's, or the kernel launched early: no faster).  Divisions as the compiler makes them cost 24 us more, two
 // encodings from both sides of the quotient with a division where they differ 22: rows of the page's largest
 // scale often hit ties.  One sequence of 16,384 fp16 tokens to 2,048, 2 KV heads of 64: 19 us, the rounds' barriers
-// (a cluster of eight blocks took 13 us longer than one).
+// (by a cluster of eight blocks 37 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -748,8 +749,8 @@ static argus_status status_of(cudaError_t e, const char* what) {
 
 static argus_status launch(const VParams& p, int D, cudaStream_t s) {
   // blocks per row: one holds 32,768 keys; more than 8 times that are read again in every round.  (More
-  // blocks than a row needs cost more in the cluster's barriers than they save: 16,384 keys 28 us
-  // by one block, 37 by eight.)
+  // blocks than a row needs cost more in the cluster's barriers than they save: a call of 16,384 keys 19 us
+  // by one block, 37 by eight; 16 sequences of up to 32,768 keys 90 and 361.)
   const long long keys = (long long)kSelThreads * kRegKeys, longest = (long long)p.max_pages * p.P;
   int C = 1;
   while (C < kMaxCluster && C * keys < longest) C *= 2;

@@ -41,7 +41,7 @@
 // 131,072 FP8 tokens, 16/2 heads of 128: 1.02 ms, 1.07 PFLOP/s (56% of cuBLAS bf16);
 // with neither softmax nor MMAs the loads and conversions alone took 0.71 ms, the
 // MMAs alone 0.67 ms.  BF16, FP8 and INT8 pages mixed, 8 sequences of up to 16,384
-// with 1 to 256 new tokens: 247 us (the same in FP8 alone 152, INT8 217, BF16 315: a
+// with 1 to 256 new tokens: 245 us (the same in FP8 alone 152, INT8 217, BF16 315: a
 // 16-bit page is twice the bytes for every query tile, and the second half of its rows
 // of 128 dims is read only when it is stored).
 // Per-item cost is what bounds short sequences (1,024 of 64 tokens: 263 us): its code

@@ -20,15 +20,16 @@
 // Measured (GB300, CUDA events, buffers rotated past the L2): two video prompts of 52,768
 // tokens together, 14/2 heads of 64, three axes: 54 us, 4.5 TB/s (66% of a plain copy);
 // five prompts of 777 to 2,048 tokens, 32/8 heads of 128: 35 us, 5.1 TB/s (75%); a
-// decode step of 32 rows: 4.4 us in a graph, its launch and two dependent reads.  Warps on
+// decode step of 32 rows: 4.4 us in a graph (7.9 with the L2 flushed, with norms 8.6), its launch and two dependent reads.  Warps on
 // runs of neighbouring tokens (sequence and page looked up once) were no faster, nor
 // sines and cosines kept in registers: 36 and 52 us at best, with more registers.
 //
 // The norm, y = x w / sqrt(mean x^2 + eps) over a head's D elements, is one more
 // value per head: an item's sum of squares goes around the D / 16 neighbouring lanes that
 // hold the head, in fp32, between the loads and the rotation; nothing is read twice and
-// nothing rounded in between.  Six prompts of 777 to 2,500 tokens, 32/4 heads of 128: 46.5 us, 4.3 TB/s (65% of
-// a copy), issue slots 58%; with four items in flight, as without norms, two blocks fit an SM: 69 us.
+// nothing rounded in between.  Six prompts of 777 to 2,500 tokens, 32/4 heads of 128: 46 us, 4.4 TB/s (65% of
+// a copy): latency, with half of the issue slots used and a third of the warps there; with four items in flight, as
+// without norms, two blocks fit an SM: 69 us.
 #include <algorithm>
 #include <cmath>
 

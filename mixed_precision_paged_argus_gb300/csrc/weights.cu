@@ -23,8 +23,8 @@
 // (78 to 80% of a plain copy).  On the way: chunks loaded into registers when they were wanted 238 us, a ring of single
 // chunks 168 to 204 (spilled values came back from the L2, as the rings leave the L1 little room), pairs with three
 // blocks of 80 registers per SM 171, with two of 127 as it is.  11 sequences of 3,736 to 13,632 tokens, 32/8 heads of 128:
-// INT4, one token 24 us, 21 tokens 153 (215 with one tile of rows per pass, 148 with four, in bf16 187 and 190: four
-// cost registers, and with them warps); 4 tokens over 16-bit pages 38 (58 with one).
+// INT4, one token 24 us, 21 tokens 155 (215 with one tile of rows per pass, 148 with four, in bf16 187 and 190: four
+// cost registers, and with them warps); 4 tokens over 16-bit pages 37 (58 with one).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -589,7 +589,7 @@ static argus_status launch_d(WParams p, bool bf, cudaStream_t s) {
   if (group && !decode && p.B > 1 && all_rows > 8) {
     // more than a tile of rows: two tiles per pass, as the large tiles know no group codes; apart from the others
     // also because a chunk of many rows is many times their work.  The kernel that likely has the fewer sequences
-    // leads.  (A single sequence of 21 tokens: 67 us by one kernel, 71 by two.)
+    // leads: where it has none, batches of 4 to 21 tokens each lose 1 to 3% (a single sequence 6%: one kernel there).
     const auto part = [&](auto tiles, bool follows) {
       p.few = decltype(tiles)::value == 2 ? 8 : -1;
       p.many = decltype(tiles)::value == 2 ? 0x7fffffff : 8;

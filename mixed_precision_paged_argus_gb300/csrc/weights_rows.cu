@@ -14,7 +14,7 @@
 // One block per SM; key blocks, weighted by their tiles, are dealt in equal ranges.
 //
 // Measured (GB300): the last 32 tokens of 4 sequences of 4,096 to 32,768 BF16 tokens, 32/8 heads of 128 (one tile of 128 rows
-// per KV head): 46 us, 3.2 TB/s (47% of a plain copy), tensor pipe 20%.  What bounds it: loader warps hold one block of 32 KB per
+// per KV head): 45 us, 3.2 TB/s (48% of a plain copy), tensor pipe 20%.  What bounds it: loader warps hold one block of 32 KB per
 // SM in registers (a block every 2,200 cycles), and a group's wait, TMEM loads, exponentials and sums in a row
 // take 700.  Tried: two groups of 64 columns 55 us (1,100 to 1,800 cycles of sums), two sets of loaders
 // beside them 56 to 62, pages prefetched toward the L2 52 to 64.  By weights.cu's path the same call takes 380 us.
