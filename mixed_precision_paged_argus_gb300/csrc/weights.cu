@@ -579,8 +579,8 @@ static argus_status launch_d(WParams p, bool bf, cudaStream_t s) {
   const std::integral_constant<int, 2> two;
   // A call of as many tokens as sequences is taken for a decode step, with one token each.  In any other, one sequence may
   // have all the tokens, whatever the average is (idle slots), and the sequences of many rows get a kernel of their own,
-  // beside which the other one may run.  Where no sequence has many it is empty: 2 us of a small step of 16 us, 0 to 2 of
-  // one of 69.  One sequence of 16,384 tokens asks with 32, 63 slots are empty: FP8 25 us (68 without), BF16 26 (85);
+  // beside which the other one may run.  Where no sequence has many it is empty: 2 to 4 us beside a small step of 16 us, 0 to 2
+  // beside one of 69.  One sequence of 16,384 tokens asks with 32, 63 slots are empty: FP8 25 us (68 without), BF16 26 (85);
   // the 63 hold 2,000 to 8,192 tokens: FP8 108 (691), BF16 169 (1,214), INT4, with 21 tokens, 184 (1,267).
   const long long all_rows = (long long)p.total_q * p.G;
   const bool decode = p.total_q == p.B, more = all_rows > 8ll * p.B;   // more than one tile of rows on average
